@@ -73,6 +73,9 @@ extern "C" {
 #define BLEND_POOL_DEVICE 0
 #define BLEND_POOL_HOST 1
 
+#define BLEND_PAGES_MODEL 0 /* pages hold rows of the model's dtype */
+#define BLEND_PAGES_INT4 1  /* pages hold rows of 4-bit codes with a scale for each 32 dims */
+
 #define BLEND_DEV_KV 0 /* deviation = |k-k'|^2 + |v-v'|^2 */
 #define BLEND_DEV_V 1  /* deviation = |v-v'|^2 */
 
@@ -81,6 +84,7 @@ extern "C" {
 #define BLEND_MAX_WINDOW 64
 #define BLEND_MAX_SPAN 64              /* longest span of the span rule */
 #define BLEND_MAX_ALIGN_TARGETS 131072 /* target tokens of one align_expand call */
+#define BLEND_MAX_SEQS 1024            /* sequences of one paged cache table */
 #define BLEND_GU_BLOCK 16 /* gate/up row interleave of w_gu, see blend_weights */
 
 /* ---- model ----------------------------------------------------------------- */
@@ -426,6 +430,88 @@ int blend_prefill(blend_handle* h, int32_t n_req, const blend_request* reqs,
  * another dtype.  Any alignment of hidden is accepted (16-byte aligned rows read faster). */
 int importance_scores(const void* hidden, int32_t n, int32_t n_layers, int32_t dim,
                       int32_t dtype, float* out, void* stream);
+
+/* ---- paged cache -------------------------------------------------------------
+ * What follows the prefill: the finished caches of many sequences, kept in pages of a shared
+ * pool, grown token by token and attended by the tokens that are generated (the pages' systems
+ * hand the finished KV cache to a serving engine: CacheBlend blog, "The system").  One
+ * blend_pages describes one layer.
+ *
+ * Token t of sequence s lies in page table[s][t / page_tokens] at row t % page_tokens of each
+ * kv head.  Table entries of pages that hold no token of a sequence are not read.  Sequences
+ * may share pages.
+ *
+ * BLEND_PAGES_INT4: the 32 dims of a group (dims 32g..32g+31 of one head's row) share a bf16
+ * scale s = bf16(max |x| / 7), and a dim is held as code n + 8 with n = round-to-even(x / s) in
+ * -7..7 (0 where s is 0), every step in fp32; its value is n * s.  A group with an infinity or a
+ * NaN gets a NaN scale: all its values are NaN.  A K row of d / 2 bytes holds dim 32g + 8c + e
+ * (c < 4, e < 8) at bit 4 * (e / 2) + 16 * (e % 2) of the little-endian 32-bit word at byte
+ * c * d / 8 + 4 * g; a V row holds dim 32g + 4r + e (r < 8, e < 4) at bit 4 * e of the 16-bit
+ * word at byte r * d / 16 + 2 * g.  (The orders are those in which the attention kernel's matrix
+ * instructions take their operands.) */
+typedef struct {
+    int32_t format;       /* BLEND_PAGES_MODEL | BLEND_PAGES_INT4 */
+    int32_t page_tokens;  /* 16, 32, 64 or 128 */
+    int32_t n_pages;      /* pages in k and v */
+    int32_t n_seq;        /* rows of table, 1..BLEND_MAX_SEQS */
+    int32_t max_pages;    /* columns of table: pages of one sequence at most (up to 2^24 tokens) */
+    const int32_t* table; /* device [n_seq][max_pages], page indices */
+    void* k;              /* device [n_pages][hkv][page_tokens][d], or [..][d / 2] bytes for INT4 */
+    void* v;
+    void* k_scale;        /* INT4: device bf16 [n_pages][hkv][page_tokens][d / 32]; else NULL */
+    void* v_scale;
+} blend_pages;
+
+/* Appends rows to the cache: for i < *n (device scalar, at most max_n rows) writes row i of
+ * k_new, rotated by rot[i] positions, and row i of v_new to token pos[i] of sequence seq[i].
+ * rot: device [max_n] (|rot| < max_pos, as delta of rope_realign) or NULL to rotate by pos[i], the
+ * step of a new token; keys that already carry a position take the shift from it (0: as they
+ * are, bit for bit).  k_new, v_new: device [max_n][hkv][d] of the model dtype with ld_k, ld_v
+ * elements between rows, so slices of a fused projection need no copy.  With q (device
+ * [max_n][hq][d], ld_q between rows) the query heads are rotated alike into q_out (device
+ * [max_n][hq][d], rows adjacent; q itself when ld_q = hq * d); NULL leaves both out.  Rotations
+ * are fp32, each product and sum rounded by itself.
+ * A row with seq[i] < 0 is left alone (padding).  Rows of one call must name distinct tokens:
+ * where two name the same one, its row may mix theirs (no other token is touched).
+ * Device-side checks (BLEND_EDEVICE from blend_device_status): a count outside 0..max_n is
+ * clamped; a row whose sequence, token, rotation or page index is out of range is left alone.
+ * Errors: BLEND_EINVAL for NULL or not 16-byte aligned tensors, row strides that are below a
+ * row or no multiple of 16 bytes, or a bad blend_pages (nothing is launched). */
+int paged_append(blend_handle* h, const blend_pages* pages, const void* k_new, int64_t ld_k, const void* v_new,
+                 int64_t ld_v, const void* q, int64_t ld_q, void* q_out, const int32_t* seq, const int32_t* pos,
+                 const int32_t* rot, const int32_t* n, int32_t max_n, void* stream);
+
+/* Reads rows back: k_out[i], v_out[i] (device [max_n][hkv][d], model dtype) = token pos[i] of
+ * sequence seq[i], the key rotated by rot[i] positions (NULL: not rotated), in fp32 and rounded
+ * once.  So a chunk held in pages, in 4 bits or not, becomes rows of a contiguous blended cache at
+ * its new positions.  Padding rows, checks and errors as for paged_append; a row that fails a
+ * check leaves its outputs as they were.  Rows may repeat. */
+int paged_gather(blend_handle* h, const blend_pages* pages, const int32_t* seq, const int32_t* pos,
+                 const int32_t* rot, const int32_t* n, int32_t max_n, void* k_out, void* v_out, void* stream);
+
+/* Attention over the paged cache.  Sequence s holds kv_len[s] tokens (device [n_seq]) and its
+ * query rows are rows q_start[s]..q_start[s+1]-1 of q (device [n_seq + 1], ascending): its last
+ * tokens, so row q_start[s+1]-1 sits at position kv_len[s]-1 (append first, then attend).  A row
+ * at position p sees token j <= p when window is 0, or j > p - window, or j < n_sink: a sliding
+ * window behind a few first tokens that stay visible (the shared prefix, an attention sink;
+ * CacheClip blog 6.1).  out[row] = softmax(q . k / sqrt(d)) v per head, GQA as in the model.
+ * q: device [max_rows][hq][d] after rotation, model dtype, ld_q elements between rows; out: device
+ * [max_rows][hq * d], rows adjacent, not overlapping q.  A row that sees nothing (more rows than
+ * tokens) gets zeros; rows of out that belong to no sequence are left as they were.
+ * max_q (host): most query rows of one sequence; it picks the kernels (single tokens and few
+ * rows: the keys split over all SMs; long pieces: tiles of 128 pairs on the tensor cores).
+ * Keys and values of tokens no row of the call sees are not used: slots past a length may hold
+ * anything.  A NaN or infinity in a token that some rows see reaches them, and may reach other
+ * rows of the same sequence in the call.  The result does not depend on timing.
+ * Uses the handle's workspace: calls on one handle must not overlap, replays of captured ones
+ * included.  Device-side checks (BLEND_EDEVICE): a sequence with row bounds outside 0..max_rows or
+ * descending, more than max_q rows, or a length outside its table is skipped; a page index
+ * outside the pool is read as page 0.
+ * Errors: BLEND_EINVAL for NULL or unaligned tensors, bad strides, negative sizes, window or
+ * n_sink, max_q < 1 with rows, out equal to q, or a bad blend_pages (nothing is launched). */
+int paged_attention(blend_handle* h, const blend_pages* pages, const void* q, int64_t ld_q, const int32_t* q_start,
+                    const int32_t* kv_len, int32_t max_rows, int32_t max_q, int32_t window, int32_t n_sink,
+                    void* out, void* stream);
 
 #ifdef __cplusplus
 }

@@ -27,6 +27,8 @@ MAX_BATCH = 64
 MAX_SPAN = 64
 MAX_ALIGN_TARGETS = 131072
 GU_BLOCK = 16
+PAGES_MODEL, PAGES_INT4 = 0, 1
+MAX_SEQS = 1024
 
 MODES = {"ext": SEL_EXT, "hkvd": SEL_HKVD, "forced": SEL_FORCED, "full": SEL_FULL, "epic": SEL_EPIC}
 BUDGETS = {"final": BUDGET_FINAL, "candidate": BUDGET_CANDIDATE}
@@ -82,6 +84,12 @@ class Outputs(C.Structure):
                                           "dev2", "q_last")]
 
 
+class Pages(C.Structure):
+    _fields_ = [("format", C.c_int32), ("page_tokens", C.c_int32), ("n_pages", C.c_int32), ("n_seq", C.c_int32),
+                ("max_pages", C.c_int32), ("table", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p),
+                ("k_scale", C.c_void_p), ("v_scale", C.c_void_p)]
+
+
 _lib = None
 
 
@@ -127,6 +135,9 @@ def lib() -> C.CDLL:
             "blend_pick_storage": (C.c_int, [C.c_double, C.c_double, i32, i32, C.POINTER(C.c_double),
                                              C.POINTER(C.c_double), C.POINTER(i32)]),
             "align_expand": (C.c_int, [vp, vp, vp, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp]),
+            "paged_append": (C.c_int, [vp, C.POINTER(Pages), vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, i32, vp]),
+            "paged_gather": (C.c_int, [vp, C.POINTER(Pages), vp, vp, vp, vp, i32, vp, vp, vp]),
+            "paged_attention": (C.c_int, [vp, C.POINTER(Pages), vp, i64, vp, vp, i32, i32, i32, i32, vp, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -141,7 +152,8 @@ EXPORTED = ("blend_workspace_size", "blend_init", "blend_destroy", "blend_last_e
             "kv_deviation", "topk_select_dilate", "gather_rows", "scatter_kv", "selective_layer",
             "blend_prefill", "importance_scores", "blend_profile", "blend_profile_stages", "blend_wait_flag", "blend_profile_read",
             "blend_profile_name", "blend_launch_count", "topk_select_dilate_noalloc", "span_select",
-            "align_expand", "aux_attention_scores", "blend_ratio_controller", "blend_pick_storage")
+            "align_expand", "aux_attention_scores", "blend_ratio_controller", "blend_pick_storage",
+            "paged_append", "paged_gather", "paged_attention")
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -414,6 +426,126 @@ def blend_pick_storage(full_prefill_s: float, kv_bytes: float, floor_bp: int, by
     out = C.c_int32()
     _check(lib().blend_pick_storage(full_prefill_s, kv_bytes, floor_bp, n, bw, cost, C.byref(out)))
     return out.value
+
+
+# ---------------------------------------------------------------- paged cache
+class PagesRef:
+    """Host-side description of one layer's paged cache (see blend_pages): k, v contiguous
+    [n_pages][hkv][page_tokens][d] of the model's dtype, or uint8 [..][d / 2] with bf16 scales
+    [..][d / 32] for 4-bit pages; table int32 [n_seq][max_pages].  All on one GPU."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
+                 v_scale: Optional[torch.Tensor] = None):
+        int4 = k.dtype == torch.uint8
+        if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype:
+            raise ValueError("k and v must be alike: [n_pages][kv heads][page tokens][head dim]")
+        if table.dim() != 2 or table.dtype != torch.int32:
+            raise ValueError("table must be int32 [n_seq][max_pages]")
+        if int4:
+            want = (*k.shape[:3], k.shape[3] * 2 // 32)
+            for s in (k_scale, v_scale):
+                if s is None or s.dtype != torch.bfloat16 or tuple(s.shape) != want:
+                    raise ValueError(f"4-bit pages need bf16 scales of shape {want}")
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("scales go with 4-bit pages (uint8 k and v)")
+        self.t = tuple(x for x in (k, v, table, k_scale, v_scale) if x is not None)
+        if any(not x.is_contiguous() or x.device != k.device for x in self.t):
+            raise ValueError("the tensors of a paged cache must be contiguous and on one device")
+        self.device, self.dtype, self.n_kv_heads = k.device, k.dtype, k.shape[1]
+        self.head_dim = k.shape[3] * (2 if int4 else 1)
+        self.c = Pages(PAGES_INT4 if int4 else PAGES_MODEL, k.shape[2], k.shape[0], table.shape[0], table.shape[1],
+                       *[None if x is None else x.data_ptr() for x in (table, k, v, k_scale, v_scale)])
+        self.ref = C.byref(self.c)
+
+
+def _paged_stream(h: Handle, pages: PagesRef, stream):
+    """The call's stream, after a look at the pages: they must be the handle's model's and on the
+    stream's GPU."""
+    want = torch.uint8 if pages.c.format == PAGES_INT4 else torch.bfloat16 if h.cfg.dtype == BF16 else torch.float32
+    if pages.dtype != want or pages.n_kv_heads != h.cfg.n_kv_heads or pages.head_dim != h.cfg.head_dim:
+        raise ValueError("the pages are not of the handle's model")
+    if stream is None:
+        stream = torch.cuda.current_stream(pages.device)
+    if stream.device != pages.device or torch.cuda.current_device() != pages.device.index:
+        raise ValueError(f"the pages are on {pages.device}: make it the current device and use a stream of it")
+    return stream.cuda_stream
+
+
+def _paged_rows(h: Handle, pages: PagesRef, t: torch.Tensor, heads: int, what: str) -> int:
+    """Distance between the rows of t [rows][heads][head dim] in elements."""
+    d = h.cfg.head_dim
+    st, sh = t.stride(), t.shape
+    flat = len(sh) == 2 and sh[1] == heads * d and st[1] == 1
+    if not flat and not (len(sh) == 3 and sh[1] == heads and sh[2] == d and st[2] == 1 and (st[1] == d or heads == 1)):
+        raise ValueError(f"{what} must be [rows][{heads}][{d}] with adjacent heads")
+    if t.dtype != (torch.bfloat16 if h.cfg.dtype == BF16 else torch.float32) or t.device != pages.device:
+        raise ValueError(f"{what} must be of the model's dtype and on {pages.device}")
+    return st[0] if sh[0] > 1 else heads * d
+
+
+def _paged_index(pages: PagesRef, n: int, what: str, *ts):
+    for t in ts:
+        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n or
+                              t.device != pages.device):
+            raise ValueError(f"{what} must be contiguous int32 of at least {n} entries on {pages.device}")
+
+
+def paged_append(h: Handle, pages: PagesRef, k_new, v_new, seq, pos, n, max_n, q=None, q_out=None, rot=None,
+                 stream=None):
+    """k_new, v_new (and q): [rows][heads][head dim], rows at any stride of 16 bytes; seq, pos, rot
+    int32 per row; n a device int32 count of at most max_n rows."""
+    s = _paged_stream(h, pages, stream)
+    hkv, hq = h.cfg.n_kv_heads, h.cfg.n_q_heads
+    ld_k, ld_v = _paged_rows(h, pages, k_new, hkv, "k_new"), _paged_rows(h, pages, v_new, hkv, "v_new")
+    _paged_index(pages, max_n, "seq, pos and rot", seq, pos, rot)
+    _paged_index(pages, 1, "n", n)
+    if min(k_new.shape[0], v_new.shape[0]) < max_n:
+        raise ValueError("fewer rows than max_n")
+    ld_q = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        ld_q = _paged_rows(h, pages, q, hq, "q")
+        if _paged_rows(h, pages, q_out, hq, "q_out") != hq * h.cfg.head_dim or min(q.shape[0], q_out.shape[0]) < max_n:
+            raise ValueError("q_out must hold max_n adjacent rows, and q as many")
+    if max_n == 0:
+        return
+    _check(lib().paged_append(h.ptr, pages.ref, k_new.data_ptr(), ld_k, v_new.data_ptr(), ld_v,
+                              None if q is None else q.data_ptr(), ld_q, None if q is None else q_out.data_ptr(),
+                              seq.data_ptr(), pos.data_ptr(), None if rot is None else rot.data_ptr(), n.data_ptr(),
+                              max_n, s), h)
+
+
+def paged_gather(h: Handle, pages: PagesRef, seq, pos, n, max_n, k_out, v_out, rot=None, stream=None):
+    """k_out, v_out: [rows][kv heads][head dim], rows adjacent, of the model's dtype."""
+    s = _paged_stream(h, pages, stream)
+    hkv = h.cfg.n_kv_heads
+    for t in (k_out, v_out):
+        if _paged_rows(h, pages, t, hkv, "k_out and v_out") != hkv * h.cfg.head_dim or t.shape[0] < max_n:
+            raise ValueError("k_out and v_out must hold max_n adjacent rows")
+    _paged_index(pages, max_n, "seq, pos and rot", seq, pos, rot)
+    _paged_index(pages, 1, "n", n)
+    if max_n == 0:
+        return
+    _check(lib().paged_gather(h.ptr, pages.ref, seq.data_ptr(), pos.data_ptr(), None if rot is None else rot.data_ptr(),
+                              n.data_ptr(), max_n, k_out.data_ptr(), v_out.data_ptr(), s), h)
+
+
+def paged_attention(h: Handle, pages: PagesRef, q, q_start, kv_len, max_q, out, window=0, n_sink=0, stream=None):
+    """q: [rows][hq][head dim] (rows at any stride of 16 bytes); out: [rows][hq * head dim], rows
+    adjacent; q_start int32 [n_seq + 1], kv_len int32 [n_seq] on the device; max_q: most query rows of
+    one sequence."""
+    s = _paged_stream(h, pages, stream)
+    hq = h.cfg.n_q_heads
+    ld_q = _paged_rows(h, pages, q, hq, "q")
+    if _paged_rows(h, pages, out, hq, "out") != hq * h.cfg.head_dim or out.shape[0] < q.shape[0]:
+        raise ValueError("out must hold as many adjacent rows as q")
+    _paged_index(pages, pages.c.n_seq, "kv_len", kv_len)
+    _paged_index(pages, pages.c.n_seq + 1, "q_start", q_start)
+    if q.shape[0] == 0:
+        return
+    _check(lib().paged_attention(h.ptr, pages.ref, q.data_ptr(), ld_q, q_start.data_ptr(), kv_len.data_ptr(),
+                                 q.shape[0], max_q, window, n_sink, out.data_ptr(), s), h)
 
 
 # ---------------------------------------------------------------- weight layout

@@ -16,6 +16,7 @@
 
 #include "common.cuh"
 #include "gemm_tc.cuh"
+#include "paged.cuh"
 
 namespace {
 thread_local std::string g_err;
@@ -97,6 +98,8 @@ struct blend_handle {
     cudaEvent_t ev_free[2] = {nullptr, nullptr};
     std::vector<cudaEvent_t> ev_layer;
     int use_tc;  // tensor-core GEMM for bf16
+    float* paged_part;   // paged_attention: partial results of split key ranges
+    int32_t* paged_count;  // and the arrivals at each split item (zero between calls)
     float* split_ws;  // tensor-core GEMM: K-half partials of last-wave tiles
     int host_rc = 0;  // first failure of an internal launch during the current call
     std::string last_error;
@@ -278,6 +281,8 @@ Layout make_layout(const blend_model_cfg* c, const blend_limits* l) {
         L.add((size_t)l->max_tokens * kvd * es);
     L.add(M * NORM_PARTS_MAX * sizeof(float));             // 39 folded-RMSNorm partial sums of squares
     L.add((size_t)l->max_batch * ((l->max_chunk_rows + 2047) / 2048 * 2048) * 8);  // 40 sorted rank keys
+    L.add(paged_part_bytes(c->head_dim));                  // 41 paged attention: partial results
+    L.add(PAGED_MAX_CTAS * sizeof(int32_t));               // 42 and arrival counters
     return L;
 }
 
@@ -497,9 +502,12 @@ int blend_init(const blend_model_cfg* cfg, const blend_weights* w, const blend_l
     for (int q = 0; q < 4; ++q) h->stage[q] = b + L.off[i++];
     h->ssq = (float*)(b + L.off[i++]);
     h->rank_keys = (unsigned long long*)(b + L.off[i++]);
+    h->paged_part = (float*)(b + L.off[i++]);
+    h->paged_count = (int32_t*)(b + L.off[i++]);
     h->use_tc = cfg->dtype == BLEND_BF16 ? tc_available() : 0;
     cudaStream_t s = (cudaStream_t)stream;
     cudaMemsetAsync(h->err, 0, 16, s);
+    cudaMemsetAsync(h->paged_count, 0, PAGED_MAX_CTAS * sizeof(int32_t), s);
     launch_rope_table(h->rope, cfg->max_pos, cfg->head_dim, cfg->rope_theta, s);
     int rc = check_cuda(h, "blend_init");
     if (rc != BLEND_OK) {
@@ -1334,4 +1342,120 @@ extern "C" int aux_attention_scores(blend_handle* h, int32_t n_req, const blend_
                       h->aux_stats, tc_score_spans(h->lim.max_tokens), scores, h->err, h->use_tc != 0,
                       (cudaStream_t)stream);
     return check_cuda(h, "aux_attention_scores");
+}
+
+// ---------------------------------------------------------------- paged cache
+namespace {
+// Checks a blend_pages against the handle's model and fills the kernels' view of it.
+int view_pages(blend_handle* h, const blend_pages* p, PageView* v) {
+    if (!p) return fail(h, BLEND_EINVAL, "pages is NULL");
+    if (p->format != BLEND_PAGES_MODEL && p->format != BLEND_PAGES_INT4)
+        return fail(h, BLEND_EINVAL, "bad page format %d", p->format);
+    if (p->page_tokens != 16 && p->page_tokens != 32 && p->page_tokens != 64 && p->page_tokens != 128)
+        return fail(h, BLEND_EINVAL, "page_tokens=%d is not 16, 32, 64 or 128", p->page_tokens);
+    if (p->n_pages < 1 || p->n_seq < 1 || p->n_seq > BLEND_MAX_SEQS || p->max_pages < 1 ||
+        (long long)p->max_pages * p->page_tokens > (1ll << 24))
+        return fail(h, BLEND_EINVAL, "bad page counts (n_pages=%d n_seq=%d max_pages=%d)", p->n_pages, p->n_seq,
+                    p->max_pages);
+    if (!p->table || !p->k || !p->v) return fail(h, BLEND_EINVAL, "NULL pointer in pages");
+    if (((uintptr_t)p->k | (uintptr_t)p->v) & 15) return fail(h, BLEND_EINVAL, "pages must be 16-byte aligned");
+    if ((uintptr_t)p->table & 3) return fail(h, BLEND_EINVAL, "the page table must be 4-byte aligned");
+    if (p->format == BLEND_PAGES_INT4) {
+        if (!p->k_scale || !p->v_scale) return fail(h, BLEND_EINVAL, "4-bit pages without scales");
+        if (((uintptr_t)p->k_scale | (uintptr_t)p->v_scale) & 15)
+            return fail(h, BLEND_EINVAL, "scales must be 16-byte aligned");
+    }
+    v->k = (const char*)p->k;
+    v->v = (const char*)p->v;
+    v->ks = (const char*)p->k_scale;
+    v->vs = (const char*)p->v_scale;
+    v->table = p->table;
+    v->n_pages = p->n_pages;
+    v->n_seq = p->n_seq;
+    v->max_pages = p->max_pages;
+    v->shift = p->page_tokens == 16 ? 4 : p->page_tokens == 32 ? 5 : p->page_tokens == 64 ? 6 : 7;
+    v->hkv = h->cfg.n_kv_heads;
+    return BLEND_OK;
+}
+// Distance between rows of `heads` heads: at least one row, a multiple of 16 bytes.
+bool row_stride_ok(const blend_handle* h, long long ld, int heads) {
+    return ld >= (long long)heads * h->cfg.head_dim && ld % (long long)(16 / elem_size(h->cfg.dtype)) == 0 &&
+           ld <= (1ll << 40);
+}
+}  // namespace
+
+int paged_append(blend_handle* h, const blend_pages* pages, const void* k_new, int64_t ld_k, const void* v_new,
+                 int64_t ld_v, const void* q, int64_t ld_q, void* q_out, const int32_t* seq, const int32_t* pos,
+                 const int32_t* rot, const int32_t* n, int32_t max_n, void* stream) {
+    if (!h) return fail(nullptr, BLEND_EINVAL, "handle is NULL");
+    const blend_model_cfg& c = h->cfg;
+    PageView pv;
+    if (int rc = view_pages(h, pages, &pv)) return rc;
+    if (!k_new || !v_new || !seq || !pos || !n) return fail(h, BLEND_EINVAL, "NULL pointer");
+    if (!q != !q_out) return fail(h, BLEND_EINVAL, "q and q_out go together");
+    if (((uintptr_t)k_new | (uintptr_t)v_new | (uintptr_t)q | (uintptr_t)q_out) & 15)
+        return fail(h, BLEND_EINVAL, "k_new, v_new, q and q_out must be 16-byte aligned");
+    if (!row_stride_ok(h, ld_k, c.n_kv_heads) || !row_stride_ok(h, ld_v, c.n_kv_heads) ||
+        (q && !row_stride_ok(h, ld_q, c.n_q_heads)))
+        return fail(h, BLEND_EINVAL, "bad row stride (%lld, %lld, %lld)", (long long)ld_k, (long long)ld_v,
+                    (long long)ld_q);
+    if (q && q == q_out && ld_q != (int64_t)c.n_q_heads * c.head_dim)
+        return fail(h, BLEND_EINVAL, "q_out may be q only where q's rows are adjacent");
+    if (max_n < 0 || max_n > (1 << 24)) return fail(h, BLEND_EINVAL, "max_n=%d outside 0..2^24", max_n);
+    if (max_n == 0) return BLEND_OK;
+    launch_paged_append(c.dtype, pages->format == BLEND_PAGES_INT4, pv, c.n_q_heads, c.head_dim, k_new, ld_k, v_new,
+                        ld_v, q, ld_q, q_out, seq, pos, rot, n, max_n, h->rope, c.max_pos, h->err, (cudaStream_t)stream);
+    return check_cuda(h, "paged_append");
+}
+
+int paged_gather(blend_handle* h, const blend_pages* pages, const int32_t* seq, const int32_t* pos,
+                 const int32_t* rot, const int32_t* n, int32_t max_n, void* k_out, void* v_out, void* stream) {
+    if (!h) return fail(nullptr, BLEND_EINVAL, "handle is NULL");
+    const blend_model_cfg& c = h->cfg;
+    PageView pv;
+    if (int rc = view_pages(h, pages, &pv)) return rc;
+    if (!seq || !pos || !n || !k_out || !v_out) return fail(h, BLEND_EINVAL, "NULL pointer");
+    if (((uintptr_t)k_out | (uintptr_t)v_out) & 15) return fail(h, BLEND_EINVAL, "k_out/v_out must be 16-byte aligned");
+    if (max_n < 0 || max_n > (1 << 24)) return fail(h, BLEND_EINVAL, "max_n=%d outside 0..2^24", max_n);
+    if (max_n == 0) return BLEND_OK;
+    launch_paged_gather(c.dtype, pages->format == BLEND_PAGES_INT4, pv, c.head_dim, seq, pos, rot, n, max_n, k_out,
+                        v_out, h->rope, c.max_pos, h->err, (cudaStream_t)stream);
+    return check_cuda(h, "paged_gather");
+}
+
+int paged_attention(blend_handle* h, const blend_pages* pages, const void* q, int64_t ld_q, const int32_t* q_start,
+                    const int32_t* kv_len, int32_t max_rows, int32_t max_q, int32_t window, int32_t n_sink,
+                    void* out, void* stream) {
+    if (!h) return fail(nullptr, BLEND_EINVAL, "handle is NULL");
+    const blend_model_cfg& c = h->cfg;
+    PagedAttn a;
+    if (int rc = view_pages(h, pages, &a.pg)) return rc;
+    if (!q || !q_start || !kv_len || !out) return fail(h, BLEND_EINVAL, "NULL pointer");
+    if (((uintptr_t)q | (uintptr_t)out) & 15) return fail(h, BLEND_EINVAL, "q and out must be 16-byte aligned");
+    if (q == out) return fail(h, BLEND_EINVAL, "out overlaps q");
+    if (!row_stride_ok(h, ld_q, c.n_q_heads)) return fail(h, BLEND_EINVAL, "bad row stride %lld", (long long)ld_q);
+    if (max_rows < 0 || max_rows > (1 << 24) || max_q < (max_rows > 0 ? 1 : 0) || window < 0 || n_sink < 0)
+        return fail(h, BLEND_EINVAL, "bad max_rows=%d max_q=%d window=%d n_sink=%d", max_rows, max_q, window, n_sink);
+    // the keys of all sequences and heads are counted in 32 bits by the split kernels
+    if ((long long)pages->n_seq * c.n_kv_heads * ((long long)pages->max_pages * pages->page_tokens / PAGED_STEP + 1) >=
+        (1ll << 31))
+        return fail(h, BLEND_EINVAL, "table too large: n_seq * n_kv_heads * tokens / 16 must stay below 2^31");
+    if (max_rows == 0) return BLEND_OK;
+    a.q = q;
+    a.ld_q = ld_q;
+    a.q_start = q_start;
+    a.kv_len = kv_len;
+    a.max_rows = max_rows;
+    a.max_q = max_q < max_rows ? max_q : max_rows;
+    a.hq = c.n_q_heads;
+    a.group = c.n_q_heads / c.n_kv_heads;
+    a.window = window == 0 || window > PAGED_NO_WINDOW ? PAGED_NO_WINDOW : window;
+    a.n_sink = n_sink;
+    a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.head_dim));
+    a.out = out;
+    a.part = h->paged_part;
+    a.count = h->paged_count;
+    a.err = h->err;
+    launch_paged_attn_simt(c.dtype, pages->format == BLEND_PAGES_INT4, a, c.head_dim, (cudaStream_t)stream);
+    return check_cuda(h, "paged_attention");
 }

@@ -1,0 +1,137 @@
+// Paged KV cache of one layer: what the append, gather and attention kernels share.
+#pragma once
+#include "common.cuh"
+
+namespace blend {
+
+constexpr int PAGED_STEP = 16;       // keys of one step of the row-split kernels; every page holds whole steps
+constexpr int PAGED_MAX_CTAS = 640;  // CTAs of a launch that may leave partial results
+constexpr int PAGED_NO_WINDOW = 1 << 30;  // past every position, and position - window stays in 32 bits
+constexpr int PAGED_MAX_TILE = 32;   // (row, head) pairs of one tile of those kernels
+// fp32 partial results: two slots per CTA, each [pair][head_dim] sums, then maxima and sums per pair
+constexpr size_t paged_slot_floats(int d) { return (size_t)PAGED_MAX_TILE * (d + 2); }
+constexpr size_t paged_part_bytes(int d) { return 2 * (size_t)PAGED_MAX_CTAS * paged_slot_floats(d) * 4; }
+
+// The pages as the kernels see them (blend_pages with the model's head count).
+struct PageView {
+    const char* k;
+    const char* v;
+    const char* ks;  // 4-bit pages: bf16 scales [page][head][token][d/32]
+    const char* vs;
+    const int32_t* table;
+    int n_pages, n_seq, max_pages;
+    int shift;  // log2(tokens per page)
+    int hkv;
+};
+
+// Bytes of one head's K or V row in the pages, and of its scales.
+template <typename T, bool I4> __host__ __device__ constexpr int held_bytes(int d) { return I4 ? d / 2 : d * (int)sizeof(T); }
+
+// The page that holds tokens [t, ...) of sequence `seq`; a table entry outside the pool is
+// reported and page 0 read in its place.
+__device__ __forceinline__ int page_of(const PageView& p, int seq, int t, int32_t* err) {
+    int pg = __ldg(p.table + (long long)seq * p.max_pages + (t >> p.shift));
+    if ((unsigned)pg >= (unsigned)p.n_pages) {
+        set_error(err, BLEND_EDEVICE);
+        pg = 0;
+    }
+    return pg;
+}
+// Row of (page, head, token in page) counted in rows of the pool: 64 bits, pools pass 2^31 elements.
+__device__ __forceinline__ long long page_row(const PageView& p, int page, int head, int in_page) {
+    return (((long long)page * p.hkv + head) << p.shift) + in_page;
+}
+
+// ---- packed 4-bit rows (layout in blend.h at BLEND_PAGES_INT4)
+// Eight consecutive dims 32g + 8c .. +7 of a K row are one 32-bit word; dim e of them sits at
+// bit 4 (e / 2) + 16 (e % 2), so (w >> 4 i) & 0x000F000F is the pair (2i, 2i + 1).
+__device__ __forceinline__ int k4_word(int d, int g, int c) { return c * (d / 8) + 4 * g; }  // byte offset in the row
+__device__ __forceinline__ int k4_bit(int e) { return 4 * (e >> 1) + 16 * (e & 1); }
+// Four consecutive dims 32g + 4r .. +3 of a V row are one 16-bit word, dim e at bit 4 e.
+__device__ __forceinline__ int v4_half(int d, int g, int r) { return r * (d / 16) + 2 * g; }
+
+// Arguments of the attention kernels.
+struct PagedAttn {
+    PageView pg;
+    const void* q;
+    long long ld_q;  // elements between rows of q
+    const int32_t* q_start;
+    const int32_t* kv_len;
+    int max_rows, max_q;
+    int hq, group;
+    int window;  // PAGED_NO_WINDOW: none
+    int n_sink;
+    float scale_log2;  // log2(e) / sqrt(d)
+    void* out;
+    float* part;
+    int32_t* count;
+    int32_t* err;
+};
+
+// Query rows and length of one sequence; a bad entry is reported and gives no rows.
+struct SeqInfo {
+    int row0, n_q, len;
+};
+__device__ __forceinline__ SeqInfo seq_info(const PagedAttn& a, int s) {
+    SeqInfo i;
+    i.row0 = __ldg(a.q_start + s);
+    const int end = __ldg(a.q_start + s + 1);
+    i.len = __ldg(a.kv_len + s);
+    i.n_q = end - i.row0;
+    if (i.row0 < 0 || end < i.row0 || end > a.max_rows || i.n_q > a.max_q || i.len < 0 ||
+        i.len > (a.pg.max_pages << a.pg.shift)) {
+        set_error(a.err, BLEND_EDEVICE);
+        i.row0 = 0;
+        i.n_q = 0;
+        i.len = 0;
+    }
+    return i;
+}
+
+// Keys that rows at positions p0..p1 of one sequence see, as blocks of BLK keys: the sinks'
+// blocks 0..n_a-1, then blocks first_b.. of the window's range (n_b of them).
+struct KeyRange {
+    int n_a, first_b, n_b;
+    __device__ __forceinline__ int total() const { return n_a + n_b; }
+    __device__ __forceinline__ int block(int i) const { return i < n_a ? i : first_b + (i - n_a); }
+};
+template <int BLK>
+__device__ __forceinline__ KeyRange key_range(int p0, int p1, int window, int n_sink) {
+    KeyRange r{0, 0, 0};
+    if (p1 < 0) return r;
+    const int lo = max(0, max(p0, 0) - window + 1);
+    r.first_b = lo / BLK;
+    if (lo > 0) r.n_a = min((min(n_sink, p1 + 1) + BLK - 1) / BLK, r.first_b);
+    r.n_b = p1 / BLK + 1 - r.first_b;
+    return r;
+}
+// Key j is visible to a row at position p.
+__device__ __forceinline__ bool sees(int j, int p, int window, int n_sink) {
+    return j <= p && (j > p - window || j < n_sink);
+}
+// Key j is visible to some row at positions p0..p1.
+__device__ __forceinline__ bool seen_by_any(int j, int p0, int p1, int window, int n_sink) {
+    return j <= p1 && (j < n_sink || j > p0 - window);
+}
+// Every key of [j0, j1] is visible to every row at positions p0..p1.
+__device__ __forceinline__ bool all_see(int j0, int j1, int p0, int p1, int window, int n_sink) {
+    return j1 <= p0 && (j0 > p1 - window || j1 < n_sink);
+}
+
+// Maximum that keeps a NaN: a running maximum that dropped one would give its row no weight
+// when the shares of the keys are joined.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+void launch_paged_append(int dtype, bool i4, const PageView& pg, int hq, int d, const void* k_new, long long ld_k,
+                         const void* v_new, long long ld_v, const void* q, long long ld_q, void* q_out,
+                         const int32_t* seq, const int32_t* pos, const int32_t* rot, const int32_t* n_dev, int max_n,
+                         const float2* tab, int max_pos, int32_t* err, cudaStream_t s);
+void launch_paged_gather(int dtype, bool i4, const PageView& pg, int d, const int32_t* seq, const int32_t* pos,
+                         const int32_t* rot, const int32_t* n_dev, int max_n, void* k_out, void* v_out,
+                         const float2* tab, int max_pos, int32_t* err, cudaStream_t s);
+void launch_paged_attn_simt(int dtype, bool i4, const PagedAttn& a, int d, cudaStream_t s);
+}  // namespace blend
