@@ -1456,6 +1456,9 @@ int paged_attention(blend_handle* h, const blend_pages* pages, const void* q, in
     a.part = h->paged_part;
     a.count = h->paged_count;
     a.err = h->err;
-    launch_paged_attn_simt(c.dtype, pages->format == BLEND_PAGES_INT4, a, c.head_dim, (cudaStream_t)stream);
+    if (c.dtype == BLEND_BF16 && h->use_tc && a.max_q * a.group <= PAGED_MAX_TILE)
+        launch_paged_attn_split(pages->format == BLEND_PAGES_INT4, a, c.head_dim, (cudaStream_t)stream);
+    else
+        launch_paged_attn_simt(c.dtype, pages->format == BLEND_PAGES_INT4, a, c.head_dim, (cudaStream_t)stream);
     return check_cuda(h, "paged_attention");
 }
