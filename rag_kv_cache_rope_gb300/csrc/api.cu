@@ -1380,7 +1380,7 @@ int view_pages(blend_handle* h, const blend_pages* p, PageView* v) {
 // Distance between rows of `heads` heads: at least one row, a multiple of 16 bytes.
 bool row_stride_ok(const blend_handle* h, long long ld, int heads) {
     return ld >= (long long)heads * h->cfg.head_dim && ld % (long long)(16 / elem_size(h->cfg.dtype)) == 0 &&
-           ld <= (1ll << 40);
+           ld <= (1ll << 32);
 }
 }  // namespace
 
@@ -1456,9 +1456,17 @@ int paged_attention(blend_handle* h, const blend_pages* pages, const void* q, in
     a.part = h->paged_part;
     a.count = h->paged_count;
     a.err = h->err;
-    if (c.dtype == BLEND_BF16 && h->use_tc && a.max_q * a.group <= PAGED_MAX_TILE)
-        launch_paged_attn_split(pages->format == BLEND_PAGES_INT4, a, c.head_dim, (cudaStream_t)stream);
-    else
-        launch_paged_attn_simt(c.dtype, pages->format == BLEND_PAGES_INT4, a, c.head_dim, (cudaStream_t)stream);
+    const bool i4 = pages->format == BLEND_PAGES_INT4;
+    cudaStream_t s = (cudaStream_t)stream;
+    // bf16: sequences of few (row, head) pairs and long pieces have a kernel each; which of the two a
+    // sequence is only the device knows, so a call that may hold pieces launches both
+    bool tc = c.dtype == BLEND_BF16 && h->use_tc;
+    if (tc && (long long)a.max_q * a.group > PAGED_MAX_TILE) {
+        const int rc = launch_paged_attn_tile(i4, a, c.head_dim, s);
+        if (rc == BLEND_ECUDA) return check_cuda(h, "paged_attention");
+        tc = rc == BLEND_OK;
+    }
+    if (tc) launch_paged_attn_split(i4, a, c.head_dim, s);
+    else launch_paged_attn_simt(c.dtype, i4, a, c.head_dim, s);
     return check_cuda(h, "paged_attention");
 }

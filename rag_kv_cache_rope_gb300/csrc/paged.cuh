@@ -133,6 +133,10 @@ void launch_paged_append(int dtype, bool i4, const PageView& pg, int hq, int d, 
 void launch_paged_gather(int dtype, bool i4, const PageView& pg, int d, const int32_t* seq, const int32_t* pos,
                          const int32_t* rot, const int32_t* n_dev, int max_n, void* k_out, void* v_out,
                          const float2* tab, int max_pos, int32_t* err, cudaStream_t s);
+// Sequences of more than 32 (row, head) pairs, bf16 (paged_tile.cu); others are left alone.
+// Returns BLEND_EUNSUPPORTED, with nothing launched, where no pair of CTAs fits or an operand has no
+// tensor map, and BLEND_ECUDA (the error left to be read) when the launch fails.
+int launch_paged_attn_tile(bool i4, const PagedAttn& a, int d, cudaStream_t s);
 // Sequences of at most 32 (row, head) pairs, bf16 (paged_split.cu); others are left alone.
 void launch_paged_attn_split(bool i4, const PagedAttn& a, int d, cudaStream_t s);
 void launch_paged_attn_simt(int dtype, bool i4, const PagedAttn& a, int d, cudaStream_t s);

@@ -1,0 +1,850 @@
+// Attention of prompt pieces over a paged cache (paged_attention in blend.h), bf16 models: tcgen05
+// on CTA pairs, after the prefill's k_attn_pair.
+//
+// A tile is the 128 / group rows (times the group) of one kv head that fill TMEM's 128 lanes; an
+// item is two neighbouring tiles of one sequence and kv head, one per CTA of a cluster of two, which
+// share every 128-key block.  Per block each CTA stages 64 of the keys (for S) and half of V's
+// columns (for P.V); the leading CTA issues M256 products for both.  TMEM holds three S buffers,
+// each block's P over its own S, and O: see k_attn_pair for why.
+//
+// Work: all items' blocks form one line (as in the split kernel) and every cluster takes an equal
+// stretch of it, so a few long rows fill the GPU as well as many pieces do and ragged lengths
+// leave no tail.  A tile cut by a border leaves its unnormalised O, maximum and sum per row in the
+// workspace; each warp owns 32 rows, and the warp that arrives last at them joins the parts in
+// order.  Blocks outside every row's window are not visited.
+//
+// Pages: model pages come by TMA, one box per page and column half (a page of 16 tokens is eight
+// boxes a block), 4-bit pages through four more warps per CTA that turn codes into bf16 n s in
+// the swizzled layout the products read, one block ahead in registers.  V rows of tokens that no
+// row of the item sees are zeroed (they may hold anything, and 0 x NaN is NaN): by those warps,
+// or, in the few blocks at an edge, by the producer warp after the boxes have landed.  Pages without
+// a token that the item sees are not touched at all.
+// Rounding: P to bf16 (as everywhere on tensor cores), n s of 4-bit pages to bf16.
+#include <cmath>
+
+#include "attn_tc.cuh"
+#include "paged.cuh"
+
+namespace blend {
+namespace {
+
+constexpr int TQ = 128;    // lanes of a tile
+constexpr int TKEYS = 128;  // keys of a block
+constexpr int Q_HALF = TQ * 128;    // 64 columns of a Q tile
+constexpr int K_HALF = 64 * 128;    // 64 columns of a CTA's 64 keys
+constexpr int NSBUF = 3;
+constexpr uint32_t O_COL = 384;
+constexpr int TMEM_COLS = 512;
+constexpr int S_WARP = 6;  // 0 producer, 1 TMEM + P.V issue, 2..5 softmax, 6 S issue, 7..10 4-bit pages
+constexpr int MAX_CLUSTERS = 76;
+constexpr int MIN_QUOTA = 2;  // blocks of a cluster's stretch at least
+
+template <bool I4, int D> struct TileCfg {
+    static constexpr int NH = D / 64;
+    static constexpr int THREADS = I4 ? 352 : 224;
+    static constexpr int VCOL = D / 2;                      // V columns of a CTA
+    static constexpr int QT = NH * Q_HALF;
+    static constexpr int KB = NH * K_HALF;
+    static constexpr int VB = TKEYS * VCOL * 2;
+    static constexpr int STAGE = KB + VB;
+    static constexpr int STAGES = D == 128 ? 4 : 8;
+    static constexpr int SMEM = 2 * QT + STAGES * STAGE + 1024;
+    // kind::f16, bf16 inputs, fp32 accumulate, M256 (the pair); S: N128, P.V: N = D with B MN-major
+    static constexpr uint32_t IDESC_S = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((256u >> 4) << 24);
+    static constexpr uint32_t IDESC_PV =
+        (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (((uint32_t)D >> 3) << 17) | ((256u >> 4) << 24);
+    // fp32 partial result of one tile: [D / 4][128 lanes][4], then maxima and sums per lane
+    static constexpr size_t PART = (size_t)TQ * (D + 2);
+};
+static_assert(4 * MAX_CLUSTERS * TileCfg<false, 128>::PART * 4 <= paged_part_bytes(128), "workspace");
+static_assert(4 * MAX_CLUSTERS * TileCfg<false, 64>::PART * 4 <= paged_part_bytes(64), "workspace");
+static_assert(8 * MAX_CLUSTERS <= PAGED_MAX_CTAS, "arrival counters");
+
+// MN-major B operand (V), a CTA's columns in one swizzle atom: 64 columns (128-byte swizzle, 8-key
+// groups 1024 B apart) or 32 (64-byte swizzle, 512 B apart).
+template <int D> __device__ __forceinline__ uint64_t desc_v(uint32_t a) {
+    const uint64_t group = D == 128 ? 1024 : 512, layout = D == 128 ? 2 : 4;
+    return (uint64_t)((a & 0x3FFFF) >> 4) | ((uint64_t)(16384 >> 4) << 16) | ((group >> 4) << 32) | ((uint64_t)1 << 46) |
+           (layout << 61);
+}
+__device__ __forceinline__ void tma_4d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4, %5, %6}], [%2];" ::"r"(su32(dst)),
+        "l"((uint64_t)m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+// Arrival on the leader's barrier that publishes this thread's shared-memory writes to the pair.
+__device__ __forceinline__ void arrive_leader_release(uint64_t* b) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(b)) : "memory");
+}
+__device__ __forceinline__ bool wait_cl_acquire(uint64_t* b, uint32_t par, volatile int* abort_flag) {
+    for (long long i = 0; i < 64 * SPIN_LIMIT; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(ok)
+            : "r"(su32(b)), "r"(par)
+            : "memory");
+        if (ok) return true;
+        if ((i & 1023) == 1023 && *abort_flag) return false;
+    }
+    return false;
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ int tiles2(int n_q, int rows2) { return (n_q + rows2 - 1) / rows2; }
+// Positions of item tp's rows (two tiles of rows2 rows) and its 128-key blocks; an item that sees
+// nothing keeps one block, all masked, which gives its rows their zeros.
+struct ItemRange {
+    int p_lo, p_hi, n;
+    KeyRange kr;
+};
+__device__ __forceinline__ ItemRange item_range(const PagedAttn& a, const SeqInfo& si, int tp, int rows2) {
+    ItemRange r;
+    const int first = si.len - si.n_q;
+    r.p_lo = first + tp * rows2;
+    r.p_hi = first + min(si.n_q, (tp + 1) * rows2) - 1;
+    r.kr = key_range<TKEYS>(r.p_lo, r.p_hi, a.window, a.n_sink);
+    r.n = max(1, r.kr.total());
+    return r;
+}
+
+// A cluster's stretch [x, x_end) of the line of blocks, item by item.  Every role walks its own.
+struct Walk {
+    const PagedAttn& a;
+    const int* pre;
+    int rows2, x, x_end;
+    int seq, head, tp;
+    SeqInfo si;
+    ItemRange it;
+    int b0, b1;  // this stretch's blocks of the item
+
+    __device__ __forceinline__ Walk(const PagedAttn& a_, const int* pre_, int rows2_, int x_, int x_end_)
+        : a(a_), pre(pre_), rows2(rows2_), x(x_), x_end(x_end_) {
+        int lo = 0, hi = a.pg.n_seq - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (pre[mid] <= x) lo = mid;
+            else hi = mid - 1;
+        }
+        seq = lo;
+        while (pre[seq + 1] <= x) ++seq;
+        const int per_head = (pre[seq + 1] - pre[seq]) / a.pg.hkv;
+        int rem = x - pre[seq];
+        head = rem / per_head;
+        rem -= head * per_head;
+        si = seq_info(a, seq);
+        tp = 0;
+        it = item_range(a, si, 0, rows2);
+        while (rem >= it.n) {
+            rem -= it.n;
+            it = item_range(a, si, ++tp, rows2);
+        }
+        b0 = rem;
+        b1 = min(it.n, b0 + (x_end - x));
+    }
+    __device__ __forceinline__ bool more() const { return x < x_end; }
+    __device__ __forceinline__ void next() {
+        x += b1 - b0;
+        if (x >= x_end) return;
+        if (++tp == tiles2(si.n_q, rows2)) {
+            tp = 0;
+            if (++head == a.pg.hkv) {
+                head = 0;
+                do ++seq;
+                while (pre[seq + 1] <= x);
+                si = seq_info(a, seq);
+            }
+        }
+        it = item_range(a, si, tp, rows2);
+        b0 = 0;
+        b1 = min(it.n, x_end - x);
+    }
+    __device__ __forceinline__ bool any_seen(int j0, int j1) const {
+        return j0 <= it.p_hi && (j0 < a.n_sink || j1 > it.p_lo - a.window);
+    }
+    __device__ __forceinline__ bool all_seen(int j0, int j1) const {
+        return j1 <= it.p_hi && (j1 < a.n_sink || j0 > it.p_lo - a.window);
+    }
+};
+
+// Eight bf16 values n s of a word with pairs (2i, 2i + 1) at bits 4 i and 16 + 4 i.
+__device__ __forceinline__ uint32_t pair_value(uint32_t w, int i, uint32_t scale2) {
+    uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+    const uint32_t off = 0x43084308u;
+    const __nv_bfloat162 n = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&off));
+    const __nv_bfloat162 v = __hmul2(n, *reinterpret_cast<__nv_bfloat162*>(&scale2));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t both(uint32_t w, int hi) { return __byte_perm(w, w, hi ? 0x3232 : 0x1010); }
+
+template <bool I4, int D>
+__global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
+    k_paged_tile(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                 const __grid_constant__ CUtensorMap mapV, const __grid_constant__ PagedAttn a, int rpt) {
+    using T = TileCfg<I4, D>;
+    constexpr int NH = T::NH, STAGES = T::STAGES, STAGE = T::STAGE, QT = T::QT, KB = T::KB, VCOL = T::VCOL;
+    constexpr int WARPS = T::THREADS / 32;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t q_full[2], q_empty[2], kv_full[STAGES], kv_empty[STAGES], s_full[NSBUF],
+        p_full[NSBUF], o_full, o_free, edge_full;
+    __shared__ uint32_t tmem_sh;
+    __shared__ volatile int abort_flag;
+    __shared__ int pend_kv[STAGES], pend_q[2], pend_edge;
+    __shared__ int pre[BLEND_MAX_SEQS + 1];
+
+    uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t* sQ = smem;              // Q buffer qb at qb * QT
+    uint8_t* sKV = smem + 2 * QT;    // stage s at s * STAGE: K column halves, V
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = (int)cta_rank();
+    const int grp = (int)(blockIdx.x >> 1), n_grp = (int)(gridDim.x >> 1);
+    const int rows2 = 2 * rpt, group = a.group, n_seq = a.pg.n_seq;
+
+    // ---- the line of blocks: pre[s] = blocks of all items of sequences before s
+    for (int s = warp; s < n_seq; s += WARPS) {
+        const SeqInfo si = seq_info(a, s);
+        int n = 0;
+        if (si.n_q * group > PAGED_MAX_TILE)  // shorter ones are the split kernel's
+            for (int tp = lane; tp < tiles2(si.n_q, rows2); tp += 32) n += item_range(a, si, tp, rows2).n;
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) pre[s + 1] = n * a.pg.hkv;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int base = 0;
+        for (int s0 = 0; s0 < n_seq; s0 += 32) {
+            const int s = s0 + lane;
+            int v = s < n_seq ? pre[s + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += y;
+            }
+            if (s < n_seq) pre[s + 1] = base + v;
+            base += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) pre[0] = 0;
+    }
+    __syncthreads();
+    const int total = pre[n_seq];
+    const int quota = max(MIN_QUOTA, (total + n_grp - 1) / n_grp);
+    const long long x64 = (long long)grp * quota;
+    if (x64 >= total) return;  // both CTAs of the cluster
+    const int x_first = (int)x64, x_end = (int)min((long long)total, x64 + quota);
+
+    // Lanes of a tile past its rows read a Q of zeros
+    for (int i = threadIdx.x; i < 2 * QT / 16; i += T::THREADS) reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
+    fence_async_smem();
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&q_full[b], 1);
+            mbar_init(&q_empty[b], 1);
+            pend_q[b] = -1;
+        }
+        for (int b = 0; b < NSBUF; ++b) {
+            mbar_init(&s_full[b], 1);
+            mbar_init(&p_full[b], 8);  // 4 softmax warps in each CTA
+        }
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&kv_full[s], I4 ? 8 : 2);  // 4 warps of each CTA, or each CTA's producer
+            mbar_init(&kv_empty[s], 1);
+            pend_kv[s] = -1;
+        }
+        mbar_init(&o_full, 1);
+        mbar_init(&o_free, 8);
+        mbar_init(&edge_full, 1);
+        pend_edge = -1;
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_smem();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&tmem_sh)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before either signals the other's
+    fence_after();
+    const uint32_t tb = tmem_sh;
+
+    if (warp == 0) {
+        // ------------------------------------------------ producer warp (both CTAs): Q, model pages
+        uint32_t it = 0, edges = 0;
+        bool ok = true;
+        int tl = 0;
+        const int kr_rows = min(1 << a.pg.shift, 64), v_rows = min(1 << a.pg.shift, TKEYS);
+        for (Walk w(a, pre, rows2, x_first, x_end); ok && w.more(); w.next(), ++tl) {
+            const int qb = tl & 1;
+            ok = warp_wait_cl(&q_empty[qb], ((tl >> 1) & 1) ^ 1, &abort_flag);
+            if (!ok) break;
+            if (lane == 0) {
+                if (rank == 0) {
+                    mbar_expect_tx(&q_full[qb], 2u * NH * 128u * (uint32_t)(group * rpt));  // both CTAs' tiles
+                    pend_q[qb] = (tl >> 1) & 1;
+                }
+                // an absent second tile reloads the first (finite data, never stored)
+                const int t_row = w.tp * rows2 + rank * rpt;
+                const int row = w.si.row0 + (t_row < w.si.n_q ? t_row : w.tp * rows2);
+                const uint32_t qf = leader_addr(&q_full[qb]);
+#pragma unroll
+                for (int hh = 0; hh < NH; ++hh) tma_4d_pair(sQ + qb * QT + hh * Q_HALF, &mapQ, qf, hh * 64, 0, w.head, row);
+            }
+            __syncwarp();
+            for (int b = w.b0; b < (I4 ? w.b0 : w.b1); ++b, ++it) {  // (4-bit pages have warps of their own)
+                const int st = it % STAGES;
+                ok = warp_wait_cl(&kv_empty[st], ((it / STAGES) & 1) ^ 1, &abort_flag);
+                if (!ok) break;
+                const int k0 = w.it.kr.block(b) * TKEYS;
+                const bool edge = !w.all_seen(k0, k0 + TKEYS - 1);
+                // lane i < 8: the page of the block's tokens 16 i..
+                int page = 0;
+                if (lane < 8 && w.any_seen(k0 + 16 * lane, k0 + 16 * lane + 15)) page = page_of(a.pg, w.seq, k0 + 16 * lane, a.err);
+                uint8_t* dst = sKV + st * STAGE;
+                const uint32_t kf = leader_addr(&kv_full[st]);
+                uint32_t k_bytes = 0, v_bytes = 0;
+                const int mask = (1 << a.pg.shift) - 1;
+                if (rank == 0 && lane == 0) pend_kv[st] = (int)((it / STAGES) & 1);
+                for (int u = 0; u < TKEYS; u += kr_rows) {  // both CTAs' keys are counted at the leader
+                    // the page of a piece is known to the first lane of it that sees a token: find one
+                    int pg = __shfl_sync(0xffffffffu, page, u / 16);
+                    const int j = k0 + u;
+                    if (!w.any_seen(j, j + kr_rows - 1)) continue;
+                    if (!w.any_seen(j, j + 15)) pg = page_of(a.pg, w.seq, j, a.err);
+                    k_bytes += (uint32_t)kr_rows * D * 2;
+                    if (u / 64 == rank && lane == 0)
+#pragma unroll
+                        for (int hh = 0; hh < NH; ++hh)
+                            tma_3d_pair(dst + hh * K_HALF + (u & 63) * 128, &mapK, kf, hh * 64, j & mask, pg * a.pg.hkv + w.head);
+                }
+                if (!edge) {
+                    for (int u = 0; u < TKEYS; u += v_rows) {
+                        const int pg = __shfl_sync(0xffffffffu, page, u / 16);
+                        if (lane == 0)
+                            tma_3d_pair(dst + KB + u * VCOL * 2, &mapV, kf, VCOL * rank, (k0 + u) & mask, pg * a.pg.hkv + w.head);
+                    }
+                    v_bytes = 2u * T::VB;  // both CTAs'
+                } else {
+                    uint32_t mine = 0;
+                    for (int u = 0; u < TKEYS; u += v_rows)
+                        if (w.any_seen(k0 + u, k0 + u + v_rows - 1)) mine += (uint32_t)v_rows * VCOL * 2;
+                    if (mine) {
+                        if (lane == 0) {
+                            mbar_expect_tx(&edge_full, mine);
+                            pend_edge = (int)(edges & 1);
+                        }
+                        for (int u = 0; u < TKEYS; u += v_rows) {
+                            const int j = k0 + u;
+                            if (!w.any_seen(j, j + v_rows - 1)) continue;
+                            const int pg = page_of(a.pg, w.seq, j, a.err);
+                            if (lane == 0)
+                                tma_3d(dst + KB + u * VCOL * 2, &mapV, &edge_full, VCOL * rank, j & mask, pg * a.pg.hkv + w.head);
+                        }
+                        ok = warp_wait(&edge_full, edges & 1, &abort_flag);
+                        if (!ok) break;
+                        if (lane == 0) pend_edge = -1;
+                        ++edges;
+                    }
+                    constexpr int CH = VCOL / 8;  // 16-byte chunks of a row (the swizzle stays within it)
+                    for (int i = lane; i < TKEYS * CH; i += 32) {
+                        const int j = k0 + i / CH;
+                        if (!w.any_seen(j, j)) *reinterpret_cast<uint4*>(dst + KB + i * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0) {
+                    if (rank == 0) mbar_expect_tx(&kv_full[st], k_bytes + v_bytes);
+                    else arrive_leader_release(&kv_full[st]);
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok) {
+            abort_flag = 1;
+            if (lane == 0) set_error(a.err, BLEND_ETIMEOUT);
+        }
+    } else if (warp == S_WARP && lane == 0 && rank == 0) {
+        // ------------------------------------------------ S issuer (leader, for both CTAs)
+        uint32_t it = 0;
+        bool ok = true;
+        int tl = 0;
+        for (Walk w(a, pre, rows2, x_first, x_end); ok && w.more(); w.next(), ++tl) {
+            const int qb = tl & 1;
+            if (!wait_cl(&q_full[qb], (tl >> 1) & 1, &abort_flag)) {
+                ok = false;
+                break;
+            }
+            pend_q[qb] = -1;
+            const uint64_t qd = desc_k(su32(sQ + qb * QT));
+            for (int b = w.b0; b < w.b1; ++b, ++it) {
+                const int sb = it % NSBUF, st = it % STAGES;
+                const uint32_t pv = it - NSBUF;  // the P.V that last read this buffer
+                if ((it >= NSBUF && !wait_cl(&kv_empty[pv % STAGES], (pv / STAGES) & 1, &abort_flag)) ||
+                    !wait_cl_acquire(&kv_full[st], (it / STAGES) & 1, &abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                pend_kv[st] = -1;
+                fence_after();
+                const uint64_t kd = desc_k(su32(sKV + st * STAGE));
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (kk & 3) * 32, half = kk >> 2;
+                    umma_ss2(tb + sb * 128, qd + ((half * Q_HALF + off) >> 4), kd + ((half * K_HALF + off) >> 4), T::IDESC_S,
+                             kk > 0 ? 1u : 0u);
+                }
+                commit2(&s_full[sb]);
+            }
+            if (!ok) break;
+            commit2(&q_empty[qb]);
+        }
+        if (!ok) {
+            abort_flag = 1;
+            set_error(a.err, BLEND_ETIMEOUT);
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // ------------------------------------------------ P.V issuer (leader, for both CTAs)
+        uint32_t it = 0;
+        bool ok = true;
+        int tl = 0;
+        for (Walk w(a, pre, rows2, x_first, x_end); ok && w.more(); w.next(), ++tl) {
+            for (int b = w.b0; b < w.b1; ++b, ++it) {
+                const int sb = it % NSBUF, st = it % STAGES;
+                if (!wait_cl(&p_full[sb], (it / NSBUF) & 1, &abort_flag) ||
+                    (b == w.b0 && !wait_cl(&o_free, (tl & 1) ^ 1, &abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                fence_after();
+                const uint64_t vd = desc_v<D>(su32(sKV + st * STAGE + KB));
+                const uint32_t pa = tb + sb * 128;
+#pragma unroll
+                for (int kk = 0; kk < TKEYS / 16; ++kk)
+                    umma_ts2(tb + O_COL, pa + kk * 8, vd + ((kk * 16 * VCOL * 2) >> 4), T::IDESC_PV,
+                             (b > w.b0 || kk > 0) ? 1u : 0u);
+                commit2(&kv_empty[st]);
+            }
+            if (!ok) break;
+            commit2(&o_full);
+        }
+        if (!ok) {
+            abort_flag = 1;
+            set_error(a.err, BLEND_ETIMEOUT);
+        }
+    } else if (warp >= 2 && warp < S_WARP) {
+        // ------------------------------------------------ softmax of this CTA's tile + output
+        const int sp = warp & 3;  // TMEM lane quarter of this warp
+        const int r_in = sp * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(sp * 32) << 16;
+        const uint32_t o_col = tb + lane_off + O_COL;
+        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
+        bf16* out = reinterpret_cast<bf16*>(a.out);
+        uint32_t it = 0;
+        bool ok = true;
+        int tl = 0;
+        for (Walk w(a, pre, rows2, x_first, x_end); ok && w.more(); w.next(), ++tl) {
+            const int t_row = w.tp * rows2 + rank * rpt;            // first row of this CTA's tile
+            const int rows = min(rpt, w.si.n_q - t_row);            // <= 0: the tile is absent
+            const bool valid = r_in < rows * group;
+            const int row = t_row + (valid ? r_in / group : 0);
+            const int first = w.si.len - w.si.n_q;
+            const int t_lo = first + t_row, t_hi = t_lo + max(rows, 1) - 1;
+            const int my_pos = valid ? first + row : t_lo;
+            // lanes without a row never hold up their warp: a reference of 0 keeps them off the exact path
+            float m_used = valid && my_pos >= 0 ? -INFINITY : 0.f, l = 0.f;
+            for (int b = w.b0; b < w.b1; ++b, ++it) {
+                const int sb = it % NSBUF;
+                const uint32_t s_col = tb + lane_off + sb * 128;
+                if (!warp_wait_cl(&s_full[sb], (it / NSBUF) & 1, &abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                fence_after();
+                const int k0 = w.it.kr.block(b) * TKEYS;
+                const bool cut = !all_see(k0, k0 + TKEYS - 1, t_lo, t_hi, a.window, a.n_sink);
+                uint32_t s[128];
+                auto load = [&]() {
+                    TMEM_LD32(s_col, s);
+                    TMEM_LD32(s_col + 32, (s + 32));
+                    TMEM_LD32(s_col + 64, (s + 64));
+                    TMEM_LD32(s_col + 96, (s + 96));
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                    if (cut) {
+                        const int hi = my_pos - k0, lo = hi - a.window, sink = a.n_sink - k0;
+#pragma unroll
+                        for (int i = 0; i < 128; ++i)
+                            if (!(i <= hi && (i > lo || i < sink))) s[i] = __float_as_uint(-INFINITY);
+                    }
+                };
+                load();
+                float2 accs = make_float2(0.f, 0.f);
+                auto weights = [&]() {
+                    float2 acc2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    const float ref = m_used == -INFINITY ? 0.f : -m_used;
+                    const float2 nm2 = make_float2(ref, ref);
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) {
+                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), sc2, nm2);
+                        const float p0 = ex2(x.x), p1 = ex2(x.y);
+                        acc2[e & 1] = __fadd2_rn(acc2[e & 1], make_float2(p0, p1));
+                        s[e] = pack_bf16x2(p0, p1);
+                    }
+                    accs = __fadd2_rn(acc2[0], acc2[1]);
+                };
+                bool rescale = false;
+                float corr = 1.f;
+                // as in k_attn_pair: without this block's maximum while its sum stays below 2^50
+                bool exact = !__all_sync(0xffffffffu, m_used != -INFINITY);
+                if (!exact) {
+                    weights();
+                    exact = __any_sync(0xffffffffu, !(accs.x + accs.y <= 0x1p50f));
+                    if (exact) load();
+                }
+                if (exact) {
+                    float mx;
+                    {
+                        float y[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[i] = fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 8]));
+#pragma unroll
+                        for (int i = 16; i < 128; i += 16)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                y[e] = max3f(y[e], __uint_as_float(s[i + e]), __uint_as_float(s[i + 8 + e]));
+                        mx = max3f(max3f(y[0], y[1], y[2]), max3f(y[3], y[4], y[5]), fmaxf(y[6], y[7]));
+                    }
+                    const float mxs = mx * a.scale_log2;
+                    const bool need = mxs > m_used + RESCALE_LOG2;
+                    rescale = __any_sync(0xffffffffu, need);
+                    if (rescale) {
+                        const float m_new = need ? mxs : m_used;
+                        corr = need ? ex2(m_used - m_new) : 1.f;
+                        l *= corr;
+                        m_used = m_new;
+                    }
+                    weights();
+                }
+                TMEM_ST32(s_col, s);
+                TMEM_ST32(s_col + 32, (s + 32));
+                if (rescale && b > w.b0) {
+                    const uint32_t pv = it - 1;  // O must hold every block before this one
+                    if (!warp_wait_cl(&kv_empty[pv % STAGES], (pv / STAGES) & 1, &abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
+#pragma unroll
+                    for (int e = 0; e < D; e += 32) {
+                        uint32_t o[32];
+                        TMEM_LD32(o_col + e, o);
+                        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+                        TMEM_ST32(o_col + e, o);
+                    }
+                }
+                l += accs.x + accs.y;
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                fence_before();
+                warp_arrive_leader(&p_full[sb], rank);
+            }
+            if (!ok) break;
+            if (!warp_wait_cl(&o_full, tl & 1, &abort_flag)) {
+                ok = false;
+                break;
+            }
+            fence_after();
+            const bool whole = w.b0 == 0 && w.b1 == w.it.n;
+            bf16* dst = out + ((long long)(w.si.row0 + row) * a.hq + w.head * group + (valid ? r_in % group : 0)) * D;
+            if (whole) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+                for (int e = 0; e < D; e += 32) {
+                    uint32_t o[32];
+                    TMEM_LD32(o_col + e, o);
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                    if (valid) {
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            uint32_t w4[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                w4[i] = pack_bf16x2(__uint_as_float(o[v * 8 + 2 * i]) * inv,
+                                                    __uint_as_float(o[v * 8 + 2 * i + 1]) * inv);
+                            *reinterpret_cast<uint4*>(dst + e + v * 8) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                        }
+                    }
+                }
+                fence_before();
+                warp_arrive_leader(&o_free, rank);
+                continue;
+            }
+            // ---- part of an item: leave it, and join the parts of these 32 rows when last to arrive
+            const int item0 = w.x - w.b0, g_first = item0 / quota, n_part = (item0 + w.it.n - 1) / quota - g_first + 1;
+            auto slot = [&](int g, int which) { return a.part + (size_t)((2 * g + which) * 2 + rank) * T::PART; };
+            float* mine = slot(grp, w.b0 == 0 ? 1 : 0);
+#pragma unroll
+            for (int e = 0; e < D; e += 32) {
+                uint32_t o[32];
+                TMEM_LD32(o_col + e, o);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                for (int v = 0; v < 8; ++v)
+                    *reinterpret_cast<uint4*>(mine + (size_t)((e / 4 + v) * TQ + r_in) * 4) =
+                        make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+            }
+            mine[TQ * D + r_in] = m_used;
+            mine[TQ * (D + 1) + r_in] = l;
+            fence_before();
+            warp_arrive_leader(&o_free, rank);  // O may be written again
+            __threadfence();
+            __syncwarp();
+            int last = 0;
+            int32_t* count = a.count + (g_first * 2 + rank) * 4 + sp;
+            if (lane == 0) {
+                last = atomicAdd(count, 1) == n_part - 1;
+                if (last) *count = 0;  // ready for the next launch
+            }
+            last = __shfl_sync(0xffffffffu, last, 0);
+            if (!last) continue;
+            __threadfence();
+            // part k lies with cluster g_first + k: in its slot 1 when the item starts there, else in slot 0
+            float mx = -INFINITY, sum = 0.f;
+            for (int k = 0; k < n_part; ++k) mx = max_nan(mx, __ldcg(slot(g_first + k, k == 0) + TQ * D + r_in));
+            const float ref = mx == -INFINITY ? 0.f : mx;
+            float acc[D];
+#pragma unroll
+            for (int e = 0; e < D; ++e) acc[e] = 0.f;
+            for (int k = 0; k < n_part; ++k) {
+                const float* p = slot(g_first + k, k == 0);
+                const float f = ex2(__ldcg(p + TQ * D + r_in) - ref);
+                sum += __ldcg(p + TQ * (D + 1) + r_in) * f;
+#pragma unroll
+                for (int e = 0; e < D / 4; ++e) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(p) + e * TQ + r_in);
+                    acc[4 * e] = fmaf(v.x, f, acc[4 * e]);
+                    acc[4 * e + 1] = fmaf(v.y, f, acc[4 * e + 1]);
+                    acc[4 * e + 2] = fmaf(v.z, f, acc[4 * e + 2]);
+                    acc[4 * e + 3] = fmaf(v.w, f, acc[4 * e + 3]);
+                }
+            }
+            if (valid) {
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+                for (int v = 0; v < D / 8; ++v) {
+                    uint32_t w4[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w4[i] = pack_bf16x2(acc[v * 8 + 2 * i] * inv, acc[v * 8 + 2 * i + 1] * inv);
+                    *reinterpret_cast<uint4*>(dst + v * 8) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                }
+            }
+        }
+        if (!ok) {
+            abort_flag = 1;
+            if (lane == 0) set_error(a.err, BLEND_ETIMEOUT);
+        }
+    } else if (I4 && warp > S_WARP) {
+        // ------------------------------------------------ 4-bit pages to bf16 operands (both CTAs)
+        const int t = threadIdx.x - (S_WARP + 1) * 32;  // V: token t of the block; K: half a row of this CTA's token t / 2
+        constexpr int RB = D / 2, SB = D / 16;          // bytes of a row and of its scales
+        uint32_t kw[D / 16], vw[8], ksc[D / 64], vsc = 0;  // raw words of the next block
+        const int mask = (1 << a.pg.shift) - 1;
+        auto fetch = [&](const Walk& w, int b) {
+            const int k0 = w.it.kr.block(b) * TKEYS;
+            const int jk = k0 + 64 * rank + (t >> 1), jv = k0 + t;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) kw[i] = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) vw[i] = 0;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) ksc[i] = 0;
+            vsc = 0;
+            if (w.any_seen(jk, jk)) {
+                const long long row = page_row(a.pg, page_of(a.pg, w.seq, jk, a.err), w.head, jk & mask);
+                const uint4* p = reinterpret_cast<const uint4*>(a.pg.k + row * RB) + (t & 1) * (D / 64);
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    const uint4 v = __ldg(p + i);
+                    kw[4 * i] = v.x; kw[4 * i + 1] = v.y; kw[4 * i + 2] = v.z; kw[4 * i + 3] = v.w;
+                }
+                const uint32_t* sp = reinterpret_cast<const uint32_t*>(a.pg.ks + row * SB);
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) ksc[i] = __ldg(sp + i);
+            }
+            if (w.any_seen(jv, jv)) {
+                const long long row = page_row(a.pg, page_of(a.pg, w.seq, jv, a.err), w.head, jv & mask);
+                const uint4* p = reinterpret_cast<const uint4*>(a.pg.v + row * RB);
+                if constexpr (D == 128) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {  // word r: groups 2 rank, 2 rank + 1 of half r
+                        const uint4 v = __ldg(p + i);
+                        vw[2 * i] = rank ? v.y : v.x;
+                        vw[2 * i + 1] = rank ? v.w : v.z;
+                    }
+                    vsc = __ldg(reinterpret_cast<const uint32_t*>(a.pg.vs + row * SB) + rank);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {  // word r: groups 0, 1 of half r
+                        const uint4 v = __ldg(p + i);
+                        vw[4 * i] = v.x; vw[4 * i + 1] = v.y; vw[4 * i + 2] = v.z; vw[4 * i + 3] = v.w;
+                    }
+                    vsc = __ldg(reinterpret_cast<const uint32_t*>(a.pg.vs + row * SB));
+                }
+            }
+        };
+        uint32_t it = 0;
+        bool ok = true;
+        Walk w(a, pre, rows2, x_first, x_end);
+        int b = w.b0;
+        fetch(w, b);
+        while (ok) {
+            const int st = it % STAGES;
+            ok = warp_wait_cl(&kv_empty[st], ((it / STAGES) & 1) ^ 1, &abort_flag);
+            if (!ok) break;
+            uint8_t* dk = sKV + st * STAGE;
+            const int tk = t >> 1;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                // word i of this half row: c = 2 (t & 1) + i / G, g = i % G  (G = D / 32 words per c)
+                constexpr int G = D / 32;
+                const int c = 2 * (t & 1) + i / G, g = i % G;
+                const uint32_t sc = both(ksc[g >> 1], g & 1);
+                const int ch = 4 * (g & 1) + c;
+                *reinterpret_cast<uint4*>(dk + (g >> 1) * K_HALF + tk * 128 + ((ch ^ (tk & 7)) << 4)) =
+                    make_uint4(pair_value(kw[i], 0, sc), pair_value(kw[i], 1, sc), pair_value(kw[i], 2, sc), pair_value(kw[i], 3, sc));
+            }
+            uint8_t* dv = dk + KB;
+#pragma unroll
+            for (int g = 0; g < (D == 128 ? 2 : 1); ++g)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int hi = D == 128 ? g : rank;  // which 16-bit half of the words
+                    const uint32_t sc = both(vsc, hi);
+                    const uint32_t h0 = (hi ? vw[2 * c] >> 16 : vw[2 * c] & 0xffffu), h1 = (hi ? vw[2 * c + 1] >> 16 : vw[2 * c + 1] & 0xffffu);
+                    const uint32_t y0 = h0 | (h0 << 12), y1 = h1 | (h1 << 12);  // nibbles 0, 1 and 2, 3 as pairs at bits 0 and 8
+                    const int ch = 4 * g + c;
+                    const int at = D == 128 ? t * 128 + ((ch ^ (t & 7)) << 4) : t * 64 + ((ch ^ ((t >> 1) & 3)) << 4);
+                    *reinterpret_cast<uint4*>(dv + at) = make_uint4(pair_value(y0, 0, sc), pair_value(y0, 2, sc), pair_value(y1, 0, sc), pair_value(y1, 2, sc));
+                }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_leader_release(&kv_full[st]);
+            ++it;
+            if (++b == w.b1) {
+                w.next();
+                if (!w.more()) break;
+                b = w.b0;
+            }
+            fetch(w, b);
+        }
+        if (!ok) {
+            abort_flag = 1;
+            if (lane == 0) set_error(a.err, BLEND_ETIMEOUT);
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && abort_flag) {
+        // let the copies still in flight land before the shared memory is released
+        if (rank == 0 && !I4)
+            for (int s = 0; s < STAGES; ++s)
+                if (pend_kv[s] >= 0)
+                    for (long long i = 0; i < SPIN_LIMIT && !mbar_try(&kv_full[s], (uint32_t)pend_kv[s]); ++i) {
+                    }
+        if (rank == 0)
+            for (int b = 0; b < 2; ++b)
+                if (pend_q[b] >= 0)
+                    for (long long i = 0; i < SPIN_LIMIT && !mbar_try(&q_full[b], (uint32_t)pend_q[b]); ++i) {
+                    }
+        if (pend_edge >= 0)
+            for (long long i = 0; i < SPIN_LIMIT && !mbar_try(&edge_full, (uint32_t)pend_edge); ++i) {
+            }
+    }
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves while the other may still signal its barriers
+    if (warp == 1) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tb), "r"(TMEM_COLS) : "memory");
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 g_enc = nullptr;
+
+bool encode(CUtensorMap* map, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return g_enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, es,
+                 CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool I4, int D> int launch_tile(const PagedAttn& a, cudaStream_t s) {
+    using T = TileCfg<I4, D>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(T::THREADS);
+    cfg.dynamicSmemBytes = T::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    static int clusters = -1;
+    if (clusters < 0) {
+        cudaFuncSetAttribute(k_paged_tile<I4, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+        cfg.gridDim = dim3(2 * MAX_CLUSTERS);
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, k_paged_tile<I4, D>, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        clusters = n < MAX_CLUSTERS ? n : MAX_CLUSTERS;
+    }
+    if (clusters <= 0) return BLEND_EUNSUPPORTED;
+    const int rpt = TQ / a.group, page = 1 << a.pg.shift;
+    CUtensorMap mq, mk, mv;
+    const cuuint64_t qd[4] = {(cuuint64_t)D, (cuuint64_t)a.group, (cuuint64_t)a.pg.hkv, (cuuint64_t)a.max_rows};
+    const cuuint64_t qs[3] = {(cuuint64_t)D * 2, (cuuint64_t)a.group * D * 2, (cuuint64_t)a.ld_q * 2};
+    const cuuint32_t qb[4] = {64, (cuuint32_t)a.group, 1, (cuuint32_t)rpt};
+    if (!encode(&mq, 4, a.q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B)) return BLEND_EUNSUPPORTED;
+    mk = mv = mq;  // not read for 4-bit pages
+    if (!I4) {
+        const cuuint64_t kd[3] = {(cuuint64_t)D, (cuuint64_t)page, (cuuint64_t)a.pg.hkv * a.pg.n_pages};
+        const cuuint64_t ks[2] = {(cuuint64_t)D * 2, (cuuint64_t)page * D * 2};
+        const cuuint32_t kb[3] = {64, (cuuint32_t)(page < 64 ? page : 64), 1};
+        const cuuint32_t vb[3] = {(cuuint32_t)T::VCOL, (cuuint32_t)page, 1};
+        if (!encode(&mk, 3, a.pg.k, kd, ks, kb, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode(&mv, 3, a.pg.v, kd, ks, vb, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+            return BLEND_EUNSUPPORTED;
+    }
+    cfg.gridDim = dim3(2 * clusters);
+    if (cudaLaunchKernelEx(&cfg, k_paged_tile<I4, D>, mq, mk, mv, a, rpt) != cudaSuccess) return BLEND_ECUDA;
+    note_launch(1);
+    return BLEND_OK;
+}
+
+}  // namespace
+
+int launch_paged_attn_tile(bool i4, const PagedAttn& a, int d, cudaStream_t s) {
+    if (!g_enc) {
+        cudaDriverEntryPointQueryResult qr;
+        void* fn = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &qr) !=
+                cudaSuccess ||
+            qr != cudaDriverEntryPointSuccess || !fn)
+            return BLEND_EUNSUPPORTED;
+        g_enc = (PFN_cuTensorMapEncodeTiled_v12000)fn;
+    }
+    if (i4) return d == 64 ? launch_tile<true, 64>(a, s) : launch_tile<true, 128>(a, s);
+    return d == 64 ? launch_tile<false, 64>(a, s) : launch_tile<false, 128>(a, s);
+}
+
+}  // namespace blend
