@@ -118,6 +118,18 @@ __device__ __forceinline__ bool all_see(int j0, int j1, int p0, int p1, int wind
     return j1 <= p0 && (j0 > p1 - window || j1 < n_sink);
 }
 
+// ---- cp.async
+// BYTES from global to shared memory; zeros when !ok.
+template <int BYTES> __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool ok) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(ok ? BYTES : 0)
+                     : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // Maximum that keeps a NaN: a running maximum that dropped one would give its row no weight
 // when the shares of the keys are joined.
 __device__ __forceinline__ float max_nan(float a, float b) {

@@ -47,8 +47,12 @@ template <bool I4, int D> struct TileCfg {
     static constexpr int KB = NH * K_HALF;
     static constexpr int VB = TKEYS * VCOL * 2;
     static constexpr int STAGE = KB + VB;
-    static constexpr int STAGES = D == 128 ? 4 : 8;
-    static constexpr int SMEM = 2 * QT + STAGES * STAGE + 1024;
+    static constexpr int STAGES = D == 64 ? 8 : I4 ? 3 : 4;
+    // 4-bit pages: raw rows on their way, a slot per thread (half a K row, a V row, their scales)
+    static constexpr int RAW_STAGES = 4;
+    static constexpr int SB = D / 16;
+    static constexpr int RAW = I4 ? 128 * (D / 4 + D / 2 + 2 * SB) : 0;
+    static constexpr int SMEM = 2 * QT + STAGES * STAGE + RAW_STAGES * RAW + 1024;
     // kind::f16, bf16 inputs, fp32 accumulate, M256 (the pair); S: N128, P.V: N = D with B MN-major
     static constexpr uint32_t IDESC_S = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((256u >> 4) << 24);
     static constexpr uint32_t IDESC_PV =
@@ -77,6 +81,18 @@ __device__ __forceinline__ void tma_4d_pair(void* dst, const CUtensorMap* m, uin
 // Arrival on the leader's barrier that publishes this thread's shared-memory writes to the pair.
 __device__ __forceinline__ void arrive_leader_release(uint64_t* b) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(b)) : "memory");
+}
+// Warp-level bounded wait by polling: a blocking try_wait on a barrier that the other CTA's commits
+// reach resumes late (see test_cl), which a producer cannot hide.
+__device__ __forceinline__ bool warp_poll(uint64_t* b, uint32_t par, volatile int* abort_flag) {
+    for (long long i = 0; i < 64 * SPIN_LIMIT; ++i) {
+        if (__all_sync(0xffffffffu, test_cl(b, par))) return true;
+        if ((i & 1023) == 1023 && __any_sync(0xffffffffu, *abort_flag != 0)) return false;
+    }
+    return false;
+}
+__device__ __forceinline__ void arrive_leader(uint64_t* b) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(b)) : "memory");
 }
 __device__ __forceinline__ bool wait_cl_acquire(uint64_t* b, uint32_t par, volatile int* abort_flag) {
     for (long long i = 0; i < 64 * SPIN_LIMIT; ++i) {
@@ -189,7 +205,7 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
     constexpr int WARPS = T::THREADS / 32;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t q_full[2], q_empty[2], kv_full[STAGES], kv_empty[STAGES], s_full[NSBUF],
-        p_full[NSBUF], o_full, o_free, edge_full;
+        p_full[NSBUF], o_full, o_free, edge_full, own_full[STAGES];
     __shared__ uint32_t tmem_sh;
     __shared__ volatile int abort_flag;
     __shared__ int pend_kv[STAGES], pend_q[2], pend_edge;
@@ -249,7 +265,8 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
             mbar_init(&p_full[b], 8);  // 4 softmax warps in each CTA
         }
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&kv_full[s], I4 ? 8 : 2);  // 4 warps of each CTA, or each CTA's producer
+            mbar_init(&kv_full[s], 2);  // each CTA's producer warp
+            mbar_init(&own_full[s], 4);  // 4-bit pages: this CTA's dequantising warps
             mbar_init(&kv_empty[s], 1);
             pend_kv[s] = -1;
         }
@@ -275,76 +292,85 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------ producer warp (both CTAs): Q, model pages
+        // Lane i owns one box of every block: first the CTA's 64 keys by pages and column halves, then
+        // the 128 keys' V columns by pages.  The page of its next box is read a block ahead.
+        const int k_rows = min(1 << a.pg.shift, 64), v_rows = 1 << a.pg.shift;
+        const int n_k = (64 / k_rows) * NH, n_v = TKEYS / v_rows;
+        const bool is_k = lane < n_k, mine = !I4 && lane < n_k + n_v;
+        const int piece = is_k ? lane / NH : lane - n_k;
+        const int rows = is_k ? k_rows : v_rows;
+        const int tok = is_k ? 64 * rank + piece * k_rows : piece * v_rows;  // first token of the box in a block
+        const int col = is_k ? (lane % NH) * 64 : VCOL * rank;
+        const int box_at = is_k ? (lane % NH) * K_HALF + piece * k_rows * 128 : KB + tok * VCOL * 2;
+        const int page_mask = (1 << a.pg.shift) - 1;
         uint32_t it = 0, edges = 0;
         bool ok = true;
-        int tl = 0;
-        const int kr_rows = min(1 << a.pg.shift, 64), v_rows = min(1 << a.pg.shift, TKEYS);
-        for (Walk w(a, pre, rows2, x_first, x_end); ok && w.more(); w.next(), ++tl) {
-            const int qb = tl & 1;
-            ok = warp_wait_cl(&q_empty[qb], ((tl >> 1) & 1) ^ 1, &abort_flag);
-            if (!ok) break;
-            if (lane == 0) {
-                if (rank == 0) {
-                    mbar_expect_tx(&q_full[qb], 2u * NH * 128u * (uint32_t)(group * rpt));  // both CTAs' tiles
-                    pend_q[qb] = (tl >> 1) & 1;
-                }
-                // an absent second tile reloads the first (finite data, never stored)
-                const int t_row = w.tp * rows2 + rank * rpt;
-                const int row = w.si.row0 + (t_row < w.si.n_q ? t_row : w.tp * rows2);
-                const uint32_t qf = leader_addr(&q_full[qb]);
-#pragma unroll
-                for (int hh = 0; hh < NH; ++hh) tma_4d_pair(sQ + qb * QT + hh * Q_HALF, &mapQ, qf, hh * 64, 0, w.head, row);
-            }
-            __syncwarp();
-            for (int b = w.b0; b < (I4 ? w.b0 : w.b1); ++b, ++it) {  // (4-bit pages have warps of their own)
-                const int st = it % STAGES;
-                ok = warp_wait_cl(&kv_empty[st], ((it / STAGES) & 1) ^ 1, &abort_flag);
+        int tl = 0, page = 0, k0 = 0;
+        bool need = false;
+        Walk w(a, pre, rows2, x_first, x_end);
+        int b = w.b0;
+        auto look = [&]() {  // this lane's box of block b: whether a row sees any of it, and its page
+            k0 = w.it.kr.block(b) * TKEYS;
+            need = mine && w.any_seen(k0 + tok, k0 + tok + rows - 1);
+            page = need ? page_of(a.pg, w.seq, k0 + tok, a.err) : 0;
+        };
+        look();
+        while (ok) {
+            if (b == w.b0) {
+                const int qb = tl & 1;
+                ok = warp_poll(&q_empty[qb], ((tl >> 1) & 1) ^ 1, &abort_flag);
                 if (!ok) break;
-                const int k0 = w.it.kr.block(b) * TKEYS;
+                if (lane == 0) {
+                    if (rank == 0) {
+                        mbar_expect_tx(&q_full[qb], 2u * NH * 128u * (uint32_t)(group * rpt));  // both CTAs' tiles
+                        pend_q[qb] = (tl >> 1) & 1;
+                    }
+                    // an absent second tile reloads the first (finite data, never stored)
+                    const int t_row = w.tp * rows2 + rank * rpt;
+                    const int row = w.si.row0 + (t_row < w.si.n_q ? t_row : w.tp * rows2);
+                    const uint32_t qf = leader_addr(&q_full[qb]);
+#pragma unroll
+                    for (int hh = 0; hh < NH; ++hh) tma_4d_pair(sQ + qb * QT + hh * Q_HALF, &mapQ, qf, hh * 64, 0, w.head, row);
+                }
+                __syncwarp();
+                ++tl;
+            }
+            const int st = it % STAGES;
+            if constexpr (I4) {
+                // the dequantising warps' rows, passed on to the leader: one release to the cluster per
+                // block instead of one per warp, and off those warps' path
+                ok = warp_poll(&own_full[st], (it / STAGES) & 1, &abort_flag);
+                if (!ok) break;
+                if (lane == 0) arrive_leader_release(&kv_full[st]);
+                __syncwarp();
+            } else {
+                ok = warp_poll(&kv_empty[st], ((it / STAGES) & 1) ^ 1, &abort_flag);
+                if (!ok) break;
                 const bool edge = !w.all_seen(k0, k0 + TKEYS - 1);
-                // lane i < 8: the page of the block's tokens 16 i..
-                int page = 0;
-                if (lane < 8 && w.any_seen(k0 + 16 * lane, k0 + 16 * lane + 15)) page = page_of(a.pg, w.seq, k0 + 16 * lane, a.err);
                 uint8_t* dst = sKV + st * STAGE;
                 const uint32_t kf = leader_addr(&kv_full[st]);
-                uint32_t k_bytes = 0, v_bytes = 0;
-                const int mask = (1 << a.pg.shift) - 1;
+                uint32_t bytes = 2u * (KB + T::VB);  // both CTAs' boxes count at the leader
                 if (rank == 0 && lane == 0) pend_kv[st] = (int)((it / STAGES) & 1);
-                for (int u = 0; u < TKEYS; u += kr_rows) {  // both CTAs' keys are counted at the leader
-                    // the page of a piece is known to the first lane of it that sees a token: find one
-                    int pg = __shfl_sync(0xffffffffu, page, u / 16);
-                    const int j = k0 + u;
-                    if (!w.any_seen(j, j + kr_rows - 1)) continue;
-                    if (!w.any_seen(j, j + 15)) pg = page_of(a.pg, w.seq, j, a.err);
-                    k_bytes += (uint32_t)kr_rows * D * 2;
-                    if (u / 64 == rank && lane == 0)
-#pragma unroll
-                        for (int hh = 0; hh < NH; ++hh)
-                            tma_3d_pair(dst + hh * K_HALF + (u & 63) * 128, &mapK, kf, hh * 64, j & mask, pg * a.pg.hkv + w.head);
-                }
                 if (!edge) {
-                    for (int u = 0; u < TKEYS; u += v_rows) {
-                        const int pg = __shfl_sync(0xffffffffu, page, u / 16);
-                        if (lane == 0)
-                            tma_3d_pair(dst + KB + u * VCOL * 2, &mapV, kf, VCOL * rank, (k0 + u) & mask, pg * a.pg.hkv + w.head);
-                    }
-                    v_bytes = 2u * T::VB;  // both CTAs'
+                    if (mine)
+                        tma_3d_pair(dst + box_at, is_k ? &mapK : &mapV, kf, col, (k0 + tok) & page_mask, page * a.pg.hkv + w.head);
                 } else {
-                    uint32_t mine = 0;
-                    for (int u = 0; u < TKEYS; u += v_rows)
-                        if (w.any_seen(k0 + u, k0 + u + v_rows - 1)) mine += (uint32_t)v_rows * VCOL * 2;
-                    if (mine) {
-                        if (lane == 0) {
-                            mbar_expect_tx(&edge_full, mine);
-                            pend_edge = (int)(edges & 1);
-                        }
-                        for (int u = 0; u < TKEYS; u += v_rows) {
-                            const int j = k0 + u;
-                            if (!w.any_seen(j, j + v_rows - 1)) continue;
-                            const int pg = page_of(a.pg, w.seq, j, a.err);
-                            if (lane == 0)
-                                tma_3d(dst + KB + u * VCOL * 2, &mapV, &edge_full, VCOL * rank, j & mask, pg * a.pg.hkv + w.head);
-                        }
+                    const unsigned k_seen = __ballot_sync(0xffffffffu, lane * k_rows < TKEYS && w.any_seen(k0 + lane * k_rows, k0 + (lane + 1) * k_rows - 1));
+                    bytes = (uint32_t)__popc(k_seen) * (uint32_t)k_rows * D * 2;
+                    const unsigned v_seen = __ballot_sync(0xffffffffu, need && !is_k);
+                    if (lane == 0 && v_seen) {
+                        mbar_expect_tx(&edge_full, (uint32_t)__popc(v_seen) * (uint32_t)v_rows * VCOL * 2);
+                        pend_edge = (int)(edges & 1);
+                    }
+                    __syncwarp();
+                    if (need) {
+                        if (is_k)
+                            tma_3d_pair(dst + box_at, &mapK, kf, col, (k0 + tok) & page_mask, page * a.pg.hkv + w.head);
+                        else
+                            tma_3d(dst + box_at, &mapV, &edge_full, col, (k0 + tok) & page_mask, page * a.pg.hkv + w.head);
+                    }
+                    __syncwarp();
+                    if (v_seen) {
                         ok = warp_wait(&edge_full, edges & 1, &abort_flag);
                         if (!ok) break;
                         if (lane == 0) pend_edge = -1;
@@ -359,11 +385,19 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                     __syncwarp();
                 }
                 if (lane == 0) {
-                    if (rank == 0) mbar_expect_tx(&kv_full[st], k_bytes + v_bytes);
-                    else arrive_leader_release(&kv_full[st]);
+                    if (rank == 0) mbar_expect_tx(&kv_full[st], bytes);
+                    else if (edge) arrive_leader_release(&kv_full[st]);
+                    else arrive_leader(&kv_full[st]);  // nothing of this thread's to publish: the boxes count themselves
                 }
                 __syncwarp();
             }
+            ++it;
+            if (++b == w.b1) {
+                w.next();
+                if (!w.more()) break;
+                b = w.b0;
+            }
+            if constexpr (!I4) look();
         }
         if (!ok) {
             abort_flag = 1;
@@ -651,61 +685,80 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
         }
     } else if (I4 && warp > S_WARP) {
         // ------------------------------------------------ 4-bit pages to bf16 operands (both CTAs)
+        // Each thread copies its own raw rows RAW_STAGES - 1 blocks ahead with cp.async, so it waits
+        // for its own copies alone; their pages are read one block earlier still.
         const int t = threadIdx.x - (S_WARP + 1) * 32;  // V: token t of the block; K: half a row of this CTA's token t / 2
-        constexpr int RB = D / 2, SB = D / 16;          // bytes of a row and of its scales
-        uint32_t kw[D / 16], vw[8], ksc[D / 64], vsc = 0;  // raw words of the next block
-        const int mask = (1 << a.pg.shift) - 1;
-        auto fetch = [&](const Walk& w, int b) {
-            const int k0 = w.it.kr.block(b) * TKEYS;
-            const int jk = k0 + 64 * rank + (t >> 1), jv = k0 + t;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) kw[i] = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) vw[i] = 0;
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) ksc[i] = 0;
-            vsc = 0;
-            if (w.any_seen(jk, jk)) {
-                const long long row = page_row(a.pg, page_of(a.pg, w.seq, jk, a.err), w.head, jk & mask);
-                const uint4* p = reinterpret_cast<const uint4*>(a.pg.k + row * RB) + (t & 1) * (D / 64);
-#pragma unroll
-                for (int i = 0; i < D / 64; ++i) {
-                    const uint4 v = __ldg(p + i);
-                    kw[4 * i] = v.x; kw[4 * i + 1] = v.y; kw[4 * i + 2] = v.z; kw[4 * i + 3] = v.w;
-                }
-                const uint32_t* sp = reinterpret_cast<const uint32_t*>(a.pg.ks + row * SB);
-#pragma unroll
-                for (int i = 0; i < D / 64; ++i) ksc[i] = __ldg(sp + i);
-            }
-            if (w.any_seen(jv, jv)) {
-                const long long row = page_row(a.pg, page_of(a.pg, w.seq, jv, a.err), w.head, jv & mask);
-                const uint4* p = reinterpret_cast<const uint4*>(a.pg.v + row * RB);
-                if constexpr (D == 128) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {  // word r: groups 2 rank, 2 rank + 1 of half r
-                        const uint4 v = __ldg(p + i);
-                        vw[2 * i] = rank ? v.y : v.x;
-                        vw[2 * i + 1] = rank ? v.w : v.z;
-                    }
-                    vsc = __ldg(reinterpret_cast<const uint32_t*>(a.pg.vs + row * SB) + rank);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {  // word r: groups 0, 1 of half r
-                        const uint4 v = __ldg(p + i);
-                        vw[4 * i] = v.x; vw[4 * i + 1] = v.y; vw[4 * i + 2] = v.z; vw[4 * i + 3] = v.w;
-                    }
-                    vsc = __ldg(reinterpret_cast<const uint32_t*>(a.pg.vs + row * SB));
-                }
-            }
-        };
-        uint32_t it = 0;
-        bool ok = true;
+        constexpr int RB = D / 2, SB = T::SB, RS = T::RAW_STAGES;
+        constexpr int VAT = 128 * (D / 4), KSAT = VAT + 128 * (D / 2), VSAT = KSAT + 128 * SB;  // in a raw stage
+        uint8_t* raw = sKV + STAGES * STAGE;
+        const int page_mask = (1 << a.pg.shift) - 1;
+        const int n_blocks = x_end - x_first;
         Walk w(a, pre, rows2, x_first, x_end);
-        int b = w.b0;
-        fetch(w, b);
-        while (ok) {
-            const int st = it % STAGES;
-            ok = warp_wait_cl(&kv_empty[st], ((it / STAGES) & 1) ^ 1, &abort_flag);
+        int b = w.b0, jk = 0, jv = 0, pk = 0, pv = 0;
+        bool sk = false, sv = false;
+        auto look = [&]() {
+            const int k0 = w.it.kr.block(b) * TKEYS;
+            jk = k0 + 64 * rank + (t >> 1);
+            jv = k0 + t;
+            sk = w.any_seen(jk, jk);
+            sv = w.any_seen(jv, jv);
+            pk = sk ? page_of(a.pg, w.seq, jk, a.err) : 0;
+            pv = sv ? page_of(a.pg, w.seq, jv, a.err) : 0;
+        };
+        auto copy = [&](int stage) {  // the block that look() saw, zeros for what no row sees
+            const uint32_t dst = su32(raw + stage * T::RAW);
+            const long long rk = page_row(a.pg, pk, w.head, jk & page_mask), rv = page_row(a.pg, pv, w.head, jv & page_mask);
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) cp_async<16>(dst + (i * 128 + t) * 16, a.pg.k + rk * RB + (t & 1) * (D / 4) + i * 16, sk);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) cp_async<16>(dst + VAT + (i * 128 + t) * 16, a.pg.v + rv * RB + i * 16, sv);
+            cp_async<SB>(dst + KSAT + t * SB, a.pg.ks + rk * SB, sk);
+            cp_async<SB>(dst + VSAT + t * SB, a.pg.vs + rv * SB, sv);
+        };
+        auto step = [&](int stage) {
+            if (!w.more()) return;
+            copy(stage);
+            if (++b == w.b1) {
+                w.next();
+                if (!w.more()) return;
+                b = w.b0;
+            }
+            look();
+        };
+        look();
+        for (int i = 0; i < RS - 1; ++i) {
+            step(i);
+            cp_commit();
+        }
+        bool ok = true;
+        for (int i = 0; i < n_blocks; ++i) {
+            const int st = i % STAGES;
+            step((i + RS - 1) % RS);
+            cp_commit();
+            cp_wait<RS - 1>();
+            uint32_t kw[D / 16], vw[8], ksc[D / 64], vsc;
+            {
+                const uint8_t* p = raw + (i % RS) * T::RAW;
+#pragma unroll
+                for (int q = 0; q < D / 64; ++q) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(p + (q * 128 + t) * 16);
+                    kw[4 * q] = v.x; kw[4 * q + 1] = v.y; kw[4 * q + 2] = v.z; kw[4 * q + 3] = v.w;
+                }
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(p + VAT + (q * 128 + t) * 16);
+                    if constexpr (D == 128) {  // word r: groups 2 rank, 2 rank + 1 of half r
+                        vw[2 * q] = rank ? v.y : v.x;
+                        vw[2 * q + 1] = rank ? v.w : v.z;
+                    } else {  // word r: groups 0, 1 of half r
+                        vw[4 * q] = v.x; vw[4 * q + 1] = v.y; vw[4 * q + 2] = v.z; vw[4 * q + 3] = v.w;
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < D / 64; ++q) ksc[q] = *reinterpret_cast<const uint32_t*>(p + KSAT + t * SB + 4 * q);
+                vsc = *reinterpret_cast<const uint32_t*>(p + VSAT + t * SB + (D == 128 ? 4 * rank : 0));
+            }
+            ok = warp_poll(&kv_empty[st], ((i / STAGES) & 1) ^ 1, &abort_flag);
             if (!ok) break;
             uint8_t* dk = sKV + st * STAGE;
             const int tk = t >> 1;
@@ -733,16 +786,9 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                     *reinterpret_cast<uint4*>(dv + at) = make_uint4(pair_value(y0, 0, sc), pair_value(y0, 2, sc), pair_value(y1, 0, sc), pair_value(y1, 2, sc));
                 }
             fence_async_smem();
-            __syncwarp();
-            if (lane == 0) arrive_leader_release(&kv_full[st]);
-            ++it;
-            if (++b == w.b1) {
-                w.next();
-                if (!w.more()) break;
-                b = w.b0;
-            }
-            fetch(w, b);
+            warp_arrive(&own_full[st]);
         }
+        cp_wait<0>();
         if (!ok) {
             abort_flag = 1;
             if (lane == 0) set_error(a.err, BLEND_ETIMEOUT);
