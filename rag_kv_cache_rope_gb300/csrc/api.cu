@@ -99,6 +99,7 @@ struct blend_handle {
     std::vector<cudaEvent_t> ev_layer;
     int use_tc;  // tensor-core GEMM for bf16
     float* paged_part;   // paged_attention: partial results of split key ranges
+    int32_t* paged_pre;  // prefix sums over the sequences, one set per CTA
     int32_t* paged_count;  // and the arrivals at each split item (zero between calls)
     float* split_ws;  // tensor-core GEMM: K-half partials of last-wave tiles
     int host_rc = 0;  // first failure of an internal launch during the current call
@@ -283,6 +284,7 @@ Layout make_layout(const blend_model_cfg* c, const blend_limits* l) {
     L.add((size_t)l->max_batch * ((l->max_chunk_rows + 2047) / 2048 * 2048) * 8);  // 40 sorted rank keys
     L.add(paged_part_bytes(c->head_dim));                  // 41 paged attention: partial results
     L.add(PAGED_MAX_CTAS * sizeof(int32_t));               // 42 and arrival counters
+    L.add(PAGED_PRE_INTS * sizeof(int32_t));               // 43 and prefix sums over sequences
     return L;
 }
 
@@ -504,6 +506,7 @@ int blend_init(const blend_model_cfg* cfg, const blend_weights* w, const blend_l
     h->rank_keys = (unsigned long long*)(b + L.off[i++]);
     h->paged_part = (float*)(b + L.off[i++]);
     h->paged_count = (int32_t*)(b + L.off[i++]);
+    h->paged_pre = (int32_t*)(b + L.off[i++]);
     h->use_tc = cfg->dtype == BLEND_BF16 ? tc_available() : 0;
     cudaStream_t s = (cudaStream_t)stream;
     cudaMemsetAsync(h->err, 0, 16, s);
@@ -1455,6 +1458,7 @@ int paged_attention(blend_handle* h, const blend_pages* pages, const void* q, in
     a.out = out;
     a.part = h->paged_part;
     a.count = h->paged_count;
+    a.pre = h->paged_pre;
     a.err = h->err;
     const bool i4 = pages->format == BLEND_PAGES_INT4;
     cudaStream_t s = (cudaStream_t)stream;

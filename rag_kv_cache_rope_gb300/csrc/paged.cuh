@@ -10,6 +10,7 @@ constexpr int PAGED_NO_WINDOW = 1 << 30;  // past every position, and position -
 constexpr int PAGED_MAX_TILE = 32;   // (row, head) pairs of one tile of those kernels
 // fp32 partial results: two slots per CTA, each [pair][head_dim] sums, then maxima and sums per pair
 constexpr size_t paged_slot_floats(int d) { return (size_t)PAGED_MAX_TILE * (d + 2); }
+constexpr size_t PAGED_PRE_INTS = (size_t)152 * (BLEND_MAX_SEQS + 1);
 constexpr size_t paged_part_bytes(int d) { return 2 * (size_t)PAGED_MAX_CTAS * paged_slot_floats(d) * 4; }
 
 // The pages as the kernels see them (blend_pages with the model's head count).
@@ -27,15 +28,18 @@ struct PageView {
 // Bytes of one head's K or V row in the pages, and of its scales.
 template <typename T, bool I4> __host__ __device__ constexpr int held_bytes(int d) { return I4 ? d / 2 : d * (int)sizeof(T); }
 
+__device__ __forceinline__ int page_entry(const PageView& p, int seq, int t) {
+    return __ldg(p.table + (long long)seq * p.max_pages + (t >> p.shift));
+}
+__device__ __forceinline__ int checked_page(const PageView& p, int page, int32_t* err) {
+    if ((unsigned)page < (unsigned)p.n_pages) return page;
+    set_error(err, BLEND_EDEVICE);
+    return 0;
+}
 // The page that holds tokens [t, ...) of sequence `seq`; a table entry outside the pool is
 // reported and page 0 read in its place.
 __device__ __forceinline__ int page_of(const PageView& p, int seq, int t, int32_t* err) {
-    int pg = __ldg(p.table + (long long)seq * p.max_pages + (t >> p.shift));
-    if ((unsigned)pg >= (unsigned)p.n_pages) {
-        set_error(err, BLEND_EDEVICE);
-        pg = 0;
-    }
-    return pg;
+    return checked_page(p, page_entry(p, seq, t), err);
 }
 // Row of (page, head, token in page) counted in rows of the pool: 64 bits, pools pass 2^31 elements.
 __device__ __forceinline__ long long page_row(const PageView& p, int page, int head, int in_page) {
@@ -65,6 +69,7 @@ struct PagedAttn {
     void* out;
     float* part;
     int32_t* count;
+    int* pre;  // tile kernel: each CTA's prefix sums over the sequences
     int32_t* err;
 };
 

@@ -35,19 +35,21 @@ constexpr int K_HALF = 64 * 128;    // 64 columns of a CTA's 64 keys
 constexpr int NSBUF = 3;
 constexpr uint32_t O_COL = 384;
 constexpr int TMEM_COLS = 512;
-constexpr int S_WARP = 6;  // 0 producer, 1 TMEM + P.V issue, 2..5 softmax, 6 S issue, 7..10 4-bit pages
+// Warps: 0 producer, 1 TMEM + P.V issue, 2..5 softmax, 6 S issue; model pages: 7 edge blocks; 4-bit
+// pages: 7..10 codes to operands, 11 every other block's signal to the leader
+constexpr int S_WARP = 6;
 constexpr int MAX_CLUSTERS = 76;
 constexpr int MIN_QUOTA = 2;  // blocks of a cluster's stretch at least
 
 template <bool I4, int D> struct TileCfg {
     static constexpr int NH = D / 64;
-    static constexpr int THREADS = I4 ? 352 : 224;
+    static constexpr int THREADS = I4 ? 384 : 256;
     static constexpr int VCOL = D / 2;                      // V columns of a CTA
     static constexpr int QT = NH * Q_HALF;
     static constexpr int KB = NH * K_HALF;
     static constexpr int VB = TKEYS * VCOL * 2;
     static constexpr int STAGE = KB + VB;
-    static constexpr int STAGES = D == 64 ? 8 : I4 ? 3 : 4;
+    static constexpr int STAGES = D == 64 ? 8 : I4 ? 3 : 5;
     // 4-bit pages: raw rows on their way, a slot per thread (half a K row, a V row, their scales)
     static constexpr int RAW_STAGES = 4;
     static constexpr int SB = D / 16;
@@ -63,6 +65,7 @@ template <bool I4, int D> struct TileCfg {
 static_assert(4 * MAX_CLUSTERS * TileCfg<false, 128>::PART * 4 <= paged_part_bytes(128), "workspace");
 static_assert(4 * MAX_CLUSTERS * TileCfg<false, 64>::PART * 4 <= paged_part_bytes(64), "workspace");
 static_assert(8 * MAX_CLUSTERS <= PAGED_MAX_CTAS, "arrival counters");
+static_assert(2 * MAX_CLUSTERS * (size_t)(BLEND_MAX_SEQS + 1) <= PAGED_PRE_INTS, "prefix sums");
 
 // MN-major B operand (V), a CTA's columns in one swizzle atom: 64 columns (128-byte swizzle, 8-key
 // groups 1024 B apart) or 32 (64-byte swizzle, 512 B apart).
@@ -107,6 +110,15 @@ __device__ __forceinline__ bool wait_cl_acquire(uint64_t* b, uint32_t par, volat
         if ((i & 1023) == 1023 && *abort_flag) return false;
     }
     return false;
+}
+// A block that the dequantising warps of this CTA have written, signalled to the leader: a release to
+// the cluster takes over 1000 cycles, so one thread per CTA and block does it for four warps (whose
+// arrivals at the CTA's own barrier it has seen), and two warps take turns.
+__device__ __forceinline__ bool pass_on(uint64_t* own, uint64_t* leader, uint32_t par, volatile int* abort_flag) {
+    if (!warp_poll(own, par, abort_flag)) return false;
+    if ((threadIdx.x & 31) == 0) arrive_leader_release(leader);
+    __syncwarp();
+    return true;
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -205,11 +217,12 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
     constexpr int WARPS = T::THREADS / 32;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t q_full[2], q_empty[2], kv_full[STAGES], kv_empty[STAGES], s_full[NSBUF],
-        p_full[NSBUF], o_full, o_free, edge_full, own_full[STAGES];
+        p_full[NSBUF], o_full, o_free, edge_full[STAGES], own_full[STAGES];
     __shared__ uint32_t tmem_sh;
     __shared__ volatile int abort_flag;
-    __shared__ int pend_kv[STAGES], pend_q[2], pend_edge;
-    __shared__ int pre[BLEND_MAX_SEQS + 1];
+    __shared__ int pend_kv[STAGES], pend_q[2], pend_edge[STAGES];
+    // in the workspace (shared memory is full of stages); read again only where a role changes sequence
+    int* pre = a.pre + (size_t)blockIdx.x * (BLEND_MAX_SEQS + 1);
 
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t* sQ = smem;              // Q buffer qb at qb * QT
@@ -265,15 +278,15 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
             mbar_init(&p_full[b], 8);  // 4 softmax warps in each CTA
         }
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&kv_full[s], 2);  // each CTA's producer warp
+            mbar_init(&kv_full[s], 2);  // once from each CTA
+            mbar_init(&edge_full[s], 1);
+            pend_edge[s] = -1;
             mbar_init(&own_full[s], 4);  // 4-bit pages: this CTA's dequantising warps
             mbar_init(&kv_empty[s], 1);
             pend_kv[s] = -1;
         }
         mbar_init(&o_full, 1);
         mbar_init(&o_free, 8);
-        mbar_init(&edge_full, 1);
-        pend_edge = -1;
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_smem();
@@ -303,18 +316,19 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
         const int col = is_k ? (lane % NH) * 64 : VCOL * rank;
         const int box_at = is_k ? (lane % NH) * K_HALF + piece * k_rows * 128 : KB + tok * VCOL * 2;
         const int page_mask = (1 << a.pg.shift) - 1;
-        uint32_t it = 0, edges = 0;
+        uint32_t it = 0;
         bool ok = true;
         int tl = 0, page = 0, k0 = 0;
-        bool need = false;
+        bool need = false, edge = false;
         Walk w(a, pre, rows2, x_first, x_end);
         int b = w.b0;
         auto look = [&]() {  // this lane's box of block b: whether a row sees any of it, and its page
             k0 = w.it.kr.block(b) * TKEYS;
+            edge = !w.all_seen(k0, k0 + TKEYS - 1);
             need = mine && w.any_seen(k0 + tok, k0 + tok + rows - 1);
-            page = need ? page_of(a.pg, w.seq, k0 + tok, a.err) : 0;
+            if (need) page = page_entry(a.pg, w.seq, k0 + tok);  // looked at when the stage is free
         };
-        look();
+        if constexpr (!I4) look();
         while (ok) {
             if (b == w.b0) {
                 const int qb = tl & 1;
@@ -337,57 +351,35 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
             }
             const int st = it % STAGES;
             if constexpr (I4) {
-                // the dequantising warps' rows, passed on to the leader: one release to the cluster per
-                // block instead of one per warp, and off those warps' path
-                ok = warp_poll(&own_full[st], (it / STAGES) & 1, &abort_flag);
+                if (!(it & 1)) ok = pass_on(&own_full[st], &kv_full[st], (it / STAGES) & 1, &abort_flag);
                 if (!ok) break;
-                if (lane == 0) arrive_leader_release(&kv_full[st]);
-                __syncwarp();
             } else {
                 ok = warp_poll(&kv_empty[st], ((it / STAGES) & 1) ^ 1, &abort_flag);
                 if (!ok) break;
-                const bool edge = !w.all_seen(k0, k0 + TKEYS - 1);
                 uint8_t* dst = sKV + st * STAGE;
-                const uint32_t kf = leader_addr(&kv_full[st]);
-                uint32_t bytes = 2u * (KB + T::VB);  // both CTAs' boxes count at the leader
-                if (rank == 0 && lane == 0) pend_kv[st] = (int)((it / STAGES) & 1);
-                if (!edge) {
-                    if (mine)
-                        tma_3d_pair(dst + box_at, is_k ? &mapK : &mapV, kf, col, (k0 + tok) & page_mask, page * a.pg.hkv + w.head);
-                } else {
-                    const unsigned k_seen = __ballot_sync(0xffffffffu, lane * k_rows < TKEYS && w.any_seen(k0 + lane * k_rows, k0 + (lane + 1) * k_rows - 1));
-                    bytes = (uint32_t)__popc(k_seen) * (uint32_t)k_rows * D * 2;
+                if (lane == 0) {
+                    if (rank == 0) pend_kv[st] = (int)((it / STAGES) & 1);
+                    // a whole block: the leader expects both CTAs' boxes, the other CTA has nothing of its own
+                    // to publish; an edge block is signalled by the edge warp, which first waits for V
+                    if (!edge) {
+                        if (rank == 0) mbar_expect_tx(&kv_full[st], 2u * (KB + T::VB));
+                        else arrive_leader(&kv_full[st]);
+                    }
+                }
+                if (edge) {
                     const unsigned v_seen = __ballot_sync(0xffffffffu, need && !is_k);
                     if (lane == 0 && v_seen) {
-                        mbar_expect_tx(&edge_full, (uint32_t)__popc(v_seen) * (uint32_t)v_rows * VCOL * 2);
-                        pend_edge = (int)(edges & 1);
+                        mbar_expect_tx(&edge_full[st], (uint32_t)__popc(v_seen) * (uint32_t)v_rows * VCOL * 2);
+                        pend_edge[st] = 1;
                     }
-                    __syncwarp();
-                    if (need) {
-                        if (is_k)
-                            tma_3d_pair(dst + box_at, &mapK, kf, col, (k0 + tok) & page_mask, page * a.pg.hkv + w.head);
-                        else
-                            tma_3d(dst + box_at, &mapV, &edge_full, col, (k0 + tok) & page_mask, page * a.pg.hkv + w.head);
-                    }
-                    __syncwarp();
-                    if (v_seen) {
-                        ok = warp_wait(&edge_full, edges & 1, &abort_flag);
-                        if (!ok) break;
-                        if (lane == 0) pend_edge = -1;
-                        ++edges;
-                    }
-                    constexpr int CH = VCOL / 8;  // 16-byte chunks of a row (the swizzle stays within it)
-                    for (int i = lane; i < TKEYS * CH; i += 32) {
-                        const int j = k0 + i / CH;
-                        if (!w.any_seen(j, j)) *reinterpret_cast<uint4*>(dst + KB + i * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_async_smem();
                     __syncwarp();
                 }
-                if (lane == 0) {
-                    if (rank == 0) mbar_expect_tx(&kv_full[st], bytes);
-                    else if (edge) arrive_leader_release(&kv_full[st]);
-                    else arrive_leader(&kv_full[st]);  // nothing of this thread's to publish: the boxes count themselves
+                if (need) {
+                    const int pg = checked_page(a.pg, page, a.err);
+                    const int c1 = (k0 + tok) & page_mask, c2 = pg * a.pg.hkv + w.head;
+                    if (is_k) tma_3d_pair(dst + box_at, &mapK, leader_addr(&kv_full[st]), col, c1, c2);
+                    else if (!edge) tma_3d_pair(dst + box_at, &mapV, leader_addr(&kv_full[st]), col, c1, c2);
+                    else tma_3d(dst + box_at, &mapV, &edge_full[st], col, c1, c2);
                 }
                 __syncwarp();
             }
@@ -683,6 +675,55 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
             abort_flag = 1;
             if (lane == 0) set_error(a.err, BLEND_ETIMEOUT);
         }
+    } else if (!I4 && warp > S_WARP) {
+        // ------------------------------------------------ edge blocks of model pages (both CTAs)
+        // V has its own barrier here; rows that no row sees are zeroed once it has landed, then the
+        // block is signalled: the leader's own arrival carries the bytes of both CTAs' keys.
+        const int k_rows = min(1 << a.pg.shift, 64), v_rows = 1 << a.pg.shift;
+        uint32_t it = 0, phases = 0;  // phases: bit st, the parity of edge_full[st]
+        bool ok = true;
+        for (Walk w(a, pre, rows2, x_first, x_end); ok && w.more(); w.next())
+            for (int b = w.b0; b < w.b1; ++b, ++it) {
+                const int k0 = w.it.kr.block(b) * TKEYS;
+                if (w.all_seen(k0, k0 + TKEYS - 1)) continue;
+                const int st = it % STAGES;
+                // the stage must be this block's before anything is written to it
+                ok = warp_poll(&kv_empty[st], ((it / STAGES) & 1) ^ 1, &abort_flag);
+                if (!ok) break;
+                const unsigned k_seen = __ballot_sync(0xffffffffu, lane * k_rows < TKEYS && w.any_seen(k0 + lane * k_rows, k0 + (lane + 1) * k_rows - 1));
+                const unsigned v_seen = __ballot_sync(0xffffffffu, lane * v_rows < TKEYS && w.any_seen(k0 + lane * v_rows, k0 + (lane + 1) * v_rows - 1));
+                if (v_seen) {
+                    ok = warp_poll(&edge_full[st], (phases >> st) & 1, &abort_flag);
+                    if (!ok) break;
+                    if (lane == 0) pend_edge[st] = -1;
+                    phases ^= 1u << st;
+                }
+                uint8_t* dst = sKV + st * STAGE + KB;
+                constexpr int CH = VCOL / 8;  // 16-byte chunks of a row (the swizzle stays within it)
+                for (int i = lane; i < TKEYS * CH; i += 32) {
+                    const int j = k0 + i / CH;
+                    if (!w.any_seen(j, j)) *reinterpret_cast<uint4*>(dst + i * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0) mbar_expect_tx(&kv_full[st], (uint32_t)__popc(k_seen) * (uint32_t)k_rows * D * 2);
+                    else arrive_leader_release(&kv_full[st]);
+                }
+                __syncwarp();
+            }
+        if (!ok) {
+            abort_flag = 1;
+            if (lane == 0) set_error(a.err, BLEND_ETIMEOUT);
+        }
+    } else if (I4 && warp == S_WARP + 5) {
+        // ------------------------------------------------ odd blocks' signals (warp 0 has the even ones)
+        bool ok = true;
+        for (int i = 1; ok && i < x_end - x_first; i += 2) ok = pass_on(&own_full[i % STAGES], &kv_full[i % STAGES], (i / STAGES) & 1, &abort_flag);
+        if (!ok) {
+            abort_flag = 1;
+            if (lane == 0) set_error(a.err, BLEND_ETIMEOUT);
+        }
     } else if (I4 && warp > S_WARP) {
         // ------------------------------------------------ 4-bit pages to bf16 operands (both CTAs)
         // Each thread copies its own raw rows RAW_STAGES - 1 blocks ahead with cp.async, so it waits
@@ -702,12 +743,13 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
             jv = k0 + t;
             sk = w.any_seen(jk, jk);
             sv = w.any_seen(jv, jv);
-            pk = sk ? page_of(a.pg, w.seq, jk, a.err) : 0;
-            pv = sv ? page_of(a.pg, w.seq, jv, a.err) : 0;
+            if (sk) pk = page_entry(a.pg, w.seq, jk);
+            if (sv) pv = page_entry(a.pg, w.seq, jv);
         };
         auto copy = [&](int stage) {  // the block that look() saw, zeros for what no row sees
             const uint32_t dst = su32(raw + stage * T::RAW);
-            const long long rk = page_row(a.pg, pk, w.head, jk & page_mask), rv = page_row(a.pg, pv, w.head, jv & page_mask);
+            const int gk = sk ? checked_page(a.pg, pk, a.err) : 0, gv = sv ? checked_page(a.pg, pv, a.err) : 0;
+            const long long rk = page_row(a.pg, gk, w.head, jk & page_mask), rv = page_row(a.pg, gv, w.head, jv & page_mask);
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) cp_async<16>(dst + (i * 128 + t) * 16, a.pg.k + rk * RB + (t & 1) * (D / 4) + i * 16, sk);
 #pragma unroll
@@ -808,9 +850,12 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                 if (pend_q[b] >= 0)
                     for (long long i = 0; i < SPIN_LIMIT && !mbar_try(&q_full[b], (uint32_t)pend_q[b]); ++i) {
                     }
-        if (pend_edge >= 0)
-            for (long long i = 0; i < SPIN_LIMIT && !mbar_try(&edge_full, (uint32_t)pend_edge); ++i) {
-            }
+        // (an edge barrier's parity is its warp's; it is waited for in both, which costs a bounded wait)
+        for (int st = 0; st < STAGES; ++st)
+            if (pend_edge[st] >= 0)
+                for (int par = 0; par < 2; ++par)
+                    for (long long i = 0; i < SPIN_LIMIT / 16 && !mbar_try(&edge_full[st], (uint32_t)par); ++i) {
+                    }
     }
     __syncthreads();
     cluster_sync();  // neither CTA leaves while the other may still signal its barriers
