@@ -17,19 +17,29 @@
 //   O^T += V^T P^T  P^T comes from S^T by one 8x8 transpose per 8 keys (movmatrix), all in registers
 // The running maximum used for P is raised only when it grows by more than 2^8 (as in the
 // prefill's kernel); sums use the same reference, so O / l is exact.
-// 4-bit pages: codes go from shared memory to operands in registers, (w >> 4 i) & 0x000F000F being
-// a pair of operand elements in the order that the rows are packed in; n + 128 is the bf16 0x4300
-// | n, so one subtraction gives n - 8 exactly.  A key's scales multiply its partial scores of
-// each 32 dims in fp32, a value's scale multiplies P (rounded to bf16 once more: a value n s would
-// be rounded there as well).
+// 4-bit pages: codes go from shared memory to operands in registers.  Keys: a code n + 8 in the low
+// bits of a half float is the subnormal (n + 8) 2^-24, so a mask alone makes operands of a packed
+// word (codes at bits 4..7 count 16 times, and their queries a sixteenth); queries are turned into
+// fp16 with the row's own power of two, the -8 is the accumulator's start, -8 2^-24 sum q, and a
+// key's scales multiply its partial scores of each 32 dims in fp32: the scores are exact to fp32.
+// Values: n + 128 is the bf16 0x4300 | n, one subtraction gives n - 8 exactly (here an offset in
+// the sums would cancel against results that are far smaller than it), and the value's scale
+// multiplies P in fp32 before its one rounding to bf16.
 // Measured (GB300, 6.8 TB/s copy rate): 64 sequences of 3.3-8.2 K tokens, window 4096, Mistral-7B
 // heads 172 us, 6.2 TB/s of pages.
 // Tokens that no row sees are filled with zeros instead of loaded (values, scales), so what they
 // hold does not matter.
+#include <climits>
+
+#include <cuda_fp16.h>
+
 #include "paged.cuh"
 
 namespace blend {
 namespace {
+
+constexpr int SPLIT_CTAS = 304;  // two on each of 152 SMs
+static_assert(SPLIT_CTAS <= PAGED_MAX_CTAS, "workspace");
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
@@ -65,16 +75,41 @@ __device__ __forceinline__ float pow2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t x) { return __half22float2(*reinterpret_cast<__half2*>(&x)); }
 // Codes at bits 4 i and 16 + 4 i of w as two bf16 values n - 8.
 __device__ __forceinline__ uint32_t codes2(uint32_t w, int i) {
     uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;  // 128 + n
     const uint32_t off = 0x43084308u;                            // 136
     const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&off));
     return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// The G bf16 scales of a row as fp32.
+template <int G> __device__ __forceinline__ void scales(const uint8_t* p, float (&f)[G]) {
+    uint32_t w[G / 2];
+    if constexpr (G == 4) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p);
+        w[0] = x.x;
+        w[1] = x.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+#pragma unroll
+    for (int i = 0; i < G / 2; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
 }
 
 // Token (0..15) of a step that takes row i of the 4-bit S^T tile: the order under which the lanes'
@@ -90,24 +125,27 @@ template <bool I4, int D> struct StepCfg {
     static constexpr int SCALE = I4 ? D / 16 : 0;             // bytes of a row's scales
     static constexpr int BYTES = 2 * KV + 2 * PAGED_STEP * SCALE;  // K, V, K scales, V scales
 };
-template <bool I4, int D, int NT, int W, int STAGES> struct SplitCfg {
-    static constexpr int RING = W * STAGES * StepCfg<I4, D>::BYTES;
+// U: steps of a stage (and of a pass through the softmax)
+template <bool I4, int D, int NT, int W, int STAGES, int U> struct SplitCfg {
+    static constexpr int RING = W * STAGES * U * StepCfg<I4, D>::BYTES;
     static constexpr int OPAD = D + 4;  // distinct banks for the four pairs of a quad
     static constexpr int JOIN = W * 8 * NT * OPAD * 4;
-    static constexpr int PARTS = PAGED_MAX_CTAS * 4;  // weights of an item's parts, one pair at a time
-    static constexpr int SMEM = (RING > JOIN ? RING : JOIN) > PARTS ? (RING > JOIN ? RING : JOIN) : PARTS;
+    static constexpr int PARTS = SPLIT_CTAS * 8 * NT * 4 + W * 32 * 16;  // weights of an item's parts, sums of a round
+    static constexpr int MOST = RING > JOIN ? RING : JOIN;
+    static constexpr int SMEM = MOST > PARTS ? MOST : PARTS;
 };
 
-template <bool I4, int D, int NT, int W, int STAGES>
+template <bool I4, int D, int NT, int W, int STAGES, int U>
 __global__ void __launch_bounds__(W * 32, 2)
     k_paged_split(const __grid_constant__ PagedAttn a) {
     using S = StepCfg<I4, D>;
-    using Cfg = SplitCfg<I4, D, NT, W, STAGES>;
+    using Cfg = SplitCfg<I4, D, NT, W, STAGES, U>;
     constexpr int R = 8 * NT, T = W * 32, KT = D / 16, G = D / 32, OPAD = Cfg::OPAD;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int pre[BLEND_MAX_SEQS + 1];
     __shared__ int scan[W];
     __shared__ float sm[W][R], sl[W][R], sM[R], sL[R];
+    __shared__ __align__(8) float s_start[I4 ? W : 1][G][R];  // 4-bit keys: -8 2^-24 sum q of each 32 dims
     __shared__ int last_sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r = lane >> 2, c = lane & 3;
@@ -164,8 +202,8 @@ __global__ void __launch_bounds__(W * 32, 2)
         }
         seq = lo;
     }
-    const uint32_t ring = smem_u32(smem) + warp * STAGES * S::BYTES;
-    uint8_t* ring_p = smem + warp * STAGES * S::BYTES;
+    const uint32_t ring = smem_u32(smem) + warp * STAGES * U * S::BYTES;
+    uint8_t* ring_p = smem + warp * STAGES * U * S::BYTES;
 
     while (x < x_end) {
         while (pre[seq + 1] <= x) ++seq;  // skips sequences without steps
@@ -179,15 +217,18 @@ __global__ void __launch_bounds__(W * 32, 2)
         const KeyRange kr = key_range<PAGED_STEP>(p0, p1, a.window, a.n_sink);
         const int n_real = min(s1, kr.total());  // the empty step of a sequence without keys is none
 
-        // ---- loads of step i into a stage
-        auto load = [&](int i, int stage, int page) {
+        // steps of the window's range that every row sees whole: no masks, no token to leave out
+        const int clean0 = kr.n_a + max(0, (max(p1 - a.window, -1) + PAGED_STEP) / PAGED_STEP - kr.first_b);
+        const int n_clean = (p0 + 1) / PAGED_STEP - kr.first_b + kr.n_a - clean0;
+        auto clean = [&](int i) { return n_clean > 0 && (unsigned)(i - clean0) < (unsigned)n_clean; };
+
+        // ---- loads of step i into a place of the ring
+        auto load = [&](int i, uint32_t dst, int entry) {
             const int j0 = kr.block(i) * PAGED_STEP;
-            const long long row = page_row(a.pg, page, head, j0 & ((1 << a.pg.shift) - 1));
-            const int j1 = j0 + PAGED_STEP - 1;
-            const bool whole = j1 <= p1 && (j1 < a.n_sink || j0 > p0 - a.window);  // some row sees each of them
-            const uint32_t dst = ring + stage * S::BYTES;
-            const char* ksrc = a.pg.k + row * S::ROW;
-            const char* vsrc = a.pg.v + row * S::ROW;
+            const long long row = page_row(a.pg, checked_page(a.pg, entry, a.err), head, j0 & ((1 << a.pg.shift) - 1));
+            const bool whole = clean(i);
+            const char* ksrc = a.pg.k + row * S::ROW + lane * 16;
+            const char* vsrc = a.pg.v + row * S::ROW + lane * 16;
             constexpr int CH = S::ROW / 16, N = S::KV / 512;
 #pragma unroll
             for (int u = 0; u < N; ++u) {
@@ -199,8 +240,8 @@ __global__ void __launch_bounds__(W * 32, 2)
                     kch = ch;
                     vch = D == 128 ? ch ^ (((t >> 1) & 1) << 1) : ch;
                 }
-                cp_async<16>(dst + t * S::ROW + kch * 16, ksrc + q * 16, ok);
-                cp_async<16>(dst + S::KV + t * S::ROW + vch * 16, vsrc + q * 16, ok);
+                cp_async<16>(dst + t * S::ROW + kch * 16, ksrc + u * 512, ok);
+                cp_async<16>(dst + S::KV + t * S::ROW + vch * 16, vsrc + u * 512, ok);
             }
             if constexpr (I4) {
                 const int t = lane & 15;
@@ -209,41 +250,93 @@ __global__ void __launch_bounds__(W * 32, 2)
                                    whole || seen_by_any(j0 + t, p0, p1, a.window, a.n_sink));
             }
         };
-        auto page_at = [&](int i) { return page_of(a.pg, seq, kr.block(i) * PAGED_STEP, a.err); };
+        auto entry_at = [&](int i) { return page_entry(a.pg, seq, kr.block(i) * PAGED_STEP); };
 
-        // ---- first steps on their way
-        int li = s0 + warp;  // next step to load
-        int page = li < n_real ? page_at(li) : 0;
+        // ---- first steps on their way; the warp takes U neighbouring steps of every U W
+        int li = s0 + U * warp;  // next step to load
+        int entry[U];
+        auto next_entries = [&]() {
 #pragma unroll
-        for (int st = 0; st < STAGES - 1; ++st) {
+            for (int u = 0; u < U; ++u)
+                if (li + u < n_real) entry[u] = entry_at(li + u);
+        };
+        auto load_next = [&](int st) {
             if (li < n_real) {
-                load(li, st, page);
-                li += W;
-                if (li < n_real) page = page_at(li);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (li + u < n_real) load(li + u, ring + (st * U + u) * S::BYTES, entry[u]);
+                li += U * W;
+                next_entries();
             }
             cp_commit();
-        }
+        };
+        next_entries();
+#pragma unroll
+        for (int st = 0; st < STAGES - 1; ++st) load_next(st);
         // ---- queries (B operand) and the pairs' positions
         uint32_t qf[NT][KT][2];
         int rp[NT][2];
+        float sc[NT][2];  // score to exponent of 2
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int p = nt * 8 + r;
             const bool ok = p < npair;
             const bf16* qr = reinterpret_cast<const bf16*>(a.q) + (long long)(si.row0 + (ok ? p / a.group : 0)) * a.ld_q +
                              (head * a.group + (ok ? p % a.group : 0)) * D;
+            float row_scale = 1.f;
+            if constexpr (!I4) {
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                // 4-bit: the dims of a lane are 8 in a row of each 32
-                const int e0 = I4 ? 32 * (kt >> 1) + 8 * c + 4 * (kt & 1) : 16 * kt + 2 * c, e1 = I4 ? e0 + 2 : e0 + 8;
-                qf[nt][kt][0] = ok ? *reinterpret_cast<const uint32_t*>(qr + e0) : 0u;
-                qf[nt][kt][1] = ok ? *reinterpret_cast<const uint32_t*>(qr + e1) : 0u;
+                for (int kt = 0; kt < KT; ++kt) {
+                    qf[nt][kt][0] = ok ? *reinterpret_cast<const uint32_t*>(qr + 16 * kt + 2 * c) : 0u;
+                    qf[nt][kt][1] = ok ? *reinterpret_cast<const uint32_t*>(qr + 16 * kt + 2 * c + 8) : 0u;
+                }
+            } else {
+                // dims 32 g + 8 c .. +7 of the row, by a power of two that brings its largest into [1, 2)
+                uint4 raw[G];
+                float top = 0.f;
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    raw[g] = ok ? *reinterpret_cast<const uint4*>(qr + 32 * g + 8 * c) : make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int ex = min(max((int)((__float_as_uint(top) >> 23) & 255) - 127, -100), 100);
+                const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+                row_scale = __uint_as_float((uint32_t)(127 + ex) << 23);
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+                    float sum = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float f = (e & 1) ? down * 0.0625f : down;
+                        const uint32_t h = pack_f16(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
+                        qf[nt][2 * g + (e >> 1)][e & 1] = h;
+                        const float2 back = unpack_f16(h);  // what the products will see
+                        sum += (back.x + back.y) * ((e & 1) ? 16.f : 1.f);
+                    }
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    if (c == 0) s_start[warp][g][p] = sum * -0x1p-21f;
+                }
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int pc = nt * 8 + 2 * c + e;
                 rp[nt][e] = pc < npair ? p0 + pc / a.group : -1;
+                sc[nt][e] = a.scale_log2;
+                if constexpr (I4) sc[nt][e] *= 0x1p24f * __shfl_sync(0xffffffffu, row_scale, 4 * (2 * c + e));
             }
+        }
+        if constexpr (I4) __syncwarp();
+        float2 start1[G];  // one tile of pairs: held in registers
+        if constexpr (I4 && NT == 1) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) start1[g] = *reinterpret_cast<const float2*>(&s_start[warp][g][2 * c]);
         }
         float m[NT][2], l[NT][2], o[KT][NT][4];
 #pragma unroll
@@ -257,95 +350,91 @@ __global__ void __launch_bounds__(W * 32, 2)
         }
 
         int stage = 0;
-        for (int i = s0 + warp; i < n_real; i += W) {
+        for (int i = s0 + U * warp; i < n_real; i += U * W) {
             cp_wait<STAGES - 2>();
             __syncwarp();
-            {
-                const int ns = stage == 0 ? STAGES - 1 : stage - 1;
-                if (li < n_real) {
-                    load(li, ns, page);
-                    li += W;
-                    if (li < n_real) page = page_at(li);
-                }
-                cp_commit();
-            }
-            const uint32_t kb = ring + stage * S::BYTES, vb = kb + S::KV;
-            float s[NT][4];
+            load_next(stage == 0 ? STAGES - 1 : stage - 1);
+            float s[U][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-            if constexpr (!I4) {
+            for (int u = 0; u < U; ++u) {
+                const uint32_t kb = ring + (stage * U + u) * S::BYTES;
+                if constexpr (!I4) {
 #pragma unroll
-                for (int kt = 0; kt < KT; ++kt) {
-                    uint32_t k[4];
-                    const int t = lane & 15, ch = 2 * kt + (lane >> 4);
-                    ldsm4(k, kb + t * S::ROW + ((ch ^ (t & 7)) << 4));
+                    for (int nt = 0; nt < NT; ++nt) s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.f;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma(s[nt], k, qf[nt][kt][0], qf[nt][kt][1]);
-                }
-            } else {
-                const uint8_t* kp = ring_p + stage * S::BYTES;
-                const int t0 = token4(r), t1 = t0 + 8;
-                uint32_t w0[G], w1[G];
-                float f0[G], f1[G];
-                const uint8_t* sp = kp + 2 * S::KV;
-                if constexpr (D == 128) {
-                    const uint4 u0 = *reinterpret_cast<const uint4*>(kp + t0 * S::ROW + c * 16);
-                    const uint4 u1 = *reinterpret_cast<const uint4*>(kp + t1 * S::ROW + c * 16);
-                    w0[0] = u0.x; w0[1] = u0.y; w0[2] = u0.z; w0[3] = u0.w;
-                    w1[0] = u1.x; w1[1] = u1.y; w1[2] = u1.z; w1[3] = u1.w;
-                    const uint2 a0 = *reinterpret_cast<const uint2*>(sp + t0 * 8), a1 = *reinterpret_cast<const uint2*>(sp + t1 * 8);
-                    f0[0] = __uint_as_float(a0.x << 16); f0[1] = __uint_as_float(a0.x & 0xffff0000u);
-                    f0[2] = __uint_as_float(a0.y << 16); f0[3] = __uint_as_float(a0.y & 0xffff0000u);
-                    f1[0] = __uint_as_float(a1.x << 16); f1[1] = __uint_as_float(a1.x & 0xffff0000u);
-                    f1[2] = __uint_as_float(a1.y << 16); f1[3] = __uint_as_float(a1.y & 0xffff0000u);
+                    for (int kt = 0; kt < KT; ++kt) {
+                        uint32_t k[4];
+                        const int t = lane & 15, ch = 2 * kt + (lane >> 4);
+                        ldsm4(k, kb + t * S::ROW + ((ch ^ (t & 7)) << 4));
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma(s[u][nt], k, qf[nt][kt][0], qf[nt][kt][1]);
+                    }
                 } else {
-                    const uint2 u0 = *reinterpret_cast<const uint2*>(kp + t0 * S::ROW + c * 8);
-                    const uint2 u1 = *reinterpret_cast<const uint2*>(kp + t1 * S::ROW + c * 8);
-                    w0[0] = u0.x; w0[1] = u0.y;
-                    w1[0] = u1.x; w1[1] = u1.y;
-                    const uint32_t a0 = *reinterpret_cast<const uint32_t*>(sp + t0 * 4), a1 = *reinterpret_cast<const uint32_t*>(sp + t1 * 4);
-                    f0[0] = __uint_as_float(a0 << 16); f0[1] = __uint_as_float(a0 & 0xffff0000u);
-                    f1[0] = __uint_as_float(a1 << 16); f1[1] = __uint_as_float(a1 & 0xffff0000u);
-                }
+                    const uint8_t* kp = ring_p + (stage * U + u) * S::BYTES;
+                    const int t0 = token4(r), t1 = t0 + 8;
+                    uint32_t w0[G], w1[G];
+                    float f0[G], f1[G];
+                    const uint8_t* sp = kp + 2 * S::KV;
+                    if constexpr (D == 128) {
+                        const uint4 u0 = *reinterpret_cast<const uint4*>(kp + t0 * S::ROW + c * 16);
+                        const uint4 u1 = *reinterpret_cast<const uint4*>(kp + t1 * S::ROW + c * 16);
+                        w0[0] = u0.x; w0[1] = u0.y; w0[2] = u0.z; w0[3] = u0.w;
+                        w1[0] = u1.x; w1[1] = u1.y; w1[2] = u1.z; w1[3] = u1.w;
+                    } else {
+                        const uint2 u0 = *reinterpret_cast<const uint2*>(kp + t0 * S::ROW + c * 8);
+                        const uint2 u1 = *reinterpret_cast<const uint2*>(kp + t1 * S::ROW + c * 8);
+                        w0[0] = u0.x; w0[1] = u0.y;
+                        w1[0] = u1.x; w1[1] = u1.y;
+                    }
+                    scales<G>(sp + t0 * S::SCALE, f0);
+                    scales<G>(sp + t1 * S::SCALE, f1);
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const uint32_t ka[4] = {codes2(w0[g], 0), codes2(w1[g], 0), codes2(w0[g], 1), codes2(w1[g], 1)};
-                    const uint32_t kc[4] = {codes2(w0[g], 2), codes2(w1[g], 2), codes2(w0[g], 3), codes2(w1[g], 3)};
+                    for (int g = 0; g < G; ++g) {
+                        const uint32_t v0 = w0[g] >> 8, v1 = w1[g] >> 8;
+                        const uint32_t ka[4] = {w0[g] & 0x000F000Fu, w1[g] & 0x000F000Fu, w0[g] & 0x00F000F0u, w1[g] & 0x00F000F0u};
+                        const uint32_t kc[4] = {v0 & 0x000F000Fu, v1 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x00F000F0u};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float d[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma(d, ka, qf[nt][2 * g][0], qf[nt][2 * g][1]);
-                        mma(d, kc, qf[nt][2 * g + 1][0], qf[nt][2 * g + 1][1]);
-                        s[nt][0] = fmaf(d[0], f0[g], s[nt][0]);
-                        s[nt][1] = fmaf(d[1], f0[g], s[nt][1]);
-                        s[nt][2] = fmaf(d[2], f1[g], s[nt][2]);
-                        s[nt][3] = fmaf(d[3], f1[g], s[nt][3]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float2 st;
+                            if constexpr (NT == 1) st = start1[g];
+                            else st = *reinterpret_cast<const float2*>(&s_start[warp][g][nt * 8 + 2 * c]);
+                            float d[4];
+                            mma_f16(d, ka, qf[nt][2 * g][0], qf[nt][2 * g][1], st.x, st.y, st.x, st.y);
+                            mma_f16(d, kc, qf[nt][2 * g + 1][0], qf[nt][2 * g + 1][1], d[0], d[1], d[2], d[3]);
+                            s[u][nt][0] = g ? fmaf(d[0], f0[g], s[u][nt][0]) : d[0] * f0[g];
+                            s[u][nt][1] = g ? fmaf(d[1], f0[g], s[u][nt][1]) : d[1] * f0[g];
+                            s[u][nt][2] = g ? fmaf(d[2], f1[g], s[u][nt][2]) : d[2] * f1[g];
+                            s[u][nt][3] = g ? fmaf(d[3], f1[g], s[u][nt][3]) : d[3] * f1[g];
+                        }
                     }
                 }
-            }
-            // ---- mask (steps at an edge), running maximum, P
-            const int j0 = kr.block(i) * PAGED_STEP;
-            const int ja = j0 + (I4 ? token4(r) : r), jb = ja + 8;
-            if (!all_see(j0, j0 + PAGED_STEP - 1, p0, p1, a.window, a.n_sink)) {
+                // ---- mask (steps at an edge, and a pass's missing last step)
+                if (!clean(i + u) || i + u >= n_real) {
+                    const int j0 = kr.block(i + u) * PAGED_STEP;
+                    const int ja = i + u < n_real ? j0 + (I4 ? token4(r) : r) : INT_MAX - 8, jb = ja + 8;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        if (!sees(ja, rp[nt][e], a.window, a.n_sink)) s[nt][e] = -INFINITY;
-                        if (!sees(jb, rp[nt][e], a.window, a.n_sink)) s[nt][2 + e] = -INFINITY;
-                    }
+                        for (int e = 0; e < 2; ++e) {
+                            if (!sees(ja, rp[nt][e], a.window, a.n_sink)) s[u][nt][e] = -INFINITY;
+                            if (!sees(jb, rp[nt][e], a.window, a.n_sink)) s[u][nt][2 + e] = -INFINITY;
+                        }
+                }
             }
+            // ---- running maximum, P
             bool need = false;
             float mx[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float v = fmaxf(s[nt][e], s[nt][2 + e]);
+                    float v = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
+#pragma unroll
+                    for (int u = 1; u < U; ++u) v = fmaxf(v, fmaxf(s[u][nt][e], s[u][nt][2 + e]));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                    mx[nt][e] = v * a.scale_log2;
+                    mx[nt][e] = v * sc[nt][e];
                     need = need || mx[nt][e] > m[nt][e] + 8.f;
                 }
             if (__any_sync(0xffffffffu, need)) {
@@ -364,62 +453,66 @@ __global__ void __launch_bounds__(W * 32, 2)
                         }
                     }
             }
-            uint32_t pb[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float pv[4];
+            for (int u = 0; u < U; ++u) {
+                const uint32_t vb = ring + (stage * U + u) * S::BYTES + S::KV;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float ref = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
-                    pv[e] = pow2(fmaf(s[nt][e], a.scale_log2, -ref));
-                    pv[2 + e] = pow2(fmaf(s[nt][2 + e], a.scale_log2, -ref));
-                    l[nt][e] += pv[e] + pv[2 + e];
-                }
-                pb[nt][0] = transpose8(pack2(pv[0], pv[1]));
-                pb[nt][1] = transpose8(pack2(pv[2], pv[3]));
-            }
-            if constexpr (!I4) {
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int t = 0; t < KT; ++t) {
-                    uint32_t v[4];
-                    const int tok = ((lane >> 4) << 3) + (lane & 7), ch = 2 * t + ((lane >> 3) & 1);
-                    ldsm4t(v, vb + tok * S::ROW + ((ch ^ (tok & 7)) << 4));
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma(o[t][nt], v, pb[nt][0], pb[nt][1]);
-                }
-            } else {
-                const uint8_t* vp = ring_p + stage * S::BYTES + S::KV;
-                const uint8_t* sp = vp + S::KV + PAGED_STEP * S::SCALE;
-                // tokens of columns 2c, 2c + 1, 2c + 8, 2c + 9 of V^T
-                const int tk[4] = {c, 4 + (c ^ 1), 8 + c, 12 + (c ^ 1)};
-                uint32_t v[4][G / 2], f[4][G / 2];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    if constexpr (D == 128) {
-                        const uint2 w = *reinterpret_cast<const uint2*>(
-                            vp + tk[u] * S::ROW + (((r >> 1) ^ (((tk[u] >> 1) & 1) << 1)) << 4) + ((r & 1) << 3));
-                        const uint2 g = *reinterpret_cast<const uint2*>(sp + tk[u] * 8);
-                        v[u][0] = w.x; v[u][1] = w.y;
-                        f[u][0] = g.x; f[u][1] = g.y;
-                    } else {
-                        v[u][0] = *reinterpret_cast<const uint32_t*>(vp + tk[u] * S::ROW + (r << 2));
-                        f[u][0] = *reinterpret_cast<const uint32_t*>(sp + tk[u] * 4);
+                    for (int e = 0; e < 2; ++e) {
+                        const float ref = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+                        s[u][nt][e] = pow2(fmaf(s[u][nt][e], sc[nt][e], -ref));
+                        s[u][nt][2 + e] = pow2(fmaf(s[u][nt][2 + e], sc[nt][e], -ref));
+                        l[nt][e] += s[u][nt][e] + s[u][nt][2 + e];
                     }
-                }
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const uint32_t sel = (g & 1) ? 0x7632 : 0x5410;  // the 16-bit half of group g
-                    const uint32_t x01 = __byte_perm(v[0][g >> 1], v[1][g >> 1], sel);
-                    const uint32_t x23 = __byte_perm(v[2][g >> 1], v[3][g >> 1], sel);
-                    const uint32_t f01 = __byte_perm(f[0][g >> 1], f[1][g >> 1], sel);
-                    const uint32_t f23 = __byte_perm(f[2][g >> 1], f[3][g >> 1], sel);
-                    const uint32_t va[4] = {codes2(x01, 0), codes2(x01, 1), codes2(x23, 0), codes2(x23, 1)};
-                    const uint32_t vc[4] = {codes2(x01, 2), codes2(x01, 3), codes2(x23, 2), codes2(x23, 3)};
+                if constexpr (!I4) {
+                    uint32_t pb[NT][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const uint32_t b0 = mul2(pb[nt][0], f01), b1 = mul2(pb[nt][1], f23);
-                        mma(o[2 * g][nt], va, b0, b1);
-                        mma(o[2 * g + 1][nt], vc, b0, b1);
+                        pb[nt][0] = transpose8(pack2(s[u][nt][0], s[u][nt][1]));
+                        pb[nt][1] = transpose8(pack2(s[u][nt][2], s[u][nt][3]));
+                    }
+#pragma unroll
+                    for (int t = 0; t < KT; ++t) {
+                        uint32_t v[4];
+                        const int tok = ((lane >> 4) << 3) + (lane & 7), ch = 2 * t + ((lane >> 3) & 1);
+                        ldsm4t(v, vb + tok * S::ROW + ((ch ^ (tok & 7)) << 4));
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma(o[t][nt], v, pb[nt][0], pb[nt][1]);
+                    }
+                } else if (u == 0 || i + u < n_real) {  // (a missing step's place in the ring holds no values)
+                    const uint8_t* vp = ring_p + (stage * U + u) * S::BYTES + S::KV;
+                    const uint8_t* sp = vp + S::KV + PAGED_STEP * S::SCALE;
+                    float f0[G], f1[G];  // scales of the keys whose P this lane holds
+                    scales<G>(sp + token4(r) * S::SCALE, f0);
+                    scales<G>(sp + (token4(r) + 8) * S::SCALE, f1);
+                    // tokens of columns 2c, 2c + 1, 2c + 8, 2c + 9 of V^T
+                    const int tk[4] = {c, 4 + (c ^ 1), 8 + c, 12 + (c ^ 1)};
+                    uint32_t v[4][G / 2];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if constexpr (D == 128) {
+                            const uint2 w = *reinterpret_cast<const uint2*>(
+                                vp + tk[q] * S::ROW + (((r >> 1) ^ (((tk[q] >> 1) & 1) << 1)) << 4) + ((r & 1) << 3));
+                            v[q][0] = w.x; v[q][1] = w.y;
+                        } else {
+                            v[q][0] = *reinterpret_cast<const uint32_t*>(vp + tk[q] * S::ROW + (r << 2));
+                        }
+                    }
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        const uint32_t sel = (g & 1) ? 0x7632 : 0x5410;  // the 16-bit half of group g
+                        const uint32_t x01 = __byte_perm(v[0][g >> 1], v[1][g >> 1], sel);
+                        const uint32_t x23 = __byte_perm(v[2][g >> 1], v[3][g >> 1], sel);
+                        const uint32_t va[4] = {codes2(x01, 0), codes2(x01, 1), codes2(x23, 0), codes2(x23, 1)};
+                        const uint32_t vc[4] = {codes2(x01, 2), codes2(x01, 3), codes2(x23, 2), codes2(x23, 3)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint32_t b0 = transpose8(pack2(s[u][nt][0] * f0[g], s[u][nt][1] * f0[g]));
+                            const uint32_t b1 = transpose8(pack2(s[u][nt][2] * f1[g], s[u][nt][3] * f1[g]));
+                            mma(o[2 * g][nt], va, b0, b1);
+                            mma(o[2 * g + 1][nt], vc, b0, b1);
+                        }
                     }
                 }
             }
@@ -504,31 +597,65 @@ __global__ void __launch_bounds__(W * 32, 2)
             __syncthreads();
             if (last_sh) {
                 __threadfence();
-                // part k is CTA first + k's: its slot 1 when the item starts there, else slot 0
+                // Part k is CTA first + k's: its slot 1 when the item starts there, else slot 0.  First the
+                // parts' weights, a warp per pair; then threads share the parts of every four outputs.
                 const size_t sf = paged_slot_floats(D);
                 const float* base = a.part + (size_t)2 * first * sf;
                 auto part = [&](int k) { return base + (size_t)(2 * k + (k == 0 ? 1 : 0)) * sf; };
-                float* wt = so;  // weights of the parts of one pair
-                for (int p = 0; p < npair; ++p) {
+                float* wt = reinterpret_cast<float*>(smem);  // [part][R], of the ring
+                for (int p = warp; p < npair; p += W) {
                     float mx = -INFINITY;
-                    for (int k = 0; k < n_part; ++k) mx = max_nan(mx, __ldcg(part(k) + PAGED_MAX_TILE * D + p));
+                    for (int k = lane; k < n_part; k += 32) {
+                        const float v = __ldcg(part(k) + PAGED_MAX_TILE * D + p);
+                        wt[k * R + p] = v;
+                        mx = max_nan(mx, v);
+                    }
+#pragma unroll
+                    for (int x2 = 16; x2; x2 >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, x2));
                     const float ref = mx == -INFINITY ? 0.f : mx;
-                    for (int k = tid; k < n_part; k += T) wt[k] = pow2(__ldcg(part(k) + PAGED_MAX_TILE * D + p) - ref);
-                    __syncthreads();
                     float sum = 0.f;
-                    for (int k = 0; k < n_part; ++k) sum += wt[k] * __ldcg(part(k) + PAGED_MAX_TILE * (D + 1) + p);
+                    for (int k = lane; k < n_part; k += 32) {
+                        const float f = pow2(wt[k * R + p] - ref);
+                        wt[k * R + p] = f;
+                        sum += f * __ldcg(part(k) + PAGED_MAX_TILE * (D + 1) + p);
+                    }
+#pragma unroll
+                    for (int x2 = 16; x2; x2 >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x2);
                     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    for (int e = 2 * tid; e < D; e += 2 * T) {
-                        float y0 = 0.f, y1 = 0.f;
-#pragma unroll 4
-                        for (int k = 0; k < n_part; ++k) {
-                            const float2 v = __ldcg(reinterpret_cast<const float2*>(part(k) + p * D + e));
-                            y0 = fmaf(v.x, wt[k], y0);
-                            y1 = fmaf(v.y, wt[k], y1);
+                    for (int k = lane; k < n_part; k += 32) wt[k * R + p] *= inv;
+                }
+                __syncthreads();
+                // each warp adds every W-th part of 32 x 4 outputs, then the warps' sums are added in order
+                constexpr int V4 = D / 4;
+                float4* acc = reinterpret_cast<float4*>(wt + ((n_part * R + 3) & ~3));  // [W][32 lanes] of one round
+                for (int q0 = 0; q0 < npair * V4; q0 += 32) {
+                    const int q = q0 + lane, p = q / V4, e4 = q % V4;
+                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (q < npair * V4)
+#pragma unroll 8
+                        for (int k = warp; k < n_part; k += W) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(part(k) + p * D) + e4);
+                            const float f = wt[k * R + p];
+                            y.x = fmaf(v.x, f, y.x);
+                            y.y = fmaf(v.y, f, y.y);
+                            y.z = fmaf(v.z, f, y.z);
+                            y.w = fmaf(v.w, f, y.w);
+                        }
+                    acc[warp * 32 + lane] = y;
+                    __syncthreads();
+                    if (warp == 0 && q < npair * V4) {
+                        float4 t = acc[lane];
+#pragma unroll
+                        for (int x2 = 1; x2 < W; ++x2) {
+                            const float4 v = acc[x2 * 32 + lane];
+                            t.x += v.x;
+                            t.y += v.y;
+                            t.z += v.z;
+                            t.w += v.w;
                         }
                         const long long row = si.row0 + p / a.group;
-                        *reinterpret_cast<uint32_t*>(out + (row * a.hq + head * a.group + p % a.group) * D + e) =
-                            pack2(y0 * inv, y1 * inv);
+                        *reinterpret_cast<uint2*>(out + (row * a.hq + head * a.group + p % a.group) * D + 4 * e4) =
+                            make_uint2(pack2(t.x, t.y), pack2(t.z, t.w));
                     }
                     __syncthreads();
                 }
@@ -539,23 +666,25 @@ __global__ void __launch_bounds__(W * 32, 2)
     }
 }
 
-template <bool I4, int D, int NT, int W, int STAGES> void launch_one(const PagedAttn& a, cudaStream_t s) {
-    using Cfg = SplitCfg<I4, D, NT, W, STAGES>;
-    auto kern = k_paged_split<I4, D, NT, W, STAGES>;
+template <bool I4, int D, int NT, int W, int STAGES, int U> void launch_one(const PagedAttn& a, cudaStream_t s) {
+    using Cfg = SplitCfg<I4, D, NT, W, STAGES, U>;
+    auto kern = k_paged_split<I4, D, NT, W, STAGES, U>;
     static const bool ready = [&] {
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
         return true;
     }();
     (void)ready;
-    kern<<<304, W * 32, Cfg::SMEM, s>>>(a);  // two CTAs on each of 152 SMs
+    kern<<<SPLIT_CTAS, W * 32, Cfg::SMEM, s>>>(a);
     note_launch(1);
 }
 template <bool I4, int D> void launch_nt(const PagedAttn& a, cudaStream_t s) {
     const int pairs = a.max_q * a.group;
-    constexpr int W1 = I4 ? 8 : 4, ST = I4 ? 5 : 3;
-    if (pairs <= 8) launch_one<I4, D, 1, W1, ST>(a, s);
-    else if (pairs <= 16) launch_one<I4, D, 2, 4, ST>(a, s);
-    else launch_one<I4, D, 4, 4, ST>(a, s);
+    constexpr int ST = I4 ? 5 : 3;
+    if (pairs <= 8) {
+        if constexpr (I4) launch_one<I4, D, 1, 8, 3, 2>(a, s);
+        else launch_one<I4, D, 1, 4, ST, 1>(a, s);
+    } else if (pairs <= 16) launch_one<I4, D, 2, 4, ST, 1>(a, s);
+    else launch_one<I4, D, 4, 4, ST, 1>(a, s);
 }
 
 }  // namespace
