@@ -54,6 +54,20 @@ __device__ __forceinline__ int k4_bit(int e) { return 4 * (e >> 1) + 16 * (e & 1
 // Four consecutive dims 32g + 4r .. +3 of a V row are one 16-bit word, dim e at bit 4 e.
 __device__ __forceinline__ int v4_half(int d, int g, int r) { return r * (d / 16) + 2 * g; }
 
+// Two codes as bf16 values (n - 8) / 64, exact.  A code n + 8 alone in the low bits of a bf16 is
+// (n + 8) 2^-133, and alone at bits 4..7 it is 16 times that (bf16 is linear up to bit pattern 255),
+// so a mask selects a pair and one multiply-add shifts and scales it; no bits are moved for half of
+// the codes.  HI: the codes at bits 4..7 and 20..23.
+constexpr float CODE_UNIT = 64.f;
+template <bool HI> __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
+    uint32_t x = w & (HI ? 0x00F000F0u : 0x000F000Fu);
+    const uint32_t up = HI ? 0x7D007D00u : 0x7F007F00u;  // 2^123, 2^127
+    const uint32_t off = 0xBE00BE00u;                    // -1/8
+    const __nv_bfloat162 r = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&up),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&off));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // Arguments of the attention kernels.
 struct PagedAttn {
     PageView pg;
@@ -131,6 +145,10 @@ template <int BYTES> __device__ __forceinline__ void cp_async(uint32_t dst, cons
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(ok ? BYTES : 0)
                      : "memory");
+}
+template <int BYTES> __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }

@@ -22,9 +22,9 @@
 // word (codes at bits 4..7 count 16 times, and their queries a sixteenth); queries are turned into
 // fp16 with the row's own power of two, the -8 is the accumulator's start, -8 2^-24 sum q, and a
 // key's scales multiply its partial scores of each 32 dims in fp32: the scores are exact to fp32.
-// Values: n + 128 is the bf16 0x4300 | n, one subtraction gives n - 8 exactly (here an offset in
-// the sums would cancel against results that are far smaller than it), and the value's scale
-// multiplies P in fp32 before its one rounding to bf16.
+// Values: a mask and one multiply-add give (n - 8) / 64 exactly (see code_pair; an offset left in the
+// sums would cancel against results that are far smaller than it), and the value's scale
+// multiplies P in fp32 before its one rounding to bf16; the 64 goes into the last division.
 // Measured (GB300, 6.8 TB/s copy rate): 64 sequences of 3.3-8.2 K tokens, window 4096, Mistral-7B
 // heads 172 us, 6.2 TB/s of pages.
 // Tokens that no row sees are filled with zeros instead of loaded (values, scales), so what they
@@ -87,14 +87,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return r;
 }
 __device__ __forceinline__ float2 unpack_f16(uint32_t x) { return __half22float2(*reinterpret_cast<__half2*>(&x)); }
-// Codes at bits 4 i and 16 + 4 i of w as two bf16 values n - 8.
-__device__ __forceinline__ uint32_t codes2(uint32_t w, int i) {
-    uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;  // 128 + n
-    const uint32_t off = 0x43084308u;                            // 136
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&off));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 // The G bf16 scales of a row as fp32.
 template <int G> __device__ __forceinline__ void scales(const uint8_t* p, float (&f)[G]) {
     uint32_t w[G / 2];
@@ -205,6 +197,20 @@ __global__ void __launch_bounds__(W * 32, 2)
     const uint32_t ring = smem_u32(smem) + warp * STAGES * U * S::BYTES;
     uint8_t* ring_p = smem + warp * STAGES * U * S::BYTES;
 
+    // where this lane's 16-byte chunks of a step come from and go to; the chunks of a row are permuted
+    // in shared memory so that the rows of one read fall on distinct banks (bf16: chunk ^ row % 8)
+    constexpr int CH = S::ROW / 16;
+    auto ring_at = [&](uint32_t first, int u) {  // the lane's chunk 32 u further on: 32 / CH rows down
+        return (I4 ? first : first ^ (uint32_t)(((32 / CH * u) & 7) << 4)) + u * 512;
+    };
+    const int t_lane = lane / CH, ch_lane = lane % CH;
+    const uint32_t k_at = t_lane * S::ROW + (I4 ? ch_lane : ch_lane ^ (t_lane & 7)) * 16;
+    const uint32_t v_at = S::KV + t_lane * S::ROW +
+                          (!I4 ? ch_lane ^ (t_lane & 7) : D == 128 ? ch_lane ^ (((t_lane >> 1) & 1) << 1) : ch_lane) * 16;
+    const char* k_lane = a.pg.k + lane * 16;
+    const char* v_lane = a.pg.v + lane * 16;
+    const char* s_lane = (lane < 16 ? a.pg.ks : a.pg.vs) + (lane & 15) * S::SCALE;
+
     while (x < x_end) {
         while (pre[seq + 1] <= x) ++seq;  // skips sequences without steps
         const SeqInfo si = seq_info(a, seq);
@@ -226,28 +232,26 @@ __global__ void __launch_bounds__(W * 32, 2)
         auto load = [&](int i, uint32_t dst, int entry) {
             const int j0 = kr.block(i) * PAGED_STEP;
             const long long row = page_row(a.pg, checked_page(a.pg, entry, a.err), head, j0 & ((1 << a.pg.shift) - 1));
-            const bool whole = clean(i);
-            const char* ksrc = a.pg.k + row * S::ROW + lane * 16;
-            const char* vsrc = a.pg.v + row * S::ROW + lane * 16;
-            constexpr int CH = S::ROW / 16, N = S::KV / 512;
+            const char* ksrc = k_lane + row * S::ROW;
+            const char* vsrc = v_lane + row * S::ROW;
+            constexpr int N = S::KV / 512;
+            if (clean(i)) {
 #pragma unroll
-            for (int u = 0; u < N; ++u) {
-                const int q = lane + 32 * u, t = q / CH, ch = q % CH;
-                const bool ok = whole || seen_by_any(j0 + t, p0, p1, a.window, a.n_sink);
-                int kch, vch;  // chunk order in shared memory: rows of one read on distinct banks
-                if constexpr (!I4) kch = vch = ch ^ (t & 7);
-                else {
-                    kch = ch;
-                    vch = D == 128 ? ch ^ (((t >> 1) & 1) << 1) : ch;
+                for (int u = 0; u < N; ++u) {
+                    cp_async<16>(dst + ring_at(k_at, u), ksrc + u * 512);
+                    cp_async<16>(dst + ring_at(v_at, u), vsrc + u * 512);
                 }
-                cp_async<16>(dst + t * S::ROW + kch * 16, ksrc + u * 512, ok);
-                cp_async<16>(dst + S::KV + t * S::ROW + vch * 16, vsrc + u * 512, ok);
-            }
-            if constexpr (I4) {
-                const int t = lane & 15;
-                const char* src = (lane < 16 ? a.pg.ks : a.pg.vs) + (row + t) * S::SCALE;
-                cp_async<S::SCALE>(dst + 2 * S::KV + lane * S::SCALE, src,
-                                   whole || seen_by_any(j0 + t, p0, p1, a.window, a.n_sink));
+                if constexpr (I4) cp_async<S::SCALE>(dst + 2 * S::KV + lane * S::SCALE, s_lane + row * S::SCALE);
+            } else {
+#pragma unroll
+                for (int u = 0; u < N; ++u) {
+                    const bool ok = seen_by_any(j0 + (lane + 32 * u) / CH, p0, p1, a.window, a.n_sink);
+                    cp_async<16>(dst + ring_at(k_at, u), ksrc + u * 512, ok);
+                    cp_async<16>(dst + ring_at(v_at, u), vsrc + u * 512, ok);
+                }
+                if constexpr (I4)
+                    cp_async<S::SCALE>(dst + 2 * S::KV + lane * S::SCALE, s_lane + row * S::SCALE,
+                                       seen_by_any(j0 + (lane & 15), p0, p1, a.window, a.n_sink));
             }
         };
         auto entry_at = [&](int i) { return page_entry(a.pg, seq, kr.block(i) * PAGED_STEP); };
@@ -504,8 +508,9 @@ __global__ void __launch_bounds__(W * 32, 2)
                         const uint32_t sel = (g & 1) ? 0x7632 : 0x5410;  // the 16-bit half of group g
                         const uint32_t x01 = __byte_perm(v[0][g >> 1], v[1][g >> 1], sel);
                         const uint32_t x23 = __byte_perm(v[2][g >> 1], v[3][g >> 1], sel);
-                        const uint32_t va[4] = {codes2(x01, 0), codes2(x01, 1), codes2(x23, 0), codes2(x23, 1)};
-                        const uint32_t vc[4] = {codes2(x01, 2), codes2(x01, 3), codes2(x23, 2), codes2(x23, 3)};
+                        const uint32_t y01 = x01 >> 8, y23 = x23 >> 8;
+                        const uint32_t va[4] = {code_pair<false>(x01), code_pair<true>(x01), code_pair<false>(x23), code_pair<true>(x23)};
+                        const uint32_t vc[4] = {code_pair<false>(y01), code_pair<true>(y01), code_pair<false>(y23), code_pair<true>(y23)};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             const uint32_t b0 = transpose8(pack2(s[u][nt][0] * f0[g], s[u][nt][1] * f0[g]));
@@ -557,7 +562,7 @@ __global__ void __launch_bounds__(W * 32, 2)
                 sm[w][tid] = f;
             }
             sM[tid] = mx;
-            sL[tid] = sum;
+            sL[tid] = I4 ? sum * (1.f / CODE_UNIT) : sum;  // (the outputs lack the unit of their codes)
         }
         __syncthreads();
         const bool whole_item = s0 == 0 && s1 == steps;
@@ -681,7 +686,7 @@ template <bool I4, int D> void launch_nt(const PagedAttn& a, cudaStream_t s) {
     const int pairs = a.max_q * a.group;
     constexpr int ST = I4 ? 5 : 3;
     if (pairs <= 8) {
-        if constexpr (I4) launch_one<I4, D, 1, 8, 3, 2>(a, s);
+        if constexpr (I4) launch_one<I4, D, 1, 8, 2, 2>(a, s);
         else launch_one<I4, D, 1, 4, ST, 1>(a, s);
     } else if (pairs <= 16) launch_one<I4, D, 2, 4, ST, 1>(a, s);
     else launch_one<I4, D, 4, 4, ST, 1>(a, s);

@@ -198,15 +198,19 @@ struct Walk {
     }
 };
 
-// Eight bf16 values n s of a word with pairs (2i, 2i + 1) at bits 4 i and 16 + 4 i.
-__device__ __forceinline__ uint32_t pair_value(uint32_t w, int i, uint32_t scale2) {
-    uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-    const uint32_t off = 0x43084308u;
-    const __nv_bfloat162 n = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&off));
-    const __nv_bfloat162 v = __hmul2(n, *reinterpret_cast<__nv_bfloat162*>(&scale2));
+// A pair's values n s: (n - 8) / 64 exactly, then rounded once as the product with 64 s.
+template <bool HI> __device__ __forceinline__ uint32_t pair_value(uint32_t w, uint32_t scale2) {
+    const uint32_t n = code_pair<HI>(w);
+    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&n), *reinterpret_cast<__nv_bfloat162*>(&scale2));
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ uint32_t both(uint32_t w, int hi) { return __byte_perm(w, w, hi ? 0x3232 : 0x1010); }
+// One of two bf16 scales, twice, times 64.
+__device__ __forceinline__ uint32_t both(uint32_t w, int hi) {
+    uint32_t s2 = __byte_perm(w, w, hi ? 0x3232 : 0x1010);
+    const uint32_t unit = 0x42804280u;
+    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&s2), *reinterpret_cast<const __nv_bfloat162*>(&unit));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
 
 template <bool I4, int D>
 __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
@@ -812,7 +816,7 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                 const uint32_t sc = both(ksc[g >> 1], g & 1);
                 const int ch = 4 * (g & 1) + c;
                 *reinterpret_cast<uint4*>(dk + (g >> 1) * K_HALF + tk * 128 + ((ch ^ (tk & 7)) << 4)) =
-                    make_uint4(pair_value(kw[i], 0, sc), pair_value(kw[i], 1, sc), pair_value(kw[i], 2, sc), pair_value(kw[i], 3, sc));
+                    make_uint4(pair_value<false>(kw[i], sc), pair_value<true>(kw[i], sc), pair_value<false>(kw[i] >> 8, sc), pair_value<true>(kw[i] >> 8, sc));
             }
             uint8_t* dv = dk + KB;
 #pragma unroll
@@ -825,7 +829,7 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                     const uint32_t y0 = h0 | (h0 << 12), y1 = h1 | (h1 << 12);  // nibbles 0, 1 and 2, 3 as pairs at bits 0 and 8
                     const int ch = 4 * g + c;
                     const int at = D == 128 ? t * 128 + ((ch ^ (t & 7)) << 4) : t * 64 + ((ch ^ ((t >> 1) & 3)) << 4);
-                    *reinterpret_cast<uint4*>(dv + at) = make_uint4(pair_value(y0, 0, sc), pair_value(y0, 2, sc), pair_value(y1, 0, sc), pair_value(y1, 2, sc));
+                    *reinterpret_cast<uint4*>(dv + at) = make_uint4(pair_value<false>(y0, sc), pair_value<false>(y0 >> 8, sc), pair_value<false>(y1, sc), pair_value<false>(y1 >> 8, sc));
                 }
             fence_async_smem();
             warp_arrive(&own_full[st]);
