@@ -342,11 +342,11 @@ __global__ void __launch_bounds__(W * 32, 2)
 #pragma unroll
             for (int g = 0; g < G; ++g) start1[g] = *reinterpret_cast<const float2*>(&s_start[warp][g][2 * c]);
         }
-        float m[NT][2], l[NT][2], o[KT][NT][4];
+        float m[NT][2], ref[NT][2], l[NT][2], o[KT][NT][4];  // ref: m, or 0 while no key was seen
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = -INFINITY;
-            l[nt][0] = l[nt][1] = 0.f;
+            ref[nt][0] = ref[nt][1] = l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
             for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -425,9 +425,8 @@ __global__ void __launch_bounds__(W * 32, 2)
                         }
                 }
             }
-            // ---- running maximum, P
+            // ---- running maximum: looked at across lanes only when some score has outgrown it by 2^8
             bool need = false;
-            float mx[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -435,20 +434,23 @@ __global__ void __launch_bounds__(W * 32, 2)
                     float v = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
 #pragma unroll
                     for (int u = 1; u < U; ++u) v = fmaxf(v, fmaxf(s[u][nt][e], s[u][nt][2 + e]));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                    mx[nt][e] = v * sc[nt][e];
-                    need = need || mx[nt][e] > m[nt][e] + 8.f;
+                    need = need || v * sc[nt][e] > m[nt][e] + 8.f;
                 }
             if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        if (!(mx[nt][e] > m[nt][e] + 8.f)) continue;
-                        const float corr = pow2(m[nt][e] - mx[nt][e]);
-                        m[nt][e] = mx[nt][e];
+                        float v = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
+#pragma unroll
+                        for (int u = 1; u < U; ++u) v = fmaxf(v, fmaxf(s[u][nt][e], s[u][nt][2 + e]));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                        const float mx = v * sc[nt][e];
+                        if (!(mx > m[nt][e] + 8.f)) continue;
+                        const float corr = pow2(m[nt][e] - mx);
+                        m[nt][e] = ref[nt][e] = mx;
                         l[nt][e] *= corr;
 #pragma unroll
                         for (int t = 0; t < KT; ++t) {
@@ -464,9 +466,8 @@ __global__ void __launch_bounds__(W * 32, 2)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float ref = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
-                        s[u][nt][e] = pow2(fmaf(s[u][nt][e], sc[nt][e], -ref));
-                        s[u][nt][2 + e] = pow2(fmaf(s[u][nt][2 + e], sc[nt][e], -ref));
+                        s[u][nt][e] = pow2(fmaf(s[u][nt][e], sc[nt][e], -ref[nt][e]));
+                        s[u][nt][2 + e] = pow2(fmaf(s[u][nt][2 + e], sc[nt][e], -ref[nt][e]));
                         l[nt][e] += s[u][nt][e] + s[u][nt][2 + e];
                     }
                 if constexpr (!I4) {
