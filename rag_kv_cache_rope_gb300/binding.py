@@ -451,43 +451,52 @@ class PagesRef:
         self.t = tuple(x for x in (k, v, table, k_scale, v_scale) if x is not None)
         if any(not x.is_contiguous() or x.device != k.device for x in self.t):
             raise ValueError("the tensors of a paged cache must be contiguous and on one device")
-        self.device, self.dtype, self.n_kv_heads = k.device, k.dtype, k.shape[1]
+        self.device, self.dtype, self.n_kv_heads, self.n_seq = k.device, k.dtype, k.shape[1], table.shape[0]
+        self.index = k.get_device()  # -1: not on a GPU
+        self._checked = None         # the model these pages were last found to fit
         self.head_dim = k.shape[3] * (2 if int4 else 1)
         self.c = Pages(PAGES_INT4 if int4 else PAGES_MODEL, k.shape[2], k.shape[0], table.shape[0], table.shape[1],
                        *[None if x is None else x.data_ptr() for x in (table, k, v, k_scale, v_scale)])
         self.ref = C.byref(self.c)
 
 
+# A decode step makes these calls once per layer with kernels of a few microseconds: the checks below
+# read each property once, and what holds for a pair of handle and pages is remembered in the pages.
 def _paged_stream(h: Handle, pages: PagesRef, stream):
     """The call's stream, after a look at the pages: they must be the handle's model's and on the
     stream's GPU."""
-    want = torch.uint8 if pages.c.format == PAGES_INT4 else torch.bfloat16 if h.cfg.dtype == BF16 else torch.float32
-    if pages.dtype != want or pages.n_kv_heads != h.cfg.n_kv_heads or pages.head_dim != h.cfg.head_dim:
-        raise ValueError("the pages are not of the handle's model")
-    if stream is None:
-        stream = torch.cuda.current_stream(pages.device)
-    if stream.device != pages.device or torch.cuda.current_device() != pages.device.index:
+    if pages._checked is not h.cfg:
+        want = torch.uint8 if pages.c.format == PAGES_INT4 else torch.bfloat16 if h.cfg.dtype == BF16 else torch.float32
+        if pages.dtype != want or pages.n_kv_heads != h.cfg.n_kv_heads or pages.head_dim != h.cfg.head_dim:
+            raise ValueError("the pages are not of the handle's model")
+        if pages.index < 0:
+            raise ValueError("the pages are not on a GPU")
+        pages._checked = h.cfg
+    dev = pages.index
+    if torch.cuda.current_device() != dev or (stream is not None and stream.device_index != dev):
         raise ValueError(f"the pages are on {pages.device}: make it the current device and use a stream of it")
-    return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _paged_rows(h: Handle, pages: PagesRef, t: torch.Tensor, heads: int, what: str) -> int:
     """Distance between the rows of t [rows][heads][head dim] in elements."""
     d = h.cfg.head_dim
     st, sh = t.stride(), t.shape
-    flat = len(sh) == 2 and sh[1] == heads * d and st[1] == 1
-    if not flat and not (len(sh) == 3 and sh[1] == heads and sh[2] == d and st[2] == 1 and (st[1] == d or heads == 1)):
+    if len(sh) == 3:
+        ok = sh[1] == heads and sh[2] == d and st[2] == 1 and (st[1] == d or heads == 1)
+    else:
+        ok = len(sh) == 2 and sh[1] == heads * d and st[1] == 1
+    if not ok:
         raise ValueError(f"{what} must be [rows][{heads}][{d}] with adjacent heads")
-    if t.dtype != (torch.bfloat16 if h.cfg.dtype == BF16 else torch.float32) or t.device != pages.device:
+    if t.dtype is not (torch.bfloat16 if h.cfg.dtype == BF16 else torch.float32) or t.get_device() != pages.index:
         raise ValueError(f"{what} must be of the model's dtype and on {pages.device}")
     return st[0] if sh[0] > 1 else heads * d
 
 
-def _paged_index(pages: PagesRef, n: int, what: str, *ts):
-    for t in ts:
-        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n or
-                              t.device != pages.device):
-            raise ValueError(f"{what} must be contiguous int32 of at least {n} entries on {pages.device}")
+def _paged_index(pages: PagesRef, n: int, what: str, t: torch.Tensor):
+    if t.dtype is not torch.int32 or t.numel() < n or not t.is_contiguous() or t.get_device() != pages.index:
+        raise ValueError(f"{what} must be contiguous int32 of at least {n} entries on {pages.device}")
+    return t.data_ptr()
 
 
 def paged_append(h: Handle, pages: PagesRef, k_new, v_new, seq, pos, n, max_n, q=None, q_out=None, rot=None,
@@ -495,25 +504,29 @@ def paged_append(h: Handle, pages: PagesRef, k_new, v_new, seq, pos, n, max_n, q
     """k_new, v_new (and q): [rows][heads][head dim], rows at any stride of 16 bytes; seq, pos, rot
     int32 per row; n a device int32 count of at most max_n rows."""
     s = _paged_stream(h, pages, stream)
-    hkv, hq = h.cfg.n_kv_heads, h.cfg.n_q_heads
+    hkv = h.cfg.n_kv_heads
     ld_k, ld_v = _paged_rows(h, pages, k_new, hkv, "k_new"), _paged_rows(h, pages, v_new, hkv, "v_new")
-    _paged_index(pages, max_n, "seq, pos and rot", seq, pos, rot)
-    _paged_index(pages, 1, "n", n)
-    if min(k_new.shape[0], v_new.shape[0]) < max_n:
+    seq, pos = _paged_index(pages, max_n, "seq", seq), _paged_index(pages, max_n, "pos", pos)
+    if rot is not None:
+        rot = _paged_index(pages, max_n, "rot", rot)
+    n = _paged_index(pages, 1, "n", n)
+    if k_new.shape[0] < max_n or v_new.shape[0] < max_n:
         raise ValueError("fewer rows than max_n")
-    ld_q = 0
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out go together")
-    if q is not None:
+    ld_q = pq = po = None
+    if q is not None and q_out is not None:
+        hq = h.cfg.n_q_heads
         ld_q = _paged_rows(h, pages, q, hq, "q")
         if _paged_rows(h, pages, q_out, hq, "q_out") != hq * h.cfg.head_dim or min(q.shape[0], q_out.shape[0]) < max_n:
             raise ValueError("q_out must hold max_n adjacent rows, and q as many")
+        pq, po = q.data_ptr(), q_out.data_ptr()
+    elif q is not None or q_out is not None:
+        raise ValueError("q and q_out go together")
     if max_n == 0:
         return
-    _check(lib().paged_append(h.ptr, pages.ref, k_new.data_ptr(), ld_k, v_new.data_ptr(), ld_v,
-                              None if q is None else q.data_ptr(), ld_q, None if q is None else q_out.data_ptr(),
-                              seq.data_ptr(), pos.data_ptr(), None if rot is None else rot.data_ptr(), n.data_ptr(),
-                              max_n, s), h)
+    rc = lib().paged_append(h.ptr, pages.ref, k_new.data_ptr(), ld_k, v_new.data_ptr(), ld_v, pq, ld_q or 0, po, seq,
+                            pos, rot, n, max_n, s)
+    if rc:
+        _check(rc, h)
 
 
 def paged_gather(h: Handle, pages: PagesRef, seq, pos, n, max_n, k_out, v_out, rot=None, stream=None):
@@ -523,12 +536,15 @@ def paged_gather(h: Handle, pages: PagesRef, seq, pos, n, max_n, k_out, v_out, r
     for t in (k_out, v_out):
         if _paged_rows(h, pages, t, hkv, "k_out and v_out") != hkv * h.cfg.head_dim or t.shape[0] < max_n:
             raise ValueError("k_out and v_out must hold max_n adjacent rows")
-    _paged_index(pages, max_n, "seq, pos and rot", seq, pos, rot)
-    _paged_index(pages, 1, "n", n)
+    seq, pos = _paged_index(pages, max_n, "seq", seq), _paged_index(pages, max_n, "pos", pos)
+    if rot is not None:
+        rot = _paged_index(pages, max_n, "rot", rot)
+    n = _paged_index(pages, 1, "n", n)
     if max_n == 0:
         return
-    _check(lib().paged_gather(h.ptr, pages.ref, seq.data_ptr(), pos.data_ptr(), None if rot is None else rot.data_ptr(),
-                              n.data_ptr(), max_n, k_out.data_ptr(), v_out.data_ptr(), s), h)
+    rc = lib().paged_gather(h.ptr, pages.ref, seq, pos, rot, n, max_n, k_out.data_ptr(), v_out.data_ptr(), s)
+    if rc:
+        _check(rc, h)
 
 
 def paged_attention(h: Handle, pages: PagesRef, q, q_start, kv_len, max_q, out, window=0, n_sink=0, stream=None):
@@ -536,16 +552,18 @@ def paged_attention(h: Handle, pages: PagesRef, q, q_start, kv_len, max_q, out, 
     adjacent; q_start int32 [n_seq + 1], kv_len int32 [n_seq] on the device; max_q: most query rows of
     one sequence."""
     s = _paged_stream(h, pages, stream)
-    hq = h.cfg.n_q_heads
+    hq, n_seq, rows = h.cfg.n_q_heads, pages.n_seq, q.shape[0]
     ld_q = _paged_rows(h, pages, q, hq, "q")
-    if _paged_rows(h, pages, out, hq, "out") != hq * h.cfg.head_dim or out.shape[0] < q.shape[0]:
+    if _paged_rows(h, pages, out, hq, "out") != hq * h.cfg.head_dim or out.shape[0] < rows:
         raise ValueError("out must hold as many adjacent rows as q")
-    _paged_index(pages, pages.c.n_seq, "kv_len", kv_len)
-    _paged_index(pages, pages.c.n_seq + 1, "q_start", q_start)
-    if q.shape[0] == 0:
+    kv_len = _paged_index(pages, n_seq, "kv_len", kv_len)
+    q_start = _paged_index(pages, n_seq + 1, "q_start", q_start)
+    if rows == 0:
         return
-    _check(lib().paged_attention(h.ptr, pages.ref, q.data_ptr(), ld_q, q_start.data_ptr(), kv_len.data_ptr(),
-                                 q.shape[0], max_q, window, n_sink, out.data_ptr(), s), h)
+    rc = lib().paged_attention(h.ptr, pages.ref, q.data_ptr(), ld_q, q_start, kv_len, rows, max_q, window, n_sink,
+                               out.data_ptr(), s)
+    if rc:
+        _check(rc, h)
 
 
 # ---------------------------------------------------------------- weight layout

@@ -122,7 +122,7 @@ template <bool I4, int D, int NT, int W, int STAGES, int U> struct SplitCfg {
     static constexpr int RING = W * STAGES * U * StepCfg<I4, D>::BYTES;
     static constexpr int OPAD = D + 4;  // distinct banks for the four pairs of a quad
     static constexpr int JOIN = W * 8 * NT * OPAD * 4;
-    static constexpr int PARTS = SPLIT_CTAS * 8 * NT * 4 + W * 32 * 16;  // weights of an item's parts, sums of a round
+    static constexpr int PARTS = SPLIT_CTAS * 8 * NT * 4 + W * 4 * 32 * 16;  // weights of an item's parts, sums of a round
     static constexpr int MOST = RING > JOIN ? RING : JOIN;
     static constexpr int SMEM = MOST > PARTS ? MOST : PARTS;
 };
@@ -631,34 +631,45 @@ __global__ void __launch_bounds__(W * 32, 2)
                     for (int k = lane; k < n_part; k += 32) wt[k * R + p] *= inv;
                 }
                 __syncthreads();
-                // each warp adds every W-th part of 32 x 4 outputs, then the warps' sums are added in order
-                constexpr int V4 = D / 4;
-                float4* acc = reinterpret_cast<float4*>(wt + ((n_part * R + 3) & ~3));  // [W][32 lanes] of one round
-                for (int q0 = 0; q0 < npair * V4; q0 += 32) {
-                    const int q = q0 + lane, p = q / V4, e4 = q % V4;
-                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (q < npair * V4)
-#pragma unroll 8
-                        for (int k = warp; k < n_part; k += W) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4*>(part(k) + p * D) + e4);
-                            const float f = wt[k * R + p];
-                            y.x = fmaf(v.x, f, y.x);
-                            y.y = fmaf(v.y, f, y.y);
-                            y.z = fmaf(v.z, f, y.z);
-                            y.w = fmaf(v.w, f, y.w);
+                // each warp adds every W-th part of 128 x 4 outputs (four of a lane: 16 loads on their way), then
+                // the warps' sums are added in order
+                constexpr int V4 = D / 4, Q = 4;
+                const int n_out = npair * V4;
+                float4* acc = reinterpret_cast<float4*>(wt + ((n_part * R + 3) & ~3));  // [W][Q][32] of one round
+                for (int q0 = 0; q0 < n_out; q0 += 32 * Q) {
+                    float4 y[Q];
+#pragma unroll
+                    for (int j = 0; j < Q; ++j) y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                    for (int k = warp; k < n_part; k += W) {
+                        const float4* src = reinterpret_cast<const float4*>(part(k));  // pair p's output e4 is p V4 + e4
+#pragma unroll
+                        for (int j = 0; j < Q; ++j) {
+                            const int q = q0 + 32 * j + lane;
+                            if (q < n_out) {
+                                const float4 v = __ldcg(src + q);
+                                const float f = wt[k * R + q / V4];
+                                y[j].x = fmaf(v.x, f, y[j].x);
+                                y[j].y = fmaf(v.y, f, y[j].y);
+                                y[j].z = fmaf(v.z, f, y[j].z);
+                                y[j].w = fmaf(v.w, f, y[j].w);
+                            }
                         }
-                    acc[warp * 32 + lane] = y;
+                    }
+#pragma unroll
+                    for (int j = 0; j < Q; ++j) acc[(warp * Q + j) * 32 + lane] = y[j];
                     __syncthreads();
-                    if (warp == 0 && q < npair * V4) {
-                        float4 t = acc[lane];
+                    for (int i = tid; i < 32 * Q && q0 + i < n_out; i += T) {
+                        float4 t = acc[i];
 #pragma unroll
                         for (int x2 = 1; x2 < W; ++x2) {
-                            const float4 v = acc[x2 * 32 + lane];
+                            const float4 v = acc[x2 * 32 * Q + i];
                             t.x += v.x;
                             t.y += v.y;
                             t.z += v.z;
                             t.w += v.w;
                         }
+                        const int p = (q0 + i) / V4, e4 = (q0 + i) % V4;
                         const long long row = si.row0 + p / a.group;
                         *reinterpret_cast<uint2*>(out + (row * a.hq + head * a.group + p % a.group) * D + 4 * e4) =
                             make_uint2(pack2(t.x, t.y), pack2(t.z, t.w));
