@@ -1,11 +1,12 @@
 // Paged KV cache: rows appended with their rotation, and read back (paged_append,
 // paged_gather in blend.h).
 //
-// One thread owns the 16 dims i..i+7 and i+d/2..i+d/2+7 of one head of one row: the eight
-// rotation pairs it needs sit in its own registers, and in the 4-bit form these are one
-// 32-bit word of each of two 32-dim groups, whose maxima are shared by the four threads of a
-// group (two shuffles).  The d/16 threads of a head sit side by side and a warp covers
-// neighbouring heads of a row, so the loads are whole 128-byte lines.
+// One thread owns the 16 dims i..i+7 and i+d/2..i+d/2+7 of one head's key and value (or of one query
+// head) of one row: the eight rotation pairs it needs sit in its own registers, its four 16-byte
+// loads are on their way together, and in the 4-bit form its dims are eight of each of two 32-dim
+// groups, whose maxima the four threads of a group share by two shuffles.  The d/16 threads of a
+// head sit side by side and a warp covers neighbouring heads of a row, so loads are whole 128-byte
+// lines; 4-bit rows leave as 8 bytes per thread after one exchange between the two halves of a head.
 // Both kernels are bound by HBM: rows in, rows out, nothing read twice but the rotation
 // table, which stays in L2 (one row of it per position, shared by all heads).
 //
@@ -73,10 +74,53 @@ __device__ __forceinline__ bf16 group_scale(const float* x) {
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
     return __float2bfloat16_rn(isfinite(m) ? __fdiv_rn(m, 7.f) : __int_as_float(0x7fc00000));
 }
-// Code of x, 1..15 (value code - 8), 8 where the scale is zero or NaN.
-__device__ __forceinline__ uint32_t code4(float x, float scale) {
-    if (!(scale > 0.f)) return 8u;
-    return (uint32_t)(8 + (int)fminf(fmaxf(rintf(__fdiv_rn(x, scale)), -7.f), 7.f));
+// Codes n + 8 of eight values with scale `s` (n = round-to-even of the fp32 quotient x / s, -7..7), as
+// two sums of four codes each: `even` for values 0, 2, 4, 6 and `odd` for 1, 3, 5, 7, code k of the four
+// at bit 4 k.  All codes are 8 where the scale is zero or NaN.
+//
+// The quotient has to be the correctly rounded one, since a code is a rounding of it.  With y = 1 / s
+// correctly rounded, q = x y, r = x - q s (exact) and q + r y is x / s correctly rounded (Markstein's
+// theorem, P. Markstein, IBM J. Res. Dev. 34, 1990) as long as nothing leaves the normal range: three
+// operations a value instead of a division.  Scales outside 2^-100..2^100 divide.
+__device__ __forceinline__ void codes8(const float* x, float s, uint32_t& even, uint32_t& odd) {
+    float c[8];
+    if (s >= 0x1p-100f && s <= 0x1p100f) {
+        const float y = __frcp_rn(s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float q = __fmul_rn(x[e], y);
+            // max |x| / s stays below 7.5 for such scales, so the code is in range without a clamp;
+            // adding 1.5 2^23 rounds to an integer, ties to even
+            const float n = __fadd_rn(__fmaf_rn(__fmaf_rn(-q, s, x[e]), y, q), 12582912.f);
+            c[e] = n - (12582912.f - 8.f);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c[e] = s > 0.f ? 8.f + fminf(fmaxf(rintf(__fdiv_rn(x[e], s)), -7.f), 7.f) : 8.f;
+    }
+    // four codes in 16 bits of a float's mantissa
+    even = __float_as_uint(fmaf(c[6], 4096.f, fmaf(c[4], 256.f, fmaf(c[2], 16.f, c[0]))) + 8388608.f);
+    odd = __float_as_uint(fmaf(c[7], 4096.f, fmaf(c[5], 256.f, fmaf(c[3], 16.f, c[1]))) + 8388608.f);
+}
+// K: even codes in the low half of a word, odd ones in the high half.
+__device__ __forceinline__ uint32_t k_word(uint32_t even, uint32_t odd) { return __byte_perm(even, odd, 0x5410); }
+// V: codes 0..3 in the low half, 4..7 in the high half, in order.
+__device__ __forceinline__ uint32_t v_word(uint32_t even, uint32_t odd) {
+    // even: c0 c2 c4 c6, odd: c1 c3 c5 c7 from bit 0 up; spread each to every other nibble
+    uint32_t e = even & 0xffffu, o = odd & 0xffffu;
+    e = (e | (e << 8)) & 0x00FF00FFu;
+    o = (o | (o << 8)) & 0x00FF00FFu;
+    e = (e | (e << 4)) & 0x0F0F0F0Fu;
+    o = (o | (o << 4)) & 0x0F0F0F0Fu;
+    return e | (o << 4);
+}
+// The codes of a K word (see k_word) or V word times the scale.
+template <bool KROW> __device__ __forceinline__ void values8(uint32_t w, float s, float* x) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t code = (w >> (KROW ? k4_bit(e) : 4 * e)) & 15u;
+        x[e] = __fmul_rn(__uint_as_float(0x4B000000u | code) - 8388616.f, s);  // 2^23 + code, exact
+    }
 }
 
 struct RowAt {
@@ -118,7 +162,7 @@ __device__ __forceinline__ int checked_count(const int32_t* n_dev, int max_n, in
     return n;
 }
 
-// Head slots of a row: hkv keys, hkv values, then (with q) hq query heads.
+// Slots of a row: hkv kv heads (key and value), then (with q) hq query heads.
 template <typename T, bool I4, int D>
 __global__ void __launch_bounds__(MEM_THREADS)
     k_paged_append(PageView pg, int hq, const T* __restrict__ k_new, long long ld_k, const T* __restrict__ v_new,
@@ -127,65 +171,91 @@ __global__ void __launch_bounds__(MEM_THREADS)
                    int max_n, const float2* __restrict__ tab, int max_pos, int32_t* err) {
     constexpr int TPH = D / 16, HALF = D / 2;
     const int n = checked_count(n_dev, max_n, err);
-    const int slots = 2 * pg.hkv + (q ? hq : 0);
+    const int slots = pg.hkv + (q ? hq : 0);
     const long long unit = ((long long)blockIdx.x * MEM_THREADS + threadIdx.x) / TPH;
-    const int i0 = (threadIdx.x % TPH) * 8;
+    const int t = threadIdx.x % TPH, i0 = t * 8;
     const long long row64 = unit / slots;
     const int slot = (int)(unit - row64 * slots);
-    RowAt r{false, 0, 0, 0, 0};
     const int row = (int)row64;
-    if (row64 < n) r = row_at(pg, seq, pos, rot, true, row, max_pos, err);
-    const bool is_k = slot < pg.hkv, is_v = !is_k && slot < 2 * pg.hkv;
-    const int head = is_k ? slot : is_v ? slot - pg.hkv : slot - 2 * pg.hkv;
-    float a[8] = {}, b[8] = {};
-    if (r.ok) {
-        const T* src = (is_k ? k_new + row * ld_k : is_v ? v_new + row * ld_v : q + row * ld_q) + head * D;
+    const bool live = row64 < n, is_kv = slot < pg.hkv;
+    const int head = is_kv ? slot : slot - pg.hkv;
+    float a[8] = {}, b[8] = {}, va[8] = {}, vb[8] = {};
+    if (live) {
+        const T* src = is_kv ? k_new + row * ld_k + head * D : q + row * ld_q + head * D;
         load8(src + i0, a);
         load8(src + i0 + HALF, b);
-        if (!is_v) rotate8(a, b, r.rot, i0, HALF, tab);
-    }
-    if (!is_k && !is_v) {
-        if (r.ok) {
-            T* dst = q_out + ((long long)row * hq + head) * D;
-            store8(dst + i0, a);
-            store8(dst + i0 + HALF, b);
+        if (is_kv) {
+            const T* sv = v_new + row * ld_v + head * D;
+            load8(sv + i0, va);
+            load8(sv + i0 + HALF, vb);
         }
-        if (!I4) return;
     }
-    const long long at = r.at + ((long long)head << pg.shift);
-    char* base = const_cast<char*>(is_k ? pg.k : pg.v);
-    if constexpr (!I4) {
-        if (!r.ok) return;
-        T* dst = reinterpret_cast<T*>(base) + at * D;
+    RowAt r{false, 0, 0, 0, 0};
+    if (live) r = row_at(pg, seq, pos, rot, true, row, max_pos, err);
+    if (r.ok) rotate8(a, b, r.rot, i0, HALF, tab);
+    if (!is_kv && r.ok) {
+        T* dst = q_out + ((long long)row * hq + head) * D;
         store8(dst + i0, a);
         store8(dst + i0 + HALF, b);
+    }
+    const bool store = r.ok && is_kv;
+    const long long at = r.at + ((long long)head << pg.shift);
+    if constexpr (!I4) {
+        if (!store) return;
+        T* dk = reinterpret_cast<T*>(const_cast<char*>(pg.k)) + at * D;
+        T* dv = reinterpret_cast<T*>(const_cast<char*>(pg.v)) + at * D;
+        store8(dk + i0, a);
+        store8(dk + i0 + HALF, b);
+        store8(dv + i0, va);
+        store8(dv + i0 + HALF, vb);
     } else {
-        // all lanes take part in the shuffles; the words are stored by those with a row
-        const bf16 sa = group_scale(a), sb = group_scale(b);
-        if (!r.ok || (!is_k && !is_v)) return;
-        const float fa = __bfloat162float(sa), fb = __bfloat162float(sb);
-        const int g = i0 / 32, g2 = (i0 + HALF) / 32, c = (i0 % 32) / 8;
-        char* dst = base + at * (D / 2);
-        uint32_t wa = 0, wb = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int bit = is_k ? k4_bit(e) : 4 * e;
-            wa |= code4(a[e], fa) << bit;
-            wb |= code4(b[e], fb) << bit;
-        }
-        if (is_k) {
-            *reinterpret_cast<uint32_t*>(dst + k4_word(D, g, c)) = wa;
-            *reinterpret_cast<uint32_t*>(dst + k4_word(D, g2, c)) = wb;
+        // all lanes take part in the shuffles
+        const bf16 ka = group_scale(a), kb = group_scale(b), sa = group_scale(va), sb = group_scale(vb);
+        uint32_t e0, o0, e1, o1;
+        codes8(a, __bfloat162float(ka), e0, o0);
+        codes8(b, __bfloat162float(kb), e1, o1);
+        uint32_t k0 = k_word(e0, o0), k1 = k_word(e1, o1);  // words (c, g) and (c, g + D / 64)
+        codes8(va, __bfloat162float(sa), e0, o0);
+        codes8(vb, __bfloat162float(sb), e1, o1);
+        const uint32_t w0 = v_word(e0, o0), w1 = v_word(e1, o1);  // halves (g, 2c), (g, 2c + 1) and those of g + D / 64
+        uint32_t v0 = __byte_perm(w0, w1, 0x5410), v1 = __byte_perm(w0, w1, 0x7632);  // by half: 2c, 2c + 1
+        uint32_t ks = (uint32_t)__bfloat16_as_ushort(ka) | (uint32_t)__bfloat16_as_ushort(kb) << 16;
+        uint32_t vs = (uint32_t)__bfloat16_as_ushort(sa) | (uint32_t)__bfloat16_as_ushort(sb) << 16;
+        uint2 kw, vw, sk, sv;
+        if constexpr (D == 128) {
+            // thread t holds groups g = t / 4 and g + 2; t ^ 4 has the other two of the same dims.  The lower
+            // thread takes words 0, 1 of chunk c and half 2c, the upper one words 2, 3 and half 2c + 1.
+            const bool up = t >= 4;
+            const uint32_t ko = __shfl_xor_sync(0xffffffffu, up ? k0 : k1, 4);
+            kw = up ? make_uint2(ko, k1) : make_uint2(k0, ko);
+            const uint32_t vo = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 4);  // groups (g, g + 2) of the partner
+            const uint32_t mine = up ? v1 : v0, g02 = up ? vo : mine, g13 = up ? mine : vo;
+            vw = make_uint2(__byte_perm(g02, g13, 0x5410), __byte_perm(g02, g13, 0x7632));
+            const uint32_t k_up = __shfl_xor_sync(0xffffffffu, ks, 4), v_up = __shfl_xor_sync(0xffffffffu, vs, 4);
+            sk = make_uint2(__byte_perm(ks, k_up, 0x5410), __byte_perm(ks, k_up, 0x7632));
+            sv = make_uint2(__byte_perm(vs, v_up, 0x5410), __byte_perm(vs, v_up, 0x7632));
         } else {
-            *reinterpret_cast<uint16_t*>(dst + v4_half(D, g, 2 * c)) = (uint16_t)wa;
-            *reinterpret_cast<uint16_t*>(dst + v4_half(D, g, 2 * c + 1)) = (uint16_t)(wa >> 16);
-            *reinterpret_cast<uint16_t*>(dst + v4_half(D, g2, 2 * c)) = (uint16_t)wb;
-            *reinterpret_cast<uint16_t*>(dst + v4_half(D, g2, 2 * c + 1)) = (uint16_t)(wb >> 16);
+            kw = make_uint2(k0, k1);
+            vw = make_uint2(v0, v1);
+            sk = make_uint2(ks, 0);
+            sv = make_uint2(vs, 0);
         }
-        if (c == 0) {
-            bf16* sc = reinterpret_cast<bf16*>(const_cast<char*>(is_k ? pg.ks : pg.vs)) + at * (D / 32);
-            sc[g] = sa;
-            sc[g2] = sb;
+        if (!store) return;
+        const int c = t & 3;
+        char* dk = const_cast<char*>(pg.k) + at * (D / 2);
+        char* dv = const_cast<char*>(pg.v) + at * (D / 2);
+        *reinterpret_cast<uint2*>(dk + (D == 128 ? c * 16 + (t >> 2) * 8 : c * 8)) = kw;
+        *reinterpret_cast<uint2*>(dv + (D == 128 ? (2 * c + (t >> 2)) * 8 : c * 8)) = vw;
+        if (t == 0) {
+            char* ds = const_cast<char*>(pg.ks) + at * (D / 16);
+            char* dt = const_cast<char*>(pg.vs) + at * (D / 16);
+            if constexpr (D == 128) {
+                *reinterpret_cast<uint2*>(ds) = sk;
+                *reinterpret_cast<uint2*>(dt) = sv;
+            } else {
+                *reinterpret_cast<uint32_t*>(ds) = sk.x;
+                *reinterpret_cast<uint32_t*>(dt) = sv.x;
+            }
         }
     }
 }
@@ -198,56 +268,86 @@ __global__ void __launch_bounds__(MEM_THREADS)
                    int32_t* err) {
     constexpr int TPH = D / 16, HALF = D / 2;
     const int n = checked_count(n_dev, max_n, err);
-    const int slots = 2 * pg.hkv;
     const long long unit = ((long long)blockIdx.x * MEM_THREADS + threadIdx.x) / TPH;
-    const int i0 = (threadIdx.x % TPH) * 8;
-    const long long row64 = unit / slots;
-    if (row64 >= n) return;
-    const int row = (int)row64, slot = (int)(unit - row64 * slots);
-    const RowAt r = row_at(pg, seq, pos, rot, false, row, max_pos, err);
-    if (!r.ok) return;
-    const bool is_k = slot < pg.hkv;
-    const int head = is_k ? slot : slot - pg.hkv;
+    const int t = threadIdx.x % TPH, i0 = t * 8;
+    const long long row64 = unit / pg.hkv;
+    const int row = (int)row64, head = (int)(unit - row64 * pg.hkv);
+    RowAt r{false, 0, 0, 0, 0};
+    if (row64 < n) r = row_at(pg, seq, pos, rot, false, row, max_pos, err);
+    if (!I4 && !r.ok) return;
     const long long at = r.at + ((long long)head << pg.shift);
-    const char* base = is_k ? pg.k : pg.v;
-    float a[8], b[8];
+    float a[8], b[8], va[8], vb[8];
     if constexpr (!I4) {
-        const T* src = reinterpret_cast<const T*>(base) + at * D;
-        load8(src + i0, a);
-        load8(src + i0 + HALF, b);
+        const T* sk = reinterpret_cast<const T*>(pg.k) + at * D;
+        const T* sv = reinterpret_cast<const T*>(pg.v) + at * D;
+        load8(sk + i0, a);
+        load8(sk + i0 + HALF, b);
+        load8(sv + i0, va);
+        load8(sv + i0 + HALF, vb);
     } else {
-        const int g = i0 / 32, g2 = (i0 + HALF) / 32, c = (i0 % 32) / 8;
-        const char* src = base + at * (D / 2);
-        uint32_t wa, wb;
-        if (is_k) {
-            wa = *reinterpret_cast<const uint32_t*>(src + k4_word(D, g, c));
-            wb = *reinterpret_cast<const uint32_t*>(src + k4_word(D, g2, c));
+        // the layout and the exchange of k_paged_append, backwards
+        uint2 kw = make_uint2(0, 0), vw = kw, sk = kw, sv = kw;
+        const int c = t & 3;
+        if (r.ok) {
+            const char* pk = pg.k + at * (D / 2);
+            const char* pv = pg.v + at * (D / 2);
+            const char* ps = pg.ks + at * (D / 16);
+            const char* pt = pg.vs + at * (D / 16);
+            kw = *reinterpret_cast<const uint2*>(pk + (D == 128 ? c * 16 + (t >> 2) * 8 : c * 8));
+            vw = *reinterpret_cast<const uint2*>(pv + (D == 128 ? (2 * c + (t >> 2)) * 8 : c * 8));
+            if constexpr (D == 128) {
+                sk = *reinterpret_cast<const uint2*>(ps);
+                sv = *reinterpret_cast<const uint2*>(pt);
+            } else {
+                sk.x = *reinterpret_cast<const uint32_t*>(ps);
+                sv.x = *reinterpret_cast<const uint32_t*>(pt);
+            }
+        }
+        uint32_t k0, k1, w0, w1;
+        float ka, kb, sa, sb;
+        if constexpr (D == 128) {
+            const bool up = t >= 4;
+            const uint32_t ko = __shfl_xor_sync(0xffffffffu, up ? kw.x : kw.y, 4);
+            k0 = up ? ko : kw.x;
+            k1 = up ? kw.y : ko;
+            const uint32_t g02 = __byte_perm(vw.x, vw.y, 0x5410), g13 = __byte_perm(vw.x, vw.y, 0x7632);
+            const uint32_t vo = __shfl_xor_sync(0xffffffffu, up ? g02 : g13, 4);
+            const uint32_t v0 = up ? vo : g02, v1 = up ? g13 : vo;  // this thread's groups by half: 2c, 2c + 1
+            w0 = __byte_perm(v0, v1, 0x5410);
+            w1 = __byte_perm(v0, v1, 0x7632);
+            ka = __uint_as_float(up ? sk.x & 0xffff0000u : sk.x << 16);
+            kb = __uint_as_float(up ? sk.y & 0xffff0000u : sk.y << 16);
+            sa = __uint_as_float(up ? sv.x & 0xffff0000u : sv.x << 16);
+            sb = __uint_as_float(up ? sv.y & 0xffff0000u : sv.y << 16);
         } else {
-            wa = *reinterpret_cast<const uint16_t*>(src + v4_half(D, g, 2 * c)) |
-                 (uint32_t)*reinterpret_cast<const uint16_t*>(src + v4_half(D, g, 2 * c + 1)) << 16;
-            wb = *reinterpret_cast<const uint16_t*>(src + v4_half(D, g2, 2 * c)) |
-                 (uint32_t)*reinterpret_cast<const uint16_t*>(src + v4_half(D, g2, 2 * c + 1)) << 16;
+            k0 = kw.x;
+            k1 = kw.y;
+            w0 = __byte_perm(vw.x, vw.y, 0x5410);
+            w1 = __byte_perm(vw.x, vw.y, 0x7632);
+            ka = __uint_as_float(sk.x << 16);
+            kb = __uint_as_float(sk.x & 0xffff0000u);
+            sa = __uint_as_float(sv.x << 16);
+            sb = __uint_as_float(sv.x & 0xffff0000u);
         }
-        const bf16* sc = reinterpret_cast<const bf16*>(is_k ? pg.ks : pg.vs) + at * (D / 32);
-        const float fa = __bfloat162float(sc[g]), fb = __bfloat162float(sc[g2]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int bit = is_k ? k4_bit(e) : 4 * e;
-            a[e] = __fmul_rn((float)((int)((wa >> bit) & 15u) - 8), fa);
-            b[e] = __fmul_rn((float)((int)((wb >> bit) & 15u) - 8), fb);
-        }
+        if (!r.ok) return;
+        values8<true>(k0, ka, a);
+        values8<true>(k1, kb, b);
+        values8<false>(w0, sa, va);
+        values8<false>(w1, sb, vb);
     }
-    if (is_k) rotate8(a, b, r.rot, i0, HALF, tab);
-    T* dst = (is_k ? k_out : v_out) + ((long long)row * pg.hkv + head) * D;
-    store8(dst + i0, a);
-    store8(dst + i0 + HALF, b);
+    rotate8(a, b, r.rot, i0, HALF, tab);
+    const long long out = ((long long)row * pg.hkv + head) * D;
+    store8(k_out + out + i0, a);
+    store8(k_out + out + i0 + HALF, b);
+    store8(v_out + out + i0, va);
+    store8(v_out + out + i0 + HALF, vb);
 }
 
 template <typename T, bool I4, int D>
 void append_d(const PageView& pg, int hq, const void* k_new, long long ld_k, const void* v_new, long long ld_v,
               const void* q, long long ld_q, void* q_out, const int32_t* seq, const int32_t* pos, const int32_t* rot,
               const int32_t* n_dev, int max_n, const float2* tab, int max_pos, int32_t* err, cudaStream_t s) {
-    const long long threads = (long long)max_n * (2 * pg.hkv + (q ? hq : 0)) * (D / 16);
+    const long long threads = (long long)max_n * (pg.hkv + (q ? hq : 0)) * (D / 16);
     const long long blocks = (threads + MEM_THREADS - 1) / MEM_THREADS;
     k_paged_append<T, I4, D><<<(unsigned)blocks, MEM_THREADS, 0, s>>>(
         pg, hq, (const T*)k_new, ld_k, (const T*)v_new, ld_v, (const T*)q, ld_q, (T*)q_out, seq, pos, rot, n_dev, max_n,
@@ -256,7 +356,7 @@ void append_d(const PageView& pg, int hq, const void* k_new, long long ld_k, con
 template <typename T, bool I4, int D>
 void gather_d(const PageView& pg, const int32_t* seq, const int32_t* pos, const int32_t* rot, const int32_t* n_dev,
               int max_n, void* k_out, void* v_out, const float2* tab, int max_pos, int32_t* err, cudaStream_t s) {
-    const long long threads = (long long)max_n * 2 * pg.hkv * (D / 16);
+    const long long threads = (long long)max_n * pg.hkv * (D / 16);
     const long long blocks = (threads + MEM_THREADS - 1) / MEM_THREADS;
     k_paged_gather<T, I4, D><<<(unsigned)blocks, MEM_THREADS, 0, s>>>(pg, seq, pos, rot, n_dev, max_n, (T*)k_out,
                                                                      (T*)v_out, tab, max_pos, err);
