@@ -20,17 +20,7 @@ namespace {
 
 constexpr int MEM_THREADS = 256;
 
-// Eight consecutive dims as fp32.
-__device__ __forceinline__ void load8(const bf16* p, float* x) {
-    const Vec<bf16> v = ld16(p);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = v.get(e);
-}
-__device__ __forceinline__ void load8(const float* p, float* x) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
+// Eight consecutive dims from fp32.
 __device__ __forceinline__ void store8(bf16* p, const float* x) {
     Vec<bf16> v;
 #pragma unroll
@@ -41,6 +31,24 @@ __device__ __forceinline__ void store8(float* p, const float* x) {
     *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
     *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
 }
+
+// Eight consecutive dims as they are.
+template <typename T> struct Raw8 {
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+    __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = w[i];
+    }
+    __device__ __forceinline__ void get(float* x) const {
+        const T* p = reinterpret_cast<const T*>(w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = to_f<T>(p[e]);
+    }
+};
 
 // Pairs (a[e], b[e]) of dims i0 + e, i0 + e + half rotated by `rot` positions; 0 leaves them
 // bit for bit as they are (an infinity stays one).
@@ -62,16 +70,11 @@ __device__ __forceinline__ void rotate8(float* a, float* b, int rot, int i0, int
 // Scale of the 32 dims that four neighbouring threads hold eight each of: bf16 of max / 7;
 // NaN when one of them is not finite.  Call it with all 32 lanes.
 __device__ __forceinline__ bf16 group_scale(const float* x) {
-    float m = 0.f;
-    bool fin = true;
+    float m = fabsf(x[0]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        m = fmaxf(m, fabsf(x[e]));
-        fin = fin && isfinite(x[e]);
-    }
-    m = fin ? m : INFINITY;
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    for (int e = 1; e < 8; ++e) m = max_nan(m, fabsf(x[e]));
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
     return __float2bfloat16_rn(isfinite(m) ? __fdiv_rn(m, 7.f) : __int_as_float(0x7fc00000));
 }
 // Codes n + 8 of eight values with scale `s` (n = round-to-even of the fp32 quotient x / s, -7..7), as
@@ -83,24 +86,24 @@ __device__ __forceinline__ bf16 group_scale(const float* x) {
 // theorem, P. Markstein, IBM J. Res. Dev. 34, 1990) as long as nothing leaves the normal range: three
 // operations a value instead of a division.  Scales outside 2^-100..2^100 divide.
 __device__ __forceinline__ void codes8(const float* x, float s, uint32_t& even, uint32_t& odd) {
-    float c[8];
+    uint32_t c[8];  // the code, under a power of two from bit 22 up
     if (s >= 0x1p-100f && s <= 0x1p100f) {
         const float y = __frcp_rn(s);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float q = __fmul_rn(x[e], y);
-            // max |x| / s stays below 7.5 for such scales, so the code is in range without a clamp;
-            // adding 1.5 2^23 rounds to an integer, ties to even
-            const float n = __fadd_rn(__fmaf_rn(__fmaf_rn(-q, s, x[e]), y, q), 12582912.f);
-            c[e] = n - (12582912.f - 8.f);
+            // max |x| / s stays below 7.5 for such scales, so the code is in range without a clamp; adding
+            // 1.5 2^23 rounds to an integer, ties to even (and the 8 keeps its parity)
+            c[e] = __float_as_uint(__fadd_rn(__fmaf_rn(__fmaf_rn(-q, s, x[e]), y, q), 12582920.f));
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = s > 0.f ? 8.f + fminf(fmaxf(rintf(__fdiv_rn(x[e], s)), -7.f), 7.f) : 8.f;
+        for (int e = 0; e < 8; ++e)
+            c[e] = s > 0.f ? (uint32_t)(8 + (int)fminf(fmaxf(rintf(__fdiv_rn(x[e], s)), -7.f), 7.f)) : 8u;
     }
-    // four codes in 16 bits of a float's mantissa
-    even = __float_as_uint(fmaf(c[6], 4096.f, fmaf(c[4], 256.f, fmaf(c[2], 16.f, c[0]))) + 8388608.f);
-    odd = __float_as_uint(fmaf(c[7], 4096.f, fmaf(c[5], 256.f, fmaf(c[3], 16.f, c[1]))) + 8388608.f);
+    // the low 16 bits are the four codes
+    even = c[0] + c[2] * 16u + c[4] * 256u + c[6] * 4096u;
+    odd = c[1] + c[3] * 16u + c[5] * 256u + c[7] * 4096u;
 }
 // K: even codes in the low half of a word, odd ones in the high half.
 __device__ __forceinline__ uint32_t k_word(uint32_t even, uint32_t odd) { return __byte_perm(even, odd, 0x5410); }
@@ -164,37 +167,39 @@ __device__ __forceinline__ int checked_count(const int32_t* n_dev, int max_n, in
 
 // Slots of a row: hkv kv heads (key and value), then (with q) hq query heads.
 template <typename T, bool I4, int D>
-__global__ void __launch_bounds__(MEM_THREADS)
+__global__ void __launch_bounds__(MEM_THREADS, I4 || sizeof(T) == 4 ? 4 : 5)
     k_paged_append(PageView pg, int hq, const T* __restrict__ k_new, long long ld_k, const T* __restrict__ v_new,
                    long long ld_v, const T* q, long long ld_q, T* q_out, const int32_t* __restrict__ seq,
                    const int32_t* __restrict__ pos, const int32_t* __restrict__ rot, const int32_t* __restrict__ n_dev,
-                   int max_n, const float2* __restrict__ tab, int max_pos, int32_t* err) {
+                   int max_n, long long row0, const float2* __restrict__ tab, int max_pos, int32_t* err) {
     constexpr int TPH = D / 16, HALF = D / 2;
     const int n = checked_count(n_dev, max_n, err);
     const int slots = pg.hkv + (q ? hq : 0);
-    const long long unit = ((long long)blockIdx.x * MEM_THREADS + threadIdx.x) / TPH;
+    const unsigned unit = (blockIdx.x * MEM_THREADS + threadIdx.x) / TPH;  // below 2^32 / TPH (launcher)
     const int t = threadIdx.x % TPH, i0 = t * 8;
-    const long long row64 = unit / slots;
-    const int slot = (int)(unit - row64 * slots);
-    const int row = (int)row64;
-    const bool live = row64 < n, is_kv = slot < pg.hkv;
+    const long long row = row0 + unit / (unsigned)slots;
+    const int slot = (int)(unit % (unsigned)slots);
+    const bool live = row < n, is_kv = slot < pg.hkv;
     const int head = is_kv ? slot : slot - pg.hkv;
-    float a[8] = {}, b[8] = {}, va[8] = {}, vb[8] = {};
+    Raw8<T> ra{}, rb{}, rva{}, rvb{};
     if (live) {
         const T* src = is_kv ? k_new + row * ld_k + head * D : q + row * ld_q + head * D;
-        load8(src + i0, a);
-        load8(src + i0 + HALF, b);
+        ra.load(src + i0);
+        rb.load(src + i0 + HALF);
         if (is_kv) {
             const T* sv = v_new + row * ld_v + head * D;
-            load8(sv + i0, va);
-            load8(sv + i0 + HALF, vb);
+            rva.load(sv + i0);
+            rvb.load(sv + i0 + HALF);
         }
     }
     RowAt r{false, 0, 0, 0, 0};
-    if (live) r = row_at(pg, seq, pos, rot, true, row, max_pos, err);
+    if (live) r = row_at(pg, seq, pos, rot, true, (int)row, max_pos, err);
+    float a[8], b[8];
+    ra.get(a);
+    rb.get(b);
     if (r.ok) rotate8(a, b, r.rot, i0, HALF, tab);
     if (!is_kv && r.ok) {
-        T* dst = q_out + ((long long)row * hq + head) * D;
+        T* dst = q_out + (row * hq + head) * D;
         store8(dst + i0, a);
         store8(dst + i0 + HALF, b);
     }
@@ -206,9 +211,12 @@ __global__ void __launch_bounds__(MEM_THREADS)
         T* dv = reinterpret_cast<T*>(const_cast<char*>(pg.v)) + at * D;
         store8(dk + i0, a);
         store8(dk + i0 + HALF, b);
-        store8(dv + i0, va);
-        store8(dv + i0 + HALF, vb);
+        rva.store(dv + i0);
+        rvb.store(dv + i0 + HALF);
     } else {
+        float va[8], vb[8];
+        rva.get(va);
+        rvb.get(vb);
         // all lanes take part in the shuffles
         const bf16 ka = group_scale(a), kb = group_scale(b), sa = group_scale(va), sb = group_scale(vb);
         uint32_t e0, o0, e1, o1;
@@ -261,29 +269,35 @@ __global__ void __launch_bounds__(MEM_THREADS)
 }
 
 template <typename T, bool I4, int D>
-__global__ void __launch_bounds__(MEM_THREADS)
+__global__ void __launch_bounds__(MEM_THREADS, sizeof(T) == 4 ? 4 : 5)
     k_paged_gather(PageView pg, const int32_t* __restrict__ seq, const int32_t* __restrict__ pos,
                    const int32_t* __restrict__ rot, const int32_t* __restrict__ n_dev, int max_n,
-                   T* __restrict__ k_out, T* __restrict__ v_out, const float2* __restrict__ tab, int max_pos,
-                   int32_t* err) {
+                   long long row0, T* __restrict__ k_out, T* __restrict__ v_out, const float2* __restrict__ tab,
+                   int max_pos, int32_t* err) {
     constexpr int TPH = D / 16, HALF = D / 2;
     const int n = checked_count(n_dev, max_n, err);
-    const long long unit = ((long long)blockIdx.x * MEM_THREADS + threadIdx.x) / TPH;
+    const unsigned unit = (blockIdx.x * MEM_THREADS + threadIdx.x) / TPH;
     const int t = threadIdx.x % TPH, i0 = t * 8;
-    const long long row64 = unit / pg.hkv;
-    const int row = (int)row64, head = (int)(unit - row64 * pg.hkv);
+    const long long row = row0 + unit / (unsigned)pg.hkv;
+    const int head = (int)(unit % (unsigned)pg.hkv);
     RowAt r{false, 0, 0, 0, 0};
-    if (row64 < n) r = row_at(pg, seq, pos, rot, false, row, max_pos, err);
+    if (row < n) r = row_at(pg, seq, pos, rot, false, (int)row, max_pos, err);
     if (!I4 && !r.ok) return;
     const long long at = r.at + ((long long)head << pg.shift);
-    float a[8], b[8], va[8], vb[8];
+    const long long out = (row * pg.hkv + head) * D;
+    float a[8], b[8];
     if constexpr (!I4) {
         const T* sk = reinterpret_cast<const T*>(pg.k) + at * D;
         const T* sv = reinterpret_cast<const T*>(pg.v) + at * D;
-        load8(sk + i0, a);
-        load8(sk + i0 + HALF, b);
-        load8(sv + i0, va);
-        load8(sv + i0 + HALF, vb);
+        Raw8<T> ra, rb, rva, rvb;
+        ra.load(sk + i0);
+        rb.load(sk + i0 + HALF);
+        rva.load(sv + i0);
+        rvb.load(sv + i0 + HALF);
+        ra.get(a);
+        rb.get(b);
+        rva.store(v_out + out + i0);
+        rvb.store(v_out + out + i0 + HALF);
     } else {
         // the layout and the exchange of k_paged_append, backwards
         uint2 kw = make_uint2(0, 0), vw = kw, sk = kw, sv = kw;
@@ -330,36 +344,42 @@ __global__ void __launch_bounds__(MEM_THREADS)
             sb = __uint_as_float(sv.x & 0xffff0000u);
         }
         if (!r.ok) return;
+        values8<false>(w0, sa, a);
+        values8<false>(w1, sb, b);
+        store8(v_out + out + i0, a);
+        store8(v_out + out + i0 + HALF, b);
         values8<true>(k0, ka, a);
         values8<true>(k1, kb, b);
-        values8<false>(w0, sa, va);
-        values8<false>(w1, sb, vb);
     }
     rotate8(a, b, r.rot, i0, HALF, tab);
-    const long long out = ((long long)row * pg.hkv + head) * D;
     store8(k_out + out + i0, a);
     store8(k_out + out + i0 + HALF, b);
-    store8(v_out + out + i0, va);
-    store8(v_out + out + i0 + HALF, vb);
 }
 
 template <typename T, bool I4, int D>
 void append_d(const PageView& pg, int hq, const void* k_new, long long ld_k, const void* v_new, long long ld_v,
               const void* q, long long ld_q, void* q_out, const int32_t* seq, const int32_t* pos, const int32_t* rot,
               const int32_t* n_dev, int max_n, const float2* tab, int max_pos, int32_t* err, cudaStream_t s) {
-    const long long threads = (long long)max_n * (pg.hkv + (q ? hq : 0)) * (D / 16);
-    const long long blocks = (threads + MEM_THREADS - 1) / MEM_THREADS;
-    k_paged_append<T, I4, D><<<(unsigned)blocks, MEM_THREADS, 0, s>>>(
-        pg, hq, (const T*)k_new, ld_k, (const T*)v_new, ld_v, (const T*)q, ld_q, (T*)q_out, seq, pos, rot, n_dev, max_n,
-        tab, max_pos, err);
+    const int slots = pg.hkv + (q ? hq : 0);
+    const long long most = (1ll << 31) / (slots * (D / 16));  // rows of a launch: its threads count in 32 bits
+    for (long long row0 = 0; row0 < max_n; row0 += most) {
+        const long long threads = (max_n - row0 < most ? max_n - row0 : most) * slots * (D / 16);
+        k_paged_append<T, I4, D><<<(unsigned)((threads + MEM_THREADS - 1) / MEM_THREADS), MEM_THREADS, 0, s>>>(
+            pg, hq, (const T*)k_new, ld_k, (const T*)v_new, ld_v, (const T*)q, ld_q, (T*)q_out, seq, pos, rot, n_dev,
+            max_n, row0, tab, max_pos, err);
+        note_launch(1);
+    }
 }
 template <typename T, bool I4, int D>
 void gather_d(const PageView& pg, const int32_t* seq, const int32_t* pos, const int32_t* rot, const int32_t* n_dev,
               int max_n, void* k_out, void* v_out, const float2* tab, int max_pos, int32_t* err, cudaStream_t s) {
-    const long long threads = (long long)max_n * pg.hkv * (D / 16);
-    const long long blocks = (threads + MEM_THREADS - 1) / MEM_THREADS;
-    k_paged_gather<T, I4, D><<<(unsigned)blocks, MEM_THREADS, 0, s>>>(pg, seq, pos, rot, n_dev, max_n, (T*)k_out,
-                                                                     (T*)v_out, tab, max_pos, err);
+    const long long most = (1ll << 31) / (pg.hkv * (D / 16));
+    for (long long row0 = 0; row0 < max_n; row0 += most) {
+        const long long threads = (max_n - row0 < most ? max_n - row0 : most) * pg.hkv * (D / 16);
+        k_paged_gather<T, I4, D><<<(unsigned)((threads + MEM_THREADS - 1) / MEM_THREADS), MEM_THREADS, 0, s>>>(
+            pg, seq, pos, rot, n_dev, max_n, row0, (T*)k_out, (T*)v_out, tab, max_pos, err);
+        note_launch(1);
+    }
 }
 
 }  // namespace
@@ -375,7 +395,6 @@ void launch_paged_append(int dtype, bool i4, const PageView& pg, int hq, int d, 
                  : (i4 ? (d == 64 ? append_d<float, true, 64> : append_d<float, true, 128>)
                        : (d == 64 ? append_d<float, false, 64> : append_d<float, false, 128>));
     f(pg, hq, k_new, ld_k, v_new, ld_v, q, ld_q, q_out, seq, pos, rot, n_dev, max_n, tab, max_pos, err, s);
-    note_launch(1);
 }
 
 void launch_paged_gather(int dtype, bool i4, const PageView& pg, int d, const int32_t* seq, const int32_t* pos,
@@ -388,7 +407,6 @@ void launch_paged_gather(int dtype, bool i4, const PageView& pg, int d, const in
                  : (i4 ? (d == 64 ? gather_d<float, true, 64> : gather_d<float, true, 128>)
                        : (d == 64 ? gather_d<float, false, 64> : gather_d<float, false, 128>));
     f(pg, seq, pos, rot, n_dev, max_n, k_out, v_out, tab, max_pos, err, s);
-    note_launch(1);
 }
 
 }  // namespace blend
