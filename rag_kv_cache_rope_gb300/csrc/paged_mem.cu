@@ -67,15 +67,34 @@ __device__ __forceinline__ void rotate8(float* a, float* b, int rot, int i0, int
     }
 }
 
-// Scale of the 32 dims that four neighbouring threads hold eight each of: bf16 of max / 7;
-// NaN when one of them is not finite.  Call it with all 32 lanes.
-__device__ __forceinline__ bf16 group_scale(const float* x) {
+// Scales of the four 32-dim groups that four neighbouring threads hold eight dims each of: bf16 of
+// max / 7, NaN when a group is not finite, and their reciprocals.  Thread j of the four computes
+// group j's (a division and a reciprocal each) and the others read them.  Call it with all 32 lanes.
+struct Scale {
+    uint32_t bits;  // the bf16
+    float s, y;     // its value, and 1 / s
+};
+__device__ __forceinline__ float group_max(const float* x) {
     float m = fabsf(x[0]);
 #pragma unroll
     for (int e = 1; e < 8; ++e) m = max_nan(m, fabsf(x[e]));
     m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    return __float2bfloat16_rn(isfinite(m) ? __fdiv_rn(m, 7.f) : __int_as_float(0x7fc00000));
+    return max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
+__device__ __forceinline__ void group_scales(const float* x0, const float* x1, const float* x2, const float* x3, Scale (&out)[4]) {
+    const float m0 = group_max(x0), m1 = group_max(x1), m2 = group_max(x2), m3 = group_max(x3);
+    const int j = threadIdx.x & 3;
+    const float m = j == 0 ? m0 : j == 1 ? m1 : j == 2 ? m2 : m3;
+    const bf16 s = __float2bfloat16_rn(isfinite(m) ? __fdiv_rn(m, 7.f) : __int_as_float(0x7fc00000));
+    const uint32_t bits = __bfloat16_as_ushort(s);
+    const float y = __frcp_rn(__bfloat162float(s));
+    const int first = (threadIdx.x & 31) & ~3;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        out[k].bits = __shfl_sync(0xffffffffu, bits, first + k);
+        out[k].s = __uint_as_float(out[k].bits << 16);
+        out[k].y = __shfl_sync(0xffffffffu, y, first + k);
+    }
 }
 // Codes n + 8 of eight values with scale `s` (n = round-to-even of the fp32 quotient x / s, -7..7), as
 // two sums of four codes each: `even` for values 0, 2, 4, 6 and `odd` for 1, 3, 5, 7, code k of the four
@@ -85,10 +104,10 @@ __device__ __forceinline__ bf16 group_scale(const float* x) {
 // correctly rounded, q = x y, r = x - q s (exact) and q + r y is x / s correctly rounded (Markstein's
 // theorem, P. Markstein, IBM J. Res. Dev. 34, 1990) as long as nothing leaves the normal range: three
 // operations a value instead of a division.  Scales outside 2^-100..2^100 divide.
-__device__ __forceinline__ void codes8(const float* x, float s, uint32_t& even, uint32_t& odd) {
+__device__ __forceinline__ void codes8(const float* x, const Scale& sc, uint32_t& even, uint32_t& odd) {
+    const float s = sc.s, y = sc.y;
     uint32_t c[8];  // the code, under a power of two from bit 22 up
     if (s >= 0x1p-100f && s <= 0x1p100f) {
-        const float y = __frcp_rn(s);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float q = __fmul_rn(x[e], y);
@@ -218,17 +237,17 @@ __global__ void __launch_bounds__(MEM_THREADS, I4 || sizeof(T) == 4 ? 4 : 5)
         rva.get(va);
         rvb.get(vb);
         // all lanes take part in the shuffles
-        const bf16 ka = group_scale(a), kb = group_scale(b), sa = group_scale(va), sb = group_scale(vb);
+        Scale sc[4];
+        group_scales(a, b, va, vb, sc);
         uint32_t e0, o0, e1, o1;
-        codes8(a, __bfloat162float(ka), e0, o0);
-        codes8(b, __bfloat162float(kb), e1, o1);
+        codes8(a, sc[0], e0, o0);
+        codes8(b, sc[1], e1, o1);
         uint32_t k0 = k_word(e0, o0), k1 = k_word(e1, o1);  // words (c, g) and (c, g + D / 64)
-        codes8(va, __bfloat162float(sa), e0, o0);
-        codes8(vb, __bfloat162float(sb), e1, o1);
+        codes8(va, sc[2], e0, o0);
+        codes8(vb, sc[3], e1, o1);
         const uint32_t w0 = v_word(e0, o0), w1 = v_word(e1, o1);  // halves (g, 2c), (g, 2c + 1) and those of g + D / 64
         uint32_t v0 = __byte_perm(w0, w1, 0x5410), v1 = __byte_perm(w0, w1, 0x7632);  // by half: 2c, 2c + 1
-        uint32_t ks = (uint32_t)__bfloat16_as_ushort(ka) | (uint32_t)__bfloat16_as_ushort(kb) << 16;
-        uint32_t vs = (uint32_t)__bfloat16_as_ushort(sa) | (uint32_t)__bfloat16_as_ushort(sb) << 16;
+        const uint32_t ks = sc[0].bits | sc[1].bits << 16, vs = sc[2].bits | sc[3].bits << 16;
         uint2 kw, vw, sk, sv;
         if constexpr (D == 128) {
             // thread t holds groups g = t / 4 and g + 2; t ^ 4 has the other two of the same dims.  The lower
