@@ -14,8 +14,8 @@
 // order.  Blocks outside every row's window are not visited.
 //
 // Pages: model pages come by TMA, one box per page and column half (a page of 16 tokens is eight
-// boxes a block), 4-bit pages through four more warps per CTA that turn codes into bf16 n s in
-// the swizzled layout the products read, one block ahead in registers.  V rows of tokens that no
+// boxes a block), 4-bit pages as they are by bulk copies, and four more warps per CTA turn the codes
+// into bf16 n s in the swizzled layout the products read.  V rows of tokens that no
 // row of the item sees are zeroed (they may hold anything, and 0 x NaN is NaN): by those warps,
 // or, in the few blocks at an edge, by the producer warp after the boxes have landed.  Pages without
 // a token that the item sees are not touched at all.
@@ -36,24 +36,25 @@ constexpr int NSBUF = 3;
 constexpr uint32_t O_COL = 384;
 constexpr int TMEM_COLS = 512;
 // Warps: 0 producer, 1 TMEM + P.V issue, 2..5 softmax, 6 S issue; model pages: 7 edge blocks; 4-bit
-// pages: 7..10 codes to operands, 11 every other block's signal to the leader
+// pages: 7..10 codes to operands, and in the second CTA warps 1 and 6 its blocks' signals
 constexpr int S_WARP = 6;
 constexpr int MAX_CLUSTERS = 76;
 constexpr int MIN_QUOTA = 2;  // blocks of a cluster's stretch at least
 
 template <bool I4, int D> struct TileCfg {
     static constexpr int NH = D / 64;
-    static constexpr int THREADS = I4 ? 384 : 256;
+    static constexpr int THREADS = I4 ? 352 : 256;
     static constexpr int VCOL = D / 2;                      // V columns of a CTA
     static constexpr int QT = NH * Q_HALF;
     static constexpr int KB = NH * K_HALF;
     static constexpr int VB = TKEYS * VCOL * 2;
     static constexpr int STAGE = KB + VB;
     static constexpr int STAGES = D == 64 ? 8 : I4 ? 3 : 5;
-    // 4-bit pages: raw rows on their way, a slot per thread (half a K row, a V row, their scales)
+    // 4-bit pages: raw rows on their way (this CTA's 64 keys, the 128 values, their scales)
     static constexpr int RAW_STAGES = 4;
-    static constexpr int SB = D / 16;
-    static constexpr int RAW = I4 ? 128 * (D / 4 + D / 2 + 2 * SB) : 0;
+    static constexpr int RB = D / 2, SB = D / 16;  // bytes of a row and of its scales
+    static constexpr int RAW_V = 64 * RB, RAW_KS = RAW_V + TKEYS * RB, RAW_VS = RAW_KS + 64 * SB;
+    static constexpr int RAW = I4 ? RAW_VS + TKEYS * SB : 0;
     static constexpr int SMEM = 2 * QT + STAGES * STAGE + RAW_STAGES * RAW + 1024;
     // kind::f16, bf16 inputs, fp32 accumulate, M256 (the pair); S: N128, P.V: N = D with B MN-major
     static constexpr uint32_t IDESC_S = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((256u >> 4) << 24);
@@ -80,6 +81,12 @@ __device__ __forceinline__ void tma_4d_pair(void* dst, const CUtensorMap* m, uin
         "%4, %5, %6}], [%2];" ::"r"(su32(dst)),
         "l"((uint64_t)m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
         : "memory");
+}
+// `bytes` (a multiple of 16, as both addresses) into this CTA's shared memory
+__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(su32(dst)),
+                 "l"(src), "r"(bytes), "r"(su32(bar))
+                 : "memory");
 }
 // Arrival on the leader's barrier that publishes this thread's shared-memory writes to the pair.
 __device__ __forceinline__ void arrive_leader_release(uint64_t* b) {
@@ -111,9 +118,9 @@ __device__ __forceinline__ bool wait_cl_acquire(uint64_t* b, uint32_t par, volat
     }
     return false;
 }
-// A block that the dequantising warps of this CTA have written, signalled to the leader: a release to
-// the cluster takes over 1000 cycles, so one thread per CTA and block does it for four warps (whose
-// arrivals at the CTA's own barrier it has seen), and two warps take turns.
+// A block that the second CTA's dequantising warps have written, signalled to the leader: a release to
+// the cluster takes over 1000 cycles, so one thread per block does it for four warps (whose arrivals
+// at the CTA's own barrier it has seen), and two warps that have nothing else to do take turns.
 __device__ __forceinline__ bool pass_on(uint64_t* own, uint64_t* leader, uint32_t par, volatile int* abort_flag) {
     if (!warp_poll(own, par, abort_flag)) return false;
     if ((threadIdx.x & 31) == 0) arrive_leader_release(leader);
@@ -221,10 +228,12 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
     constexpr int WARPS = T::THREADS / 32;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t q_full[2], q_empty[2], kv_full[STAGES], kv_empty[STAGES], s_full[NSBUF],
-        p_full[NSBUF], o_full, o_free, edge_full[STAGES], own_full[STAGES];
+        p_full[NSBUF], o_full, o_free, edge_full[STAGES], own_full[STAGES],
+        raw_full[T::RAW_STAGES], raw_empty[T::RAW_STAGES];
     __shared__ uint32_t tmem_sh;
     __shared__ volatile int abort_flag;
-    __shared__ int pend_kv[STAGES], pend_q[2], pend_edge[STAGES];
+    __shared__ int pend_kv[STAGES], pend_q[2], pend_edge[STAGES], pend_raw[T::RAW_STAGES];
+    __shared__ int3 raw_at[T::RAW_STAGES];  // first key of a raw block, positions of its item's first and last row
     // in the workspace (shared memory is full of stages); read again only where a role changes sequence
     int* pre = a.pre + (size_t)blockIdx.x * (BLEND_MAX_SEQS + 1);
 
@@ -282,12 +291,17 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
             mbar_init(&p_full[b], 8);  // 4 softmax warps in each CTA
         }
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&kv_full[s], 2);  // once from each CTA
+            mbar_init(&kv_full[s], I4 ? 5 : 2);  // once from each CTA; 4-bit: the leader's four warps and the other CTA
             mbar_init(&edge_full[s], 1);
             pend_edge[s] = -1;
             mbar_init(&own_full[s], 4);  // 4-bit pages: this CTA's dequantising warps
             mbar_init(&kv_empty[s], 1);
             pend_kv[s] = -1;
+        }
+        for (int s = 0; s < T::RAW_STAGES; ++s) {
+            mbar_init(&raw_full[s], 1);
+            mbar_init(&raw_empty[s], 4);
+            pend_raw[s] = -1;
         }
         mbar_init(&o_full, 1);
         mbar_init(&o_free, 8);
@@ -309,16 +323,23 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------ producer warp (both CTAs): Q, model pages
-        // Lane i owns one box of every block: first the CTA's 64 keys by pages and column halves, then
-        // the 128 keys' V columns by pages.  The page of its next box is read a block ahead.
+        // Lane i owns one copy of every block: boxes of the CTA's 64 keys by pages and column halves, then
+        // of the 128 keys' V columns by pages; or for 4-bit pages the key rows by pages, their scales, the
+        // value rows, their scales.  The page of its next copy is read a block ahead.
         const int k_rows = min(1 << a.pg.shift, 64), v_rows = 1 << a.pg.shift;
-        const int n_k = (64 / k_rows) * NH, n_v = TKEYS / v_rows;
-        const bool is_k = lane < n_k, mine = !I4 && lane < n_k + n_v;
-        const int piece = is_k ? lane / NH : lane - n_k;
+        const int n_k = 64 / k_rows * (I4 ? 2 : NH), n_v = TKEYS / v_rows * (I4 ? 2 : 1);
+        const bool is_k = lane < n_k, mine = lane < n_k + n_v;
+        const int nth = is_k ? lane : lane - n_k;                       // of the keys' or the values' copies
+        const int pieces = is_k ? 64 / k_rows : TKEYS / v_rows;
+        const int piece = !I4 ? (is_k ? nth / NH : nth) : nth % pieces;
+        const bool scale = I4 && nth >= pieces;
         const int rows = is_k ? k_rows : v_rows;
-        const int tok = is_k ? 64 * rank + piece * k_rows : piece * v_rows;  // first token of the box in a block
-        const int col = is_k ? (lane % NH) * 64 : VCOL * rank;
-        const int box_at = is_k ? (lane % NH) * K_HALF + piece * k_rows * 128 : KB + tok * VCOL * 2;
+        const int tok = is_k ? 64 * rank + piece * k_rows : piece * v_rows;  // first token of the copy in a block
+        const int col = is_k ? (nth % NH) * 64 : VCOL * rank;
+        const int width = scale ? T::SB : T::RB;                        // 4-bit: bytes of a row
+        const int box_at = !I4 ? (is_k ? (nth % NH) * K_HALF + piece * k_rows * 128 : KB + tok * VCOL * 2)
+                               : (is_k ? (scale ? T::RAW_KS : 0) : (scale ? T::RAW_VS : T::RAW_V)) + piece * rows * width;
+        const char* src = is_k ? (scale ? a.pg.ks : a.pg.k) : (scale ? a.pg.vs : a.pg.v);
         const int page_mask = (1 << a.pg.shift) - 1;
         uint32_t it = 0;
         bool ok = true;
@@ -332,7 +353,7 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
             need = mine && w.any_seen(k0 + tok, k0 + tok + rows - 1);
             if (need) page = page_entry(a.pg, w.seq, k0 + tok);  // looked at when the stage is free
         };
-        if constexpr (!I4) look();
+        look();
         while (ok) {
             if (b == w.b0) {
                 const int qb = tl & 1;
@@ -355,8 +376,22 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
             }
             const int st = it % STAGES;
             if constexpr (I4) {
-                if (!(it & 1)) ok = pass_on(&own_full[st], &kv_full[st], (it / STAGES) & 1, &abort_flag);
+                const int rs = it % T::RAW_STAGES;
+                ok = warp_poll(&raw_empty[rs], ((it / T::RAW_STAGES) & 1) ^ 1, &abort_flag);
                 if (!ok) break;
+                const uint32_t bytes = __reduce_add_sync(0xffffffffu, need ? (unsigned)(rows * width) : 0u);
+                if (lane == 0) {
+                    raw_at[rs] = make_int3(k0, w.it.p_lo, w.it.p_hi);
+                    pend_raw[rs] = (int)((it / T::RAW_STAGES) & 1);
+                    mbar_expect_tx(&raw_full[rs], bytes);
+                }
+                __syncwarp();
+                if (need) {
+                    const int pg = checked_page(a.pg, page, a.err);
+                    bulk_copy(sKV + STAGES * STAGE + rs * T::RAW + box_at,
+                              src + page_row(a.pg, pg, w.head, (k0 + tok) & page_mask) * width, (uint32_t)(rows * width), &raw_full[rs]);
+                }
+                __syncwarp();
             } else {
                 ok = warp_poll(&kv_empty[st], ((it / STAGES) & 1) ^ 1, &abort_flag);
                 if (!ok) break;
@@ -393,8 +428,17 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                 if (!w.more()) break;
                 b = w.b0;
             }
-            if constexpr (!I4) look();
+            look();
         }
+        if (!ok) {
+            abort_flag = 1;
+            if (lane == 0) set_error(a.err, BLEND_ETIMEOUT);
+        }
+    } else if (I4 && rank == 1 && (warp == 1 || warp == S_WARP)) {
+        // ------------------------------------------------ the second CTA's blocks, signalled to the leader
+        bool ok = true;
+        for (int i = warp == 1 ? 0 : 1; ok && i < x_end - x_first; i += 2)
+            ok = pass_on(&own_full[i % STAGES], &kv_full[i % STAGES], (i / STAGES) & 1, &abort_flag);
         if (!ok) {
             abort_flag = 1;
             if (lane == 0) set_error(a.err, BLEND_ETIMEOUT);
@@ -720,121 +764,81 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
             abort_flag = 1;
             if (lane == 0) set_error(a.err, BLEND_ETIMEOUT);
         }
-    } else if (I4 && warp == S_WARP + 5) {
-        // ------------------------------------------------ odd blocks' signals (warp 0 has the even ones)
-        bool ok = true;
-        for (int i = 1; ok && i < x_end - x_first; i += 2) ok = pass_on(&own_full[i % STAGES], &kv_full[i % STAGES], (i / STAGES) & 1, &abort_flag);
-        if (!ok) {
-            abort_flag = 1;
-            if (lane == 0) set_error(a.err, BLEND_ETIMEOUT);
-        }
     } else if (I4 && warp > S_WARP) {
         // ------------------------------------------------ 4-bit pages to bf16 operands (both CTAs)
-        // Each thread copies its own raw rows RAW_STAGES - 1 blocks ahead with cp.async, so it waits
-        // for its own copies alone; their pages are read one block earlier still.
         const int t = threadIdx.x - (S_WARP + 1) * 32;  // V: token t of the block; K: half a row of this CTA's token t / 2
-        constexpr int RB = D / 2, SB = T::SB, RS = T::RAW_STAGES;
-        constexpr int VAT = 128 * (D / 4), KSAT = VAT + 128 * (D / 2), VSAT = KSAT + 128 * SB;  // in a raw stage
-        uint8_t* raw = sKV + STAGES * STAGE;
-        const int page_mask = (1 << a.pg.shift) - 1;
-        const int n_blocks = x_end - x_first;
-        Walk w(a, pre, rows2, x_first, x_end);
-        int b = w.b0, jk = 0, jv = 0, pk = 0, pv = 0;
-        bool sk = false, sv = false;
-        auto look = [&]() {
-            const int k0 = w.it.kr.block(b) * TKEYS;
-            jk = k0 + 64 * rank + (t >> 1);
-            jv = k0 + t;
-            sk = w.any_seen(jk, jk);
-            sv = w.any_seen(jv, jv);
-            if (sk) pk = page_entry(a.pg, w.seq, jk);
-            if (sv) pv = page_entry(a.pg, w.seq, jv);
-        };
-        auto copy = [&](int stage) {  // the block that look() saw, zeros for what no row sees
-            const uint32_t dst = su32(raw + stage * T::RAW);
-            const int gk = sk ? checked_page(a.pg, pk, a.err) : 0, gv = sv ? checked_page(a.pg, pv, a.err) : 0;
-            const long long rk = page_row(a.pg, gk, w.head, jk & page_mask), rv = page_row(a.pg, gv, w.head, jv & page_mask);
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) cp_async<16>(dst + (i * 128 + t) * 16, a.pg.k + rk * RB + (t & 1) * (D / 4) + i * 16, sk);
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) cp_async<16>(dst + VAT + (i * 128 + t) * 16, a.pg.v + rv * RB + i * 16, sv);
-            cp_async<SB>(dst + KSAT + t * SB, a.pg.ks + rk * SB, sk);
-            cp_async<SB>(dst + VSAT + t * SB, a.pg.vs + rv * SB, sv);
-        };
-        auto step = [&](int stage) {
-            if (!w.more()) return;
-            copy(stage);
-            if (++b == w.b1) {
-                w.next();
-                if (!w.more()) return;
-                b = w.b0;
-            }
-            look();
-        };
-        look();
-        for (int i = 0; i < RS - 1; ++i) {
-            step(i);
-            cp_commit();
-        }
+        constexpr int RB = T::RB, SB = T::SB, RS = T::RAW_STAGES, G = D / 32;
+        const int n_blocks = x_end - x_first, tk = t >> 1;
         bool ok = true;
         for (int i = 0; i < n_blocks; ++i) {
-            const int st = i % STAGES;
-            step((i + RS - 1) % RS);
-            cp_commit();
-            cp_wait<RS - 1>();
-            uint32_t kw[D / 16], vw[8], ksc[D / 64], vsc;
+            const int st = i % STAGES, rs = i % RS;
+            ok = warp_wait(&raw_full[rs], (i / RS) & 1, &abort_flag) && warp_poll(&kv_empty[st], ((i / STAGES) & 1) ^ 1, &abort_flag);
+            if (!ok) break;
+            if (t == 0) pend_raw[rs] = -1;
+            const uint8_t* raw = sKV + STAGES * STAGE + rs * T::RAW;
+            uint8_t* dk = sKV + st * STAGE;
             {
-                const uint8_t* p = raw + (i % RS) * T::RAW;
+                const uint4* p = reinterpret_cast<const uint4*>(raw + t * (RB / 2));
+                uint32_t kw[D / 16], sc[G];
 #pragma unroll
                 for (int q = 0; q < D / 64; ++q) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(p + (q * 128 + t) * 16);
+                    const uint4 v = p[q];
                     kw[4 * q] = v.x; kw[4 * q + 1] = v.y; kw[4 * q + 2] = v.z; kw[4 * q + 3] = v.w;
                 }
 #pragma unroll
-                for (int q = 0; q < D / 32; ++q) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(p + VAT + (q * 128 + t) * 16);
-                    if constexpr (D == 128) {  // word r: groups 2 rank, 2 rank + 1 of half r
-                        vw[2 * q] = rank ? v.y : v.x;
-                        vw[2 * q + 1] = rank ? v.w : v.z;
-                    } else {  // word r: groups 0, 1 of half r
-                        vw[4 * q] = v.x; vw[4 * q + 1] = v.y; vw[4 * q + 2] = v.z; vw[4 * q + 3] = v.w;
-                    }
+                for (int q = 0; q < G / 2; ++q) {
+                    const uint32_t v = *reinterpret_cast<const uint32_t*>(raw + T::RAW_KS + tk * SB + 4 * q);
+                    sc[2 * q] = both(v, 0);
+                    sc[2 * q + 1] = both(v, 1);
                 }
 #pragma unroll
-                for (int q = 0; q < D / 64; ++q) ksc[q] = *reinterpret_cast<const uint32_t*>(p + KSAT + t * SB + 4 * q);
-                vsc = *reinterpret_cast<const uint32_t*>(p + VSAT + t * SB + (D == 128 ? 4 * rank : 0));
-            }
-            ok = warp_poll(&kv_empty[st], ((i / STAGES) & 1) ^ 1, &abort_flag);
-            if (!ok) break;
-            uint8_t* dk = sKV + st * STAGE;
-            const int tk = t >> 1;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                // word i of this half row: c = 2 (t & 1) + i / G, g = i % G  (G = D / 32 words per c)
-                constexpr int G = D / 32;
-                const int c = 2 * (t & 1) + i / G, g = i % G;
-                const uint32_t sc = both(ksc[g >> 1], g & 1);
-                const int ch = 4 * (g & 1) + c;
-                *reinterpret_cast<uint4*>(dk + (g >> 1) * K_HALF + tk * 128 + ((ch ^ (tk & 7)) << 4)) =
-                    make_uint4(pair_value<false>(kw[i], sc), pair_value<true>(kw[i], sc), pair_value<false>(kw[i] >> 8, sc), pair_value<true>(kw[i] >> 8, sc));
+                for (int q = 0; q < D / 16; ++q) {
+                    // word q of this half row: c = 2 (t & 1) + q / G, g = q % G  (G words per c)
+                    const int c = 2 * (t & 1) + q / G, g = q % G, ch = 4 * (g & 1) + c;
+                    const uint32_t w = kw[q], hi = w >> 8;
+                    *reinterpret_cast<uint4*>(dk + (g >> 1) * K_HALF + tk * 128 + ((ch ^ (tk & 7)) << 4)) =
+                        make_uint4(pair_value<false>(w, sc[g]), pair_value<true>(w, sc[g]), pair_value<false>(hi, sc[g]), pair_value<true>(hi, sc[g]));
+                }
             }
             uint8_t* dv = dk + KB;
+            {
+                const int3 at = raw_at[rs];
+                const int j = at.x + t;
+                const bool seen = j <= at.z && (j < a.n_sink || j > at.y - a.window);
+                // a token that no row sees counts as zero whatever its scale (or the row, if it was not read)
+                const uint32_t vsc = seen ? *reinterpret_cast<const uint32_t*>(raw + T::RAW_VS + t * SB + (D == 128 ? 4 * rank : 0)) : 0u;
+                const uint32_t s0 = both(vsc, D == 128 ? 0 : rank), s1 = both(vsc, 1);
 #pragma unroll
-            for (int g = 0; g < (D == 128 ? 2 : 1); ++g)
+                for (int q = 0; q < 4; ++q) {
+                    // chunk c holds dims 8c.. of each group: halves r = 2c, 2c + 1; threads start at different
+                    // chunks so that a warp's reads fall on distinct banks
+                    const int c = (q + (t >> 1)) & 3;
+                    uint32_t x, y;  // words of halves 2c, 2c + 1 with this CTA's groups
+                    if constexpr (D == 128) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(raw + T::RAW_V + t * RB + c * 16);
+                        x = rank ? v.y : v.x;
+                        y = rank ? v.w : v.z;
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2*>(raw + T::RAW_V + t * RB + c * 8);
+                        x = rank ? v.x >> 16 : v.x;
+                        y = rank ? v.y >> 16 : v.y;
+                    }
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int hi = D == 128 ? g : rank;  // which 16-bit half of the words
-                    const uint32_t sc = both(vsc, hi);
-                    const uint32_t h0 = (hi ? vw[2 * c] >> 16 : vw[2 * c] & 0xffffu), h1 = (hi ? vw[2 * c + 1] >> 16 : vw[2 * c + 1] & 0xffffu);
-                    const uint32_t y0 = h0 | (h0 << 12), y1 = h1 | (h1 << 12);  // nibbles 0, 1 and 2, 3 as pairs at bits 0 and 8
-                    const int ch = 4 * g + c;
-                    const int at = D == 128 ? t * 128 + ((ch ^ (t & 7)) << 4) : t * 64 + ((ch ^ ((t >> 1) & 3)) << 4);
-                    *reinterpret_cast<uint4*>(dv + at) = make_uint4(pair_value<false>(y0, sc), pair_value<false>(y0 >> 8, sc), pair_value<false>(y1, sc), pair_value<false>(y1 >> 8, sc));
+                    for (int g = 0; g < D / 64; ++g) {  // low halves of x, y, then the high ones
+                        const uint32_t h0 = g ? x >> 16 : x & 0xffffu, h1 = g ? y >> 16 : y & 0xffffu;
+                        const uint32_t y0 = h0 | (h0 << 12), y1 = h1 | (h1 << 12);  // codes 0, 1 and 2, 3 as pairs at bits 0 and 8
+                        const uint32_t sc = g ? s1 : s0;
+                        const int ch = 4 * g + c;
+                        const int to = D == 128 ? t * 128 + ((ch ^ (t & 7)) << 4) : t * 64 + ((ch ^ ((t >> 1) & 3)) << 4);
+                        *reinterpret_cast<uint4*>(dv + to) = make_uint4(pair_value<false>(y0, sc), pair_value<false>(y0 >> 8, sc),
+                                                                        pair_value<false>(y1, sc), pair_value<false>(y1 >> 8, sc));
+                    }
                 }
+            }
+            warp_arrive(&raw_empty[rs]);
             fence_async_smem();
-            warp_arrive(&own_full[st]);
+            warp_arrive(rank == 0 ? &kv_full[st] : &own_full[st]);
         }
-        cp_wait<0>();
         if (!ok) {
             abort_flag = 1;
             if (lane == 0) set_error(a.err, BLEND_ETIMEOUT);
@@ -853,6 +857,11 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
             for (int b = 0; b < 2; ++b)
                 if (pend_q[b] >= 0)
                     for (long long i = 0; i < SPIN_LIMIT && !mbar_try(&q_full[b], (uint32_t)pend_q[b]); ++i) {
+                    }
+        if (I4)
+            for (int s = 0; s < T::RAW_STAGES; ++s)
+                if (pend_raw[s] >= 0)
+                    for (long long i = 0; i < SPIN_LIMIT && !mbar_try(&raw_full[s], (uint32_t)pend_raw[s]); ++i) {
                     }
         // (an edge barrier's parity is its warp's; it is waited for in both, which costs a bounded wait)
         for (int st = 0; st < STAGES; ++st)
