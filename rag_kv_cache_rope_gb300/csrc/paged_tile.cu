@@ -49,13 +49,14 @@ template <bool I4, int D> struct TileCfg {
     static constexpr int KB = NH * K_HALF;
     static constexpr int VB = TKEYS * VCOL * 2;
     static constexpr int STAGE = KB + VB;
-    static constexpr int STAGES = D == 64 ? 8 : I4 ? 3 : 5;
+    static constexpr int STAGES = D == 64 ? 8 : 5;
+    static constexpr int QB = I4 ? 1 : 2;  // Q buffers: 4-bit pages need the room for stages
     // 4-bit pages: raw rows on their way (this CTA's 64 keys, the 128 values, their scales)
-    static constexpr int RAW_STAGES = 4;
+    static constexpr int RAW_STAGES = 2;
     static constexpr int RB = D / 2, SB = D / 16;  // bytes of a row and of its scales
     static constexpr int RAW_V = 64 * RB, RAW_KS = RAW_V + TKEYS * RB, RAW_VS = RAW_KS + 64 * SB;
     static constexpr int RAW = I4 ? RAW_VS + TKEYS * SB : 0;
-    static constexpr int SMEM = 2 * QT + STAGES * STAGE + RAW_STAGES * RAW + 1024;
+    static constexpr int SMEM = QB * QT + STAGES * STAGE + RAW_STAGES * RAW + 1024;
     // kind::f16, bf16 inputs, fp32 accumulate, M256 (the pair); S: N128, P.V: N = D with B MN-major
     static constexpr uint32_t IDESC_S = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((256u >> 4) << 24);
     static constexpr uint32_t IDESC_PV =
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
 
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t* sQ = smem;              // Q buffer qb at qb * QT
-    uint8_t* sKV = smem + 2 * QT;    // stage s at s * STAGE: K column halves, V
+    uint8_t* sKV = smem + T::QB * QT;    // stage s at s * STAGE: K column halves, V
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = (int)cta_rank();
     const int grp = (int)(blockIdx.x >> 1), n_grp = (int)(gridDim.x >> 1);
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
     const int x_first = (int)x64, x_end = (int)min((long long)total, x64 + quota);
 
     // Lanes of a tile past its rows read a Q of zeros
-    for (int i = threadIdx.x; i < 2 * QT / 16; i += T::THREADS) reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < T::QB * QT / 16; i += T::THREADS) reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
     fence_async_smem();
     if (threadIdx.x == 0) {
         for (int b = 0; b < 2; ++b) {
@@ -356,13 +357,13 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
         look();
         while (ok) {
             if (b == w.b0) {
-                const int qb = tl & 1;
-                ok = warp_poll(&q_empty[qb], ((tl >> 1) & 1) ^ 1, &abort_flag);
+                const int qb = tl % T::QB;
+                ok = warp_poll(&q_empty[qb], ((tl / T::QB) & 1) ^ 1, &abort_flag);
                 if (!ok) break;
                 if (lane == 0) {
                     if (rank == 0) {
                         mbar_expect_tx(&q_full[qb], 2u * NH * 128u * (uint32_t)(group * rpt));  // both CTAs' tiles
-                        pend_q[qb] = (tl >> 1) & 1;
+                        pend_q[qb] = (tl / T::QB) & 1;
                     }
                     // an absent second tile reloads the first (finite data, never stored)
                     const int t_row = w.tp * rows2 + rank * rpt;
@@ -449,8 +450,8 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
         bool ok = true;
         int tl = 0;
         for (Walk w(a, pre, rows2, x_first, x_end); ok && w.more(); w.next(), ++tl) {
-            const int qb = tl & 1;
-            if (!wait_cl(&q_full[qb], (tl >> 1) & 1, &abort_flag)) {
+            const int qb = tl % T::QB;
+            if (!wait_cl(&q_full[qb], (tl / T::QB) & 1, &abort_flag)) {
                 ok = false;
                 break;
             }
@@ -690,32 +691,45 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
             __threadfence();
             // part k lies with cluster g_first + k: in its slot 1 when the item starts there, else in slot 0
             float mx = -INFINITY, sum = 0.f;
+#pragma unroll 4
             for (int k = 0; k < n_part; ++k) mx = max_nan(mx, __ldcg(slot(g_first + k, k == 0) + TQ * D + r_in));
             const float ref = mx == -INFINITY ? 0.f : mx;
-            float acc[D];
-#pragma unroll
-            for (int e = 0; e < D; ++e) acc[e] = 0.f;
+#pragma unroll 4
             for (int k = 0; k < n_part; ++k) {
                 const float* p = slot(g_first + k, k == 0);
-                const float f = ex2(__ldcg(p + TQ * D + r_in) - ref);
-                sum += __ldcg(p + TQ * (D + 1) + r_in) * f;
-#pragma unroll
-                for (int e = 0; e < D / 4; ++e) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(p) + e * TQ + r_in);
-                    acc[4 * e] = fmaf(v.x, f, acc[4 * e]);
-                    acc[4 * e + 1] = fmaf(v.y, f, acc[4 * e + 1]);
-                    acc[4 * e + 2] = fmaf(v.z, f, acc[4 * e + 2]);
-                    acc[4 * e + 3] = fmaf(v.w, f, acc[4 * e + 3]);
-                }
+                sum += __ldcg(p + TQ * (D + 1) + r_in) * ex2(__ldcg(p + TQ * D + r_in) - ref);
             }
-            if (valid) {
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            // 32 columns at a time, so that all loads of two parts are on their way together
+#pragma unroll 1
+            for (int e = 0; e < D; e += 32) {
+                float acc[32];
 #pragma unroll
-                for (int v = 0; v < D / 8; ++v) {
-                    uint32_t w4[4];
+                for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+#pragma unroll 2
+                for (int k = 0; k < n_part; ++k) {
+                    const float* p = slot(g_first + k, k == 0);
+                    const float f = ex2(__ldcg(p + TQ * D + r_in) - ref) * inv;
+                    const float4* q = reinterpret_cast<const float4*>(p) + (e / 4) * TQ + r_in;
+                    float4 v[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) w4[i] = pack_bf16x2(acc[v * 8 + 2 * i] * inv, acc[v * 8 + 2 * i + 1] * inv);
-                    *reinterpret_cast<uint4*>(dst + v * 8) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                    for (int i = 0; i < 8; ++i) v[i] = __ldcg(q + i * TQ);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        acc[4 * i] = fmaf(v[i].x, f, acc[4 * i]);
+                        acc[4 * i + 1] = fmaf(v[i].y, f, acc[4 * i + 1]);
+                        acc[4 * i + 2] = fmaf(v[i].z, f, acc[4 * i + 2]);
+                        acc[4 * i + 3] = fmaf(v[i].w, f, acc[4 * i + 3]);
+                    }
+                }
+                if (valid) {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        uint32_t w4[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w4[i] = pack_bf16x2(acc[v * 8 + 2 * i], acc[v * 8 + 2 * i + 1]);
+                        *reinterpret_cast<uint4*>(dst + e + v * 8) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                    }
                 }
             }
         }
