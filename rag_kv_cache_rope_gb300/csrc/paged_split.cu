@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(W * 32, 2)
     constexpr int R = 8 * NT, T = W * 32, KT = D / 16, G = D / 32, OPAD = Cfg::OPAD;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int pre[BLEND_MAX_SEQS + 1];
-    __shared__ int scan[W];
+    __shared__ int scan[W], items[W];
     __shared__ float sm[W][R], sl[W][R], sM[R], sL[R];
     __shared__ __align__(8) float s_start[I4 ? W : 1][G][R];  // 4-bit keys: -8 2^-24 sum q of each 32 dims
     __shared__ int last_sh;
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(W * 32, 2)
     // ---- the line of steps: pre[s] = steps of all items of sequences before s
     {
         const int per = (n_seq + T - 1) / T;
-        int mine = 0;
+        int mine = 0, active = 0;
         for (int i = 0; i < per; ++i) {
             const int s = tid * per + i;
             if (s >= n_seq) break;
@@ -158,7 +158,9 @@ __global__ void __launch_bounds__(W * 32, 2)
                 n = max(1, key_range<PAGED_STEP>(si.len - si.n_q, si.len - 1, a.window, a.n_sink).total());
             pre[s + 1] = n * hkv;
             mine += n * hkv;
+            active += n > 0;
         }
+        active = __reduce_add_sync(0xffffffffu, active);
         int incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -166,6 +168,7 @@ __global__ void __launch_bounds__(W * 32, 2)
             if (lane >= o) incl += y;
         }
         if (lane == 31) scan[warp] = incl;
+        if (lane == 0) items[warp] = active;
         __syncthreads();
         int at = incl - mine;
         for (int w = 0; w < warp; ++w) at += scan[w];
@@ -179,7 +182,18 @@ __global__ void __launch_bounds__(W * 32, 2)
         __syncthreads();
     }
     const int total = pre[n_seq];
-    const int quota = max(W, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+    int n_item = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) n_item += items[w];
+    if (n_item == 0) return;
+    n_item *= hkv;
+    // An equal share of the line, but at least a step per warp.  Leaving parts of an item and joining
+    // them takes about 5 us, so items of up to four steps per warp are never cut, for a small total
+    // nor at a border (GB300, bf16: 8 items of 7 steps 8.8 us whole and 14.7 us in two parts; 8 items of
+    // 44 steps 10.9 us in 11 parts, 12.9 in 6 and 14.6 in 3; 128 sequences of 50-200 tokens LATER).
+    constexpr int SHORT = 4 * W;
+    const int per_item = (total + n_item - 1) / n_item;
+    const int quota = max((total + (int)gridDim.x - 1) / (int)gridDim.x, per_item <= SHORT ? per_item : W);
     long long x64 = (long long)blockIdx.x * quota;
     if (x64 >= total) return;
     int x = (int)x64;
@@ -217,7 +231,13 @@ __global__ void __launch_bounds__(W * 32, 2)
         const int steps = (pre[seq + 1] - pre[seq]) / hkv;
         const int head = (x - pre[seq]) / steps;
         const int item0 = pre[seq] + head * steps;
-        const int s0 = x - item0, s1 = min(steps, s0 + (x_end - x));
+        const int s0 = x - item0;
+        // a short item is never cut: it is the CTA's where it starts
+        if (steps <= SHORT && s0 > 0) {
+            x = item0 + steps;
+            continue;
+        }
+        const int s1 = steps <= SHORT ? steps : min(steps, s0 + (x_end - x));
         const int npair = si.n_q * a.group;
         const int p0 = si.len - si.n_q, p1 = si.len - 1;
         const KeyRange kr = key_range<PAGED_STEP>(p0, p1, a.window, a.n_sink);
