@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(W * 32, 2)
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int pre[BLEND_MAX_SEQS + 1];
     __shared__ int scan[W], items[W];
+    __shared__ int s_row[R], s_off[R];  // a pair's row, and its offset in the output from the item's first
     __shared__ float sm[W][R], sl[W][R], sM[R], sL[R];
     __shared__ __align__(8) float s_start[I4 ? W : 1][G][R];  // 4-bit keys: -8 2^-24 sum q of each 32 dims
     __shared__ int last_sh;
@@ -143,6 +144,10 @@ __global__ void __launch_bounds__(W * 32, 2)
     const int r = lane >> 2, c = lane & 3;
     const int hkv = a.pg.hkv, n_seq = a.pg.n_seq;
 
+    if (tid < R) {
+        s_row[tid] = tid / a.group;
+        s_off[tid] = (tid / a.group * a.hq + tid % a.group) * D;
+    }
     // ---- the line of steps: pre[s] = steps of all items of sequences before s
     {
         const int per = (n_seq + T - 1) / T;
@@ -225,10 +230,25 @@ __global__ void __launch_bounds__(W * 32, 2)
     const char* v_lane = a.pg.v + lane * 16;
     const char* s_lane = (lane < 16 ? a.pg.ks : a.pg.vs) + (lane & 15) * S::SCALE;
 
+    // what holds for all heads of a sequence
+    SeqInfo si{0, 0, 0};
+    KeyRange kr{0, 0, 0};
+    int known = -1, steps = 0, npair = 0, p0 = 0, p1 = 0, clean0 = 0, n_clean = 0;
+
     while (x < x_end) {
         while (pre[seq + 1] <= x) ++seq;  // skips sequences without steps
-        const SeqInfo si = seq_info(a, seq);
-        const int steps = (pre[seq + 1] - pre[seq]) / hkv;
+        if (seq != known) {
+            known = seq;
+            si = seq_info(a, seq);
+            steps = (pre[seq + 1] - pre[seq]) / hkv;
+            npair = si.n_q * a.group;
+            p0 = si.len - si.n_q;
+            p1 = si.len - 1;
+            kr = key_range<PAGED_STEP>(p0, p1, a.window, a.n_sink);
+            // steps of the window's range that every row sees whole: no masks, no token to leave out
+            clean0 = kr.n_a + max(0, (max(p1 - a.window, -1) + PAGED_STEP) / PAGED_STEP - kr.first_b);
+            n_clean = (p0 + 1) / PAGED_STEP - kr.first_b + kr.n_a - clean0;
+        }
         const int head = (x - pre[seq]) / steps;
         const int item0 = pre[seq] + head * steps;
         const int s0 = x - item0;
@@ -238,14 +258,7 @@ __global__ void __launch_bounds__(W * 32, 2)
             continue;
         }
         const int s1 = steps <= SHORT ? steps : min(steps, s0 + (x_end - x));
-        const int npair = si.n_q * a.group;
-        const int p0 = si.len - si.n_q, p1 = si.len - 1;
-        const KeyRange kr = key_range<PAGED_STEP>(p0, p1, a.window, a.n_sink);
         const int n_real = min(s1, kr.total());  // the empty step of a sequence without keys is none
-
-        // steps of the window's range that every row sees whole: no masks, no token to leave out
-        const int clean0 = kr.n_a + max(0, (max(p1 - a.window, -1) + PAGED_STEP) / PAGED_STEP - kr.first_b);
-        const int n_clean = (p0 + 1) / PAGED_STEP - kr.first_b + kr.n_a - clean0;
         auto clean = [&](int i) { return n_clean > 0 && (unsigned)(i - clean0) < (unsigned)n_clean; };
 
         // ---- loads of step i into a place of the ring
@@ -276,6 +289,27 @@ __global__ void __launch_bounds__(W * 32, 2)
         };
         auto entry_at = [&](int i) { return page_entry(a.pg, seq, kr.block(i) * PAGED_STEP); };
 
+        // ---- queries, asked for before the keys
+        uint32_t qf[NT][KT][2];
+        uint4 raw[I4 ? NT : 1][G];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int p = nt * 8 + r;
+            const bool ok = p < npair;
+            const bf16* qr = reinterpret_cast<const bf16*>(a.q) + (si.row0 + (ok ? s_row[p] : 0)) * a.ld_q + head * a.group * D +
+                             (ok ? s_off[p] - s_row[p] * a.hq * D : 0);
+            if constexpr (!I4) {
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt) {
+                    qf[nt][kt][0] = ok ? *reinterpret_cast<const uint32_t*>(qr + 16 * kt + 2 * c) : 0u;
+                    qf[nt][kt][1] = ok ? *reinterpret_cast<const uint32_t*>(qr + 16 * kt + 2 * c + 8) : 0u;
+                }
+            } else {
+#pragma unroll
+                for (int g = 0; g < G; ++g)  // dims 32 g + 8 c .. +7
+                    raw[nt][g] = ok ? *reinterpret_cast<const uint4*>(qr + 32 * g + 8 * c) : make_uint4(0, 0, 0, 0);
+            }
+        }
         // ---- first steps on their way; the warp takes U neighbouring steps of every U W
         int li = s0 + U * warp;  // next step to load
         int entry[U];
@@ -297,31 +331,19 @@ __global__ void __launch_bounds__(W * 32, 2)
         next_entries();
 #pragma unroll
         for (int st = 0; st < STAGES - 1; ++st) load_next(st);
-        // ---- queries (B operand) and the pairs' positions
-        uint32_t qf[NT][KT][2];
+        // ---- queries as B operands, and the pairs' positions
         int rp[NT][2];
         float sc[NT][2];  // score to exponent of 2
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int p = nt * 8 + r;
-            const bool ok = p < npair;
-            const bf16* qr = reinterpret_cast<const bf16*>(a.q) + (long long)(si.row0 + (ok ? p / a.group : 0)) * a.ld_q +
-                             (head * a.group + (ok ? p % a.group : 0)) * D;
             float row_scale = 1.f;
-            if constexpr (!I4) {
-#pragma unroll
-                for (int kt = 0; kt < KT; ++kt) {
-                    qf[nt][kt][0] = ok ? *reinterpret_cast<const uint32_t*>(qr + 16 * kt + 2 * c) : 0u;
-                    qf[nt][kt][1] = ok ? *reinterpret_cast<const uint32_t*>(qr + 16 * kt + 2 * c + 8) : 0u;
-                }
-            } else {
-                // dims 32 g + 8 c .. +7 of the row, by a power of two that brings its largest into [1, 2)
-                uint4 raw[G];
+            if constexpr (I4) {
+                // by a power of two that brings the row's largest into [1, 2)
                 float top = 0.f;
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    raw[g] = ok ? *reinterpret_cast<const uint4*>(qr + 32 * g + 8 * c) : make_uint4(0, 0, 0, 0);
-                    const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+                    const uint32_t w[4] = {raw[nt][g].x, raw[nt][g].y, raw[nt][g].z, raw[nt][g].w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
@@ -333,7 +355,7 @@ __global__ void __launch_bounds__(W * 32, 2)
                 row_scale = __uint_as_float((uint32_t)(127 + ex) << 23);
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+                    const uint32_t w[4] = {raw[nt][g].x, raw[nt][g].y, raw[nt][g].z, raw[nt][g].w};
                     float sum = 0.f;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -351,7 +373,7 @@ __global__ void __launch_bounds__(W * 32, 2)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int pc = nt * 8 + 2 * c + e;
-                rp[nt][e] = pc < npair ? p0 + pc / a.group : -1;
+                rp[nt][e] = pc < npair ? p0 + s_row[pc] : -1;
                 sc[nt][e] = a.scale_log2;
                 if constexpr (I4) sc[nt][e] *= 0x1p24f * __shfl_sync(0xffffffffu, row_scale, 4 * (2 * c + e));
             }
@@ -587,9 +609,8 @@ __global__ void __launch_bounds__(W * 32, 2)
         }
         __syncthreads();
         const bool whole_item = s0 == 0 && s1 == steps;
-        const int first = item0 / quota, n_part = (item0 + steps - 1) / quota - first + 1;
         float* slot = a.part + (size_t)(2 * blockIdx.x + (s0 == 0 ? 1 : 0)) * paged_slot_floats(D);
-        bf16* out = reinterpret_cast<bf16*>(a.out);
+        bf16* out = reinterpret_cast<bf16*>(a.out) + ((long long)si.row0 * a.hq + head * a.group) * D;
         for (int i = tid; i < npair * (D / 2); i += T) {
             const int p = i / (D / 2), e = 2 * (i % (D / 2));
             float y0 = 0.f, y1 = 0.f;
@@ -602,13 +623,13 @@ __global__ void __launch_bounds__(W * 32, 2)
             }
             if (whole_item) {
                 const float inv = sL[p] == 0.f ? 0.f : 1.f / sL[p];
-                const long long row = si.row0 + p / a.group;
-                *reinterpret_cast<uint32_t*>(out + (row * a.hq + head * a.group + p % a.group) * D + e) = pack2(y0 * inv, y1 * inv);
+                *reinterpret_cast<uint32_t*>(out + s_off[p] + e) = pack2(y0 * inv, y1 * inv);
             } else {
                 *reinterpret_cast<float2*>(slot + p * D + e) = make_float2(y0, y1);
             }
         }
         if (!whole_item) {
+            const int first = item0 / quota, n_part = (item0 + steps - 1) / quota - first + 1;
             if (tid < npair) {
                 slot[PAGED_MAX_TILE * D + tid] = sM[tid];
                 slot[PAGED_MAX_TILE * (D + 1) + tid] = sL[tid];
@@ -690,9 +711,7 @@ __global__ void __launch_bounds__(W * 32, 2)
                             t.w += v.w;
                         }
                         const int p = (q0 + i) / V4, e4 = (q0 + i) % V4;
-                        const long long row = si.row0 + p / a.group;
-                        *reinterpret_cast<uint2*>(out + (row * a.hq + head * a.group + p % a.group) * D + 4 * e4) =
-                            make_uint2(pack2(t.x, t.y), pack2(t.z, t.w));
+                        *reinterpret_cast<uint2*>(out + s_off[p] + 4 * e4) = make_uint2(pack2(t.x, t.y), pack2(t.z, t.w));
                     }
                     __syncthreads();
                 }
