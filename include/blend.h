@@ -501,7 +501,7 @@ int paged_gather(blend_handle* h, const blend_pages* pages, const int32_t* seq, 
  * max_q (host): most query rows of one sequence; it picks the kernels (single tokens and few
  * rows: the keys split over all SMs; long pieces: tiles of 128 pairs on the tensor cores).
  * Keys and values of tokens no row of the call sees are not used: slots past a length may hold
- * anything.  A NaN or infinity in a token that some rows see reaches them, and may reach other
+ * anything, and table entries of pages without a token that some row sees are not read.  A NaN or infinity in a token that some rows see reaches them, and may reach other
  * rows of the same sequence in the call.  The result does not depend on timing.
  * Uses the handle's workspace: calls on one handle must not overlap, replays of captured ones
  * included.  Device-side checks (BLEND_EDEVICE): a sequence with row bounds outside 0..max_rows or

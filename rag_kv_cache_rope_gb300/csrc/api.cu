@@ -1439,10 +1439,13 @@ int paged_attention(blend_handle* h, const blend_pages* pages, const void* q, in
     if (!row_stride_ok(h, ld_q, c.n_q_heads)) return fail(h, BLEND_EINVAL, "bad row stride %lld", (long long)ld_q);
     if (max_rows < 0 || max_rows > (1 << 24) || max_q < (max_rows > 0 ? 1 : 0) || window < 0 || n_sink < 0)
         return fail(h, BLEND_EINVAL, "bad max_rows=%d max_q=%d window=%d n_sink=%d", max_rows, max_q, window, n_sink);
-    // the keys of all sequences and heads are counted in 32 bits by the split kernels
-    if ((long long)pages->n_seq * c.n_kv_heads * ((long long)pages->max_pages * pages->page_tokens / PAGED_STEP + 1) >=
-        (1ll << 31))
-        return fail(h, BLEND_EINVAL, "table too large: n_seq * n_kv_heads * tokens / 16 must stay below 2^31");
+    // 16-key steps of all sequences and heads, and 128-key blocks of all their tiles, are counted in 32 bits
+    const long long tokens = (long long)pages->max_pages * pages->page_tokens;
+    const int tile_rows = 2 * (128 / (c.n_q_heads / c.n_kv_heads));
+    if ((long long)pages->n_seq * c.n_kv_heads * (tokens / PAGED_STEP + 1) >= (1ll << 31) ||
+        ((long long)max_rows / tile_rows + pages->n_seq) * c.n_kv_heads * (tokens / 128 + 1) >= (1ll << 31))
+        return fail(h, BLEND_EINVAL, "table too large: its tokens (in steps of 16 per sequence and kv head, in blocks of "
+                    "128 per tile and kv head) must stay below 2^31");
     if (max_rows == 0) return BLEND_OK;
     a.q = q;
     a.ld_q = ld_q;

@@ -259,6 +259,93 @@ def test_attention_long_ragged():
         assert (np.abs(got[s] - want[0]) <= attention_bound("bf16", "model", want, mag, lin, lens[s], False)[0]).all()
 
 
+@pytest.mark.parametrize("dtype,fmt", [("bf16", "model"), ("bf16", "int4"), ("f32", "model")])
+@pytest.mark.parametrize("n_seq", [129, 300, 1024])
+def test_attention_many_sequences(dtype, fmt, n_seq):
+    """As many sequences as a table may have, some empty, and among few-row ones a few long pieces."""
+    rng = np.random.default_rng(n_seq)
+    seqs = [(int(rng.integers(0, 3)), int(rng.integers(0, 60))) for _ in range(n_seq)]
+    seqs[n_seq // 2], seqs[-1] = (0, 0), (1, 7)
+    check_attention(dtype, fmt, 4, 2, 64, 16, seqs, 0, 0, 73)
+    if dtype == "bf16":
+        for i in rng.integers(0, n_seq, 5):
+            seqs[i] = (40, 40 + int(rng.integers(0, 90)))
+        check_attention(dtype, fmt, 4, 2, 64, 16, seqs, 33, 5, 79)
+
+
+@pytest.mark.parametrize("fmt", ["model", "int4"])
+def test_attention_parts_of_every_tile_size(fmt):
+    """Long contexts of few heads, cut into many parts: 1 to 32 pairs, and two-tile items."""
+    for hq, seqs in ((5, [(1, 5000)]), (4, [(3, 3000), (1, 20)]), (4, [(8, 3000), (5, 900)]), (16, [(1, 2500)]),
+                     (4, [(40, 5000)]), (2, [(120, 2000), (300, 1500), (17, 900)]), (32, [(9, 2000)])):
+        check_attention("bf16", fmt, hq, 1, 128, 64, seqs, 0, 0, 83)
+    check_attention("bf16", fmt, 6, 2, 64, 32, [(150, 2600), (400, 400), (1, 1500)], 1000, 40, 89)
+
+
+@pytest.mark.parametrize("fmt", ["model", "int4"])
+def test_queries_and_keys_of_extreme_size(fmt):
+    """Scores of ordinary size from huge queries and tiny keys, and the other way round."""
+    for up in (2.0 ** 60, 2.0 ** -60):
+        for rows in (1, 40):
+            h = handle("bf16", 8, 2, 128)
+            c = filled("bf16", fmt, 2, 128, 16, [300], 97, poison=False)
+            if fmt == "model":
+                c.tensors["k"].div_(up)
+            else:
+                c.tensors["k_scale"].div_(up)
+            q = (torch.randn(rows, 8, 128, device="cuda") * up).bfloat16()
+            got = f64(attend(h, c, q, i32([0, rows]), [300], rows)).reshape(rows, 8, 128)
+            want, mag, lin = P.attention(f64(q), c.k[0] / up, c.v[0], 300, 0, 0)
+            assert (np.abs(got - want) <= attention_bound("bf16", fmt, want, mag, lin, 300, rows > 8)).all()
+
+
+@pytest.mark.parametrize("dtype,fmt", [("bf16", "model"), ("bf16", "int4"), ("f32", "model")])
+@pytest.mark.parametrize("page", [16, 128])
+def test_pages_left_behind_by_the_window_may_be_gone(dtype, fmt, page):
+    """Table entries of pages that no row sees (a serving loop frees them) are not read or reported."""
+    h = handle(dtype, 8, 2, 128)
+    lens, window, sink = [1000, 700], 150, 3
+    c = filled(dtype, fmt, 2, 128, page, lens, 101)
+    for rows in (1, 40):
+        t = c.table.clone()
+        for s, n in enumerate(lens):
+            lo = n - rows - window + 1
+            for p in range(t.shape[1]):
+                if p * page >= sink and (p + 1) * page <= lo:
+                    t[s, p] = -5
+        pages = b.PagesRef(c.tensors["k"], c.tensors["v"], t, c.tensors["k_scale"], c.tensors["v_scale"])
+        q = torch.randn(2 * rows, 8, 128, device="cuda").to(TORCH[dtype])
+        out = torch.empty(2 * rows, 1024, dtype=q.dtype, device="cuda")
+        b.paged_attention(h, pages, q, i32([0, rows, 2 * rows]), i32(lens), rows, out, window=window, n_sink=sink)
+        b.blend_device_status(h)
+        for s, n in enumerate(lens):
+            want, mag, lin = P.attention(f64(q[s * rows:(s + 1) * rows]), c.k[s], c.v[s], n, window, sink)
+            lim = attention_bound(dtype, fmt, want, mag, lin, window + rows + 3, rows > 8)
+            assert (np.abs(f64(out[s * rows:(s + 1) * rows]).reshape(rows, 8, 128) - want) <= lim).all()
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_two_handles_on_two_streams(rows):
+    """Handles have workspaces of their own: calls in flight together give what they give alone."""
+    case = []
+    for seed in (103, 107):
+        h, st = handle("bf16", 8, 2, 128), torch.cuda.Stream()
+        lens = [5000, 300, 2100]
+        c = filled("bf16", "model", 2, 128, 16, lens, seed)
+        q = torch.randn(3 * rows, 8, 128, device="cuda").bfloat16()
+        start = i32([0, rows, 2 * rows, 3 * rows])
+        alone = attend(h, c, q, start, lens, rows)
+        case.append((h, st, c, q, start, i32(lens), alone, torch.empty_like(alone)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for h, st, c, q, start, lens, _, out in case:
+            b.paged_attention(h, c.pages, q, start, lens, rows, out, stream=st)
+    torch.cuda.synchronize()
+    for h, *_, alone, out in case:
+        assert torch.equal(alone, out)
+        b.blend_device_status(h)
+
+
 def test_nan_in_a_query_reaches_its_row_alone():
     for fmt, rows in (("model", 1), ("int4", 1), ("model", 60), ("int4", 60)):
         h = handle("bf16", 8, 2, 128)
