@@ -206,6 +206,37 @@ struct Walk {
     }
 };
 
+// A lane's row of 128 scores in TMEM: those of keys it does not see become -inf.  Seen are keys up to
+// `hi` of the block that come after hi - window or before `sink`.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }  // bits 0..n-1
+__device__ __forceinline__ void mask_scores(uint32_t s_col, int hi, int window, int sink) {
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t bits = below(hi + 1 - 32 * q) & (~below(hi - window + 1 - 32 * q) | below(sink - 32 * q));
+        if (__all_sync(0xffffffffu, bits == 0xffffffffu)) continue;
+        uint32_t v[32];
+        TMEM_LD32(s_col + 32 * q, v);
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (!(bits & (1u << i))) v[i] = __float_as_uint(-INFINITY);
+        TMEM_ST32(s_col + 32 * q, v);
+    }
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float row_max(uint32_t s_col) {
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+        uint32_t v[32];
+        TMEM_LD32(s_col + 32 * q, v);
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) mx = max3f(mx, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+    }
+    return mx;
+}
+
 // A pair's values n s: (n - 8) / 64 exactly, then rounded once as the product with 64 s.
 template <bool HI> __device__ __forceinline__ uint32_t pair_value(uint32_t w, uint32_t scale2) {
     const uint32_t n = code_pair<HI>(w);
@@ -543,23 +574,34 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                 fence_after();
                 const int k0 = w.it.kr.block(b) * TKEYS;
                 const bool cut = !all_see(k0, k0 + TKEYS - 1, t_lo, t_hi, a.window, a.n_sink);
+                if (cut) mask_scores(s_col, my_pos - k0, a.window, a.n_sink - k0);
                 uint32_t s[128];
-                auto load = [&]() {
+                float2 accs;
+                bool rescale = false;
+                float corr = 1.f;
+                // as in k_attn_pair: without this block's maximum while its sum stays below 2^50.  What few
+                // blocks need (masks, the maximum) works on TMEM in small loops, so that the path of the
+                // others is short and straight: with masks and maximum on the 128 registers, unrolled, the
+                // rest ran LATER % slower, waiting for instructions.
+                bool exact = !__all_sync(0xffffffffu, m_used != -INFINITY);
+#pragma unroll 1
+                while (true) {
+                    if (exact) {
+                        const float mxs = row_max(s_col) * a.scale_log2;
+                        const bool need = mxs > m_used + RESCALE_LOG2;
+                        rescale = __any_sync(0xffffffffu, need);
+                        if (rescale) {
+                            const float m_new = need ? mxs : m_used;
+                            corr = need ? ex2(m_used - m_new) : 1.f;
+                            l *= corr;
+                            m_used = m_new;
+                        }
+                    }
                     TMEM_LD32(s_col, s);
                     TMEM_LD32(s_col + 32, (s + 32));
                     TMEM_LD32(s_col + 64, (s + 64));
                     TMEM_LD32(s_col + 96, (s + 96));
                     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-                    if (cut) {
-                        const int hi = my_pos - k0, lo = hi - a.window, sink = a.n_sink - k0;
-#pragma unroll
-                        for (int i = 0; i < 128; ++i)
-                            if (!(i <= hi && (i > lo || i < sink))) s[i] = __float_as_uint(-INFINITY);
-                    }
-                };
-                load();
-                float2 accs = make_float2(0.f, 0.f);
-                auto weights = [&]() {
                     float2 acc2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     const float ref = m_used == -INFINITY ? 0.f : -m_used;
                     const float2 nm2 = make_float2(ref, ref);
@@ -571,39 +613,8 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                         s[e] = pack_bf16x2(p0, p1);
                     }
                     accs = __fadd2_rn(acc2[0], acc2[1]);
-                };
-                bool rescale = false;
-                float corr = 1.f;
-                // as in k_attn_pair: without this block's maximum while its sum stays below 2^50
-                bool exact = !__all_sync(0xffffffffu, m_used != -INFINITY);
-                if (!exact) {
-                    weights();
-                    exact = __any_sync(0xffffffffu, !(accs.x + accs.y <= 0x1p50f));
-                    if (exact) load();
-                }
-                if (exact) {
-                    float mx;
-                    {
-                        float y[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) y[i] = fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 8]));
-#pragma unroll
-                        for (int i = 16; i < 128; i += 16)
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                y[e] = max3f(y[e], __uint_as_float(s[i + e]), __uint_as_float(s[i + 8 + e]));
-                        mx = max3f(max3f(y[0], y[1], y[2]), max3f(y[3], y[4], y[5]), fmaxf(y[6], y[7]));
-                    }
-                    const float mxs = mx * a.scale_log2;
-                    const bool need = mxs > m_used + RESCALE_LOG2;
-                    rescale = __any_sync(0xffffffffu, need);
-                    if (rescale) {
-                        const float m_new = need ? mxs : m_used;
-                        corr = need ? ex2(m_used - m_new) : 1.f;
-                        l *= corr;
-                        m_used = m_new;
-                    }
-                    weights();
+                    if (exact || !__any_sync(0xffffffffu, !(accs.x + accs.y <= 0x1p50f))) break;
+                    exact = true;  // P is not stored yet: once more, from the block's maximum
                 }
                 TMEM_ST32(s_col, s);
                 TMEM_ST32(s_col + 32, (s + 32));
@@ -614,7 +625,7 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                         break;
                     }
                     fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int e = 0; e < D; e += 32) {
                         uint32_t o[32];
                         TMEM_LD32(o_col + e, o);
