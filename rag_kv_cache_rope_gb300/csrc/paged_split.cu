@@ -193,16 +193,16 @@ __global__ void __launch_bounds__(W * 32, 2)
     if (n_item == 0) return;
     n_item *= hkv;
     // An equal share of the line, but at least a step per warp.  Leaving parts of an item and joining
-    // them takes about 5 us, so items of up to four steps per warp are never cut, for a small total
-    // nor at a border (GB300, bf16: 8 items of 7 steps 8.8 us whole and 14.7 us in two parts; 8 items of
-    // 44 steps 10.9 us in 11 parts, 12.9 in 6 and 14.6 in 3; 128 sequences of 50-200 tokens LATER).
+    // them takes about 5 us, so items of fewer than four steps per warp are never cut, for a small
+    // total nor at a border (GB300, bf16: 8 items of 7 steps 8.8 us whole and 14.7 us in two parts; 8
+    // items of 44 steps 10.9 us in 11 parts, 12.9 in 6 and 14.6 in 3).
     constexpr int SHORT = 4 * W;
     const int per_item = (total + n_item - 1) / n_item;
-    const int quota = max((total + (int)gridDim.x - 1) / (int)gridDim.x, per_item <= SHORT ? per_item : W);
-    long long x64 = (long long)blockIdx.x * quota;
-    if (x64 >= total) return;
-    int x = (int)x64;
-    const int x_end = (int)min((long long)total, x64 + quota);
+    const int quota = max((total + (int)gridDim.x - 1) / (int)gridDim.x, per_item < SHORT ? per_item : W);
+    const Shares sh(total, quota, min(2 * W, quota));
+    const int share = blockIdx.x;
+    if (share >= sh.n) return;
+    int x = sh.start(share);
     int seq;
     {
         int lo = 0, hi = n_seq - 1;  // last sequence with pre[seq] <= x (empty ones before it share the value)
@@ -235,12 +235,21 @@ __global__ void __launch_bounds__(W * 32, 2)
     KeyRange kr{0, 0, 0};
     int known = -1, steps = 0, npair = 0, p0 = 0, p1 = 0, clean0 = 0, n_clean = 0;
 
-    while (x < x_end) {
+    while (x < total) {
         while (pre[seq + 1] <= x) ++seq;  // skips sequences without steps
+        if (seq != known) steps = (pre[seq + 1] - pre[seq]) / hkv;
+        const int head = (x - pre[seq]) / steps;
+        const int item0 = pre[seq] + head * steps;
+        x = item0 + steps;  // the next item
+        if (sh.first(item0, x) > share) break;
+        if (sh.last(item0, x) < share) {
+            known = -1;
+            continue;
+        }
+        const int s0 = sh.begin(share, item0, x), s1 = sh.end(share, item0, x);
         if (seq != known) {
             known = seq;
             si = seq_info(a, seq);
-            steps = (pre[seq + 1] - pre[seq]) / hkv;
             npair = si.n_q * a.group;
             p0 = si.len - si.n_q;
             p1 = si.len - 1;
@@ -249,15 +258,6 @@ __global__ void __launch_bounds__(W * 32, 2)
             clean0 = kr.n_a + max(0, (max(p1 - a.window, -1) + PAGED_STEP) / PAGED_STEP - kr.first_b);
             n_clean = (p0 + 1) / PAGED_STEP - kr.first_b + kr.n_a - clean0;
         }
-        const int head = (x - pre[seq]) / steps;
-        const int item0 = pre[seq] + head * steps;
-        const int s0 = x - item0;
-        // a short item is never cut: it is the CTA's where it starts
-        if (steps <= SHORT && s0 > 0) {
-            x = item0 + steps;
-            continue;
-        }
-        const int s1 = steps <= SHORT ? steps : min(steps, s0 + (x_end - x));
         const int n_real = min(s1, kr.total());  // the empty step of a sequence without keys is none
         auto clean = [&](int i) { return n_clean > 0 && (unsigned)(i - clean0) < (unsigned)n_clean; };
 
@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(W * 32, 2)
             }
         }
         if (!whole_item) {
-            const int first = item0 / quota, n_part = (item0 + steps - 1) / quota - first + 1;
+            const int first = sh.first(item0, item0 + steps), n_part = sh.last(item0, item0 + steps) - first + 1;
             if (tid < npair) {
                 slot[PAGED_MAX_TILE * D + tid] = sM[tid];
                 slot[PAGED_MAX_TILE * (D + 1) + tid] = sL[tid];
@@ -718,7 +718,6 @@ __global__ void __launch_bounds__(W * 32, 2)
             }
         }
         __syncthreads();  // the ring is loaded again for the next segment
-        x += s1 - s0;
     }
 }
 

@@ -39,7 +39,8 @@ constexpr int TMEM_COLS = 512;
 // pages: 7..10 codes to operands, and in the second CTA warps 1 and 6 its blocks' signals
 constexpr int S_WARP = 6;
 constexpr int MAX_CLUSTERS = 76;
-constexpr int MIN_QUOTA = 2;  // blocks of a cluster's stretch at least
+constexpr int MIN_QUOTA = 2;  // blocks of a cluster's share at least
+constexpr int SNAP = 4;       // an item is not cut within so many blocks of its ends
 
 template <bool I4, int D> struct TileCfg {
     static constexpr int NH = D / 64;
@@ -147,18 +148,21 @@ __device__ __forceinline__ ItemRange item_range(const PagedAttn& a, const SeqInf
     return r;
 }
 
-// A cluster's stretch [x, x_end) of the line of blocks, item by item.  Every role walks its own.
+// A cluster's share of the line of blocks, item by item.  Every role walks its own.
 struct Walk {
     const PagedAttn& a;
     const int* pre;
-    int rows2, x, x_end;
-    int seq, head, tp;
+    const Shares sh;
+    const int rows2, share, total;
+    int seq, head, tp, i0;  // i0: first unit of the item
     SeqInfo si;
     ItemRange it;
-    int b0, b1;  // this stretch's blocks of the item
+    int b0, b1;  // this share's blocks of the item
+    bool done;
 
-    __device__ __forceinline__ Walk(const PagedAttn& a_, const int* pre_, int rows2_, int x_, int x_end_)
-        : a(a_), pre(pre_), rows2(rows2_), x(x_), x_end(x_end_) {
+    __device__ __forceinline__ Walk(const PagedAttn& a_, const int* pre_, const Shares& sh_, int rows2_, int share_, int total_)
+        : a(a_), pre(pre_), sh(sh_), rows2(rows2_), share(share_), total(total_) {
+        const int x = sh.start(share);
         int lo = 0, hi = a.pg.n_seq - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -178,25 +182,32 @@ struct Walk {
             rem -= it.n;
             it = item_range(a, si, ++tp, rows2);
         }
-        b0 = rem;
-        b1 = min(it.n, b0 + (x_end - x));
+        i0 = x - rem;
+        done = sh.first(i0, i0 + it.n) > share;
+        while (!done && sh.last(i0, i0 + it.n) < share) next();
+        if (!done) cut();
     }
-    __device__ __forceinline__ bool more() const { return x < x_end; }
+    __device__ __forceinline__ void cut() {
+        b0 = sh.begin(share, i0, i0 + it.n);
+        b1 = sh.end(share, i0, i0 + it.n);
+    }
+    __device__ __forceinline__ bool more() const { return !done; }
     __device__ __forceinline__ void next() {
-        x += b1 - b0;
-        if (x >= x_end) return;
+        i0 += it.n;
+        done = i0 >= total;
+        if (done) return;
         if (++tp == tiles2(si.n_q, rows2)) {
             tp = 0;
             if (++head == a.pg.hkv) {
                 head = 0;
                 do ++seq;
-                while (pre[seq + 1] <= x);
+                while (pre[seq + 1] <= i0);
                 si = seq_info(a, seq);
             }
         }
         it = item_range(a, si, tp, rows2);
-        b0 = 0;
-        b1 = min(it.n, x_end - x);
+        done = sh.first(i0, i0 + it.n) > share;
+        cut();
     }
     __device__ __forceinline__ bool any_seen(int j0, int j1) const {
         return j0 <= it.p_hi && (j0 < a.n_sink || j1 > it.p_lo - a.window);
@@ -205,6 +216,13 @@ struct Walk {
         return j1 <= it.p_hi && (j1 < a.n_sink || j0 > it.p_lo - a.window);
     }
 };
+
+// Blocks of a whole share.
+__device__ __forceinline__ int blocks_of(Walk w) {
+    int n = 0;
+    for (; w.more(); w.next()) n += w.b1 - w.b0;
+    return n;
+}
 
 // A lane's row of 128 scores in TMEM: those of keys it does not see become -inf.  Seen are keys up to
 // `hi` of the block that come after hi - window or before `sink`.
@@ -305,9 +323,8 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
     __syncthreads();
     const int total = pre[n_seq];
     const int quota = max(MIN_QUOTA, (total + n_grp - 1) / n_grp);
-    const long long x64 = (long long)grp * quota;
-    if (x64 >= total) return;  // both CTAs of the cluster
-    const int x_first = (int)x64, x_end = (int)min((long long)total, x64 + quota);
+    const Shares sh(max(total, 1), quota, min(SNAP, quota));
+    if (total == 0 || grp >= sh.n) return;  // both CTAs of the cluster
 
     // Lanes of a tile past its rows read a Q of zeros
     for (int i = threadIdx.x; i < T::QB * QT / 16; i += T::THREADS) reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
@@ -377,16 +394,16 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
         bool ok = true;
         int tl = 0, page = 0, k0 = 0;
         bool need = false, edge = false;
-        Walk w(a, pre, rows2, x_first, x_end);
-        int b = w.b0;
+        Walk w(a, pre, sh, rows2, grp, total);
+        int b = w.more() ? w.b0 : 0;
         auto look = [&]() {  // this lane's box of block b: whether a row sees any of it, and its page
             k0 = w.it.kr.block(b) * TKEYS;
             edge = !w.all_seen(k0, k0 + TKEYS - 1);
             need = mine && w.any_seen(k0 + tok, k0 + tok + rows - 1);
             if (need) page = page_entry(a.pg, w.seq, k0 + tok);  // looked at when the stage is free
         };
-        look();
-        while (ok) {
+        if (w.more()) look();
+        while (ok && w.more()) {
             if (b == w.b0) {
                 const int qb = tl % T::QB;
                 ok = warp_poll(&q_empty[qb], ((tl / T::QB) & 1) ^ 1, &abort_flag);
@@ -469,7 +486,8 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
     } else if (I4 && rank == 1 && (warp == 1 || warp == S_WARP)) {
         // ------------------------------------------------ the second CTA's blocks, signalled to the leader
         bool ok = true;
-        for (int i = warp == 1 ? 0 : 1; ok && i < x_end - x_first; i += 2)
+        const int n_blocks = blocks_of(Walk(a, pre, sh, rows2, grp, total));
+        for (int i = warp == 1 ? 0 : 1; ok && i < n_blocks; i += 2)
             ok = pass_on(&own_full[i % STAGES], &kv_full[i % STAGES], (i / STAGES) & 1, &abort_flag);
         if (!ok) {
             abort_flag = 1;
@@ -480,7 +498,7 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
         uint32_t it = 0;
         bool ok = true;
         int tl = 0;
-        for (Walk w(a, pre, rows2, x_first, x_end); ok && w.more(); w.next(), ++tl) {
+        for (Walk w(a, pre, sh, rows2, grp, total); ok && w.more(); w.next(), ++tl) {
             const int qb = tl % T::QB;
             if (!wait_cl(&q_full[qb], (tl / T::QB) & 1, &abort_flag)) {
                 ok = false;
@@ -519,7 +537,7 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
         uint32_t it = 0;
         bool ok = true;
         int tl = 0;
-        for (Walk w(a, pre, rows2, x_first, x_end); ok && w.more(); w.next(), ++tl) {
+        for (Walk w(a, pre, sh, rows2, grp, total); ok && w.more(); w.next(), ++tl) {
             for (int b = w.b0; b < w.b1; ++b, ++it) {
                 const int sb = it % NSBUF, st = it % STAGES;
                 if (!wait_cl(&p_full[sb], (it / NSBUF) & 1, &abort_flag) ||
@@ -554,7 +572,7 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
         uint32_t it = 0;
         bool ok = true;
         int tl = 0;
-        for (Walk w(a, pre, rows2, x_first, x_end); ok && w.more(); w.next(), ++tl) {
+        for (Walk w(a, pre, sh, rows2, grp, total); ok && w.more(); w.next(), ++tl) {
             const int t_row = w.tp * rows2 + rank * rpt;            // first row of this CTA's tile
             const int rows = min(rpt, w.si.n_q - t_row);            // <= 0: the tile is absent
             const bool valid = r_in < rows * group;
@@ -581,8 +599,9 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                 float corr = 1.f;
                 // as in k_attn_pair: without this block's maximum while its sum stays below 2^50.  What few
                 // blocks need (masks, the maximum) works on TMEM in small loops, so that the path of the
-                // others is short and straight: with masks and maximum on the 128 registers, unrolled, the
-                // rest ran LATER % slower, waiting for instructions.
+                // others is short and straight (masks and maximum on the 128 registers, unrolled, put
+                // some 15 KB of instructions into the middle of it: 468 instead of 457 us for four
+                // prompt pieces of 2048 rows, window 4096, and 220 bytes of spills with 4-bit pages).
                 bool exact = !__all_sync(0xffffffffu, m_used != -INFINITY);
 #pragma unroll 1
                 while (true) {
@@ -672,7 +691,7 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                 continue;
             }
             // ---- part of an item: leave it, and join the parts of these 32 rows when last to arrive
-            const int item0 = w.x - w.b0, g_first = item0 / quota, n_part = (item0 + w.it.n - 1) / quota - g_first + 1;
+            const int g_first = sh.first(w.i0, w.i0 + w.it.n), n_part = sh.last(w.i0, w.i0 + w.it.n) - g_first + 1;
             auto slot = [&](int g, int which) { return a.part + (size_t)((2 * g + which) * 2 + rank) * T::PART; };
             float* mine = slot(grp, w.b0 == 0 ? 1 : 0);
 #pragma unroll
@@ -711,22 +730,22 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                 sum += __ldcg(p + TQ * (D + 1) + r_in) * ex2(__ldcg(p + TQ * D + r_in) - ref);
             }
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            // 32 columns at a time, so that all loads of two parts are on their way together
+            // 64 columns at a time, 16 loads on their way together
 #pragma unroll 1
-            for (int e = 0; e < D; e += 32) {
-                float acc[32];
+            for (int e = 0; e < D; e += 64) {
+                float acc[64];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-#pragma unroll 2
+                for (int i = 0; i < 64; ++i) acc[i] = 0.f;
+#pragma unroll 1
                 for (int k = 0; k < n_part; ++k) {
                     const float* p = slot(g_first + k, k == 0);
                     const float f = ex2(__ldcg(p + TQ * D + r_in) - ref) * inv;
                     const float4* q = reinterpret_cast<const float4*>(p) + (e / 4) * TQ + r_in;
-                    float4 v[8];
+                    float4 v[16];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = __ldcg(q + i * TQ);
+                    for (int i = 0; i < 16; ++i) v[i] = __ldcg(q + i * TQ);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 16; ++i) {
                         acc[4 * i] = fmaf(v[i].x, f, acc[4 * i]);
                         acc[4 * i + 1] = fmaf(v[i].y, f, acc[4 * i + 1]);
                         acc[4 * i + 2] = fmaf(v[i].z, f, acc[4 * i + 2]);
@@ -735,7 +754,7 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                 }
                 if (valid) {
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
+                    for (int v = 0; v < 8; ++v) {
                         uint32_t w4[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) w4[i] = pack_bf16x2(acc[v * 8 + 2 * i], acc[v * 8 + 2 * i + 1]);
@@ -755,7 +774,7 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
         const int k_rows = min(1 << a.pg.shift, 64), v_rows = 1 << a.pg.shift;
         uint32_t it = 0, phases = 0;  // phases: bit st, the parity of edge_full[st]
         bool ok = true;
-        for (Walk w(a, pre, rows2, x_first, x_end); ok && w.more(); w.next())
+        for (Walk w(a, pre, sh, rows2, grp, total); ok && w.more(); w.next())
             for (int b = w.b0; b < w.b1; ++b, ++it) {
                 const int k0 = w.it.kr.block(b) * TKEYS;
                 if (w.all_seen(k0, k0 + TKEYS - 1)) continue;
@@ -793,7 +812,7 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
         // ------------------------------------------------ 4-bit pages to bf16 operands (both CTAs)
         const int t = threadIdx.x - (S_WARP + 1) * 32;  // V: token t of the block; K: half a row of this CTA's token t / 2
         constexpr int RB = T::RB, SB = T::SB, RS = T::RAW_STAGES, G = D / 32;
-        const int n_blocks = x_end - x_first, tk = t >> 1;
+        const int n_blocks = blocks_of(Walk(a, pre, sh, rows2, grp, total)), tk = t >> 1;
         bool ok = true;
         for (int i = 0; i < n_blocks; ++i) {
             const int st = i % STAGES, rs = i % RS;
