@@ -1466,14 +1466,18 @@ int paged_attention(blend_handle* h, const blend_pages* pages, const void* q, in
     const bool i4 = pages->format == BLEND_PAGES_INT4;
     cudaStream_t s = (cudaStream_t)stream;
     // bf16: sequences of few (row, head) pairs and long pieces have a kernel each; which of the two a
-    // sequence is only the device knows, so a call that may hold pieces launches both
-    bool tc = c.dtype == BLEND_BF16 && h->use_tc;
+    // sequence is only the device knows, so a call that may hold both launches both.  One whose row
+    // counts say that every sequence has max_q rows leaves short ones, should the device find any, to
+    // the pieces' kernel (they cost a tile each, where a second launch costs every call 4 us).
+    bool tc = c.dtype == BLEND_BF16 && h->use_tc, pieces = false;
+    const bool uniform = (long long)max_rows == (long long)pages->n_seq * max_q;
+    a.short_pairs = uniform ? 0 : PAGED_MAX_TILE;
     if (tc && (long long)a.max_q * a.group > PAGED_MAX_TILE) {
         const int rc = launch_paged_attn_tile(i4, a, c.head_dim, s);
         if (rc == BLEND_ECUDA) return check_cuda(h, "paged_attention");
-        tc = rc == BLEND_OK;
+        tc = pieces = rc == BLEND_OK;
     }
-    if (tc) launch_paged_attn_split(i4, a, c.head_dim, s);
-    else launch_paged_attn_simt(c.dtype, i4, a, c.head_dim, s);
+    if (!tc) launch_paged_attn_simt(c.dtype, i4, a, c.head_dim, s);
+    else if (!pieces || !uniform) launch_paged_attn_split(i4, a, c.head_dim, s);
     return check_cuda(h, "paged_attention");
 }

@@ -76,6 +76,7 @@ struct PagedAttn {
     const int32_t* q_start;
     const int32_t* kv_len;
     int max_rows, max_q;
+    int short_pairs;  // tile kernel: sequences of up to so many pairs are the split kernel's
     int hq, group;
     int window;  // PAGED_NO_WINDOW: none
     int n_sink;
@@ -186,7 +187,7 @@ void launch_paged_append(int dtype, bool i4, const PageView& pg, int hq, int d, 
 void launch_paged_gather(int dtype, bool i4, const PageView& pg, int d, const int32_t* seq, const int32_t* pos,
                          const int32_t* rot, const int32_t* n_dev, int max_n, void* k_out, void* v_out,
                          const float2* tab, int max_pos, int32_t* err, cudaStream_t s);
-// Sequences of more than 32 (row, head) pairs, bf16 (paged_tile.cu); others are left alone.
+// Sequences of more than a.short_pairs (row, head) pairs, bf16 (paged_tile.cu); others are left alone.
 // Returns BLEND_EUNSUPPORTED, with nothing launched, where no pair of CTAs fits or an operand has no
 // tensor map, and BLEND_ECUDA (the error left to be read) when the launch fails.
 int launch_paged_attn_tile(bool i4, const PagedAttn& a, int d, cudaStream_t s);

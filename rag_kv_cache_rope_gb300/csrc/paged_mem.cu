@@ -96,17 +96,15 @@ __device__ __forceinline__ void group_scales(const float* x0, const float* x1, c
         out[k].y = __shfl_sync(0xffffffffu, y, first + k);
     }
 }
-// Codes n + 8 of eight values with scale `s` (n = round-to-even of the fp32 quotient x / s, -7..7), as
-// two sums of four codes each: `even` for values 0, 2, 4, 6 and `odd` for 1, 3, 5, 7, code k of the four
-// at bit 4 k.  All codes are 8 where the scale is zero or NaN.
+// Codes n + 8 of eight values (n = round-to-even of the fp32 quotient x / s, -7..7), each in the low
+// four bits of c[e], whose other bits below 22 are zero.  All are 8 where the scale is zero or NaN.
 //
 // The quotient has to be the correctly rounded one, since a code is a rounding of it.  With y = 1 / s
 // correctly rounded, q = x y, r = x - q s (exact) and q + r y is x / s correctly rounded (Markstein's
 // theorem, P. Markstein, IBM J. Res. Dev. 34, 1990) as long as nothing leaves the normal range: three
 // operations a value instead of a division.  Scales outside 2^-100..2^100 divide.
-__device__ __forceinline__ void codes8(const float* x, const Scale& sc, uint32_t& even, uint32_t& odd) {
+__device__ __forceinline__ void codes8(const float* x, const Scale& sc, uint32_t (&c)[8]) {
     const float s = sc.s, y = sc.y;
-    uint32_t c[8];  // the code, under a power of two from bit 22 up
     if (s >= 0x1p-100f && s <= 0x1p100f) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -120,28 +118,40 @@ __device__ __forceinline__ void codes8(const float* x, const Scale& sc, uint32_t
         for (int e = 0; e < 8; ++e)
             c[e] = s > 0.f ? (uint32_t)(8 + (int)fminf(fmaxf(rintf(__fdiv_rn(x[e], s)), -7.f), 7.f)) : 8u;
     }
-    // the low 16 bits are the four codes
-    even = c[0] + c[2] * 16u + c[4] * 256u + c[6] * 4096u;
-    odd = c[1] + c[3] * 16u + c[5] * 256u + c[7] * 4096u;
 }
-// K: even codes in the low half of a word, odd ones in the high half.
-__device__ __forceinline__ uint32_t k_word(uint32_t even, uint32_t odd) { return __byte_perm(even, odd, 0x5410); }
-// V: codes 0..3 in the low half, 4..7 in the high half, in order.
-__device__ __forceinline__ uint32_t v_word(uint32_t even, uint32_t odd) {
-    // even: c0 c2 c4 c6, odd: c1 c3 c5 c7 from bit 0 up; spread each to every other nibble
-    uint32_t e = even & 0xffffu, o = odd & 0xffffu;
-    e = (e | (e << 8)) & 0x00FF00FFu;
-    o = (o | (o << 8)) & 0x00FF00FFu;
-    e = (e | (e << 4)) & 0x0F0F0F0Fu;
-    o = (o | (o << 4)) & 0x0F0F0F0Fu;
-    return e | (o << 4);
+// Four codes to 16 bits, in the low half (what the codes carry from bit 22 up stays above).
+__device__ __forceinline__ uint32_t four(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return a + b * 16u + c * 256u + d * 4096u;
 }
-// The codes of a K word (see k_word) or V word times the scale.
-template <bool KROW> __device__ __forceinline__ void values8(uint32_t w, float s, float* x) {
+// K: even codes in the low half of a word, odd ones in the high half.  V: in order.
+__device__ __forceinline__ uint32_t k_word(const uint32_t (&c)[8]) {
+    return __byte_perm(four(c[0], c[2], c[4], c[6]), four(c[1], c[3], c[5], c[7]), 0x5410);
+}
+__device__ __forceinline__ uint32_t v_word(const uint32_t (&c)[8]) {
+    return __byte_perm(four(c[0], c[1], c[2], c[3]), four(c[4], c[5], c[6], c[7]), 0x5410);
+}
+// A K word's values n s: a pair of codes is (n - 8) / 64 in bf16, exactly (code_pair).
+__device__ __forceinline__ void k_values(uint32_t w, float s, float* x) {
+    const float unit = __fmul_rn(s, CODE_UNIT);  // exact but for scales past 2^121
+    const uint32_t p[4] = {code_pair<false>(w), code_pair<true>(w), code_pair<false>(w >> 8), code_pair<true>(w >> 8)};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t code = (w >> (KROW ? k4_bit(e) : 4 * e)) & 15u;
-        x[e] = __fmul_rn(__uint_as_float(0x4B000000u | code) - 8388616.f, s);  // 2^23 + code, exact
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __fmul_rn(__uint_as_float(p[i] << 16), unit);
+        x[2 * i + 1] = __fmul_rn(__uint_as_float(p[i] & 0xffff0000u), unit);
+    }
+}
+// A V word's values: codes 0, 1 and 2, 3 of a half are pairs once the half is repeated 12 bits up.
+__device__ __forceinline__ void v_values(uint32_t w, float s, float* x) {
+    const float unit = __fmul_rn(s, CODE_UNIT);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t c = h ? w >> 16 : w & 0xffffu, y = c | (c << 12);
+        const uint32_t p[2] = {code_pair<false>(y), code_pair<false>(y >> 8)};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            x[4 * h + 2 * i] = __fmul_rn(__uint_as_float(p[i] << 16), unit);
+            x[4 * h + 2 * i + 1] = __fmul_rn(__uint_as_float(p[i] & 0xffff0000u), unit);
+        }
     }
 }
 
@@ -239,13 +249,15 @@ __global__ void __launch_bounds__(MEM_THREADS, I4 || sizeof(T) == 4 ? 4 : 5)
         // all lanes take part in the shuffles
         Scale sc[4];
         group_scales(a, b, va, vb, sc);
-        uint32_t e0, o0, e1, o1;
-        codes8(a, sc[0], e0, o0);
-        codes8(b, sc[1], e1, o1);
-        uint32_t k0 = k_word(e0, o0), k1 = k_word(e1, o1);  // words (c, g) and (c, g + D / 64)
-        codes8(va, sc[2], e0, o0);
-        codes8(vb, sc[3], e1, o1);
-        const uint32_t w0 = v_word(e0, o0), w1 = v_word(e1, o1);  // halves (g, 2c), (g, 2c + 1) and those of g + D / 64
+        uint32_t c8[8];
+        codes8(a, sc[0], c8);
+        const uint32_t k0 = k_word(c8);  // word (c, g)
+        codes8(b, sc[1], c8);
+        const uint32_t k1 = k_word(c8);  // and (c, g + D / 64)
+        codes8(va, sc[2], c8);
+        const uint32_t w0 = v_word(c8);  // halves (g, 2c), (g, 2c + 1)
+        codes8(vb, sc[3], c8);
+        const uint32_t w1 = v_word(c8);  // and those of g + D / 64
         uint32_t v0 = __byte_perm(w0, w1, 0x5410), v1 = __byte_perm(w0, w1, 0x7632);  // by half: 2c, 2c + 1
         const uint32_t ks = sc[0].bits | sc[1].bits << 16, vs = sc[2].bits | sc[3].bits << 16;
         uint2 kw, vw, sk, sv;
@@ -363,12 +375,12 @@ __global__ void __launch_bounds__(MEM_THREADS, sizeof(T) == 4 ? 4 : 5)
             sb = __uint_as_float(sv.x & 0xffff0000u);
         }
         if (!r.ok) return;
-        values8<false>(w0, sa, a);
-        values8<false>(w1, sb, b);
+        v_values(w0, sa, a);
+        v_values(w1, sb, b);
         store8(v_out + out + i0, a);
         store8(v_out + out + i0 + HALF, b);
-        values8<true>(k0, ka, a);
-        values8<true>(k1, kb, b);
+        k_values(k0, ka, a);
+        k_values(k1, kb, b);
     }
     rotate8(a, b, r.rot, i0, HALF, tab);
     store8(k_out + out + i0, a);

@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
     for (int s = warp; s < n_seq; s += WARPS) {
         const SeqInfo si = seq_info(a, s);
         int n = 0;
-        if (si.n_q * group > PAGED_MAX_TILE)  // shorter ones are the split kernel's
+        if (si.n_q * group > a.short_pairs)  // the others are the split kernel's
             for (int tp = lane; tp < tiles2(si.n_q, rows2); tp += 32) n += item_range(a, si, tp, rows2).n;
         n = __reduce_add_sync(0xffffffffu, n);
         if (lane == 0) pre[s + 1] = n * a.pg.hkv;

@@ -283,6 +283,26 @@ def test_attention_parts_of_every_tile_size(fmt):
 
 
 @pytest.mark.parametrize("fmt", ["model", "int4"])
+def test_short_sequences_in_a_call_sized_for_pieces(fmt):
+    """Row counts that announce a full batch of pieces, and a device that holds shorter ones, or none."""
+    h = handle("bf16", 8, 2, 128)
+    lens = [300, 70, 0, 5, 1000]
+    c = filled("bf16", fmt, 2, 128, 16, lens, 109)
+    q = torch.randn(5 * 40, 8, 128, device="cuda").bfloat16()
+    for n_q in ([40, 40, 0, 5, 1], [1, 1, 0, 1, 1], [0, 0, 0, 0, 40], [0, 0, 0, 0, 0], [40, 8, 1, 9, 40]):
+        start = np.concatenate([[0], np.cumsum(n_q)])
+        out = attend(h, c, q, i32(start), lens, 40)
+        b.blend_device_status(h)
+        assert (f64(out)[start[-1]:] == 3.0).all()
+        for s in range(5):
+            if n_q[s]:
+                want, mag, lin = P.attention(f64(q[start[s]:start[s + 1]]), c.k[s], c.v[s], lens[s], 0, 0)
+                lim = attention_bound("bf16", fmt, want, mag, lin, lens[s], True)
+                got = f64(out[start[s]:start[s + 1]]).reshape(n_q[s], 8, 128)
+                assert (np.abs(got - want) <= lim).all(), (n_q, s)
+
+
+@pytest.mark.parametrize("fmt", ["model", "int4"])
 def test_queries_and_keys_of_extreme_size(fmt):
     """Scores of ordinary size from huge queries and tiny keys, and the other way round."""
     for up in (2.0 ** 60, 2.0 ** -60):
