@@ -155,36 +155,32 @@ __device__ __forceinline__ void v_values(uint32_t w, float s, float* x) {
     }
 }
 
+// Where row i goes, in the three steps of its loads (so that two rows' loads can be on their way
+// together): its entries; the page of its token; the place.  A negative sequence marks a row to
+// leave alone, anything out of range is reported and left alone as well.
 struct RowAt {
     bool ok;
-    int seq, pos, rot;
-    long long at;  // pool row of head 0
+    int seq, pos, rot, page;
+    __device__ __forceinline__ void read(const int32_t* seq_, const int32_t* pos_, const int32_t* rot_, bool by_pos, long long i, bool in) {
+        seq = in ? __ldg(seq_ + i) : -1;
+        pos = in ? __ldg(pos_ + i) : 0;
+        rot = rot_ ? (in ? __ldg(rot_ + i) : 0) : by_pos ? pos : 0;
+    }
+    __device__ __forceinline__ void find(const PageView& pg, int max_pos, bool live, int32_t* err) {
+        ok = live && seq >= 0;
+        const bool bad = seq >= pg.n_seq || pos < 0 || pos >= (pg.max_pages << pg.shift) || rot <= -max_pos || rot >= max_pos;
+        if (ok && bad) set_error(err, BLEND_EDEVICE);
+        ok = ok && !bad;
+        page = ok ? page_entry(pg, seq, pos) : 0;
+    }
+    __device__ __forceinline__ long long place(const PageView& pg, int head, int32_t* err) {  // its pool row
+        if ((unsigned)page >= (unsigned)pg.n_pages) {
+            set_error(err, BLEND_EDEVICE);
+            ok = false;
+        }
+        return ok ? page_row(pg, page, head, pos & ((1 << pg.shift) - 1)) : 0;
+    }
 };
-// Place and rotation of row i; a negative sequence marks a row to leave alone, anything out
-// of range is reported and left alone as well.
-__device__ __forceinline__ RowAt row_at(const PageView& pg, const int32_t* seq, const int32_t* pos, const int32_t* rot,
-                                        bool by_pos, int i, int max_pos, int32_t* err) {
-    RowAt r;
-    r.seq = __ldg(seq + i);
-    r.pos = __ldg(pos + i);
-    r.rot = rot ? __ldg(rot + i) : by_pos ? r.pos : 0;
-    r.ok = r.seq >= 0;
-    r.at = 0;
-    if (!r.ok) return r;
-    if (r.seq >= pg.n_seq || r.pos < 0 || r.pos >= (pg.max_pages << pg.shift) || r.rot <= -max_pos || r.rot >= max_pos) {
-        set_error(err, BLEND_EDEVICE);
-        r.ok = false;
-        return r;
-    }
-    const int page = __ldg(pg.table + (long long)r.seq * pg.max_pages + (r.pos >> pg.shift));
-    if ((unsigned)page >= (unsigned)pg.n_pages) {
-        set_error(err, BLEND_EDEVICE);
-        r.ok = false;
-        return r;
-    }
-    r.at = page_row(pg, page, 0, r.pos & ((1 << pg.shift) - 1));
-    return r;
-}
 __device__ __forceinline__ int checked_count(const int32_t* n_dev, int max_n, int32_t* err) {
     const int n = __ldg(n_dev);
     if (n < 0 || n > max_n) {
@@ -196,22 +192,23 @@ __device__ __forceinline__ int checked_count(const int32_t* n_dev, int max_n, in
 
 // Slots of a row: hkv kv heads (key and value), then (with q) hq query heads.
 template <typename T, bool I4, int D>
-__global__ void __launch_bounds__(MEM_THREADS, I4 || sizeof(T) == 4 ? 4 : 5)
+__global__ void __launch_bounds__(MEM_THREADS, 4)
     k_paged_append(PageView pg, int hq, const T* __restrict__ k_new, long long ld_k, const T* __restrict__ v_new,
                    long long ld_v, const T* q, long long ld_q, T* q_out, const int32_t* __restrict__ seq,
                    const int32_t* __restrict__ pos, const int32_t* __restrict__ rot, const int32_t* __restrict__ n_dev,
                    int max_n, long long row0, const float2* __restrict__ tab, int max_pos, int32_t* err) {
     constexpr int TPH = D / 16, HALF = D / 2;
-    const int n = checked_count(n_dev, max_n, err);
     const int slots = pg.hkv + (q ? hq : 0);
     const unsigned unit = (blockIdx.x * MEM_THREADS + threadIdx.x) / TPH;  // below 2^32 / TPH (launcher)
     const int t = threadIdx.x % TPH, i0 = t * 8;
     const long long row = row0 + unit / (unsigned)slots;
     const int slot = (int)(unit % (unsigned)slots);
-    const bool live = row < n, is_kv = slot < pg.hkv;
+    const bool in = row < max_n, is_kv = slot < pg.hkv;
     const int head = is_kv ? slot : slot - pg.hkv;
+    RowAt r;
+    r.read(seq, pos, rot, true, row, in);
     Raw8<T> ra{}, rb{}, rva{}, rvb{};
-    if (live) {
+    if (in) {  // (without waiting for the count)
         const T* src = is_kv ? k_new + row * ld_k + head * D : q + row * ld_q + head * D;
         ra.load(src + i0);
         rb.load(src + i0 + HALF);
@@ -221,8 +218,8 @@ __global__ void __launch_bounds__(MEM_THREADS, I4 || sizeof(T) == 4 ? 4 : 5)
             rvb.load(sv + i0 + HALF);
         }
     }
-    RowAt r{false, 0, 0, 0, 0};
-    if (live) r = row_at(pg, seq, pos, rot, true, (int)row, max_pos, err);
+    r.find(pg, max_pos, row < checked_count(n_dev, max_n, err), err);
+    const long long at = r.place(pg, head, err);
     float a[8], b[8];
     ra.get(a);
     rb.get(b);
@@ -233,7 +230,6 @@ __global__ void __launch_bounds__(MEM_THREADS, I4 || sizeof(T) == 4 ? 4 : 5)
         store8(dst + i0 + HALF, b);
     }
     const bool store = r.ok && is_kv;
-    const long long at = r.at + ((long long)head << pg.shift);
     if constexpr (!I4) {
         if (!store) return;
         T* dk = reinterpret_cast<T*>(const_cast<char*>(pg.k)) + at * D;
@@ -299,92 +295,120 @@ __global__ void __launch_bounds__(MEM_THREADS, I4 || sizeof(T) == 4 ? 4 : 5)
     }
 }
 
-template <typename T, bool I4, int D>
-__global__ void __launch_bounds__(MEM_THREADS, sizeof(T) == 4 ? 4 : 5)
+// U rows of a thread, whose loads are on their way together.
+template <typename T, bool I4, int D, int U>
+__global__ void __launch_bounds__(MEM_THREADS, !I4 && U == 2 ? 3 : 4)
     k_paged_gather(PageView pg, const int32_t* __restrict__ seq, const int32_t* __restrict__ pos,
                    const int32_t* __restrict__ rot, const int32_t* __restrict__ n_dev, int max_n,
                    long long row0, T* __restrict__ k_out, T* __restrict__ v_out, const float2* __restrict__ tab,
                    int max_pos, int32_t* err) {
     constexpr int TPH = D / 16, HALF = D / 2;
-    const int n = checked_count(n_dev, max_n, err);
-    const unsigned unit = (blockIdx.x * MEM_THREADS + threadIdx.x) / TPH;
     const int t = threadIdx.x % TPH, i0 = t * 8;
-    const long long row = row0 + unit / (unsigned)pg.hkv;
-    const int head = (int)(unit % (unsigned)pg.hkv);
-    RowAt r{false, 0, 0, 0, 0};
-    if (row < n) r = row_at(pg, seq, pos, rot, false, (int)row, max_pos, err);
-    if (!I4 && !r.ok) return;
-    const long long at = r.at + ((long long)head << pg.shift);
-    const long long out = (row * pg.hkv + head) * D;
-    float a[8], b[8];
+    RowAt r[U];
+    long long at[U], row[U];
+    int head[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const unsigned unit = (blockIdx.x * U + u) * (MEM_THREADS / TPH) + threadIdx.x / TPH;  // below 2^31 (launcher)
+        row[u] = row0 + unit / (unsigned)pg.hkv;
+        head[u] = (int)(unit % (unsigned)pg.hkv);
+        r[u].read(seq, pos, rot, false, row[u], row[u] < max_n);
+    }
+    const int n = checked_count(n_dev, max_n, err);
+#pragma unroll
+    for (int u = 0; u < U; ++u) r[u].find(pg, max_pos, row[u] < n, err);
+#pragma unroll
+    for (int u = 0; u < U; ++u) at[u] = r[u].place(pg, head[u], err);
     if constexpr (!I4) {
-        const T* sk = reinterpret_cast<const T*>(pg.k) + at * D;
-        const T* sv = reinterpret_cast<const T*>(pg.v) + at * D;
-        Raw8<T> ra, rb, rva, rvb;
-        ra.load(sk + i0);
-        rb.load(sk + i0 + HALF);
-        rva.load(sv + i0);
-        rvb.load(sv + i0 + HALF);
-        ra.get(a);
-        rb.get(b);
-        rva.store(v_out + out + i0);
-        rvb.store(v_out + out + i0 + HALF);
+        Raw8<T> ra[U], rb[U], rva[U], rvb[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (r[u].ok) {
+                const T* sk = reinterpret_cast<const T*>(pg.k) + at[u] * D;
+                const T* sv = reinterpret_cast<const T*>(pg.v) + at[u] * D;
+                ra[u].load(sk + i0);
+                rb[u].load(sk + i0 + HALF);
+                rva[u].load(sv + i0);
+                rvb[u].load(sv + i0 + HALF);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (r[u].ok) {
+                const long long out = (row[u] * pg.hkv + head[u]) * D;
+                rva[u].store(v_out + out + i0);
+                rvb[u].store(v_out + out + i0 + HALF);
+                float a[8], b[8];
+                ra[u].get(a);
+                rb[u].get(b);
+                rotate8(a, b, r[u].rot, i0, HALF, tab);
+                store8(k_out + out + i0, a);
+                store8(k_out + out + i0 + HALF, b);
+            }
     } else {
         // the layout and the exchange of k_paged_append, backwards
-        uint2 kw = make_uint2(0, 0), vw = kw, sk = kw, sv = kw;
         const int c = t & 3;
-        if (r.ok) {
-            const char* pk = pg.k + at * (D / 2);
-            const char* pv = pg.v + at * (D / 2);
-            const char* ps = pg.ks + at * (D / 16);
-            const char* pt = pg.vs + at * (D / 16);
-            kw = *reinterpret_cast<const uint2*>(pk + (D == 128 ? c * 16 + (t >> 2) * 8 : c * 8));
-            vw = *reinterpret_cast<const uint2*>(pv + (D == 128 ? (2 * c + (t >> 2)) * 8 : c * 8));
-            if constexpr (D == 128) {
-                sk = *reinterpret_cast<const uint2*>(ps);
-                sv = *reinterpret_cast<const uint2*>(pt);
-            } else {
-                sk.x = *reinterpret_cast<const uint32_t*>(ps);
-                sv.x = *reinterpret_cast<const uint32_t*>(pt);
+        uint2 kw[U], vw[U], sk[U], sv[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            kw[u] = vw[u] = sk[u] = sv[u] = make_uint2(0, 0);
+            if (r[u].ok) {
+                const char* pk = pg.k + at[u] * (D / 2);
+                const char* pv = pg.v + at[u] * (D / 2);
+                const char* ps = pg.ks + at[u] * (D / 16);
+                const char* pt = pg.vs + at[u] * (D / 16);
+                kw[u] = *reinterpret_cast<const uint2*>(pk + (D == 128 ? c * 16 + (t >> 2) * 8 : c * 8));
+                vw[u] = *reinterpret_cast<const uint2*>(pv + (D == 128 ? (2 * c + (t >> 2)) * 8 : c * 8));
+                if constexpr (D == 128) {
+                    sk[u] = *reinterpret_cast<const uint2*>(ps);
+                    sv[u] = *reinterpret_cast<const uint2*>(pt);
+                } else {
+                    sk[u].x = *reinterpret_cast<const uint32_t*>(ps);
+                    sv[u].x = *reinterpret_cast<const uint32_t*>(pt);
+                }
             }
         }
-        uint32_t k0, k1, w0, w1;
-        float ka, kb, sa, sb;
-        if constexpr (D == 128) {
-            const bool up = t >= 4;
-            const uint32_t ko = __shfl_xor_sync(0xffffffffu, up ? kw.x : kw.y, 4);
-            k0 = up ? ko : kw.x;
-            k1 = up ? kw.y : ko;
-            const uint32_t g02 = __byte_perm(vw.x, vw.y, 0x5410), g13 = __byte_perm(vw.x, vw.y, 0x7632);
-            const uint32_t vo = __shfl_xor_sync(0xffffffffu, up ? g02 : g13, 4);
-            const uint32_t v0 = up ? vo : g02, v1 = up ? g13 : vo;  // this thread's groups by half: 2c, 2c + 1
-            w0 = __byte_perm(v0, v1, 0x5410);
-            w1 = __byte_perm(v0, v1, 0x7632);
-            ka = __uint_as_float(up ? sk.x & 0xffff0000u : sk.x << 16);
-            kb = __uint_as_float(up ? sk.y & 0xffff0000u : sk.y << 16);
-            sa = __uint_as_float(up ? sv.x & 0xffff0000u : sv.x << 16);
-            sb = __uint_as_float(up ? sv.y & 0xffff0000u : sv.y << 16);
-        } else {
-            k0 = kw.x;
-            k1 = kw.y;
-            w0 = __byte_perm(vw.x, vw.y, 0x5410);
-            w1 = __byte_perm(vw.x, vw.y, 0x7632);
-            ka = __uint_as_float(sk.x << 16);
-            kb = __uint_as_float(sk.x & 0xffff0000u);
-            sa = __uint_as_float(sv.x << 16);
-            sb = __uint_as_float(sv.x & 0xffff0000u);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            uint32_t k0, k1, w0, w1;
+            float ka, kb, sa, sb;
+            if constexpr (D == 128) {
+                const bool up = t >= 4;
+                const uint32_t ko = __shfl_xor_sync(0xffffffffu, up ? kw[u].x : kw[u].y, 4);
+                k0 = up ? ko : kw[u].x;
+                k1 = up ? kw[u].y : ko;
+                const uint32_t g02 = __byte_perm(vw[u].x, vw[u].y, 0x5410), g13 = __byte_perm(vw[u].x, vw[u].y, 0x7632);
+                const uint32_t vo = __shfl_xor_sync(0xffffffffu, up ? g02 : g13, 4);
+                const uint32_t v0 = up ? vo : g02, v1 = up ? g13 : vo;  // this thread's groups by half: 2c, 2c + 1
+                w0 = __byte_perm(v0, v1, 0x5410);
+                w1 = __byte_perm(v0, v1, 0x7632);
+                ka = __uint_as_float(up ? sk[u].x & 0xffff0000u : sk[u].x << 16);
+                kb = __uint_as_float(up ? sk[u].y & 0xffff0000u : sk[u].y << 16);
+                sa = __uint_as_float(up ? sv[u].x & 0xffff0000u : sv[u].x << 16);
+                sb = __uint_as_float(up ? sv[u].y & 0xffff0000u : sv[u].y << 16);
+            } else {
+                k0 = kw[u].x;
+                k1 = kw[u].y;
+                w0 = __byte_perm(vw[u].x, vw[u].y, 0x5410);
+                w1 = __byte_perm(vw[u].x, vw[u].y, 0x7632);
+                ka = __uint_as_float(sk[u].x << 16);
+                kb = __uint_as_float(sk[u].x & 0xffff0000u);
+                sa = __uint_as_float(sv[u].x << 16);
+                sb = __uint_as_float(sv[u].x & 0xffff0000u);
+            }
+            if (!r[u].ok) continue;
+            const long long out = (row[u] * pg.hkv + head[u]) * D;
+            float a[8], b[8];
+            v_values(w0, sa, a);
+            v_values(w1, sb, b);
+            store8(v_out + out + i0, a);
+            store8(v_out + out + i0 + HALF, b);
+            k_values(k0, ka, a);
+            k_values(k1, kb, b);
+            rotate8(a, b, r[u].rot, i0, HALF, tab);
+            store8(k_out + out + i0, a);
+            store8(k_out + out + i0 + HALF, b);
         }
-        if (!r.ok) return;
-        v_values(w0, sa, a);
-        v_values(w1, sb, b);
-        store8(v_out + out + i0, a);
-        store8(v_out + out + i0 + HALF, b);
-        k_values(k0, ka, a);
-        k_values(k1, kb, b);
     }
-    rotate8(a, b, r.rot, i0, HALF, tab);
-    store8(k_out + out + i0, a);
-    store8(k_out + out + i0 + HALF, b);
 }
 
 template <typename T, bool I4, int D>
@@ -407,8 +431,14 @@ void gather_d(const PageView& pg, const int32_t* seq, const int32_t* pos, const 
     const long long most = (1ll << 31) / (pg.hkv * (D / 16));
     for (long long row0 = 0; row0 < max_n; row0 += most) {
         const long long threads = (max_n - row0 < most ? max_n - row0 : most) * pg.hkv * (D / 16);
-        k_paged_gather<T, I4, D><<<(unsigned)((threads + MEM_THREADS - 1) / MEM_THREADS), MEM_THREADS, 0, s>>>(
-            pg, seq, pos, rot, n_dev, max_n, row0, (T*)k_out, (T*)v_out, tab, max_pos, err);
+        const long long blocks = (threads + MEM_THREADS - 1) / MEM_THREADS;
+        // two rows a thread once that still fills four CTAs on each of 152 SMs
+        if (blocks >= 2 * 608)
+            k_paged_gather<T, I4, D, 2><<<(unsigned)((blocks + 1) / 2), MEM_THREADS, 0, s>>>(
+                pg, seq, pos, rot, n_dev, max_n, row0, (T*)k_out, (T*)v_out, tab, max_pos, err);
+        else
+            k_paged_gather<T, I4, D, 1><<<(unsigned)blocks, MEM_THREADS, 0, s>>>(
+                pg, seq, pos, rot, n_dev, max_n, row0, (T*)k_out, (T*)v_out, tab, max_pos, err);
         note_launch(1);
     }
 }
