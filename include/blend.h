@@ -469,14 +469,15 @@ typedef struct {
  * are, bit for bit).  k_new, v_new: device [max_n][hkv][d] of the model dtype with ld_k, ld_v
  * elements between rows, so slices of a fused projection need no copy.  With q (device
  * [max_n][hq][d], ld_q between rows) the query heads are rotated alike into q_out (device
- * [max_n][hq][d], rows adjacent; q itself when ld_q = hq * d); NULL leaves both out.  Rotations
- * are fp32, each product and sum rounded by itself.
+ * [max_n][hq][d], rows adjacent; q itself when ld_q = hq * d, else apart from the inputs' rows);
+ * NULL leaves both out.  Rotations are fp32, each product and sum rounded by itself.
  * A row with seq[i] < 0 is left alone (padding).  Rows of one call must name distinct tokens:
  * where two name the same one, its row may mix theirs (no other token is touched).
  * Device-side checks (BLEND_EDEVICE from blend_device_status): a count outside 0..max_n is
  * clamped; a row whose sequence, token, rotation or page index is out of range is left alone.
  * Errors: BLEND_EINVAL for NULL or not 16-byte aligned tensors, row strides that are below a
- * row or no multiple of 16 bytes, or a bad blend_pages (nothing is launched). */
+ * row or no multiple of 16 bytes, q_out over k_new, v_new or other rows of q, or a bad blend_pages
+ * (nothing is launched). */
 int paged_append(blend_handle* h, const blend_pages* pages, const void* k_new, int64_t ld_k, const void* v_new,
                  int64_t ld_v, const void* q, int64_t ld_q, void* q_out, const int32_t* seq, const int32_t* pos,
                  const int32_t* rot, const int32_t* n, int32_t max_n, void* stream);
@@ -501,14 +502,16 @@ int paged_gather(blend_handle* h, const blend_pages* pages, const int32_t* seq, 
  * max_q (host): most query rows of one sequence; it picks the kernels (single tokens and few
  * rows: the keys split over all SMs; long pieces: tiles of 128 pairs on the tensor cores).
  * Keys and values of tokens no row of the call sees are not used: slots past a length may hold
- * anything, and table entries of pages without a token that some row sees are not read.  A NaN or infinity in a token that some rows see reaches them, and may reach other
- * rows of the same sequence in the call.  The result does not depend on timing.
+ * anything, and table entries of pages without a token that some row sees are not read.  A NaN or
+ * infinity in a token that some rows see reaches them, and may reach other rows of the same
+ * sequence in the call.  bf16 queries over 4-bit pages may be as large as 2^115 (beyond: NaN).
+ * The result does not depend on timing.
  * Uses the handle's workspace: calls on one handle must not overlap, replays of captured ones
  * included.  Device-side checks (BLEND_EDEVICE): a sequence with row bounds outside 0..max_rows or
  * descending, more than max_q rows, or a length outside its table is skipped; a page index
  * outside the pool is read as page 0.
  * Errors: BLEND_EINVAL for NULL or unaligned tensors, bad strides, negative sizes, window or
- * n_sink, max_q < 1 with rows, out equal to q, or a bad blend_pages (nothing is launched). */
+ * n_sink, max_q < 1 with rows, out over q, or a bad blend_pages (nothing is launched). */
 int paged_attention(blend_handle* h, const blend_pages* pages, const void* q, int64_t ld_q, const int32_t* q_start,
                     const int32_t* kv_len, int32_t max_rows, int32_t max_q, int32_t window, int32_t n_sink,
                     void* out, void* stream);

@@ -1385,6 +1385,13 @@ bool row_stride_ok(const blend_handle* h, long long ld, int heads) {
     return ld >= (long long)heads * h->cfg.head_dim && ld % (long long)(16 / elem_size(h->cfg.dtype)) == 0 &&
            ld <= (1ll << 32);
 }
+// Bytes from the first of `rows` rows to the end of the last; two such ranges that meet.
+long long rows_span(const blend_handle* h, long long rows, long long ld, int heads) {
+    return ((rows - 1) * ld + (long long)heads * h->cfg.head_dim) * (long long)elem_size(h->cfg.dtype);
+}
+bool overlap(const void* a, long long na, const void* b, long long nb) {
+    return (uintptr_t)a < (uintptr_t)b + (uintptr_t)nb && (uintptr_t)b < (uintptr_t)a + (uintptr_t)na;
+}
 }  // namespace
 
 int paged_append(blend_handle* h, const blend_pages* pages, const void* k_new, int64_t ld_k, const void* v_new,
@@ -1406,6 +1413,13 @@ int paged_append(blend_handle* h, const blend_pages* pages, const void* k_new, i
         return fail(h, BLEND_EINVAL, "q_out may be q only where q's rows are adjacent");
     if (max_n < 0 || max_n > (1 << 24)) return fail(h, BLEND_EINVAL, "max_n=%d outside 0..2^24", max_n);
     if (max_n == 0) return BLEND_OK;
+    if (q) {
+        const long long span = rows_span(h, max_n, (long long)c.n_q_heads * c.head_dim, c.n_q_heads);
+        if (overlap(q_out, span, k_new, rows_span(h, max_n, ld_k, c.n_kv_heads)) ||
+            overlap(q_out, span, v_new, rows_span(h, max_n, ld_v, c.n_kv_heads)) ||
+            (q != q_out && overlap(q_out, span, q, rows_span(h, max_n, ld_q, c.n_q_heads))))
+            return fail(h, BLEND_EINVAL, "q_out overlaps an input");
+    }
     launch_paged_append(c.dtype, pages->format == BLEND_PAGES_INT4, pv, c.n_q_heads, c.head_dim, k_new, ld_k, v_new,
                         ld_v, q, ld_q, q_out, seq, pos, rot, n, max_n, h->rope, c.max_pos, h->err, (cudaStream_t)stream);
     return check_cuda(h, "paged_append");
@@ -1447,6 +1461,9 @@ int paged_attention(blend_handle* h, const blend_pages* pages, const void* q, in
         return fail(h, BLEND_EINVAL, "table too large: its tokens (in steps of 16 per sequence and kv head, in blocks of "
                     "128 per tile and kv head) must stay below 2^31");
     if (max_rows == 0) return BLEND_OK;
+    if (overlap(out, rows_span(h, max_rows, (long long)c.n_q_heads * c.head_dim, c.n_q_heads), q,
+                rows_span(h, max_rows, ld_q, c.n_q_heads)))
+        return fail(h, BLEND_EINVAL, "out overlaps q");
     a.q = q;
     a.ld_q = ld_q;
     a.q_start = q_start;

@@ -411,12 +411,20 @@ __global__ void __launch_bounds__(MEM_THREADS, !I4 && U == 2 ? 3 : 4)
     }
 }
 
+// Rows of one launch: its threads count in 32 bits, and it ends with a whole pair of CTAs, so that no
+// thread of it reaches a row of the next one (query heads may be rotated in place, and once only).
+long long rows_of_launch(int slots, int d) {
+    constexpr long long step = 2 * MEM_THREADS;
+    const long long n = (1ll << 31) / ((long long)slots * (d / 16)) / step;
+    return (n > 1 ? n : 1) * step;
+}
+
 template <typename T, bool I4, int D>
 void append_d(const PageView& pg, int hq, const void* k_new, long long ld_k, const void* v_new, long long ld_v,
               const void* q, long long ld_q, void* q_out, const int32_t* seq, const int32_t* pos, const int32_t* rot,
               const int32_t* n_dev, int max_n, const float2* tab, int max_pos, int32_t* err, cudaStream_t s) {
     const int slots = pg.hkv + (q ? hq : 0);
-    const long long most = (1ll << 31) / (slots * (D / 16));  // rows of a launch: its threads count in 32 bits
+    const long long most = rows_of_launch(slots, D);
     for (long long row0 = 0; row0 < max_n; row0 += most) {
         const long long threads = (max_n - row0 < most ? max_n - row0 : most) * slots * (D / 16);
         k_paged_append<T, I4, D><<<(unsigned)((threads + MEM_THREADS - 1) / MEM_THREADS), MEM_THREADS, 0, s>>>(
@@ -428,7 +436,7 @@ void append_d(const PageView& pg, int hq, const void* k_new, long long ld_k, con
 template <typename T, bool I4, int D>
 void gather_d(const PageView& pg, const int32_t* seq, const int32_t* pos, const int32_t* rot, const int32_t* n_dev,
               int max_n, void* k_out, void* v_out, const float2* tab, int max_pos, int32_t* err, cudaStream_t s) {
-    const long long most = (1ll << 31) / (pg.hkv * (D / 16));
+    const long long most = rows_of_launch(pg.hkv, D);
     for (long long row0 = 0; row0 < max_n; row0 += most) {
         const long long threads = (max_n - row0 < most ? max_n - row0 : most) * pg.hkv * (D / 16);
         const long long blocks = (threads + MEM_THREADS - 1) / MEM_THREADS;

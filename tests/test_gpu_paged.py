@@ -445,6 +445,39 @@ def test_pool_past_32_bit_offsets(fmt):
         assert (np.abs(f64(out).reshape(rows, hq, d) - want) <= lim).all()
 
 
+def test_append_rows_that_take_two_launches():
+    """More rows than the threads of one launch, queries in place: rows on both sides of the border are
+    rotated once.  All rows but a few are padding."""
+    hq, hkv, d = 32, 2, 64
+    most = (1 << 31) // ((hq + hkv) * (d // 16))
+    n = most + 700
+    need = n * d * (hq + 2 * hkv) * 2 + 3 * n * 4
+    if torch.cuda.mem_get_info()[0] < need + (20 << 30):
+        pytest.skip("needs some 95 GB of free memory")
+    h = handle("bf16", hq, hkv, d)
+    c = filled("bf16", "model", hkv, d, 16, [64], 109)
+    q = torch.empty(n, hq, d, dtype=torch.bfloat16, device="cuda")
+    kv = torch.empty(2, n, hkv, d, dtype=torch.bfloat16, device="cuda")
+    rows = torch.tensor([0, most - 512, most - 1, most, most + 1, n - 1] + [most // 512 * 512 + i for i in range(-1, 40)])
+    q[rows.cuda()] = torch.randn(len(rows), hq, d, device="cuda").bfloat16()
+    kv[:, rows.cuda()] = torch.randn(2, len(rows), hkv, d, device="cuda").bfloat16()
+    seq, pos = torch.full((n,), -1, dtype=torch.int32, device="cuda"), torch.zeros(n, dtype=torch.int32, device="cuda")
+    where = torch.arange(len(rows), dtype=torch.int32, device="cuda")
+    seq[rows.cuda()], pos[rows.cuda()] = 0, where
+    before = f64(q[rows.cuda()])
+    b.paged_append(h, c.pages, kv[0], kv[1], seq, pos, i32([n]), n, q=q, q_out=q)
+    b.blend_device_status(h)
+    got = f64(q[rows.cuda()])
+    for i, r in enumerate(rows):
+        want = P.rotate(before[i], i, THETA)
+        assert (np.abs(got[i] - want) <= STEP["bf16"] * np.abs(want) + 1e-5).all(), r
+    ko, vo = torch.empty(2, len(rows), hkv, d, dtype=torch.bfloat16, device="cuda")
+    b.paged_gather(h, c.pages, i32([0] * len(rows)), where, i32([len(rows)]), len(rows), ko, vo)
+    assert torch.equal(vo, kv[1][rows.cuda()])
+    del q, kv
+    torch.cuda.empty_cache()
+
+
 # ---------------------------------------------------------------- refusals and device-side checks
 def test_refused_calls_launch_nothing():
     h = handle("bf16", 8, 2, 128)
@@ -501,6 +534,35 @@ def test_refused_calls_launch_nothing():
         with pytest.raises(ValueError):
             bad()
     assert L_() <= before + 4  # the two handles' own
+
+
+def test_outputs_over_inputs_are_refused():
+    h = handle("bf16", 8, 2, 128)
+    c = filled("bf16", "model", 2, 128, 16, [40], 3)
+    buf = torch.zeros(32768, dtype=torch.bfloat16, device="cuda")
+    rows, at = 5, buf.data_ptr()
+    start, ln, n = i32([0, rows]), i32([40]), i32([rows])
+    seq, pos = i32([0] * rows), i32(list(range(rows)))
+    lib, before = b.lib(), b.blend_launch_count()
+
+    def att(q, ld, o):
+        return lib.paged_attention(h.ptr, c.pages.ref, at + 2 * q, ld, start.data_ptr(), ln.data_ptr(), rows, rows, 0, 0,
+                                   at + 2 * o, None)
+
+    def app(k, v, ldk, q, ldq, qo):
+        return lib.paged_append(h.ptr, c.pages.ref, at + 2 * k, ldk, at + 2 * v, ldk, at + 2 * q, ldq, at + 2 * qo,
+                                seq.data_ptr(), pos.data_ptr(), None, n.data_ptr(), rows, None)
+
+    for a in ((0, 1024, 1024), (0, 1024, 5112), (5112, 1024, 0), (0, 2048, 9208), (1024, 1024, 1024)):
+        assert att(*a) == b.EINVAL, a
+    for a in ((0, 16384, 256, 8192, 1024, 1272), (16384, 0, 256, 8192, 1024, 1272), (20000, 24000, 256, 0, 1024, 5112),
+              (1024, 1280, 1536, 0, 1536, 7672)):
+        assert app(*a) == b.EINVAL, a
+    assert b.blend_launch_count() == before
+    assert att(0, 1024, 5120) == b.OK and att(0, 2048, 9216) == b.OK
+    assert app(20000, 24000, 256, 0, 1024, 8192) == b.OK and app(20000, 24000, 256, 0, 1024, 0) == b.OK
+    assert app(1024, 1280, 1536, 0, 1536, 7680) == b.OK
+    b.blend_device_status(h)
 
 
 def status(h):
@@ -614,6 +676,34 @@ def test_captured_decode_steps_replay_with_new_lengths(dtype, fmt):
         assert torch.equal(got, out)
     b.blend_device_status(h)
     assert torch.equal(c.tensors["k"].view(torch.uint8), ref.tensors["k"].view(torch.uint8))
+
+
+@pytest.mark.parametrize("fmt", ["model", "int4"])
+@pytest.mark.parametrize("most", [48, 60])
+def test_captured_pieces_replay_with_new_lengths(fmt, most):
+    """Pieces in a captured call (one launch where every sequence could have max_q rows, else two),
+    replayed between eager calls with other row counts and lengths."""
+    h, other, side = handle("bf16", 8, 2, 128), handle("bf16", 8, 2, 128), torch.cuda.Stream()
+    c = filled("bf16", fmt, 2, 128, 16, [900, 500, 70], 127, poison=False)
+    q = torch.randn(144, 8, 128, device="cuda").bfloat16()
+    start, lens = i32([0, 48, 96, 144]), i32([900, 500, 70])
+    out = torch.empty(144, 1024, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        b.paged_attention(h, c.pages, q, start, lens, most, out, window=300, n_sink=4, stream=side)
+    for rows, ln in (([48, 48, 48], [900, 500, 70]), ([1, 48, 0], [17, 48, 0]), ([40, 7, 33], [41, 300, 33])):
+        start.copy_(i32(np.concatenate([[0], np.cumsum(rows)]).tolist()))
+        lens.copy_(i32(ln))
+        out.fill_(3.0)
+        g.replay()
+        got = out.clone()
+        out.fill_(3.0)
+        b.paged_attention(other, c.pages, q, start, lens, most, out, window=300, n_sink=4)
+        assert torch.equal(got, out)
+        b.paged_attention(h, c.pages, q, start, lens, most, out, window=300, n_sink=4)
+        assert torch.equal(got, out)
+    b.blend_device_status(h)
 
 
 # ---------------------------------------------------------------- together, behind a prefill
