@@ -19,8 +19,19 @@
 // row of the item sees are zeroed (they may hold anything, and 0 x NaN is NaN): by those warps,
 // or, in the few blocks at an edge, by the producer warp after the boxes have landed.  Pages without
 // a token that the item sees are not touched at all.
-// Rounding: P to bf16 (as everywhere on tensor cores), n s of 4-bit pages to bf16.
+// Rounding: P to bf16 (as everywhere on tensor cores).  4-bit pages: n s has 11 significant bits.  Keys
+// are held as two bf16 parts, n s rounded and the three bits that this leaves, and S takes both (the
+// reduction is twice as long, over the same queries).  Values are exact in fp16 where the scales of
+// 32 tokens lie within 2^-14..2^6 (or are 0), and those tokens' P is rounded to fp16 too; else both
+// are bf16.  The choice is one bit per 32 tokens that the dequantising warp leaves for the softmax
+// (both CTAs see the same scales) and for the P.V instruction's descriptor.
+// Measured: 64-row pieces of 8 sequences of 6-8 K tokens, against 64 bits relative to the result's norm,
+// 1.7e-3, which is the result's own rounding, in 105 us.  (Keys, values and P in bf16: 3.6e-3, 76 us;
+// only the keys in one bf16 part: 2.7e-3, 85 us.  Of the 29 us the second part's stores and products
+// are 13, three stages instead of five 7, the look at the scales 8.)
 #include <cmath>
+
+#include <cuda_fp16.h>
 
 #include "attn_tc.cuh"
 #include "paged.cuh"
@@ -47,10 +58,10 @@ template <bool I4, int D> struct TileCfg {
     static constexpr int THREADS = I4 ? 352 : 256;
     static constexpr int VCOL = D / 2;                      // V columns of a CTA
     static constexpr int QT = NH * Q_HALF;
-    static constexpr int KB = NH * K_HALF;
+    static constexpr int KB = (I4 ? 2 : 1) * NH * K_HALF;   // 4-bit pages: the keys as bf16, and what that leaves of them
     static constexpr int VB = TKEYS * VCOL * 2;
     static constexpr int STAGE = KB + VB;
-    static constexpr int STAGES = D == 64 ? 8 : 5;
+    static constexpr int STAGES = D == 64 ? (I4 ? 6 : 8) : I4 ? 3 : 5;
     static constexpr int QB = I4 ? 1 : 2;  // Q buffers: 4-bit pages need the room for stages
     // 4-bit pages: raw rows on their way (this CTA's 64 keys, the 128 values, their scales)
     static constexpr int RAW_STAGES = 2;
@@ -62,6 +73,11 @@ template <bool I4, int D> struct TileCfg {
     static constexpr uint32_t IDESC_S = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((256u >> 4) << 24);
     static constexpr uint32_t IDESC_PV =
         (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (((uint32_t)D >> 3) << 17) | ((256u >> 4) << 24);
+    static constexpr uint32_t IDESC_PV_F16 = IDESC_PV & ~((1u << 7) | (1u << 10));
+    // The exponent that P keeps in hand: fp16 holds P up to 2^15 (the largest sum of a block that is kept
+    // without its maximum), and 2^5 above the maximum's own weight keeps 2^-30 of it.
+    static constexpr float P_UP = I4 ? 5.f : 0.f;
+    static constexpr float SUM_MAX = I4 ? 0x1p15f : 0x1p50f;
     // fp32 partial result of one tile: [D / 4][128 lanes][4], then maxima and sums per lane
     static constexpr size_t PART = (size_t)TQ * (D + 2);
 };
@@ -261,12 +277,67 @@ template <bool HI> __device__ __forceinline__ uint32_t pair_value(uint32_t w, ui
     const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&n), *reinterpret_cast<__nv_bfloat162*>(&scale2));
     return *reinterpret_cast<const uint32_t*>(&v);
 }
+// The same, and what the rounding leaves (three bits, exactly).
+template <bool HI> __device__ __forceinline__ void pair_parts(uint32_t w, uint32_t scale2, uint32_t& value, uint32_t& rest) {
+    const uint32_t n = code_pair<HI>(w);
+    const __nv_bfloat162 n2 = *reinterpret_cast<const __nv_bfloat162*>(&n), s2 = *reinterpret_cast<__nv_bfloat162*>(&scale2);
+    const __nv_bfloat162 v = __hmul2(n2, s2), r = __hfma2(n2, s2, __hneg2(v));
+    value = *reinterpret_cast<const uint32_t*>(&v);
+    rest = *reinterpret_cast<const uint32_t*>(&r);
+}
 // One of two bf16 scales, twice, times 64.
 __device__ __forceinline__ uint32_t both(uint32_t w, int hi) {
     uint32_t s2 = __byte_perm(w, w, hi ? 0x3232 : 0x1010);
     const uint32_t unit = 0x42804280u;
     const __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&s2), *reinterpret_cast<const __nv_bfloat162*>(&unit));
     return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// The same in fp16, exact for scales that fit_f16 lets through: a code in the low bits of 1024 (the
+// codes at bits 0 and 16) is 1024 + n + 8.
+__device__ __forceinline__ uint32_t pair_f16(uint32_t w, uint32_t scale2) {
+    uint32_t x = (w & 0x000F000Fu) | 0x64006400u;
+    const uint32_t off = 0x64086408u;
+    const __half2 v = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<const __half2*>(&off)),
+                              *reinterpret_cast<__half2*>(&scale2));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t both_f16(uint32_t w, int hi) {
+    const float f = __uint_as_float(hi ? w & 0xffff0000u : w << 16);
+    return pack_f16x2(f, f);
+}
+// Both bf16 scales of w are 0 or within 2^-14..2^6: n s is exact in fp16 (2^-17..2^13 would do for
+// that), and weights so small that fp16 loses them, under 2^-30 of a row's largest, cannot matter by
+// having values that much larger.
+__device__ __forceinline__ bool fit_f16(uint32_t w) {
+    const uint32_t lo = w & 0xffffu, hi = w >> 16;
+    return (lo == 0u || lo - 0x3880u <= 0x0A00u) && (hi == 0u || hi - 0x3880u <= 0x0A00u);
+}
+constexpr uint32_t ALL_F16 = 0x01010101u;
+// P of a block with tokens whose values are bf16, 32 keys at a time from the row's reference (which
+// holds the block's maximum): packed over the scores; returns the sum.
+__device__ __forceinline__ float mixed_block(uint32_t s_col, uint32_t f16, float scale, float ref) {
+    float sum = 0.f;
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+        uint32_t v[32];
+        TMEM_LD32(s_col + 32 * q, v);
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        const bool h = (f16 >> (8 * q)) & 1u;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float p0 = ex2(fmaf(__uint_as_float(v[2 * i]), scale, ref)), p1 = ex2(fmaf(__uint_as_float(v[2 * i + 1]), scale, ref));
+            sum += p0 + p1;
+            v[i] = h ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+        }
+        TMEM_ST16(s_col + 16 * q, v);
+    }
+    return sum;
 }
 
 template <bool I4, int D>
@@ -283,6 +354,7 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
     __shared__ uint32_t tmem_sh;
     __shared__ volatile int abort_flag;
     __shared__ int pend_kv[STAGES], pend_q[2], pend_edge[STAGES], pend_raw[T::RAW_STAGES];
+    __shared__ uint32_t v_f16[STAGES];  // 4-bit pages: byte q is 1 where tokens 32 q .. +31 of the stage are fp16
     __shared__ int3 raw_at[T::RAW_STAGES];  // first key of a raw block, positions of its item's first and last row
     // in the workspace (shared memory is full of stages); read again only where a role changes sequence
     int* pre = a.pre + (size_t)blockIdx.x * (BLEND_MAX_SEQS + 1);
@@ -518,10 +590,10 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                 fence_after();
                 const uint64_t kd = desc_k(su32(sKV + st * STAGE));
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
+                for (int kk = 0; kk < (I4 ? 2 : 1) * D / 16; ++kk) {  // 4-bit pages: twice, with both parts of the keys
                     const uint32_t off = (kk & 3) * 32, half = kk >> 2;
-                    umma_ss2(tb + sb * 128, qd + ((half * Q_HALF + off) >> 4), kd + ((half * K_HALF + off) >> 4), T::IDESC_S,
-                             kk > 0 ? 1u : 0u);
+                    umma_ss2(tb + sb * 128, qd + (((half % NH) * Q_HALF + off) >> 4), kd + ((half * K_HALF + off) >> 4),
+                             T::IDESC_S, kk > 0 ? 1u : 0u);
                 }
                 commit2(&s_full[sb]);
             }
@@ -548,10 +620,11 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                 fence_after();
                 const uint64_t vd = desc_v<D>(su32(sKV + st * STAGE + KB));
                 const uint32_t pa = tb + sb * 128;
+                const uint32_t f16 = I4 ? *(volatile uint32_t*)&v_f16[st] : 0u;
 #pragma unroll
                 for (int kk = 0; kk < TKEYS / 16; ++kk)
-                    umma_ts2(tb + O_COL, pa + kk * 8, vd + ((kk * 16 * VCOL * 2) >> 4), T::IDESC_PV,
-                             (b > w.b0 || kk > 0) ? 1u : 0u);
+                    umma_ts2(tb + O_COL, pa + kk * 8, vd + ((kk * 16 * VCOL * 2) >> 4),
+                             I4 && ((f16 >> (8 * (kk / 2))) & 1u) ? T::IDESC_PV_F16 : T::IDESC_PV, (b > w.b0 || kk > 0) ? 1u : 0u);
                 commit2(&kv_empty[st]);
             }
             if (!ok) break;
@@ -593,6 +666,7 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                 const int k0 = w.it.kr.block(b) * TKEYS;
                 const bool cut = !all_see(k0, k0 + TKEYS - 1, t_lo, t_hi, a.window, a.n_sink);
                 if (cut) mask_scores(s_col, my_pos - k0, a.window, a.n_sink - k0);
+                const uint32_t f16 = I4 ? *(volatile uint32_t*)&v_f16[it % STAGES] : ALL_F16;
                 uint32_t s[128];
                 float2 accs;
                 bool rescale = false;
@@ -602,41 +676,49 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                 // others is short and straight (masks and maximum on the 128 registers, unrolled, put
                 // some 15 KB of instructions into the middle of it: 468 instead of 457 us for four
                 // prompt pieces of 2048 rows, window 4096, and 220 bytes of spills with 4-bit pages).
+                auto raise = [&]() {
+                    const float mxs = row_max(s_col) * a.scale_log2;
+                    const bool need = mxs > m_used + RESCALE_LOG2;
+                    rescale = __any_sync(0xffffffffu, need);
+                    if (rescale) {
+                        const float m_new = need ? mxs - T::P_UP : m_used;
+                        corr = need ? ex2(m_used - m_new) : 1.f;
+                        l *= corr;
+                        m_used = m_new;
+                    }
+                };
+                const bool mixed = I4 && f16 != ALL_F16;
+                if (mixed) {
+                    raise();
+                    accs = make_float2(mixed_block(s_col, f16, a.scale_log2, m_used == -INFINITY ? 0.f : -m_used), 0.f);
+                }
                 bool exact = !__all_sync(0xffffffffu, m_used != -INFINITY);
 #pragma unroll 1
-                while (true) {
-                    if (exact) {
-                        const float mxs = row_max(s_col) * a.scale_log2;
-                        const bool need = mxs > m_used + RESCALE_LOG2;
-                        rescale = __any_sync(0xffffffffu, need);
-                        if (rescale) {
-                            const float m_new = need ? mxs : m_used;
-                            corr = need ? ex2(m_used - m_new) : 1.f;
-                            l *= corr;
-                            m_used = m_new;
-                        }
-                    }
+                while (!mixed) {
+                    if (exact) raise();
+                    const float ref = m_used == -INFINITY ? 0.f : -m_used;
                     TMEM_LD32(s_col, s);
                     TMEM_LD32(s_col + 32, (s + 32));
                     TMEM_LD32(s_col + 64, (s + 64));
                     TMEM_LD32(s_col + 96, (s + 96));
                     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
                     float2 acc2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    const float ref = m_used == -INFINITY ? 0.f : -m_used;
                     const float2 nm2 = make_float2(ref, ref);
 #pragma unroll
                     for (int e = 0; e < 64; ++e) {
                         const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), sc2, nm2);
                         const float p0 = ex2(x.x), p1 = ex2(x.y);
                         acc2[e & 1] = __fadd2_rn(acc2[e & 1], make_float2(p0, p1));
-                        s[e] = pack_bf16x2(p0, p1);
+                        s[e] = I4 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
                     }
                     accs = __fadd2_rn(acc2[0], acc2[1]);
-                    if (exact || !__any_sync(0xffffffffu, !(accs.x + accs.y <= 0x1p50f))) break;
+                    if (exact || !__any_sync(0xffffffffu, !(accs.x + accs.y <= T::SUM_MAX))) break;
                     exact = true;  // P is not stored yet: once more, from the block's maximum
                 }
-                TMEM_ST32(s_col, s);
-                TMEM_ST32(s_col + 32, (s + 32));
+                if (!mixed) {
+                    TMEM_ST32(s_col, s);
+                    TMEM_ST32(s_col + 32, (s + 32));
+                }
                 if (rescale && b > w.b0) {
                     const uint32_t pv = it - 1;  // O must hold every block before this one
                     if (!warp_wait_cl(&kv_empty[pv % STAGES], (pv / STAGES) & 1, &abort_flag)) {
@@ -840,8 +922,14 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                     // word q of this half row: c = 2 (t & 1) + q / G, g = q % G  (G words per c)
                     const int c = 2 * (t & 1) + q / G, g = q % G, ch = 4 * (g & 1) + c;
                     const uint32_t w = kw[q], hi = w >> 8;
-                    *reinterpret_cast<uint4*>(dk + (g >> 1) * K_HALF + tk * 128 + ((ch ^ (tk & 7)) << 4)) =
-                        make_uint4(pair_value<false>(w, sc[g]), pair_value<true>(w, sc[g]), pair_value<false>(hi, sc[g]), pair_value<true>(hi, sc[g]));
+                    uint4 x, y;
+                    pair_parts<false>(w, sc[g], x.x, y.x);
+                    pair_parts<true>(w, sc[g], x.y, y.y);
+                    pair_parts<false>(hi, sc[g], x.z, y.z);
+                    pair_parts<true>(hi, sc[g], x.w, y.w);
+                    uint8_t* to = dk + (g >> 1) * K_HALF + tk * 128 + ((ch ^ (tk & 7)) << 4);
+                    *reinterpret_cast<uint4*>(to) = x;
+                    *reinterpret_cast<uint4*>(to + NH * K_HALF) = y;
                 }
             }
             uint8_t* dv = dk + KB;
@@ -850,34 +938,42 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                 const int j = at.x + t;
                 const bool seen = j <= at.z && (j < a.n_sink || j > at.y - a.window);
                 // a token that no row sees counts as zero whatever its scale (or the row, if it was not read)
-                const uint32_t vsc = seen ? *reinterpret_cast<const uint32_t*>(raw + T::RAW_VS + t * SB + (D == 128 ? 4 * rank : 0)) : 0u;
-                const uint32_t s0 = both(vsc, D == 128 ? 0 : rank), s1 = both(vsc, 1);
+                uint32_t sw[G / 2];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    // chunk c holds dims 8c.. of each group: halves r = 2c, 2c + 1; threads start at different
-                    // chunks so that a warp's reads fall on distinct banks
-                    const int c = (q + (t >> 1)) & 3;
-                    uint32_t x, y;  // words of halves 2c, 2c + 1 with this CTA's groups
-                    if constexpr (D == 128) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(raw + T::RAW_V + t * RB + c * 16);
-                        x = rank ? v.y : v.x;
-                        y = rank ? v.w : v.z;
-                    } else {
-                        const uint2 v = *reinterpret_cast<const uint2*>(raw + T::RAW_V + t * RB + c * 8);
-                        x = rank ? v.x >> 16 : v.x;
-                        y = rank ? v.y >> 16 : v.y;
-                    }
+                for (int g = 0; g < G / 2; ++g) sw[g] = seen ? *reinterpret_cast<const uint32_t*>(raw + T::RAW_VS + t * SB + 4 * g) : 0u;
+                const bool f16 = __all_sync(0xffffffffu, fit_f16(sw[0]) && fit_f16(sw[G / 2 - 1]));
+                if (lane == 0) reinterpret_cast<volatile uint8_t*>(&v_f16[st])[t >> 5] = f16 ? 1 : 0;
+                auto turn = [&](uint32_t s0, uint32_t s1, auto pair) {
 #pragma unroll
-                    for (int g = 0; g < D / 64; ++g) {  // low halves of x, y, then the high ones
-                        const uint32_t h0 = g ? x >> 16 : x & 0xffffu, h1 = g ? y >> 16 : y & 0xffffu;
-                        const uint32_t y0 = h0 | (h0 << 12), y1 = h1 | (h1 << 12);  // codes 0, 1 and 2, 3 as pairs at bits 0 and 8
-                        const uint32_t sc = g ? s1 : s0;
-                        const int ch = 4 * g + c;
-                        const int to = D == 128 ? t * 128 + ((ch ^ (t & 7)) << 4) : t * 64 + ((ch ^ ((t >> 1) & 3)) << 4);
-                        *reinterpret_cast<uint4*>(dv + to) = make_uint4(pair_value<false>(y0, sc), pair_value<false>(y0 >> 8, sc),
-                                                                        pair_value<false>(y1, sc), pair_value<false>(y1 >> 8, sc));
+                    for (int q = 0; q < 4; ++q) {
+                        // chunk c holds dims 8c.. of each group: halves r = 2c, 2c + 1; threads start at different
+                        // chunks so that a warp's reads fall on distinct banks
+                        const int c = (q + (t >> 1)) & 3;
+                        uint32_t x, y;  // words of halves 2c, 2c + 1 with this CTA's groups
+                        if constexpr (D == 128) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(raw + T::RAW_V + t * RB + c * 16);
+                            x = rank ? v.y : v.x;
+                            y = rank ? v.w : v.z;
+                        } else {
+                            const uint2 v = *reinterpret_cast<const uint2*>(raw + T::RAW_V + t * RB + c * 8);
+                            x = rank ? v.x >> 16 : v.x;
+                            y = rank ? v.y >> 16 : v.y;
+                        }
+#pragma unroll
+                        for (int g = 0; g < D / 64; ++g) {  // low halves of x, y, then the high ones
+                            const uint32_t h0 = g ? x >> 16 : x & 0xffffu, h1 = g ? y >> 16 : y & 0xffffu;
+                            const uint32_t y0 = h0 | (h0 << 12), y1 = h1 | (h1 << 12);  // codes 0, 1 and 2, 3 as pairs at bits 0 and 8
+                            const uint32_t sc = g ? s1 : s0;
+                            const int ch = 4 * g + c;
+                            const int to = D == 128 ? t * 128 + ((ch ^ (t & 7)) << 4) : t * 64 + ((ch ^ ((t >> 1) & 3)) << 4);
+                            *reinterpret_cast<uint4*>(dv + to) = make_uint4(pair(y0, sc), pair(y0 >> 8, sc), pair(y1, sc), pair(y1 >> 8, sc));
+                        }
                     }
-                }
+                };
+                const uint32_t vsc = sw[D == 128 ? rank : 0];
+                const int first = D == 128 ? 0 : rank;
+                if (f16) turn(both_f16(vsc, first), both_f16(vsc, 1), [](uint32_t w, uint32_t sc) { return pair_f16(w, sc); });
+                else turn(both(vsc, first), both(vsc, 1), [](uint32_t w, uint32_t sc) { return pair_value<false>(w, sc); });
             }
             warp_arrive(&raw_empty[rs]);
             fence_async_smem();

@@ -319,6 +319,59 @@ def test_queries_and_keys_of_extreme_size(fmt):
             assert (np.abs(got - want) <= attention_bound("bf16", fmt, want, mag, lin, 300, rows > 8)).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_int4_values_of_pieces_are_exact(d):
+    """Rows of few keys, keys that are bf16 values: what is left are the weights' fp16 rounding (half a
+    step 2^-11, and 2^-30 of the largest weight where that is lost) and the result's."""
+    rows, n = 70, 300
+    h, c = handle("bf16", 8, 2, d), filled("bf16", "int4", 2, d, 32, [n], 131)
+    ks = c.tensors["k_scale"]
+    ks.copy_(torch.where(torch.isnan(ks), ks, torch.full_like(ks, 0.125)))
+    k, v = torch.empty(2, n, 2, d, dtype=torch.bfloat16, device="cuda")
+    b.paged_gather(h, c.pages, i32([0] * n), i32(list(range(n))), i32([n]), n, k, v)  # n / 8 is a bf16 value
+    q = torch.randn(rows, 8, d, device="cuda").bfloat16()
+    for window, sink in ((4, 0), (1, 2), (3, 1)):
+        got = f64(attend(h, c, q, i32([0, rows]), [n], rows, window, sink)).reshape(rows, 8, d)
+        want, mag, lin = P.attention(f64(q), f64(k), c.v[0], n, window, sink)
+        x = (d + 4) * 2.0 ** -24 * lin + 2.0 ** -22
+        moved = (np.exp(2 * x) - 1)[..., None] + 2.0 ** -11 + 20 * 2.0 ** -24
+        lim = 1.01 * moved * mag + 4 * 2.0 ** -30 * np.abs(c.v[0]).max() + STEP["bf16"] * np.abs(want)
+        assert (np.abs(got - want) <= lim).all(), (np.abs(got - want) / lim).max()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [16, 32])
+def test_int4_value_scales_of_any_size(d, page):
+    """Scales far from 1 and zero, over whole sequences, in turn by pages, and in single groups of 32 dims."""
+    lens, n_q = [300, 500, 260, 400], [40, 64, 33, 128]
+    h, c = handle("bf16", 8, 2, d), filled("bf16", "int4", 2, d, page, lens, 137)
+    vs, table, rng = c.tensors["v_scale"], c.table.cpu().numpy(), np.random.default_rng(5)
+    for s, n in enumerate(lens):
+        for p in range((n + page - 1) // page):
+            up = np.ones(d // 32)
+            if s == 0:
+                up[:] = 2.0 ** -40
+            elif s == 1:
+                up[:] = 2.0 ** (10 * (p // 2 % 3))  # 1, 2^10 and 2^20 by turns
+            elif s == 2:
+                up[rng.integers(d // 32)] = [2.0 ** 30, 2.0 ** -30, 0.0][p % 3]
+            else:
+                up[:] = 2.0 ** rng.integers(-8, 8)
+            vs[int(table[s, p])] *= torch.from_numpy(up).to(vs)
+            at = slice(p * page, min((p + 1) * page, n))
+            c.v[s][at] *= up.repeat(32)
+    start = np.concatenate([[0], np.cumsum(n_q)])
+    q = torch.randn(start[-1], 8, d, device="cuda").bfloat16()
+    for window, sink in ((0, 0), (70, 3)):
+        out = f64(attend(h, c, q, i32(start.tolist()), lens, 128, window, sink))
+        for s, n in enumerate(lens):
+            got = out[start[s]:start[s + 1]].reshape(-1, 8, d)
+            want, mag, lin = P.attention(f64(q[start[s]:start[s + 1]]), c.k[s], c.v[s], n, window, sink)
+            lim = attention_bound("bf16", "int4", want, mag, lin, n, True)
+            assert (np.abs(got - want) <= lim).all(), (s, (np.abs(got - want) / lim).max())
+    b.blend_device_status(h)
+
+
 @pytest.mark.parametrize("dtype,fmt", [("bf16", "model"), ("bf16", "int4"), ("f32", "model")])
 @pytest.mark.parametrize("page", [16, 128])
 def test_pages_left_behind_by_the_window_may_be_gone(dtype, fmt, page):
