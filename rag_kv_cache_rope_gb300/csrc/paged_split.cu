@@ -25,8 +25,11 @@
 // Values: a mask and one multiply-add give (n - 8) / 64 exactly (see code_pair; an offset left in the
 // sums would cancel against results that are far smaller than it), and the value's scale
 // multiplies P in fp32 before its one rounding to bf16; the 64 goes into the last division.
-// Measured (GB300, 6.8 TB/s copy rate): 64 sequences of 3.3-8.2 K tokens, window 4096, Mistral-7B
-// heads 172 us, 6.2 TB/s of pages.
+// Measured (GB300, 6.8 TB/s copy rate), host call included: 64 sequences of 3.3-8.2 K tokens, window
+// 4096, Mistral-7B heads 163 us, 6.5 TB/s of pages; one sequence of 128 K tokens, 14B heads, 93 us, 5.7 TB/s
+// (10 us of it are finding the shares and joining 304 parts).  4-bit pages, 32 sequences of 7.3-16 K
+// tokens: 111 us, 4.5 TB/s: bound by instruction issue and its dependencies (56 % of the issue slots;
+// two CTAs are what 195 registers leave room for), not by HBM (57 %).
 // Tokens that no row sees are filled with zeros instead of loaded (values, scales), so what they
 // hold does not matter.
 #include <climits>
