@@ -453,7 +453,7 @@ class PagesRef:
             raise ValueError("the tensors of a paged cache must be contiguous and on one device")
         self.device, self.dtype, self.n_kv_heads, self.n_seq = k.device, k.dtype, k.shape[1], table.shape[0]
         self.index = k.get_device()  # -1: not on a GPU
-        self._checked = None         # the model these pages were last found to fit
+        self._fit = (None, None, 0)  # the model these pages were last found to fit, its element type and query heads
         self.head_dim = k.shape[3] * (2 if int4 else 1)
         self.c = Pages(PAGES_INT4 if int4 else PAGES_MODEL, k.shape[2], k.shape[0], table.shape[0], table.shape[1],
                        *[None if x is None else x.data_ptr() for x in (table, k, v, k_scale, v_scale)])
@@ -463,24 +463,25 @@ class PagesRef:
 # A decode step makes these calls once per layer with kernels of a few microseconds: the checks below
 # read each property once, and what holds for a pair of handle and pages is remembered in the pages.
 def _paged_stream(h: Handle, pages: PagesRef, stream):
-    """The call's stream, after a look at the pages: they must be the handle's model's and on the
-    stream's GPU."""
-    if pages._checked is not h.cfg:
-        want = torch.uint8 if pages.c.format == PAGES_INT4 else torch.bfloat16 if h.cfg.dtype == BF16 else torch.float32
-        if pages.dtype != want or pages.n_kv_heads != h.cfg.n_kv_heads or pages.head_dim != h.cfg.head_dim:
+    """The call's stream, the model's element type and query heads, after a look at the pages: they must
+    be the handle's model's and on the stream's GPU."""
+    fit = pages._fit
+    if fit[0] is not h.cfg:
+        model = torch.bfloat16 if h.cfg.dtype == BF16 else torch.float32
+        if pages.dtype != (torch.uint8 if pages.c.format == PAGES_INT4 else model) or pages.n_kv_heads != h.cfg.n_kv_heads or pages.head_dim != h.cfg.head_dim:
             raise ValueError("the pages are not of the handle's model")
         if pages.index < 0:
             raise ValueError("the pages are not on a GPU")
-        pages._checked = h.cfg
+        pages._fit = fit = (h.cfg, model, h.cfg.n_q_heads)
     dev = pages.index
     if torch.cuda.current_device() != dev or (stream is not None and stream.device_index != dev):
         raise ValueError(f"the pages are on {pages.device}: make it the current device and use a stream of it")
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream, fit[1], fit[2]
 
 
-def _paged_rows(h: Handle, pages: PagesRef, t: torch.Tensor, heads: int, what: str) -> int:
+def _paged_rows(pages: PagesRef, dtype, t: torch.Tensor, heads: int, what: str) -> int:
     """Distance between the rows of t [rows][heads][head dim] in elements."""
-    d = h.cfg.head_dim
+    d = pages.head_dim
     st, sh = t.stride(), t.shape
     if len(sh) == 3:
         ok = sh[1] == heads and sh[2] == d and st[2] == 1 and (st[1] == d or heads == 1)
@@ -488,7 +489,7 @@ def _paged_rows(h: Handle, pages: PagesRef, t: torch.Tensor, heads: int, what: s
         ok = len(sh) == 2 and sh[1] == heads * d and st[1] == 1
     if not ok:
         raise ValueError(f"{what} must be [rows][{heads}][{d}] with adjacent heads")
-    if t.dtype is not (torch.bfloat16 if h.cfg.dtype == BF16 else torch.float32) or t.get_device() != pages.index:
+    if t.dtype is not dtype or t.get_device() != pages.index:
         raise ValueError(f"{what} must be of the model's dtype and on {pages.device}")
     return st[0] if sh[0] > 1 else heads * d
 
@@ -503,9 +504,9 @@ def paged_append(h: Handle, pages: PagesRef, k_new, v_new, seq, pos, n, max_n, q
                  stream=None):
     """k_new, v_new (and q): [rows][heads][head dim], rows at any stride of 16 bytes; seq, pos, rot
     int32 per row; n a device int32 count of at most max_n rows."""
-    s = _paged_stream(h, pages, stream)
-    hkv = h.cfg.n_kv_heads
-    ld_k, ld_v = _paged_rows(h, pages, k_new, hkv, "k_new"), _paged_rows(h, pages, v_new, hkv, "v_new")
+    s, dt, hq = _paged_stream(h, pages, stream)
+    hkv = pages.n_kv_heads
+    ld_k, ld_v = _paged_rows(pages, dt, k_new, hkv, "k_new"), _paged_rows(pages, dt, v_new, hkv, "v_new")
     seq, pos = _paged_index(pages, max_n, "seq", seq), _paged_index(pages, max_n, "pos", pos)
     if rot is not None:
         rot = _paged_index(pages, max_n, "rot", rot)
@@ -514,9 +515,8 @@ def paged_append(h: Handle, pages: PagesRef, k_new, v_new, seq, pos, n, max_n, q
         raise ValueError("fewer rows than max_n")
     ld_q = pq = po = None
     if q is not None and q_out is not None:
-        hq = h.cfg.n_q_heads
-        ld_q = _paged_rows(h, pages, q, hq, "q")
-        if _paged_rows(h, pages, q_out, hq, "q_out") != hq * h.cfg.head_dim or min(q.shape[0], q_out.shape[0]) < max_n:
+        ld_q = _paged_rows(pages, dt, q, hq, "q")
+        if _paged_rows(pages, dt, q_out, hq, "q_out") != hq * pages.head_dim or min(q.shape[0], q_out.shape[0]) < max_n:
             raise ValueError("q_out must hold max_n adjacent rows, and q as many")
         pq, po = q.data_ptr(), q_out.data_ptr()
     elif q is not None or q_out is not None:
@@ -531,10 +531,10 @@ def paged_append(h: Handle, pages: PagesRef, k_new, v_new, seq, pos, n, max_n, q
 
 def paged_gather(h: Handle, pages: PagesRef, seq, pos, n, max_n, k_out, v_out, rot=None, stream=None):
     """k_out, v_out: [rows][kv heads][head dim], rows adjacent, of the model's dtype."""
-    s = _paged_stream(h, pages, stream)
-    hkv = h.cfg.n_kv_heads
+    s, dt, _ = _paged_stream(h, pages, stream)
+    hkv = pages.n_kv_heads
     for t in (k_out, v_out):
-        if _paged_rows(h, pages, t, hkv, "k_out and v_out") != hkv * h.cfg.head_dim or t.shape[0] < max_n:
+        if _paged_rows(pages, dt, t, hkv, "k_out and v_out") != hkv * pages.head_dim or t.shape[0] < max_n:
             raise ValueError("k_out and v_out must hold max_n adjacent rows")
     seq, pos = _paged_index(pages, max_n, "seq", seq), _paged_index(pages, max_n, "pos", pos)
     if rot is not None:
@@ -551,10 +551,10 @@ def paged_attention(h: Handle, pages: PagesRef, q, q_start, kv_len, max_q, out, 
     """q: [rows][hq][head dim] (rows at any stride of 16 bytes); out: [rows][hq * head dim], rows
     adjacent; q_start int32 [n_seq + 1], kv_len int32 [n_seq] on the device; max_q: most query rows of
     one sequence."""
-    s = _paged_stream(h, pages, stream)
-    hq, n_seq, rows = h.cfg.n_q_heads, pages.n_seq, q.shape[0]
-    ld_q = _paged_rows(h, pages, q, hq, "q")
-    if _paged_rows(h, pages, out, hq, "out") != hq * h.cfg.head_dim or out.shape[0] < rows:
+    s, dt, hq = _paged_stream(h, pages, stream)
+    n_seq, rows = pages.n_seq, q.shape[0]
+    ld_q = _paged_rows(pages, dt, q, hq, "q")
+    if _paged_rows(pages, dt, out, hq, "out") != hq * pages.head_dim or out.shape[0] < rows:
         raise ValueError("out must hold as many adjacent rows as q")
     kv_len = _paged_index(pages, n_seq, "kv_len", kv_len)
     q_start = _paged_index(pages, n_seq + 1, "q_start", q_start)

@@ -109,12 +109,16 @@ __device__ __forceinline__ void group_scales(const float* x0, const float* x1, c
 __device__ __forceinline__ void codes8(const float* x, const Scale& sc, uint32_t (&c)[8]) {
     const float s = sc.s, y = sc.y;
     if (s >= 0x1p-100f && s <= 0x1p100f) {
+        // (two values an instruction)
+        const float2 y2 = make_float2(y, y), ns2 = make_float2(-s, -s), up2 = make_float2(12582920.f, 12582920.f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float q = __fmul_rn(x[e], y);
+        for (int e = 0; e < 8; e += 2) {
+            const float2 x2 = make_float2(x[e], x[e + 1]), q = __fmul2_rn(x2, y2);
             // max |x| / s stays below 7.5 for such scales, so the code is in range without a clamp; adding
             // 1.5 2^23 rounds to an integer, ties to even (and the 8 keeps its parity)
-            c[e] = __float_as_uint(__fadd_rn(__fmaf_rn(__fmaf_rn(-q, s, x[e]), y, q), 12582920.f));
+            const float2 r = __fadd2_rn(__ffma2_rn(__ffma2_rn(q, ns2, x2), y2, q), up2);
+            c[e] = __float_as_uint(r.x);
+            c[e + 1] = __float_as_uint(r.y);
         }
     } else {
 #pragma unroll
