@@ -538,6 +538,8 @@ int blend_device_status(blend_handle* h, void* stream) {
         return check_cuda(h, "blend_device_status");
     if (e != 0) {
         cudaMemset(h->err, 0, 4);
+        // a kernel that gave up waiting (the word may hold an earlier error) may not have counted all arrivals
+        cudaMemset(h->paged_count, 0, PAGED_MAX_CTAS * sizeof(int32_t));
         return fail(h, e == BLEND_ETIMEOUT ? BLEND_ETIMEOUT : BLEND_EDEVICE,
                     "device-side check failed (code %d)", e);
     }

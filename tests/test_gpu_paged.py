@@ -694,6 +694,18 @@ def test_bad_sequences_are_skipped_and_reported(fmt, rows):
     assert torch.equal(out[:rows], good[:rows]) and torch.equal(out[2 * rows:], good[2 * rows:])
 
 
+def test_attention_after_an_expired_wait():
+    """blend_device_status after a timeout leaves the handle as it was: parts are joined as before."""
+    h = handle("bf16", 8, 2, 128)
+    c = filled("bf16", "model", 2, 128, 16, [3000, 700], 139)
+    q, start = torch.randn(41, 8, 128, device="cuda").bfloat16(), i32([0, 1, 41])
+    want = attend(h, c, q, start, [3000, 700], 40)
+    b.blend_wait_flag(h, i32([0]), 10)
+    assert status(h) == b.ETIMEOUT and status(h) == b.OK
+    assert torch.equal(attend(h, c, q, start, [3000, 700], 40), want)
+    b.blend_device_status(h)
+
+
 # ---------------------------------------------------------------- streams, graphs
 @pytest.mark.parametrize("dtype,fmt", [("bf16", "model"), ("bf16", "int4"), ("f32", "model")])
 def test_captured_decode_steps_replay_with_new_lengths(dtype, fmt):
