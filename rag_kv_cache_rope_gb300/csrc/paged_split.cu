@@ -196,10 +196,12 @@ __global__ void __launch_bounds__(W * 32, 2)
     if (n_item == 0) return;
     n_item *= hkv;
     // An equal share of the line, but at least a step per warp.  Leaving parts of an item and joining
-    // them takes about 5 us, so items of fewer than four steps per warp are never cut, for a small
-    // total nor at a border (GB300, bf16: 8 items of 7 steps 8.8 us whole and 14.7 us in two parts; 8
-    // items of 44 steps 10.9 us in 11 parts, 12.9 in 6 and 14.6 in 3).
-    constexpr int SHORT = 4 * W;
+    // them takes about as long as five more steps of every warp, so items of fewer than six steps per
+    // warp are never cut for a small total, nor those of fewer than four at a border (GB300, bf16, 8 items, in a
+    // captured graph: 22 steps 7.5 us whole, 8.4 in six parts; 32 steps 8.1 either way; 44 steps 8.3 in 11
+    // parts).  Eight warps on every SM, one CTA each, measured 7.0, 7.6 and 8.6 us there, but 9.1 instead of
+    // 8.8 for 63 steps and 15.6 instead of 13.8 for 1000.
+    constexpr int SHORT = 6 * W;
     const int per_item = (total + n_item - 1) / n_item;
     const int quota = max((total + (int)gridDim.x - 1) / (int)gridDim.x, per_item < SHORT ? per_item : W);
     const Shares sh(total, quota, min(2 * W, quota));
