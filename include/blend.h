@@ -442,11 +442,11 @@ int importance_scores(const void* hidden, int32_t n, int32_t n_layers, int32_t d
  * may share pages.
  *
  * BLEND_PAGES_INT4: the 32 dims of a group (dims 32g..32g+31 of one head's row) share a bf16
- * scale s = bf16(max |x| / 7), and a dim is held as code n + 8 with n = round-to-even(x / s) in
- * -7..7 (0 where s is 0), every step in fp32; its value is n * s.  A group with an infinity or a
- * NaN gets a NaN scale: all its values are NaN.  A K row of d / 2 bytes holds dim 32g + 8c + e
- * (c < 4, e < 8) at bit 4 * (e / 2) + 16 * (e % 2) of the little-endian 32-bit word at byte
- * c * d / 8 + 4 * g; a V row holds dim 32g + 4r + e (r < 8, e < 4) at bit 4 * e of the 16-bit
+ * scale s = bf16(max |x| * (1/7 rounded to fp32)), and a dim is held as code n + 8 with n =
+ * round-to-even(x / s) in -7..7 (0 where s is 0), every step in fp32; its value is n * s.  A group
+ * with an infinity or a NaN gets a NaN scale: all its values are NaN.  A K row of d / 2 bytes holds
+ * dim 32g + 8c + e (c < 4, e < 8) at bit 4 * (e / 2) + 16 * (e % 2) of the little-endian 32-bit word at
+ * byte c * d / 8 + 4 * g; a V row holds dim 32g + 4r + e (r < 8, e < 4) at bit 4 * e of the 16-bit
  * word at byte r * d / 16 + 2 * g.  (The orders are those in which the attention kernel's matrix
  * instructions take their operands.) */
 typedef struct {

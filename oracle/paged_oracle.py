@@ -46,12 +46,12 @@ def rotate_f32(x, pos, theta):
 
 
 def quantise(x):
-    """(codes -7..7, scales) of x [..][d] fp32: 32 dims share bf16(max|x| / 7); a group that is not
-    finite gets a NaN scale and codes 0."""
+    """(codes -7..7, scales) of x [..][d] fp32: 32 dims share bf16(max|x| * (1/7 in fp32));
+    a group that is not finite gets a NaN scale and codes 0."""
     y = np.asarray(x, dtype=F32).reshape(*x.shape[:-1], x.shape[-1] // 32, 32)
     with np.errstate(all="ignore"):
         fin = np.isfinite(y).all(-1)
-        s = np.where(fin, bf16(np.abs(np.where(np.isfinite(y), y, 0)).max(-1) / F32(7)), F32(np.nan))
+        s = np.where(fin, bf16(np.abs(np.where(np.isfinite(y), y, 0)).max(-1) * (F32(1) / F32(7))), F32(np.nan))
         n = np.where((s > 0)[..., None], np.clip(np.rint(y / s[..., None]), -7, 7), 0)
     return n.reshape(x.shape).astype(np.int64), s
 

@@ -71,8 +71,8 @@ __device__ __forceinline__ void rotate8(float* a, float* b, int rot, int i0, int
 }
 
 // Scales of the four 32-dim groups that four neighbouring threads hold eight dims each of: bf16 of
-// max / 7, NaN when a group is not finite, and their reciprocals.  Thread j of the four computes
-// group j's (a division and a reciprocal each) and the others read them.  Call it with all 32 lanes.
+// max * (1/7 in fp32), NaN when a group is not finite, and their reciprocals.  Thread j of the four computes
+// group j's (a product and a reciprocal each) and the others read them.  Call it with all 32 lanes.
 struct Scale {
     uint32_t bits;  // the bf16
     float s, y;     // its value, and 1 / s
@@ -88,7 +88,7 @@ __device__ __forceinline__ void group_scales(const float* x0, const float* x1, c
     const float m0 = group_max(x0), m1 = group_max(x1), m2 = group_max(x2), m3 = group_max(x3);
     const int j = threadIdx.x & 3;
     const float m = j == 0 ? m0 : j == 1 ? m1 : j == 2 ? m2 : m3;
-    const bf16 s = __float2bfloat16_rn(isfinite(m) ? __fdiv_rn(m, 7.f) : __int_as_float(0x7fc00000));
+    const bf16 s = __float2bfloat16_rn(isfinite(m) ? __fmul_rn(m, 1.f / 7.f) : __int_as_float(0x7fc00000));
     const uint32_t bits = __bfloat16_as_ushort(s);
     const float y = __frcp_rn(__bfloat162float(s));
     const int first = (threadIdx.x & 31) & ~3;

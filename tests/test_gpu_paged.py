@@ -119,6 +119,26 @@ def test_append_int4_pages_bit_for_bit(dtype, hq, hkv, d, page, rot):
         assert same.all(), k
 
 
+def test_int4_scale_is_the_product_with_a_seventh():
+    """Maxima just below ties of bf16, where a product with fp32's 1/7 and a division by 7 part."""
+    tie = 7 * (1 + (1 + 2 * np.arange(64)) * 2.0 ** -8)
+    m = np.nextafter(tie.astype(np.float32), np.float32(0)) * np.float32(2.0) ** np.arange(-32, 32).astype(np.float32)
+    assert (P.bf16(m * (np.float32(1) / np.float32(7))) != P.bf16(m / np.float32(7))).any()
+    rng = np.random.default_rng(3)
+    x = (rng.uniform(-1, 1, (64, 4, 32)) * m[:, None, None]).astype(np.float32)
+    x[:, :, 5] = m[:, None]
+    x = x.reshape(64, 2, 64)
+    h, c = handle("f32", 4, 2, 64), filled("f32", "int4", 2, 64, 64, [64], 3)
+    kv = torch.from_numpy(x).cuda()
+    b.paged_append(h, c.pages, kv, kv, i32([0] * 64), i32(list(range(64))), i32([64]), 64, rot=i32([0] * 64))
+    b.blend_device_status(h)
+    codes, s = P.quantise(x)
+    at = int(c.table[0, 0])
+    for i, (name, scale) in enumerate((("k", "k_scale"), ("v", "v_scale"))):
+        assert np.array_equal(c.tensors[name][at].cpu().numpy(), P.pack(codes, i == 1).transpose(1, 0, 2))
+        assert np.array_equal(f64(c.tensors[scale][at]), s.transpose(1, 0, 2))
+
+
 def test_append_in_place_q_one_row_and_no_rows():
     h = handle("bf16", 8, 2, 128)
     c = filled("bf16", "model", 2, 128, 16, [5], 3)

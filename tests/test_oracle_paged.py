@@ -51,6 +51,10 @@ def test_quantise_hand_cases():
     y = np.full((1, 32), 7 * (1 + 2.0 ** -9), dtype=np.float32)
     n, s = P.quantise(y)
     assert s[0, 0] == 1.0 and (n == 7).all()
+    # the scale is the fp32 product with fp32's 1/7: just below a tie of bf16 it is the tie, where a
+    # division would stay below it
+    y = np.full((1, 32), np.nextafter(np.float32(7 * (1 + 3 * 2.0 ** -8)), np.float32(0)), dtype=np.float32)
+    assert P.quantise(y)[1][0, 0] == 1 + 2.0 ** -6
 
 
 def test_rotation_forms_agree():
