@@ -4,13 +4,16 @@
 //
 //   o = sum_j 2^(c q.k_j - m) v_j / sum_j 2^(c q.k_j - m),  c = log2(e) / sqrt(d), m the running maximum
 //
-// A CTA takes one tile of eight (row, head) pairs of one kv head and one of `splits` shares of
-// the keys they see; its eight warps take 32-key blocks in turn, each with its own running
+// A CTA takes one tile of SR (row, head) pairs of one kv head (1, 4 or 8: no more than a sequence's rows
+// fill, since empty places cost as much as others) and one of `splits` shares of the keys they see; its eight warps take 32-key blocks in turn, each with its own running
 // maximum, sums and outputs in registers, and join through shared memory.  With splits > 1 the
 // joined results go to the workspace, and the CTA that arrives last at the item's counter joins
 // them in split order, so the result does not depend on the order of arrival.
-// Bound by latency, not bandwidth: 14-18 % of the copy rate on long fp32 contexts (a key's loads wait for
-// its page, its weight for a reduction over eight lanes).
+// Bound by latency and issue, not bandwidth.  Measured (GB300, 6.8 TB/s copy rate, fp32, in a captured
+// graph): 32 tokens over 2000 each, 32 heads over 8 x 128, 202 us (38 % of the copy rate; with tiles of eight
+// 439); one over 64 K with 40 heads 339 (23 %; 566 with the 144 registers that the compiler takes
+// unasked, one CTA per SM); two over 11-64 K, 9 heads over 3 x 64, 104 (28 %; 160 and 183 with three and two
+// CTAs per SM); 4-bit pages, 27 over a window of 159, 25 (38 with two CTAs).
 // Keys that no row of the tile sees are never loaded, and a weight of zero adds nothing, so what
 // lies in masked slots (an infinity, a NaN) has no effect on any row.
 #include "paged.cuh"
@@ -18,7 +21,6 @@
 namespace blend {
 namespace {
 
-constexpr int SR = 8;      // pairs of a tile
 constexpr int SW = 8;      // warps
 constexpr int SKEYS = 32;  // keys of a warp's block
 
@@ -62,6 +64,7 @@ template <bool I4, int D> __device__ __forceinline__ float scale_of(const char* 
 struct Found {
     int seq, tile;
 };
+template <int SR>
 __device__ __forceinline__ Found find_tile(const PagedAttn& a, int tile, int* sh) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     if (t == 0) sh[SW] = -1;
@@ -94,8 +97,11 @@ __device__ __forceinline__ Found find_tile(const PagedAttn& a, int tile, int* sh
     return Found{sh[SW], sh[SW + 1]};
 }
 
-template <typename T, bool I4, int D>
-__global__ void __launch_bounds__(SW * 32)
+// CTAs that an SM should hold: loads in flight against registers, as measured (fp32 models, GB300; see above).
+constexpr int simt_ctas(bool i4, int d, int sr) { return sr == 8 ? 2 : sr == 1 || d == 64 ? 4 : i4 ? 3 : 2; }
+
+template <typename T, bool I4, int D, int SR>
+__global__ void __launch_bounds__(SW * 32, simt_ctas(I4, D, SR))
     k_paged_simt(const PagedAttn a, int splits) {
     constexpr int NI = D / 32;  // four-dim pieces of a key that a lane of eight takes
     constexpr int DV = D / 32;  // output dims of a lane
@@ -107,7 +113,7 @@ __global__ void __launch_bounds__(SW * 32)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int item = blockIdx.x / splits, split = blockIdx.x % splits;
     const int head = item % a.pg.hkv;
-    const Found f = find_tile(a, item / a.pg.hkv, sh);
+    const Found f = find_tile<SR>(a, item / a.pg.hkv, sh);
     if (f.seq < 0) return;
     const SeqInfo si = seq_info(a, f.seq);
     const int pair0 = f.tile * SR, npair = min(SR, si.n_q * a.group - pair0);
@@ -137,13 +143,20 @@ __global__ void __launch_bounds__(SW * 32)
         for (int e = 0; e < DV; ++e) acc[r][e] = 0.f;
     }
     const int kk = lane >> 3, part = lane & 7;
+    // the table entry of the next block's keys is read a block ahead
+    auto entry_of = [&](int b) {
+        const int j = kr.block(b) * SKEYS + lane;
+        return b < b1 && seen_by_any(j, p0, p1, a.window, a.n_sink) ? page_entry(a.pg, f.seq, j) : 0;
+    };
+    int entry = entry_of(b0 + warp);
     for (int b = b0 + warp; b < b1; b += SW) {
         const int j0 = kr.block(b) * SKEYS, j = j0 + lane;
         const bool seen = seen_by_any(j, p0, p1, a.window, a.n_sink);
         const unsigned mask = __ballot_sync(0xffffffffu, seen);
         long long row = 0;
-        if (seen) row = page_row(a.pg, page_of(a.pg, f.seq, j, a.err), head, j & ((1 << a.pg.shift) - 1));
-#pragma unroll 2
+        if (seen) row = page_row(a.pg, checked_page(a.pg, entry, a.err), head, j & ((1 << a.pg.shift) - 1));
+        entry = entry_of(b + SW);
+#pragma unroll (SR == 8 ? 2 : 4)
         for (int ps = 0; ps < SKEYS / 4; ++ps) {
             const int key = 4 * ps + kk;
             const long long kr_row = __shfl_sync(0xffffffffu, row, key);
@@ -188,7 +201,7 @@ __global__ void __launch_bounds__(SW * 32)
             sc[warp][r][lane] = w;
         }
         __syncwarp();
-#pragma unroll 4
+#pragma unroll (SR == 8 ? 4 : 8)
         for (int key = 0; key < SKEYS; ++key) {
             const long long v_row = __shfl_sync(0xffffffffu, row, key);
             if (!((mask >> key) & 1u)) continue;
@@ -276,11 +289,23 @@ __global__ void __launch_bounds__(SW * 32)
     }
 }
 
+template <typename T, bool I4, int D> void (*simt_kernel(int sr))(PagedAttn, int) {
+    if constexpr (sizeof(T) == 4) {
+        if (sr == 1) return k_paged_simt<T, I4, D, 1>;
+        if (sr == 4) return k_paged_simt<T, I4, D, 4>;
+    }
+    return k_paged_simt<T, I4, D, 8>;
+}
+
 }  // namespace
 
 void launch_paged_attn_simt(int dtype, bool i4, const PagedAttn& a, int d, cudaStream_t s) {
-    const long long per_seq = ((long long)a.max_q * a.group + SR - 1) / SR;
-    long long tiles = (long long)a.max_rows * a.group / SR + a.pg.n_seq;
+    // Pairs of a tile: as few as every sequence's rows fill (fp32: bf16 models come here with tensor cores
+    // off alone).
+    const long long pairs = (long long)a.max_q * a.group;
+    const int sr = dtype == BLEND_BF16 || pairs > 4 ? 8 : pairs > 1 ? 4 : 1;
+    const long long per_seq = (pairs + sr - 1) / sr;
+    long long tiles = (long long)a.max_rows * a.group / sr + a.pg.n_seq;
     tiles = tiles < per_seq * a.pg.n_seq ? tiles : per_seq * a.pg.n_seq;
     const long long items = tiles * a.pg.hkv;
     if (items <= 0) return;
@@ -295,25 +320,12 @@ void launch_paged_attn_simt(int dtype, bool i4, const PagedAttn& a, int d, cudaS
         if (splits > most) splits = most;
         if (splits < 1) splits = 1;
     }
-    const unsigned grid = (unsigned)(items * splits);
-    const int n = (int)splits;
-    if (dtype == BLEND_BF16) {
-        if (i4) {
-            if (d == 64) k_paged_simt<bf16, true, 64><<<grid, SW * 32, 0, s>>>(a, n);
-            else k_paged_simt<bf16, true, 128><<<grid, SW * 32, 0, s>>>(a, n);
-        } else {
-            if (d == 64) k_paged_simt<bf16, false, 64><<<grid, SW * 32, 0, s>>>(a, n);
-            else k_paged_simt<bf16, false, 128><<<grid, SW * 32, 0, s>>>(a, n);
-        }
-    } else {
-        if (i4) {
-            if (d == 64) k_paged_simt<float, true, 64><<<grid, SW * 32, 0, s>>>(a, n);
-            else k_paged_simt<float, true, 128><<<grid, SW * 32, 0, s>>>(a, n);
-        } else {
-            if (d == 64) k_paged_simt<float, false, 64><<<grid, SW * 32, 0, s>>>(a, n);
-            else k_paged_simt<float, false, 128><<<grid, SW * 32, 0, s>>>(a, n);
-        }
-    }
+    auto kern = dtype == BLEND_BF16
+                    ? (i4 ? (d == 64 ? simt_kernel<bf16, true, 64>(sr) : simt_kernel<bf16, true, 128>(sr))
+                          : (d == 64 ? simt_kernel<bf16, false, 64>(sr) : simt_kernel<bf16, false, 128>(sr)))
+                    : (i4 ? (d == 64 ? simt_kernel<float, true, 64>(sr) : simt_kernel<float, true, 128>(sr))
+                          : (d == 64 ? simt_kernel<float, false, 64>(sr) : simt_kernel<float, false, 128>(sr)));
+    kern<<<(unsigned)(items * splits), SW * 32, 0, s>>>(a, (int)splits);
     note_launch(1);
 }
 
