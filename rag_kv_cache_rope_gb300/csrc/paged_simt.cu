@@ -5,8 +5,9 @@
 //   o = sum_j 2^(c q.k_j - m) v_j / sum_j 2^(c q.k_j - m),  c = log2(e) / sqrt(d), m the running maximum
 //
 // A CTA takes one tile of SR (row, head) pairs of one kv head (1, 4 or 8: no more than a sequence's rows
-// fill, since empty places cost as much as others) and one of `splits` shares of the keys they see; its eight warps take 32-key blocks in turn, each with its own running
-// maximum, sums and outputs in registers, and join through shared memory.  With splits > 1 the
+// fill, since empty places cost as much as others) and one of `splits` shares of the keys they see; its
+// eight warps take 32-key blocks in turn, each with its own running maximum, sums and outputs in
+// registers, and join through shared memory.  With splits > 1 the
 // joined results go to the workspace, and the CTA that arrives last at the item's counter joins
 // them in split order, so the result does not depend on the order of arrival.
 // Bound by latency and issue, not bandwidth.  Measured (GB300, 6.8 TB/s copy rate, fp32, in a captured
@@ -105,8 +106,8 @@ __global__ void __launch_bounds__(SW * 32, simt_ctas(I4, D, SR))
     k_paged_simt(const PagedAttn a, int splits) {
     constexpr int NI = D / 32;  // four-dim pieces of a key that a lane of eight takes
     constexpr int DV = D / 32;  // output dims of a lane
-    __shared__ float sq[SR][D];
-    __shared__ float sc[SW][SR][SKEYS];
+    __shared__ __align__(16) float sq[SR][D];
+    __shared__ __align__(16) float sc[SW][SR][SKEYS];
     __shared__ float so[SW][SR][D];
     __shared__ float sml[SW][SR][2];
     __shared__ int sh[SW + 4];
@@ -201,24 +202,32 @@ __global__ void __launch_bounds__(SW * 32, simt_ctas(I4, D, SR))
             sc[warp][r][lane] = w;
         }
         __syncwarp();
-#pragma unroll (SR == 8 ? 4 : 8)
-        for (int key = 0; key < SKEYS; ++key) {
-            const long long v_row = __shfl_sync(0xffffffffu, row, key);
-            if (!((mask >> key) & 1u)) continue;
-            float x[4];
-            if constexpr (DV == 4) {
-                Row<T, I4, D>::v4(a.pg.v, v_row, lane, scale_of<I4, D>(a.pg.vs, v_row, lane), x);
-            } else {
-                float y[4];
-                Row<T, I4, D>::v4(a.pg.v, v_row, lane >> 1, scale_of<I4, D>(a.pg.vs, v_row, lane >> 1), y);
-                x[0] = (lane & 1) ? y[2] : y[0];
-                x[1] = (lane & 1) ? y[3] : y[1];
+#pragma unroll (SR == 8 ? 1 : 2)
+        for (int k0 = 0; k0 < SKEYS; k0 += 4) {  // four keys, whose weights are one load per pair
+            float x[4][DV];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const long long v_row = __shfl_sync(0xffffffffu, row, k0 + u);
+                if (!((mask >> (k0 + u)) & 1u)) {
+#pragma unroll
+                    for (int e = 0; e < DV; ++e) x[u][e] = 0.f;
+                } else if constexpr (DV == 4) {
+                    Row<T, I4, D>::v4(a.pg.v, v_row, lane, scale_of<I4, D>(a.pg.vs, v_row, lane), x[u]);
+                } else {
+                    float y[4];
+                    Row<T, I4, D>::v4(a.pg.v, v_row, lane >> 1, scale_of<I4, D>(a.pg.vs, v_row, lane >> 1), y);
+                    x[u][0] = (lane & 1) ? y[2] : y[0];
+                    x[u][1] = (lane & 1) ? y[3] : y[1];
+                }
             }
 #pragma unroll
             for (int r = 0; r < SR; ++r) {
-                const float w = sc[warp][r][key];
+                const float4 w4 = *reinterpret_cast<const float4*>(&sc[warp][r][k0]);
+                const float w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-                for (int e = 0; e < DV; ++e) acc[r][e] = w != 0.f ? fmaf(w, x[e], acc[r][e]) : acc[r][e];
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int e = 0; e < DV; ++e) acc[r][e] = w[u] != 0.f ? fmaf(w[u], x[u][e], acc[r][e]) : acc[r][e];
             }
         }
         __syncwarp();
