@@ -11,10 +11,13 @@
 // joined results go to the workspace, and the CTA that arrives last at the item's counter joins
 // them in split order, so the result does not depend on the order of arrival.
 // Bound by latency and issue, not bandwidth.  Measured (GB300, 6.8 TB/s copy rate, fp32, in a captured
-// graph): 32 tokens over 2000 each, 32 heads over 8 x 128, 202 us (38 % of the copy rate; with tiles of eight
-// 439); one over 64 K with 40 heads 339 (23 %; 566 with the 144 registers that the compiler takes
-// unasked, one CTA per SM); two over 11-64 K, 9 heads over 3 x 64, 104 (28 %; 160 and 183 with three and two
-// CTAs per SM); 4-bit pages, 27 over a window of 159, 25 (38 with two CTAs).
+// graph): 32 tokens over 2000 each, 32 heads over 8 x 128, 117 us (66 % of the copy rate); one over 64 K with
+// 40 heads 258 (31 %); two over 11-64 K, 9 heads over 3 x 64, 78 (38 %); 4-bit pages, 27 over a window of
+// 159, 25.  Values are loaded four keys at a time without a branch between them (203, 340 and 105 us one by
+// one).  Before that: tiles of eight for four pairs 439 instead of 241; one CTA per SM, with the 144
+// registers that the compiler takes unasked for eight pairs, 566 instead of 339; d = 64 with three and two
+// CTAs per SM 160 and 183 instead of 104; 4-bit pages with two 38.  Keys in the same way gain 10 % for
+// four pairs and lose 7 % with 4-bit pages (registers), so they stay as they are.
 // Keys that no row of the tile sees are never loaded, and a weight of zero adds nothing, so what
 // lies in masked slots (an infinity, a NaN) has no effect on any row.
 #include "paged.cuh"
@@ -157,31 +160,37 @@ __global__ void __launch_bounds__(SW * 32, simt_ctas(I4, D, SR))
         long long row = 0;
         if (seen) row = page_row(a.pg, checked_page(a.pg, entry, a.err), head, j & ((1 << a.pg.shift) - 1));
         entry = entry_of(b + SW);
-#pragma unroll (SR == 8 ? 2 : 4)
-        for (int ps = 0; ps < SKEYS / 4; ++ps) {
-            const int key = 4 * ps + kk;
-            const long long kr_row = __shfl_sync(0xffffffffu, row, key);
-            float dot[SR] = {};
-            if ((mask >> key) & 1u) {
-                float x[NI][4];
+        constexpr int U = SR == 8 ? 2 : 4;  // passes of four keys whose loads are on their way together
+#pragma unroll 1
+        for (int ps = 0; ps < SKEYS / 4; ps += U) {
+            float x[U][NI][4];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int key = 4 * (ps + u) + kk;
+                const long long kr_row = __shfl_sync(0xffffffffu, row, key);
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
                     const int i4 = part + 8 * i;
-                    Row<T, I4, D>::k4(a.pg.k, kr_row, i4, scale_of<I4, D>(a.pg.ks, kr_row, i4), x[i]);
+                    if ((mask >> key) & 1u) Row<T, I4, D>::k4(a.pg.k, kr_row, i4, scale_of<I4, D>(a.pg.ks, kr_row, i4), x[u][i]);
+                    else x[u][i][0] = x[u][i][1] = x[u][i][2] = x[u][i][3] = 0.f;
                 }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float dot[SR] = {};
 #pragma unroll
                 for (int r = 0; r < SR; ++r)
 #pragma unroll
                     for (int i = 0; i < NI; ++i) {
                         const float4 qv = *reinterpret_cast<const float4*>(&sq[r][4 * (part + 8 * i)]);
-                        dot[r] += qv.x * x[i][0] + qv.y * x[i][1] + qv.z * x[i][2] + qv.w * x[i][3];
+                        dot[r] += qv.x * x[u][i][0] + qv.y * x[u][i][1] + qv.z * x[u][i][2] + qv.w * x[u][i][3];
                     }
-            }
 #pragma unroll
-            for (int r = 0; r < SR; ++r) {
+                for (int r = 0; r < SR; ++r) {
 #pragma unroll
-                for (int o = 1; o < 8; o <<= 1) dot[r] += __shfl_xor_sync(0xffffffffu, dot[r], o);
-                if (part == r) sc[warp][r][key] = dot[r];
+                    for (int o = 1; o < 8; o <<= 1) dot[r] += __shfl_xor_sync(0xffffffffu, dot[r], o);
+                    if (part == r) sc[warp][r][4 * (ps + u) + kk] = dot[r];
+                }
             }
         }
         __syncwarp();
