@@ -220,7 +220,9 @@ int blend_destroy(blend_handle* h);
 const char* blend_last_error(const blend_handle* h);
 /* Synchronises `stream`, then returns BLEND_OK, or BLEND_EDEVICE / BLEND_ETIMEOUT if a
  * device-side check of an earlier call on this handle failed (bad positions in a
- * caller-given set, an out-of-range shift, an expired bounded wait).  Clears the word. */
+ * caller-given set, an out-of-range shift, an expired bounded wait).  Clears the word (and what an
+ * interrupted paged_attention left in the workspace) before it returns.  The handle's other work must be
+ * on `stream` or done. */
 int blend_device_status(blend_handle* h, void* stream);
 /* Bounded device-side wait (the pages have no counterpart): enqueues on the stream a wait
  * until *flag (device int32, 4-byte aligned) is nonzero, polling at most max_polls times

@@ -528,18 +528,22 @@ int blend_destroy(blend_handle* h) {
     return BLEND_OK;
 }
 
-// Synchronises `stream`, then reports (and clears) the handle's device error word.
+// Synchronises `stream`, then reports (and clears) the handle's device error word.  Copies and resets go
+// through `stream` and are waited for: on the legacy default stream they would wait for other streams' work,
+// and a reset there is not ordered before the next call on a non-blocking stream.
 int blend_device_status(blend_handle* h, void* stream) {
     if (!h) return fail(nullptr, BLEND_EINVAL, "handle is NULL");
     cudaStream_t s = (cudaStream_t)stream;
     if (cudaStreamSynchronize(s) != cudaSuccess) return check_cuda(h, "blend_device_status");
     int32_t e = 0;
-    if (cudaMemcpy(&e, h->err, 4, cudaMemcpyDeviceToHost) != cudaSuccess)
+    if (cudaMemcpyAsync(&e, h->err, 4, cudaMemcpyDeviceToHost, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
         return check_cuda(h, "blend_device_status");
     if (e != 0) {
-        cudaMemset(h->err, 0, 4);
         // a kernel that gave up waiting (the word may hold an earlier error) may not have counted all arrivals
-        cudaMemset(h->paged_count, 0, PAGED_MAX_CTAS * sizeof(int32_t));
+        if (cudaMemsetAsync(h->err, 0, 4, s) != cudaSuccess ||
+            cudaMemsetAsync(h->paged_count, 0, PAGED_MAX_CTAS * sizeof(int32_t), s) != cudaSuccess ||
+            cudaStreamSynchronize(s) != cudaSuccess)
+            return check_cuda(h, "blend_device_status");
         return fail(h, e == BLEND_ETIMEOUT ? BLEND_ETIMEOUT : BLEND_EDEVICE,
                     "device-side check failed (code %d)", e);
     }
