@@ -165,19 +165,20 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // How the line of all items' units is shared out: share b takes units b quota .. (b + 1) quota - 1,
 // except that a border within `snap` units of an item's end moves to that end (to the nearer one of a
 // short item): a part costs its share a fixed time, and the join another.  So an item of fewer than
-// 2 snap units is never cut.
+// 2 snap units is never cut.  Totals reach 2^31 - 1, so nothing here is rounded up by an addition to them.
 struct Shares {
     int quota, snap, n;
-    __device__ __forceinline__ Shares(int total, int quota_, int snap_)
-        : quota(quota_), snap(snap_), n((total + quota_ - 1) / quota_) {}
+    __host__ __device__ __forceinline__ Shares(int total, int quota_, int snap_)
+        : quota(quota_), snap(snap_), n(parts(total, quota_)) {}
+    static __host__ __device__ __forceinline__ int parts(int total, int of) { return (total - 1) / of + 1; }  // total >= 1
     // a unit from whose item on share b has to look for its own
-    __device__ __forceinline__ int start(int b) const { return max(0, b * quota - (snap - 1)); }
+    __host__ __device__ __forceinline__ int start(int b) const { return max(0, b * quota - (snap - 1)); }
     // first and last share of the item of units [i0, i1)
-    __device__ __forceinline__ int first(int i0, int i1) const { return (i0 + min(snap, (i1 - i0 + 1) >> 1) - 1) / quota; }
-    __device__ __forceinline__ int last(int i0, int i1) const { return max((i1 - snap) / quota, first(i0, i1)); }
+    __host__ __device__ __forceinline__ int first(int i0, int i1) const { return (i0 + min(snap, i1 - i0 - ((i1 - i0) >> 1)) - 1) / quota; }
+    __host__ __device__ __forceinline__ int last(int i0, int i1) const { return max((i1 - snap) / quota, first(i0, i1)); }
     // share b's units of it, from i0
-    __device__ __forceinline__ int begin(int b, int i0, int i1) const { return b == first(i0, i1) ? 0 : b * quota - i0; }
-    __device__ __forceinline__ int end(int b, int i0, int i1) const { return b == last(i0, i1) ? i1 - i0 : (b + 1) * quota - i0; }
+    __host__ __device__ __forceinline__ int begin(int b, int i0, int i1) const { return b == first(i0, i1) ? 0 : b * quota - i0; }
+    __host__ __device__ __forceinline__ int end(int b, int i0, int i1) const { return b == last(i0, i1) ? i1 - i0 : (b + 1) * quota - i0; }
 };
 
 void launch_paged_append(int dtype, bool i4, const PageView& pg, int hq, int d, const void* k_new, long long ld_k,

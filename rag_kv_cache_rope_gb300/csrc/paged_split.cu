@@ -202,8 +202,8 @@ __global__ void __launch_bounds__(W * 32, 2)
     // parts).  Eight warps on every SM, one CTA each, measured 7.0, 7.6 and 8.6 us there, but 9.1 instead of
     // 8.8 for 63 steps and 15.6 instead of 13.8 for 1000.
     constexpr int SHORT = 6 * W;
-    const int per_item = (total + n_item - 1) / n_item;
-    const int quota = max((total + (int)gridDim.x - 1) / (int)gridDim.x, per_item < SHORT ? per_item : W);
+    const int per_item = Shares::parts(total, n_item);
+    const int quota = max(Shares::parts(total, (int)gridDim.x), per_item < SHORT ? per_item : W);
     const Shares sh(total, quota, min(2 * W, quota));
     const int share = blockIdx.x;
     if (share >= sh.n) return;

@@ -399,9 +399,10 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
     }
     __syncthreads();
     const int total = pre[n_seq];
-    const int quota = max(MIN_QUOTA, (total + n_grp - 1) / n_grp);
-    const Shares sh(max(total, 1), quota, min(SNAP, quota));
-    if (total == 0 || grp >= sh.n) return;  // both CTAs of the cluster
+    if (total == 0) return;  // both CTAs of the cluster
+    const int quota = max(MIN_QUOTA, Shares::parts(total, n_grp));
+    const Shares sh(total, quota, min(SNAP, quota));
+    if (grp >= sh.n) return;
 
     // Lanes of a tile past its rows read a Q of zeros
     for (int i = threadIdx.x; i < T::QB * QT / 16; i += T::THREADS) reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
