@@ -510,8 +510,9 @@ int paged_gather(blend_handle* h, const blend_pages* pages, const int32_t* seq, 
  * The result does not depend on timing.
  * Uses the handle's workspace: calls on one handle must not overlap, replays of captured ones
  * included.  Device-side checks (BLEND_EDEVICE): a sequence with row bounds outside 0..max_rows or
- * descending, more than max_q rows, or a length outside its table is skipped; a page index
- * outside the pool is read as page 0.  After BLEND_ETIMEOUT results are void until
+ * descending, more than max_q rows, or a length outside its table is skipped (where bounds that go down
+ * and up again let sequences claim the same rows, those rows hold any of their results and other rows may be
+ * left out); a page index outside the pool is read as page 0.  After BLEND_ETIMEOUT results are void until
  * blend_device_status has been called, which also clears what the call left in the workspace.
  * Errors: BLEND_EINVAL for NULL or unaligned tensors, bad strides, negative sizes, window or
  * n_sink, max_q < 1 with rows, out over q, or a bad blend_pages (nothing is launched). */

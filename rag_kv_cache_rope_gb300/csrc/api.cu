@@ -1462,10 +1462,10 @@ int paged_attention(blend_handle* h, const blend_pages* pages, const void* q, in
     // 16-key steps of all sequences and heads, and 128-key blocks of all their tiles, are counted in 32 bits
     const long long tokens = (long long)pages->max_pages * pages->page_tokens;
     const int tile_rows = 2 * (128 / (c.n_q_heads / c.n_kv_heads));
-    if ((long long)pages->n_seq * c.n_kv_heads * (tokens / PAGED_STEP + 1) >= (1ll << 31) ||
-        ((long long)max_rows / tile_rows + pages->n_seq) * c.n_kv_heads * (tokens / 128 + 1) >= (1ll << 31))
+    if ((long long)pages->n_seq * c.n_kv_heads * (tokens / PAGED_STEP + 1) >= PAGED_MAX_UNITS ||
+        ((long long)max_rows / tile_rows + pages->n_seq) * c.n_kv_heads * (tokens / 128 + 1) >= PAGED_MAX_UNITS)
         return fail(h, BLEND_EINVAL, "table too large: its tokens (in steps of 16 per sequence and kv head, in blocks of "
-                    "128 per tile and kv head) must stay below 2^31");
+                    "128 per tile and kv head) must stay below 2^31 - 1");
     if (max_rows == 0) return BLEND_OK;
     if (overlap(out, rows_span(h, max_rows, (long long)c.n_q_heads * c.head_dim, c.n_q_heads), q,
                 rows_span(h, max_rows, ld_q, c.n_q_heads)))

@@ -108,6 +108,14 @@ __device__ __forceinline__ SeqInfo seq_info(const PagedAttn& a, int s) {
     return i;
 }
 
+// Sums over sequences are capped: bounds that go down and up again may claim the same rows many times, so
+// that what the caller's sizes bound for ascending ones passes 32 bits.  Terms are at most `cap` < 2^31.
+__host__ __device__ __forceinline__ int add_capped(int x, int y, int cap) {
+    const unsigned s = (unsigned)x + (unsigned)y;
+    return s < (unsigned)cap ? (int)s : cap;
+}
+constexpr int PAGED_MAX_UNITS = 0x7fffffff;  // work units of a call: fewer than this
+
 // Keys that rows at positions p0..p1 of one sequence see, as blocks of BLK keys: the sinks'
 // blocks 0..n_a-1, then blocks first_b.. of the window's range (n_b of them).
 struct KeyRange {

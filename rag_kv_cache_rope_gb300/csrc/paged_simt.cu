@@ -71,6 +71,7 @@ struct Found {
 };
 template <int SR>
 __device__ __forceinline__ Found find_tile(const PagedAttn& a, int tile, int* sh) {
+    constexpr int CAP = (1 << 30) - 1;  // a sequence has at most 2^26 tiles, a launch 2^26 + 1024
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     if (t == 0) sh[SW] = -1;
     int base = 0;
@@ -81,14 +82,14 @@ __device__ __forceinline__ Found find_tile(const PagedAttn& a, int tile, int* sh
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
+            if (lane >= o) incl = add_capped(incl, y, CAP);
         }
         if (lane == 31) sh[warp] = incl;
         __syncthreads();
         int before = base, all = base;
         for (int w = 0; w < SW; ++w) {
-            if (w < warp) before += sh[w];
-            all += sh[w];
+            if (w < warp) before = add_capped(before, sh[w], CAP);
+            all = add_capped(all, sh[w], CAP);
         }
         const int excl = before + incl - mine;
         if (tile >= excl && tile < excl + mine) {

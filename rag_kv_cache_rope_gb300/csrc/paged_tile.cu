@@ -390,16 +390,21 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += y;
+                if (lane >= o) v = add_capped(v, y, PAGED_MAX_UNITS);
             }
-            if (s < n_seq) pre[s + 1] = base + v;
-            base += __shfl_sync(0xffffffffu, v, 31);
+            v = add_capped(v, base, PAGED_MAX_UNITS);
+            if (s < n_seq) pre[s + 1] = v;
+            base = __shfl_sync(0xffffffffu, v, 31);
         }
         if (lane == 0) pre[0] = 0;
     }
     __syncthreads();
     const int total = pre[n_seq];
     if (total == 0) return;  // both CTAs of the cluster
+    if (total == PAGED_MAX_UNITS) {  // sequences that claim the same rows again and again
+        if (threadIdx.x == 0) set_error(a.err, BLEND_EDEVICE);
+        return;
+    }
     const int quota = max(MIN_QUOTA, Shares::parts(total, n_grp));
     const Shares sh(total, quota, min(SNAP, quota));
     if (grp >= sh.n) return;

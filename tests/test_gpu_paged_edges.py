@@ -78,3 +78,30 @@ def test_status_is_ordered_on_its_own_stream():
     assert not busy.query()
     torch.cuda.synchronize()
     assert torch.equal(out, want) and not left.any()
+
+
+# ---------------------------------------------------------------- totals
+def test_rows_claimed_again_and_again_are_reported():
+    """Bounds that go down and up again: 512 sequences claim the same 8192 rows, more work units than 32 bits
+    count.  Nothing of it is done, and the call says so."""
+    hq, hkv, d, page, n_seq, rows, tokens = 256, 8, 64, 128, 1024, 8192, 1 << 17
+    h = handle("bf16", hq, hkv, d)
+    k = torch.zeros(1, hkv, page, d, dtype=torch.bfloat16, device="cuda")
+    pages = b.PagesRef(k, k.clone(), torch.zeros(n_seq, tokens // page, dtype=torch.int32, device="cuda"))
+    q = torch.zeros(rows, hq, d, dtype=torch.bfloat16, device="cuda")
+    out = attend(h, pages, q, [0, rows] * (n_seq // 2) + [0], [tokens] * n_seq, rows)
+    assert status(h) == b.EDEVICE and bool((out == 3.0).all())
+
+
+@pytest.mark.parametrize("dtype,fmt", [("bf16", "model"), ("bf16", "int4"), ("f32", "model")])
+def test_rows_claimed_twice(dtype, fmt):
+    """Rows that two sequences claim hold either's result; the first sequence's own rows are right."""
+    h = handle(dtype, 8, 2, 128)
+    c = filled(dtype, fmt, 2, 128, 16, [60, 60, 60], 3, poison=False)
+    q = torch.randn(80, 8, 128, device="cuda").to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    out = attend(h, c.pages, q, [0, 40, 20, 60], [60, 60, 60], 40)
+    assert status(h) == b.EDEVICE and torch.isfinite(out).all()
+    want, mag, lin = P.attention(f64(q[:40]), c.k[0], c.v[0], 60, 0, 0)
+    lim = attention_bound(dtype, fmt, want, mag, lin, 60, True)
+    assert (np.abs(f64(out[:20]).reshape(20, 8, 128) - want[:20]) <= lim[:20]).all()
+    assert bool((out[60:] == 3.0).all())

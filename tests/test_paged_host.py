@@ -63,3 +63,19 @@ def run_host(tmp_path, source):
 
 def test_shares_cover_the_line_up_to_the_largest_total(tmp_path):
     run_host(tmp_path, SHARES)
+
+
+CAPPED = r"""
+#include "paged.cuh"
+int main(void) {
+    const int cap = blend::PAGED_MAX_UNITS, half = (1 << 30) - 1;
+    if (blend::add_capped(3, 4, cap) != 7 || blend::add_capped(cap - 2, 1, cap) != cap - 1) return 1;
+    if (blend::add_capped(cap - 1, 1, cap) != cap || blend::add_capped(cap, cap, cap) != cap) return 2;
+    if (blend::add_capped(half - 1, 1, half) != half || blend::add_capped(half, half, half) != half) return 3;
+    return 0;
+}
+"""
+
+
+def test_capped_sums(tmp_path):
+    run_host(tmp_path, CAPPED)
