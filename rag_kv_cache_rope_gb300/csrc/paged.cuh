@@ -68,6 +68,14 @@ template <bool HI> __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// Two codes at bits 0..3 and 16..19 as bf16 values n, exact: in the low bits of 128 a code is 128 + n + 8.
+__device__ __forceinline__ uint32_t code_ints(uint32_t w) {
+    uint32_t x = (w & 0x000F000Fu) | 0x43004300u;
+    const uint32_t off = 0x43084308u;  // 136
+    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&off));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // Arguments of the attention kernels.
 struct PagedAttn {
     PageView pg;

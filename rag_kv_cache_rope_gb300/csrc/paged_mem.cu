@@ -137,27 +137,26 @@ __device__ __forceinline__ uint32_t k_word(const uint32_t (&c)[8]) {
 __device__ __forceinline__ uint32_t v_word(const uint32_t (&c)[8]) {
     return __byte_perm(four(c[0], c[1], c[2], c[3]), four(c[4], c[5], c[6], c[7]), 0x5410);
 }
-// A K word's values n s: a pair of codes is (n - 8) / 64 in bf16, exactly (code_pair).
+// A K word's values n s, each a product of exact numbers rounded once.  (As (n / 64) (64 s), which saves the
+// two shifts, scales from 2^122 on gave infinities, and NaN for a code of 0.)
 __device__ __forceinline__ void k_values(uint32_t w, float s, float* x) {
-    const float unit = __fmul_rn(s, CODE_UNIT);  // exact but for scales past 2^121
-    const uint32_t p[4] = {code_pair<false>(w), code_pair<true>(w), code_pair<false>(w >> 8), code_pair<true>(w >> 8)};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __fmul_rn(__uint_as_float(p[i] << 16), unit);
-        x[2 * i + 1] = __fmul_rn(__uint_as_float(p[i] & 0xffff0000u), unit);
+        const uint32_t p = code_ints(w >> (4 * i));
+        x[2 * i] = __fmul_rn(__uint_as_float(p << 16), s);
+        x[2 * i + 1] = __fmul_rn(__uint_as_float(p & 0xffff0000u), s);
     }
 }
 // A V word's values: codes 0, 1 and 2, 3 of a half are pairs once the half is repeated 12 bits up.
 __device__ __forceinline__ void v_values(uint32_t w, float s, float* x) {
-    const float unit = __fmul_rn(s, CODE_UNIT);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const uint32_t c = h ? w >> 16 : w & 0xffffu, y = c | (c << 12);
-        const uint32_t p[2] = {code_pair<false>(y), code_pair<false>(y >> 8)};
+        const uint32_t p[2] = {code_ints(y), code_ints(y >> 8)};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            x[4 * h + 2 * i] = __fmul_rn(__uint_as_float(p[i] << 16), unit);
-            x[4 * h + 2 * i + 1] = __fmul_rn(__uint_as_float(p[i] & 0xffff0000u), unit);
+            x[4 * h + 2 * i] = __fmul_rn(__uint_as_float(p[i] << 16), s);
+            x[4 * h + 2 * i + 1] = __fmul_rn(__uint_as_float(p[i] & 0xffff0000u), s);
         }
     }
 }

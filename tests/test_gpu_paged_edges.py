@@ -105,3 +105,41 @@ def test_rows_claimed_twice(dtype, fmt):
     lim = attention_bound(dtype, fmt, want, mag, lin, 60, True)
     assert (np.abs(f64(out[:20]).reshape(20, 8, 128) - want[:20]) <= lim[:20]).all()
     assert bool((out[60:] == 3.0).all())
+
+
+# ---------------------------------------------------------------- 4-bit scales of any size
+def scaled_pages(hkv, d, page, n, seed, k_exp, v_exp):
+    """n tokens of one sequence with codes -8..7 of every dim and scales of full bf16 mantissas and exponents
+    drawn from the given ranges, and their values n s in float64."""
+    rng = np.random.default_rng(seed)
+    n_pages = (n + page - 1) // page
+    ten, val = [], []
+    for lo, hi in (k_exp, v_exp):
+        codes = rng.integers(-8, 8, (n_pages, hkv, page, d))
+        sc = np.ldexp(1 + rng.integers(0, 128, (n_pages, hkv, page, d // 32)) / 128, rng.integers(lo, hi, (n_pages, hkv, page, d // 32)))
+        packed = P.pack(codes, len(ten) == 1)
+        x = P.unpack(packed, sc, len(ten) == 1)
+        val.append(np.moveaxis(x, 1, 2).reshape(-1, hkv, d)[:n])
+        ten.append((torch.from_numpy(packed).cuda(), torch.from_numpy(sc).to("cuda", torch.bfloat16)))
+    table = torch.arange(n_pages, dtype=torch.int32, device="cuda")[None].contiguous()
+    return b.PagesRef(ten[0][0], ten[1][0], table, ten[0][1], ten[1][1]), val[0], val[1]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_gather_of_scales_of_any_size(dtype, d):
+    """Every value is n s, from denormal scales to the largest whose values are finite, bit for bit."""
+    h, n, dt = handle(dtype, 4, 2, d), 600, torch.bfloat16 if dtype == "bf16" else torch.float32
+    pages, k, v = scaled_pages(2, d, 16, n, 7, (-126, 125), (118, 125))
+    ko, vo = (torch.empty(n, 2, d, dtype=dt, device="cuda") for _ in range(2))
+    b.paged_gather(h, pages, i32([0] * n), i32(list(range(n))), i32([n]), n, ko, vo)
+    assert status(h) == b.OK
+    assert torch.equal(ko.cpu(), torch.from_numpy(k).float().to(dt)) and torch.equal(vo.cpu(), torch.from_numpy(v).float().to(dt))
+    assert torch.isfinite(vo).all()  # 8 (2 - 2^-7) 2^124 at most
+    # turned: what a rotation adds is within its own rounding
+    pages, k, v = scaled_pages(2, d, 16, n, 8, (118, 123), (118, 125))
+    rot = np.arange(n) - n // 2
+    b.paged_gather(h, pages, i32([0] * n), i32(list(range(n))), i32([n]), n, ko, vo, rot=i32(rot))
+    lim = 4 * 2.0 ** -24 * np.abs(k).reshape(n, -1, 2, d // 2).sum(2).repeat(2, 1).reshape(n, -1, d)
+    want = np.stack([P.rotate(k[i], rot[i], 1e4) for i in range(n)])
+    assert (np.abs(f64(ko) - want) <= lim + (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) * (np.abs(want) + lim)).all()
