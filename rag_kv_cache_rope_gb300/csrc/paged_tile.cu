@@ -276,27 +276,22 @@ __device__ __forceinline__ float row_max(uint32_t s_col) {
     return mx;
 }
 
-// A pair's values n s: (n - 8) / 64 exactly, then rounded once as the product with 64 s.
-template <bool HI> __device__ __forceinline__ uint32_t pair_value(uint32_t w, uint32_t scale2) {
-    const uint32_t n = code_pair<HI>(w);
+// The values n s of the codes at bits 0..3 and 16..19, rounded once.
+__device__ __forceinline__ uint32_t pair_value(uint32_t w, uint32_t scale2) {
+    const uint32_t n = code_ints(w);
     const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&n), *reinterpret_cast<__nv_bfloat162*>(&scale2));
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 // The same, and what the rounding leaves (three bits, exactly).
-template <bool HI> __device__ __forceinline__ void pair_parts(uint32_t w, uint32_t scale2, uint32_t& value, uint32_t& rest) {
-    const uint32_t n = code_pair<HI>(w);
+__device__ __forceinline__ void pair_parts(uint32_t w, uint32_t scale2, uint32_t& value, uint32_t& rest) {
+    const uint32_t n = code_ints(w);
     const __nv_bfloat162 n2 = *reinterpret_cast<const __nv_bfloat162*>(&n), s2 = *reinterpret_cast<__nv_bfloat162*>(&scale2);
     const __nv_bfloat162 v = __hmul2(n2, s2), r = __hfma2(n2, s2, __hneg2(v));
     value = *reinterpret_cast<const uint32_t*>(&v);
     rest = *reinterpret_cast<const uint32_t*>(&r);
 }
-// One of two bf16 scales, twice, times 64.
-__device__ __forceinline__ uint32_t both(uint32_t w, int hi) {
-    uint32_t s2 = __byte_perm(w, w, hi ? 0x3232 : 0x1010);
-    const uint32_t unit = 0x42804280u;
-    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&s2), *reinterpret_cast<const __nv_bfloat162*>(&unit));
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
+// One of two bf16 scales, twice.
+__device__ __forceinline__ uint32_t both(uint32_t w, int hi) { return __byte_perm(w, w, hi ? 0x3232 : 0x1010); }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
@@ -932,12 +927,12 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                 for (int q = 0; q < D / 16; ++q) {
                     // word q of this half row: c = 2 (t & 1) + q / G, g = q % G  (G words per c)
                     const int c = 2 * (t & 1) + q / G, g = q % G, ch = 4 * (g & 1) + c;
-                    const uint32_t w = kw[q], hi = w >> 8;
+                    const uint32_t w = kw[q];
                     uint4 x, y;
-                    pair_parts<false>(w, sc[g], x.x, y.x);
-                    pair_parts<true>(w, sc[g], x.y, y.y);
-                    pair_parts<false>(hi, sc[g], x.z, y.z);
-                    pair_parts<true>(hi, sc[g], x.w, y.w);
+                    pair_parts(w, sc[g], x.x, y.x);
+                    pair_parts(w >> 4, sc[g], x.y, y.y);
+                    pair_parts(w >> 8, sc[g], x.z, y.z);
+                    pair_parts(w >> 12, sc[g], x.w, y.w);
                     uint8_t* to = dk + (g >> 1) * K_HALF + tk * 128 + ((ch ^ (tk & 7)) << 4);
                     *reinterpret_cast<uint4*>(to) = x;
                     *reinterpret_cast<uint4*>(to + NH * K_HALF) = y;
@@ -984,7 +979,7 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                 const uint32_t vsc = sw[D == 128 ? rank : 0];
                 const int first = D == 128 ? 0 : rank;
                 if (f16) turn(both_f16(vsc, first), both_f16(vsc, 1), [](uint32_t w, uint32_t sc) { return pair_f16(w, sc); });
-                else turn(both(vsc, first), both(vsc, 1), [](uint32_t w, uint32_t sc) { return pair_value<false>(w, sc); });
+                else turn(both(vsc, first), both(vsc, 1), [](uint32_t w, uint32_t sc) { return pair_value(w, sc); });
             }
             warp_arrive(&raw_empty[rs]);
             fence_async_smem();

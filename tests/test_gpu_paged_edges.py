@@ -7,6 +7,7 @@ import torch
 from oracle import paged_oracle as P
 from rag_kv_cache_rope_gb300 import binding as b
 from pagedcase import attention_bound, f64, filled, handle, i32
+from pagedtight import bound
 
 pytestmark = pytest.mark.gpu
 
@@ -143,3 +144,25 @@ def test_gather_of_scales_of_any_size(dtype, d):
     lim = 4 * 2.0 ** -24 * np.abs(k).reshape(n, -1, 2, d // 2).sum(2).repeat(2, 1).reshape(n, -1, d)
     want = np.stack([P.rotate(k[i], rot[i], 1e4) for i in range(n)])
     assert (np.abs(f64(ko) - want) <= lim + (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) * (np.abs(want) + lim)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("k_exp,v_exp", [((110, 115), (-100, 50)), ((122, 125), (-3, 2)), ((-110, -105), (40, 57))])
+def test_pieces_over_scales_of_any_size(dtype, d, k_exp, v_exp):
+    """Keys of every scale against queries that bring the scores to ordinary size, values up to 2^60."""
+    n, rows = 150, 40
+    h = handle(dtype, 4, 2, d)
+    pages, k, v = scaled_pages(2, d, 16, n, 9, k_exp, v_exp)
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn(rows, 4, d, generator=g).double() * 2.0 ** (-2 - k_exp[1])
+    q = q.to("cuda", torch.bfloat16 if dtype == "bf16" else torch.float32)
+    out = attend(h, pages, q, [0, rows], [n], rows, window=90, sink=5)
+    assert status(h) == b.OK
+    want, mag, lin = P.attention(f64(q), k, v, n, 90, 5)
+    got = f64(out).reshape(rows, 4, d)
+    if dtype == "bf16":  # P and n s in bf16, keys in two parts
+        lim = bound(want, mag, lin, n, [2.0 ** -8, 2.0 ** -8], 2.0 ** -8, lost=2.0 ** -30 * np.abs(v).max(), terms=2)
+    else:
+        lim = bound(want, mag, lin, n, [], 2.0 ** -24)
+    assert (np.abs(got - want) <= lim).all(), (np.abs(got - want) / lim).max()
