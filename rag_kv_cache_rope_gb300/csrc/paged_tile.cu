@@ -282,9 +282,10 @@ __device__ __forceinline__ uint32_t pair_value(uint32_t w, uint32_t scale2) {
     const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&n), *reinterpret_cast<__nv_bfloat162*>(&scale2));
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-// The same, and what the rounding leaves (three bits, exactly).
-__device__ __forceinline__ void pair_parts(uint32_t w, uint32_t scale2, uint32_t& value, uint32_t& rest) {
-    const uint32_t n = code_ints(w);
+// A 64th of the values, which saves shifts (code_pair) and goes into the scores' factor, rounded once, and what
+// the rounding leaves (three bits, exactly).
+template <bool HI> __device__ __forceinline__ void pair_parts(uint32_t w, uint32_t scale2, uint32_t& value, uint32_t& rest) {
+    const uint32_t n = code_pair<HI>(w);
     const __nv_bfloat162 n2 = *reinterpret_cast<const __nv_bfloat162*>(&n), s2 = *reinterpret_cast<__nv_bfloat162*>(&scale2);
     const __nv_bfloat162 v = __hmul2(n2, s2), r = __hfma2(n2, s2, __hneg2(v));
     value = *reinterpret_cast<const uint32_t*>(&v);
@@ -646,7 +647,8 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
         const int r_in = sp * 32 + lane;
         const uint32_t lane_off = (uint32_t)(sp * 32) << 16;
         const uint32_t o_col = tb + lane_off + O_COL;
-        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
+        const float scale = I4 ? a.scale_log2 * CODE_UNIT : a.scale_log2;
+        const float2 sc2 = make_float2(scale, scale);
         bf16* out = reinterpret_cast<bf16*>(a.out);
         uint32_t it = 0;
         bool ok = true;
@@ -683,7 +685,7 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                 // some 15 KB of instructions into the middle of it: 468 instead of 457 us for four
                 // prompt pieces of 2048 rows, window 4096, and 220 bytes of spills with 4-bit pages).
                 auto raise = [&]() {
-                    const float mxs = row_max(s_col) * a.scale_log2;
+                    const float mxs = row_max(s_col) * scale;
                     const bool need = mxs > m_used + RESCALE_LOG2;
                     rescale = __any_sync(0xffffffffu, need);
                     if (rescale) {
@@ -696,7 +698,7 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                 const bool mixed = I4 && f16 != ALL_F16;
                 if (mixed) {
                     raise();
-                    accs = make_float2(mixed_block(s_col, f16, a.scale_log2, m_used == -INFINITY ? 0.f : -m_used), 0.f);
+                    accs = make_float2(mixed_block(s_col, f16, scale, m_used == -INFINITY ? 0.f : -m_used), 0.f);
                 }
                 bool exact = !__all_sync(0xffffffffu, m_used != -INFINITY);
 #pragma unroll 1
@@ -927,12 +929,12 @@ __global__ void __launch_bounds__(TileCfg<I4, D>::THREADS, 1)
                 for (int q = 0; q < D / 16; ++q) {
                     // word q of this half row: c = 2 (t & 1) + q / G, g = q % G  (G words per c)
                     const int c = 2 * (t & 1) + q / G, g = q % G, ch = 4 * (g & 1) + c;
-                    const uint32_t w = kw[q];
+                    const uint32_t w = kw[q], hi = w >> 8;
                     uint4 x, y;
-                    pair_parts(w, sc[g], x.x, y.x);
-                    pair_parts(w >> 4, sc[g], x.y, y.y);
-                    pair_parts(w >> 8, sc[g], x.z, y.z);
-                    pair_parts(w >> 12, sc[g], x.w, y.w);
+                    pair_parts<false>(w, sc[g], x.x, y.x);
+                    pair_parts<true>(w, sc[g], x.y, y.y);
+                    pair_parts<false>(hi, sc[g], x.z, y.z);
+                    pair_parts<true>(hi, sc[g], x.w, y.w);
                     uint8_t* to = dk + (g >> 1) * K_HALF + tk * 128 + ((ch ^ (tk & 7)) << 4);
                     *reinterpret_cast<uint4*>(to) = x;
                     *reinterpret_cast<uint4*>(to + NH * K_HALF) = y;
