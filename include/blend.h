@@ -506,8 +506,9 @@ int paged_gather(blend_handle* h, const blend_pages* pages, const int32_t* seq, 
  * Keys and values of tokens no row of the call sees are not used: slots past a length may hold
  * anything, and table entries of pages without a token that some row sees are not read.  A NaN or
  * infinity in a token that some rows see reaches them, and may reach other rows of the same
- * sequence in the call.  Scores have to be finite in fp32, and values may be as large as 2^60: a row's
- * unnormalised sum, in fp32 too, holds weights of up to 2^67 together.  bf16 queries over 4-bit pages may be as large as 2^115 (beyond: NaN).
+ * sequence in the call.  Scores have to be finite in fp32 (over 4-bit pages, their parts of 32 dims
+ * also before the keys' scale is applied), and values may be as large as 2^60: a row's unnormalised sum, in fp32
+ * too, holds weights of up to 2^67 together.
  * The result does not depend on timing.
  * Uses the handle's workspace: calls on one handle must not overlap, replays of captured ones
  * included.  Device-side checks (BLEND_EDEVICE): a sequence with row bounds outside 0..max_rows or

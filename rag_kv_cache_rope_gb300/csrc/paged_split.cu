@@ -17,14 +17,15 @@
 //   O^T += V^T P^T  P^T comes from S^T by one 8x8 transpose per 8 keys (movmatrix), all in registers
 // The running maximum used for P is raised only when it grows by more than 2^8 (as in the
 // prefill's kernel); sums use the same reference, so O / l is exact.
-// 4-bit pages: codes go from shared memory to operands in registers.  Keys: a code n + 8 in the low
-// bits of a half float is the subnormal (n + 8) 2^-24, so a mask alone makes operands of a packed
-// word (codes at bits 4..7 count 16 times, and their queries a sixteenth); queries are turned into
-// fp16 with the row's own power of two, the -8 is the accumulator's start, -8 2^-24 sum q, and a
-// key's scales multiply its partial scores of each 32 dims in fp32: the scores are exact to fp32.
-// Values: a mask and one multiply-add give (n - 8) / 64 exactly (see code_pair; an offset left in the
-// sums would cancel against results that are far smaller than it), and the value's scale
-// multiplies P in fp32 before its one rounding to bf16; the 64 goes into the last division.
+// 4-bit pages: codes go from shared memory to operands in registers: a mask and one multiply-add give a
+// pair's (n - 8) / 64 exactly (see code_pair; an offset left in the sums would cancel against results that
+// are far smaller than it).  Keys: their products with the bf16 queries are exact, a key's scales multiply
+// its partial scores of each 32 dims in fp32, and the 64 goes into the scores' factor.  (A mask alone makes
+// fp16 operands (n + 8) 2^-24 for queries turned into fp16: 113 instead of 119 us for the 32 sequences below,
+// but a score was off by up to 2^-21 of the row's largest element times the keys' scales, which is much where
+// the codes at the large elements are 0.)
+// Values: the value's scale multiplies P in fp32 before its one rounding to bf16; the 64 goes into the last
+// division.
 // Measured (GB300, 6.8 TB/s copy rate), host call included: 64 sequences of 3.3-8.2 K tokens, window
 // 4096, Mistral-7B heads 163 us, 6.5 TB/s of pages; one sequence of 128 K tokens, 14B heads, 93 us, 5.7 TB/s
 // (10 us of it are finding the shares and joining 304 parts).  4-bit pages, 32 sequences of 7.3-16 K
@@ -33,8 +34,6 @@
 // Tokens that no row sees are filled with zeros instead of loaded (values, scales), so what they
 // hold does not matter.
 #include <climits>
-
-#include <cuda_fp16.h>
 
 #include "paged.cuh"
 
@@ -78,18 +77,6 @@ __device__ __forceinline__ float pow2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float2 unpack_f16(uint32_t x) { return __half22float2(*reinterpret_cast<__half2*>(&x)); }
 // The G bf16 scales of a row as fp32.
 template <int G> __device__ __forceinline__ void scales(const uint8_t* p, float (&f)[G]) {
     uint32_t w[G / 2];
@@ -141,10 +128,10 @@ __global__ void __launch_bounds__(W * 32, 2)
     __shared__ int scan[W], items[W];
     __shared__ int s_row[R], s_off[R];  // a pair's row, and its offset in the output from the item's first
     __shared__ float sm[W][R], sl[W][R], sM[R], sL[R];
-    __shared__ __align__(8) float s_start[I4 ? W : 1][G][R];  // 4-bit keys: -8 2^-24 sum q of each 32 dims
     __shared__ int last_sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r = lane >> 2, c = lane & 3;
+    const float sc = I4 ? a.scale_log2 * CODE_UNIT : a.scale_log2;  // score to exponent of 2
     const int hkv = a.pg.hkv, n_seq = a.pg.n_seq;
 
     if (tid < R) {
@@ -296,7 +283,6 @@ __global__ void __launch_bounds__(W * 32, 2)
 
         // ---- queries, asked for before the keys
         uint32_t qf[NT][KT][2];
-        uint4 raw[I4 ? NT : 1][G];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int p = nt * 8 + r;
@@ -311,8 +297,13 @@ __global__ void __launch_bounds__(W * 32, 2)
                 }
             } else {
 #pragma unroll
-                for (int g = 0; g < G; ++g)  // dims 32 g + 8 c .. +7
-                    raw[nt][g] = ok ? *reinterpret_cast<const uint4*>(qr + 32 * g + 8 * c) : make_uint4(0, 0, 0, 0);
+                for (int g = 0; g < G; ++g) {  // dims 32 g + 8 c .. +7
+                    const uint4 w = ok ? *reinterpret_cast<const uint4*>(qr + 32 * g + 8 * c) : make_uint4(0, 0, 0, 0);
+                    qf[nt][2 * g][0] = w.x;
+                    qf[nt][2 * g][1] = w.y;
+                    qf[nt][2 * g + 1][0] = w.z;
+                    qf[nt][2 * g + 1][1] = w.w;
+                }
             }
         }
         // ---- first steps on their way; the warp takes U neighbouring steps of every U W
@@ -336,59 +327,15 @@ __global__ void __launch_bounds__(W * 32, 2)
         next_entries();
 #pragma unroll
         for (int st = 0; st < STAGES - 1; ++st) load_next(st);
-        // ---- queries as B operands, and the pairs' positions
+        // ---- the pairs' positions
         int rp[NT][2];
-        float sc[NT][2];  // score to exponent of 2
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int p = nt * 8 + r;
-            float row_scale = 1.f;
-            if constexpr (I4) {
-                // by a power of two that brings the row's largest into [1, 2)
-                float top = 0.f;
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const uint32_t w[4] = {raw[nt][g].x, raw[nt][g].y, raw[nt][g].z, raw[nt][g].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
-                }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int ex = min(max((int)((__float_as_uint(top) >> 23) & 255) - 127, -100), 100);
-                const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-                row_scale = __uint_as_float((uint32_t)(127 + ex) << 23);
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const uint32_t w[4] = {raw[nt][g].x, raw[nt][g].y, raw[nt][g].z, raw[nt][g].w};
-                    float sum = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float f = (e & 1) ? down * 0.0625f : down;
-                        const uint32_t h = pack_f16(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
-                        qf[nt][2 * g + (e >> 1)][e & 1] = h;
-                        const float2 back = unpack_f16(h);  // what the products will see
-                        sum += (back.x + back.y) * ((e & 1) ? 16.f : 1.f);
-                    }
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                    if (c == 0) s_start[warp][g][p] = sum * -0x1p-21f;
-                }
-            }
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int pc = nt * 8 + 2 * c + e;
                 rp[nt][e] = pc < npair ? p0 + s_row[pc] : -1;
-                sc[nt][e] = a.scale_log2;
-                if constexpr (I4) sc[nt][e] *= 0x1p24f * __shfl_sync(0xffffffffu, row_scale, 4 * (2 * c + e));
             }
-        }
-        if constexpr (I4) __syncwarp();
-        float2 start1[G];  // one tile of pairs: held in registers
-        if constexpr (I4 && NT == 1) {
-#pragma unroll
-            for (int g = 0; g < G; ++g) start1[g] = *reinterpret_cast<const float2*>(&s_start[warp][g][2 * c]);
-        }
         float m[NT][2], ref[NT][2], l[NT][2], o[KT][NT][4];  // ref: m, or 0 while no key was seen
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -442,16 +389,13 @@ __global__ void __launch_bounds__(W * 32, 2)
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
                         const uint32_t v0 = w0[g] >> 8, v1 = w1[g] >> 8;
-                        const uint32_t ka[4] = {w0[g] & 0x000F000Fu, w1[g] & 0x000F000Fu, w0[g] & 0x00F000F0u, w1[g] & 0x00F000F0u};
-                        const uint32_t kc[4] = {v0 & 0x000F000Fu, v1 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x00F000F0u};
+                        const uint32_t ka[4] = {code_pair<false>(w0[g]), code_pair<false>(w1[g]), code_pair<true>(w0[g]), code_pair<true>(w1[g])};
+                        const uint32_t kc[4] = {code_pair<false>(v0), code_pair<false>(v1), code_pair<true>(v0), code_pair<true>(v1)};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            float2 st;
-                            if constexpr (NT == 1) st = start1[g];
-                            else st = *reinterpret_cast<const float2*>(&s_start[warp][g][nt * 8 + 2 * c]);
-                            float d[4];
-                            mma_f16(d, ka, qf[nt][2 * g][0], qf[nt][2 * g][1], st.x, st.y, st.x, st.y);
-                            mma_f16(d, kc, qf[nt][2 * g + 1][0], qf[nt][2 * g + 1][1], d[0], d[1], d[2], d[3]);
+                            float d[4] = {0.f, 0.f, 0.f, 0.f};
+                            mma(d, ka, qf[nt][2 * g][0], qf[nt][2 * g][1]);
+                            mma(d, kc, qf[nt][2 * g + 1][0], qf[nt][2 * g + 1][1]);
                             s[u][nt][0] = g ? fmaf(d[0], f0[g], s[u][nt][0]) : d[0] * f0[g];
                             s[u][nt][1] = g ? fmaf(d[1], f0[g], s[u][nt][1]) : d[1] * f0[g];
                             s[u][nt][2] = g ? fmaf(d[2], f1[g], s[u][nt][2]) : d[2] * f1[g];
@@ -481,7 +425,7 @@ __global__ void __launch_bounds__(W * 32, 2)
                     float v = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
 #pragma unroll
                     for (int u = 1; u < U; ++u) v = fmaxf(v, fmaxf(s[u][nt][e], s[u][nt][2 + e]));
-                    need = need || v * sc[nt][e] > m[nt][e] + 8.f;
+                    need = need || v * sc > m[nt][e] + 8.f;
                 }
             if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
@@ -494,7 +438,7 @@ __global__ void __launch_bounds__(W * 32, 2)
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                        const float mx = v * sc[nt][e];
+                        const float mx = v * sc;
                         if (!(mx > m[nt][e] + 8.f)) continue;
                         const float corr = pow2(m[nt][e] - mx);
                         m[nt][e] = ref[nt][e] = mx;
@@ -513,8 +457,8 @@ __global__ void __launch_bounds__(W * 32, 2)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        s[u][nt][e] = pow2(fmaf(s[u][nt][e], sc[nt][e], -ref[nt][e]));
-                        s[u][nt][2 + e] = pow2(fmaf(s[u][nt][2 + e], sc[nt][e], -ref[nt][e]));
+                        s[u][nt][e] = pow2(fmaf(s[u][nt][e], sc, -ref[nt][e]));
+                        s[u][nt][2 + e] = pow2(fmaf(s[u][nt][2 + e], sc, -ref[nt][e]));
                         l[nt][e] += s[u][nt][e] + s[u][nt][2 + e];
                     }
                 if constexpr (!I4) {

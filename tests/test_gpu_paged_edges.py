@@ -146,9 +146,64 @@ def test_gather_of_scales_of_any_size(dtype, d):
     assert (np.abs(f64(ko) - want) <= lim + (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) * (np.abs(want) + lim)).all()
 
 
+SCALES = [((110, 115), (-100, 50)), ((122, 125), (-3, 2)), ((-110, -105), (40, 57))]
+
+
+@pytest.mark.parametrize("rows", [1, 3, 8])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("k_exp,v_exp", SCALES)
+def test_few_rows_over_scales_of_any_size(rows, d, k_exp, v_exp):
+    n, h = 150, handle("bf16", 4, 1, d)
+    pages, k, v = scaled_pages(1, d, 16, n, 10, k_exp, v_exp)
+    g = torch.Generator().manual_seed(4)
+    q = (torch.randn(rows, 4, d, generator=g).double() * 2.0 ** (-2 - k_exp[1])).to("cuda", torch.bfloat16)
+    out = attend(h, pages, q, [0, rows], [n], rows, window=90, sink=5)
+    assert status(h) == b.OK
+    want, mag, lin = P.attention(f64(q), k, v, n, 90, 5)
+    # P times the values' scale is rounded once, to bf16; queries below 2^-126 have fewer bits than fp32 products
+    # keep of them: 2^-150 a product, times the largest scale
+    lim = bound(want, mag, lin + d * 2.0 ** -126 * 2.0 ** k_exp[1], n, [2.0 ** -8], 2.0 ** -8)
+    assert (np.abs(f64(out).reshape(rows, 4, d) - want) <= lim).all()
+
+
+@pytest.mark.parametrize("rows", [1, 3, 8, 40])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("fmt", ["model", "int4"])
+def test_scores_of_queries_with_a_wide_range(rows, d, fmt):
+    """Every eighth element of a query is 2^16 to 2^20 times the others, where the keys are 0: the scores are the
+    small ones', and as near as sums of those alone."""
+    n, h = 40, handle("bf16", 4, 1, d)
+    rng = np.random.default_rng(11)
+    big = np.arange(d) % 8 == 3
+    codes = rng.integers(-7, 8, (3, 1, 16, d))
+    codes[..., big] = 0
+    sc = np.ldexp(1 + rng.integers(0, 128, (3, 1, 16, d // 32)) / 128, rng.integers(10, 13, (3, 1, 16, d // 32)))
+    ones = np.full((3, 1, 16, d // 32), 0.125)
+    vc = rng.integers(-7, 8, (3, 1, 16, d))
+    table = i32([[2, 0, 1]])
+    k, v = P.unpack(P.pack(codes, False), sc, False), P.unpack(P.pack(vc, True), ones, True)
+    if fmt == "int4":
+        pages = b.PagesRef(torch.from_numpy(P.pack(codes, False)).cuda(), torch.from_numpy(P.pack(vc, True)).cuda(), table,
+                           torch.from_numpy(sc).to("cuda", torch.bfloat16), torch.from_numpy(ones).to("cuda", torch.bfloat16))
+    else:
+        k, v = P.bf16(k).astype(np.float64), P.bf16(v).astype(np.float64)
+        pages = b.PagesRef(torch.from_numpy(k).to("cuda", torch.bfloat16), torch.from_numpy(v).to("cuda", torch.bfloat16), table)
+    k, v = (np.moveaxis(x[[2, 0, 1]], 1, 2).reshape(-1, 1, d)[:n] for x in (k, v))
+    q = rng.normal(size=(rows, 4, d)) * 2.0 ** -14
+    q[..., big] *= 2.0 ** rng.integers(16, 21, (rows, 4, int(big.sum())))
+    q = torch.from_numpy(q).to("cuda", torch.bfloat16)
+    out = attend(h, pages, q, [0, rows], [n], rows)
+    assert status(h) == b.OK
+    want, mag, lin = P.attention(f64(q), k, v, n, 0, 0)
+    # weights in bf16, those of pieces over 4-bit pages in fp16
+    half = 2.0 ** -11 if fmt == "int4" and rows == 40 else 2.0 ** -8
+    lim = bound(want, mag, lin, n, [half], 2.0 ** -8, lost=2.0 ** -30 if half < 2.0 ** -8 else 0.0, terms=2 if rows == 40 else 1)
+    assert (np.abs(f64(out).reshape(rows, 4, d) - want) <= lim).all()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("k_exp,v_exp", [((110, 115), (-100, 50)), ((122, 125), (-3, 2)), ((-110, -105), (40, 57))])
+@pytest.mark.parametrize("k_exp,v_exp", SCALES)
 def test_pieces_over_scales_of_any_size(dtype, d, k_exp, v_exp):
     """Keys of every scale against queries that bring the scores to ordinary size, values up to 2^60."""
     n, rows = 150, 40
