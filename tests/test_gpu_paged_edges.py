@@ -7,7 +7,7 @@ import torch
 from oracle import paged_oracle as P
 from rag_kv_cache_rope_gb300 import binding as b
 from pagedcase import attention_bound, f64, filled, handle, i32
-from pagedtight import bound
+from pagedtight import bound, piece_bound, piece_case
 
 pytestmark = pytest.mark.gpu
 
@@ -221,3 +221,57 @@ def test_pieces_over_scales_of_any_size(dtype, d, k_exp, v_exp):
     else:
         lim = bound(want, mag, lin, n, [], 2.0 ** -24)
     assert (np.abs(got - want) <= lim).all(), (np.abs(got - want) / lim).max()
+
+
+# ---------------------------------------------------------------- pieces over 4-bit pages, tight
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("seed", [12, 13, 14])
+def test_int4_keys_of_pieces_are_exact(d, page, seed):
+    """Scores within fp32 of those of n s, for scales of full mantissas."""
+    n, rows, codes, sc, k, v, q = piece_case(d, seed)
+    h = handle("bf16", 4, 1, d)
+    n_pages = -(-n // page)
+    table = np.random.default_rng(seed).permutation(n_pages).astype(np.int32)
+    ten = []
+    for i in range(2):
+        packed = np.zeros((n_pages, 1, page, d // 2), dtype=np.uint8)
+        scale = np.full((n_pages, 1, page, d // 32), np.nan)
+        for t in range(n):
+            packed[table[t // page], :, t % page] = P.pack(codes[i, t], i == 1)
+            scale[table[t // page], :, t % page] = sc[i, t]
+        ten.append((torch.from_numpy(packed).cuda(), torch.from_numpy(scale).to("cuda", torch.bfloat16)))
+    pages = b.PagesRef(ten[0][0], ten[1][0], i32(table)[None].contiguous(), ten[0][1], ten[1][1])
+    out = attend(h, pages, torch.from_numpy(q).to("cuda", torch.bfloat16), [0, rows], [n], rows, window=12, sink=2)
+    assert status(h) == b.OK
+    want, mag, lin = P.attention(q, k, v, n, 12, 2)
+    err = np.abs(f64(out).reshape(rows, 4, d) - want) / piece_bound(want, mag, lin, v)
+    assert err.max() <= 1, err.max()
+
+
+# ---------------------------------------------------------------- between the sinks and the window
+@pytest.mark.parametrize("dtype,fmt", [("bf16", "model"), ("bf16", "int4"), ("f32", "model"), ("f32", "int4")])
+@pytest.mark.parametrize("rows", [3, 48, 200])
+@pytest.mark.parametrize("page", [16, 64, 128])
+def test_tokens_between_sinks_and_window_may_hold_anything(dtype, fmt, rows, page):
+    """NaN and infinities in every token that no row sees, a part of a block, a page and a tile at both ends."""
+    n, window, sink = 700, 60, 21
+    h = handle(dtype, 8, 2, 128)
+    c = filled(dtype, fmt, 2, 128, page, [n, n], 17, poison=False)
+    q = torch.randn(2 * rows, 8, 128, device="cuda").to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    start = [0, rows, 2 * rows]
+    want = attend(h, c.pages, q, start, [n, n], rows, window, sink)
+    assert status(h) == b.OK and torch.isfinite(want).all()
+    tok = torch.arange(sink, n - rows - window + 1, device="cuda")
+    ten = c.tensors
+    for s in range(2):
+        pg, at = ten["table"][s].long()[tok // page], tok % page
+        for i, name in enumerate(("k", "v")):
+            into = ten[name] if fmt == "model" else ten[name + "_scale"]
+            into[pg, :, at] = float("nan")
+            into[pg[i::3], :, at[i::3]] = float("inf")
+            if fmt == "int4":
+                ten[name][pg, :, at] = 0x8F
+    got = attend(h, c.pages, q, start, [n, n], rows, window, sink)
+    assert status(h) == b.OK
+    assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
