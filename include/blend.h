@@ -212,7 +212,9 @@ size_t blend_workspace_size(const blend_model_cfg* cfg, const blend_limits* lim)
 
 /* Create a handle.  `workspace` (device, >= blend_workspace_size bytes, 256-byte
  * aligned) is owned by the caller and used by the handle until blend_destroy.
- * Builds the RoPE table (angles in fp64, cos/sin stored fp32) on `stream`. */
+ * Builds the RoPE table (angles in fp64, cos/sin stored fp32) on `stream`.  A process uses one GPU: kernels
+ * with more than 48 KB of shared memory are set up on the one that is current at their first launch, and
+ * on another they are refused (BLEND_ECUDA). */
 int blend_init(const blend_model_cfg* cfg, const blend_weights* w, const blend_limits* lim,
                void* workspace, size_t ws_bytes, void* stream, blend_handle** out);
 int blend_destroy(blend_handle* h);

@@ -25,21 +25,14 @@ struct PageView {
     int hkv;
 };
 
-// Bytes of one head's K or V row in the pages, and of its scales.
-template <typename T, bool I4> __host__ __device__ constexpr int held_bytes(int d) { return I4 ? d / 2 : d * (int)sizeof(T); }
-
 __device__ __forceinline__ int page_entry(const PageView& p, int seq, int t) {
     return __ldg(p.table + (long long)seq * p.max_pages + (t >> p.shift));
 }
+// A table entry outside the pool is reported and page 0 read in its place.
 __device__ __forceinline__ int checked_page(const PageView& p, int page, int32_t* err) {
     if ((unsigned)page < (unsigned)p.n_pages) return page;
     set_error(err, BLEND_EDEVICE);
     return 0;
-}
-// The page that holds tokens [t, ...) of sequence `seq`; a table entry outside the pool is
-// reported and page 0 read in its place.
-__device__ __forceinline__ int page_of(const PageView& p, int seq, int t, int32_t* err) {
-    return checked_page(p, page_entry(p, seq, t), err);
 }
 // Row of (page, head, token in page) counted in rows of the pool: 64 bits, pools pass 2^31 elements.
 __device__ __forceinline__ long long page_row(const PageView& p, int page, int head, int in_page) {
