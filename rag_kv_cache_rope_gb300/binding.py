@@ -558,6 +558,8 @@ def paged_attention(h: Handle, pages: PagesRef, q, q_start, kv_len, max_q, out, 
         raise ValueError("out must hold as many adjacent rows as q")
     kv_len = _paged_index(pages, n_seq, "kv_len", kv_len)
     q_start = _paged_index(pages, n_seq + 1, "q_start", q_start)
+    if max(window, n_sink, max_q) >= 1 << 31:  # (the call takes 32 bits, and more would wrap)
+        raise ValueError("window, n_sink and max_q must be below 2^31")
     if rows == 0:
         return
     rc = lib().paged_attention(h.ptr, pages.ref, q.data_ptr(), ld_q, q_start, kv_len, rows, max_q, window, n_sink,

@@ -275,3 +275,20 @@ def test_tokens_between_sinks_and_window_may_hold_anything(dtype, fmt, rows, pag
     got = attend(h, c.pages, q, start, [n, n], rows, window, sink)
     assert status(h) == b.OK
     assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
+
+
+# ---------------------------------------------------------------- refusals
+def test_numbers_past_32_bits_are_refused():
+    h = handle("bf16", 8, 2, 128)
+    c = filled("bf16", "model", 2, 128, 16, [40], 3)
+    q, out = torch.zeros(5, 8, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(5, 1024, dtype=torch.bfloat16, device="cuda")
+    start, lens = i32([0, 5]), i32([40])
+    before = b.blend_launch_count()
+    for kw in (dict(window=(1 << 32) + 1), dict(window=1 << 31), dict(n_sink=(1 << 32) + 2), dict(n_sink=1 << 63)):
+        with pytest.raises(ValueError):
+            b.paged_attention(h, c.pages, q, start, lens, 5, out, **kw)
+    with pytest.raises(ValueError):
+        b.paged_attention(h, c.pages, q, start, lens, (1 << 32) + 5, out)
+    assert b.blend_launch_count() == before
+    b.paged_attention(h, c.pages, q, start, lens, 5, out, window=(1 << 31) - 1, n_sink=(1 << 31) - 1)
+    assert status(h) == b.OK
