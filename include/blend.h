@@ -476,7 +476,8 @@ typedef struct {
  * [max_n][hq][d], rows adjacent; q itself when ld_q = hq * d, else apart from the inputs' rows);
  * NULL leaves both out.  Rotations are fp32, each product and sum rounded by itself.
  * A row with seq[i] < 0 is left alone (padding).  Rows of one call must name distinct tokens:
- * where two name the same one, its row may mix theirs (no other token is touched).
+ * where two name the same one, its row may mix theirs (no other token is touched).  k_new, v_new and q lie
+ * apart from the tokens that are written.
  * Device-side checks (BLEND_EDEVICE from blend_device_status): a count outside 0..max_n is
  * clamped; a row whose sequence, token, rotation or page index is out of range is left alone.
  * Errors: BLEND_EINVAL for NULL or not 16-byte aligned tensors, row strides that are below a
@@ -489,8 +490,9 @@ int paged_append(blend_handle* h, const blend_pages* pages, const void* k_new, i
 /* Reads rows back: k_out[i], v_out[i] (device [max_n][hkv][d], model dtype) = token pos[i] of
  * sequence seq[i], the key rotated by rot[i] positions (NULL: not rotated), in fp32 and rounded
  * once.  So a chunk held in pages, in 4 bits or not, becomes rows of a contiguous blended cache at
- * its new positions.  Padding rows, checks and errors as for paged_append; a row that fails a
- * check leaves its outputs as they were.  Rows may repeat. */
+ * its new positions.  Padding rows, checks and errors as for paged_append, and BLEND_EINVAL for k_out over
+ * v_out; a row that fails a check leaves its outputs as they were.  Rows may repeat.  The outputs lie apart
+ * from the tokens that are read. */
 int paged_gather(blend_handle* h, const blend_pages* pages, const int32_t* seq, const int32_t* pos,
                  const int32_t* rot, const int32_t* n, int32_t max_n, void* k_out, void* v_out, void* stream);
 

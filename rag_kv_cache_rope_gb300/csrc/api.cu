@@ -1441,6 +1441,8 @@ int paged_gather(blend_handle* h, const blend_pages* pages, const int32_t* seq, 
     if (((uintptr_t)k_out | (uintptr_t)v_out) & 15) return fail(h, BLEND_EINVAL, "k_out/v_out must be 16-byte aligned");
     if (max_n < 0 || max_n > (1 << 24)) return fail(h, BLEND_EINVAL, "max_n=%d outside 0..2^24", max_n);
     if (max_n == 0) return BLEND_OK;
+    const long long span = rows_span(h, max_n, (long long)c.n_kv_heads * c.head_dim, c.n_kv_heads);
+    if (overlap(k_out, span, v_out, span)) return fail(h, BLEND_EINVAL, "k_out overlaps v_out");
     launch_paged_gather(c.dtype, pages->format == BLEND_PAGES_INT4, pv, c.head_dim, seq, pos, rot, n, max_n, k_out,
                         v_out, h->rope, c.max_pos, h->err, (cudaStream_t)stream);
     return check_cuda(h, "paged_gather");

@@ -292,3 +292,18 @@ def test_numbers_past_32_bits_are_refused():
     assert b.blend_launch_count() == before
     b.paged_attention(h, c.pages, q, start, lens, 5, out, window=(1 << 31) - 1, n_sink=(1 << 31) - 1)
     assert status(h) == b.OK
+
+
+def test_gathered_rows_over_each_other_are_refused():
+    h = handle("bf16", 8, 2, 128)
+    c = filled("bf16", "model", 2, 128, 16, [40], 3)
+    rows = torch.zeros(10, 2, 128, dtype=torch.bfloat16, device="cuda")
+    seq, pos, n = i32([0] * 5), i32(list(range(5))), i32([5])
+    before = b.blend_launch_count()
+    for ko, vo in ((rows[:5], rows[:5]), (rows[:5], rows[4:9]), (rows[3:8], rows[:5])):
+        with pytest.raises(b.BlendError) as e:
+            b.paged_gather(h, c.pages, seq, pos, n, 5, ko, vo)
+        assert e.value.code == b.EINVAL
+    assert b.blend_launch_count() == before
+    b.paged_gather(h, c.pages, seq, pos, n, 5, rows[:5], rows[5:])
+    assert status(h) == b.OK and rows.any()
