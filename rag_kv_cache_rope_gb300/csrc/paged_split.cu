@@ -15,6 +15,10 @@
 //   S^T = K Q^T   mma.m16n8k16: 16 keys x 8 pairs, so a group of 4 to 8 heads wastes no more than
 //                 half of the tile (with pairs as the 16-row side it would be 8 of 16 or more)
 //   O^T += V^T P^T  P^T comes from S^T by one 8x8 transpose per 8 keys (movmatrix), all in registers
+// P goes into its product as two bf16 parts (2^-16 of it is lost) for up to 16 pairs, where reading the pages
+// hides the second product: 163 us for the 64 sequences below either way, 159 and 158 for 16 sequences with three
+// rows.  With 32 pairs the products bound the kernel (265 instead of 225 us for eight rows), and over 4-bit
+// pages its issue slots do: there P is rounded to bf16 once, as in the prefill's attention.
 // The running maximum used for P is raised only when it grows by more than 2^8 (as in the
 // prefill's kernel); sums use the same reference, so O / l is exact.
 // 4-bit pages: codes go from shared memory to operands in registers: a mask and one multiply-add give a
@@ -123,6 +127,7 @@ __global__ void __launch_bounds__(W * 32, 2)
     using S = StepCfg<I4, D>;
     using Cfg = SplitCfg<I4, D, NT, W, STAGES, U>;
     constexpr int R = 8 * NT, T = W * 32, KT = D / 16, G = D / 32, OPAD = Cfg::OPAD;
+    constexpr bool P2 = !I4 && NT <= 2;  // P in two parts
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int pre[BLEND_MAX_SEQS + 1];
     __shared__ int scan[W], items[W];
@@ -462,19 +467,26 @@ __global__ void __launch_bounds__(W * 32, 2)
                         l[nt][e] += s[u][nt][e] + s[u][nt][2 + e];
                     }
                 if constexpr (!I4) {
-                    uint32_t pb[NT][2];
+                    uint32_t pb[NT][2], pl[NT][2];  // P, and what its rounding leaves
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        pb[nt][0] = transpose8(pack2(s[u][nt][0], s[u][nt][1]));
-                        pb[nt][1] = transpose8(pack2(s[u][nt][2], s[u][nt][3]));
-                    }
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float x = s[u][nt][2 * e], y = s[u][nt][2 * e + 1];
+                            const uint32_t hi = pack2(x, y);
+                            pb[nt][e] = transpose8(hi);
+                            if constexpr (P2) pl[nt][e] = transpose8(pack2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u)));
+                        }
 #pragma unroll
                     for (int t = 0; t < KT; ++t) {
                         uint32_t v[4];
                         const int tok = ((lane >> 4) << 3) + (lane & 7), ch = 2 * t + ((lane >> 3) & 1);
                         ldsm4t(v, vb + tok * S::ROW + ((ch ^ (tok & 7)) << 4));
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma(o[t][nt], v, pb[nt][0], pb[nt][1]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma(o[t][nt], v, pb[nt][0], pb[nt][1]);
+                            if constexpr (P2) mma(o[t][nt], v, pl[nt][0], pl[nt][1]);
+                        }
                     }
                 } else if (u == 0 || i + u < n_real) {  // (a missing step's place in the ring holds no values)
                     const uint8_t* vp = ring_p + (stage * U + u) * S::BYTES + S::KV;

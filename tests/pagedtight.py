@@ -35,3 +35,16 @@ def piece_case(d, seed=12):
 def piece_bound(want, mag, lin, v):
     """Weights in fp16 (2^-30 of the row's largest may be lost whole), keys exact in two parts, values exact."""
     return bound(want, mag, lin, 14, [2.0 ** -11], 2.0 ** -8, lost=2.0 ** -30 * np.abs(v).max(), terms=2)
+
+
+def few_case(d, rows, seed=15):
+    """Few rows of 4 heads over one kv head, values whose weighted sums cancel: what weights lose shows.  bf16."""
+    rng = np.random.default_rng(seed)
+    n = 60
+    q, k, v = (P.bf16(rng.normal(size=(m, w, d)).astype(np.float32)).astype(np.float64) for m, w in ((rows, 4), (n, 1), (n, 1)))
+    return n, q, k, v
+
+
+def few_bound(want, mag, lin, n):
+    """Weights in two bf16 parts: each rounding leaves 2^-8 at most, the second one of the first's rest."""
+    return bound(want, mag, lin, n, [2.0 ** -16], 2.0 ** -8)

@@ -7,7 +7,7 @@ import torch
 from oracle import paged_oracle as P
 from rag_kv_cache_rope_gb300 import binding as b
 from pagedcase import attention_bound, f64, filled, handle, i32
-from pagedtight import bound, piece_bound, piece_case
+from pagedtight import bound, few_bound, few_case, piece_bound, piece_case
 
 pytestmark = pytest.mark.gpu
 
@@ -246,6 +246,26 @@ def test_int4_keys_of_pieces_are_exact(d, page, seed):
     assert status(h) == b.OK
     want, mag, lin = P.attention(q, k, v, n, 12, 2)
     err = np.abs(f64(out).reshape(rows, 4, d) - want) / piece_bound(want, mag, lin, v)
+    assert err.max() <= 1, err.max()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [1, 2, 4])
+@pytest.mark.parametrize("seed", [15, 16])
+def test_weights_of_few_rows_keep_their_bits(d, rows, seed):
+    """Up to 16 (row, head) pairs a tile over bf16 pages: weights in two parts."""
+    n, q, k, v = few_case(d, rows, seed)
+    h = handle("bf16", 4, 1, d)
+    ten = []
+    for x in (k, v):
+        pool = torch.full((4, 1, 16, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+        for t in range(n):
+            pool[3 - t // 16, :, t % 16] = torch.from_numpy(x[t]).to("cuda", torch.bfloat16)
+        ten.append(pool)
+    out = attend(h, b.PagesRef(*ten, i32([[3, 2, 1, 0]])), torch.from_numpy(q).to("cuda", torch.bfloat16), [0, rows], [n], rows)
+    assert status(h) == b.OK
+    want, mag, lin = P.attention(q, k, v, n, 0, 0)
+    err = np.abs(f64(out).reshape(rows, 4, d) - want) / few_bound(want, mag, lin, n)
     assert err.max() <= 1, err.max()
 
 

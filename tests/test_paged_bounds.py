@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from oracle import paged_oracle as P
-from pagedtight import piece_bound, piece_case
+from pagedtight import few_bound, few_case, piece_bound, piece_case
 
 
 def worst(got, want, lim):
@@ -29,3 +29,23 @@ def test_bound_of_pieces_shows_what_keys_lose(d):
                   high + np.roll(rest, 1, 0),                         # of the token before
                   high + np.where(np.arange(d) < d // 2, rest, 0)):   # half of the products left out
         assert worst(out(wrong), want, lim) > 2
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [1, 4])
+def test_bound_of_few_rows_shows_what_weights_lose(d, rows):
+    n, q, k, v = few_case(d, rows)
+    want, mag, lin = P.attention(q, k, v, n, 0, 0)
+    lim = few_bound(want, mag, lin, n)
+
+    def out(parts):
+        got = np.zeros_like(want)
+        for i in range(rows):
+            for h in range(4):
+                s = k[:n - rows + i + 1, 0] @ q[i, h] / np.sqrt(d)
+                w = np.exp(s - s.max()).astype(np.float32)
+                high = P.bf16(w)
+                got[i, h] = (high.astype(np.float64) + (P.bf16(w - high) if parts == 2 else 0)) @ v[:len(s), 0] / w.astype(np.float64).sum()
+        return got
+
+    assert worst(out(2), want, lim) < 1 and worst(out(1), want, lim) > 2
