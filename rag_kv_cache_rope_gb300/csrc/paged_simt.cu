@@ -12,8 +12,8 @@
 // them in split order, so the result does not depend on the order of arrival.
 // Bound by latency and issue, not bandwidth.  Measured (GB300, 6.8 TB/s copy rate, fp32, in a captured
 // graph): 32 tokens over 2000 each, 32 heads over 8 x 128, 103 us (75 % of the copy rate); one over 64 K with
-// 40 heads 250 (32 %); two over 11-64 K, 9 heads over 3 x 64, 76 (39 %); 4-bit pages, 27 over a window of
-// 159, 29.  Values are loaded four keys at a time without a branch between them (203, 340 and 105 us one by
+// 40 heads 250 (32 %); two over 11-64 K, 9 heads over 3 x 64, 76 (39 %); 4-bit pages, 27 behind a window of
+// 159, 9 heads over 3 x 64, 21.  Values are loaded four keys at a time without a branch between them (203, 340 and 105 us one by
 // one).  Before that: tiles of eight for four pairs 439 instead of 241; one CTA per SM, with the 144
 // registers that the compiler takes unasked for eight pairs, 566 instead of 339; d = 64 with three and two
 // CTAs per SM 160 and 183 instead of 104; 4-bit pages with two 38.  Keys come sixteen at a time in the same
@@ -162,41 +162,63 @@ __global__ void __launch_bounds__(SW * 32, simt_ctas(I4, D, SR))
         long long row = 0;
         if (seen) row = page_row(a.pg, checked_page(a.pg, entry, a.err), head, j & ((1 << a.pg.shift) - 1));
         entry = entry_of(b + SW);
-        // passes of four keys whose loads are on their way together: four for few pairs; eight pairs and 4-bit
-        // pages have no registers for it, and branch around keys that no row sees
-        constexpr int U = SR < 8 && !I4 ? 4 : 1;
-#pragma unroll (U == 4 ? 1 : 2)
-        for (int ps = 0; ps < SKEYS / 4; ps += U) {
-            float x[U][NI][4];
-            auto seen_key = [&](int u) { return (mask >> (4 * (ps + u) + kk)) & 1u; };
+        auto add = [&](float (&dot)[SR], const float (&x)[NI][4]) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const long long kr_row = __shfl_sync(0xffffffffu, row, 4 * (ps + u) + kk);
+            for (int r = 0; r < SR; ++r)
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
-                    const int i4 = part + 8 * i;
-                    if (seen_key(u)) Row<T, I4, D>::k4(a.pg.k, kr_row, i4, scale_of<I4, D>(a.pg.ks, kr_row, i4), x[u][i]);
-                    else if (U > 1) x[u][i][0] = x[u][i][1] = x[u][i][2] = x[u][i][3] = 0.f;
+                    const float4 qv = *reinterpret_cast<const float4*>(&sq[r][4 * (part + 8 * i)]);
+                    dot[r] += qv.x * x[i][0] + qv.y * x[i][1] + qv.z * x[i][2] + qv.w * x[i][3];
+                }
+        };
+        auto keep = [&](float (&dot)[SR], int key) {
+#pragma unroll
+            for (int r = 0; r < SR; ++r) {
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) dot[r] += __shfl_xor_sync(0xffffffffu, dot[r], o);
+                if (part == r) sc[warp][r][key] = dot[r];
+            }
+        };
+        if constexpr (!I4) {
+            // passes of four keys, for few pairs the loads of four passes on their way together; eight pairs have no
+            // registers for that and branch around keys that no row sees
+            constexpr int U = SR < 8 ? 4 : 1;
+#pragma unroll (U == 4 ? 1 : 2)
+            for (int ps = 0; ps < SKEYS / 4; ps += U) {
+                float x[U][NI][4];
+                auto seen_key = [&](int u) { return (mask >> (4 * (ps + u) + kk)) & 1u; };
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const long long kr_row = __shfl_sync(0xffffffffu, row, 4 * (ps + u) + kk);
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) {
+                        if (seen_key(u)) Row<T, I4, D>::k4(a.pg.k, kr_row, part + 8 * i, 1.f, x[u][i]);
+                        else if (U > 1) x[u][i][0] = x[u][i][1] = x[u][i][2] = x[u][i][3] = 0.f;
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float dot[SR] = {};
+                    if (U > 1 || seen_key(u)) add(dot, x[u]);
+                    keep(dot, 4 * (ps + u) + kk);
                 }
             }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
+        } else {
+            // 4-bit pages: one branch around a key's loads and products (a branch each, as above: 24 instead of 21 us for
+            // 27 tokens behind a window; eight pairs over model pages are 2-4 % faster with those)
+#pragma unroll (SR == 8 ? 2 : 4)
+            for (int ps = 0; ps < SKEYS / 4; ++ps) {
+                const int key = 4 * ps + kk;
+                const long long kr_row = __shfl_sync(0xffffffffu, row, key);
                 float dot[SR] = {};
-                if (U > 1 || seen_key(u)) {
+                if ((mask >> key) & 1u) {
+                    float x[NI][4];
 #pragma unroll
-                    for (int r = 0; r < SR; ++r)
-#pragma unroll
-                        for (int i = 0; i < NI; ++i) {
-                            const float4 qv = *reinterpret_cast<const float4*>(&sq[r][4 * (part + 8 * i)]);
-                            dot[r] += qv.x * x[u][i][0] + qv.y * x[u][i][1] + qv.z * x[u][i][2] + qv.w * x[u][i][3];
-                        }
+                    for (int i = 0; i < NI; ++i)
+                        Row<T, I4, D>::k4(a.pg.k, kr_row, part + 8 * i, scale_of<I4, D>(a.pg.ks, kr_row, part + 8 * i), x[i]);
+                    add(dot, x);
                 }
-#pragma unroll
-                for (int r = 0; r < SR; ++r) {
-#pragma unroll
-                    for (int o = 1; o < 8; o <<= 1) dot[r] += __shfl_xor_sync(0xffffffffu, dot[r], o);
-                    if (part == r) sc[warp][r][4 * (ps + u) + kk] = dot[r];
-                }
+                keep(dot, key);
             }
         }
         __syncwarp();
