@@ -183,7 +183,7 @@ struct Shares {
     // a unit from whose item on share b has to look for its own
     __host__ __device__ __forceinline__ int start(int b) const { return max(0, b * quota - (snap - 1)); }
     // first and last share of the item of units [i0, i1)
-    __host__ __device__ __forceinline__ int first(int i0, int i1) const { return (i0 + min(snap, i1 - i0 - ((i1 - i0) >> 1)) - 1) / quota; }
+    __host__ __device__ __forceinline__ int first(int i0, int i1) const { return (i0 + min(snap, (int)(((unsigned)(i1 - i0) + 1u) >> 1)) - 1) / quota; }
     __host__ __device__ __forceinline__ int last(int i0, int i1) const { return max((i1 - snap) / quota, first(i0, i1)); }
     // share b's units of it, from i0
     __host__ __device__ __forceinline__ int begin(int b, int i0, int i1) const { return b == first(i0, i1) ? 0 : b * quota - i0; }
