@@ -18,23 +18,23 @@
 // P goes into its product as two bf16 parts (2^-16 of it is lost) for up to 16 pairs, where reading the pages
 // hides the second product: 163 us for the 64 sequences below either way, 159 and 158 for 16 sequences with three
 // rows.  With 32 pairs the products bound the kernel (265 instead of 225 us for eight rows), and over 4-bit
-// pages its issue slots do: there P is rounded to bf16 once, as in the prefill's attention.
+// pages its issue slots do (15 % more for the 32 sequences below, 22 % for three rows of 16): there P is
+// rounded to bf16 once, as in the prefill's attention.
 // The running maximum used for P is raised only when it grows by more than 2^8 (as in the
 // prefill's kernel); sums use the same reference, so O / l is exact.
 // 4-bit pages: codes go from shared memory to operands in registers: a mask and one multiply-add give a
 // pair's (n - 8) / 64 exactly (see code_pair; an offset left in the sums would cancel against results that
 // are far smaller than it).  Keys: their products with the bf16 queries are exact, a key's scales multiply
 // its partial scores of each 32 dims in fp32, and the 64 goes into the scores' factor.  (A mask alone makes
-// fp16 operands (n + 8) 2^-24 for queries turned into fp16: 113 instead of 119 us for the 32 sequences below,
-// but a score was off by up to 2^-21 of the row's largest element times the keys' scales, which is much where
-// the codes at the large elements are 0.)
+// fp16 operands (n + 8) 2^-24 for queries turned into fp16: 113 instead of 119 us for the 32 sequences below
+// with two CTAs per SM, but a score was off by up to 2^-21 of the row's largest element times the keys' scales,
+// which is much where the codes at the large elements are 0.)
 // Values: the value's scale multiplies P in fp32 before its one rounding to bf16; the 64 goes into the last
 // division.
 // Measured (GB300, 6.8 TB/s copy rate), host call included: 64 sequences of 3.3-8.2 K tokens, window
 // 4096, Mistral-7B heads 163 us, 6.5 TB/s of pages; one sequence of 128 K tokens, 14B heads, 93 us, 5.7 TB/s
 // (10 us of it are finding the shares and joining 304 parts).  4-bit pages, 32 sequences of 7.3-16 K
-// tokens: 111 us, 4.5 TB/s: bound by instruction issue and its dependencies (56 % of the issue slots;
-// two CTAs are what 195 registers leave room for), not by HBM (57 %).
+// tokens: 112 us, 4.4 TB/s: bound by instruction issue and its dependencies, not by HBM.
 // Tokens that no row sees are filled with zeros instead of loaded (values, scales), so what they
 // hold does not matter.
 #include <climits>
@@ -43,9 +43,6 @@
 
 namespace blend {
 namespace {
-
-constexpr int SPLIT_CTAS = 304;  // two on each of 152 SMs
-static_assert(SPLIT_CTAS <= PAGED_MAX_CTAS, "workspace");
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
@@ -113,16 +110,19 @@ template <bool I4, int D> struct StepCfg {
 };
 // U: steps of a stage (and of a pass through the softmax)
 template <bool I4, int D, int NT, int W, int STAGES, int U> struct SplitCfg {
+    static constexpr int PER_SM = I4 && NT == 1 ? 3 : 2;  // CTAs of an SM (see launch_nt)
+    static constexpr int CTAS = 152 * PER_SM;
+    static_assert(CTAS <= PAGED_MAX_CTAS, "workspace");
     static constexpr int RING = W * STAGES * U * StepCfg<I4, D>::BYTES;
     static constexpr int OPAD = D + 4;  // distinct banks for the four pairs of a quad
     static constexpr int JOIN = W * 8 * NT * OPAD * 4;
-    static constexpr int PARTS = SPLIT_CTAS * 8 * NT * 4 + W * 4 * 32 * 16;  // weights of an item's parts, sums of a round
+    static constexpr int PARTS = CTAS * 8 * NT * 4 + W * 4 * 32 * 16;  // weights of an item's parts, sums of a round
     static constexpr int MOST = RING > JOIN ? RING : JOIN;
     static constexpr int SMEM = MOST > PARTS ? MOST : PARTS;
 };
 
 template <bool I4, int D, int NT, int W, int STAGES, int U>
-__global__ void __launch_bounds__(W * 32, 2)
+__global__ void __launch_bounds__(W * 32, (SplitCfg<I4, D, NT, W, STAGES, U>::PER_SM))
     k_paged_split(const __grid_constant__ PagedAttn a) {
     using S = StepCfg<I4, D>;
     using Cfg = SplitCfg<I4, D, NT, W, STAGES, U>;
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(W * 32, 2)
     for (int w = 0; w < W; ++w) n_item += items[w];
     if (n_item == 0) return;
     n_item *= hkv;
-    // An equal share of the line, but at least a step per warp.  Leaving parts of an item and joining
+    // An equal share of the line, but at least a pass per warp.  Leaving parts of an item and joining
     // them takes about as long as five more steps of every warp, so items of fewer than six steps per
     // warp are never cut for a small total, nor those of fewer than four at a border (GB300, bf16, 8 items, in a
     // captured graph: 22 steps 7.5 us whole, 8.4 in six parts; 32 steps 8.1 either way; 44 steps 8.3 in 11
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(W * 32, 2)
     // 8.8 for 63 steps and 15.6 instead of 13.8 for 1000.
     constexpr int SHORT = 6 * W;
     const int per_item = Shares::parts(total, n_item);
-    const int quota = max(Shares::parts(total, (int)gridDim.x), per_item < SHORT ? per_item : W);
+    const int quota = max(Shares::parts(total, (int)gridDim.x), per_item < SHORT ? per_item : U * W);
     const Shares sh(total, quota, min(2 * W, quota));
     const int share = blockIdx.x;
     if (share >= sh.n) return;
@@ -690,15 +690,14 @@ template <bool I4, int D, int NT, int W, int STAGES, int U> void launch_one(cons
         return true;
     }();
     (void)ready;
-    kern<<<SPLIT_CTAS, W * 32, Cfg::SMEM, s>>>(a);
+    kern<<<Cfg::CTAS, W * 32, Cfg::SMEM, s>>>(a);
     note_launch(1);
 }
 template <bool I4, int D> void launch_nt(const PagedAttn& a, cudaStream_t s) {
     const int pairs = a.max_q * a.group;
-    // Four warps, two CTAs per SM.  4-bit pages of up to 8 pairs: two steps a pass (32 sequences of up to
-    // 16 K tokens: 111 us; one step in a ring of four 121; eight warps at 128 registers, two steps 113,
-    // 33 instead of 25 us for 128 short sequences; three CTAs at 168 registers 110, 19 instead of 17 us
-    // for one of 8 K tokens).
+    // Four warps, two CTAs per SM.  4-bit pages of up to 8 pairs: two steps a pass and three CTAs, at 165 registers (32
+    // sequences of up to 16 K tokens, 128 short ones, one of 8 K: 111.7, 33.7 and 14.0 us; two CTAs 119, 37.4 and 13.2;
+    // those with eight warps each 116, 36.5 and 14.5, or with one step a pass in a ring of four 128, 35.9 and 13.1).
     if (pairs <= 8) {
         if constexpr (I4) launch_one<I4, D, 1, 4, 3, 2>(a, s);
         else launch_one<I4, D, 1, 4, 3, 1>(a, s);

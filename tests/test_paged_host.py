@@ -35,7 +35,7 @@ static int check(int total, int len, int grid, int min_quota, int max_snap) {
 int main(void) {
     const int totals[] = {1, 2, 303, 304, 305, 9999, 1 << 20, 2147000000, 2147483343, 2147483344, 2147483646, 2147483647};
     const int lens[] = {1, 7, 8, 9, 100, 65537, (1 << 20) - 1, 1 << 20, 2147483647};
-    const int grids[] = {304, 76, 1}, snaps[] = {1, 4, 8};
+    const int grids[] = {456, 304, 76, 1}, snaps[] = {1, 4, 8};
     for (int t : totals)
         for (int len : lens)
             for (int g : grids)
