@@ -207,7 +207,8 @@ typedef struct {
 } blend_outputs;
 
 /* ---- handle ---------------------------------------------------------------- */
-/* Bytes of device workspace a handle needs for `cfg` and `lim`. 0 on bad input. */
+/* Bytes of device workspace a handle needs for `cfg` and `lim` (12 or 22 MB of it, at head_dim 64 or 128, for
+ * paged_attention's partial results). 0 on bad input. */
 size_t blend_workspace_size(const blend_model_cfg* cfg, const blend_limits* lim);
 
 /* Create a handle.  `workspace` (device, >= blend_workspace_size bytes, 256-byte

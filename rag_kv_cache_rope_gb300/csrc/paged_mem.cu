@@ -11,7 +11,7 @@
 // position, shared by all heads).  Measured (GB300, 6.8 TB/s copy rate), 16 064 rows of 8 heads x 128 into
 // bf16 pages: 25 us, 5.2 TB/s, bound by HBM; out of 4-bit pages 20 us, 4.1 TB/s, where the chain count and
 // entries, page, row is as long as the transfer (hence two rows a thread).  Into 4-bit pages the kernel
-// is bound by instruction issue, 72 % of its slots: 57 K rows 88 us, 3.4 TB/s.
+// is bound by instruction issue and its dependencies, 57 % of the slots: 57 K rows 92 us, 3.3 TB/s.
 //
 // The rotation is (x1 c - x2 s, x2 c + x1 s) with every product and sum rounded to fp32 on
 // its own (no contraction): the 4-bit codes are a rounding of these values, so their bits

@@ -33,7 +33,7 @@
 // division.
 // Measured (GB300, 6.8 TB/s copy rate), host call included: 64 sequences of 3.3-8.2 K tokens, window
 // 4096, Mistral-7B heads 163 us, 6.5 TB/s of pages; one sequence of 128 K tokens, 14B heads, 93 us, 5.7 TB/s
-// (10 us of it are finding the shares and joining 304 parts).  4-bit pages, 32 sequences of 7.3-16 K
+// (10 us of it are finding the shares and joining 304 parts).  4-bit pages, 32 sequences of 10-16 K
 // tokens: 112 us, 4.4 TB/s: bound by instruction issue and its dependencies, not by HBM.
 // Tokens that no row sees are filled with zeros instead of loaded (values, scales), so what they
 // hold does not matter.

@@ -19,9 +19,9 @@
 // row of the item sees are zeroed (they may hold anything, and 0 x NaN is NaN): by those warps,
 // or, in the few blocks at an edge, by the producer warp after the boxes have landed.  Pages without
 // a token that the item sees are not touched at all.
-// Measured (GB300): four pieces of 2048 rows, window 4096, 32 heads over 8 kv heads x 128, 457 us, 1.2
+// Measured (GB300): four pieces of 2048 rows, window 4096, 32 heads over 8 kv heads x 128, 450-474 us, 1.2
 // PFLOP/s (63 % of the library's matrix product): bound by the softmax of a block, about 1750 cycles
-// for 128 x 128 scores (tensor pipe 54 %, issue 34 %, DRAM 21 %).
+// for 128 x 128 scores (tensor pipe 54 %, issue 34 %, DRAM 16 %).
 //
 // Rounding: P to bf16 (as everywhere on tensor cores).  4-bit pages: n s has 11 significant bits.  Keys
 // are held as two bf16 parts, n s rounded and the three bits that this leaves, and S takes both (the
@@ -30,7 +30,7 @@
 // are bf16.  The choice is one bit per 32 tokens that the dequantising warp leaves for the softmax
 // (both CTAs see the same scales) and for the P.V instruction's descriptor.
 // Measured: 64-row pieces of 8 sequences of 6-8 K tokens, against 64 bits relative to the result's norm,
-// 1.7e-3, which is the result's own rounding, in 105 us.  (Keys, values and P in bf16: 3.6e-3, 76 us;
+// 1.7e-3, which is the result's own rounding, in 106 us.  (Keys, values and P in bf16: 3.6e-3, 76 us;
 // only the keys in one bf16 part: 2.7e-3, 85 us.  Of the 29 us the second part's stores and products
 // are 13, three stages instead of five 7, the look at the scales 8.  More run-ahead does not help: a
 // ring of the keys' own, free after S, with four stages of values takes 111 us.)
