@@ -23,9 +23,10 @@
 // PFLOP/s (63 % of the library's matrix product): bound by the softmax of a block, about 1750 cycles
 // for 128 x 128 scores (tensor pipe 54 %, issue 34 %, DRAM 16 %).
 //
-// Rounding: P to bf16 (as everywhere on tensor cores).  4-bit pages: n s has 11 significant bits.  Keys
-// are held as two bf16 parts, n s rounded and the three bits that this leaves, and S takes both (the
-// reduction is twice as long, over the same queries).  Values are exact in fp16 where the scales of
+// Rounding: P to bf16, once, as in the prefill's attention (a second part would be work of the softmax, which bounds
+// the kernel).  4-bit pages: n s has 11 significant bits.  Keys are held as two bf16 parts (of a 64th of n s),
+// rounded and the three bits that this leaves, and S takes both (the reduction is twice as long, over the same
+// queries).  Values are exact in fp16 where the scales of
 // 32 tokens lie within 2^-14..2^6 (or are 0), and those tokens' P is rounded to fp16 too; else both
 // are bf16.  The choice is one bit per 32 tokens that the dequantising warp leaves for the softmax
 // (both CTAs see the same scales) and for the P.V instruction's descriptor.
