@@ -76,6 +76,20 @@ extern "C" {
 #define BLEND_PAGES_MODEL 0 /* pages hold rows of the model's dtype */
 #define BLEND_PAGES_INT4 1  /* pages hold rows of 4-bit codes with a scale for each 32 dims */
 
+/* Epilogues of w4_linear. */
+#define BLEND_W4_STORE 0  /* y = x W^T */
+#define BLEND_W4_ADD 1    /* y += x W^T (fp32 y) */
+#define BLEND_W4_SWIGLU 2 /* y = silu(gate) * up, gate and up rows interleaved as in w_gu */
+
+/* Rotary layouts and frequency scalings of rope_rows. */
+#define BLEND_ROPE_HALF 0   /* pairs (i, i + rot_dim / 2) */
+#define BLEND_ROPE_PAIRS 1  /* pairs (2i, 2i + 1) */
+#define BLEND_ROPE_NONE 0   /* f_i = theta^(-2i / rot_dim) */
+#define BLEND_ROPE_LINEAR 1 /* f_i / factor: positions interpolated */
+#define BLEND_ROPE_BASE 2   /* theta * factor^(rot_dim / (rot_dim - 2)) in theta's place */
+#define BLEND_ROPE_BANDS 3  /* by bands of wavelength: long ones / factor, short ones kept */
+#define BLEND_ROPE_YARN 4   /* a ramp over the pairs from kept to / factor */
+
 #define BLEND_DEV_KV 0 /* deviation = |k-k'|^2 + |v-v'|^2 */
 #define BLEND_DEV_V 1  /* deviation = |v-v'|^2 */
 
@@ -85,6 +99,7 @@ extern "C" {
 #define BLEND_MAX_SPAN 64              /* longest span of the span rule */
 #define BLEND_MAX_ALIGN_TARGETS 131072 /* target tokens of one align_expand call */
 #define BLEND_MAX_SEQS 1024            /* sequences of one paged cache table */
+#define BLEND_MAX_TOP 32               /* alternatives of one token_logprobs row */
 #define BLEND_GU_BLOCK 16 /* gate/up row interleave of w_gu, see blend_weights */
 
 /* ---- model ----------------------------------------------------------------- */
@@ -526,6 +541,116 @@ int paged_gather(blend_handle* h, const blend_pages* pages, const int32_t* seq, 
 int paged_attention(blend_handle* h, const blend_pages* pages, const void* q, int64_t ld_q, const int32_t* q_start,
                     const int32_t* kv_len, int32_t max_rows, int32_t max_q, int32_t window, int32_t n_sink,
                     void* out, void* stream);
+
+/* ---- products with 4-bit weights ----------------------------------------------
+ * What a generated token costs is the reading of the weights: held in 4 bits they are a quarter.
+ * A weight matrix [n][k] (nn.Linear layout, as the weights above) in 4 bits: the `group` inputs
+ * group * g .. group * g + group - 1 of a row share a bf16 scale s, and weight (j, i) is (code - 8) * s
+ * with a 4-bit code 0..15.  Rows are padded to whole chunks of 128 inputs: a row holds
+ * C = ceil(k / 128) chunks of 64 bytes and C * 128 / group scales; what the padding holds is not used.
+ * 32-bit little-endian word 4t + w of a chunk (t, w < 4) holds inputs 32w + 8t + e (e < 8), input e's code at
+ * bit 4 * (e / 2) + 16 * (e % 2): sixteen bytes are a lane's operands of four 32-input steps of the
+ * kernel's matrix instructions. */
+typedef struct {
+    int32_t n;         /* rows (output features), 1..2^24 */
+    int32_t k;         /* inputs, a multiple of 8, 8..32768 */
+    int32_t group;     /* 32, 64 or 128 */
+    void* codes;       /* device [n][C * 64] bytes */
+    void* scale;       /* device bf16 [n][C * 128 / group] */
+} blend_w4;
+
+/* Packs weights: w is device [n][k] of the model dtype, ld_w elements between rows (a multiple of 16
+ * bytes).  s = bf16(max |x| / 7) of each group, code = 8 + n with n the exact quotient x / s rounded to an
+ * integer, ties to even, -7..7 (0 where s is 0).  A group with an infinity or a NaN gets a NaN scale:
+ * all its values are NaN.  Padding: codes of 8, scales of 0.
+ * Errors: BLEND_EINVAL for NULL or not 16-byte aligned pointers, bad sizes or strides, w over the packed
+ * form (nothing is launched). */
+int w4_pack(blend_handle* h, const blend_w4* w4, const void* w, int64_t ld_w, void* stream);
+
+/* Values of packed weights, (code - 8) * s rounded once to the model dtype: out is device [n][k] with
+ * ld_out elements between rows.  Errors as for w4_pack. */
+int w4_unpack(blend_handle* h, const blend_w4* w4, void* out, int64_t ld_out, void* stream);
+
+/* y[r][j] = sum over i of x[r][i] * weight (j, i) for rows r < n_rows (at most 2^18): x device [n_rows][k] of the
+ * model dtype, ld_x elements between rows (a multiple of 16 bytes); sums in fp32, codes and inputs enter
+ * them without rounding.  epi: BLEND_W4_STORE writes y device [n_rows][n]; BLEND_W4_ADD adds to it;
+ * BLEND_W4_SWIGLU (n a multiple of 2 * BLEND_GU_BLOCK, rows interleaved as in w_gu) writes
+ * silu(gate) * up, y device [n_rows][n / 2].  y is of y_dtype (BLEND_F32 | BLEND_BF16; F32 for
+ * BLEND_W4_ADD) with ld_y elements between rows, any alignment of its elements; rows of y stay apart
+ * from x.  Inputs and scales have to be finite, |x| below 2^127; an infinity or a NaN in a row of x can make
+ * that row of y NaN, no other.  The result does not depend on timing.
+ * Errors: BLEND_EINVAL for NULL or unaligned pointers, bad sizes, strides, group, dtype or epi, y over
+ * x (nothing is launched). */
+int w4_linear(blend_handle* h, const blend_w4* w4, const void* x, int64_t ld_x, int32_t n_rows, void* y,
+              int64_t ld_y, int32_t y_dtype, int32_t epi, void* stream);
+
+/* ---- log probabilities --------------------------------------------------------
+ * What is read off the logits of n_rows tokens (logits device [n_rows][vocab] of `dtype`, BLEND_F32 |
+ * BLEND_BF16, ld elements between rows, any alignment of its elements).  With z = scale * logits (scale:
+ * 1 / temperature, positive) and p = softmax(z), per row and in fp32:
+ *   logp[r][i] = log p of token ids[r][i], i < n_ids (ids, logp device [n_rows][n_ids]; 0 for an id
+ *   below 0, which stands for no token);
+ *   entropy[r] = - sum p log p (device [n_rows], or NULL);
+ *   top_id[r][j], top_logp[r][j], j < top: the `top` (0..BLEND_MAX_TOP, at most vocab) tokens of highest
+ *   logit, descending, ties by token ascending, -0 == +0, NaN last (device [n_rows][top], NULL with
+ *   top 0; top_logp may be NULL).
+ * A logit of -infinity is a token that is not allowed: log p is -infinity and it adds nothing.  A row
+ * that allows nothing has log p of -infinity everywhere and an entropy of 0.  A NaN or +infinity makes
+ * its row's log p and entropy NaN; top_id is still the ranking above.  Masks may be as low as the type
+ * goes, also in a row that holds nothing else.  Deterministic.  Rows of logits are read once (a few parts of
+ * a row twice for the ranking).
+ * Device-side check: an id of vocab or more gives NaN and BLEND_EDEVICE from blend_device_status (the
+ * handle is used only for that).  Errors: BLEND_EINVAL for NULL or unaligned pointers, bad sizes, dtype,
+ * scale or top (nothing is launched). */
+int token_logprobs(blend_handle* h, const void* logits, int64_t ld, int32_t dtype, int32_t n_rows, int32_t vocab,
+                   float scale, const int32_t* ids, int32_t n_ids, float* logp, float* entropy, int32_t top,
+                   int32_t* top_id, float* top_logp, void* stream);
+
+/* ---- rotary positions of other layouts ----------------------------------------
+ * Rotation of the first rot_dim dims of a head (the others are copied): pair i turns by the angle
+ * rot * f_i, (x1, x2) -> magnitude * (x1 cos - x2 sin, x2 cos + x1 sin).  Pairs by `layout`, f_i by `scaling`, with
+ * e_i = theta^(-2i / rot_dim) and turns_i = trained_len * e_i / (2 pi):
+ *   NONE    e_i
+ *   LINEAR  e_i / factor
+ *   BASE    e_i with theta * factor^(rot_dim / (rot_dim - 2))
+ *   BANDS   e_i * (m + (1 - m) / factor), m = (turns_i - low) / (high - low) held to 0..1: pairs that turn
+ *           less than `low` times over the trained length are interpolated, those above `high` kept
+ *   YARN    e_i * (m + (1 - m) / factor), m = 1 - (i - a) / max(b - a, 0.001) held to 0..1, where a =
+ *           max(0, floor(D(high))), b = min(rot_dim - 1, ceil(D(low))) and D(t) = rot_dim * ln(trained_len /
+ *           (2 pi t)) / (2 ln theta), the pair that turns t times
+ * Angles are formed as a 64-bit fraction of a turn, so far positions lose nothing, and no table limits
+ * them; cos and sin are fp32.  (The other calls rotate by the handle's rope_theta in the plain half layout;
+ * rows rotated here go into paged_append with a rot of zeros.) */
+typedef struct {
+    int32_t layout;      /* BLEND_ROPE_HALF | BLEND_ROPE_PAIRS */
+    int32_t rot_dim;     /* a multiple of 16, 16..head_dim */
+    int32_t scaling;     /* BLEND_ROPE_NONE .. BLEND_ROPE_YARN */
+    int32_t trained_len; /* BANDS, YARN: positions the model was trained on, >= 1 */
+    double theta;        /* above 1 */
+    double factor;       /* >= 1 (unused by NONE) */
+    double low, high;    /* BANDS, YARN: 0 < low < high */
+    float magnitude;     /* factor on the rotated dims (YaRN's attention factor); 1 for cached keys that move */
+} blend_rope;
+/* Rows of one kind (keys, or queries) over n_layers layers: [n_layers][rows][heads][head_dim] of the model
+ * dtype, rows and layers any multiple of 16 bytes apart (strides in elements), heads adjacent. */
+typedef struct {
+    const void* src;
+    void* dst;           /* src itself where the strides are the same, else apart from every src */
+    int64_t src_row, src_layer, dst_row, dst_layer;
+    int32_t heads;       /* 1..2^16 */
+    int32_t n_layers;    /* 1..2^16 */
+} blend_rope_rows;
+
+/* Rotates row i < *n (device scalar, at most max_n) of every layer of parts[0..n_parts-1] (host; one or
+ * two parts, e.g. the queries and keys of a projection, or the cached keys of all layers) by rot[i] positions
+ * (device [max_n], |rot[i]| <= 2^24; negative: back).  Rows with rot 0 and magnitude 1 are copied bit for
+ * bit; fp32 arithmetic, one rounding.
+ * Device-side checks (BLEND_EDEVICE from blend_device_status): a count outside 0..max_n is clamped; a row
+ * whose rot is out of range is left alone.  Errors: BLEND_EINVAL for NULL or not 16-byte aligned pointers,
+ * bad strides, sizes or blend_rope, a dst that meets a src (unless it is its own) or the other dst (nothing
+ * is launched). */
+int rope_rows(blend_handle* h, const blend_rope* rope, const blend_rope_rows* parts, int32_t n_parts,
+              const int32_t* rot, const int32_t* n, int32_t max_n, void* stream);
 
 #ifdef __cplusplus
 }

@@ -29,11 +29,18 @@ MAX_ALIGN_TARGETS = 131072
 GU_BLOCK = 16
 PAGES_MODEL, PAGES_INT4 = 0, 1
 MAX_SEQS = 1024
+MAX_TOP = 32
+W4_STORE, W4_ADD, W4_SWIGLU = 0, 1, 2
+ROPE_HALF, ROPE_PAIRS = 0, 1
+ROPE_NONE, ROPE_LINEAR, ROPE_BASE, ROPE_BANDS, ROPE_YARN = 0, 1, 2, 3, 4
 
 MODES = {"ext": SEL_EXT, "hkvd": SEL_HKVD, "forced": SEL_FORCED, "full": SEL_FULL, "epic": SEL_EPIC}
 BUDGETS = {"final": BUDGET_FINAL, "candidate": BUDGET_CANDIDATE}
 DEVMODES = {"kv": DEV_KV, "v": DEV_V}
 GROUP_RULES = {"window": GROUP_WINDOW, "span": GROUP_SPAN}
+W4_EPIS = {"store": W4_STORE, "add": W4_ADD, "swiglu": W4_SWIGLU}
+ROPE_LAYOUTS = {"half": ROPE_HALF, "pairs": ROPE_PAIRS}
+ROPE_SCALINGS = {"none": ROPE_NONE, "linear": ROPE_LINEAR, "base": ROPE_BASE, "bands": ROPE_BANDS, "yarn": ROPE_YARN}
 
 
 class BlendError(RuntimeError):
@@ -90,6 +97,21 @@ class Pages(C.Structure):
                 ("k_scale", C.c_void_p), ("v_scale", C.c_void_p)]
 
 
+class W4(C.Structure):
+    _fields_ = [("n", C.c_int32), ("k", C.c_int32), ("group", C.c_int32), ("codes", C.c_void_p), ("scale", C.c_void_p)]
+
+
+class Rope(C.Structure):
+    _fields_ = [("layout", C.c_int32), ("rot_dim", C.c_int32), ("scaling", C.c_int32), ("trained_len", C.c_int32),
+                ("theta", C.c_double), ("factor", C.c_double), ("low", C.c_double), ("high", C.c_double),
+                ("magnitude", C.c_float)]
+
+
+class RopeRows(C.Structure):
+    _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p), ("src_row", C.c_int64), ("src_layer", C.c_int64),
+                ("dst_row", C.c_int64), ("dst_layer", C.c_int64), ("heads", C.c_int32), ("n_layers", C.c_int32)]
+
+
 _lib = None
 
 
@@ -138,6 +160,11 @@ def lib() -> C.CDLL:
             "paged_append": (C.c_int, [vp, C.POINTER(Pages), vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, i32, vp]),
             "paged_gather": (C.c_int, [vp, C.POINTER(Pages), vp, vp, vp, vp, i32, vp, vp, vp]),
             "paged_attention": (C.c_int, [vp, C.POINTER(Pages), vp, i64, vp, vp, i32, i32, i32, i32, vp, vp]),
+            "w4_pack": (C.c_int, [vp, C.POINTER(W4), vp, i64, vp]),
+            "w4_unpack": (C.c_int, [vp, C.POINTER(W4), vp, i64, vp]),
+            "w4_linear": (C.c_int, [vp, C.POINTER(W4), vp, i64, i32, vp, i64, i32, i32, vp]),
+            "token_logprobs": (C.c_int, [vp, vp, i64, i32, i32, i32, C.c_float, vp, i32, vp, vp, i32, vp, vp, vp]),
+            "rope_rows": (C.c_int, [vp, C.POINTER(Rope), C.POINTER(RopeRows), i32, vp, vp, i32, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -153,7 +180,8 @@ EXPORTED = ("blend_workspace_size", "blend_init", "blend_destroy", "blend_last_e
             "blend_prefill", "importance_scores", "blend_profile", "blend_profile_stages", "blend_wait_flag", "blend_profile_read",
             "blend_profile_name", "blend_launch_count", "topk_select_dilate_noalloc", "span_select",
             "align_expand", "aux_attention_scores", "blend_ratio_controller", "blend_pick_storage",
-            "paged_append", "paged_gather", "paged_attention")
+            "paged_append", "paged_gather", "paged_attention", "w4_pack", "w4_unpack", "w4_linear",
+            "token_logprobs", "rope_rows")
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -564,6 +592,194 @@ def paged_attention(h: Handle, pages: PagesRef, q, q_start, kv_len, max_q, out, 
         return
     rc = lib().paged_attention(h.ptr, pages.ref, q.data_ptr(), ld_q, q_start, kv_len, rows, max_q, window, n_sink,
                                out.data_ptr(), s)
+    if rc:
+        _check(rc, h)
+
+
+# ---------------------------------------------------------------- behind the cache: tokens
+# (Called once or more per layer and token, as the paged calls: each property is read once.)
+def _token_stream(index: int, stream):
+    """The call's stream: the tensors' GPU must be the current one, and the stream's."""
+    if index < 0:
+        raise ValueError("the tensors are not on a GPU")
+    if torch.cuda.current_device() != index or (stream is not None and stream.device_index != index):
+        raise ValueError(f"the tensors are on cuda:{index}: make it the current device and use a stream of it")
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _matrix(t: torch.Tensor, what: str, dtype, index: int, rows: Optional[int], cols: int) -> int:
+    """Distance between the rows of t [rows][cols] in elements (neighbouring columns adjacent)."""
+    sh, st = t.shape, t.stride()
+    if len(sh) != 2 or sh[1] != cols or (rows is not None and sh[0] != rows) or (st[1] != 1 and cols > 1):
+        raise ValueError(f"{what} must be [{'rows' if rows is None else rows}][{cols}] with adjacent columns")
+    if t.dtype is not dtype or t.get_device() != index:
+        raise ValueError(f"{what} must be {dtype} on cuda:{index}")
+    return st[0] if sh[0] > 1 else cols
+
+
+def _model_dtype(h: Handle):
+    return torch.bfloat16 if h.cfg.dtype == BF16 else torch.float32
+
+
+class W4Ref:
+    """Host-side description of 4-bit weights [n][k] (see blend_w4): codes uint8 [n][chunks * 64], scale
+    bf16 [n][chunks * 128 / group], chunks = ceil(k / 128), contiguous and on one GPU."""
+
+    def __init__(self, codes: torch.Tensor, scale: torch.Tensor, k: int, group: int = 128):
+        if group not in (32, 64, 128):
+            raise ValueError("group must be 32, 64 or 128")
+        chunks = (k + 127) // 128
+        n = codes.shape[0]
+        if codes.dtype != torch.uint8 or tuple(codes.shape) != (n, chunks * 64):
+            raise ValueError(f"codes must be uint8 [n][{chunks * 64}]")
+        if scale.dtype != torch.bfloat16 or tuple(scale.shape) != (n, chunks * (128 // group)):
+            raise ValueError(f"scale must be bf16 [{n}][{chunks * (128 // group)}]")
+        if not codes.is_contiguous() or not scale.is_contiguous() or codes.device != scale.device:
+            raise ValueError("codes and scale must be contiguous and on one device")
+        self.codes, self.scale, self.n, self.k, self.group = codes, scale, n, k, group
+        self.index = codes.get_device()
+        self.c = W4(n, k, group, codes.data_ptr(), scale.data_ptr())
+        self.ref = C.byref(self.c)
+
+    @classmethod
+    def empty(cls, n: int, k: int, group: int = 128, device="cuda") -> "W4Ref":
+        chunks = (k + 127) // 128
+        return cls(torch.empty(n, chunks * 64, dtype=torch.uint8, device=device),
+                   torch.empty(n, chunks * (128 // group), dtype=torch.bfloat16, device=device), k, group)
+
+
+def w4_layout(codes: torch.Tensor) -> torch.Tensor:
+    """Codes 0..15 [n][k] (integers; weight = (code - 8) * scale) in the packed rows of blend_w4."""
+    n, k = codes.shape
+    u = torch.nn.functional.pad(codes.to(torch.uint8), (0, -k % 128), value=8)
+    u = u.reshape(n, -1, 4, 4, 4, 2).permute(0, 1, 3, 2, 5, 4).reshape(n, -1, 2)  # chunk, part, step, half, pair
+    return (u[..., 0] | (u[..., 1] << 4)).contiguous()
+
+
+def w4_pack(h: Handle, w: torch.Tensor, w4: W4Ref, stream=None):
+    """w: [n][k] of the model's dtype (rows at any stride of 16 bytes)."""
+    s = _token_stream(w4.index, stream)
+    ld = _matrix(w, "w", _model_dtype(h), w4.index, w4.n, w4.k)
+    rc = lib().w4_pack(h.ptr, w4.ref, w.data_ptr(), ld, s)
+    if rc:
+        _check(rc, h)
+
+
+def w4_unpack(h: Handle, w4: W4Ref, out: torch.Tensor, stream=None):
+    """out: [n][k] of the model's dtype (rows at any stride of 16 bytes)."""
+    s = _token_stream(w4.index, stream)
+    ld = _matrix(out, "out", _model_dtype(h), w4.index, w4.n, w4.k)
+    rc = lib().w4_unpack(h.ptr, w4.ref, out.data_ptr(), ld, s)
+    if rc:
+        _check(rc, h)
+
+
+def w4_linear(h: Handle, w4: W4Ref, x: torch.Tensor, y: torch.Tensor, epi: str = "store", stream=None):
+    """x: [rows][k] of the model's dtype (rows at any stride of 16 bytes); y: [rows][n] ([n / 2] for
+    "swiglu"), fp32 or bf16 (fp32 for "add"), rows at any stride."""
+    s = _token_stream(w4.index, stream)
+    code = W4_EPIS[epi]
+    dt = y.dtype
+    if dt is not torch.float32 and dt is not torch.bfloat16:
+        raise ValueError("y must be fp32 or bf16")
+    rows = x.shape[0]
+    ld_x = _matrix(x, "x", _model_dtype(h), w4.index, None, w4.k)
+    ld_y = _matrix(y, "y", dt, w4.index, rows, w4.n // 2 if code == W4_SWIGLU else w4.n)
+    if rows == 0:
+        return
+    rc = lib().w4_linear(h.ptr, w4.ref, x.data_ptr(), ld_x, rows, y.data_ptr(), ld_y, F32 if dt is torch.float32 else BF16,
+                         code, s)
+    if rc:
+        _check(rc, h)
+
+
+def token_logprobs(h: Handle, logits: torch.Tensor, ids=None, logp=None, entropy=None, top_id=None, top_logp=None,
+                   scale: float = 1.0, stream=None):
+    """logits: [rows][vocab], fp32 or bf16, rows at any stride; ids int32 and logp fp32 [rows][n_ids]; entropy
+    fp32 [rows]; top_id int32 and top_logp fp32 [rows][top].  What is None is left out."""
+    dt, index = logits.dtype, logits.get_device()
+    s = _token_stream(index, stream)
+    if dt is not torch.float32 and dt is not torch.bfloat16:
+        raise ValueError("logits must be fp32 or bf16")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows][vocab]")
+    rows, vocab = logits.shape
+    ld = _matrix(logits, "logits", dt, index, rows, vocab)
+    if (ids is None) != (logp is None):
+        raise ValueError("ids and logp go together")
+
+    def flat(t, what, dtype, width):
+        if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous() or tuple(t.shape) != width:
+            raise ValueError(f"{what} must be contiguous {dtype} of shape {width} on cuda:{index}")
+        return t.data_ptr()
+
+    n_ids = top = 0
+    p_ids = p_logp = p_ent = p_top = p_top_logp = None
+    if ids is not None:
+        n_ids = ids.shape[1] if ids.dim() == 2 else -1
+        p_ids, p_logp = flat(ids, "ids", torch.int32, (rows, n_ids)), flat(logp, "logp", torch.float32, (rows, n_ids))
+    if entropy is not None:
+        p_ent = flat(entropy, "entropy", torch.float32, (rows,))
+    if top_id is not None:
+        top = top_id.shape[1] if top_id.dim() == 2 else -1
+        p_top = flat(top_id, "top_id", torch.int32, (rows, top))
+    if top_logp is not None:
+        if top_id is None:
+            raise ValueError("top_logp goes with top_id")
+        p_top_logp = flat(top_logp, "top_logp", torch.float32, (rows, top))
+    if rows == 0:
+        return
+    rc = lib().token_logprobs(h.ptr, logits.data_ptr(), ld, F32 if dt is torch.float32 else BF16, rows, vocab, scale, p_ids,
+                              n_ids, p_logp, p_ent, top, p_top, p_top_logp, s)
+    if rc:
+        _check(rc, h)
+
+
+def rope_desc(theta: float, rot_dim: int, layout: str = "half", scaling: str = "none", factor: float = 1.0,
+              low: float = 0.0, high: float = 0.0, trained_len: int = 0, magnitude: float = 1.0) -> Rope:
+    """Rotary layout and frequencies of a model (see blend_rope)."""
+    return Rope(ROPE_LAYOUTS[layout], rot_dim, ROPE_SCALINGS[scaling], trained_len, theta, factor, low, high, magnitude)
+
+
+def _rope_part(h: Handle, src: torch.Tensor, dst: torch.Tensor, heads: int, max_n: int, what: str) -> RopeRows:
+    """src, dst: [rows][heads][head dim] or [layers][rows][heads][head dim]."""
+    d = h.cfg.head_dim
+    st = []
+    for t in (src, dst):
+        sh, sr = t.shape, t.stride()
+        n = len(sh)
+        if n not in (3, 4) or sh[n - 2] != heads or sh[n - 1] != d or sr[n - 1] != 1 or (heads > 1 and sr[n - 2] != d):
+            raise ValueError(f"{what} must be [rows][{heads}][{d}] or [layers][rows][{heads}][{d}] with adjacent heads")
+        if sh[n - 3] < max_n:
+            raise ValueError("fewer rows than max_n")
+        st.append((sr[n - 3] if sh[n - 3] > 1 else heads * d, sr[0] if n == 4 else 0, sh[0] if n == 4 else 1))
+    if st[0][2] != st[1][2]:
+        raise ValueError(f"{what} and its output must have the same layers")
+    return RopeRows(src.data_ptr(), dst.data_ptr(), st[0][0], st[0][1], st[1][0], st[1][1], heads, st[0][2])
+
+
+def rope_rows(h: Handle, rope: Rope, k, k_out, rot, n, max_n, q=None, q_out=None, stream=None):
+    """k, k_out: [rows][kv heads][head dim], or [layers][rows][..], of the model's dtype (rows at any stride
+    of 16 bytes); q, q_out the same with the model's query heads; rot int32 per row; n a device int32 count of
+    at most max_n rows.  An output may be its own input."""
+    index = k.get_device()
+    s = _token_stream(index, stream)
+    dt = _model_dtype(h)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    for t, what in ((k, "k"), (k_out, "k_out"), (q, "q"), (q_out, "q_out")):
+        if t is not None and (t.dtype is not dt or t.get_device() != index):
+            raise ValueError(f"{what} must be of the model's dtype and on cuda:{index}")
+    for t, what, least in ((rot, "rot", max_n), (n, "n", 1)):
+        if t.dtype is not torch.int32 or t.numel() < least or not t.is_contiguous() or t.get_device() != index:
+            raise ValueError(f"{what} must be contiguous int32 of at least {least} entries on cuda:{index}")
+    parts = (RopeRows * 2)()
+    parts[0] = _rope_part(h, k, k_out, h.cfg.n_kv_heads, max_n, "k")
+    if q is not None:
+        parts[1] = _rope_part(h, q, q_out, h.cfg.n_q_heads, max_n, "q")
+    if max_n == 0 or parts[0].n_layers == 0:
+        return
+    rc = lib().rope_rows(h.ptr, C.byref(rope), parts, 1 if q is None else 2, rot.data_ptr(), n.data_ptr(), max_n, s)
     if rc:
         _check(rc, h)
 

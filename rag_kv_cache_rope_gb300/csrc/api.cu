@@ -17,6 +17,7 @@
 #include "common.cuh"
 #include "gemm_tc.cuh"
 #include "paged.cuh"
+#include "tokens.cuh"
 
 namespace {
 thread_local std::string g_err;
@@ -1505,4 +1506,247 @@ int paged_attention(blend_handle* h, const blend_pages* pages, const void* q, in
     if (!tc) launch_paged_attn_simt(c.dtype, i4, a, c.head_dim, s);
     else if (!pieces || !uniform) launch_paged_attn_split(i4, a, c.head_dim, s);
     return check_cuda(h, "paged_attention");
+}
+
+// ---------------------------------------------------------------- behind the cache: tokens
+namespace {
+// A launcher's code as the call's status (a CUDA error's text where there is one).
+int launched(blend_handle* h, int rc, const char* where) {
+    if (const int e = check_cuda(h, where)) return e;
+    return rc == BLEND_OK ? BLEND_OK : fail(h, rc, "%s: the kernel could not be set up on this device", where);
+}
+
+// Checks a blend_w4 and fills the kernels' view of it.
+int view_w4(blend_handle* h, const blend_w4* w, W4View* v) {
+    if (!w) return fail(h, BLEND_EINVAL, "w4 is NULL");
+    if (w->n < 1 || w->n > (1 << 24) || w->k < 8 || w->k > 32768 || w->k % 8)
+        return fail(h, BLEND_EINVAL, "bad weight sizes n=%d k=%d", w->n, w->k);
+    if (w->group != 32 && w->group != 64 && w->group != 128)
+        return fail(h, BLEND_EINVAL, "group=%d is not 32, 64 or 128", w->group);
+    if (!w->codes || !w->scale) return fail(h, BLEND_EINVAL, "NULL pointer in w4");
+    if (((uintptr_t)w->codes | (uintptr_t)w->scale) & 15)
+        return fail(h, BLEND_EINVAL, "codes and scales must be 16-byte aligned");
+    v->codes = (const uint4*)w->codes;
+    v->scale = (const bf16*)w->scale;
+    v->n = w->n;
+    v->k = w->k;
+    v->group = w->group;
+    v->chunks = (w->k + 127) / 128;
+    return BLEND_OK;
+}
+// Distance between rows of `width` elements of `dtype`: at least one row, a multiple of 16 bytes.
+bool stride16_ok(int dtype, long long ld, long long width) {
+    return ld >= width && ld % (long long)(16 / elem_size(dtype)) == 0 && ld <= (1ll << 32);
+}
+int w4_copy_checks(blend_handle* h, const blend_w4* w4, const void* p, int64_t ld, W4View* v) {
+    if (int rc = view_w4(h, w4, v)) return rc;
+    if (!p) return fail(h, BLEND_EINVAL, "NULL pointer");
+    if ((uintptr_t)p & 15) return fail(h, BLEND_EINVAL, "weights must be 16-byte aligned");
+    if (!stride16_ok(h->cfg.dtype, ld, w4->k)) return fail(h, BLEND_EINVAL, "bad row stride %lld", (long long)ld);
+    const long long bytes = ((w4->n - 1ll) * ld + w4->k) * (long long)elem_size(h->cfg.dtype);
+    if (overlap(p, bytes, w4->codes, (long long)w4->n * v->chunks * 64) ||
+        overlap(p, bytes, w4->scale, (long long)w4->n * v->chunks * (128 / w4->group) * 2))
+        return fail(h, BLEND_EINVAL, "weights overlap their packed form");
+    return BLEND_OK;
+}
+}  // namespace
+
+extern "C" int w4_pack(blend_handle* h, const blend_w4* w4, const void* w, int64_t ld_w, void* stream) {
+    if (!h) return fail(nullptr, BLEND_EINVAL, "handle is NULL");
+    W4View v;
+    if (int rc = w4_copy_checks(h, w4, w, ld_w, &v)) return rc;
+    launch_w4_pack(h->cfg.dtype, v, w, ld_w, (cudaStream_t)stream);
+    return check_cuda(h, "w4_pack");
+}
+
+extern "C" int w4_unpack(blend_handle* h, const blend_w4* w4, void* out, int64_t ld_out, void* stream) {
+    if (!h) return fail(nullptr, BLEND_EINVAL, "handle is NULL");
+    W4View v;
+    if (int rc = w4_copy_checks(h, w4, out, ld_out, &v)) return rc;
+    launch_w4_unpack(h->cfg.dtype, v, out, ld_out, (cudaStream_t)stream);
+    return check_cuda(h, "w4_unpack");
+}
+
+extern "C" int w4_linear(blend_handle* h, const blend_w4* w4, const void* x, int64_t ld_x, int32_t n_rows, void* y,
+                         int64_t ld_y, int32_t y_dtype, int32_t epi, void* stream) {
+    if (!h) return fail(nullptr, BLEND_EINVAL, "handle is NULL");
+    W4Linear a;
+    if (int rc = view_w4(h, w4, &a.w)) return rc;
+    if (!x || !y) return fail(h, BLEND_EINVAL, "NULL pointer");
+    if ((uintptr_t)x & 15) return fail(h, BLEND_EINVAL, "x must be 16-byte aligned");
+    if (y_dtype != BLEND_F32 && y_dtype != BLEND_BF16) return fail(h, BLEND_EINVAL, "bad y_dtype %d", y_dtype);
+    if ((uintptr_t)y & (elem_size(y_dtype) - 1)) return fail(h, BLEND_EINVAL, "y must be aligned to its elements");
+    if (epi != BLEND_W4_STORE && epi != BLEND_W4_ADD && epi != BLEND_W4_SWIGLU)
+        return fail(h, BLEND_EINVAL, "bad epi %d", epi);
+    if (epi == BLEND_W4_ADD && y_dtype != BLEND_F32) return fail(h, BLEND_EINVAL, "BLEND_W4_ADD adds to fp32 rows");
+    if (epi == BLEND_W4_SWIGLU && w4->n % (2 * BLEND_GU_BLOCK))
+        return fail(h, BLEND_EINVAL, "n=%d is no multiple of %d", w4->n, 2 * BLEND_GU_BLOCK);
+    if (n_rows < 0 || n_rows > (1 << 18)) return fail(h, BLEND_EINVAL, "n_rows=%d outside 0..2^18", n_rows);
+    const long long wide = epi == BLEND_W4_SWIGLU ? w4->n / 2 : w4->n;
+    if (!stride16_ok(h->cfg.dtype, ld_x, w4->k) || ld_y < wide || ld_y > (1ll << 32))
+        return fail(h, BLEND_EINVAL, "bad row stride (%lld, %lld)", (long long)ld_x, (long long)ld_y);
+    if (n_rows == 0) return BLEND_OK;
+    const long long x_span = ((n_rows - 1ll) * ld_x + w4->k) * (long long)elem_size(h->cfg.dtype);
+    const long long y_span = ((n_rows - 1ll) * ld_y + wide) * (long long)elem_size(y_dtype);
+    if (overlap(y, y_span, x, x_span)) return fail(h, BLEND_EINVAL, "y overlaps x");
+    if (overlap(y, y_span, w4->codes, (long long)w4->n * a.w.chunks * 64) ||
+        overlap(y, y_span, w4->scale, (long long)w4->n * a.w.chunks * (128 / w4->group) * 2))
+        return fail(h, BLEND_EINVAL, "y overlaps the weights");
+    a.x = x;
+    a.ld_x = ld_x;
+    a.rows = n_rows;
+    a.y = y;
+    a.ld_y = ld_y;
+    a.y_f32 = y_dtype == BLEND_F32;
+    a.epi = epi;
+    return launched(h, launch_w4_linear(h->cfg.dtype, a, (cudaStream_t)stream), "w4_linear");
+}
+
+extern "C" int token_logprobs(blend_handle* h, const void* logits, int64_t ld, int32_t dtype, int32_t n_rows,
+                              int32_t vocab, float scale, const int32_t* ids, int32_t n_ids, float* logp,
+                              float* entropy, int32_t top, int32_t* top_id, float* top_logp, void* stream) {
+    if (!h) return fail(nullptr, BLEND_EINVAL, "handle is NULL");
+    if (!logits) return fail(h, BLEND_EINVAL, "NULL pointer");
+    if (dtype != BLEND_F32 && dtype != BLEND_BF16) return fail(h, BLEND_EINVAL, "bad dtype %d", dtype);
+    if ((uintptr_t)logits & (elem_size(dtype) - 1)) return fail(h, BLEND_EINVAL, "logits must be aligned to their elements");
+    if (n_rows < 0 || n_rows > (1 << 24) || vocab < 1 || vocab > (1 << 24) || n_ids < 0 || n_ids > (1 << 24))
+        return fail(h, BLEND_EINVAL, "bad sizes n_rows=%d vocab=%d n_ids=%d", n_rows, vocab, n_ids);
+    if (ld < vocab || ld > (1ll << 32)) return fail(h, BLEND_EINVAL, "bad row stride %lld", (long long)ld);
+    if (!(scale > 0.f) || !std::isfinite(scale)) return fail(h, BLEND_EINVAL, "scale must be positive and finite");
+    if (top < 0 || top > BLEND_MAX_TOP || top > vocab)
+        return fail(h, BLEND_EINVAL, "top=%d outside 0..%d or above vocab", top, BLEND_MAX_TOP);
+    if ((n_ids > 0 && (!ids || !logp)) || (top > 0 && !top_id)) return fail(h, BLEND_EINVAL, "NULL pointer");
+    if (((uintptr_t)ids | (uintptr_t)logp | (uintptr_t)entropy | (uintptr_t)top_id | (uintptr_t)top_logp) & 3)
+        return fail(h, BLEND_EINVAL, "ids and outputs must be 4-byte aligned");
+    if (n_rows == 0) return BLEND_OK;
+    Logprobs a;
+    a.logits = logits;
+    a.ld = ld;
+    a.rows = n_rows;
+    a.vocab = vocab;
+    a.scale = scale;
+    a.ids = ids;
+    a.n_ids = n_ids;
+    a.logp = logp;
+    a.entropy = entropy;
+    a.top = top;
+    a.top_id = top_id;
+    a.top_logp = top_logp;
+    a.err = h->err;
+    return launched(h, launch_logprobs(dtype, a, (cudaStream_t)stream), "token_logprobs");
+}
+
+namespace {
+// Frequencies of a blend_rope's pairs (radians per position); false if a field is out of range.
+bool rope_freqs(const blend_rope* r, double* f, std::string* why) {
+    const int n = r->rot_dim / 2;
+    const double pi2 = 6.283185307179586477;
+    if (!(r->theta > 1.0) || !std::isfinite(r->theta)) { *why = "theta must be above 1"; return false; }
+    const bool scaled = r->scaling != BLEND_ROPE_NONE;
+    if (scaled && (!(r->factor >= 1.0) || !std::isfinite(r->factor))) { *why = "factor must be at least 1"; return false; }
+    const bool bands = r->scaling == BLEND_ROPE_BANDS, yarn = r->scaling == BLEND_ROPE_YARN;
+    if ((bands || yarn) && (r->trained_len < 1 || !(r->low > 0.0) || !(r->high > r->low) || !std::isfinite(r->high))) {
+        *why = "trained_len must be positive and 0 < low < high";
+        return false;
+    }
+    double theta = r->theta;
+    if (r->scaling == BLEND_ROPE_BASE) theta *= std::pow(r->factor, (double)r->rot_dim / (r->rot_dim - 2));
+    if (!std::isfinite(theta)) { *why = "theta * factor^(..) overflows"; return false; }
+    double a = 0.0, b = 1.0;
+    if (yarn) {
+        const double per_log = r->rot_dim / (2.0 * std::log(theta));
+        a = std::max(0.0, std::floor(per_log * std::log(r->trained_len / (pi2 * r->high))));
+        b = std::min(r->rot_dim - 1.0, std::ceil(per_log * std::log(r->trained_len / (pi2 * r->low))));
+    }
+    for (int i = 0; i < n; ++i) {
+        const double e = std::pow(theta, -2.0 * i / r->rot_dim);
+        double keep = 1.0;
+        if (r->scaling == BLEND_ROPE_LINEAR) keep = 0.0;
+        if (bands) keep = (r->trained_len * e / pi2 - r->low) / (r->high - r->low);
+        if (yarn) keep = 1.0 - (i - a) / std::max(b - a, 0.001);
+        keep = std::min(1.0, std::max(0.0, keep));
+        f[i] = scaled && r->scaling != BLEND_ROPE_BASE ? e * (keep + (1.0 - keep) / r->factor) : e;
+    }
+    return true;
+}
+// Do rows [layers][n][width] at a and b meet?  (Bytes; where both step alike, rows that lie side by side in
+// one buffer do not, although their ranges do.)
+bool rows_meet(const void* pa, long long row_a, long long layer_a, long long layers_a, long long wa, const void* pb,
+               long long row_b, long long layer_b, long long layers_b, long long wb, long long n) {
+    if (!overlap(pa, (layers_a - 1) * layer_a + (n - 1) * row_a + wa, pb, (layers_b - 1) * layer_b + (n - 1) * row_b + wb))
+        return false;
+    if (row_a != row_b || (layers_a > 1 && layer_a % row_a) || (layers_b > 1 && layer_b % row_b)) return true;
+    const long long d = (((long long)((intptr_t)pb - (intptr_t)pa)) % row_a + row_a) % row_a;  // b's place in a's rows
+    return d < wa || d + wb > row_a;
+}
+}  // namespace
+
+extern "C" int rope_rows(blend_handle* h, const blend_rope* rope, const blend_rope_rows* parts, int32_t n_parts,
+                         const int32_t* rot, const int32_t* n, int32_t max_n, void* stream) {
+    if (!h) return fail(nullptr, BLEND_EINVAL, "handle is NULL");
+    const blend_model_cfg& c = h->cfg;
+    if (!rope || !parts || !rot || !n) return fail(h, BLEND_EINVAL, "NULL pointer");
+    if (((uintptr_t)rot | (uintptr_t)n) & 3) return fail(h, BLEND_EINVAL, "rot and n must be 4-byte aligned");
+    if (n_parts < 1 || n_parts > 2) return fail(h, BLEND_EINVAL, "n_parts=%d is not 1 or 2", n_parts);
+    if (max_n < 0 || max_n > (1 << 24)) return fail(h, BLEND_EINVAL, "max_n=%d outside 0..2^24", max_n);
+    if (rope->layout != BLEND_ROPE_HALF && rope->layout != BLEND_ROPE_PAIRS)
+        return fail(h, BLEND_EINVAL, "bad rotary layout %d", rope->layout);
+    if (rope->scaling < BLEND_ROPE_NONE || rope->scaling > BLEND_ROPE_YARN)
+        return fail(h, BLEND_EINVAL, "bad rotary scaling %d", rope->scaling);
+    if (rope->rot_dim < 16 || rope->rot_dim > c.head_dim || rope->rot_dim % 16)
+        return fail(h, BLEND_EINVAL, "rot_dim=%d is no multiple of 16 up to head_dim", rope->rot_dim);
+    if (!std::isfinite(rope->magnitude)) return fail(h, BLEND_EINVAL, "magnitude must be finite");
+    double f[64];
+    std::string why;
+    if (!rope_freqs(rope, f, &why)) return fail(h, BLEND_EINVAL, "%s", why.c_str());
+    const long long es = (long long)elem_size(c.dtype);
+    for (int i = 0; i < n_parts; ++i) {
+        const blend_rope_rows& p = parts[i];
+        if (!p.src || !p.dst) return fail(h, BLEND_EINVAL, "NULL pointer");
+        if (((uintptr_t)p.src | (uintptr_t)p.dst) & 15) return fail(h, BLEND_EINVAL, "rows must be 16-byte aligned");
+        if (p.heads < 1 || p.heads > (1 << 16) || p.n_layers < 1 || p.n_layers > (1 << 16) ||
+            (long long)p.heads * p.n_layers > (1 << 24))
+            return fail(h, BLEND_EINVAL, "bad heads=%d or n_layers=%d", p.heads, p.n_layers);
+        const long long width = (long long)p.heads * c.head_dim;
+        if (!stride16_ok(c.dtype, p.src_row, width) || !stride16_ok(c.dtype, p.dst_row, width))
+            return fail(h, BLEND_EINVAL, "bad row stride (%lld, %lld)", (long long)p.src_row, (long long)p.dst_row);
+        if (p.n_layers > 1 && (p.src_layer < width || p.dst_layer < width || p.src_layer > (1ll << 40) ||
+                               p.dst_layer > (1ll << 40) || p.src_layer % (16 / es) || p.dst_layer % (16 / es)))
+            return fail(h, BLEND_EINVAL, "bad layer stride (%lld, %lld)", (long long)p.src_layer, (long long)p.dst_layer);
+    }
+    if (max_n == 0) return BLEND_OK;
+    for (int i = 0; i < n_parts; ++i) {
+        const blend_rope_rows& d = parts[i];
+        const long long width = (long long)d.heads * c.head_dim, dw = width * es;
+        // a part's rows are distinct: whole layers one behind the other, or interleaved within a row's stride
+        const bool stacked = d.n_layers == 1 || d.dst_layer >= (max_n - 1ll) * d.dst_row + width;
+        const bool woven = d.n_layers == 1 || d.dst_row >= (d.n_layers - 1ll) * d.dst_layer + width;
+        if (!stacked && !woven) return fail(h, BLEND_EINVAL, "layers of dst overlap");
+        for (int j = 0; j < n_parts; ++j) {
+            const blend_rope_rows& s = parts[j];
+            const long long sw = (long long)s.heads * c.head_dim * es;
+            const bool own = i == j && d.src == d.dst && d.src_row == d.dst_row && (d.n_layers == 1 || d.src_layer == d.dst_layer);
+            if (!own && rows_meet(d.dst, d.dst_row * es, d.dst_layer * es, d.n_layers, dw, s.src, s.src_row * es,
+                                  s.src_layer * es, s.n_layers, sw, max_n))
+                return fail(h, BLEND_EINVAL, "dst overlaps a src");
+            if (j > i && rows_meet(d.dst, d.dst_row * es, d.dst_layer * es, d.n_layers, dw, s.dst, s.dst_row * es,
+                                   s.dst_layer * es, s.n_layers, sw, max_n))
+                return fail(h, BLEND_EINVAL, "the two parts' dst overlap");
+        }
+    }
+    RopeArgs a;
+    memset(&a, 0, sizeof a);
+    for (int i = 0; i < n_parts; ++i) a.part[i] = parts[i];
+    a.n_parts = n_parts;
+    a.max_n = max_n;
+    a.rot_dim = rope->rot_dim;
+    a.head_dim = c.head_dim;
+    a.pairs = rope->layout == BLEND_ROPE_PAIRS;
+    a.magnitude = rope->magnitude;
+    a.rot = rot;
+    a.n = n;
+    a.err = h->err;
+    for (int i = 0; i < rope->rot_dim / 2; ++i) a.freq[i] = (uint64_t)std::ldexp(f[i] / 6.283185307179586477, 64);
+    launch_rope_rows(c.dtype, a, (cudaStream_t)stream);
+    return check_cuda(h, "rope_rows");
 }

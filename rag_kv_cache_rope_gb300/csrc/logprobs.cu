@@ -1,0 +1,448 @@
+// Log probabilities of given tokens, entropy and top alternatives from logits (token_logprobs in
+// blend.h): bound by reading the logits once.
+//
+// A row belongs to a cluster of 1..16 CTAs, each with a stretch of the vocabulary (few rows: many CTAs a
+// row, so that every SM reads; many rows: one CTA each).  Threads stream 16-byte vectors and keep, against
+// a reference R that is raised only when a term would pass 4, Z = sum 2^(x c - R) and
+// S = sum 2^(x c - R) (x c - R), c = scale log2(e); then log p = ln 2 (x c - R - log2 Z) and the entropy is
+// ln 2 (log2 Z - S / Z).  R is whatever rounded number it is: every term uses the same one, in one
+// multiply-add, so its rounding cancels.
+//
+// Ranking without sorting and without a second pass: a thread also keeps the largest logit it saw.  The
+// k-th largest of the maxima of 64 groups of threads is a lower bound T of the k-th largest logit, which
+// at most a few dozen logits of the stretch reach, and those lie with the few threads whose maximum reaches T: only
+// these threads' vectors are read again (from L2).  The candidates, 64-bit keys of value and index, are
+// ranked by counting.  Ties at T in numbers (a masked row) and NaN at the end of the ranking are taken in
+// order of their index.  Each CTA of a cluster ranks its own stretch; the first joins sums and lists through
+// distributed shared memory in the CTAs' order, so nothing depends on timing and no workspace is needed.
+#include <cooperative_groups.h>
+
+#include "tokens.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace blend {
+namespace {
+
+constexpr int LP_THREADS = 512;
+constexpr int LP_GROUPS = 64;   // groups of threads whose maxima bound the k-th logit: twice the largest k
+constexpr int LP_CAND = 1024;   // candidates of one stretch
+constexpr int LP_MAX_CLUSTER = 16;
+constexpr float LP_RAISE = 2.f;
+// References beyond this are not used: x c - R, a rounding of R by then, could be anything.
+constexpr float LP_HUGE = 16777216.f;
+constexpr float LN2 = 0.693147180559945309f;
+constexpr float FAR = -200.f;  // 2^FAR is 0 in fp32, and 0 times FAR is a number
+
+using key_t = unsigned long long;
+
+// Ranking key: value (order-preserving bits, -0 as +0, NaN lowest), then lower index first.
+__device__ __forceinline__ key_t rank_key(float x, int idx) {
+    const uint32_t b = __float_as_uint(x + 0.f);
+    const uint32_t o = x != x ? 0u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
+    return ((key_t)o << 32) | (uint32_t)~idx;
+}
+__device__ __forceinline__ float key_value(key_t k) {
+    const uint32_t o = (uint32_t)(k >> 32);
+    if (o == 0) return __int_as_float(0x7fc00000);
+    return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ int key_index(key_t k) { return (int)~(uint32_t)k; }
+
+__device__ __forceinline__ float ex2f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A row as aligned 16-byte vectors: vector j holds elements j VE - off .. + VE - 1 (off of the first are
+// before the row).  Vectors that reach over an end of the row are read element by element; what is not in
+// the row comes back as -infinity.
+template <typename T> struct Row {
+    static constexpr int VE = 16 / sizeof(T);
+    const T* p;  // the row's first element
+    int off, vocab, n_vec;
+    __device__ Row(const T* row, int v) {
+        p = row;
+        vocab = v;
+        off = (int)(((uintptr_t)row & 15) / sizeof(T));
+        n_vec = (int)(((long long)off + v + VE - 1) / VE);
+    }
+    __device__ __forceinline__ void load(int j, float (&x)[VE]) const {
+        const int e0 = j * VE - off;
+        if (e0 >= 0 && e0 + VE <= vocab) {
+            const Vec<T> v = ld16(p + e0);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) x[i] = v.get(i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VE; ++i) x[i] = e0 + i >= 0 && e0 + i < vocab ? to_f<T>(p[e0 + i]) : -INFINITY;
+        }
+    }
+    __device__ __forceinline__ bool holds(int j, int i) const {  // element i of vector j is in the row
+        const int e = j * VE - off + i;
+        return e >= 0 && e < vocab;
+    }
+    __device__ __forceinline__ int index(int j, int i) const { return j * VE - off + i; }
+};
+
+struct Sums {
+    float r, z, s;  // reference, sum of 2^(t), sum of 2^(t) t with t = x c - r
+};
+// Two partial sums under the larger reference.  A part without a finite term has z = 0 and r = -infinity.
+__device__ __forceinline__ Sums join(Sums a, Sums b) {
+    Sums o;
+    o.r = fmaxf(a.r, b.r);
+    const float da = a.r - o.r, db = b.r - o.r;
+    if (o.r == -INFINITY) return {o.r, a.z + b.z, a.s + b.s};
+    // (a part whose reference is -infinity holds no term: 0, or NaN; 2^FAR is 0 already)
+    const float fa = ex2f(da), fb = ex2f(db);
+    o.z = a.z * fa + b.z * fb;
+    o.s = fa * (a.s + a.z * fmaxf(da, FAR)) + fb * (b.s + b.z * fmaxf(db, FAR));
+    return o;
+}
+
+struct Shared {
+    key_t cand[LP_CAND];
+    key_t list[BLEND_MAX_TOP];       // this stretch's ranking
+    key_t all[LP_MAX_CLUSTER][BLEND_MAX_TOP];
+    key_t merged[BLEND_MAX_TOP];
+    Sums sums[LP_THREADS / 32];
+    Sums total;
+    float group_max[LP_GROUPS];
+    int active[LP_THREADS];
+    int n_active, n_cand, overflow, warp_tot[LP_THREADS / 32];
+    float bound;
+};
+
+// Appends elements of the stretch's vectors [v0, v1) that `take` accepts to sh.cand, in ascending index, from
+// sh.n_cand on until it holds `until`.  All threads; barriers inside.
+template <typename T, typename Take>
+__device__ void take_in_order(const Row<T>& row, int v0, int v1, int until, Shared& sh, Take take) {
+    constexpr int VE = Row<T>::VE;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int j0 = v0; j0 < v1; j0 += LP_THREADS) {
+        const int have = sh.n_cand;
+        if (have >= until) break;
+        const int j = j0 + tid;
+        float x[VE];
+        unsigned m = 0;
+        if (j < v1) {
+            row.load(j, x);
+#pragma unroll
+            for (int i = 0; i < VE; ++i)
+                if (row.holds(j, i) && take(x[i])) m |= 1u << i;
+        }
+        int incl = __popc(m);
+        const int mine = incl;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) sh.warp_tot[warp] = incl;
+        __syncthreads();
+        int at = have + incl - mine, total = have;
+        for (int w = 0; w < LP_THREADS / 32; ++w) {
+            if (w < warp) at += sh.warp_tot[w];
+            total += sh.warp_tot[w];
+        }
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+            if ((m >> i & 1) && at < until) sh.cand[at++] = rank_key(x[i], row.index(j, i));
+        __syncthreads();
+        if (tid == 0) sh.n_cand = min(total, until);
+        __syncthreads();
+    }
+}
+
+// The stretch's `top` highest keys, descending, into sh.list (0 behind the last).  All threads.
+template <typename T>
+__device__ void rank_stretch(const Row<T>& row, int v0, int v1, int top, float my_max, Shared& sh) {
+    constexpr int VE = Row<T>::VE;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int PER_GROUP = LP_THREADS / LP_GROUPS;
+    float g = my_max;
+#pragma unroll
+    for (int o = 1; o < PER_GROUP; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+    if (tid % PER_GROUP == 0) sh.group_max[tid / PER_GROUP] = g;
+    if (tid < BLEND_MAX_TOP) sh.list[tid] = 0;
+    if (tid == 0) sh.n_active = sh.n_cand = sh.overflow = 0;
+    __syncthreads();
+    if (tid < LP_GROUPS) {
+        const float m = sh.group_max[tid];
+        int above = 0;
+#pragma unroll 8
+        for (int i = 0; i < LP_GROUPS; ++i) {
+            const float y = sh.group_max[i];
+            above += y > m || (y == m && i < tid);
+        }
+        if (above == top - 1) sh.bound = m;
+    }
+    __syncthreads();
+    const float bound = sh.bound;
+    // threads that hold a candidate
+    if (my_max >= bound) sh.active[atomicAdd(&sh.n_active, 1)] = tid;
+    __syncthreads();
+    const int n_active = sh.n_active;
+    for (int a = warp; a < n_active; a += LP_THREADS / 32) {
+        const int t = sh.active[a];
+        for (int j = v0 + t + lane * LP_THREADS; j < v1; j += 32 * LP_THREADS) {
+            float x[VE];
+            row.load(j, x);
+#pragma unroll
+            for (int i = 0; i < VE; ++i)
+                if (x[i] >= bound && row.holds(j, i)) {
+                    const int at = atomicAdd(&sh.n_cand, 1);
+                    if (at < LP_CAND) sh.cand[at] = rank_key(x[i], row.index(j, i));
+                    else sh.overflow = 1;
+                }
+        }
+    }
+    __syncthreads();
+    if (sh.overflow) {
+        // Many equal logits at the bound (or few threads holding nearly all of the largest): those above it,
+        // and of the equal ones the first `top`.
+        __syncthreads();
+        if (tid == 0) sh.n_cand = 0;
+        __syncthreads();
+        take_in_order(row, v0, v1, LP_CAND - BLEND_MAX_TOP, sh, [&](float x) { return x > bound; });
+        if (sh.n_cand >= LP_CAND - BLEND_MAX_TOP) {
+            // Still too many: the ranking one by one, each the highest key below the last.
+            key_t last = ~0ull;
+            for (int r = 0; r < top; ++r) {
+                key_t best = 0;
+                for (int j = v0 + tid; j < v1; j += LP_THREADS) {
+                    float x[VE];
+                    row.load(j, x);
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) {
+                        const key_t k = rank_key(x[i], row.index(j, i));
+                        if (row.holds(j, i) && k < last && k > best) best = k;
+                    }
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    const key_t y = __shfl_xor_sync(0xffffffffu, best, o);
+                    best = y > best ? y : best;
+                }
+                __syncthreads();
+                if (lane == 0) sh.cand[warp] = best;
+                __syncthreads();
+                for (int w = 0; w < LP_THREADS / 32; ++w) best = sh.cand[w] > best ? sh.cand[w] : best;
+                if (tid == 0) sh.list[r] = best;
+                last = best;
+            }
+            __syncthreads();
+            return;
+        }
+        const int until = sh.n_cand + BLEND_MAX_TOP;
+        __syncthreads();
+        take_in_order(row, v0, v1, until, sh, [&](float x) { return x == bound; });
+    }
+    // fewer numbers than asked for: NaN in order
+    if (sh.n_cand < top) {
+        __syncthreads();
+        take_in_order(row, v0, v1, top, sh, [](float x) { return x != x; });
+    }
+    const int n = sh.n_cand;
+    for (int c = tid; c < n; c += LP_THREADS) {
+        const key_t k = sh.cand[c];
+        int above = 0;
+        for (int i = 0; i < n; ++i) above += sh.cand[i] > k;
+        if (above < top) sh.list[above] = k;
+    }
+    __syncthreads();
+}
+
+// The threads' sums joined in order, for every thread.  Two barriers.
+__device__ __forceinline__ Sums block_join(Sums t, Shared& sh) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Sums y = {__shfl_xor_sync(0xffffffffu, t.r, o), __shfl_xor_sync(0xffffffffu, t.z, o),
+                        __shfl_xor_sync(0xffffffffu, t.s, o)};
+        t = (threadIdx.x & o) ? join(y, t) : join(t, y);
+    }
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) sh.sums[threadIdx.x / 32] = t;
+    __syncthreads();
+    t = sh.sums[0];
+    for (int w = 1; w < LP_THREADS / 32; ++w) t = join(t, sh.sums[w]);
+    return t;
+}
+__device__ __forceinline__ float block_max(float m, Shared& sh) {
+    return block_join({m, 0.f, 0.f}, sh).r;
+}
+
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(LP_THREADS) k_logprobs(const Logprobs a, int cluster, float c) {
+    constexpr int VE = Row<T>::VE, U = 4;
+    __shared__ Shared sh;
+    const int tid = threadIdx.x;
+    const int rank = cluster > 1 ? (int)cg::this_cluster().block_rank() : 0;
+    const long long r = blockIdx.x / cluster;
+    const T* logits = (const T*)a.logits + r * a.ld;
+    const Row<T> row(logits, a.vocab);
+    const int v0 = (int)((long long)row.n_vec * rank / cluster), v1 = (int)((long long)row.n_vec * (rank + 1) / cluster);
+
+    float ref = -INFINITY, z = 0.f, s = 0.f, top_x = -INFINITY;
+    auto step = [&](const float (&x)[VE]) {
+        float m = x[0];
+#pragma unroll
+        for (int i = 1; i < VE; ++i) m = fmaxf(m, x[i]);
+        if (TOP) top_x = fmaxf(top_x, m);
+        const float t_max = m * c;
+        if (t_max > fmaxf(ref + LP_RAISE, -LP_HUGE)) {
+            if (ref > -INFINITY) {
+                const float d = ref - t_max, f = ex2f(d);
+                s = f * (s + z * fmaxf(d, FAR));
+                z *= f;
+            }
+            ref = t_max;
+        }
+        const float neg = ref == -INFINITY ? 0.f : -ref;
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+            const float t = fmaf(x[i], c, neg), e = ex2f(t);
+            z += e;
+            s = fmaf(e, fmaxf(t, FAR), s);
+        }
+    };
+    int j = v0 + tid;
+    for (; j + (U - 1) * LP_THREADS < v1; j += U * LP_THREADS) {
+        float x[U][VE];
+#pragma unroll
+        for (int u = 0; u < U; ++u) row.load(j + u * LP_THREADS, x[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) step(x[u]);
+    }
+    for (; j < v1; j += LP_THREADS) {
+        float x[VE];
+        row.load(j, x);
+        step(x);
+    }
+    Sums t = block_join({ref, z, s}, sh);
+    if (TOP) rank_stretch(row, v0, v1, a.top, top_x, sh);
+    if (tid == 0) sh.total = t;
+    const key_t* list = sh.list;
+    if (cluster > 1) {
+        cg::cluster_group cl = cg::this_cluster();
+        cl.sync();
+        if (rank == 0) {
+            if (tid == 0) {
+                for (int q = 1; q < cluster; ++q) t = join(t, cl.map_shared_rank(&sh, q)->total);
+                sh.total = t;
+            }
+            if (TOP) {
+                for (int i = tid; i < cluster * BLEND_MAX_TOP; i += LP_THREADS)
+                    sh.all[i / BLEND_MAX_TOP][i % BLEND_MAX_TOP] = cl.map_shared_rank(&sh, i / BLEND_MAX_TOP)->list[i % BLEND_MAX_TOP];
+                __syncthreads();
+                for (int i = tid; i < cluster * BLEND_MAX_TOP; i += LP_THREADS) {
+                    const int q = i / BLEND_MAX_TOP;
+                    const key_t k = sh.all[q][i % BLEND_MAX_TOP];
+                    int above = i % BLEND_MAX_TOP;
+                    for (int o = 0; o < cluster; ++o) {
+                        if (o == q) continue;
+                        int lo = 0;  // keys of list o above k: lists descend
+#pragma unroll
+                        for (int w = BLEND_MAX_TOP / 2; w > 0; w >>= 1)
+                            if (sh.all[o][lo + w - 1] > k) lo += w;
+                        above += lo + (sh.all[o][lo] > k);
+                    }
+                    if (k != 0 && above < a.top) sh.merged[above] = k;
+                }
+            }
+        }
+        cl.sync();
+        if (rank != 0) return;
+        list = sh.merged;
+    } else
+        __syncthreads();
+    t = sh.total;
+    // Nothing counted (R is -infinity): nothing is allowed, or every logit is far below 0 (masks of the type's
+    // lowest value in a row that allows nothing else).  Such a row, and one of huge logits, once more,
+    // against its maximum.
+    float low = 0.f;
+    bool none = false;
+    if (!(fabsf(t.r) <= LP_HUGE)) {
+        float m = -INFINITY;
+        for (int j = tid; j < row.n_vec; j += LP_THREADS) {
+            float x[VE];
+            row.load(j, x);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) m = fmaxf(m, x[i]);
+        }
+        low = block_max(m, sh);
+        if (low == -INFINITY)
+            none = t.z == 0.f;  // (else there is a NaN)
+        else {
+            z = s = 0.f;
+            for (int j = tid; j < row.n_vec; j += LP_THREADS) {
+                float x[VE];
+                row.load(j, x);
+#pragma unroll
+                for (int i = 0; i < VE; ++i) {
+                    const float d = (x[i] - low) * c, e = ex2f(d);
+                    z += e;
+                    s = fmaf(e, fmaxf(d, FAR), s);
+                }
+            }
+            t = block_join({0.f, z, s}, sh);
+        }
+    }
+    const float lz = log2f(t.z);
+    // log p = ln 2 (x c - R - log2 Z); where x c alone is too low for fp32, the rest does not count
+    auto logp_of = [&](float x) {
+        if (none) return x != x ? x : -INFINITY;
+        const float d = fmaf(x - low, c, -t.r);
+        return d == -INFINITY && x > d && lz == lz ? (x - low) * a.scale : LN2 * (d - lz);
+    };
+    if (tid == 0 && a.entropy) a.entropy[r] = none ? 0.f : LN2 * (lz - t.s / t.z);
+    for (int i = tid; i < a.n_ids; i += LP_THREADS) {
+        const int id = __ldg(a.ids + r * a.n_ids + i);
+        float lp = 0.f;
+        if (id >= a.vocab) {
+            set_error(a.err, BLEND_EDEVICE);
+            lp = __int_as_float(0x7fc00000);
+        } else if (id >= 0)
+            lp = logp_of(to_f<T>(logits[id]));
+        a.logp[r * a.n_ids + i] = lp;
+    }
+    if (TOP && tid < a.top) {
+        const key_t k = list[tid];
+        a.top_id[r * a.top + tid] = key_index(k);
+        if (a.top_logp) a.top_logp[r * a.top + tid] = logp_of(key_value(k));
+    }
+}
+
+template <typename T, bool TOP> int launch(const Logprobs& a, cudaStream_t s) {
+    // A row's CTAs: as many as keep 152 SMs of two CTAs busy, each with 4096 logits at least.
+    int cluster = 1;
+    while (cluster < LP_MAX_CLUSTER && (long long)a.rows * cluster * 2 <= 304 && a.vocab / (cluster * 2) >= 4096) cluster *= 2;
+    auto* kern = k_logprobs<T, TOP>;
+    if (cluster > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return BLEND_ECUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.rows * (long long)cluster));
+    cfg.blockDim = dim3(LP_THREADS);
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    const float c = (float)((double)a.scale * 1.4426950408889634);
+    if (cudaLaunchKernelEx(&cfg, kern, a, cluster, c) != cudaSuccess) return BLEND_ECUDA;
+    note_launch();
+    return BLEND_OK;
+}
+
+}  // namespace
+
+int launch_logprobs(int dtype, const Logprobs& a, cudaStream_t s) {
+    if (dtype == BLEND_BF16) return a.top ? launch<bf16, true>(a, s) : launch<bf16, false>(a, s);
+    return a.top ? launch<float, true>(a, s) : launch<float, false>(a, s);
+}
+
+}  // namespace blend

@@ -1,0 +1,59 @@
+// What follows the finished cache, per generated token: products with 4-bit weights, log
+// probabilities, rotary positions.  Launch interfaces.
+#pragma once
+#include "common.cuh"
+
+namespace blend {
+
+// ---- 4-bit weights (w4.cu); layout in blend.h at blend_w4
+struct W4View {
+    const uint4* codes;  // [n][4 chunks] sixteen-byte pieces
+    const bf16* scale;   // [n][chunks * 128 / group]
+    int n, k, group, chunks;
+};
+void launch_w4_pack(int dtype, const W4View& w, const void* src, long long ld, cudaStream_t s);
+void launch_w4_unpack(int dtype, const W4View& w, void* out, long long ld, cudaStream_t s);
+struct W4Linear {
+    W4View w;
+    const void* x;
+    long long ld_x;
+    int rows;
+    void* y;
+    long long ld_y;
+    int y_f32, epi;
+};
+// x of `dtype`.  Returns BLEND_OK or the code of a failed launch set-up.
+int launch_w4_linear(int dtype, const W4Linear& a, cudaStream_t s);
+
+// ---- log probabilities (logprobs.cu)
+struct Logprobs {
+    const void* logits;
+    long long ld;
+    int rows, vocab;
+    float scale;
+    const int32_t* ids;
+    int n_ids;
+    float* logp;
+    float* entropy;
+    int top;
+    int32_t* top_id;
+    float* top_logp;
+    int32_t* err;
+};
+int launch_logprobs(int dtype, const Logprobs& a, cudaStream_t s);
+
+// ---- rotary positions (rope_rows.cu)
+constexpr int ROPE_MAX_SHIFT = 1 << 24;
+struct RopeArgs {
+    blend_rope_rows part[2];
+    int n_parts, max_n, rot_dim, head_dim;
+    int pairs;        // BLEND_ROPE_PAIRS
+    float magnitude;
+    const int32_t* rot;
+    const int32_t* n;
+    int32_t* err;
+    uint64_t freq[64];  // each pair's turn per position, in 2^-64 of a turn
+};
+void launch_rope_rows(int dtype, const RopeArgs& a, cudaStream_t s);
+
+}  // namespace blend
