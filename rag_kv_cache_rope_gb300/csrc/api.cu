@@ -1599,6 +1599,8 @@ extern "C" int w4_linear(blend_handle* h, const blend_w4* w4, const void* x, int
     a.ld_y = ld_y;
     a.y_f32 = y_dtype == BLEND_F32;
     a.epi = epi;
+    a.tc = h->use_tc != 0;
+    a.err = h->err;
     return launched(h, launch_w4_linear(h->cfg.dtype, a, (cudaStream_t)stream), "w4_linear");
 }
 

@@ -21,6 +21,8 @@ struct W4Linear {
     void* y;
     long long ld_y;
     int y_f32, epi;
+    bool tc;  // tcgen05 may be used
+    int32_t* err;
 };
 // x of `dtype`.  Returns BLEND_OK or the code of a failed launch set-up.
 int launch_w4_linear(int dtype, const W4Linear& a, cudaStream_t s);

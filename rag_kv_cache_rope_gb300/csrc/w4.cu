@@ -9,8 +9,7 @@
 // codes nor scales are rounded.  fp32 inputs enter as three bf16 parts, which hold all 24 bits.
 #include <cooperative_groups.h>
 
-#include "paged.cuh"
-#include "tokens.cuh"
+#include "w4.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -98,6 +97,7 @@ __global__ void __launch_bounds__(PACK_THREADS)
 // ---------------------------------------------------------------- products
 constexpr int LIN_WARPS = 8, LIN_THREADS = 32 * LIN_WARPS;
 constexpr int LIN_RING = 4;         // chunks on their way per warp
+constexpr int LIN_TILE_ROWS = 16;   // more rows of inputs go to the tcgen05 kernel
 constexpr int LIN_MAX_CLUSTER = 8;  // CTAs that share a weight row's inputs
 
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -106,31 +106,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
-    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-}
-
-// Scales of one row's chunk: 128 / G bf16.
-template <int G> struct Scales;
-template <> struct Scales<32> {
-    uint2 v;
-    __device__ __forceinline__ void load(const bf16* p) { v = __ldg((const uint2*)p); }
-    __device__ __forceinline__ float get(int i) const {
-        const uint32_t w = i < 2 ? v.x : v.y;
-        return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
-    }
-};
-template <> struct Scales<64> {
-    uint32_t v;
-    __device__ __forceinline__ void load(const bf16* p) { v = __ldg((const uint32_t*)p); }
-    __device__ __forceinline__ float get(int i) const { return __uint_as_float(i & 1 ? v & 0xffff0000u : v << 16); }
-};
-template <> struct Scales<128> {
-    unsigned short v;
-    __device__ __forceinline__ void load(const bf16* p) { v = __ldg((const unsigned short*)p); }
-    __device__ __forceinline__ float get(int) const { return __uint_as_float((uint32_t)v << 16); }
-};
-
 // Where a CTA's share of the inputs lies and how its rows are laid out in shared memory: rows of whole
 // chunks and 64 bytes more, so that the two rows of a quarter warp's 16-byte reads use different banks.
 __host__ __device__ __forceinline__ int lin_row_bytes(int chunks) { return chunks * 256 + 64; }
@@ -396,6 +371,10 @@ void launch_w4_unpack(int dtype, const W4View& w, void* out, long long ld, cudaS
 }
 
 int launch_w4_linear(int dtype, const W4Linear& a, cudaStream_t s) {
+    if (dtype == BLEND_BF16 && a.tc && a.rows > LIN_TILE_ROWS && a.w.n >= 128 && a.w.k >= 64) {
+        const int rc = launch_w4_tile(a, s);
+        if (rc != BLEND_EUNSUPPORTED) return rc;
+    }
     if (dtype == BLEND_BF16) return a.rows <= 8 ? go_group<bf16, 1>(a, s) : go_group<bf16, 2>(a, s);
     return go_group<float, 1>(a, s);
 }
