@@ -13,27 +13,22 @@
 // Few tiles share their inputs' length among the CTAs of a cluster, which join their sums in order through
 // distributed shared memory.  All waits are bounded: on expiry the error word gets BLEND_ETIMEOUT, copies and
 // products in flight are waited for and TMEM is freed.
-#include <cooperative_groups.h>
-
 #include "attn_tc.cuh"
 #include "w4.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace blend {
 namespace {
 
 constexpr int TILE_M = 128, TILE_THREADS = 512;
-constexpr int X_STAGES = 6;   // of 64 inputs
-constexpr int C_STAGES = 6;   // of 128 inputs' codes
-constexpr int A_STAGES = 4;   // of 64 inputs in TMEM, 32 columns each
+constexpr int STAGES = 4;     // chunks of 128 inputs on their way: codes, operands in TMEM, inputs
 constexpr int D_STAGES = 2;   // accumulators of a group
 constexpr int CODE_BYTES = TILE_M * 64;
-constexpr int A_COL = 256, TILE_COLS = 512;
+constexpr int A_COL = 256, TILE_COLS = 512;  // accumulators, then 64 columns a stage
 constexpr int TILE_MAX_CLUSTER = 8;
+constexpr int WAIT_LIMIT = 1 << 24;
 
-template <int NT> constexpr int tile_smem(bool joined) {
-    return X_STAGES * NT * 128 + C_STAGES * CODE_BYTES + (joined ? NT * TILE_M * 4 : 0) + 1024;
+template <int NT> constexpr int tile_smem() {
+    return STAGES * (NT * 256 + CODE_BYTES) + NT * TILE_M * 4 + 1024;
 }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t* r) {
@@ -43,6 +38,48 @@ __device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t* r) {
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(t));
 }
+// shared::cluster address of this CTA's variable in CTA `rank` of the cluster, and a load from one
+__device__ __forceinline__ uint32_t peer_addr(const void* p, int rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(su32(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float ld_peer(uint32_t at) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+// Bounded wait, of one thread or of whole warps, in few instructions: the roles' loops are short and run side by
+// side, and what limited a first version was fetching their unrolled code.
+__device__ __forceinline__ bool phase_wait(uint64_t* b, uint32_t par, volatile int* abort_flag) {
+#pragma unroll 1
+    for (int i = 0; i < WAIT_LIMIT; ++i) {
+        if (mbar_try(b, par)) return true;
+        if (*abort_flag) return false;
+    }
+    return false;
+}
+// The same for a warp whose lanes go on together.
+__device__ __forceinline__ bool warp_phase(uint64_t* b, uint32_t par, volatile int* abort_flag) {
+    return __all_sync(0xffffffffu, phase_wait(b, par, abort_flag));
+}
+// One lane of a converged warp, in a form that the compiler knows to be one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+    return p != 0;
+}
+// A place in a ring of N stages.
+template <int N> struct Ring {
+    int at = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void step() {
+        if (++at == N) {
+            at = 0;
+            phase ^= 1;
+        }
+    }
+};
 
 // NT: input rows of a tile; G: inputs of a group.
 template <int NT, int G>
@@ -50,29 +87,27 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     k_w4_tile(const __grid_constant__ CUtensorMap m_codes, const __grid_constant__ CUtensorMap m_x, const W4Linear a, int cluster) {
     constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((NT >> 3) << 17) | ((TILE_M >> 4) << 24);
     constexpr int SPC = 128 / G, CW = NT / 2;  // groups of a chunk; columns of an epilogue thread
+    constexpr int X_BYTES = NT * 256;          // two halves of 64 inputs
     extern __shared__ char smem_raw[];
-    __shared__ uint64_t x_full[X_STAGES], x_empty[X_STAGES], c_full[C_STAGES], c_empty[C_STAGES], a_full[A_STAGES],
-        a_empty[A_STAGES], d_full[D_STAGES], d_empty[D_STAGES], drain;
+    // in: codes and inputs have come; full: four warps' operands; empty: their products are done
+    __shared__ uint64_t in[STAGES], full[STAGES], empty[STAGES], c_empty[STAGES], d_full[D_STAGES], d_empty[D_STAGES], drain;
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_sh;
     volatile int* abort_flag = &abort_sh;
     char* smem = (char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     char* s_x = smem;
-    char* s_codes = smem + X_STAGES * NT * 128;
-    float* part = (float*)(s_codes + C_STAGES * CODE_BYTES);  // [NT][128]: this CTA's sums (cluster > 1)
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    char* s_codes = smem + STAGES * X_BYTES;
+    float* part = (float*)(s_codes + STAGES * CODE_BYTES);  // [NT][128]: this CTA's sums
+    const int tid = threadIdx.x, lane = tid & 31;
+    // (the same for all lanes, and known to be: the roles' loops run in uniform registers, where the operands of
+    // tcgen05.mma and TMA have to be; with a loop of lane 0 alone each product took 100 cycles to issue)
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     if (tid == 0) {
-        for (int i = 0; i < X_STAGES; ++i) {
-            mbar_init(&x_full[i], 1);
-            mbar_init(&x_empty[i], 1);
-        }
-        for (int i = 0; i < C_STAGES; ++i) {
-            mbar_init(&c_full[i], 1);
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(&in[i], 1);
+            mbar_init(&full[i], 4);
+            mbar_init(&empty[i], 1);
             mbar_init(&c_empty[i], 4);
-        }
-        for (int i = 0; i < A_STAGES; ++i) {
-            mbar_init(&a_full[i], 4);
-            mbar_init(&a_empty[i], 1);
         }
         for (int i = 0; i < D_STAGES; ++i) {
             mbar_init(&d_full[i], 1);
@@ -90,7 +125,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tb = tmem_sh;
+    const uint32_t tb = __shfl_sync(0xffffffffu, tmem_sh, 0);
 
     const int rank = cluster > 1 ? (int)cta_rank() : 0;
     const int n_t = (a.rows + NT - 1) / NT, total = (a.w.n + TILE_M - 1) / TILE_M * n_t;
@@ -104,94 +139,87 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             set_error(a.err, BLEND_ETIMEOUT);
         }
     };
-    uint32_t it_x = 0, it_c = 0, it_a = 0, it_d = 0;  // uses of the rings so far, by role
+    Ring<STAGES> st;   // this role's stage
+    Ring<D_STAGES> sd;
 
     for (int tile = tile0; tile < total; tile += tile_step) {
         const int wt = tile / n_t, tt = tile - wt * n_t;
         if (warp == 0) {
-            if (lane == 0) {
-                for (int c = c0; c < c1 && ok; ++c) {
-                    const int sc = it_c % C_STAGES;
-                    if (!mbar_wait(&c_empty[sc], (it_c / C_STAGES & 1) ^ 1, abort_flag)) {
-                        give_up();
-                        break;
-                    }
-                    mbar_expect_tx(&c_full[sc], CODE_BYTES);
-                    tma_2d(s_codes + sc * CODE_BYTES, &m_codes, &c_full[sc], c * 64, wt * TILE_M);
-                    ++it_c;
-                    for (int h = 0; h < 2 && ok; ++h) {
-                        const int sx = it_x % X_STAGES;
-                        if (!mbar_wait(&x_empty[sx], (it_x / X_STAGES & 1) ^ 1, abort_flag)) {
-                            give_up();
-                            break;
-                        }
-                        mbar_expect_tx(&x_full[sx], NT * 128);
-                        tma_2d(s_x + sx * NT * 128, &m_x, &x_full[sx], c * 128 + h * 64, tt * NT);
-                        ++it_x;
-                    }
-                }
-            }
-            __syncwarp();
-        } else if (warp == 1) {
-            if (lane == 0) {
-                for (int c = c0; c < c1 && ok; ++c) {
-                    for (int h = 0; h < 2 && ok; ++h) {
-                        const int sx = it_x % X_STAGES, sa = it_a % A_STAGES;
-                        if (!mbar_wait(&x_full[sx], it_x / X_STAGES & 1, abort_flag) ||
-                            !mbar_wait(&a_full[sa], it_a / A_STAGES & 1, abort_flag)) {
-                            give_up();
-                            break;
-                        }
-                        fence_after();
-                        const uint64_t xd = desc_k(su32(s_x + sx * NT * 128));
-                        const uint32_t at = tb + A_COL + sa * 32;
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            const int k = h * 64 + kk * 16, sd = it_d % D_STAGES;
-                            if (k % G == 0) {
-                                if (!mbar_wait(&d_empty[sd], (it_d / D_STAGES & 1) ^ 1, abort_flag)) {
-                                    give_up();
-                                    break;
-                                }
-                                fence_after();
-                            }
-                            umma_ts(tb + sd * NT, at + kk * 8, xd + (kk * 32 >> 4), IDESC, k % G ? 1u : 0u);
-                            if ((k + 16) % G == 0) {
-                                commit(&d_full[sd]);
-                                ++it_d;
-                            }
-                        }
-                        commit(&x_empty[sx]);
-                        commit(&a_empty[sa]);
-                        ++it_x;
-                        ++it_a;
-                    }
-                }
-            }
-            __syncwarp();
-        } else if (warp >= 4 && warp < 8) {
-            const int r = (warp - 4) * 32 + lane;
-            const uint32_t t_row = (uint32_t)(warp - 4) << 21;  // lanes 32 (warp - 4) .. of TMEM
+#pragma unroll 1
             for (int c = c0; c < c1 && ok; ++c) {
-                const int sc = it_c % C_STAGES;
-                if (!warp_wait(&c_full[sc], it_c / C_STAGES & 1, abort_flag)) {
+                if (!warp_phase(&c_empty[st.at], st.phase ^ 1, abort_flag) || !warp_phase(&empty[st.at], st.phase ^ 1, abort_flag)) {
                     give_up();
                     break;
                 }
-                // piece t of the row's 64 bytes: words of inputs 32 w + 8 t (64-byte swizzle)
-                uint4 q[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) q[t] = *(const uint4*)(s_codes + sc * CODE_BYTES + r * 64 + ((t ^ (r >> 1 & 3)) << 4));
-                warp_arrive(&c_empty[sc]);
-                ++it_c;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int sa = it_a % A_STAGES;
-                    if (!warp_wait(&a_empty[sa], (it_a / A_STAGES & 1) ^ 1, abort_flag)) {
+                if (elect_one()) {
+                    uint64_t* bar = &in[st.at];
+                    char* x = s_x + st.at * X_BYTES;
+                    mbar_expect_tx(bar, CODE_BYTES + X_BYTES);
+                    tma_2d(s_codes + st.at * CODE_BYTES, &m_codes, bar, c * 64, wt * TILE_M);
+                    tma_2d(x, &m_x, bar, c * 128, tt * NT);
+                    tma_2d(x + X_BYTES / 2, &m_x, bar, c * 128 + 64, tt * NT);
+                }
+                __syncwarp();
+                st.step();
+            }
+        } else if (warp == 1) {
+#pragma unroll 1
+            for (int c = c0; c < c1 && ok; ++c) {
+                if (!warp_phase(&in[st.at], st.phase, abort_flag) || !warp_phase(&full[st.at], st.phase, abort_flag)) {
+                    give_up();
+                    break;
+                }
+                uint64_t xd = desc_k(su32(s_x + st.at * X_BYTES));
+                uint32_t at = tb + A_COL + st.at * 64;
+#pragma unroll 1
+                for (int g = 0; g < SPC; ++g) {
+                    if (!warp_phase(&d_empty[sd.at], sd.phase ^ 1, abort_flag)) {
                         give_up();
                         break;
                     }
                     fence_after();
+                    const uint32_t d = tb + sd.at * NT;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < G / 16; ++kk) {
+                            const int k = kk * 16;  // (the second 64 inputs are NT rows of 128 bytes behind)
+                            umma_ts(d, at + k / 2, xd + ((k / 64 * NT * 128 + k % 64 * 2) >> 4), IDESC, kk ? 1u : 0u);
+                        }
+                        commit(&d_full[sd.at]);
+                        if (g == SPC - 1) commit(&empty[st.at]);
+                    }
+                    __syncwarp();
+                    sd.step();
+                    at += G / 2;
+                    xd += (G == 128 ? 0 : G == 64 ? NT * 128 : g == 1 ? NT * 128 - 64 : 64) >> 4;
+                }
+                st.step();
+            }
+        } else if (warp >= 4 && warp < 8) {
+            const int r = (warp - 4) * 32 + lane;
+            const uint32_t t_row = tb + ((uint32_t)(warp - 4) << 21) + A_COL;  // lanes 32 (warp - 4) .. of TMEM
+            // piece t of the row's 64 bytes: words of inputs 32 w + 8 t (64-byte swizzle)
+            uint4 q[4];
+            auto read_codes = [&]() {
+                if (!warp_phase(&in[st.at], st.phase, abort_flag)) return false;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) q[t] = *(const uint4*)(s_codes + st.at * CODE_BYTES + r * 64 + ((t ^ (r >> 1 & 3)) << 4));
+                return true;
+            };
+            if (!read_codes()) give_up();
+#pragma unroll 1
+            for (int c = c0; c < c1 && ok; ++c) {
+                uint64_t* done = &full[st.at];
+                warp_arrive(&c_empty[st.at]);
+                if (!warp_phase(&empty[st.at], st.phase ^ 1, abort_flag)) {
+                    give_up();
+                    break;
+                }
+                fence_after();
+                const uint32_t col = t_row + st.at * 64;
+                st.step();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
                     uint32_t v[32];
 #pragma unroll
                     for (int w = 0; w < 2; ++w)
@@ -204,12 +232,13 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                             o[2] = code_pair<false>(x >> 8);
                             o[3] = code_pair<true>(x >> 8);
                         }
-                    TMEM_ST32(tb + t_row + A_COL + sa * 32, v);
-                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                    fence_before();
-                    warp_arrive(&a_full[sa]);
-                    ++it_a;
+                    TMEM_ST32(col + h * 32, v);
                 }
+                // the next codes while these are stored
+                if (c + 1 < c1 && !read_codes()) give_up();
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                fence_before();
+                warp_arrive(done);
             }
         } else if (warp >= 8) {
             const int quarter = warp & 3, half = (warp - 8) >> 2;
@@ -221,13 +250,13 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             for (int i = 0; i < CW / 2; ++i) acc[i] = make_float2(0.f, 0.f);
             Scales<G> next;
             next.load(sp + (long long)c0 * SPC);
+#pragma unroll 1
             for (int c = c0; c < c1 && ok; ++c) {
                 const Scales<G> sc = next;
                 if (c + 1 < c1) next.load(sp + (long long)(c + 1) * SPC);
-#pragma unroll
+#pragma unroll 1
                 for (int g = 0; g < SPC; ++g) {
-                    const int sd = it_d % D_STAGES;
-                    if (!warp_wait(&d_full[sd], it_d / D_STAGES & 1, abort_flag)) {
+                    if (!warp_phase(&d_full[sd.at], sd.phase, abort_flag)) {
                         give_up();
                         break;
                     }
@@ -240,65 +269,67 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                     for (int b = 0; b < CW; b += B) {
                         uint32_t v[B];
 #pragma unroll
-                        for (int i = 0; i < B; i += 16) tmem_ld16(t_at + sd * NT + b + i, v + i);
+                        for (int i = 0; i < B; i += 16) tmem_ld16(t_at + sd.at * NT + b + i, v + i);
                         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
                         if (b + B == CW) {
                             fence_before();
-                            warp_arrive(&d_empty[sd]);
+                            warp_arrive(&d_empty[sd.at]);
                         }
 #pragma unroll
                         for (int i = 0; i < B; i += 2)
                             acc[(b + i) / 2] = __ffma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), s2, acc[(b + i) / 2]);
                     }
-                    ++it_d;
+                    sd.step();
                 }
             }
-            auto value = [&](int i) { return CODE_UNIT * (i & 1 ? acc[i / 2].y : acc[i / 2].x); };
-            // one column of the tile: the weight rows' results for one row of inputs (all lanes)
-            auto store = [&](int col, float v) {
-                const int t = tt * NT + half * CW + col;
-                if (t >= a.rows) return;
+            // this CTA's sums, [column][weight row], then the columns that are this CTA's to finish
+            float* mine = part + (half * CW) * TILE_M + r;
+#pragma unroll
+            for (int i = 0; i < CW; ++i) mine[i * TILE_M] = CODE_UNIT * (i & 1 ? acc[i / 2].y : acc[i / 2].x);
+            __syncwarp();
+            if (cluster > 1) cluster_sync();
+            const int i0 = CW * rank / cluster, i1 = min(CW * (rank + 1) / cluster, a.rows - tt * NT - half * CW);
+            constexpr int U = CW < 16 ? CW : 16;  // columns whose loads are on their way together
+#pragma unroll 1
+            for (int i = i0; i < i1 && ok; i += U) {
+                float v[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) v[u] = 0.f;
+                for (int q = 0; q < cluster; ++q) {
+                    const uint32_t from = peer_addr(mine + i * TILE_M, q);
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (i + u < i1) v[u] += ld_peer(from + u * TILE_M * 4);
+                }
+                const long long row = (long long)(tt * NT + half * CW + i) * a.ld_y;
                 if (a.epi == BLEND_W4_SWIGLU) {
                     // lanes 0..15 hold gate rows, 16..31 the up rows that go with them
-                    const float up = __shfl_down_sync(0xffffffffu, v, 16);
-                    if (lane >= 16 || j >= a.w.n) return;
-                    const float y = v / (1.f + __expf(-v)) * up;
-                    const long long at = (long long)t * a.ld_y + (wt * TILE_M + quarter * 32) / 2 + lane;
-                    if (a.y_f32) ((float*)a.y)[at] = y;
-                    else ((bf16*)a.y)[at] = __float2bfloat16_rn(y);
-                    return;
-                }
-                if (j >= a.w.n) return;
-                const long long at = (long long)t * a.ld_y + j;
-                if (a.epi == BLEND_W4_ADD) ((float*)a.y)[at] += v;
-                else if (a.y_f32) ((float*)a.y)[at] = v;
-                else ((bf16*)a.y)[at] = __float2bfloat16_rn(v);
-            };
-            if (cluster == 1) {
-                if (ok) {
+                    const long long at = row + (wt * TILE_M + quarter * 32) / 2 + lane;
 #pragma unroll
-                    for (int i = 0; i < CW; ++i) store(i, value(i));
-                }
-            } else {
+                    for (int u = 0; u < U; ++u) {
+                        const float up = __shfl_down_sync(0xffffffffu, v[u], 16);
+                        const float y = v[u] / (1.f + __expf(-v[u])) * up;
+                        if (lane >= 16 || j >= a.w.n || i + u >= i1) continue;
+                        if (a.y_f32) ((float*)a.y)[at + u * a.ld_y] = y;
+                        else ((bf16*)a.y)[at + u * a.ld_y] = __float2bfloat16_rn(y);
+                    }
+                } else if (j < a.w.n) {
 #pragma unroll
-                for (int i = 0; i < CW; ++i) part[(half * CW + i) * TILE_M + r] = value(i);
-                __syncwarp();
-                cluster_sync();
-                if (ok) {
-                    const int i0 = CW * rank / cluster, i1 = CW * (rank + 1) / cluster;
-                    for (int i = i0; i < i1; ++i) {
-                        float v = 0.f;
-                        for (int q = 0; q < cluster; ++q)
-                            v += cg::this_cluster().map_shared_rank(part, q)[(half * CW + i) * TILE_M + r];
-                        store(i, v);
+                    for (int u = 0; u < U; ++u) {
+                        if (i + u >= i1) continue;
+                        const long long at = row + j + u * a.ld_y;
+                        if (a.epi == BLEND_W4_ADD) ((float*)a.y)[at] += v[u];
+                        else if (a.y_f32) ((float*)a.y)[at] = v[u];
+                        else ((bf16*)a.y)[at] = __float2bfloat16_rn(v[u]);
                     }
                 }
-                __syncwarp();
-                cluster_sync();
             }
+            __syncwarp();
+            if (cluster > 1) cluster_sync();
         }
         if (cluster > 1 && warp < 8) {
             // the epilogue's two meetings
+            __syncwarp();
             cluster_sync();
             cluster_sync();
         }
@@ -308,12 +339,15 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     if (*abort_flag) {
         int never = 0;
         if (warp == 0 && lane == 0) {
-            for (uint32_t i = it_c > C_STAGES ? it_c - C_STAGES : 0; i < it_c; ++i) mbar_wait(&c_full[i % C_STAGES], i / C_STAGES & 1, &never);
-            for (uint32_t i = it_x > X_STAGES ? it_x - X_STAGES : 0; i < it_x; ++i) mbar_wait(&x_full[i % X_STAGES], i / X_STAGES & 1, &never);
+            // the last copies into each stage: a stage's use before st.at is of this round, others of the last
+            for (int i = 0; i < STAGES; ++i) {
+                const uint32_t par = i < st.at ? st.phase : st.phase ^ 1;
+                phase_wait(&in[i], par, &never);
+            }
         }
         if (warp == 1 && lane == 0) {
             commit(&drain);
-            mbar_wait(&drain, 0, &never);
+            phase_wait(&drain, 0, &never);
         }
         __syncwarp();
     }
@@ -347,12 +381,12 @@ template <int NT, int G> int go_tile(const W4Linear& a, cudaStream_t s) {
     // clusters of 1..8 CTAs that run side by side
     static int fit[TILE_MAX_CLUSTER + 1] = {-1};
     if (fit[0] < 0) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_smem<NT>(true)) != cudaSuccess) return BLEND_ECUDA;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_smem<NT>()) != cudaSuccess) return BLEND_ECUDA;
         for (int c = 1; c <= TILE_MAX_CLUSTER; ++c) {
             attr.val.clusterDim.x = (unsigned)c;
             cfg.numAttrs = 1;
             cfg.gridDim = dim3(152u / c * c);
-            cfg.dynamicSmemBytes = tile_smem<NT>(c > 1);
+            cfg.dynamicSmemBytes = tile_smem<NT>();
             int n = 0;
             if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
                 cudaGetLastError();
@@ -384,7 +418,7 @@ template <int NT, int G> int go_tile(const W4Linear& a, cudaStream_t s) {
     attr.val.clusterDim.x = (unsigned)cluster;
     cfg.numAttrs = cluster > 1 ? 1 : 0;
     cfg.gridDim = dim3((unsigned)((tiles < fit[cluster] ? tiles : fit[cluster]) * cluster));
-    cfg.dynamicSmemBytes = tile_smem<NT>(cluster > 1);
+    cfg.dynamicSmemBytes = tile_smem<NT>();
     if (cudaLaunchKernelEx(&cfg, kern, mc, mx, a, cluster) != cudaSuccess) return BLEND_ECUDA;
     note_launch();
     return BLEND_OK;
