@@ -61,6 +61,7 @@ __device__ __forceinline__ bool phase_wait(uint64_t* b, uint32_t par, volatile i
 }
 // The same for a warp whose lanes go on together.
 __device__ __forceinline__ bool warp_phase(uint64_t* b, uint32_t par, volatile int* abort_flag) {
+    if (__all_sync(0xffffffffu, mbar_try(b, par))) return true;
     return __all_sync(0xffffffffu, phase_wait(b, par, abort_flag));
 }
 // One lane of a converged warp, in a form that the compiler knows to be one.
@@ -125,9 +126,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tb = __shfl_sync(0xffffffffu, tmem_sh, 0);
+    // (all of TMEM: the columns begin at 0)
+    constexpr uint32_t tb = 0;
 
-    const int rank = cluster > 1 ? (int)cta_rank() : 0;
+    const int rank = blockIdx.x % cluster;
     const int n_t = (a.rows + NT - 1) / NT, total = (a.w.n + TILE_M - 1) / TILE_M * n_t;
     const int tile0 = blockIdx.x / cluster, tile_step = gridDim.x / cluster;
     const int c0 = a.w.chunks * rank / cluster, c1 = a.w.chunks * (rank + 1) / cluster;
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     __syncthreads();
     if (warp == 1) {
         fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tb), "r"(TILE_COLS) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_sh), "r"(TILE_COLS) : "memory");
     }
 }
 
