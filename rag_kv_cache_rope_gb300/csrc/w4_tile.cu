@@ -19,9 +19,9 @@
 namespace blend {
 namespace {
 
-constexpr int TILE_M = 128, TILE_THREADS = 512;
+constexpr int TILE_M = 128, TILE_THREADS = 512, EPI_WARPS = 8;
 constexpr int STAGES = 4;     // chunks of 128 inputs on their way: codes, operands in TMEM, inputs
-constexpr int D_STAGES = 2;   // accumulators of a group
+constexpr int D_STAGES = 2;   // of 128 columns: the accumulators of one group or, with fewer rows, of several
 constexpr int CODE_BYTES = TILE_M * 64;
 constexpr int A_COL = 256, TILE_COLS = 512;  // accumulators, then 64 columns a stage
 constexpr int TILE_MAX_CLUSTER = 8;
@@ -31,12 +31,21 @@ template <int NT> constexpr int tile_smem() {
     return STAGES * (NT * 256 + CODE_BYTES) + NT * TILE_M * 4 + 1024;
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t* r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(t));
+// C columns of a warp's lanes: 16, 32 or 64.
+template <int C> __device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[C]) {
+    if constexpr (C == 64) {
+        TMEM_LD32(t, r);
+        uint32_t* h = r + 32;
+        TMEM_LD32(t + 32, h);
+    } else if constexpr (C == 32) {
+        TMEM_LD32(t, r);
+    } else {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+              "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(t));
+    }
 }
 // shared::cluster address of this CTA's variable in CTA `rank` of the cluster, and a load from one
 __device__ __forceinline__ uint32_t peer_addr(const void* p, int rank) {
@@ -59,10 +68,41 @@ __device__ __forceinline__ bool phase_wait(uint64_t* b, uint32_t par, volatile i
     }
     return false;
 }
-// The same for a warp whose lanes go on together.
-__device__ __forceinline__ bool warp_phase(uint64_t* b, uint32_t par, volatile int* abort_flag) {
-    if (__all_sync(0xffffffffu, mbar_try(b, par))) return true;
-    return __all_sync(0xffffffffu, phase_wait(b, par, abort_flag));
+// A warp's wait for one to three phases: a look at a barrier takes 70 cycles, so they are looked at together.
+// (One lane looking for its warp took 300.)
+__device__ __forceinline__ bool warp_phases(volatile int* abort_flag, uint64_t* b0, uint32_t p0, uint64_t* b1 = nullptr, uint32_t p1 = 0,
+                                            uint64_t* b2 = nullptr, uint32_t p2 = 0) {
+    bool done = mbar_try(b0, p0);
+    if (b1) done &= mbar_try(b1, p1);
+    if (b2) done &= mbar_try(b2, p2);
+    if (__all_sync(0xffffffffu, done)) return true;
+    done = phase_wait(b0, p0, abort_flag);
+    if (b1) done = done && phase_wait(b1, p1, abort_flag);
+    if (b2) done = done && phase_wait(b2, p2, abort_flag);
+    return __all_sync(0xffffffffu, done);
+}
+// A warp's wait for a phase that other CTAs' arrivals end, and its arrival on a barrier in every CTA of the
+// cluster.  (They are looked at without blocking: a blocking look resumes late after an arrival from outside.)
+__device__ __forceinline__ bool cluster_phase(uint64_t* b, uint32_t par, volatile int* abort_flag) {
+    bool done = false;
+#pragma unroll 1
+    for (int i = 0; i < WAIT_LIMIT && !done; ++i) {
+        uint32_t p;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+                     : "=r"(p)
+                     : "r"(su32(b)), "r"(par)
+                     : "memory");
+        done = p != 0;
+        if (!done && *abort_flag) break;
+    }
+    return __all_sync(0xffffffffu, done);
+}
+__device__ __forceinline__ void meet(uint64_t* b, int cluster) {
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    __syncwarp();
+    if ((int)(threadIdx.x & 31) < cluster)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(b, threadIdx.x & 31)) : "memory");
+    __syncwarp();
 }
 // One lane of a converged warp, in a form that the compiler knows to be one.
 __device__ __forceinline__ bool elect_one() {
@@ -88,10 +128,12 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     k_w4_tile(const __grid_constant__ CUtensorMap m_codes, const __grid_constant__ CUtensorMap m_x, const W4Linear a, int cluster) {
     constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((NT >> 3) << 17) | ((TILE_M >> 4) << 24);
     constexpr int SPC = 128 / G, CW = NT / 2;  // groups of a chunk; columns of an epilogue thread
+    constexpr int GB = SPC < 128 / NT ? SPC : 128 / NT;  // groups whose accumulators make a stage
     constexpr int X_BYTES = NT * 256;          // two halves of 64 inputs
     extern __shared__ char smem_raw[];
     // in: codes and inputs have come; full: four warps' operands; empty: their products are done
-    __shared__ uint64_t in[STAGES], full[STAGES], empty[STAGES], c_empty[STAGES], d_full[D_STAGES], d_empty[D_STAGES], drain;
+    __shared__ uint64_t in[STAGES], full[STAGES], empty[STAGES], c_empty[STAGES], d_full[D_STAGES], d_empty[D_STAGES],
+        p_full, p_empty, drain;  // p: sums of the cluster's CTAs
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_sh;
     volatile int* abort_flag = &abort_sh;
@@ -112,8 +154,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         }
         for (int i = 0; i < D_STAGES; ++i) {
             mbar_init(&d_full[i], 1);
-            mbar_init(&d_empty[i], 8);
+            mbar_init(&d_empty[i], EPI_WARPS);
         }
+        mbar_init(&p_full, EPI_WARPS * cluster);
+        mbar_init(&p_empty, EPI_WARPS * cluster);
         mbar_init(&drain, 1);
         abort_sh = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -125,6 +169,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     }
     fence_before();
     __syncthreads();
+    if (cluster > 1) cluster_sync();  // all CTAs' barriers exist
     fence_after();
     // (all of TMEM: the columns begin at 0)
     constexpr uint32_t tb = 0;
@@ -143,13 +188,27 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     };
     Ring<STAGES> st;   // this role's stage
     Ring<D_STAGES> sd;
+    Ring<1> met;
 
+    // The roles' ends are their own, with no code in common: what runs on fewer registers stays within them.
+    auto end_of_work = [&]() {
+        fence_before();
+        asm volatile("barrier.sync 0;" ::: "memory");
+    };
+    auto end_of_cluster = [&]() {
+        fence_before();
+        asm volatile("barrier.sync 0;" ::: "memory");
+        if (cluster > 1) cluster_sync();  // no CTA leaves while another reads its sums
+    };
+    // Each role walks over the tiles by itself; registers go from the first four warps to the epilogue's.
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0) {
     for (int tile = tile0; tile < total; tile += tile_step) {
         const int wt = tile / n_t, tt = tile - wt * n_t;
-        if (warp == 0) {
 #pragma unroll 1
             for (int c = c0; c < c1 && ok; ++c) {
-                if (!warp_phase(&c_empty[st.at], st.phase ^ 1, abort_flag) || !warp_phase(&empty[st.at], st.phase ^ 1, abort_flag)) {
+                if (!warp_phases(abort_flag, &c_empty[st.at], st.phase ^ 1, &empty[st.at], st.phase ^ 1)) {
                     give_up();
                     break;
                 }
@@ -164,88 +223,122 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                 __syncwarp();
                 st.step();
             }
+            }
         } else if (warp == 1) {
+    for (int tile = tile0; tile < total; tile += tile_step) {
 #pragma unroll 1
             for (int c = c0; c < c1 && ok; ++c) {
-                if (!warp_phase(&in[st.at], st.phase, abort_flag) || !warp_phase(&full[st.at], st.phase, abort_flag)) {
+                if (!warp_phases(abort_flag, &in[st.at], st.phase, &full[st.at], st.phase, &d_empty[sd.at], sd.phase ^ 1)) {
                     give_up();
                     break;
                 }
-                uint64_t xd = desc_k(su32(s_x + st.at * X_BYTES));
-                uint32_t at = tb + A_COL + st.at * 64;
-#pragma unroll 1
-                for (int g = 0; g < SPC; ++g) {
-                    if (!warp_phase(&d_empty[sd.at], sd.phase ^ 1, abort_flag)) {
+                const uint64_t xd = desc_k(su32(s_x + st.at * X_BYTES));
+                const uint32_t at = tb + A_COL + st.at * 64;
+#pragma unroll
+                for (int b = 0; b < SPC / GB; ++b) {
+                    if (b > 0 && !warp_phases(abort_flag, &d_empty[sd.at], sd.phase ^ 1)) {
                         give_up();
                         break;
                     }
                     fence_after();
-                    const uint32_t d = tb + sd.at * NT;
+                    const uint32_t d = tb + sd.at * 128;
                     if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < G / 16; ++kk) {
-                            const int k = kk * 16;  // (the second 64 inputs are NT rows of 128 bytes behind)
-                            umma_ts(d, at + k / 2, xd + ((k / 64 * NT * 128 + k % 64 * 2) >> 4), IDESC, kk ? 1u : 0u);
+                        for (int kk = 0; kk < GB * G / 16; ++kk) {
+                            const int k = b * GB * G + kk * 16;  // (the second 64 inputs are NT rows of 128 bytes behind)
+                            umma_ts(d + kk * 16 / G * NT, at + k / 2, xd + ((k / 64 * NT * 128 + k % 64 * 2) >> 4), IDESC, k % G ? 1u : 0u);
                         }
                         commit(&d_full[sd.at]);
-                        if (g == SPC - 1) commit(&empty[st.at]);
+                        if (b == SPC / GB - 1) commit(&empty[st.at]);
                     }
                     __syncwarp();
                     sd.step();
-                    at += G / 2;
-                    xd += (G == 128 ? 0 : G == 64 ? NT * 128 : g == 1 ? NT * 128 - 64 : 64) >> 4;
                 }
                 st.step();
             }
-        } else if (warp >= 4 && warp < 8) {
+            }
+        }
+        end_of_work();
+        if (*abort_flag) {
+            // after a wait that ran out, what is still in flight: copies, then products
+            int never = 0;
+            if (warp == 0) {
+                // (a stage's use before st.at is of this round, others of the last)
+#pragma unroll 1
+                for (int i = 0; i < STAGES; ++i) phase_wait(&in[i], i < st.at ? st.phase : st.phase ^ 1, &never);
+            }
+            if (warp == 1) {
+                if (elect_one()) commit(&drain);
+                __syncwarp();
+                phase_wait(&drain, 0, &never);
+            }
+            __syncwarp();
+        }
+        end_of_cluster();
+        if (warp == 1) {
+            fence_after();
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_sh), "r"(TILE_COLS) : "memory");
+        }
+    } else if (warp < 8) {
+    for (int tile = tile0; tile < total; tile += tile_step) {
             const int r = (warp - 4) * 32 + lane;
             const uint32_t t_row = tb + ((uint32_t)(warp - 4) << 21) + A_COL;  // lanes 32 (warp - 4) .. of TMEM
             // piece t of the row's 64 bytes: words of inputs 32 w + 8 t (64-byte swizzle)
             uint4 q[4];
             auto read_codes = [&]() {
-                if (!warp_phase(&in[st.at], st.phase, abort_flag)) return false;
 #pragma unroll
                 for (int t = 0; t < 4; ++t) q[t] = *(const uint4*)(s_codes + st.at * CODE_BYTES + r * 64 + ((t ^ (r >> 1 & 3)) << 4));
-                return true;
             };
-            if (!read_codes()) give_up();
+            if (warp_phases(abort_flag, &in[st.at], st.phase)) read_codes();
+            else give_up();
+            uint64_t* stored = nullptr;  // the chunk before, whose operands are on their way to TMEM
+            auto publish = [&]() {
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                fence_before();
+                warp_arrive(stored);
+            };
 #pragma unroll 1
             for (int c = c0; c < c1 && ok; ++c) {
-                uint64_t* done = &full[st.at];
                 warp_arrive(&c_empty[st.at]);
-                if (!warp_phase(&empty[st.at], st.phase ^ 1, abort_flag)) {
+                if (!warp_phases(abort_flag, &empty[st.at], st.phase ^ 1)) {
                     give_up();
                     break;
                 }
                 fence_after();
-                const uint32_t col = t_row + st.at * 64;
+                uint32_t v[2][32];
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const uint32_t x = word_of(q[t], w);
+                        uint32_t* o = v[w >> 1] + 16 * (w & 1) + 4 * t;
+                        o[0] = code_pair<false>(x);
+                        o[1] = code_pair<true>(x);
+                        o[2] = code_pair<false>(x >> 8);
+                        o[3] = code_pair<true>(x >> 8);
+                    }
+                if (stored) publish();
+                stored = &full[st.at];
+                TMEM_ST32(t_row + st.at * 64, v[0]);
+                TMEM_ST32(t_row + st.at * 64 + 32, v[1]);
                 st.step();
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t v[32];
-#pragma unroll
-                    for (int w = 0; w < 2; ++w)
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            const uint32_t x = word_of(q[t], 2 * h + w);
-                            uint32_t* o = v + 16 * w + 4 * t;
-                            o[0] = code_pair<false>(x);
-                            o[1] = code_pair<true>(x);
-                            o[2] = code_pair<false>(x >> 8);
-                            o[3] = code_pair<true>(x >> 8);
-                        }
-                    TMEM_ST32(col + h * 32, v);
-                }
                 // the next codes while these are stored
-                if (c + 1 < c1 && !read_codes()) give_up();
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                fence_before();
-                warp_arrive(done);
+                if (c + 1 < c1) {
+                    if (warp_phases(abort_flag, &in[st.at], st.phase)) read_codes();
+                    else give_up();
+                }
             }
-        } else if (warp >= 8) {
-            const int quarter = warp & 3, half = (warp - 8) >> 2;
+            if (stored) publish();
+    }
+        end_of_work();
+        end_of_cluster();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    for (int tile = tile0; tile < total; tile += tile_step) {
+        const int wt = tile / n_t, tt = tile - wt * n_t;
+            const int quarter = warp & 3, cols = (warp - 8) >> 2;
             const int r = quarter * 32 + lane, j = wt * TILE_M + r;
-            const uint32_t t_at = tb + ((uint32_t)quarter << 21) + half * CW;
+            const uint32_t t_at = tb + ((uint32_t)quarter << 21) + cols * CW;
             const bf16* sp = a.w.scale + (long long)min(j, a.w.n - 1) * a.w.chunks * SPC;
             float2 acc[CW / 2];
 #pragma unroll
@@ -257,40 +350,42 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                 const Scales<G> sc = next;
                 if (c + 1 < c1) next.load(sp + (long long)(c + 1) * SPC);
 #pragma unroll 1
-                for (int g = 0; g < SPC; ++g) {
-                    if (!warp_phase(&d_full[sd.at], sd.phase, abort_flag)) {
+                for (int b = 0; b < SPC / GB; ++b) {
+                    if (!warp_phases(abort_flag, &d_full[sd.at], sd.phase)) {
                         give_up();
                         break;
                     }
                     fence_after();
-                    // (a group behind k has no scale)
-                    const float s = c * 128 + g * G < a.w.k ? sc.get(g) : 0.f;
-                    const float2 s2 = make_float2(s, s);
-                    constexpr int B = CW < 32 ? CW : 32;
 #pragma unroll
-                    for (int b = 0; b < CW; b += B) {
-                        uint32_t v[B];
-#pragma unroll
-                        for (int i = 0; i < B; i += 16) tmem_ld16(t_at + sd.at * NT + b + i, v + i);
+                    for (int gb = 0; gb < GB; ++gb) {
+                        const int g = b * GB + gb;
+                        // (a group behind k has no scale)
+                        const float s = c * 128 + g * G < a.w.k ? sc.get(g) : 0.f;
+                        const float2 s2 = make_float2(s, s);
+                        uint32_t v[CW];
+                        tmem_ld<CW>(t_at + sd.at * 128 + gb * NT, v);
                         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-                        if (b + B == CW) {
+                        if (gb == GB - 1) {
                             fence_before();
                             warp_arrive(&d_empty[sd.at]);
                         }
 #pragma unroll
-                        for (int i = 0; i < B; i += 2)
-                            acc[(b + i) / 2] = __ffma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), s2, acc[(b + i) / 2]);
+                        for (int i = 0; i < CW; i += 2)
+                            acc[i / 2] = __ffma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), s2, acc[i / 2]);
                     }
                     sd.step();
                 }
             }
             // this CTA's sums, [column][weight row], then the columns that are this CTA's to finish
-            float* mine = part + (half * CW) * TILE_M + r;
+            float* mine = part + (cols * CW) * TILE_M + r;
+            if (cluster > 1 && ok && !cluster_phase(&p_empty, met.phase ^ 1, abort_flag)) give_up();  // the last tile's have been read
 #pragma unroll
             for (int i = 0; i < CW; ++i) mine[i * TILE_M] = CODE_UNIT * (i & 1 ? acc[i / 2].y : acc[i / 2].x);
-            __syncwarp();
-            if (cluster > 1) cluster_sync();
-            const int i0 = CW * rank / cluster, i1 = min(CW * (rank + 1) / cluster, a.rows - tt * NT - half * CW);
+            if (cluster > 1) {
+                meet(&p_full, cluster);
+                if (ok && !cluster_phase(&p_full, met.phase, abort_flag)) give_up();
+            }
+            const int i0 = CW * rank / cluster, i1 = min(CW * (rank + 1) / cluster, a.rows - tt * NT - cols * CW);
             constexpr int U = CW < 16 ? CW : 16;  // columns whose loads are on their way together
 #pragma unroll 1
             for (int i = i0; i < i1 && ok; i += U) {
@@ -303,7 +398,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                     for (int u = 0; u < U; ++u)
                         if (i + u < i1) v[u] += ld_peer(from + u * TILE_M * 4);
                 }
-                const long long row = (long long)(tt * NT + half * CW + i) * a.ld_y;
+                const long long row = (long long)(tt * NT + cols * CW + i) * a.ld_y;
                 if (a.epi == BLEND_W4_SWIGLU) {
                     // lanes 0..15 hold gate rows, 16..31 the up rows that go with them
                     const long long at = row + (wt * TILE_M + quarter * 32) / 2 + lane;
@@ -326,38 +421,13 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                     }
                 }
             }
-            __syncwarp();
-            if (cluster > 1) cluster_sync();
-        }
-        if (cluster > 1 && warp < 8) {
-            // the epilogue's two meetings
-            __syncwarp();
-            cluster_sync();
-            cluster_sync();
-        }
-    }
-    // After a wait that ran out, what is still in flight: copies, then products.
-    __syncthreads();
-    if (*abort_flag) {
-        int never = 0;
-        if (warp == 0 && lane == 0) {
-            // the last copies into each stage: a stage's use before st.at is of this round, others of the last
-            for (int i = 0; i < STAGES; ++i) {
-                const uint32_t par = i < st.at ? st.phase : st.phase ^ 1;
-                phase_wait(&in[i], par, &never);
+            if (cluster > 1) {
+                meet(&p_empty, cluster);
+                met.step();
             }
         }
-        if (warp == 1 && lane == 0) {
-            commit(&drain);
-            phase_wait(&drain, 0, &never);
-        }
-        __syncwarp();
-    }
-    fence_before();
-    __syncthreads();
-    if (warp == 1) {
-        fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_sh), "r"(TILE_COLS) : "memory");
+        end_of_work();
+        end_of_cluster();
     }
 }
 
