@@ -1,7 +1,7 @@
 // Products of many rows with 4-bit weights on tcgen05 (w4_linear in blend.h), bf16 inputs.
 //
 // A tile is 128 weight rows (M, the lanes of TMEM) by up to 128 input rows (N).  Weights are the A operand, in TMEM:
-// their codes come by TMA as 128 x 64 bytes a chunk of 128 inputs, four warps turn them into bf16
+// their codes come by TMA as 128 x 64 bytes a chunk of 128 inputs, eight warps turn them into bf16
 // integers (code - 8) / 64, which are exact, one lane a weight row, and store them to TMEM, so they never pass
 // through shared memory a second time and need no swizzle.  Inputs are the B operand, by TMA as they are.
 // Scales are not rounded into an operand: the products of one group are summed in a TMEM accumulator of
@@ -9,7 +9,7 @@
 // run.  So a result is what the few rows' kernel gives up to the order of fp32 sums.  (Scales inside the operand
 // take 11 bits: two bf16 parts and twice the products.)
 //   warp 0      TMA: codes and inputs            warp 1      tcgen05.mma of one lane, TMEM
-//   warps 4-7   codes to TMEM                    warps 8-15  scales, sums, results
+//   warps 4-11  codes to TMEM                    warps 12-19 scales, sums, results
 // Few tiles share their inputs' length among the CTAs of a cluster, which join their sums in order through
 // distributed shared memory.  All waits are bounded: on expiry the error word gets BLEND_ETIMEOUT, copies and
 // products in flight are waited for and TMEM is freed.
@@ -19,7 +19,7 @@
 namespace blend {
 namespace {
 
-constexpr int TILE_M = 128, TILE_THREADS = 512, EPI_WARPS = 8;
+constexpr int TILE_M = 128, TILE_THREADS = 640, EPI_WARPS = 8;
 constexpr int STAGES = 4;     // chunks of 128 inputs on their way: codes, operands in TMEM, inputs
 constexpr int D_STAGES = 2;   // of 128 columns: the accumulators of one group or, with fewer rows, of several
 constexpr int CODE_BYTES = TILE_M * 64;
@@ -98,7 +98,6 @@ __device__ __forceinline__ bool cluster_phase(uint64_t* b, uint32_t par, volatil
     return __all_sync(0xffffffffu, done);
 }
 __device__ __forceinline__ void meet(uint64_t* b, int cluster) {
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
     __syncwarp();
     if ((int)(threadIdx.x & 31) < cluster)
         asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(b, threadIdx.x & 31)) : "memory");
@@ -202,7 +201,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     };
     // Each role walks over the tiles by itself; registers go from the first four warps to the epilogue's.
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0) {
     for (int tile = tile0; tile < total; tile += tile_step) {
         const int wt = tile / n_t, tt = tile - wt * n_t;
@@ -279,64 +278,55 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             fence_after();
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_sh), "r"(TILE_COLS) : "memory");
         }
-    } else if (warp < 8) {
-    for (int tile = tile0; tile < total; tile += tile_step) {
-            const int r = (warp - 4) * 32 + lane;
-            const uint32_t t_row = tb + ((uint32_t)(warp - 4) << 21) + A_COL;  // lanes 32 (warp - 4) .. of TMEM
-            // piece t of the row's 64 bytes: words of inputs 32 w + 8 t (64-byte swizzle)
-            uint4 q[4];
-            auto read_codes = [&]() {
-#pragma unroll
-                for (int t = 0; t < 4; ++t) q[t] = *(const uint4*)(s_codes + st.at * CODE_BYTES + r * 64 + ((t ^ (r >> 1 & 3)) << 4));
-            };
-            if (warp_phases(abort_flag, &in[st.at], st.phase)) read_codes();
-            else give_up();
-            uint64_t* stored = nullptr;  // the chunk before, whose operands are on their way to TMEM
-            auto publish = [&]() {
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                fence_before();
-                warp_arrive(stored);
-            };
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        // two sets of four warps take every second chunk
+        const int r = (warp & 3) * 32 + lane, set = (warp >> 2) & 1;
+        const uint32_t t_row = tb + ((uint32_t)(warp & 3) << 21) + A_COL;  // lanes 32 (warp % 4) .. of TMEM
+        int turn = 1;
+        for (int tile = tile0; tile < total; tile += tile_step) {
 #pragma unroll 1
-            for (int c = c0; c < c1 && ok; ++c) {
-                warp_arrive(&c_empty[st.at]);
-                if (!warp_phases(abort_flag, &empty[st.at], st.phase ^ 1)) {
+            for (int c = c0; c < c1 && ok; ++c, st.step()) {
+                turn ^= 1;
+                if (turn != set) continue;
+                if (!warp_phases(abort_flag, &in[st.at], st.phase, &empty[st.at], st.phase ^ 1)) {
                     give_up();
                     break;
                 }
+                // piece t of the row's 64 bytes: words of inputs 32 w + 8 t (64-byte swizzle)
+                uint4 q[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) q[t] = *(const uint4*)(s_codes + st.at * CODE_BYTES + r * 64 + ((t ^ (r >> 1 & 3)) << 4));
                 fence_after();
-                uint32_t v[2][32];
 #pragma unroll
-                for (int w = 0; w < 4; ++w)
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t v[32];
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const uint32_t x = word_of(q[t], w);
-                        uint32_t* o = v[w >> 1] + 16 * (w & 1) + 4 * t;
-                        o[0] = code_pair<false>(x);
-                        o[1] = code_pair<true>(x);
-                        o[2] = code_pair<false>(x >> 8);
-                        o[3] = code_pair<true>(x >> 8);
-                    }
-                if (stored) publish();
-                stored = &full[st.at];
-                TMEM_ST32(t_row + st.at * 64, v[0]);
-                TMEM_ST32(t_row + st.at * 64 + 32, v[1]);
-                st.step();
-                // the next codes while these are stored
-                if (c + 1 < c1) {
-                    if (warp_phases(abort_flag, &in[st.at], st.phase)) read_codes();
-                    else give_up();
+                    for (int w = 0; w < 2; ++w)
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            const uint32_t x = word_of(q[t], 2 * h + w);
+                            uint32_t* o = v + 16 * w + 4 * t;
+                            o[0] = code_pair<false>(x);
+                            o[1] = code_pair<true>(x);
+                            o[2] = code_pair<false>(x >> 8);
+                            o[3] = code_pair<true>(x >> 8);
+                        }
+                    TMEM_ST32(t_row + st.at * 64 + h * 32, v);
                 }
+                warp_arrive(&c_empty[st.at]);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                fence_before();
+                warp_arrive(&full[st.at]);
             }
-            if (stored) publish();
-    }
+        }
         end_of_work();
         end_of_cluster();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     for (int tile = tile0; tile < total; tile += tile_step) {
         const int wt = tile / n_t, tt = tile - wt * n_t;
-            const int quarter = warp & 3, cols = (warp - 8) >> 2;
+            const int quarter = warp & 3, cols = (warp - 12) >> 2;
             const int r = quarter * 32 + lane, j = wt * TILE_M + r;
             const uint32_t t_at = tb + ((uint32_t)quarter << 21) + cols * CW;
             const bf16* sp = a.w.scale + (long long)min(j, a.w.n - 1) * a.w.chunks * SPC;
@@ -376,34 +366,14 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                     sd.step();
                 }
             }
-            // this CTA's sums, [column][weight row], then the columns that are this CTA's to finish
-            float* mine = part + (cols * CW) * TILE_M + r;
-            if (cluster > 1 && ok && !cluster_phase(&p_empty, met.phase ^ 1, abort_flag)) give_up();  // the last tile's have been read
-#pragma unroll
-            for (int i = 0; i < CW; ++i) mine[i * TILE_M] = CODE_UNIT * (i & 1 ? acc[i / 2].y : acc[i / 2].x);
-            if (cluster > 1) {
-                meet(&p_full, cluster);
-                if (ok && !cluster_phase(&p_full, met.phase, abort_flag)) give_up();
-            }
-            const int i0 = CW * rank / cluster, i1 = min(CW * (rank + 1) / cluster, a.rows - tt * NT - cols * CW);
-            constexpr int U = CW < 16 ? CW : 16;  // columns whose loads are on their way together
-#pragma unroll 1
-            for (int i = i0; i < i1 && ok; i += U) {
-                float v[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) v[u] = 0.f;
-                for (int q = 0; q < cluster; ++q) {
-                    const uint32_t from = peer_addr(mine + i * TILE_M, q);
-#pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        if (i + u < i1) v[u] += ld_peer(from + u * TILE_M * 4);
-                }
+            // columns i .. i + 7 (those below i1) of the tile: the weight rows' results for eight rows of inputs
+            auto store = [&](const float* v, int i, int i1) {
                 const long long row = (long long)(tt * NT + cols * CW + i) * a.ld_y;
                 if (a.epi == BLEND_W4_SWIGLU) {
                     // lanes 0..15 hold gate rows, 16..31 the up rows that go with them
                     const long long at = row + (wt * TILE_M + quarter * 32) / 2 + lane;
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
+                    for (int u = 0; u < 8; ++u) {
                         const float up = __shfl_down_sync(0xffffffffu, v[u], 16);
                         const float y = v[u] / (1.f + __expf(-v[u])) * up;
                         if (lane >= 16 || j >= a.w.n || i + u >= i1) continue;
@@ -412,7 +382,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                     }
                 } else if (j < a.w.n) {
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
+                    for (int u = 0; u < 8; ++u) {
                         if (i + u >= i1) continue;
                         const long long at = row + j + u * a.ld_y;
                         if (a.epi == BLEND_W4_ADD) ((float*)a.y)[at] += v[u];
@@ -420,10 +390,42 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                         else ((bf16*)a.y)[at] = __float2bfloat16_rn(v[u]);
                     }
                 }
-            }
+            };
+            // [column][weight row] of this CTA's sums, and the columns that are this CTA's to finish
+            float* mine = part + cols * CW * TILE_M + r;
+            const int i0 = CW * rank / cluster, i1 = min(CW * (rank + 1) / cluster, a.rows - tt * NT - cols * CW);
+            if (cluster > 1 && ok && !cluster_phase(&p_empty, met.phase ^ 1, abort_flag)) give_up();  // the last tile's have been read
+#pragma unroll
+            for (int i = 0; i < CW; ++i) mine[i * TILE_M] = CODE_UNIT * (i & 1 ? acc[i / 2].y : acc[i / 2].x);
             if (cluster > 1) {
+                meet(&p_full, cluster);
+                if (ok && !cluster_phase(&p_full, met.phase, abort_flag)) give_up();
+                // joined in the CTAs' order, and back to where this CTA's own were
+                constexpr int U = CW / 2;
+                float v[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) v[u] = 0.f;
+#pragma unroll 1
+                for (int q = 0; q < cluster; ++q) {
+                    const uint32_t from = peer_addr(mine + i0 * TILE_M, q);
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (i0 + u < i1) v[u] += ld_peer(from + u * TILE_M * 4);
+                }
                 meet(&p_empty, cluster);
                 met.step();
+                if (ok) {
+#pragma unroll
+                    for (int u = 0; u < U; u += 8) store(v + u, i0 + u, i1);
+                }
+            } else if (ok) {
+#pragma unroll 1
+                for (int i = 0; i < i1; i += 8) {
+                    float v[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) v[u] = mine[(i + u) * TILE_M];
+                    store(v, i, i1);
+                }
             }
         }
         end_of_work();
