@@ -24,7 +24,8 @@ namespace cg = cooperative_groups;
 namespace blend {
 namespace {
 
-constexpr int LP_THREADS = 512;
+constexpr int LP_THREADS = 256, LP_WARPS = LP_THREADS / 32;
+constexpr int LP_CTAS = 5;      // per SM: a row's start and end wait for memory and for one another
 constexpr int LP_GROUPS = 64;   // groups of threads whose maxima bound the k-th logit: twice the largest k
 constexpr int LP_CAND = 1024;   // candidates of one stretch
 constexpr int LP_MAX_CLUSTER = 16;
@@ -32,7 +33,9 @@ constexpr float LP_RAISE = 2.f;
 // References beyond this are not used: x c - R, a rounding of R by then, could be anything.
 constexpr float LP_HUGE = 16777216.f;
 constexpr float LN2 = 0.693147180559945309f;
-constexpr float FAR = -200.f;  // 2^FAR is 0 in fp32, and 0 times FAR is a number
+constexpr float FAR = -200.f;    // 2^FAR is 0 in fp32, and 0 times FAR is a number
+// Logits count as this at least in the sums: with a scale of up to 2^20 they are numbers then, and 2^t of them 0.
+constexpr float LP_LOW = -1e30f;
 
 using key_t = unsigned long long;
 
@@ -79,6 +82,14 @@ template <typename T> struct Row {
             for (int i = 0; i < VE; ++i) x[i] = e0 + i >= 0 && e0 + i < vocab ? to_f<T>(p[e0 + i]) : -INFINITY;
         }
     }
+    __device__ __forceinline__ uint4 raw(int j) const {
+        const int e0 = j * VE - off;
+        if (e0 >= 0 && e0 + VE <= vocab) return *reinterpret_cast<const uint4*>(p + e0);
+        Vec<T> v;
+#pragma unroll
+        for (int i = 0; i < VE; ++i) v.set(i, e0 + i >= 0 && e0 + i < vocab ? to_f<T>(p[e0 + i]) : -INFINITY);
+        return v.raw;
+    }
     __device__ __forceinline__ bool holds(int j, int i) const {  // element i of vector j is in the row
         const int e = j * VE - off + i;
         return e >= 0 && e < vocab;
@@ -89,6 +100,30 @@ template <typename T> struct Row {
 struct Sums {
     float r, z, s;  // reference, sum of 2^(t), sum of 2^(t) t with t = x c - r
 };
+__device__ __forceinline__ float max_keep_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// A vector's logits, LP_LOW at least, in pairs, and the largest of them (NaN stays NaN and is not the largest).
+__device__ __forceinline__ float pairs_of(const uint4& raw, float2 (&x)[4], bf16) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    const __nv_bfloat162 low = __float2bfloat162_rn(LP_LOW);
+    __nv_bfloat162 h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i] = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), low);
+        const uint32_t u = *reinterpret_cast<const uint32_t*>(&h[i]);
+        x[i] = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    }
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float pairs_of(const uint4& raw, float2 (&x)[2], float) {
+    x[0] = make_float2(max_keep_nan(__uint_as_float(raw.x), LP_LOW), max_keep_nan(__uint_as_float(raw.y), LP_LOW));
+    x[1] = make_float2(max_keep_nan(__uint_as_float(raw.z), LP_LOW), max_keep_nan(__uint_as_float(raw.w), LP_LOW));
+    return fmaxf(fmaxf(x[0].x, x[0].y), fmaxf(x[1].x, x[1].y));
+}
 // Two partial sums under the larger reference.  A part without a finite term has z = 0 and r = -infinity.
 __device__ __forceinline__ Sums join(Sums a, Sums b) {
     Sums o;
@@ -107,11 +142,11 @@ struct Shared {
     key_t list[BLEND_MAX_TOP];       // this stretch's ranking
     key_t all[LP_MAX_CLUSTER][BLEND_MAX_TOP];
     key_t merged[BLEND_MAX_TOP];
-    Sums sums[LP_THREADS / 32];
+    Sums sums[LP_WARPS];
     Sums total;
     float group_max[LP_GROUPS];
     int active[LP_THREADS];
-    int n_active, n_cand, overflow, warp_tot[LP_THREADS / 32];
+    int n_active, n_cand, overflow, warp_tot[LP_WARPS];
     float bound;
 };
 
@@ -143,7 +178,7 @@ __device__ void take_in_order(const Row<T>& row, int v0, int v1, int until, Shar
         if (lane == 31) sh.warp_tot[warp] = incl;
         __syncthreads();
         int at = have + incl - mine, total = have;
-        for (int w = 0; w < LP_THREADS / 32; ++w) {
+        for (int w = 0; w < LP_WARPS; ++w) {
             if (w < warp) at += sh.warp_tot[w];
             total += sh.warp_tot[w];
         }
@@ -180,12 +215,12 @@ __device__ void rank_stretch(const Row<T>& row, int v0, int v1, int top, float m
         if (above == top - 1) sh.bound = m;
     }
     __syncthreads();
-    const float bound = sh.bound;
+    const float bound = sh.bound > LP_LOW ? sh.bound : -INFINITY;
     // threads that hold a candidate
     if (my_max >= bound) sh.active[atomicAdd(&sh.n_active, 1)] = tid;
     __syncthreads();
     const int n_active = sh.n_active;
-    for (int a = warp; a < n_active; a += LP_THREADS / 32) {
+    for (int a = warp; a < n_active; a += LP_WARPS) {
         const int t = sh.active[a];
         for (int j = v0 + t + lane * LP_THREADS; j < v1; j += 32 * LP_THREADS) {
             float x[VE];
@@ -229,7 +264,7 @@ __device__ void rank_stretch(const Row<T>& row, int v0, int v1, int top, float m
                 __syncthreads();
                 if (lane == 0) sh.cand[warp] = best;
                 __syncthreads();
-                for (int w = 0; w < LP_THREADS / 32; ++w) best = sh.cand[w] > best ? sh.cand[w] : best;
+                for (int w = 0; w < LP_WARPS; ++w) best = sh.cand[w] > best ? sh.cand[w] : best;
                 if (tid == 0) sh.list[r] = best;
                 last = best;
             }
@@ -255,27 +290,36 @@ __device__ void rank_stretch(const Row<T>& row, int v0, int v1, int top, float m
     __syncthreads();
 }
 
-// The threads' sums joined in order, for every thread.  Two barriers.
-__device__ __forceinline__ Sums block_join(Sums t, Shared& sh) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const Sums y = {__shfl_xor_sync(0xffffffffu, t.r, o), __shfl_xor_sync(0xffffffffu, t.z, o),
-                        __shfl_xor_sync(0xffffffffu, t.s, o)};
-        t = (threadIdx.x & o) ? join(y, t) : join(t, y);
+// The sums of `lanes` neighbouring lanes (a power of two) under their largest reference, for all of them.
+__device__ __forceinline__ Sums lanes_join(Sums t, int lanes) {
+    float r = t.r;
+    for (int o = 1; o < lanes; o <<= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, o));
+    if (r > -INFINITY) {
+        const float d = t.r - r, f = ex2f(d);
+        t.s = f * (t.s + t.z * fmaxf(d, FAR));
+        t.z *= f;
     }
+    for (int o = 1; o < lanes; o <<= 1) {
+        t.z += __shfl_xor_sync(0xffffffffu, t.z, o);
+        t.s += __shfl_xor_sync(0xffffffffu, t.s, o);
+    }
+    t.r = r;
+    return t;
+}
+// The threads' sums joined, the same way every time, for every thread.  Two barriers.
+__device__ __forceinline__ Sums block_join(Sums t, Shared& sh) {
+    t = lanes_join(t, 32);
     __syncthreads();
     if (threadIdx.x % 32 == 0) sh.sums[threadIdx.x / 32] = t;
     __syncthreads();
-    t = sh.sums[0];
-    for (int w = 1; w < LP_THREADS / 32; ++w) t = join(t, sh.sums[w]);
-    return t;
+    return lanes_join(sh.sums[threadIdx.x % LP_WARPS], LP_WARPS);
 }
 __device__ __forceinline__ float block_max(float m, Shared& sh) {
     return block_join({m, 0.f, 0.f}, sh).r;
 }
 
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(LP_THREADS) k_logprobs(const Logprobs a, int cluster, float c) {
+__global__ void __launch_bounds__(LP_THREADS, LP_CTAS) k_logprobs(const Logprobs a, int cluster, float c) {
     constexpr int VE = Row<T>::VE, U = 4;
     __shared__ Shared sh;
     const int tid = threadIdx.x;
@@ -285,42 +329,56 @@ __global__ void __launch_bounds__(LP_THREADS) k_logprobs(const Logprobs a, int c
     const Row<T> row(logits, a.vocab);
     const int v0 = (int)((long long)row.n_vec * rank / cluster), v1 = (int)((long long)row.n_vec * (rank + 1) / cluster);
 
-    float ref = -INFINITY, z = 0.f, s = 0.f, top_x = -INFINITY;
-    auto step = [&](const float (&x)[VE]) {
-        float m = x[0];
-#pragma unroll
-        for (int i = 1; i < VE; ++i) m = fmaxf(m, x[i]);
+    // (asked for now, used at the end)
+    int my_id = -1;
+    float my_x = 0.f;
+    if (rank == 0 && tid < a.n_ids) {
+        my_id = __ldg(a.ids + r * a.n_ids + tid);
+        if (my_id >= 0 && my_id < a.vocab) my_x = to_f<T>(logits[my_id]);
+    }
+    float ref = -INFINITY, top_x = -INFINITY;
+    float2 z2 = make_float2(0.f, 0.f), s2 = z2;
+    const float2 c2 = make_float2(c, c);
+    auto step = [&](const uint4& raw) {
+        float2 x[VE / 2];
+        const float m = pairs_of(raw, x, T());
         if (TOP) top_x = fmaxf(top_x, m);
         const float t_max = m * c;
         if (t_max > fmaxf(ref + LP_RAISE, -LP_HUGE)) {
             if (ref > -INFINITY) {
-                const float d = ref - t_max, f = ex2f(d);
-                s = f * (s + z * fmaxf(d, FAR));
-                z *= f;
+                const float d = ref - t_max, f = ex2f(d), df = fmaxf(d, FAR);
+                s2 = make_float2(f * (s2.x + z2.x * df), f * (s2.y + z2.y * df));
+                z2 = make_float2(f * z2.x, f * z2.y);
             }
             ref = t_max;
         }
         const float neg = ref == -INFINITY ? 0.f : -ref;
+        const float2 neg2 = make_float2(neg, neg);
 #pragma unroll
-        for (int i = 0; i < VE; ++i) {
-            const float t = fmaf(x[i], c, neg), e = ex2f(t);
-            z += e;
-            s = fmaf(e, fmaxf(t, FAR), s);
+        for (int i = 0; i < VE / 2; ++i) {
+            const float2 t = __ffma2_rn(x[i], c2, neg2), e = make_float2(ex2f(t.x), ex2f(t.y));
+            z2 = __fadd2_rn(z2, e);
+            s2 = __ffma2_rn(e, t, s2);
         }
     };
     int j = v0 + tid;
     for (; j + (U - 1) * LP_THREADS < v1; j += U * LP_THREADS) {
-        float x[U][VE];
+        uint4 x[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) row.load(j + u * LP_THREADS, x[u]);
+        for (int u = 0; u < U; ++u) x[u] = row.raw(j + u * LP_THREADS);
 #pragma unroll
         for (int u = 0; u < U; ++u) step(x[u]);
     }
-    for (; j < v1; j += LP_THREADS) {
-        float x[VE];
-        row.load(j, x);
-        step(x);
+    {
+        uint4 x[U - 1];
+#pragma unroll
+        for (int u = 0; u < U - 1; ++u)
+            if (j + u * LP_THREADS < v1) x[u] = row.raw(j + u * LP_THREADS);
+#pragma unroll
+        for (int u = 0; u < U - 1; ++u)
+            if (j + u * LP_THREADS < v1) step(x[u]);
     }
+    float z = z2.x + z2.y, s = s2.x + s2.y;
     Sums t = block_join({ref, z, s}, sh);
     if (TOP) rank_stretch(row, v0, v1, a.top, top_x, sh);
     if (tid == 0) sh.total = t;
@@ -399,13 +457,13 @@ __global__ void __launch_bounds__(LP_THREADS) k_logprobs(const Logprobs a, int c
     };
     if (tid == 0 && a.entropy) a.entropy[r] = none ? 0.f : LN2 * (lz - t.s / t.z);
     for (int i = tid; i < a.n_ids; i += LP_THREADS) {
-        const int id = __ldg(a.ids + r * a.n_ids + i);
+        const int id = i == tid ? my_id : __ldg(a.ids + r * a.n_ids + i);
         float lp = 0.f;
         if (id >= a.vocab) {
             set_error(a.err, BLEND_EDEVICE);
             lp = __int_as_float(0x7fc00000);
         } else if (id >= 0)
-            lp = logp_of(to_f<T>(logits[id]));
+            lp = logp_of(i == tid ? my_x : to_f<T>(logits[id]));
         a.logp[r * a.n_ids + i] = lp;
     }
     if (TOP && tid < a.top) {
@@ -416,9 +474,9 @@ __global__ void __launch_bounds__(LP_THREADS) k_logprobs(const Logprobs a, int c
 }
 
 template <typename T, bool TOP> int launch(const Logprobs& a, cudaStream_t s) {
-    // A row's CTAs: as many as keep 152 SMs of two CTAs busy, each with 4096 logits at least.
+    // A row's CTAs: as many as keep 152 SMs busy, each with 2048 logits at least.
     int cluster = 1;
-    while (cluster < LP_MAX_CLUSTER && (long long)a.rows * cluster * 2 <= 304 && a.vocab / (cluster * 2) >= 4096) cluster *= 2;
+    while (cluster < LP_MAX_CLUSTER && (long long)a.rows * cluster * 2 <= 152 * LP_CTAS && a.vocab / (cluster * 2) >= 2048) cluster *= 2;
     auto* kern = k_logprobs<T, TOP>;
     if (cluster > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return BLEND_ECUDA;
