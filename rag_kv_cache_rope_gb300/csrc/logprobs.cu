@@ -124,19 +124,6 @@ __device__ __forceinline__ float pairs_of(const uint4& raw, float2 (&x)[2], floa
     x[1] = make_float2(max_keep_nan(__uint_as_float(raw.z), LP_LOW), max_keep_nan(__uint_as_float(raw.w), LP_LOW));
     return fmaxf(fmaxf(x[0].x, x[0].y), fmaxf(x[1].x, x[1].y));
 }
-// Two partial sums under the larger reference.  A part without a finite term has z = 0 and r = -infinity.
-__device__ __forceinline__ Sums join(Sums a, Sums b) {
-    Sums o;
-    o.r = fmaxf(a.r, b.r);
-    const float da = a.r - o.r, db = b.r - o.r;
-    if (o.r == -INFINITY) return {o.r, a.z + b.z, a.s + b.s};
-    // (a part whose reference is -infinity holds no term: 0, or NaN; 2^FAR is 0 already)
-    const float fa = ex2f(da), fb = ex2f(db);
-    o.z = a.z * fa + b.z * fb;
-    o.s = fa * (a.s + a.z * fmaxf(da, FAR)) + fb * (b.s + b.z * fmaxf(db, FAR));
-    return o;
-}
-
 struct Shared {
     key_t cand[LP_CAND];
     key_t list[BLEND_MAX_TOP];       // this stretch's ranking
@@ -220,9 +207,10 @@ __device__ void rank_stretch(const Row<T>& row, int v0, int v1, int top, float m
     if (my_max >= bound) sh.active[atomicAdd(&sh.n_active, 1)] = tid;
     __syncthreads();
     const int n_active = sh.n_active;
-    for (int a = warp; a < n_active; a += LP_WARPS) {
-        const int t = sh.active[a];
-        for (int j = v0 + t + lane * LP_THREADS; j < v1; j += 32 * LP_THREADS) {
+    const int each = (v1 - v0 + LP_THREADS - 1) / LP_THREADS;  // vectors of a thread
+    for (int i = tid; i < n_active * each; i += LP_THREADS) {
+        const int j = v0 + sh.active[i / each] + i % each * LP_THREADS;
+        if (j < v1) {
             float x[VE];
             row.load(j, x);
 #pragma unroll
@@ -386,33 +374,46 @@ __global__ void __launch_bounds__(LP_THREADS, LP_CTAS) k_logprobs(const Logprobs
     if (cluster > 1) {
         cg::cluster_group cl = cg::this_cluster();
         cl.sync();
+        // sums and lists of all to the first
+        const int keys = cluster * a.top;
         if (rank == 0) {
-            if (tid == 0) {
-                for (int q = 1; q < cluster; ++q) t = join(t, cl.map_shared_rank(&sh, q)->total);
-                sh.total = t;
+            if (tid < 32) {
+                t = tid < cluster ? cl.map_shared_rank(&sh, tid)->total : Sums{-INFINITY, 0.f, 0.f};
+                t = lanes_join(t, 32);
+                if (tid == 0) sh.total = t;
             }
-            if (TOP) {
-                for (int i = tid; i < cluster * BLEND_MAX_TOP; i += LP_THREADS)
-                    sh.all[i / BLEND_MAX_TOP][i % BLEND_MAX_TOP] = cl.map_shared_rank(&sh, i / BLEND_MAX_TOP)->list[i % BLEND_MAX_TOP];
-                __syncthreads();
-                for (int i = tid; i < cluster * BLEND_MAX_TOP; i += LP_THREADS) {
-                    const int q = i / BLEND_MAX_TOP;
-                    const key_t k = sh.all[q][i % BLEND_MAX_TOP];
-                    int above = i % BLEND_MAX_TOP;
-                    for (int o = 0; o < cluster; ++o) {
-                        if (o == q) continue;
-                        int lo = 0;  // keys of list o above k: lists descend
-#pragma unroll
-                        for (int w = BLEND_MAX_TOP / 2; w > 0; w >>= 1)
-                            if (sh.all[o][lo + w - 1] > k) lo += w;
-                        above += lo + (sh.all[o][lo] > k);
-                    }
-                    if (k != 0 && above < a.top) sh.merged[above] = k;
-                }
-            }
+            if (TOP)
+                for (int i = tid; i < keys; i += LP_THREADS)
+                    sh.all[i / a.top][i % a.top] = cl.map_shared_rank(&sh, i / a.top)->list[i % a.top];
         }
         cl.sync();
         if (rank != 0) return;
+        if (TOP) {
+            // The m-th largest of the lists' p-th keys, m p >= top: that many keys at least reach it, and few more.
+            const int p = (a.top + cluster - 1) / cluster, m = (a.top + p - 1) / p;
+            if (tid == 0) sh.n_cand = 0;
+            if (tid < cluster) {
+                const key_t k = sh.all[tid][p - 1];
+                int above = 0;
+                for (int q = 0; q < cluster; ++q) above += sh.all[q][p - 1] > k || (sh.all[q][p - 1] == k && q < tid);
+                if (above == m - 1) sh.merged[0] = k;
+            }
+            __syncthreads();
+            const key_t least = sh.merged[0];
+            for (int i = tid; i < keys; i += LP_THREADS) {
+                const key_t k = sh.all[i / a.top][i % a.top];
+                if (k >= least && k != 0) sh.cand[atomicAdd(&sh.n_cand, 1)] = k;
+            }
+            __syncthreads();
+            const int n = sh.n_cand;
+            for (int c = tid; c < n; c += LP_THREADS) {
+                const key_t k = sh.cand[c];
+                int above = 0;
+                for (int i = 0; i < n; ++i) above += sh.cand[i] > k;
+                if (above < a.top) sh.merged[above] = k;
+            }
+            __syncthreads();
+        }
         list = sh.merged;
     } else
         __syncthreads();
