@@ -82,14 +82,17 @@ template <typename T> struct Row {
             for (int i = 0; i < VE; ++i) x[i] = e0 + i >= 0 && e0 + i < vocab ? to_f<T>(p[e0 + i]) : -INFINITY;
         }
     }
+    // The same as it lies in memory.
     __device__ __forceinline__ uint4 raw(int j) const {
-        const int e0 = j * VE - off;
-        if (e0 >= 0 && e0 + VE <= vocab) return *reinterpret_cast<const uint4*>(p + e0);
         Vec<T> v;
+        float x[VE];
+        load(j, x);
 #pragma unroll
-        for (int i = 0; i < VE; ++i) v.set(i, e0 + i >= 0 && e0 + i < vocab ? to_f<T>(p[e0 + i]) : -INFINITY);
+        for (int i = 0; i < VE; ++i) v.set(i, x[i]);
         return v.raw;
     }
+    // A vector that is neither the first nor the last.
+    __device__ __forceinline__ uint4 inner(int j) const { return reinterpret_cast<const uint4*>(p - off)[j]; }
     __device__ __forceinline__ bool holds(int j, int i) const {  // element i of vector j is in the row
         const int e = j * VE - off + i;
         return e >= 0 && e < vocab;
@@ -191,15 +194,19 @@ __device__ void rank_stretch(const Row<T>& row, int v0, int v1, int top, float m
     if (tid < BLEND_MAX_TOP) sh.list[tid] = 0;
     if (tid == 0) sh.n_active = sh.n_cand = sh.overflow = 0;
     __syncthreads();
-    if (tid < LP_GROUPS) {
-        const float m = sh.group_max[tid];
+    {
+        // (PER_GROUP threads compare a group's maximum with a part of the others)
+        const int mine = tid / PER_GROUP, part = tid % PER_GROUP;
+        const float m = sh.group_max[mine];
         int above = 0;
-#pragma unroll 8
-        for (int i = 0; i < LP_GROUPS; ++i) {
+#pragma unroll
+        for (int i = part; i < LP_GROUPS; i += PER_GROUP) {
             const float y = sh.group_max[i];
-            above += y > m || (y == m && i < tid);
+            above += y > m || (y == m && i < mine);
         }
-        if (above == top - 1) sh.bound = m;
+#pragma unroll
+        for (int o = 1; o < PER_GROUP; o <<= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+        if (part == 0 && above == top - 1) sh.bound = m;
     }
     __syncthreads();
     const float bound = sh.bound > LP_LOW ? sh.bound : -INFINITY;
@@ -207,17 +214,25 @@ __device__ void rank_stretch(const Row<T>& row, int v0, int v1, int top, float m
     if (my_max >= bound) sh.active[atomicAdd(&sh.n_active, 1)] = tid;
     __syncthreads();
     const int n_active = sh.n_active;
-    const int each = (v1 - v0 + LP_THREADS - 1) / LP_THREADS;  // vectors of a thread
-    for (int i = tid; i < n_active * each; i += LP_THREADS) {
-        const int j = v0 + sh.active[i / each] + i % each * LP_THREADS;
-        if (j < v1) {
+    const int w0 = max(v0, 1), w1 = min(v1, row.n_vec - 1);
+    const int each = (max(w1 - w0, 0) + LP_THREADS - 1) / LP_THREADS;  // inner vectors of a thread
+    // (the row's first and last vectors besides)
+    for (int i = tid; i < n_active * each + 2; i += LP_THREADS) {
+        const int k = i - 2;
+        int j = i == 0 ? 0 : row.n_vec - 1;
+        bool mine = i == 0 ? v0 == 0 : v1 == row.n_vec && row.n_vec > 1;
+        if (k >= 0) {
+            j = w0 + sh.active[k / each] + k % each * LP_THREADS;
+            mine = j < w1;
+        }
+        if (mine) {
             float x[VE];
             row.load(j, x);
 #pragma unroll
-            for (int i = 0; i < VE; ++i)
-                if (x[i] >= bound && row.holds(j, i)) {
+            for (int e = 0; e < VE; ++e)
+                if (x[e] >= bound && row.holds(j, e)) {
                     const int at = atomicAdd(&sh.n_cand, 1);
-                    if (at < LP_CAND) sh.cand[at] = rank_key(x[i], row.index(j, i));
+                    if (at < LP_CAND) sh.cand[at] = rank_key(x[e], row.index(j, e));
                     else sh.overflow = 1;
                 }
         }
@@ -349,11 +364,15 @@ __global__ void __launch_bounds__(LP_THREADS, LP_CTAS) k_logprobs(const Logprobs
             s2 = __ffma2_rn(e, t, s2);
         }
     };
-    int j = v0 + tid;
-    for (; j + (U - 1) * LP_THREADS < v1; j += U * LP_THREADS) {
+    // the row's first and last vectors may reach over its ends: thread 0's
+    const int w0 = max(v0, 1), w1 = min(v1, row.n_vec - 1);
+    if (tid == 0 && v0 == 0 && v1 > 0) step(row.raw(0));
+    if (tid == 0 && v1 == row.n_vec && v0 < v1 && row.n_vec > 1) step(row.raw(row.n_vec - 1));
+    int j = w0 + tid;
+    for (; j + (U - 1) * LP_THREADS < w1; j += U * LP_THREADS) {
         uint4 x[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) x[u] = row.raw(j + u * LP_THREADS);
+        for (int u = 0; u < U; ++u) x[u] = row.inner(j + u * LP_THREADS);
 #pragma unroll
         for (int u = 0; u < U; ++u) step(x[u]);
     }
@@ -361,10 +380,10 @@ __global__ void __launch_bounds__(LP_THREADS, LP_CTAS) k_logprobs(const Logprobs
         uint4 x[U - 1];
 #pragma unroll
         for (int u = 0; u < U - 1; ++u)
-            if (j + u * LP_THREADS < v1) x[u] = row.raw(j + u * LP_THREADS);
+            if (j + u * LP_THREADS < w1) x[u] = row.inner(j + u * LP_THREADS);
 #pragma unroll
         for (int u = 0; u < U - 1; ++u)
-            if (j + u * LP_THREADS < v1) step(x[u]);
+            if (j + u * LP_THREADS < w1) step(x[u]);
     }
     float z = z2.x + z2.y, s = s2.x + s2.y;
     Sums t = block_join({ref, z, s}, sh);

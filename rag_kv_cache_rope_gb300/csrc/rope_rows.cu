@@ -69,7 +69,7 @@ __device__ __forceinline__ Slot find_slot(const RopeArgs& a, int slot, int slots
 // heads_in: slots that a row's threads work on side by side (a power of two); each thread takes every
 // heads_in-th slot.
 template <typename T, bool PAIRS>
-__global__ void __launch_bounds__(ROPE_THREADS)
+__global__ void __launch_bounds__(ROPE_THREADS, 4)
     k_rope_rows(const __grid_constant__ RopeArgs a, int units_log2, int heads_in_log2, int slots, int slots0) {
     const long long t = (long long)blockIdx.x * ROPE_THREADS + threadIdx.x;
     const int unit = (int)t & ((1 << units_log2) - 1);
@@ -100,20 +100,40 @@ __global__ void __launch_bounds__(ROPE_THREADS)
             cs[i].y *= a.magnitude;
         }
     }
-    for (int slot = first; slot < slots; slot += 1 << heads_in_log2) {
+    if (!turned && a.part[0].src == a.part[0].dst && (a.n_parts == 1 || a.part[1].src == a.part[1].dst)) return;
+    // U slots' loads are on their way together
+    constexpr int U = 2;
+    const int step = 1 << heads_in_log2;
+    auto turn = [&](Unit16<T>& x) {
+        if (!turned) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j1 = PAIRS ? 2 * i : i, j2 = PAIRS ? 2 * i + 1 : i + 8;
+            const float x1 = x.get(j1), x2 = x.get(j2);
+            x.set(j1, x1 * cs[i].x - x2 * cs[i].y);
+            x.set(j2, x2 * cs[i].x + x1 * cs[i].y);
+        }
+    };
+    int slot = first;
+    for (; slot + (U - 1) * step < slots; slot += U * step) {
+        Unit16<T> x[U];
+        Slot s[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            s[u] = find_slot<T>(a, slot + u * step, slots0, row);
+            x[u].load((const T*)s[u].src + ia, (const T*)s[u].src + ib);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            turn(x[u]);
+            x[u].store((T*)s[u].dst + ia, (T*)s[u].dst + ib);
+        }
+    }
+    for (; slot < slots; slot += step) {
         const Slot s = find_slot<T>(a, slot, slots0, row);
-        if (!turned && s.src == s.dst) continue;
         Unit16<T> x;
         x.load((const T*)s.src + ia, (const T*)s.src + ib);
-        if (turned) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int j1 = PAIRS ? 2 * i : i, j2 = PAIRS ? 2 * i + 1 : i + 8;
-                const float x1 = x.get(j1), x2 = x.get(j2);
-                x.set(j1, x1 * cs[i].x - x2 * cs[i].y);
-                x.set(j2, x2 * cs[i].x + x1 * cs[i].y);
-            }
-        }
+        turn(x);
         x.store((T*)s.dst + ia, (T*)s.dst + ib);
     }
 }

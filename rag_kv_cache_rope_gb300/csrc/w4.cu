@@ -17,80 +17,153 @@ namespace blend {
 namespace {
 
 // ---------------------------------------------------------------- pack, unpack
-constexpr int PACK_THREADS = 256;
-
-// Eight values as a 32-bit word of codes, see the layout.
-__device__ __forceinline__ uint32_t code_word(const float* x, float s) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float n = 0.f;
-        if (s > 0.f) {
-            const float q = __fdiv_rn(x[e], s);
-            n = rintf(q);
-            // an fp32 quotient half way between integers may stand for one beside it: the remainder tells
-            if (fabsf(q - n) == 0.5f) {
-                const float r = fmaf(-q, s, x[e]);
-                if (r != 0.f) n = r > 0.f ? ceilf(q) : floorf(q);
-            }
-            n = fminf(fmaxf(n, -7.f), 7.f);
-        }
-        w |= (uint32_t)(8 + (int)n) << (4 * (e >> 1) + 16 * (e & 1));
+// A warp takes a stretch of one row, a lane eight inputs (one word of codes) of it at a time, PACK_U times 32
+// words together: loads and stores are whole lines, and nothing is divided to find a place.
+constexpr int PACK_THREADS = 256, PACK_U = 4;
+struct PackPlace {
+    int row, w0, w1;  // words w0 .. w1 - 1 of the row, in input order
+    __device__ __forceinline__ PackPlace(const W4View& w) {
+        row = blockIdx.x * (PACK_THREADS / 32) + (threadIdx.x >> 5);
+        const int runs = (w.chunks * 16 + 32 * PACK_U - 1) / (32 * PACK_U);  // of 32 PACK_U words
+        w0 = runs * blockIdx.y / gridDim.y * (32 * PACK_U);
+        w1 = min((int)(runs * (blockIdx.y + 1) / gridDim.y) * (32 * PACK_U), w.chunks * 16);
     }
-    return w;
+};
+
+// Codes 8 + n of eight values as a 32-bit word, see the layout.
+//
+// n is the exact quotient rounded to an integer.  With y = 1 / s correctly rounded, q = x y, r = x - q s (exact) and
+// q + r y is x / s correctly rounded (Markstein's theorem, P. Markstein, IBM J. Res. Dev. 34, 1990) as long as
+// nothing leaves the normal range; scales outside 2^-100..2^100 divide.  That fp32 quotient may lie half way
+// between two integers where the exact one only lies beside it (not with bf16 inputs, whose quotients by a bf16 keep
+// further away): then the remainder tells the side.
+template <typename T> __device__ __forceinline__ uint32_t code_word(const float* x, float s) {
+    uint32_t c[8];
+    if (s >= 0x1p-100f && s <= 0x1p100f) {
+        const float y = __frcp_rn(s);
+        const float2 y2 = make_float2(y, y), ns2 = make_float2(-s, -s), up2 = make_float2(12582920.f, 12582920.f);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            const float2 x2 = make_float2(x[e], x[e + 1]), q = __fmul2_rn(x2, y2);
+            float2 d = __ffma2_rn(__ffma2_rn(q, ns2, x2), y2, q);
+            if constexpr (sizeof(T) == 4) {
+                // half way: a step of the quotient towards the exact one (|n| + 1/2 stays below 2^24)
+                const float2 r = __ffma2_rn(d, ns2, x2);
+                if (fabsf(d.x - rintf(d.x)) == 0.5f && r.x != 0.f) d.x = nextafterf(d.x, r.x > 0.f ? 100.f : -100.f);
+                if (fabsf(d.y - rintf(d.y)) == 0.5f && r.y != 0.f) d.y = nextafterf(d.y, r.y > 0.f ? 100.f : -100.f);
+            }
+            // |x| / s stays below 7.5, so the code is in range without a clamp; adding 1.5 2^23 rounds to an
+            // integer, ties to even (and the 8 keeps its parity)
+            const float2 n = __fadd2_rn(d, up2);
+            c[e] = __float_as_uint(n.x);
+            c[e + 1] = __float_as_uint(n.y);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float n = 0.f;
+            if (s > 0.f) {
+                const float q = __fdiv_rn(x[e], s), r = fmaf(-q, s, x[e]);
+                n = rintf(q);
+                if (fabsf(q - n) == 0.5f && r != 0.f) n = r > 0.f ? ceilf(q) : floorf(q);
+                n = fminf(fmaxf(n, -7.f), 7.f);
+            }
+            c[e] = (uint32_t)(8 + (int)n);
+        }
+    }
+    // inputs 0, 2, 4, 6 to the low half, 1, 3, 5, 7 to the high one (what a code carries from bit 22 up stays above)
+    const uint32_t lo = c[0] + c[2] * 16u + c[4] * 256u + c[6] * 4096u, hi = c[1] + c[3] * 16u + c[5] * 256u + c[7] * 4096u;
+    return __byte_perm(lo, hi, 0x5410);
 }
 
-// One thread packs eight inputs, i.e. one word; 4, 8 or 16 neighbouring threads share a group.
 template <typename T>
 __global__ void __launch_bounds__(PACK_THREADS)
     k_w4_pack(W4View w, const T* __restrict__ src, long long ld) {
-    const long long t = (long long)blockIdx.x * PACK_THREADS + threadIdx.x;
-    const long long row = t / (16 * w.chunks);
-    const int at = (int)(t % (16 * w.chunks));  // word of the row, in input order
-    const bool in = row < w.n;
-    float x[8];
+    const PackPlace at(w);
+    if (at.row >= w.n) return;
+    constexpr int NV = 8 / Vec<T>::N;
+    const int lane = threadIdx.x & 31;
+    const T* in = src + at.row * ld;
+    uint32_t* codes = (uint32_t*)w.codes + (long long)at.row * w.chunks * 16;
+    bf16* scale = (bf16*)w.scale + (long long)at.row * w.chunks * (128 / w.group);
+    const int k8 = w.k / 8, lanes = w.group / 8, log2_lanes = lanes == 4 ? 2 : lanes == 8 ? 3 : 4;
+    for (int w0 = at.w0; w0 < at.w1; w0 += 32 * PACK_U) {
+        Vec<T> v[PACK_U][NV];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    if (in && at * 8 < w.k) {
+        for (int u = 0; u < PACK_U; ++u) {
+            const int i = w0 + u * 32 + lane;
 #pragma unroll
-        for (int v = 0; v < 8 / Vec<T>::N; ++v) {
-            const Vec<T> r = ld16(src + row * ld + at * 8 + v * Vec<T>::N);
+            for (int n = 0; n < NV; ++n) v[u][n].raw = i < k8 ? *(const uint4*)(in + i * 8 + n * Vec<T>::N) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
-            for (int i = 0; i < Vec<T>::N; ++i) x[v * Vec<T>::N + i] = r.get(i);
+        for (int u = 0; u < PACK_U; ++u) {
+            const int i = w0 + u * 32 + lane;
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = v[u][e / Vec<T>::N].get(e % Vec<T>::N);
+            float m = fabsf(x[0]);
+#pragma unroll
+            for (int e = 1; e < 8; ++e) m = max_nan(m, fabsf(x[e]));
+            m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            if (lanes > 4) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 4));
+            if (lanes > 8) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 8));
+            // (the fp32 quotient by 7 is never half way between two bf16 unless the exact one is)
+            const bf16 sb = __float2bfloat16_rn(isfinite(m) ? __fdiv_rn(m, 7.f) : __int_as_float(0x7fc00000));
+            const uint32_t word = code_word<T>(x, __bfloat162float(sb));
+            if (i >= at.w1) continue;
+            // word 4 part + k32 of its chunk
+            codes[(i & ~15) | (i & 3) << 2 | (i >> 2 & 3)] = word;
+            if ((i & (lanes - 1)) == 0) scale[i >> log2_lanes] = sb;
         }
     }
-    float m = fabsf(x[0]);
-#pragma unroll
-    for (int e = 1; e < 8; ++e) m = max_nan(m, fabsf(x[e]));
-    for (int o = 1; o < w.group / 8; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-    // (the fp32 quotient by 7 is never half way between two bf16 unless the exact one is)
-    const bf16 sb = __float2bfloat16_rn(isfinite(m) ? __fdiv_rn(m, 7.f) : __int_as_float(0x7fc00000));
-    const uint32_t word = code_word(x, __bfloat162float(sb));
-    if (!in) return;
-    const int c = at >> 4, k32 = (at >> 2) & 3, part = at & 3;
-    ((uint32_t*)w.codes)[(row * w.chunks + c) * 16 + 4 * part + k32] = word;
-    if (at * 8 % w.group == 0) ((bf16*)w.scale)[row * w.chunks * (128 / w.group) + at * 8 / w.group] = sb;
 }
 
+// A lane reads sixteen bytes (four words, inputs 32 apart) and writes eight values of each.
+__device__ __forceinline__ void put_values(bf16* p, uint32_t word, bf16 s) {
+    const __nv_bfloat162 s2 = __halves2bfloat162(s, s);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t n = code_ints(word >> (4 * i));
+        const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&n), s2);  // exact, rounded once
+        o[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ void put_values(float* p, uint32_t word, bf16 sb) {
+    const float s = __bfloat162float(sb);
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t n = code_ints(word >> (4 * i));
+        o[2 * i] = __fmul_rn(__uint_as_float(n << 16), s);
+        o[2 * i + 1] = __fmul_rn(__uint_as_float(n & 0xffff0000u), s);
+    }
+    *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(o[4], o[5], o[6], o[7]);
+}
 template <typename T>
 __global__ void __launch_bounds__(PACK_THREADS)
     k_w4_unpack(W4View w, T* __restrict__ out, long long ld) {
-    const long long t = (long long)blockIdx.x * PACK_THREADS + threadIdx.x;
-    const long long row = t / (16 * w.chunks);
-    const int at = (int)(t % (16 * w.chunks));
-    if (row >= w.n || at * 8 >= w.k) return;
-    const int c = at >> 4, k32 = (at >> 2) & 3, part = at & 3;
-    const uint32_t word = __ldg((const uint32_t*)w.codes + (row * w.chunks + c) * 16 + 4 * part + k32);
-    const float s = __bfloat162float(w.scale[row * w.chunks * (128 / w.group) + at * 8 / w.group]);
-    float x[8];
+    const PackPlace at(w);
+    if (at.row >= w.n) return;
+    const int lane = threadIdx.x & 31, spc = 128 / w.group, log2_spc = spc == 4 ? 2 : spc == 2 ? 1 : 0;
+    T* dst = out + at.row * ld;
+    const uint4* codes = w.codes + (long long)at.row * w.chunks * 4;
+    const bf16* scale = w.scale + (long long)at.row * w.chunks * spc;
+    for (int q0 = at.w0 / 4; q0 < at.w1 / 4; q0 += 32) {
+        const int q = q0 + lane;  // piece of the row: part q % 4 of chunk q / 4
+        if (q >= at.w1 / 4) continue;
+        const uint4 v = __ldg(codes + q);
+        bf16 s[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = __fmul_rn((float)(int)((word >> (4 * (e >> 1) + 16 * (e & 1))) & 15u) - 8.f, s);
+        for (int k32 = 0; k32 < 4; ++k32) s[k32] = scale[(q >> 2 << log2_spc) + (k32 * spc >> 2)];
 #pragma unroll
-    for (int v = 0; v < 8 / Vec<T>::N; ++v) {
-        Vec<T> r;
-#pragma unroll
-        for (int i = 0; i < Vec<T>::N; ++i) r.set(i, x[v * Vec<T>::N + i]);
-        st16(out + row * ld + at * 8 + v * Vec<T>::N, r);
+        for (int k32 = 0; k32 < 4; ++k32) {
+            const int i = (q >> 2) * 128 + k32 * 32 + (q & 3) * 8;
+            if (i < w.k) put_values(dst + i, word_of(v, k32), s[k32]);
+        }
     }
 }
 
@@ -353,8 +426,12 @@ template <typename T, int NT> int go_group(const W4Linear& a, cudaStream_t s) {
     return a.w.group == 32 ? go<T, NT, 32>(a, s) : a.w.group == 64 ? go<T, NT, 64>(a, s) : go<T, NT, 128>(a, s);
 }
 
-unsigned pack_grid(const W4View& w) {
-    return (unsigned)(((long long)w.n * w.chunks * 16 + PACK_THREADS - 1) / PACK_THREADS);
+// Rows, and parts of a row where they are few: warps for 152 SMs of 32.
+dim3 pack_grid(const W4View& w) {
+    const int blocks = (w.n + PACK_THREADS / 32 - 1) / (PACK_THREADS / 32), runs = (w.chunks * 16 + 32 * PACK_U - 1) / (32 * PACK_U);
+    int parts = (152 * 4 + blocks - 1) / blocks;
+    parts = parts < runs ? parts : runs;
+    return dim3((unsigned)blocks, (unsigned)parts);
 }
 
 }  // namespace
