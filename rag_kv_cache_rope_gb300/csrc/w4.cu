@@ -7,11 +7,7 @@
 // paged.cuh: (code - 8) / 64, exact in bf16; the 64 goes into the sum's end).  The products of a group
 // are summed in fp32 by the matrix unit, and one multiply-add per result and group applies the scale: neither
 // codes nor scales are rounded.  fp32 inputs enter as three bf16 parts, which hold all 24 bits.
-#include <cooperative_groups.h>
-
 #include "w4.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace blend {
 namespace {
@@ -168,10 +164,12 @@ __global__ void __launch_bounds__(PACK_THREADS)
 }
 
 // ---------------------------------------------------------------- products
-constexpr int LIN_WARPS = 8, LIN_THREADS = 32 * LIN_WARPS;
-constexpr int LIN_RING = 4;         // chunks on their way per warp
-constexpr int LIN_TILE_ROWS = 16;   // more rows of inputs go to the tcgen05 kernel
+constexpr int LIN_WARPS = 16, LIN_THREADS = 32 * LIN_WARPS;
+constexpr int LIN_ROWS = 8;         // input rows of a launch block; more of them go to the tcgen05 kernel
+constexpr int LIN_RING = 4;         // chunks of 32 weight rows on their way per warp, at most
+constexpr int LIN_STAGE = 32 * 64;  // bytes of one
 constexpr int LIN_MAX_CLUSTER = 8;  // CTAs that share a weight row's inputs
+constexpr int LIN_SUMS = 32 * LIN_ROWS;  // results of a unit
 
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -179,234 +177,353 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The first product of a group: added to nothing.
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // Where a CTA's share of the inputs lies and how its rows are laid out in shared memory: rows of whole
 // chunks and 64 bytes more, so that the two rows of a quarter warp's 16-byte reads use different banks.
 __host__ __device__ __forceinline__ int lin_row_bytes(int chunks) { return chunks * 256 + 64; }
-
-template <typename T, int NT, int G>
-__global__ void __launch_bounds__(LIN_THREADS, 2)
-    k_w4_linear(const W4Linear a, int cluster, int row_cap) {
+// A unit is 32 weight rows (two tiles of matrix instructions, for SWIGLU the gate and the up rows of 16 outputs)
+// by all input rows.  The warps of a CTA, or each half of them, take a unit's chunks in turn and join their sums at
+// its end: two halves work on a unit each where there are enough units, and share the inputs in shared memory.
+template <typename T, int G>
+__global__ void __launch_bounds__(LIN_THREADS, 1)
+    k_w4_linear(const __grid_constant__ CUtensorMap m_codes, const W4Linear a, int cluster, int row_cap, int depth, int halves) {
     constexpr int P = sizeof(T) == 4 ? 3 : 1;  // bf16 parts of an input
-    constexpr int COLS = 8 * NT, SPC = 128 / G;
-    extern __shared__ __align__(128) char smem[];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-    const int rank = cluster > 1 ? (int)cg::this_cluster().block_rank() : 0;
-    const int unit0 = blockIdx.x / cluster, units_step = gridDim.x / cluster;
-    const int row0 = blockIdx.y * COLS, rows = min(COLS, a.rows - row0);
-    const int c0 = (int)((long long)a.w.chunks * rank / cluster), c1 = (int)((long long)a.w.chunks * (rank + 1) / cluster);
-    const int row_bytes = lin_row_bytes((a.w.chunks + cluster - 1) / cluster);
+    constexpr int SPC = 128 / G, SUMS = LIN_SUMS;
+    extern __shared__ __align__(1024) char smem[];
+    // full: a chunk of codes has come; p: the sums of a unit of the cluster's CTAs are there, have been read
+    __shared__ uint64_t full[LIN_WARPS][LIN_RING], p_full[2][2], p_free[2][2];
+    __shared__ int abort_sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), g = lane >> 2, t4 = lane & 3;
+    const int rank = blockIdx.x % cluster;
+    const int per_half = LIN_WARPS / halves, half = warp / per_half, warp_in = warp - half * per_half;
+    const int unit0 = blockIdx.x / cluster * halves + half, units_step = gridDim.x / cluster * halves;
+    const int row0 = blockIdx.y * row_cap, rows = min(row_cap, a.rows - row0);
+    const int chunks = a.w.chunks;
+    const int c0 = chunks * rank / cluster, c1 = chunks * (rank + 1) / cluster;
+    const int row_bytes = lin_row_bytes((chunks + cluster - 1) / cluster);
     const int plane = row_cap * row_bytes;
-    float* red = (float*)(smem + P * plane);              // [2][LIN_WARPS][NT][128]
-    float* part = red + 2 * LIN_WARPS * NT * 128;         // [2][NT][128]: this CTA's sums (cluster > 1)
-
-    // tiles of 16 weight rows: a gate tile, then its up tile
-    const bool glu = a.epi == BLEND_W4_SWIGLU;
-    const int tiles = (a.w.n + 15) / 16;
-    const int units = glu ? tiles / 2 : tiles;
+    // rings of codes, [2][LIN_WARPS][SUMS] sums of warps, [2 halves][2][SUMS] of this CTA (cluster > 1), inputs
+    char* ring = smem + warp * (depth * LIN_STAGE);
+    float* red = (float*)(smem + LIN_WARPS * depth * LIN_STAGE);
+    float* part = red + 2 * LIN_WARPS * SUMS;
+    char* s_x = (char*)(part + (cluster > 1 ? 4 * SUMS : 0));
+    const int units = (a.w.n + 31) / 32;
     const int my_units = unit0 < units ? (units - unit0 + units_step - 1) / units_step : 0;
-    const int my_tiles = glu ? 2 * my_units : my_units;
-    auto tile_at = [&](int i) { return glu ? 2 * (unit0 + (i >> 1) * units_step) + (i & 1) : unit0 + i * units_step; };
 
-    // this warp's chunks of a tile: c0 + warp, + LIN_WARPS, ...
-    const int per_tile = max(0, (c1 - c0 - warp + LIN_WARPS - 1) / LIN_WARPS);
-    uint4 qa[LIN_RING], qb[LIN_RING];
-    Scales<G> sa[LIN_RING], sb[LIN_RING];
-    int f_tile = 0, f_chunk = 0;  // the next chunk to ask for
+    // this warp's chunks of a unit: c0 + warp_in, + per_half, ...
+    const int per_unit = max(0, (c1 - c0 - warp_in + per_half - 1) / per_half);
+    if (lane == 0) {
+        for (int i = 0; i < depth; ++i) mbar_init(&full[warp][i], 1);
+        if (warp == 0) {
+            abort_sh = 0;
+            for (int i = 0; i < 4; ++i) {
+                mbar_init(&p_full[i >> 1][i & 1], cluster * per_half);
+                mbar_init(&p_free[i >> 1][i & 1], cluster * per_half);
+            }
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+    int f_unit = 0, f_chunk = 0, asked = 0;  // the next chunk to ask for, and how many have been
     auto fetch = [&](int slot) {
-        if (f_tile >= my_tiles) return;
-        const int tile = tile_at(f_tile), c = c0 + warp + f_chunk * LIN_WARPS;
-        const long long ra = min(tile * 16 + g, a.w.n - 1), rb = min(tile * 16 + g + 8, a.w.n - 1);
-        qa[slot] = __ldg(a.w.codes + (ra * a.w.chunks + c) * 4 + t4);
-        qb[slot] = __ldg(a.w.codes + (rb * a.w.chunks + c) * 4 + t4);
-        sa[slot].load(a.w.scale + (ra * a.w.chunks + c) * SPC);
-        sb[slot].load(a.w.scale + (rb * a.w.chunks + c) * SPC);
-        if (++f_chunk == per_tile) {
+        if (f_unit >= my_units) return;
+        if (elect_one()) {
+            mbar_expect_tx(&full[warp][slot], LIN_STAGE);
+            tma_2d(ring + slot * LIN_STAGE, &m_codes, &full[warp][slot], (c0 + warp_in + f_chunk * per_half) * 64, (unit0 + f_unit * units_step) * 32);
+        }
+        __syncwarp();
+        ++asked;
+        if (++f_chunk == per_unit) {
             f_chunk = 0;
-            ++f_tile;
+            ++f_unit;
         }
     };
-    if (per_tile > 0) {
+    if (per_unit > 0)
+        for (int i = 0; i < depth; ++i) fetch(i);
+    // The scales of the chunk after the one at hand: rows g, g + 8, g + 16, g + 24.
+    Scales<G> next[4];
+    const bf16* sp = nullptr;
+    int behind[4], n_unit = 0, n_chunk = 0;
+    auto fetch_scales = [&]() {
+        if (n_unit >= my_units) return;
+        if (n_chunk == 0) {
+            const int r0 = (unit0 + n_unit * units_step) * 32 + g, r = min(r0, a.w.n - 1);
+            sp = a.w.scale + ((long long)r * chunks + c0 + warp_in) * SPC;
 #pragma unroll
-        for (int i = 0; i < LIN_RING; ++i) fetch(i);
-    }
+            for (int i = 0; i < 4; ++i) behind[i] = (min(r0 + 8 * i, a.w.n - 1) - r) * chunks * SPC;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) next[i].load(sp + behind[i]);
+        sp += per_half * SPC;
+        if (++n_chunk == per_unit) {
+            n_chunk = 0;
+            ++n_unit;
+        }
+    };
+    if (per_unit > 0) fetch_scales();
 
     // this CTA's inputs to shared memory, zeros behind k
     {
         const int vecs = (c1 - c0) * 16;  // of eight inputs
-        for (int i = tid; i < rows * vecs; i += LIN_THREADS) {
-            const int r = i / vecs, v = i - r * vecs, at = c0 * 128 + v * 8;
-            char* dst = smem + r * row_bytes + v * 16;
-            const T* src = (const T*)a.x + (long long)(row0 + r) * a.ld_x + at;
+        for (int r = 0; r < rows; ++r) {
+            const T* src = (const T*)a.x + (long long)(row0 + r) * a.ld_x + c0 * 128;
+            char* dst = s_x + r * row_bytes;
             if constexpr (P == 1) {
-                *(uint4*)dst = at < a.w.k ? *(const uint4*)src : make_uint4(0, 0, 0, 0);
-            } else {
-                uint32_t w[P][4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float2 x = at < a.w.k ? *(const float2*)(src + 2 * e) : make_float2(0.f, 0.f);
-#pragma unroll
-                    for (int p = 0; p < P; ++p) {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
-                        w[p][e] = *(const uint32_t*)&h;
-                        x.x -= __low2float(h);
-                        x.y -= __high2float(h);
-                    }
+                for (int v = tid; v < vecs; v += LIN_THREADS) {
+                    const int bytes = c0 * 128 + v * 8 < a.w.k ? 16 : 0;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(su32(dst + v * 16)), "l"(bytes ? src + v * 8 : (const T*)a.x), "r"(bytes) : "memory");
                 }
+            } else {
+#pragma unroll 2
+                for (int v = tid; v < vecs; v += LIN_THREADS) {
+                    const bool in = c0 * 128 + v * 8 < a.w.k;
+                    float4 f[2];
 #pragma unroll
-                for (int p = 0; p < P; ++p) *(uint4*)(dst + p * plane) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+                    for (int h = 0; h < 2; ++h) f[h] = in ? *(const float4*)(src + v * 8 + h * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    const float* x = (const float*)f;
+                    uint32_t w[P][4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x0 = x[2 * e], x1 = x[2 * e + 1];
+#pragma unroll
+                        for (int p = 0; p < P; ++p) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+                            w[p][e] = *(const uint32_t*)&h;
+                            x0 -= __low2float(h);
+                            x1 -= __high2float(h);
+                        }
+                    }
+#pragma unroll
+                    for (int p = 0; p < P; ++p) *(uint4*)(dst + p * plane + v * 16) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+                }
             }
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
+    if (cluster > 1) cluster_sync();  // all CTAs' barriers exist
 
     // lanes of rows that are not there read the last one's (their columns are not stored)
-    int x_at[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) x_at[nt] = min(nt * 8 + g, rows - 1) * row_bytes + t4 * 16;
+    const char* x_at = s_x + min(g, rows - 1) * row_bytes + t4 * 16 + warp_in * 256;
 
-    float acc[NT][4];
-    auto clear = [&]() {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
+    float acc[2][4];
+    auto expired = [&]() {
+        // (the results would be wrong: the error word tells)
+        set_error(a.err, BLEND_ETIMEOUT);
+        abort_sh = 1;
+        f_unit = my_units;
     };
-    float gate[(NT * 128 + LIN_THREADS - 1) / LIN_THREADS];
-    // The warps' sums of tile number i joined in order, and its results written.
+    const int in_half = tid - half * per_half * 32, threads = per_half * 32;
+    // The warps' sums of unit number i joined in order, and its results written (by as many threads as there are).
     auto finish = [&](int i) {
-        float* mine = red + (i & 1) * (LIN_WARPS * NT * 128);
+        const int b = i & 1;
+        float* all = red + (b * LIN_WARPS + half * per_half) * SUMS;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) *(float4*)(mine + (warp * NT + nt) * 128 + lane * 4) = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
-        clear();
-        // (warps come here from different places: a barrier by number, not by place)
-        asm volatile("barrier.sync 0;" ::: "memory");
-        float* sums = part + (i & 1) * (NT * 128);
-        const int tile = tile_at(i);
+        for (int m = 0; m < 2; ++m) *(float4*)(all + warp_in * SUMS + m * 128 + lane * 4) = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
+        asm volatile("barrier.sync %0, %1;" ::"r"(half + 1), "r"(threads) : "memory");
+        // weight row m of tile t and input row col
+        auto place = [&](int t, int m, int col) { return t * 128 + ((m & 7) * 4 + (col >> 1)) * 4 + (m >> 3) * 2 + (col & 1); };
         auto warps_sum = [&](int o) {
             float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < LIN_WARPS; ++w) v += mine[w * NT * 128 + o];
+#pragma unroll 8
+            for (int w = 0; w < per_half; ++w) v += all[w * SUMS + o];
             return v;
         };
+        float* sums = part + (half * 2 + b) * SUMS;
         if (cluster > 1) {
-            for (int o = tid; o < NT * 128; o += LIN_THREADS) sums[o] = warps_sum(o);
-            cg::this_cluster().sync();
+            const uint32_t par = i >> 1 & 1;
+            if (!cluster_phase(&p_free[half][b], par ^ 1, &abort_sh)) expired();
+            for (int o = in_half; o < 32 * rows; o += threads) {
+                const int at = place(o >> 4 & 1, o & 15, o >> 5);
+                sums[at] = warps_sum(at);
+            }
+            meet(&p_full[half][b], cluster);
+            if (!cluster_phase(&p_full[half][b], par, &abort_sh)) expired();
         }
-        const int o0 = NT * 128 * rank / cluster, o1 = NT * 128 * (rank + 1) / cluster;
-#pragma unroll
-        for (int u = 0; u < (int)(sizeof(gate) / sizeof(float)); ++u) {
-            const int q = o0 + u * LIN_THREADS + tid;
-            if (q >= o1) break;
-            // neighbouring threads: neighbouring weight rows of one input row
-            const int m = q & 15, col = (q >> 4) & 7, nt = q >> 7;
-            const int o = nt * 128 + ((m & 7) * 4 + (col >> 1)) * 4 + (m >> 3) * 2 + (col & 1);
+        auto value = [&](int t, int m, int col) {
+            const int at = place(t, m, col);
             float v = 0.f;
             if (cluster > 1) {
-                for (int c = 0; c < cluster; ++c) v += cg::this_cluster().map_shared_rank(sums, c)[o];
+                for (int c = 0; c < cluster; ++c) v += ld_peer(peer_addr(sums + at, c));
             } else
-                v = warps_sum(o);
-            v *= CODE_UNIT;
-            const int r = nt * 8 + col, j = tile * 16 + m;
-            if (r >= rows || j >= a.w.n) continue;
-            const long long at = (long long)(row0 + r) * a.ld_y;
-            if (glu) {
-                if ((i & 1) == 0) {
-                    gate[u] = v;
-                    continue;
-                }
-                const float y = gate[u] / (1.f + __expf(-gate[u])) * v;
-                const long long jj = at + (tile >> 1) * 16 + m;
-                if (a.y_f32) ((float*)a.y)[jj] = y;
-                else ((bf16*)a.y)[jj] = __float2bfloat16_rn(y);
-            } else if (a.epi == BLEND_W4_ADD)
-                ((float*)a.y)[at + j] += v;
-            else if (a.y_f32)
-                ((float*)a.y)[at + j] = v;
-            else
-                ((bf16*)a.y)[at + j] = __float2bfloat16_rn(v);
-        }
-        __syncwarp();
-    };
-
-    clear();
-    if (per_tile == 0) {
-        for (int i = 0; i < my_tiles; ++i) finish(i);
-    } else {
-        int tile = 0, chunk = 0;
-        while (tile < my_tiles) {
-#pragma unroll
-            for (int slot = 0; slot < LIN_RING; ++slot) {
-                if (tile >= my_tiles) break;
-                const int c = c0 + warp + chunk * LIN_WARPS;
-                const uint4 wa = qa[slot], wb = qb[slot];
-                const Scales<G> ka = sa[slot], kb = sb[slot];
-                fetch(slot);
-                const char* xs = smem + (c - c0) * 256;
-                float grp[NT][4];
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    if (w % (G / 32) == 0) {
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) grp[nt][i] = 0.f;
-                    }
-                    const uint32_t ca = word_of(wa, w), cb = word_of(wb, w);
-                    const uint32_t a0[4] = {code_pair<false>(ca), code_pair<false>(cb), code_pair<true>(ca), code_pair<true>(cb)};
-                    const uint32_t a1[4] = {code_pair<false>(ca >> 8), code_pair<false>(cb >> 8), code_pair<true>(ca >> 8), code_pair<true>(cb >> 8)};
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int p = P - 1; p >= 0; --p) {
-                            const uint4 x = *(const uint4*)(xs + p * plane + x_at[nt] + w * 64);
-                            mma(grp[nt], a0, x.x, x.y);
-                            mma(grp[nt], a1, x.z, x.w);
-                        }
-                    if (w % (G / 32) == G / 32 - 1) {
-                        // a group behind k has no scale
-                        const bool live = (c * 128 + w * 32) / G * G < a.w.k;
-                        const float s0 = live ? ka.get(w * 32 / G) : 0.f, s1 = live ? kb.get(w * 32 / G) : 0.f;
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            acc[nt][0] = fmaf(s0, grp[nt][0], acc[nt][0]);
-                            acc[nt][1] = fmaf(s0, grp[nt][1], acc[nt][1]);
-                            acc[nt][2] = fmaf(s1, grp[nt][2], acc[nt][2]);
-                            acc[nt][3] = fmaf(s1, grp[nt][3], acc[nt][3]);
-                        }
-                    }
-                }
-                if (++chunk == per_tile) {
-                    finish(tile);
-                    chunk = 0;
-                    ++tile;
-                }
+                v = warps_sum(at);
+            return v * CODE_UNIT;
+        };
+        // neighbouring threads: neighbouring weight rows of one input row
+        const int unit = unit0 + i * units_step;
+        if (a.epi == BLEND_W4_SWIGLU) {
+            const int o1 = 16 * rows * (rank + 1) / cluster;
+            for (int o = 16 * rows * rank / cluster + in_half; o < o1; o += threads) {
+                const int m = o & 15, col = o >> 4;
+                const float gate = value(0, m, col), up = value(1, m, col);
+                const float y = gate / (1.f + __expf(-gate)) * up;
+                const long long at = (long long)(row0 + col) * a.ld_y + unit * 16 + m;
+                if (a.y_f32) ((float*)a.y)[at] = y;
+                else ((bf16*)a.y)[at] = __float2bfloat16_rn(y);
+            }
+        } else {
+            const int o1 = 32 * rows * (rank + 1) / cluster;
+            for (int o = 32 * rows * rank / cluster + in_half; o < o1; o += threads) {
+                const int m = o & 31, col = o >> 5, j = unit * 32 + m;
+                const float v = value(m >> 4, m & 15, col);
+                if (j >= a.w.n) continue;
+                const long long at = (long long)(row0 + col) * a.ld_y + j;
+                if (a.epi == BLEND_W4_ADD) ((float*)a.y)[at] += v;
+                else if (a.y_f32) ((float*)a.y)[at] = v;
+                else ((bf16*)a.y)[at] = __float2bfloat16_rn(v);
             }
         }
+        __syncwarp();
+        if (cluster > 1) meet(&p_free[half][b], cluster);
+    };
+
+    int slot = 0;
+    uint32_t phase = 0;
+    // lane (g, t4): piece t4 of rows g, g + 8, g + 16, g + 24 (64-byte swizzle: rows 8 apart alike)
+    const char* my_codes = ring + g * 64 + ((t4 ^ (g >> 1 & 3)) << 4);
+    // (one copy of the loop's code: unrolled over the ring, fetching it took a fifth of the time)
+#pragma unroll 1
+    for (int unit = 0; unit < my_units; ++unit) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] = 0.f;
+#pragma unroll 1
+        for (int chunk = 0; chunk < per_unit; ++chunk) {
+            if (!mbar_wait(&full[warp][slot], phase, &abort_sh)) expired();
+            __syncwarp();
+            const char* x_chunk = x_at + chunk * per_half * 256;
+            uint4 q[4];
+            Scales<G> sc[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                q[i] = *(const uint4*)(my_codes + slot * LIN_STAGE + i * 512);
+                sc[i] = next[i];
+            }
+            fetch_scales();
+            // groups that begin behind k have no scale (a chunk's first never does)
+            const int live = a.w.k - (c0 + warp_in + chunk * per_half) * 128;
+            float grp[2][4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                uint32_t lo[2][4], hi[2][4];
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const uint32_t ca = word_of(q[2 * m], w), cb = word_of(q[2 * m + 1], w);
+                    lo[m][0] = code_pair<false>(ca);
+                    lo[m][1] = code_pair<false>(cb);
+                    lo[m][2] = code_pair<true>(ca);
+                    lo[m][3] = code_pair<true>(cb);
+                    hi[m][0] = code_pair<false>(ca >> 8);
+                    hi[m][1] = code_pair<false>(cb >> 8);
+                    hi[m][2] = code_pair<true>(ca >> 8);
+                    hi[m][3] = code_pair<true>(cb >> 8);
+                }
+#pragma unroll
+                for (int p = P - 1; p >= 0; --p) {
+                    const uint4 x = *(const uint4*)(x_chunk + p * plane + w * 64);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        if (w % (G / 32) == 0 && p == P - 1) mma_first(grp[m], lo[m], x.x, x.y);
+                        else mma(grp[m], lo[m], x.x, x.y);
+                        mma(grp[m], hi[m], x.z, x.w);
+                    }
+                }
+                if (w % (G / 32) == G / 32 - 1) {
+                    float s[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[i] = G == 128 || w * 32 / G * G < live ? sc[i].get(w * 32 / G) : 0.f;
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        acc[m][0] = fmaf(s[2 * m], grp[m][0], acc[m][0]);
+                        acc[m][1] = fmaf(s[2 * m], grp[m][1], acc[m][1]);
+                        acc[m][2] = fmaf(s[2 * m + 1], grp[m][2], acc[m][2]);
+                        acc[m][3] = fmaf(s[2 * m + 1], grp[m][3], acc[m][3]);
+                    }
+                }
+            }
+            __syncwarp();  // all lanes have read the slot
+            fetch(slot);
+            if (++slot == depth) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
+        finish(unit);
     }
-    if (cluster > 1) cg::this_cluster().sync();  // the others may still read this CTA's sums
+    if (*(volatile int*)&abort_sh) {
+        // after a wait that ran out: the copies still on their way
+        int never = 0;
+        for (int i = max(0, asked - depth); i < asked; ++i) mbar_wait(&full[warp][i % depth], i / depth & 1, &never);
+    }
+    if (cluster > 1) {
+        __syncwarp();
+        cluster_sync();  // the others may still read this CTA's sums
+    }
 }
 
-template <typename T, int NT, int G> int go(const W4Linear& a, cudaStream_t s) {
+PFN_cuTensorMapEncodeTiled_v12000 g_enc = nullptr;
+
+bool encode(CUtensorMap* map, CUtensorMapDataType dt, const void* base, cuuint64_t inner, cuuint64_t outer, cuuint64_t stride,
+            cuuint32_t box_inner, cuuint32_t box_outer, CUtensorMapSwizzle swizzle) {
+    if (!g_enc) {
+        cudaDriverEntryPointQueryResult qr;
+        void* fn = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &qr) != cudaSuccess ||
+            qr != cudaDriverEntryPointSuccess || !fn) {
+            cudaGetLastError();
+            return false;
+        }
+        g_enc = (PFN_cuTensorMapEncodeTiled_v12000)fn;
+    }
+    const cuuint64_t dims[2] = {inner, outer}, strides[1] = {stride};
+    const cuuint32_t box[2] = {box_inner, box_outer}, es[2] = {1, 1};
+    return g_enc(map, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int G> int go(const W4Linear& a, cudaStream_t s) {
     constexpr int P = sizeof(T) == 4 ? 3 : 1;
-    constexpr int SMEM_MAX = 224 * 1024;
-    auto* kern = k_w4_linear<T, NT, G>;
+    constexpr int SMEM_MAX = 225 * 1024;
+    auto* kern = k_w4_linear<T, G>;
     static const cudaError_t set = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
     if (set != cudaSuccess) return BLEND_ECUDA;
-    const int row_cap = a.rows < 8 * NT ? a.rows : 8 * NT;
-    // CTAs that share a weight row: until the inputs' share leaves room for two CTAs per SM, and until there
-    // are tiles for all SMs
-    const int tiles = a.epi == BLEND_W4_SWIGLU ? a.w.n / 32 : (a.w.n + 15) / 16;
-    int cluster = 1;
-    auto bytes = [&](int c) {
-        return (size_t)P * row_cap * lin_row_bytes((a.w.chunks + c - 1) / c) + (size_t)(2 * LIN_WARPS + 2) * NT * 128 * 4;
-    };
-    while (cluster < LIN_MAX_CLUSTER && (bytes(cluster) > SMEM_MAX / 2 || (tiles * cluster < 304 && a.w.chunks / (2 * cluster) >= LIN_WARPS)))
-        cluster *= 2;
-    const size_t smem = bytes(cluster);
-    if (smem > SMEM_MAX) return BLEND_EUNSUPPORTED;
-    const int row_blocks = (a.rows + 8 * NT - 1) / (8 * NT);
-    int clusters = 152 * 2 / cluster;
-    clusters = clusters < tiles ? clusters : tiles;
+    // Input rows of a launch block, CTAs that share a weight row's inputs and chunks on their way per warp: the
+    // first of them that fit in shared memory, fewer chunks before more CTAs before fewer rows.
+    const int units = (a.w.n + 31) / 32;
+    int cluster = 0, depth = 0, row_cap = a.rows < LIN_ROWS ? a.rows : LIN_ROWS;
+    size_t smem = 0;
+    for (;; row_cap = (row_cap + 1) / 2) {
+        for (int c = 1; c <= LIN_MAX_CLUSTER && c <= a.w.chunks && !cluster; c *= 2)
+            for (int d = LIN_RING; d >= 2 && !cluster; --d) {
+                smem = (size_t)LIN_WARPS * d * LIN_STAGE + (size_t)(2 * LIN_WARPS + (c > 1 ? 4 : 0)) * LIN_SUMS * 4 +
+                       (size_t)P * row_cap * lin_row_bytes((a.w.chunks + c - 1) / c);
+                if (smem <= SMEM_MAX) {
+                    cluster = c;
+                    depth = d;
+                }
+            }
+        if (cluster || row_cap == 1) break;
+    }
+    if (!cluster) return BLEND_EUNSUPPORTED;
+    const int row_blocks = (a.rows + row_cap - 1) / row_cap, fit = 152 / cluster / row_blocks > 0 ? 152 / cluster / row_blocks : 1;
+    // halves with a unit each: where whole CTAs would need a second round anyway
+    const int halves = units > fit ? 2 : 1;
+    const int clusters = std::min((units + halves - 1) / halves, fit);
+    // (no more on their way than a warp has: small calls start sooner with less shared memory)
+    const int of_warp = (units + clusters * halves - 1) / (clusters * halves) *
+                        (((a.w.chunks + cluster - 1) / cluster + LIN_WARPS / halves - 1) / (LIN_WARPS / halves));
+    if (of_warp < depth) {
+        smem -= (size_t)LIN_WARPS * (depth - of_warp) * LIN_STAGE;
+        depth = of_warp;
+    }
+    CUtensorMap mc;
+    if (!w4_encode_codes(&mc, a.w, 32)) return BLEND_EUNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(clusters * cluster), (unsigned)row_blocks);
     cfg.blockDim = dim3(LIN_THREADS);
@@ -418,12 +535,12 @@ template <typename T, int NT, int G> int go(const W4Linear& a, cudaStream_t s) {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = cluster > 1 ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, kern, a, cluster, row_cap) != cudaSuccess) return BLEND_ECUDA;
+    if (cudaLaunchKernelEx(&cfg, kern, mc, a, cluster, row_cap, depth, halves) != cudaSuccess) return BLEND_ECUDA;
     note_launch();
     return BLEND_OK;
 }
-template <typename T, int NT> int go_group(const W4Linear& a, cudaStream_t s) {
-    return a.w.group == 32 ? go<T, NT, 32>(a, s) : a.w.group == 64 ? go<T, NT, 64>(a, s) : go<T, NT, 128>(a, s);
+template <typename T> int go_group(const W4Linear& a, cudaStream_t s) {
+    return a.w.group == 32 ? go<T, 32>(a, s) : a.w.group == 64 ? go<T, 64>(a, s) : go<T, 128>(a, s);
 }
 
 // Rows, and parts of a row where they are few: warps for 152 SMs of 32.
@@ -435,6 +552,15 @@ dim3 pack_grid(const W4View& w) {
 }
 
 }  // namespace
+
+bool w4_encode_codes(CUtensorMap* map, const W4View& w, int rows) {
+    const cuuint64_t bytes = (cuuint64_t)w.chunks * 64;
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, bytes, (cuuint64_t)w.n, bytes, 64, (cuuint32_t)rows, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+bool w4_encode_inputs(CUtensorMap* map, const W4Linear& a, int rows) {
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, (cuuint64_t)a.w.k, (cuuint64_t)a.rows, (cuuint64_t)a.ld_x * 2, 64, (cuuint32_t)rows,
+                  CU_TENSOR_MAP_SWIZZLE_128B);
+}
 
 void launch_w4_pack(int dtype, const W4View& w, const void* src, long long ld, cudaStream_t s) {
     if (dtype == BLEND_BF16) k_w4_pack<bf16><<<pack_grid(w), PACK_THREADS, 0, s>>>(w, (const bf16*)src, ld);
@@ -448,12 +574,11 @@ void launch_w4_unpack(int dtype, const W4View& w, void* out, long long ld, cudaS
 }
 
 int launch_w4_linear(int dtype, const W4Linear& a, cudaStream_t s) {
-    if (dtype == BLEND_BF16 && a.tc && a.rows > LIN_TILE_ROWS && a.w.n >= 128 && a.w.k >= 64) {
+    if (dtype == BLEND_BF16 && a.tc && a.rows > LIN_ROWS && a.w.n >= 128 && a.w.k >= 64) {
         const int rc = launch_w4_tile(a, s);
         if (rc != BLEND_EUNSUPPORTED) return rc;
     }
-    if (dtype == BLEND_BF16) return a.rows <= 8 ? go_group<bf16, 1>(a, s) : go_group<bf16, 2>(a, s);
-    return go_group<float, 1>(a, s);
+    return dtype == BLEND_BF16 ? go_group<bf16>(a, s) : go_group<float>(a, s);
 }
 
 }  // namespace blend

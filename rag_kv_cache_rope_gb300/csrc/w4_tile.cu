@@ -13,7 +13,6 @@
 // Few tiles share their inputs' length among the CTAs of a cluster, which join their sums in order through
 // distributed shared memory.  All waits are bounded: on expiry the error word gets BLEND_ETIMEOUT, copies and
 // products in flight are waited for and TMEM is freed.
-#include "attn_tc.cuh"
 #include "w4.cuh"
 
 namespace blend {
@@ -25,7 +24,6 @@ constexpr int D_STAGES = 2;   // of 128 columns: the accumulators of one group o
 constexpr int CODE_BYTES = TILE_M * 64;
 constexpr int A_COL = 256, TILE_COLS = 512;  // accumulators, then 64 columns a stage
 constexpr int TILE_MAX_CLUSTER = 8;
-constexpr int WAIT_LIMIT = 1 << 24;
 
 template <int NT> constexpr int tile_smem() {
     return STAGES * (NT * 256 + CODE_BYTES) + NT * TILE_M * 4 + 1024;
@@ -46,17 +44,6 @@ template <int C> __device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&
               "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
             : "r"(t));
     }
-}
-// shared::cluster address of this CTA's variable in CTA `rank` of the cluster, and a load from one
-__device__ __forceinline__ uint32_t peer_addr(const void* p, int rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(su32(p)), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ float ld_peer(uint32_t at) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-    return v;
 }
 // Bounded wait, of one thread or of whole warps, in few instructions: the roles' loops are short and run side by
 // side, and what limited a first version was fetching their unrolled code.
@@ -80,34 +67,6 @@ __device__ __forceinline__ bool warp_phases(volatile int* abort_flag, uint64_t* 
     if (b1) done = done && phase_wait(b1, p1, abort_flag);
     if (b2) done = done && phase_wait(b2, p2, abort_flag);
     return __all_sync(0xffffffffu, done);
-}
-// A warp's wait for a phase that other CTAs' arrivals end, and its arrival on a barrier in every CTA of the
-// cluster.  (They are looked at without blocking: a blocking look resumes late after an arrival from outside.)
-__device__ __forceinline__ bool cluster_phase(uint64_t* b, uint32_t par, volatile int* abort_flag) {
-    bool done = false;
-#pragma unroll 1
-    for (int i = 0; i < WAIT_LIMIT && !done; ++i) {
-        uint32_t p;
-        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
-                     : "=r"(p)
-                     : "r"(su32(b)), "r"(par)
-                     : "memory");
-        done = p != 0;
-        if (!done && *abort_flag) break;
-    }
-    return __all_sync(0xffffffffu, done);
-}
-__device__ __forceinline__ void meet(uint64_t* b, int cluster) {
-    __syncwarp();
-    if ((int)(threadIdx.x & 31) < cluster)
-        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(b, threadIdx.x & 31)) : "memory");
-    __syncwarp();
-}
-// One lane of a converged warp, in a form that the compiler knows to be one.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
-    return p != 0;
 }
 // A place in a ring of N stages.
 template <int N> struct Ring {
@@ -203,58 +162,58 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0) {
-    for (int tile = tile0; tile < total; tile += tile_step) {
-        const int wt = tile / n_t, tt = tile - wt * n_t;
+            for (int tile = tile0; tile < total; tile += tile_step) {
+                const int wt = tile / n_t, tt = tile - wt * n_t;
 #pragma unroll 1
-            for (int c = c0; c < c1 && ok; ++c) {
-                if (!warp_phases(abort_flag, &c_empty[st.at], st.phase ^ 1, &empty[st.at], st.phase ^ 1)) {
-                    give_up();
-                    break;
-                }
-                if (elect_one()) {
-                    uint64_t* bar = &in[st.at];
-                    char* x = s_x + st.at * X_BYTES;
-                    mbar_expect_tx(bar, CODE_BYTES + X_BYTES);
-                    tma_2d(s_codes + st.at * CODE_BYTES, &m_codes, bar, c * 64, wt * TILE_M);
-                    tma_2d(x, &m_x, bar, c * 128, tt * NT);
-                    tma_2d(x + X_BYTES / 2, &m_x, bar, c * 128 + 64, tt * NT);
-                }
-                __syncwarp();
-                st.step();
-            }
-            }
-        } else if (warp == 1) {
-    for (int tile = tile0; tile < total; tile += tile_step) {
-#pragma unroll 1
-            for (int c = c0; c < c1 && ok; ++c) {
-                if (!warp_phases(abort_flag, &in[st.at], st.phase, &full[st.at], st.phase, &d_empty[sd.at], sd.phase ^ 1)) {
-                    give_up();
-                    break;
-                }
-                const uint64_t xd = desc_k(su32(s_x + st.at * X_BYTES));
-                const uint32_t at = tb + A_COL + st.at * 64;
-#pragma unroll
-                for (int b = 0; b < SPC / GB; ++b) {
-                    if (b > 0 && !warp_phases(abort_flag, &d_empty[sd.at], sd.phase ^ 1)) {
+                for (int c = c0; c < c1 && ok; ++c) {
+                    if (!warp_phases(abort_flag, &c_empty[st.at], st.phase ^ 1, &empty[st.at], st.phase ^ 1)) {
                         give_up();
                         break;
                     }
-                    fence_after();
-                    const uint32_t d = tb + sd.at * 128;
                     if (elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < GB * G / 16; ++kk) {
-                            const int k = b * GB * G + kk * 16;  // (the second 64 inputs are NT rows of 128 bytes behind)
-                            umma_ts(d + kk * 16 / G * NT, at + k / 2, xd + ((k / 64 * NT * 128 + k % 64 * 2) >> 4), IDESC, k % G ? 1u : 0u);
-                        }
-                        commit(&d_full[sd.at]);
-                        if (b == SPC / GB - 1) commit(&empty[st.at]);
+                        uint64_t* bar = &in[st.at];
+                        char* x = s_x + st.at * X_BYTES;
+                        mbar_expect_tx(bar, CODE_BYTES + X_BYTES);
+                        tma_2d(s_codes + st.at * CODE_BYTES, &m_codes, bar, c * 64, wt * TILE_M);
+                        tma_2d(x, &m_x, bar, c * 128, tt * NT);
+                        tma_2d(x + X_BYTES / 2, &m_x, bar, c * 128 + 64, tt * NT);
                     }
                     __syncwarp();
-                    sd.step();
+                    st.step();
                 }
-                st.step();
             }
+        } else if (warp == 1) {
+            for (int tile = tile0; tile < total; tile += tile_step) {
+#pragma unroll 1
+                for (int c = c0; c < c1 && ok; ++c) {
+                    if (!warp_phases(abort_flag, &in[st.at], st.phase, &full[st.at], st.phase, &d_empty[sd.at], sd.phase ^ 1)) {
+                        give_up();
+                        break;
+                    }
+                    const uint64_t xd = desc_k(su32(s_x + st.at * X_BYTES));
+                    const uint32_t at = tb + A_COL + st.at * 64;
+#pragma unroll
+                    for (int b = 0; b < SPC / GB; ++b) {
+                        if (b > 0 && !warp_phases(abort_flag, &d_empty[sd.at], sd.phase ^ 1)) {
+                            give_up();
+                            break;
+                        }
+                        fence_after();
+                        const uint32_t d = tb + sd.at * 128;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kk = 0; kk < GB * G / 16; ++kk) {
+                                const int k = b * GB * G + kk * 16;  // (the second 64 inputs are NT rows of 128 bytes behind)
+                                umma_ts(d + kk * 16 / G * NT, at + k / 2, xd + ((k / 64 * NT * 128 + k % 64 * 2) >> 4), IDESC, k % G ? 1u : 0u);
+                            }
+                            commit(&d_full[sd.at]);
+                            if (b == SPC / GB - 1) commit(&empty[st.at]);
+                        }
+                        __syncwarp();
+                        sd.step();
+                    }
+                    st.step();
+                }
             }
         }
         end_of_work();
@@ -324,8 +283,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         end_of_cluster();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
-    for (int tile = tile0; tile < total; tile += tile_step) {
-        const int wt = tile / n_t, tt = tile - wt * n_t;
+        for (int tile = tile0; tile < total; tile += tile_step) {
+            const int wt = tile / n_t, tt = tile - wt * n_t;
             const int quarter = warp & 3, cols = (warp - 12) >> 2;
             const int r = quarter * 32 + lane, j = wt * TILE_M + r;
             const uint32_t t_at = tb + ((uint32_t)quarter << 21) + cols * CW;
@@ -433,16 +392,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 g_enc = nullptr;
-
-bool encode(CUtensorMap* map, CUtensorMapDataType dt, const void* base, cuuint64_t inner, cuuint64_t outer, cuuint64_t stride,
-            cuuint32_t box_inner, cuuint32_t box_outer, CUtensorMapSwizzle swizzle) {
-    const cuuint64_t dims[2] = {inner, outer}, strides[1] = {stride};
-    const cuuint32_t box[2] = {box_inner, box_outer}, es[2] = {1, 1};
-    return g_enc(map, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int NT, int G> int go_tile(const W4Linear& a, cudaStream_t s) {
     auto* kern = k_w4_tile<NT, G>;
     cudaLaunchConfig_t cfg = {};
@@ -471,12 +420,12 @@ template <int NT, int G> int go_tile(const W4Linear& a, cudaStream_t s) {
         fit[0] = 0;
     }
     const int tiles = (a.w.n + TILE_M - 1) / TILE_M * ((a.rows + NT - 1) / NT);
-    // CTAs of a tile: what takes the fewest chunks in a row, a tile's start and end counted as eight
+    // CTAs of a tile: what takes the fewest chunks in a row, a tile's end counted as eight, or fourteen with sums to join
     int cluster = 0;
     long long best = 0;
     for (int c = 1; c <= TILE_MAX_CLUSTER && c <= a.w.chunks; ++c) {
         if (fit[c] <= 0) continue;
-        const long long cost = (long long)((tiles + fit[c] - 1) / fit[c]) * ((a.w.chunks + c - 1) / c + 8);
+        const long long cost = (long long)((tiles + fit[c] - 1) / fit[c]) * ((a.w.chunks + c - 1) / c + (c == 1 ? 8 : 14));
         if (!cluster || cost < best) {
             best = cost;
             cluster = c;
@@ -484,11 +433,7 @@ template <int NT, int G> int go_tile(const W4Linear& a, cudaStream_t s) {
     }
     if (!cluster) return BLEND_EUNSUPPORTED;
     CUtensorMap mc, mx;
-    if (!encode(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w.codes, (cuuint64_t)a.w.chunks * 64, (cuuint64_t)a.w.n, (cuuint64_t)a.w.chunks * 64, 64,
-                TILE_M, CU_TENSOR_MAP_SWIZZLE_64B) ||
-        !encode(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, (cuuint64_t)a.w.k, (cuuint64_t)a.rows, (cuuint64_t)a.ld_x * 2, 64, NT,
-                CU_TENSOR_MAP_SWIZZLE_128B))
-        return BLEND_EUNSUPPORTED;
+    if (!w4_encode_codes(&mc, a.w, TILE_M) || !w4_encode_inputs(&mx, a, NT)) return BLEND_EUNSUPPORTED;
     attr.val.clusterDim.x = (unsigned)cluster;
     cfg.numAttrs = cluster > 1 ? 1 : 0;
     cfg.gridDim = dim3((unsigned)((tiles < fit[cluster] ? tiles : fit[cluster]) * cluster));
@@ -504,16 +449,6 @@ template <int NT> int go_tile_group(const W4Linear& a, cudaStream_t s) {
 }  // namespace
 
 int launch_w4_tile(const W4Linear& a, cudaStream_t s) {
-    if (!g_enc) {
-        cudaDriverEntryPointQueryResult qr;
-        void* fn = nullptr;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &qr) != cudaSuccess ||
-            qr != cudaDriverEntryPointSuccess || !fn) {
-            cudaGetLastError();
-            return BLEND_EUNSUPPORTED;
-        }
-        g_enc = (PFN_cuTensorMapEncodeTiled_v12000)fn;
-    }
     return a.rows <= 32 ? go_tile_group<32>(a, s) : a.rows <= 64 ? go_tile_group<64>(a, s) : go_tile_group<128>(a, s);
 }
 
