@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -164,7 +165,7 @@ def lib() -> C.CDLL:
             "w4_unpack": (C.c_int, [vp, C.POINTER(W4), vp, i64, vp]),
             "w4_linear": (C.c_int, [vp, C.POINTER(W4), vp, i64, i32, vp, i64, i32, i32, vp]),
             "token_logprobs": (C.c_int, [vp, vp, i64, i32, i32, i32, C.c_float, vp, i32, vp, vp, i32, vp, vp, vp]),
-            "rope_rows": (C.c_int, [vp, C.POINTER(Rope), C.POINTER(RopeRows), i32, vp, vp, i32, vp]),
+            "rope_rows": (C.c_int, [vp, C.POINTER(Rope), vp, i32, vp, vp, i32, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -741,21 +742,32 @@ def rope_desc(theta: float, rot_dim: int, layout: str = "half", scaling: str = "
     return Rope(ROPE_LAYOUTS[layout], rot_dim, ROPE_SCALINGS[scaling], trained_len, theta, factor, low, high, magnitude)
 
 
-def _rope_part(h: Handle, src: torch.Tensor, dst: torch.Tensor, heads: int, max_n: int, what: str) -> RopeRows:
+_ROPE_ROWS = struct.Struct("@QQqqqqii")  # a blend_rope_rows
+
+
+def _rope_part(src: torch.Tensor, dst: torch.Tensor, dtype, index: int, heads: int, d: int, max_n: int, what: str) -> bytes:
     """src, dst: [rows][heads][head dim] or [layers][rows][heads][head dim]."""
-    d = h.cfg.head_dim
-    st = []
-    for t in (src, dst):
-        sh, sr = t.shape, t.stride()
-        n = len(sh)
-        if n not in (3, 4) or sh[n - 2] != heads or sh[n - 1] != d or sr[n - 1] != 1 or (heads > 1 and sr[n - 2] != d):
-            raise ValueError(f"{what} must be [rows][{heads}][{d}] or [layers][rows][{heads}][{d}] with adjacent heads")
-        if sh[n - 3] < max_n:
-            raise ValueError("fewer rows than max_n")
-        st.append((sr[n - 3] if sh[n - 3] > 1 else heads * d, sr[0] if n == 4 else 0, sh[0] if n == 4 else 1))
-    if st[0][2] != st[1][2]:
+    (s_row, s_layer, layers), (d_row, d_layer, d_layers) = (_rope_strides(t, dtype, index, heads, d, max_n, what) for t in (src, dst))
+    if layers != d_layers:
         raise ValueError(f"{what} and its output must have the same layers")
-    return RopeRows(src.data_ptr(), dst.data_ptr(), st[0][0], st[0][1], st[1][0], st[1][1], heads, st[0][2])
+    return _ROPE_ROWS.pack(src.data_ptr(), dst.data_ptr(), s_row, s_layer, d_row, d_layer, heads, layers)
+
+
+def _rope_strides(t: torch.Tensor, dtype, index: int, heads: int, d: int, max_n: int, what: str):
+    sh, sr = t.shape, t.stride()
+    if len(sh) == 3:
+        (rows, n, dim), (row, head, one), layers, layer = sh, sr, 1, 0
+    elif len(sh) == 4:
+        (layers, rows, n, dim), (layer, row, head, one) = sh, sr
+    else:
+        n = -1
+    if n != heads or dim != d or one != 1 or (heads > 1 and head != d):
+        raise ValueError(f"{what} must be [rows][{heads}][{d}] or [layers][rows][{heads}][{d}] with adjacent heads")
+    if t.dtype is not dtype or t.get_device() != index:
+        raise ValueError(f"{what} must be of the model's dtype and on cuda:{index}")
+    if rows < max_n:
+        raise ValueError("fewer rows than max_n")
+    return (row if rows > 1 else heads * d), layer, layers
 
 
 def rope_rows(h: Handle, rope: Rope, k, k_out, rot, n, max_n, q=None, q_out=None, stream=None):
@@ -764,20 +776,17 @@ def rope_rows(h: Handle, rope: Rope, k, k_out, rot, n, max_n, q=None, q_out=None
     at most max_n rows.  An output may be its own input."""
     index = k.get_device()
     s = _token_stream(index, stream)
-    dt = _model_dtype(h)
+    cfg, dt = h.cfg, _model_dtype(h)
+    d = cfg.head_dim
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
-    for t, what in ((k, "k"), (k_out, "k_out"), (q, "q"), (q_out, "q_out")):
-        if t is not None and (t.dtype is not dt or t.get_device() != index):
-            raise ValueError(f"{what} must be of the model's dtype and on cuda:{index}")
     for t, what, least in ((rot, "rot", max_n), (n, "n", 1)):
         if t.dtype is not torch.int32 or t.numel() < least or not t.is_contiguous() or t.get_device() != index:
             raise ValueError(f"{what} must be contiguous int32 of at least {least} entries on cuda:{index}")
-    parts = (RopeRows * 2)()
-    parts[0] = _rope_part(h, k, k_out, h.cfg.n_kv_heads, max_n, "k")
+    parts = _rope_part(k, k_out, dt, index, cfg.n_kv_heads, d, max_n, "k")
     if q is not None:
-        parts[1] = _rope_part(h, q, q_out, h.cfg.n_q_heads, max_n, "q")
-    if max_n == 0 or parts[0].n_layers == 0:
+        parts += _rope_part(q, q_out, dt, index, cfg.n_q_heads, d, max_n, "q")
+    if max_n == 0 or 0 in k.shape or (q is not None and 0 in q.shape):
         return
     rc = lib().rope_rows(h.ptr, C.byref(rope), parts, 1 if q is None else 2, rot.data_ptr(), n.data_ptr(), max_n, s)
     if rc:

@@ -1660,8 +1660,9 @@ bool rope_freqs(const blend_rope* r, double* f, std::string* why) {
         a = std::max(0.0, std::floor(per_log * std::log(r->trained_len / (pi2 * r->high))));
         b = std::min(r->rot_dim - 1.0, std::ceil(per_log * std::log(r->trained_len / (pi2 * r->low))));
     }
+    const double step = -2.0 * std::log(theta) / r->rot_dim;
     for (int i = 0; i < n; ++i) {
-        const double e = std::pow(theta, -2.0 * i / r->rot_dim);
+        const double e = std::exp(step * i);  // theta^(-2i / rot_dim), to a few 2^-53 of it
         double keep = 1.0;
         if (r->scaling == BLEND_ROPE_LINEAR) keep = 0.0;
         if (bands) keep = (r->trained_len * e / pi2 - r->low) / (r->high - r->low);
