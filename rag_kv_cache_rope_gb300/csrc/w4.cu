@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(PACK_THREADS)
 constexpr int LIN_WARPS = 16, LIN_THREADS = 32 * LIN_WARPS;
 constexpr int LIN_ROWS = 8;         // input rows of a launch block; more of them go to the tcgen05 kernel
 constexpr int LIN_RING = 4;         // chunks of 32 weight rows on their way per warp, at most
-constexpr int LIN_STAGE = 32 * 64;  // bytes of one
+constexpr int LIN_CODES = 32 * 64, LIN_STAGE = LIN_CODES + 32 * 8;  // bytes of one: codes, and eight bytes of scales a row
 constexpr int LIN_MAX_CLUSTER = 8;  // CTAs that share a weight row's inputs
 constexpr int LIN_SUMS = 32 * LIN_ROWS;  // results of a unit
 
@@ -203,14 +203,15 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), g = lane >> 2, t4 = lane & 3;
     const int rank = blockIdx.x % cluster;
     const int per_half = LIN_WARPS / halves, half = warp / per_half, warp_in = warp - half * per_half;
-    const int unit0 = blockIdx.x / cluster * halves + half, units_step = gridDim.x / cluster * halves;
+    const int unit0 = blockIdx.x / cluster + half * (gridDim.x / cluster), units_step = gridDim.x / cluster * halves;
     const int row0 = blockIdx.y * row_cap, rows = min(row_cap, a.rows - row0);
     const int chunks = a.w.chunks;
     const int c0 = chunks * rank / cluster, c1 = chunks * (rank + 1) / cluster;
     const int row_bytes = lin_row_bytes((chunks + cluster - 1) / cluster);
     const int plane = row_cap * row_bytes;
     // rings of codes, [2][LIN_WARPS][SUMS] sums of warps, [2 halves][2][SUMS] of this CTA (cluster > 1), inputs
-    char* ring = smem + warp * (depth * LIN_STAGE);
+    char* ring = smem + warp * (depth * LIN_CODES);
+    char* scale_ring = smem + LIN_WARPS * depth * LIN_CODES + warp * (depth * 256);
     float* red = (float*)(smem + LIN_WARPS * depth * LIN_STAGE);
     float* part = red + 2 * LIN_WARPS * SUMS;
     char* s_x = (char*)(part + (cluster > 1 ? 4 * SUMS : 0));
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
     // this warp's chunks of a unit: c0 + warp_in, + per_half, ...
     const int per_unit = max(0, (c1 - c0 - warp_in + per_half - 1) / per_half);
     if (lane == 0) {
-        for (int i = 0; i < depth; ++i) mbar_init(&full[warp][i], 1);
+        for (int i = 0; i < depth; ++i) mbar_init(&full[warp][i], 1 + 32);
         if (warp == 0) {
             abort_sh = 0;
             for (int i = 0; i < 4; ++i) {
@@ -232,14 +233,25 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
     }
     __syncwarp();
     int f_unit = 0, f_chunk = 0, asked = 0;  // the next chunk to ask for, and how many have been
+    long long at_scale = 0;                  // where the scales of this lane's row begin in it, in bytes
+    const long long scale_end = (long long)a.w.n * chunks * (SPC * 2);
     auto fetch = [&](int slot) {
         if (f_unit >= my_units) return;
+        const int unit = unit0 + f_unit * units_step;
+        if (f_chunk == 0) at_scale = ((long long)min(unit * 32 + lane, a.w.n - 1) * chunks + c0 + warp_in) * (SPC * 2);
+        // a row's scales of the chunk; of one alone, the word that it lies in (as much of it as there is)
+        const uint32_t to = su32(scale_ring + slot * 256 + lane * 8);
+        const char* from = (const char*)a.w.scale + (SPC == 1 ? at_scale & ~3ll : at_scale);
+        if constexpr (SPC == 4) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+        else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(SPC == 1 && (at_scale & ~3ll) + 4 > scale_end ? 2 : 4) : "memory");
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(su32(&full[warp][slot])) : "memory");
         if (elect_one()) {
-            mbar_expect_tx(&full[warp][slot], LIN_STAGE);
-            tma_2d(ring + slot * LIN_STAGE, &m_codes, &full[warp][slot], (c0 + warp_in + f_chunk * per_half) * 64, (unit0 + f_unit * units_step) * 32);
+            mbar_expect_tx(&full[warp][slot], LIN_CODES);
+            tma_2d(ring + slot * LIN_CODES, &m_codes, &full[warp][slot], (c0 + warp_in + f_chunk * per_half) * 64, unit * 32);
         }
         __syncwarp();
         ++asked;
+        at_scale += per_half * (SPC * 2);
         if (++f_chunk == per_unit) {
             f_chunk = 0;
             ++f_unit;
@@ -247,28 +259,6 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
     };
     if (per_unit > 0)
         for (int i = 0; i < depth; ++i) fetch(i);
-    // The scales of the chunk after the one at hand: rows g, g + 8, g + 16, g + 24.
-    Scales<G> next[4];
-    const bf16* sp = nullptr;
-    int behind[4], n_unit = 0, n_chunk = 0;
-    auto fetch_scales = [&]() {
-        if (n_unit >= my_units) return;
-        if (n_chunk == 0) {
-            const int r0 = (unit0 + n_unit * units_step) * 32 + g, r = min(r0, a.w.n - 1);
-            sp = a.w.scale + ((long long)r * chunks + c0 + warp_in) * SPC;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) behind[i] = (min(r0 + 8 * i, a.w.n - 1) - r) * chunks * SPC;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) next[i].load(sp + behind[i]);
-        sp += per_half * SPC;
-        if (++n_chunk == per_unit) {
-            n_chunk = 0;
-            ++n_unit;
-        }
-    };
-    if (per_unit > 0) fetch_scales();
-
     // this CTA's inputs to shared memory, zeros behind k
     {
         const int vecs = (c1 - c0) * 16;  // of eight inputs
@@ -400,12 +390,13 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
             const char* x_chunk = x_at + chunk * per_half * 256;
             uint4 q[4];
             Scales<G> sc[4];
+            // (rows 8 apart: their scales lie alike in their words)
+            const int odd = (g * chunks + c0 + warp_in + chunk * per_half) & 1;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                q[i] = *(const uint4*)(my_codes + slot * LIN_STAGE + i * 512);
-                sc[i] = next[i];
+                q[i] = *(const uint4*)(my_codes + slot * LIN_CODES + i * 512);
+                sc[i].load_shared(scale_ring + slot * 256 + (g + 8 * i) * 8, odd);
             }
-            fetch_scales();
             // groups that begin behind k have no scale (a chunk's first never does)
             const int live = a.w.k - (c0 + warp_in + chunk * per_half) * 128;
             float grp[2][4];
@@ -514,7 +505,7 @@ template <typename T, int G> int go(const W4Linear& a, cudaStream_t s) {
     const int row_blocks = (a.rows + row_cap - 1) / row_cap, fit = 152 / cluster / row_blocks > 0 ? 152 / cluster / row_blocks : 1;
     // halves with a unit each: where whole CTAs would need a second round anyway
     const int halves = units > fit ? 2 : 1;
-    const int clusters = std::min((units + halves - 1) / halves, fit);
+    const int clusters = std::min(units, fit);
     // (no more on their way than a warp has: small calls start sooner with less shared memory)
     const int of_warp = (units + clusters * halves - 1) / (clusters * halves) *
                         (((a.w.chunks + cluster - 1) / cluster + LIN_WARPS / halves - 1) / (LIN_WARPS / halves));

@@ -16,7 +16,7 @@ template <int G> struct Scales;
 template <> struct Scales<32> {
     uint2 v;
     __device__ __forceinline__ void load(const bf16* p) { v = __ldg((const uint2*)p); }
-    __device__ __forceinline__ void load_shared(const char* p) { v = *(const uint2*)p; }
+    __device__ __forceinline__ void load_shared(const char* p, int) { v = *(const uint2*)p; }
     __device__ __forceinline__ float get(int i) const {
         const uint32_t w = i < 2 ? v.x : v.y;
         return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
@@ -25,13 +25,13 @@ template <> struct Scales<32> {
 template <> struct Scales<64> {
     uint32_t v;
     __device__ __forceinline__ void load(const bf16* p) { v = __ldg((const uint32_t*)p); }
-    __device__ __forceinline__ void load_shared(const char* p) { v = *(const uint32_t*)p; }
+    __device__ __forceinline__ void load_shared(const char* p, int) { v = *(const uint32_t*)p; }
     __device__ __forceinline__ float get(int i) const { return __uint_as_float(i & 1 ? v & 0xffff0000u : v << 16); }
 };
 template <> struct Scales<128> {
     unsigned short v;
     __device__ __forceinline__ void load(const bf16* p) { v = __ldg((const unsigned short*)p); }
-    __device__ __forceinline__ void load_shared(const char* p) { v = *(const unsigned short*)p; }
+    __device__ __forceinline__ void load_shared(const char* p, int odd) { v = *(const unsigned short*)(p + 2 * odd); }
     __device__ __forceinline__ float get(int) const { return __uint_as_float((uint32_t)v << 16); }
 };
 
