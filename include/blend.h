@@ -601,7 +601,7 @@ int w4_linear(blend_handle* h, const blend_w4* w4, const void* x, int64_t ld_x, 
  * a row twice for the ranking).
  * Device-side check: an id of vocab or more gives NaN and BLEND_EDEVICE from blend_device_status (the
  * handle is used only for that).  Errors: BLEND_EINVAL for NULL or unaligned pointers, bad sizes, dtype,
- * scale or top (nothing is launched). */
+ * scale or top, an output over the logits, the ids or another output (nothing is launched). */
 int token_logprobs(blend_handle* h, const void* logits, int64_t ld, int32_t dtype, int32_t n_rows, int32_t vocab,
                    float scale, const int32_t* ids, int32_t n_ids, float* logp, float* entropy, int32_t top,
                    int32_t* top_id, float* top_logp, void* stream);

@@ -679,7 +679,9 @@ def w4_linear(h: Handle, w4: W4Ref, x: torch.Tensor, y: torch.Tensor, epi: str =
     """x: [rows][k] of the model's dtype (rows at any stride of 16 bytes); y: [rows][n] ([n / 2] for
     "swiglu"), fp32 or bf16 (fp32 for "add"), rows at any stride."""
     s = _token_stream(w4.index, stream)
-    code = W4_EPIS[epi]
+    code = W4_EPIS.get(epi)
+    if code is None:
+        raise ValueError(f"epi must be one of {', '.join(W4_EPIS)}")
     dt = y.dtype
     if dt is not torch.float32 and dt is not torch.bfloat16:
         raise ValueError("y must be fp32 or bf16")
@@ -739,6 +741,8 @@ def token_logprobs(h: Handle, logits: torch.Tensor, ids=None, logp=None, entropy
 def rope_desc(theta: float, rot_dim: int, layout: str = "half", scaling: str = "none", factor: float = 1.0,
               low: float = 0.0, high: float = 0.0, trained_len: int = 0, magnitude: float = 1.0) -> Rope:
     """Rotary layout and frequencies of a model (see blend_rope)."""
+    if layout not in ROPE_LAYOUTS or scaling not in ROPE_SCALINGS:
+        raise ValueError(f"layout must be one of {', '.join(ROPE_LAYOUTS)}, scaling one of {', '.join(ROPE_SCALINGS)}")
     return Rope(ROPE_LAYOUTS[layout], rot_dim, ROPE_SCALINGS[scaling], trained_len, theta, factor, low, high, magnitude)
 
 

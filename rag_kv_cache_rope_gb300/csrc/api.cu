@@ -1534,6 +1534,16 @@ int view_w4(blend_handle* h, const blend_w4* w, W4View* v) {
     v->chunks = (w->k + 127) / 128;
     return BLEND_OK;
 }
+// Do rows [layers][n][width] at a and b meet?  (Bytes; where both step alike, rows that lie side by side in
+// one buffer do not, although their ranges do.)
+bool rows_meet(const void* pa, long long row_a, long long layer_a, long long layers_a, long long wa, const void* pb,
+               long long row_b, long long layer_b, long long layers_b, long long wb, long long n) {
+    if (!overlap(pa, (layers_a - 1) * layer_a + (n - 1) * row_a + wa, pb, (layers_b - 1) * layer_b + (n - 1) * row_b + wb))
+        return false;
+    if (row_a != row_b || (layers_a > 1 && layer_a % row_a) || (layers_b > 1 && layer_b % row_b)) return true;
+    const long long d = (((long long)((intptr_t)pb - (intptr_t)pa)) % row_a + row_a) % row_a;  // b's place in a's rows
+    return d < wa || d + wb > row_a;
+}
 // Distance between rows of `width` elements of `dtype`: at least one row, a multiple of 16 bytes.
 bool stride16_ok(int dtype, long long ld, long long width) {
     return ld >= width && ld % (long long)(16 / elem_size(dtype)) == 0 && ld <= (1ll << 32);
@@ -1586,9 +1596,9 @@ extern "C" int w4_linear(blend_handle* h, const blend_w4* w4, const void* x, int
     if (!stride16_ok(h->cfg.dtype, ld_x, w4->k) || ld_y < wide || ld_y > (1ll << 32))
         return fail(h, BLEND_EINVAL, "bad row stride (%lld, %lld)", (long long)ld_x, (long long)ld_y);
     if (n_rows == 0) return BLEND_OK;
-    const long long x_span = ((n_rows - 1ll) * ld_x + w4->k) * (long long)elem_size(h->cfg.dtype);
     const long long y_span = ((n_rows - 1ll) * ld_y + wide) * (long long)elem_size(y_dtype);
-    if (overlap(y, y_span, x, x_span)) return fail(h, BLEND_EINVAL, "y overlaps x");
+    const long long ey = (long long)elem_size(y_dtype), ex = (long long)elem_size(h->cfg.dtype);
+    if (rows_meet(y, ld_y * ey, 0, 1, wide * ey, x, ld_x * ex, 0, 1, w4->k * ex, n_rows)) return fail(h, BLEND_EINVAL, "y overlaps x");
     if (overlap(y, y_span, w4->codes, (long long)w4->n * a.w.chunks * 64) ||
         overlap(y, y_span, w4->scale, (long long)w4->n * a.w.chunks * (128 / w4->group) * 2))
         return fail(h, BLEND_EINVAL, "y overlaps the weights");
@@ -1621,6 +1631,14 @@ extern "C" int token_logprobs(blend_handle* h, const void* logits, int64_t ld, i
     if (((uintptr_t)ids | (uintptr_t)logp | (uintptr_t)entropy | (uintptr_t)top_id | (uintptr_t)top_logp) & 3)
         return fail(h, BLEND_EINVAL, "ids and outputs must be 4-byte aligned");
     if (n_rows == 0) return BLEND_OK;
+    // the first two are read, the others written
+    const struct { const void* p; long long bytes; } parts[] = {
+        {logits, ((n_rows - 1ll) * ld + vocab) * (long long)elem_size(dtype)}, {ids, 4ll * n_rows * n_ids}, {logp, 4ll * n_rows * n_ids},
+        {entropy, 4ll * n_rows}, {top_id, 4ll * n_rows * top}, {top_logp, 4ll * n_rows * top}};
+    for (int i = 2; i < 6; ++i)
+        for (int j = 0; j < i; ++j)
+            if (parts[i].p && parts[j].p && overlap(parts[i].p, parts[i].bytes, parts[j].p, parts[j].bytes))
+                return fail(h, BLEND_EINVAL, "an output overlaps the logits, the ids or another output");
     Logprobs a;
     a.logits = logits;
     a.ld = ld;
@@ -1671,16 +1689,6 @@ bool rope_freqs(const blend_rope* r, double* f, std::string* why) {
         f[i] = scaled && r->scaling != BLEND_ROPE_BASE ? e * (keep + (1.0 - keep) / r->factor) : e;
     }
     return true;
-}
-// Do rows [layers][n][width] at a and b meet?  (Bytes; where both step alike, rows that lie side by side in
-// one buffer do not, although their ranges do.)
-bool rows_meet(const void* pa, long long row_a, long long layer_a, long long layers_a, long long wa, const void* pb,
-               long long row_b, long long layer_b, long long layers_b, long long wb, long long n) {
-    if (!overlap(pa, (layers_a - 1) * layer_a + (n - 1) * row_a + wa, pb, (layers_b - 1) * layer_b + (n - 1) * row_b + wb))
-        return false;
-    if (row_a != row_b || (layers_a > 1 && layer_a % row_a) || (layers_b > 1 && layer_b % row_b)) return true;
-    const long long d = (((long long)((intptr_t)pb - (intptr_t)pa)) % row_a + row_a) % row_a;  // b's place in a's rows
-    return d < wa || d + wb > row_a;
 }
 }  // namespace
 

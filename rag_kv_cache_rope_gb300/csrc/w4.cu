@@ -201,10 +201,10 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
     __shared__ uint64_t full[LIN_WARPS][LIN_RING], p_full[2][2], p_free[2][2];
     __shared__ int abort_sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), g = lane >> 2, t4 = lane & 3;
-    const int rank = blockIdx.x % cluster;
+    const int rank = blockIdx.y % cluster;
     const int per_half = LIN_WARPS / halves, half = warp / per_half, warp_in = warp - half * per_half;
-    const int unit0 = blockIdx.x / cluster + half * (gridDim.x / cluster), units_step = gridDim.x / cluster * halves;
-    const int row0 = blockIdx.y * row_cap, rows = min(row_cap, a.rows - row0);
+    const int unit0 = blockIdx.y / cluster + half * (gridDim.y / cluster), units_step = gridDim.y / cluster * halves;
+    const int row0 = blockIdx.x * row_cap, rows = min(row_cap, a.rows - row0);
     const int chunks = a.w.chunks;
     const int c0 = chunks * rank / cluster, c1 = chunks * (rank + 1) / cluster;
     const int row_bytes = lin_row_bytes((chunks + cluster - 1) / cluster);
@@ -385,8 +385,7 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
         for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] = 0.f;
 #pragma unroll 1
         for (int chunk = 0; chunk < per_unit; ++chunk) {
-            if (!mbar_wait(&full[warp][slot], phase, &abort_sh)) expired();
-            __syncwarp();
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[warp][slot], phase, &abort_sh))) expired();
             const char* x_chunk = x_at + chunk * per_half * 256;
             uint4 q[4];
             Scales<G> sc[4];
@@ -516,14 +515,14 @@ template <typename T, int G> int go(const W4Linear& a, cudaStream_t s) {
     CUtensorMap mc;
     if (!w4_encode_codes(&mc, a.w, 32)) return BLEND_EUNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(clusters * cluster), (unsigned)row_blocks);
+    cfg.gridDim = dim3((unsigned)row_blocks, (unsigned)(clusters * cluster));  // (row blocks may pass 65535)
     cfg.blockDim = dim3(LIN_THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    attr.val.clusterDim.y = (unsigned)cluster;
+    attr.val.clusterDim.x = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = cluster > 1 ? 1 : 0;
     if (cudaLaunchKernelEx(&cfg, kern, mc, a, cluster, row_cap, depth, halves) != cudaSuccess) return BLEND_ECUDA;

@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
+        // (never waits: by its registers no other CTA that uses TMEM fits on the SM beside this one)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&tmem_sh)), "r"(TILE_COLS)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -401,11 +402,15 @@ template <int NT, int G> int go_tile(const W4Linear& a, cudaStream_t s) {
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
-    // clusters of 1..8 CTAs that run side by side
-    static int fit[TILE_MAX_CLUSTER + 1] = {-1};
-    if (fit[0] < 0) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_smem<NT>()) != cudaSuccess) return BLEND_ECUDA;
-        for (int c = 1; c <= TILE_MAX_CLUSTER; ++c) {
+    // clusters of 1..8 CTAs that run side by side, asked for once
+    struct Fit {
+        int of[TILE_MAX_CLUSTER + 1] = {};
+        bool ok = false;
+    };
+    static const Fit fits = [&]() {
+        Fit f;
+        f.ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_smem<NT>()) == cudaSuccess;
+        for (int c = 1; c <= TILE_MAX_CLUSTER && f.ok; ++c) {
             attr.val.clusterDim.x = (unsigned)c;
             cfg.numAttrs = 1;
             cfg.gridDim = dim3(152u / c * c);
@@ -415,10 +420,12 @@ template <int NT, int G> int go_tile(const W4Linear& a, cudaStream_t s) {
                 cudaGetLastError();
                 n = 0;
             }
-            fit[c] = n < 152 / c ? n : 152 / c;
+            f.of[c] = n < 152 / c ? n : 152 / c;
         }
-        fit[0] = 0;
-    }
+        return f;
+    }();
+    if (!fits.ok) return BLEND_ECUDA;
+    const int* fit = fits.of;
     const int tiles = (a.w.n + TILE_M - 1) / TILE_M * ((a.rows + NT - 1) / NT);
     // CTAs of a tile: what takes the fewest chunks in a row, a tile's end counted as eight, or fourteen with sums to join
     int cluster = 0;
