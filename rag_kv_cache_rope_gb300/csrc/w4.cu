@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(PACK_THREADS)
 // ---------------------------------------------------------------- products
 constexpr int LIN_WARPS = 16, LIN_THREADS = 32 * LIN_WARPS;
 constexpr int LIN_ROWS = 8;         // input rows of a launch block; more of them go to the tcgen05 kernel
-constexpr int LIN_RING = 4;         // chunks of 32 weight rows on their way per warp, at most
+constexpr int LIN_RING = 3;         // chunks of 32 weight rows on their way per warp, at most
 constexpr int LIN_CODES = 32 * 64, LIN_STAGE = LIN_CODES + 32 * 8;  // bytes of one: codes, and eight bytes of scales a row
 constexpr int LIN_MAX_CLUSTER = 8;  // CTAs that share a weight row's inputs
 constexpr int LIN_SUMS = 32 * LIN_ROWS;  // results of a unit
@@ -257,8 +257,7 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
             ++f_unit;
         }
     };
-    if (per_unit > 0)
-        for (int i = 0; i < depth; ++i) fetch(i);
+    if (per_unit > 0) fetch(0);
     // this CTA's inputs to shared memory, zeros behind k
     {
         const int vecs = (c1 - c0) * 16;  // of eight inputs
@@ -296,7 +295,10 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
             }
         }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (per_unit > 0)
+        for (int i = 1; i < depth; ++i) fetch(i);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");  // (the last scales are in no group yet)
     __syncthreads();
     if (cluster > 1) cluster_sync();  // all CTAs' barriers exist
 
