@@ -24,8 +24,11 @@ namespace cg = cooperative_groups;
 namespace blend {
 namespace {
 
-constexpr int LP_THREADS = 256, LP_WARPS = LP_THREADS / 32;
-constexpr int LP_CTAS = 5;      // per SM: a row's start and end wait for memory and for one another
+// Threads of a CTA, NT: 256, or 128 for many short rows. CTAs per SM: a row's start and end wait for memory and for
+// one another. LP_U: vectors of a thread on their way together.
+template <int NT> constexpr int LP_CTAS = NT == 256 ? 5 : 8;
+template <int NT> constexpr int LP_U = NT == 256 ? 4 : 6;
+constexpr int LP_SHORT = 32, LP_FEW = 8;  // vectors of a thread and alternatives of a row, at most, with 128 threads
 constexpr int LP_GROUPS = 64;   // groups of threads whose maxima bound the k-th logit: twice the largest k
 constexpr int LP_CAND = 1024;   // candidates of one stretch
 constexpr int LP_MAX_CLUSTER = 16;
@@ -127,26 +130,26 @@ __device__ __forceinline__ float pairs_of(const uint4& raw, float2 (&x)[2], floa
     x[1] = make_float2(max_keep_nan(__uint_as_float(raw.z), LP_LOW), max_keep_nan(__uint_as_float(raw.w), LP_LOW));
     return fmaxf(fmaxf(x[0].x, x[0].y), fmaxf(x[1].x, x[1].y));
 }
-struct Shared {
+template <int NT> struct Shared {
     key_t cand[LP_CAND];
     key_t list[BLEND_MAX_TOP];       // this stretch's ranking
     key_t all[LP_MAX_CLUSTER][BLEND_MAX_TOP];
     key_t merged[BLEND_MAX_TOP];
-    Sums sums[LP_WARPS];
+    Sums sums[NT / 32];
     Sums total;
     float group_max[LP_GROUPS];
-    int active[LP_THREADS];
-    int n_active, n_cand, overflow, warp_tot[LP_WARPS];
+    int active[NT];
+    int n_active, n_cand, overflow, warp_tot[NT / 32];
     float bound;
 };
 
 // Appends elements of the stretch's vectors [v0, v1) that `take` accepts to sh.cand, in ascending index, from
 // sh.n_cand on until it holds `until`.  All threads; barriers inside.
-template <typename T, typename Take>
-__device__ void take_in_order(const Row<T>& row, int v0, int v1, int until, Shared& sh, Take take) {
+template <int NT, typename T, typename Take>
+__device__ void take_in_order(const Row<T>& row, int v0, int v1, int until, Shared<NT>& sh, Take take) {
     constexpr int VE = Row<T>::VE;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int j0 = v0; j0 < v1; j0 += LP_THREADS) {
+    for (int j0 = v0; j0 < v1; j0 += NT) {
         const int have = sh.n_cand;
         if (have >= until) break;
         const int j = j0 + tid;
@@ -168,7 +171,7 @@ __device__ void take_in_order(const Row<T>& row, int v0, int v1, int until, Shar
         if (lane == 31) sh.warp_tot[warp] = incl;
         __syncthreads();
         int at = have + incl - mine, total = have;
-        for (int w = 0; w < LP_WARPS; ++w) {
+        for (int w = 0; w < (NT / 32); ++w) {
             if (w < warp) at += sh.warp_tot[w];
             total += sh.warp_tot[w];
         }
@@ -182,11 +185,11 @@ __device__ void take_in_order(const Row<T>& row, int v0, int v1, int until, Shar
 }
 
 // The stretch's `top` highest keys, descending, into sh.list (0 behind the last).  All threads.
-template <typename T>
-__device__ void rank_stretch(const Row<T>& row, int v0, int v1, int top, float my_max, Shared& sh) {
+template <int NT, typename T>
+__device__ void rank_stretch(const Row<T>& row, int v0, int v1, int top, float my_max, Shared<NT>& sh) {
     constexpr int VE = Row<T>::VE;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int PER_GROUP = LP_THREADS / LP_GROUPS;
+    constexpr int PER_GROUP = NT / LP_GROUPS;
     float g = my_max;
 #pragma unroll
     for (int o = 1; o < PER_GROUP; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
@@ -215,14 +218,14 @@ __device__ void rank_stretch(const Row<T>& row, int v0, int v1, int top, float m
     __syncthreads();
     const int n_active = sh.n_active;
     const int w0 = max(v0, 1), w1 = min(v1, row.n_vec - 1);
-    const int each = (max(w1 - w0, 0) + LP_THREADS - 1) / LP_THREADS;  // inner vectors of a thread
+    const int each = (max(w1 - w0, 0) + NT - 1) / NT;  // inner vectors of a thread
     // (the row's first and last vectors besides)
-    for (int i = tid; i < n_active * each + 2; i += LP_THREADS) {
+    for (int i = tid; i < n_active * each + 2; i += NT) {
         const int k = i - 2;
         int j = i == 0 ? 0 : row.n_vec - 1;
         bool mine = i == 0 ? v0 == 0 : v1 == row.n_vec && row.n_vec > 1;
         if (k >= 0) {
-            j = w0 + sh.active[k / each] + k % each * LP_THREADS;
+            j = w0 + sh.active[k / each] + k % each * NT;
             mine = j < w1;
         }
         if (mine) {
@@ -250,7 +253,7 @@ __device__ void rank_stretch(const Row<T>& row, int v0, int v1, int top, float m
             key_t last = ~0ull;
             for (int r = 0; r < top; ++r) {
                 key_t best = 0;
-                for (int j = v0 + tid; j < v1; j += LP_THREADS) {
+                for (int j = v0 + tid; j < v1; j += NT) {
                     float x[VE];
                     row.load(j, x);
 #pragma unroll
@@ -267,7 +270,7 @@ __device__ void rank_stretch(const Row<T>& row, int v0, int v1, int top, float m
                 __syncthreads();
                 if (lane == 0) sh.cand[warp] = best;
                 __syncthreads();
-                for (int w = 0; w < LP_WARPS; ++w) best = sh.cand[w] > best ? sh.cand[w] : best;
+                for (int w = 0; w < (NT / 32); ++w) best = sh.cand[w] > best ? sh.cand[w] : best;
                 if (tid == 0) sh.list[r] = best;
                 last = best;
             }
@@ -284,7 +287,7 @@ __device__ void rank_stretch(const Row<T>& row, int v0, int v1, int top, float m
         take_in_order(row, v0, v1, top, sh, [](float x) { return x != x; });
     }
     const int n = sh.n_cand;
-    for (int c = tid; c < n; c += LP_THREADS) {
+    for (int c = tid; c < n; c += NT) {
         const key_t k = sh.cand[c];
         int above = 0;
         for (int i = 0; i < n; ++i) above += sh.cand[i] > k;
@@ -310,21 +313,21 @@ __device__ __forceinline__ Sums lanes_join(Sums t, int lanes) {
     return t;
 }
 // The threads' sums joined, the same way every time, for every thread.  Two barriers.
-__device__ __forceinline__ Sums block_join(Sums t, Shared& sh) {
+template <int NT> __device__ __forceinline__ Sums block_join(Sums t, Shared<NT>& sh) {
     t = lanes_join(t, 32);
     __syncthreads();
     if (threadIdx.x % 32 == 0) sh.sums[threadIdx.x / 32] = t;
     __syncthreads();
-    return lanes_join(sh.sums[threadIdx.x % LP_WARPS], LP_WARPS);
+    return lanes_join(sh.sums[threadIdx.x % (NT / 32)], (NT / 32));
 }
-__device__ __forceinline__ float block_max(float m, Shared& sh) {
+template <int NT> __device__ __forceinline__ float block_max(float m, Shared<NT>& sh) {
     return block_join({m, 0.f, 0.f}, sh).r;
 }
 
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(LP_THREADS, LP_CTAS) k_logprobs(const Logprobs a, int cluster, float c) {
-    constexpr int VE = Row<T>::VE, U = 4;
-    __shared__ Shared sh;
+template <int NT, typename T, bool TOP>
+__global__ void __launch_bounds__(NT, LP_CTAS<NT>) k_logprobs(const Logprobs a, int cluster, float c) {
+    constexpr int VE = Row<T>::VE, U = LP_U<NT>;
+    __shared__ Shared<NT> sh;
     const int tid = threadIdx.x;
     const int rank = cluster > 1 ? (int)cg::this_cluster().block_rank() : 0;
     const long long r = blockIdx.x / cluster;
@@ -369,10 +372,10 @@ __global__ void __launch_bounds__(LP_THREADS, LP_CTAS) k_logprobs(const Logprobs
     if (tid == 0 && v0 == 0 && v1 > 0) step(row.raw(0));
     if (tid == 0 && v1 == row.n_vec && v0 < v1 && row.n_vec > 1) step(row.raw(row.n_vec - 1));
     int j = w0 + tid;
-    for (; j + (U - 1) * LP_THREADS < w1; j += U * LP_THREADS) {
+    for (; j + (U - 1) * NT < w1; j += U * NT) {
         uint4 x[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) x[u] = row.inner(j + u * LP_THREADS);
+        for (int u = 0; u < U; ++u) x[u] = row.inner(j + u * NT);
 #pragma unroll
         for (int u = 0; u < U; ++u) step(x[u]);
     }
@@ -380,10 +383,10 @@ __global__ void __launch_bounds__(LP_THREADS, LP_CTAS) k_logprobs(const Logprobs
         uint4 x[U - 1];
 #pragma unroll
         for (int u = 0; u < U - 1; ++u)
-            if (j + u * LP_THREADS < w1) x[u] = row.inner(j + u * LP_THREADS);
+            if (j + u * NT < w1) x[u] = row.inner(j + u * NT);
 #pragma unroll
         for (int u = 0; u < U - 1; ++u)
-            if (j + u * LP_THREADS < w1) step(x[u]);
+            if (j + u * NT < w1) step(x[u]);
     }
     float z = z2.x + z2.y, s = s2.x + s2.y;
     Sums t = block_join({ref, z, s}, sh);
@@ -402,7 +405,7 @@ __global__ void __launch_bounds__(LP_THREADS, LP_CTAS) k_logprobs(const Logprobs
                 if (tid == 0) sh.total = t;
             }
             if (TOP)
-                for (int i = tid; i < keys; i += LP_THREADS)
+                for (int i = tid; i < keys; i += NT)
                     sh.all[i / a.top][i % a.top] = cl.map_shared_rank(&sh, i / a.top)->list[i % a.top];
         }
         cl.sync();
@@ -419,13 +422,13 @@ __global__ void __launch_bounds__(LP_THREADS, LP_CTAS) k_logprobs(const Logprobs
             }
             __syncthreads();
             const key_t least = sh.merged[0];
-            for (int i = tid; i < keys; i += LP_THREADS) {
+            for (int i = tid; i < keys; i += NT) {
                 const key_t k = sh.all[i / a.top][i % a.top];
                 if (k >= least && k != 0) sh.cand[atomicAdd(&sh.n_cand, 1)] = k;
             }
             __syncthreads();
             const int n = sh.n_cand;
-            for (int c = tid; c < n; c += LP_THREADS) {
+            for (int c = tid; c < n; c += NT) {
                 const key_t k = sh.cand[c];
                 int above = 0;
                 for (int i = 0; i < n; ++i) above += sh.cand[i] > k;
@@ -444,7 +447,7 @@ __global__ void __launch_bounds__(LP_THREADS, LP_CTAS) k_logprobs(const Logprobs
     bool none = false;
     if (!(fabsf(t.r) <= LP_HUGE)) {
         float m = -INFINITY;
-        for (int j = tid; j < row.n_vec; j += LP_THREADS) {
+        for (int j = tid; j < row.n_vec; j += NT) {
             float x[VE];
             row.load(j, x);
 #pragma unroll
@@ -455,7 +458,7 @@ __global__ void __launch_bounds__(LP_THREADS, LP_CTAS) k_logprobs(const Logprobs
             none = t.z == 0.f;  // (else there is a NaN)
         else {
             z = s = 0.f;
-            for (int j = tid; j < row.n_vec; j += LP_THREADS) {
+            for (int j = tid; j < row.n_vec; j += NT) {
                 float x[VE];
                 row.load(j, x);
 #pragma unroll
@@ -476,7 +479,7 @@ __global__ void __launch_bounds__(LP_THREADS, LP_CTAS) k_logprobs(const Logprobs
         return d == -INFINITY && x > d && lz == lz ? (x - low) * a.scale : LN2 * (d - lz);
     };
     if (tid == 0 && a.entropy) a.entropy[r] = none ? 0.f : LN2 * (lz - t.s / t.z);
-    for (int i = tid; i < a.n_ids; i += LP_THREADS) {
+    for (int i = tid; i < a.n_ids; i += NT) {
         const int id = i == tid ? my_id : __ldg(a.ids + r * a.n_ids + i);
         float lp = 0.f;
         if (id >= a.vocab) {
@@ -493,16 +496,16 @@ __global__ void __launch_bounds__(LP_THREADS, LP_CTAS) k_logprobs(const Logprobs
     }
 }
 
-template <typename T, bool TOP> int launch(const Logprobs& a, cudaStream_t s) {
+template <int NT, typename T, bool TOP> int launch(const Logprobs& a, cudaStream_t s) {
     // A row's CTAs: as many as keep 152 SMs busy, each with 2048 logits at least.
     int cluster = 1;
-    while (cluster < LP_MAX_CLUSTER && (long long)a.rows * cluster * 2 <= 152 * LP_CTAS && a.vocab / (cluster * 2) >= 2048) cluster *= 2;
-    auto* kern = k_logprobs<T, TOP>;
+    while (cluster < LP_MAX_CLUSTER && (long long)a.rows * cluster * 2 <= 152 * LP_CTAS<256> && a.vocab / (cluster * 2) >= 2048) cluster *= 2;
+    auto* kern = k_logprobs<NT, T, TOP>;
     if (cluster > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return BLEND_ECUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.rows * (long long)cluster));
-    cfg.blockDim = dim3(LP_THREADS);
+    cfg.blockDim = dim3(NT);
     cfg.stream = s;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -516,11 +519,20 @@ template <typename T, bool TOP> int launch(const Logprobs& a, cudaStream_t s) {
     return BLEND_OK;
 }
 
+// Half the threads a row, and more rows at once, where rows are many, short and ranked for few: a CTA of 256 then
+// waits for itself (barriers, the last vectors) more than for memory. bf16 logits, 256 against 128 threads: 4096 x 4000,
+// top 5 35.0 and 26.1 us; 2047 x 32003, top 1 38.2 and 35.1, top 20 42.7 and 45.4 (a thread's vectors that are looked at
+// again are twice as many); 2047 x 65000, top 5 59.6 and 62.6; 1250 x 32000, top 5 25.9 and 30.2 (less than two rounds of 256).
+template <typename T, bool TOP> int launch_threads(const Logprobs& a, cudaStream_t s) {
+    const bool many = a.rows >= 2 * 152 * LP_CTAS<256>, is_short = a.vocab <= LP_SHORT * 128 * Row<T>::VE;
+    return many && is_short && a.top <= LP_FEW ? launch<128, T, TOP>(a, s) : launch<256, T, TOP>(a, s);
+}
+
 }  // namespace
 
 int launch_logprobs(int dtype, const Logprobs& a, cudaStream_t s) {
-    if (dtype == BLEND_BF16) return a.top ? launch<bf16, true>(a, s) : launch<bf16, false>(a, s);
-    return a.top ? launch<float, true>(a, s) : launch<float, false>(a, s);
+    if (dtype == BLEND_BF16) return a.top ? launch_threads<bf16, true>(a, s) : launch_threads<bf16, false>(a, s);
+    return a.top ? launch_threads<float, true>(a, s) : launch_threads<float, false>(a, s);
 }
 
 }  // namespace blend

@@ -1,18 +1,20 @@
 """Token operators in calls that the documentation allows and ordinary tests leave out: more row blocks than one grid
 axis holds, rows that lie beside their results, no tensor cores, several host threads and streams, a first call
 that is captured. Bounds as in the tests of each operator."""
+import math
 import os
 import subprocess
 import sys
 import threading
 
+import numpy as np
 import pytest
 import torch
 
 from oracle import token_oracle as O
 from rag_kv_cache_rope_gb300 import binding as b
-from tests.pagedcase import f64, handle, i32
-from tests.test_gpu_tokens import inside, linear_bounds, model, random_logits, rows_of, weights
+from tests.pagedcase import TORCH, f64, handle, i32
+from tests.test_gpu_tokens import inside, linear_bounds, logprobs, model, random_logits, rows_of, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -225,4 +227,40 @@ def test_rope_rows_of_a_fused_projection_in_place_on_two_streams():
     torch.cuda.synchronize()
     assert torch.equal(qkv, one) and torch.equal(qkv[:, 6:], first[:, 6:]) and torch.equal(qkv[0], first[0])
     assert not torch.equal(qkv[1:, :6], first[1:, :6])
+    b.blend_device_status(h)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("vocab,top", [(1, 1), (131, 8), (4000, 5), (16384, 8), (16385, 1), (32768, 8), (32003, 9)])
+def test_logprobs_of_many_short_rows(vocab, top, dtype):
+    """As many rows as fill the GPU with CTAs of half the threads, every row's mask and ranking its own."""
+    h = model("bf16")
+    rows, low = 1600, float(torch.finfo(TORCH[dtype]).min)
+    x = random_logits(rows, vocab, dtype, 70 + vocab)
+    x[3] = 0.0
+    x[4] = low
+    x[5] = float("-inf")
+    x[6, vocab // 2:] = float("-inf")
+    x[7, ::2] = low
+    x[8, vocab // 3] = float("nan")
+    x[9, vocab // 4] = float("inf")
+    x[10] = float("nan")
+    x[11, 1:] = float("-inf")
+    x[12] = 7.5
+    if vocab > 200:
+        x[13] = torch.arange(vocab, device="cuda").to(x.dtype) * -0.01  # the largest with few threads
+    ids = torch.randint(-1, vocab, (rows, 2), dtype=torch.int32, generator=torch.Generator().manual_seed(71)).cuda()
+    got = logprobs(h, x, ids, top, 1.0)
+    at = list(range(14)) + list(range(100, rows, 50)) + [rows - 1]
+    logp, entropy, top_id, top_logp = O.logprobs(f64(x[at]), 1.0, ids[at].cpu().numpy(), top)
+    assert np.array_equal(got["top_id"][at].cpu().numpy(), top_id)
+    # terms 2^t are off by |t| 2^-24 + 2^-22, sums by 2^-24 an addition: a 128th of the row and the joins
+    spread = math.log(vocab) + 8
+    base, step = (vocab / 128 + 64) * 2.0 ** -24 * spread, 8 * 2.0 ** -24
+    inside(f64(got["logp"][at]), logp, base + step * np.abs(np.nan_to_num(logp, posinf=0, neginf=0)))
+    inside(f64(got["top_logp"][at]), top_logp, base + step * np.abs(np.nan_to_num(top_logp, posinf=0, neginf=0)))
+    inside(f64(got["entropy"][at]), entropy, 4 * base + step * spread)
+    lse = torch.logsumexp(x[14:].double(), -1, keepdim=True)
+    want = torch.where(ids[14:] >= 0, torch.gather(x[14:].double(), 1, ids[14:].long().clamp_min(0)) - lse, 0.0)
+    inside(f64(got["logp"][14:]), f64(want), base + step * np.abs(f64(want)))
     b.blend_device_status(h)
