@@ -48,6 +48,11 @@ __device__ __forceinline__ float ld_peer(uint32_t at) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
     return v;
 }
+__device__ __forceinline__ float4 ld_peer4(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
 // A warp's wait for a phase that other CTAs' arrivals end, and its arrival on a barrier in every CTA of the
 // cluster.  (They are looked at without blocking: a blocking look resumes late after an arrival from outside.)
 __device__ __forceinline__ bool cluster_phase(uint64_t* b, uint32_t par, volatile int* abort_flag) {

@@ -8,7 +8,8 @@
 // their own, and eight warps add it, times the row's scale, to sums in registers while the next group's products
 // run.  So a result is what the few rows' kernel gives up to the order of fp32 sums.  (Scales inside the operand
 // take 11 bits: two bf16 parts and twice the products.)
-//   warp 0      TMA: codes and inputs            warp 1      tcgen05.mma of one lane, TMEM
+//   warp 0      TMA: codes                       warp 1      tcgen05.mma of one lane, TMEM
+//   warp 2      TMA: inputs
 //   warps 4-11  codes to TMEM                    warps 12-19 scales, sums, results
 // Few tiles share their inputs' length among the CTAs of a cluster, which join their sums in order through
 // distributed shared memory.  All waits are bounded: on expiry the error word gets BLEND_ETIMEOUT, copies and
@@ -19,14 +20,15 @@ namespace blend {
 namespace {
 
 constexpr int TILE_M = 128, TILE_THREADS = 640, EPI_WARPS = 8;
-constexpr int STAGES = 4;     // chunks of 128 inputs on their way: codes, operands in TMEM, inputs
-constexpr int D_STAGES = 2;   // of 128 columns: the accumulators of one group or, with fewer rows, of several
+constexpr int STAGES = 4;     // chunks of 128 inputs on their way: operands in TMEM, inputs
+// The same of codes.
+template <int NT> constexpr int C_STAGES = NT == 128 ? 4 : 8;
 constexpr int CODE_BYTES = TILE_M * 64;
 constexpr int A_COL = 256, TILE_COLS = 512;  // accumulators, then 64 columns a stage
 constexpr int TILE_MAX_CLUSTER = 8;
 
 template <int NT> constexpr int tile_smem() {
-    return STAGES * (NT * 256 + CODE_BYTES) + NT * TILE_M * 4 + 1024;
+    return STAGES * NT * 256 + C_STAGES<NT> * CODE_BYTES + NT * TILE_M * 4 + 1024;
 }
 
 // C columns of a warp's lanes: 16, 32 or 64.
@@ -87,10 +89,15 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((NT >> 3) << 17) | ((TILE_M >> 4) << 24);
     constexpr int SPC = 128 / G, CW = NT / 2;  // groups of a chunk; columns of an epilogue thread
     constexpr int GB = SPC < 128 / NT ? SPC : 128 / NT;  // groups whose accumulators make a stage
+    constexpr int D_COLS = GB * NT, D_STAGES = A_COL / D_COLS;
+    constexpr int PER = SPC / GB;              // accumulator stages of a chunk
+    constexpr int MMAS = NT == 128 ? 2 : 1;    // warps that issue products
+    static_assert(MMAS == 1 || (D_STAGES % 2 == 0 && STAGES % 2 == 0 && (PER == 1 || PER % 2 == 0)), "each MMA warp keeps to its own stages");
     constexpr int X_BYTES = NT * 256;          // two halves of 64 inputs
     extern __shared__ char smem_raw[];
-    // in: codes and inputs have come; full: four warps' operands; empty: their products are done
-    __shared__ uint64_t in[STAGES], full[STAGES], empty[STAGES], c_empty[STAGES], d_full[D_STAGES], d_empty[D_STAGES],
+    constexpr int CS = C_STAGES<NT>;
+    // c_full, in: codes, inputs have come; full: four warps' operands; empty: their products are done
+    __shared__ uint64_t c_full[CS], c_empty[CS], in[STAGES], full[STAGES], empty[STAGES], d_full[D_STAGES], d_empty[D_STAGES],
         p_full, p_empty, drain;  // p: sums of the cluster's CTAs
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_sh;
@@ -98,7 +105,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     char* smem = (char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     char* s_x = smem;
     char* s_codes = smem + STAGES * X_BYTES;
-    float* part = (float*)(s_codes + STAGES * CODE_BYTES);  // [NT][128]: this CTA's sums
+    float* part = (float*)(s_codes + CS * CODE_BYTES);  // [NT][128]: this CTA's sums
     const int tid = threadIdx.x, lane = tid & 31;
     // (the same for all lanes, and known to be: the roles' loops run in uniform registers, where the operands of
     // tcgen05.mma and TMA have to be; with a loop of lane 0 alone each product took 100 cycles to issue)
@@ -107,7 +114,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&in[i], 1);
             mbar_init(&full[i], 4);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], PER == 1 ? 1 : MMAS);
+        }
+        for (int i = 0; i < CS; ++i) {
+            mbar_init(&c_full[i], 1);
             mbar_init(&c_empty[i], 4);
         }
         for (int i = 0; i < D_STAGES; ++i) {
@@ -116,7 +126,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         }
         mbar_init(&p_full, EPI_WARPS * cluster);
         mbar_init(&p_empty, EPI_WARPS * cluster);
-        mbar_init(&drain, 1);
+        mbar_init(&drain, MMAS);
         abort_sh = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -145,7 +155,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             set_error(a.err, BLEND_ETIMEOUT);
         }
     };
-    Ring<STAGES> st;   // this role's stage
+    Ring<STAGES> st;   // this role's stages
+    Ring<CS> sc;
     Ring<D_STAGES> sd;
     Ring<1> met;
 
@@ -164,29 +175,52 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0) {
             for (int tile = tile0; tile < total; tile += tile_step) {
-                const int wt = tile / n_t, tt = tile - wt * n_t;
+                const int wt = tile / n_t;
 #pragma unroll 1
                 for (int c = c0; c < c1 && ok; ++c) {
-                    if (!warp_phases(abort_flag, &c_empty[st.at], st.phase ^ 1, &empty[st.at], st.phase ^ 1)) {
+                    if (!warp_phases(abort_flag, &c_empty[sc.at], sc.phase ^ 1)) {
                         give_up();
                         break;
                     }
                     if (elect_one()) {
-                        uint64_t* bar = &in[st.at];
+                        mbar_expect_tx(&c_full[sc.at], CODE_BYTES);
+                        tma_2d(s_codes + sc.at * CODE_BYTES, &m_codes, &c_full[sc.at], c * 64, wt * TILE_M);
+                    }
+                    __syncwarp();
+                    sc.step();
+                }
+            }
+        } else if (warp == 2) {
+            for (int tile = tile0; tile < total; tile += tile_step) {
+                const int tt = tile % n_t;
+#pragma unroll 1
+                for (int c = c0; c < c1 && ok; ++c) {
+                    if (!warp_phases(abort_flag, &empty[st.at], st.phase ^ 1)) {
+                        give_up();
+                        break;
+                    }
+                    if (elect_one()) {
                         char* x = s_x + st.at * X_BYTES;
-                        mbar_expect_tx(bar, CODE_BYTES + X_BYTES);
-                        tma_2d(s_codes + st.at * CODE_BYTES, &m_codes, bar, c * 64, wt * TILE_M);
-                        tma_2d(x, &m_x, bar, c * 128, tt * NT);
-                        tma_2d(x + X_BYTES / 2, &m_x, bar, c * 128 + 64, tt * NT);
+                        mbar_expect_tx(&in[st.at], X_BYTES);
+                        tma_2d(x, &m_x, &in[st.at], c * 128, tt * NT);
+                        tma_2d(x + X_BYTES / 2, &m_x, &in[st.at], c * 128 + 64, tt * NT);
                     }
                     __syncwarp();
                     st.step();
                 }
             }
-        } else if (warp == 1) {
+        } else if (warp < 2 * MMAS) {
+            // Each of the two has the accumulator stages of one parity, so that one looks at its barriers while the
+            // other's products run.
+            const int mine = warp >> 1;
             for (int tile = tile0; tile < total; tile += tile_step) {
 #pragma unroll 1
-                for (int c = c0; c < c1 && ok; ++c) {
+                for (int c = c0; c < c1 && ok; ++c, st.step()) {
+                    if (MMAS == 2 && PER == 1 && (sd.at & 1) != mine) {
+                        sd.step();
+                        continue;
+                    }
+                    if (MMAS == 2 && PER > 1 && mine) sd.step();
                     if (!warp_phases(abort_flag, &in[st.at], st.phase, &full[st.at], st.phase, &d_empty[sd.at], sd.phase ^ 1)) {
                         give_up();
                         break;
@@ -194,13 +228,14 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                     const uint64_t xd = desc_k(su32(s_x + st.at * X_BYTES));
                     const uint32_t at = tb + A_COL + st.at * 64;
 #pragma unroll
-                    for (int b = 0; b < SPC / GB; ++b) {
-                        if (b > 0 && !warp_phases(abort_flag, &d_empty[sd.at], sd.phase ^ 1)) {
+                    for (int b = 0; b < PER; ++b) {
+                        if (MMAS == 2 && PER > 1 && (b & 1) != mine) continue;
+                        if (b >= MMAS && !warp_phases(abort_flag, &d_empty[sd.at], sd.phase ^ 1)) {
                             give_up();
                             break;
                         }
                         fence_after();
-                        const uint32_t d = tb + sd.at * 128;
+                        const uint32_t d = tb + sd.at * D_COLS;
                         if (elect_one()) {
 #pragma unroll
                             for (int kk = 0; kk < GB * G / 16; ++kk) {
@@ -208,12 +243,13 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                                 umma_ts(d + kk * 16 / G * NT, at + k / 2, xd + ((k / 64 * NT * 128 + k % 64 * 2) >> 4), IDESC, k % G ? 1u : 0u);
                             }
                             commit(&d_full[sd.at]);
-                            if (b == SPC / GB - 1) commit(&empty[st.at]);
+                            if (b + MMAS >= PER) commit(&empty[st.at]);
                         }
                         __syncwarp();
                         sd.step();
+                        if (MMAS == 2 && PER > 1 && b + 2 < PER) sd.step();
                     }
-                    st.step();
+                    if (MMAS == 2 && PER > 1 && !mine) sd.step();
                 }
             }
         }
@@ -221,12 +257,16 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         if (*abort_flag) {
             // after a wait that ran out, what is still in flight: copies, then products
             int never = 0;
+            // (a stage's use before this one is of this round, others of the last)
             if (warp == 0) {
-                // (a stage's use before st.at is of this round, others of the last)
+#pragma unroll 1
+                for (int i = 0; i < CS; ++i) phase_wait(&c_full[i], i < sc.at ? sc.phase : sc.phase ^ 1, &never);
+            }
+            if (warp == 2) {
 #pragma unroll 1
                 for (int i = 0; i < STAGES; ++i) phase_wait(&in[i], i < st.at ? st.phase : st.phase ^ 1, &never);
             }
-            if (warp == 1) {
+            if ((warp & 1) && warp < 2 * MMAS) {
                 if (elect_one()) commit(&drain);
                 __syncwarp();
                 phase_wait(&drain, 0, &never);
@@ -246,17 +286,17 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         int turn = 1;
         for (int tile = tile0; tile < total; tile += tile_step) {
 #pragma unroll 1
-            for (int c = c0; c < c1 && ok; ++c, st.step()) {
+            for (int c = c0; c < c1 && ok; ++c, st.step(), sc.step()) {
                 turn ^= 1;
                 if (turn != set) continue;
-                if (!warp_phases(abort_flag, &in[st.at], st.phase, &empty[st.at], st.phase ^ 1)) {
+                if (!warp_phases(abort_flag, &c_full[sc.at], sc.phase, &empty[st.at], st.phase ^ 1)) {
                     give_up();
                     break;
                 }
                 // piece t of the row's 64 bytes: words of inputs 32 w + 8 t (64-byte swizzle)
                 uint4 q[4];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) q[t] = *(const uint4*)(s_codes + st.at * CODE_BYTES + r * 64 + ((t ^ (r >> 1 & 3)) << 4));
+                for (int t = 0; t < 4; ++t) q[t] = *(const uint4*)(s_codes + sc.at * CODE_BYTES + r * 64 + ((t ^ (r >> 1 & 3)) << 4));
                 fence_after();
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -274,7 +314,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                         }
                     TMEM_ST32(t_row + st.at * 64 + h * 32, v);
                 }
-                warp_arrive(&c_empty[st.at]);
+                warp_arrive(&c_empty[sc.at]);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 fence_before();
                 warp_arrive(&full[st.at]);
@@ -284,6 +324,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         end_of_cluster();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+        // results of y sixteen bytes at a time
+        const bool vec = (((uintptr_t)a.y | (uintptr_t)a.ld_y * (a.y_f32 ? 4 : 2)) & 15) == 0;
         for (int tile = tile0; tile < total; tile += tile_step) {
             const int wt = tile / n_t, tt = tile - wt * n_t;
             const int quarter = warp & 3, cols = (warp - 12) >> 2;
@@ -300,7 +342,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                 const Scales<G> sc = next;
                 if (c + 1 < c1) next.load(sp + (long long)(c + 1) * SPC);
 #pragma unroll 1
-                for (int b = 0; b < SPC / GB; ++b) {
+                for (int b = 0; b < PER; ++b) {
                     if (!warp_phases(abort_flag, &d_full[sd.at], sd.phase)) {
                         give_up();
                         break;
@@ -313,7 +355,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                         const float s = c * 128 + g * G < a.w.k ? sc.get(g) : 0.f;
                         const float2 s2 = make_float2(s, s);
                         uint32_t v[CW];
-                        tmem_ld<CW>(t_at + sd.at * 128 + gb * NT, v);
+                        tmem_ld<CW>(t_at + sd.at * D_COLS + gb * NT, v);
                         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
                         if (gb == GB - 1) {
                             fence_before();
@@ -326,66 +368,95 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                     sd.step();
                 }
             }
-            // columns i .. i + 7 (those below i1) of the tile: the weight rows' results for eight rows of inputs
-            auto store = [&](const float* v, int i, int i1) {
-                const long long row = (long long)(tt * NT + cols * CW + i) * a.ld_y;
-                if (a.epi == BLEND_W4_SWIGLU) {
-                    // lanes 0..15 hold gate rows, 16..31 the up rows that go with them
-                    const long long at = row + (wt * TILE_M + quarter * 32) / 2 + lane;
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const float up = __shfl_down_sync(0xffffffffu, v[u], 16);
-                        const float y = v[u] / (1.f + __expf(-v[u])) * up;
-                        if (lane >= 16 || j >= a.w.n || i + u >= i1) continue;
-                        if (a.y_f32) ((float*)a.y)[at + u * a.ld_y] = y;
-                        else ((bf16*)a.y)[at + u * a.ld_y] = __float2bfloat16_rn(y);
-                    }
-                } else if (j < a.w.n) {
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        if (i + u >= i1) continue;
-                        const long long at = row + j + u * a.ld_y;
-                        if (a.epi == BLEND_W4_ADD) ((float*)a.y)[at] += v[u];
-                        else if (a.y_f32) ((float*)a.y)[at] = v[u];
-                        else ((bf16*)a.y)[at] = __float2bfloat16_rn(v[u]);
-                    }
-                }
-            };
-            // [column][weight row] of this CTA's sums, and the columns that are this CTA's to finish
-            float* mine = part + cols * CW * TILE_M + r;
+            // This CTA's sums to shared memory, [column][weight row]; then a thread takes eight neighbouring results of one
+            // row of y from there (from all CTAs of the cluster, joined in their order), columns i0 .. i1 - 1 of its half.
+            float* mine = part + cols * CW * TILE_M;
             const int i0 = CW * rank / cluster, i1 = min(CW * (rank + 1) / cluster, a.rows - tt * NT - cols * CW);
             if (cluster > 1 && ok && !cluster_phase(&p_empty, met.phase ^ 1, abort_flag)) give_up();  // the last tile's have been read
+            if (cluster == 1) asm volatile("barrier.sync %0, 128;" ::"r"(1 + cols) : "memory");
 #pragma unroll
-            for (int i = 0; i < CW; ++i) mine[i * TILE_M] = CODE_UNIT * (i & 1 ? acc[i / 2].y : acc[i / 2].x);
+            for (int i = 0; i < CW; ++i) mine[i * TILE_M + r] = CODE_UNIT * (i & 1 ? acc[i / 2].y : acc[i / 2].x);
             if (cluster > 1) {
                 meet(&p_full, cluster);
                 if (ok && !cluster_phase(&p_full, met.phase, abort_flag)) give_up();
-                // joined in the CTAs' order, and back to where this CTA's own were
-                constexpr int U = CW / 2;
-                float v[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) v[u] = 0.f;
-#pragma unroll 1
-                for (int q = 0; q < cluster; ++q) {
-                    const uint32_t from = peer_addr(mine + i0 * TILE_M, q);
-#pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        if (i0 + u < i1) v[u] += ld_peer(from + u * TILE_M * 4);
+            } else
+                asm volatile("barrier.sync %0, 128;" ::"r"(1 + cols) : "memory");
+            auto sums = [&](int at, float (&v)[8]) {
+                if (cluster == 1) {
+                    *(float4*)v = *(const float4*)(mine + at);
+                    *(float4*)(v + 4) = *(const float4*)(mine + at + 4);
+                    return;
                 }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = 0.f;
+#pragma unroll 1
+                for (int c = 0; c < cluster; c += 4) {
+                    float4 q[4][2];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const uint32_t from = peer_addr(mine + at, min(c + u, cluster - 1));
+                        q[u][0] = ld_peer4(from);
+                        q[u][1] = ld_peer4(from + 16);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (c + u < cluster) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[e] += ((const float*)q[u])[e];
+                        }
+                }
+            };
+            const bool swiglu = a.epi == BLEND_W4_SWIGLU;
+            const int per_log2 = swiglu ? 3 : 4, wide = swiglu ? a.w.n / 2 : a.w.n;
+#pragma unroll 1
+            for (int o = quarter * 32 + lane; ok && o < (i1 - i0) << per_log2; o += 128) {
+                const int col = i0 + (o >> per_log2), p = o & ((1 << per_log2) - 1);
+                float v[8];
+                if (swiglu) {
+                    // sixteen gate rows, then the sixteen up rows that go with them
+                    const int at = col * TILE_M + (p >> 1) * 32 + (p & 1) * 8;
+                    float up[8];
+                    sums(at, v);
+                    sums(at + 16, up);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = v[e] / (1.f + __expf(-v[e])) * up[e];
+                } else
+                    sums(col * TILE_M + p * 8, v);
+                const int j0 = (wt * TILE_M >> (swiglu ? 1 : 0)) + p * 8;
+                const long long at = (long long)(tt * NT + cols * CW + col) * a.ld_y + j0;
+                if (vec && j0 + 8 <= wide) {
+                    if (a.y_f32) {
+                        float4* y = (float4*)((float*)a.y + at);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float4 x = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+                            if (a.epi == BLEND_W4_ADD) {
+                                const float4 old = y[h];
+                                x = make_float4(old.x + x.x, old.y + x.y, old.z + x.z, old.w + x.w);
+                            }
+                            y[h] = x;
+                        }
+                    } else {
+                        Vec<bf16> x;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x.set(e, v[e]);
+                        *(uint4*)((bf16*)a.y + at) = x.raw;
+                    }
+                } else {
+#pragma unroll 1
+                    for (int e = 0; e < 8 && j0 + e < wide; ++e) {
+                        const float x = v[0];
+#pragma unroll
+                        for (int i = 0; i < 7; ++i) v[i] = v[i + 1];
+                        if (a.epi == BLEND_W4_ADD) ((float*)a.y)[at + e] += x;
+                        else if (a.y_f32) ((float*)a.y)[at + e] = x;
+                        else ((bf16*)a.y)[at + e] = __float2bfloat16_rn(x);
+                    }
+                }
+            }
+            if (cluster > 1) {
                 meet(&p_empty, cluster);
                 met.step();
-                if (ok) {
-#pragma unroll
-                    for (int u = 0; u < U; u += 8) store(v + u, i0 + u, i1);
-                }
-            } else if (ok) {
-#pragma unroll 1
-                for (int i = 0; i < i1; i += 8) {
-                    float v[8];
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) v[u] = mine[(i + u) * TILE_M];
-                    store(v, i, i1);
-                }
             }
         }
         end_of_work();
