@@ -10,6 +10,10 @@
 // a turn with an error of |rot| * 2^-53 of the frequency and no reduction: one integer multiplication
 // where fp64 angles would need a division by 2 pi.  The fraction is cut into a quarter turn and a
 // rest of at most an eighth, whose sine and cosine are fp32.
+//
+// Cached keys of 16064 rows over 8 layers, 8 x 128 bf16: 87 us, 6.0 TB/s, 90 % of the copy rate, bound by HBM.  4099 rows of
+// 40 + 8 heads: 19.5 us (half of the dims, interleaved) to 20.8, 5 TB/s: the angles of a row are in the way of its first
+// loads.  One row: 2.6 us.
 #include "tokens.cuh"
 
 namespace blend {
@@ -151,7 +155,8 @@ void launch_rope_rows(int dtype, const RopeArgs& a, cudaStream_t s) {
     const int slots0 = a.part[0].heads * a.part[0].n_layers;
     const int slots = slots0 + (a.n_parts > 1 ? a.part[1].heads * a.part[1].n_layers : 0);
     // Slots side by side: as many as fill the GPU (152 SMs of 1024 threads), not more, since every thread
-    // computes its eight angles before it starts; a power of two, at most the slots.
+    // computes its eight angles before it starts; a power of two, at most the slots.  (4099 rows x 48 heads: 20.8 us; each
+    // thread over all heads of its row 31, one head a thread 31; 16064 rows x 64 slots: 87, 91 and 198.)
     const long long per_row = (long long)a.max_n << units_log2;
     int want = 0;
     while (want < log2_floor(slots) && (per_row << want) < 152ll * 1024) ++want;

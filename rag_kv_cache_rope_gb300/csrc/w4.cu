@@ -7,6 +7,10 @@
 // paged.cuh: (code - 8) / 64, exact in bf16; the 64 goes into the sum's end).  The products of a group
 // are summed in fp32 by the matrix unit, and one multiply-add per result and group applies the scale: neither
 // codes nor scales are rounded.  fp32 inputs enter as three bf16 parts, which hold all 24 bits.
+//
+// Up to 8 rows come here (the instruction's other side has 8 columns), and fp32 rows of any number.  bf16, against the
+// tcgen05 kernel: 8 x 27648 x 5120 (groups of 32, SwiGLU) 22 us and 39; 8 x 152064 x 5120 80 and 130; 8 x 5120 x 13824 19.8
+// and 20.8; 9 rows in two blocks of this kernel 36.5 and 38.4, 26.0 and 21.1.
 #include "w4.cuh"
 
 namespace blend {
@@ -14,7 +18,9 @@ namespace {
 
 // ---------------------------------------------------------------- pack, unpack
 // A warp takes a stretch of one row, a lane eight inputs (one word of codes) of it at a time, PACK_U times 32
-// words together: loads and stores are whole lines, and nothing is divided to find a place.
+// words together: loads and stores are whole lines, and nothing is divided to find a place.  Packing 27648 x 5120 bf16 in
+// groups of 32 takes 85 us (4.3 TB/s), bound by instruction issue (71 % of slots: a maximum, an exact quotient and
+// a code for each weight); reading back 58 us (6.3 TB/s), bound by HBM.
 constexpr int PACK_THREADS = 256, PACK_U = 4;
 struct PackPlace {
     int row, w0, w1;  // words w0 .. w1 - 1 of the row, in input order
@@ -166,7 +172,8 @@ __global__ void __launch_bounds__(PACK_THREADS)
 // ---------------------------------------------------------------- products
 constexpr int LIN_WARPS = 16, LIN_THREADS = 32 * LIN_WARPS;
 constexpr int LIN_ROWS = 8;         // input rows of a launch block; more of them go to the tcgen05 kernel
-constexpr int LIN_RING = 3;         // chunks of 32 weight rows on their way per warp, at most
+constexpr int LIN_RING = 3;         // chunks of 32 weight rows on their way per warp, at most (1 x 5120 x 13824: 15.2 us, with four
+                                    // 16.8, since L1 then holds fewer of the scales' sectors)
 constexpr int LIN_CODES = 32 * 64, LIN_STAGE = LIN_CODES + 32 * 8;  // bytes of one: codes, and eight bytes of scales a row
 constexpr int LIN_MAX_CLUSTER = 8;  // CTAs that share a weight row's inputs
 constexpr int LIN_SUMS = 32 * LIN_ROWS;  // results of a unit
@@ -191,6 +198,14 @@ __host__ __device__ __forceinline__ int lin_row_bytes(int chunks) { return chunk
 // A unit is 32 weight rows (two tiles of matrix instructions, for SWIGLU the gate and the up rows of 16 outputs)
 // by all input rows.  The warps of a CTA, or each half of them, take a unit's chunks in turn and join their sums at
 // its end: two halves work on a unit each where there are enough units, and share the inputs in shared memory.
+//
+// Codes come by TMA into a ring of each warp (no barrier of the CTA in the loop, 2 KB a copy, swizzled so that lanes
+// read them without conflicts); the scales beside them by cp.async onto the same mbarrier.  4 x 152064 x 5120 in
+// groups of 64: 79 us, 5.3 TB/s of codes and scales, 78 % of the copy rate; what is left there is issue (66 % of slots: 24
+// instructions for a word of codes).  1 x 27648 x 5120 in groups of 32: 19.8 us, 4.0 TB/s: 5-6 us are the start (inputs to
+// shared memory, the first codes) and the last units.  Inputs that do not fit beside the rings are split among a
+// cluster (8 x 13824 bf16: two CTAs); joining the sums of a unit through distributed shared memory costs 2-3 us, so no
+// more CTAs share a row than have to (8 x 5120 x 13824 with two 19.8 us, with four 31).
 template <typename T, int G>
 __global__ void __launch_bounds__(LIN_THREADS, 1)
     k_w4_linear(const __grid_constant__ CUtensorMap m_codes, const W4Linear a, int cluster, int row_cap, int depth, int halves) {
@@ -504,7 +519,8 @@ template <typename T, int G> int go(const W4Linear& a, cudaStream_t s) {
     }
     if (!cluster) return BLEND_EUNSUPPORTED;
     const int row_blocks = (a.rows + row_cap - 1) / row_cap, fit = 152 / cluster / row_blocks > 0 ? 152 / cluster / row_blocks : 1;
-    // halves with a unit each: where whole CTAs would need a second round anyway
+    // halves with a unit each: where whole CTAs would need a second round anyway (1 x 27648 x 5120 20.8 us for 24.0; 1 x 4096 x
+    // 14336, one round of whole CTAs, 11.2 for 10.8)
     const int halves = units > fit ? 2 : 1;
     const int clusters = std::min(units, fit);
     // (no more on their way than a warp has: small calls start sooner with less shared memory)

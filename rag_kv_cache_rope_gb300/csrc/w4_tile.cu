@@ -8,8 +8,16 @@
 // their own, and eight warps add it, times the row's scale, to sums in registers while the next group's products
 // run.  So a result is what the few rows' kernel gives up to the order of fp32 sums.  (Scales inside the operand
 // take 11 bits: two bf16 parts and twice the products.)
+//
+// What bounds it is that hand-over: a group's accumulators are awaited, read, released and added one after the
+// other by the same warps, about 480 cycles of 128 columns, where the products of 32 inputs take 128 and those of
+// 128 inputs 512.  So groups of 128 run near the products' rate and smaller groups do not: 500 x 27648 x 5120 in groups of 128, 64
+// and 32 takes 109, 158 and 251 us (1.30, 0.90 and 0.56 PFLOP/s), 2048 rows in groups of 128 404 us (1.43 PFLOP/s).  16 to
+// 128 rows are bound by turning codes into operands, about 650 cycles a chunk whatever its rows: 16 x 27648 x 5120 31 us,
+// 64 rows 35, 128 rows 41.  Tiles of 32 and 64 rows for as few rows: 31 us for 42, 35 for 45.
+//
 //   warp 0      TMA: codes                       warp 1      tcgen05.mma of one lane, TMEM
-//   warp 2      TMA: inputs
+//   warp 2      TMA: inputs                      warp 3      products too, with tiles of 128 rows
 //   warps 4-11  codes to TMEM                    warps 12-19 scales, sums, results
 // Few tiles share their inputs' length among the CTAs of a cluster, which join their sums in order through
 // distributed shared memory.  All waits are bounded: on expiry the error word gets BLEND_ETIMEOUT, copies and
