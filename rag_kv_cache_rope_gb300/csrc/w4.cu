@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
                 const int at = place(o >> 4 & 1, o & 15, o >> 5);
                 sums[at] = warps_sum(at);
             }
-            meet(&p_full[half][b], cluster);
+            meet(&p_full[half][b], 0, cluster);
             if (!cluster_phase(&p_full[half][b], par, &abort_sh)) expired();
         }
         auto value = [&](int t, int m, int col) {
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
             }
         }
         __syncwarp();
-        if (cluster > 1) meet(&p_free[half][b], cluster);
+        if (cluster > 1) meet(&p_free[half][b], 0, cluster);
     };
 
     int slot = 0;

@@ -53,7 +53,7 @@ __device__ __forceinline__ float4 ld_peer4(uint32_t at) {
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
     return v;
 }
-// A warp's wait for a phase that other CTAs' arrivals end, and its arrival on a barrier in every CTA of the
+// A warp's wait for a phase that other CTAs' arrivals end, and its arrival on a barrier in n CTAs of the
 // cluster.  (They are looked at without blocking: a blocking look resumes late after an arrival from outside.)
 __device__ __forceinline__ bool cluster_phase(uint64_t* b, uint32_t par, volatile int* abort_flag) {
     bool done = false;
@@ -69,10 +69,11 @@ __device__ __forceinline__ bool cluster_phase(uint64_t* b, uint32_t par, volatil
     }
     return __all_sync(0xffffffffu, done);
 }
-__device__ __forceinline__ void meet(uint64_t* b, int cluster) {
+__device__ __forceinline__ void meet(uint64_t* b, int first, int n) {
     __syncwarp();
-    if ((int)(threadIdx.x & 31) < cluster)
-        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(b, threadIdx.x & 31)) : "memory");
+    const int lane = threadIdx.x & 31;
+    if (lane < n)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(b, first + lane)) : "memory");
     __syncwarp();
 }
 // One lane of a converged warp, in a form that the compiler knows to be one.

@@ -14,13 +14,15 @@
 // 128 inputs 512.  So groups of 128 run near the products' rate and smaller groups do not: 500 x 27648 x 5120 in groups of 128, 64
 // and 32 takes 109, 158 and 251 us (1.30, 0.90 and 0.56 PFLOP/s), 2048 rows in groups of 128 404 us (1.43 PFLOP/s).  16 to
 // 128 rows are bound by turning codes into operands, about 650 cycles a chunk whatever its rows: 16 x 27648 x 5120 31 us,
-// 64 rows 35, 128 rows 41.  Tiles of 32 and 64 rows for as few rows: 31 us for 42, 35 for 45.
+// 64 rows 33, 128 rows 39.  Tiles of 32 and 64 rows for as few rows: 31 us for 42, 35 for 45.
 //
 //   warp 0      TMA: codes                       warp 1      tcgen05.mma of one lane, TMEM
 //   warp 2      TMA: inputs                      warp 3      products too, with tiles of 128 rows
 //   warps 4-11  codes to TMEM                    warps 12-19 scales, sums, results
 // Few tiles share their inputs' length among the CTAs of a cluster, which join their sums in order through
-// distributed shared memory.  All waits are bounded: on expiry the error word gets BLEND_ETIMEOUT, copies and
+// distributed shared memory (16 x 5120 x 13824: 19 us for 38).  Tiles that do not come out even over the SMs are a line of
+// chunks to a cluster, of which each CTA takes a stretch (500 x 5120 x 13824, 160 tiles on 152 SMs: 68 us for 91; 389 x 5120 x
+// 8192: 48 for 58; 128 x 27648 x 5120: 38.6 for 41.6).  All waits are bounded: on expiry the error word gets BLEND_ETIMEOUT, copies and
 // products in flight are waited for and TMEM is freed.
 #include "w4.cuh"
 
@@ -102,7 +104,7 @@ template <int N> struct Ring {
 // NT: input rows of a tile; G: inputs of a group.
 template <int NT, int G>
 __global__ void __launch_bounds__(TILE_THREADS, 1)
-    k_w4_tile(const __grid_constant__ CUtensorMap m_codes, const __grid_constant__ CUtensorMap m_x, const W4Linear a, int cluster) {
+    k_w4_tile(const __grid_constant__ CUtensorMap m_codes, const __grid_constant__ CUtensorMap m_x, const W4Linear a, int cluster, int split) {
     constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((NT >> 3) << 17) | ((TILE_M >> 4) << 24);
     constexpr int SPC = 128 / G, CW = NT / 2;  // groups of a chunk; columns of an epilogue thread
     constexpr int GB = SPC < 128 / NT ? SPC : 128 / NT;  // groups whose accumulators make a stage
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     constexpr int CS = C_STAGES<NT>;
     // c_full, in: codes, inputs have come; full: four warps' operands; empty: their products are done
     __shared__ uint64_t c_full[CS], c_empty[CS], in[STAGES], full[STAGES], empty[STAGES], d_full[D_STAGES], d_empty[D_STAGES],
-        p_full, p_empty, drain;  // p: sums of the cluster's CTAs
+        p_full[2], p_empty[2], drain;  // p: sums of the cluster's CTAs; split: of the neighbours below and above
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_sh;
     volatile int* abort_flag = &abort_sh;
@@ -141,8 +143,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             mbar_init(&d_full[i], 1);
             mbar_init(&d_empty[i], EPI_WARPS);
         }
-        mbar_init(&p_full, EPI_WARPS * cluster);
-        mbar_init(&p_empty, EPI_WARPS * cluster);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&p_full[i], EPI_WARPS * (split ? 1 : cluster));
+            mbar_init(&p_empty[i], EPI_WARPS * (split ? 1 : cluster));
+        }
         mbar_init(&drain, MMAS);
         abort_sh = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -162,8 +166,22 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
 
     const int rank = blockIdx.x % cluster;
     const int n_t = (a.rows + NT - 1) / NT, total = (a.w.n + TILE_M - 1) / TILE_M * n_t;
-    const int tile0 = blockIdx.x / cluster, tile_step = gridDim.x / cluster;
-    const int c0 = a.w.chunks * rank / cluster, c1 = a.w.chunks * (rank + 1) / cluster;
+    // The cluster's tiles: of each a share of the chunks for every CTA or, split, one line of chunks of which a CTA
+    // takes a stretch (whole tiles and a part at either end). Even ranks walk up the line, odd ones down, so that neighbours
+    // both begin or both end with the tile that they share. Who has the smaller part of it leaves its sums in shared memory,
+    // which it needs again a whole tile later, and the other, who comes last, finishes the tile: nobody waits.
+    const int first_tile = blockIdx.x / cluster, tile_step = gridDim.x / cluster, chunks = a.w.chunks;
+    const int tiles = first_tile < total ? (total - first_tile + tile_step - 1) / tile_step : 0;
+    const int lo = split ? tiles * chunks * rank / cluster : 0, hi = split ? tiles * chunks * (rank + 1) / cluster : 0;
+    const int pieces = split ? (hi - 1) / chunks - lo / chunks + 1 : tiles;
+    struct Piece {
+        int tile, c0, c1;
+    };
+    auto piece = [&](int p) {
+        if (!split) return Piece{first_tile + p * tile_step, chunks * rank / cluster, chunks * (rank + 1) / cluster};
+        const int t = rank & 1 ? (hi - 1) / chunks - p : lo / chunks + p;
+        return Piece{first_tile + t * tile_step, max(lo - t * chunks, 0), min(hi - t * chunks, chunks)};
+    };
     bool ok = true;  // this warp's waits
     auto give_up = [&]() {
         ok = false;
@@ -191,10 +209,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0) {
-            for (int tile = tile0; tile < total; tile += tile_step) {
-                const int wt = tile / n_t;
+            for (int p = 0; p < pieces; ++p) {
+                const Piece at = piece(p);
+                const int wt = at.tile / n_t;
 #pragma unroll 1
-                for (int c = c0; c < c1 && ok; ++c) {
+                for (int c = at.c0; c < at.c1 && ok; ++c) {
                     if (!warp_phases(abort_flag, &c_empty[sc.at], sc.phase ^ 1)) {
                         give_up();
                         break;
@@ -208,10 +227,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                 }
             }
         } else if (warp == 2) {
-            for (int tile = tile0; tile < total; tile += tile_step) {
-                const int tt = tile % n_t;
+            for (int p = 0; p < pieces; ++p) {
+                const Piece at = piece(p);
+                const int tt = at.tile % n_t;
 #pragma unroll 1
-                for (int c = c0; c < c1 && ok; ++c) {
+                for (int c = at.c0; c < at.c1 && ok; ++c) {
                     if (!warp_phases(abort_flag, &empty[st.at], st.phase ^ 1)) {
                         give_up();
                         break;
@@ -230,9 +250,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             // Each of the two has the accumulator stages of one parity, so that one looks at its barriers while the
             // other's products run.
             const int mine = warp >> 1;
-            for (int tile = tile0; tile < total; tile += tile_step) {
+            for (int p = 0; p < pieces; ++p) {
+                const Piece of = piece(p);
 #pragma unroll 1
-                for (int c = c0; c < c1 && ok; ++c, st.step()) {
+                for (int c = of.c0; c < of.c1 && ok; ++c, st.step()) {
                     if (MMAS == 2 && PER == 1 && (sd.at & 1) != mine) {
                         sd.step();
                         continue;
@@ -301,9 +322,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         const int r = (warp & 3) * 32 + lane, set = (warp >> 2) & 1;
         const uint32_t t_row = tb + ((uint32_t)(warp & 3) << 21) + A_COL;  // lanes 32 (warp % 4) .. of TMEM
         int turn = 1;
-        for (int tile = tile0; tile < total; tile += tile_step) {
+        for (int p = 0; p < pieces; ++p) {
+            const Piece at = piece(p);
 #pragma unroll 1
-            for (int c = c0; c < c1 && ok; ++c, st.step(), sc.step()) {
+            for (int c = at.c0; c < at.c1 && ok; ++c, st.step(), sc.step()) {
                 turn ^= 1;
                 if (turn != set) continue;
                 if (!warp_phases(abort_flag, &c_full[sc.at], sc.phase, &empty[st.at], st.phase ^ 1)) {
@@ -347,8 +369,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         bool early = false;
         // results of y sixteen bytes at a time
         const bool vec = (((uintptr_t)a.y | (uintptr_t)a.ld_y * (a.y_f32 ? 4 : 2)) & 15) == 0;
-        for (int tile = tile0; tile < total; tile += tile_step) {
-            const int wt = tile / n_t, tt = tile - wt * n_t;
+        int left_at = -1;  // the side of the neighbour who has still to read the sums that were left
+        for (int p = 0; p < pieces; ++p) {
+            const Piece of = piece(p);
+            const int wt = of.tile / n_t, tt = of.tile - wt * n_t, c0 = of.c0, c1 = of.c1;
             const int quarter = warp & 3, cols = (warp - 12) >> 2;
             const int r = quarter * 32 + lane, j = wt * TILE_M + r;
             const uint32_t t_at = tb + ((uint32_t)quarter << 21) + cols * CW;
@@ -398,42 +422,68 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                 }
             }
             // This CTA's sums to shared memory, [column][weight row]; then a thread takes eight neighbouring results of one
-            // row of y from there (from all CTAs of the cluster, joined in their order), columns i0 .. i1 - 1 of its half.
+            // row of y from there, of columns i0 .. i1 - 1 of its half: all, or this CTA's share, joined with the other CTAs'
+            // sums in their order. (The neighbour's sums of a split tile are added before.)
             float* mine = part + cols * CW * TILE_M;
-            const int i0 = CW * rank / cluster, i1 = min(CW * (rank + 1) / cluster, a.rows - tt * NT - cols * CW);
-            if (cluster > 1 && ok && !cluster_phase(&p_empty, met.phase ^ 1, abort_flag)) give_up();  // the last tile's have been read
-            if (cluster == 1) asm volatile("barrier.sync %0, 128;" ::"r"(1 + cols) : "memory");
+            const bool shared = split && c1 - c0 < chunks;
+            const int other = c0 > 0 ? rank - 1 : rank + 1, side = c0 > 0 ? 0 : 1;  // (for it, this CTA is at side ^ 1)
+            const bool finishes = !shared || 2 * (c1 - c0) > chunks || (2 * (c1 - c0) == chunks && rank < other);
+            const int i0 = split ? 0 : CW * rank / cluster, i1 = min(split ? CW : CW * (rank + 1) / cluster, a.rows - tt * NT - cols * CW);
+            // what was there has been read, by the other CTAs and by this one
+            if (split && left_at >= 0 && ok && !cluster_phase(&p_empty[left_at], 0, abort_flag)) give_up();
+            if (!split && cluster > 1 && ok && !cluster_phase(&p_empty[0], met.phase ^ 1, abort_flag)) give_up();
+            asm volatile("barrier.sync %0, 128;" ::"r"(1 + cols) : "memory");
 #pragma unroll
-            for (int i = 0; i < CW; ++i) mine[i * TILE_M + r] = CODE_UNIT * (i & 1 ? acc[i / 2].y : acc[i / 2].x);
-            if (cluster > 1) {
-                meet(&p_full, cluster);
-                if (ok && !cluster_phase(&p_full, met.phase, abort_flag)) give_up();
-            } else
-                asm volatile("barrier.sync %0, 128;" ::"r"(1 + cols) : "memory");
+            for (int i = 0; i < CW; ++i) mine[i * TILE_M + r] = i & 1 ? acc[i / 2].y : acc[i / 2].x;
+            left_at = finishes ? -1 : side;
+            if (!finishes) {
+                meet(&p_full[side ^ 1], other, 1);
+                continue;
+            }
+            if (shared) {
+                if (ok && !cluster_phase(&p_full[side], 0, abort_flag)) give_up();
+                const uint32_t from = peer_addr(mine + r, other);
+#pragma unroll 1
+                for (int i = 0; i < CW; i += 16) {
+                    float v[16];
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) v[u] = ld_peer(from + (i + u) * TILE_M * 4);
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) mine[(i + u) * TILE_M + r] += v[u];
+                }
+                meet(&p_empty[side ^ 1], other, 1);
+            }
+            if (cluster == 1 || split) asm volatile("barrier.sync %0, 128;" ::"r"(1 + cols) : "memory");
+            else {
+                meet(&p_full[0], 0, cluster);
+                if (ok && !cluster_phase(&p_full[0], met.phase, abort_flag)) give_up();
+            }
             auto sums = [&](int at, float (&v)[8]) {
-                if (cluster == 1) {
+                if (cluster == 1 || split) {
                     *(float4*)v = *(const float4*)(mine + at);
                     *(float4*)(v + 4) = *(const float4*)(mine + at + 4);
-                    return;
-                }
+                } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = 0.f;
+                    for (int e = 0; e < 8; ++e) v[e] = 0.f;
 #pragma unroll 1
-                for (int c = 0; c < cluster; c += 4) {
-                    float4 q[4][2];
+                    for (int c = 0; c < cluster; c += 4) {
+                        float4 q[4][2];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const uint32_t from = peer_addr(mine + at, min(c + u, cluster - 1));
-                        q[u][0] = ld_peer4(from);
-                        q[u][1] = ld_peer4(from + 16);
-                    }
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (c + u < cluster) {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) v[e] += ((const float*)q[u])[e];
+                        for (int u = 0; u < 4; ++u) {
+                            const uint32_t from = peer_addr(mine + at, min(c + u, cluster - 1));
+                            q[u][0] = ld_peer4(from);
+                            q[u][1] = ld_peer4(from + 16);
                         }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            if (c + u < cluster) {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) v[e] += ((const float*)q[u])[e];
+                            }
+                    }
                 }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= CODE_UNIT;
             };
             const bool swiglu = a.epi == BLEND_W4_SWIGLU;
             const int per_log2 = swiglu ? 3 : 4, wide = swiglu ? a.w.n / 2 : a.w.n;
@@ -483,8 +533,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                     }
                 }
             }
-            if (cluster > 1) {
-                meet(&p_empty, cluster);
+            if (!split && cluster > 1) {
+                meet(&p_empty[0], 0, cluster);
                 met.step();
             }
         }
@@ -527,15 +577,21 @@ template <int NT, int G> int go_tile(const W4Linear& a, cudaStream_t s) {
     if (!fits.ok) return BLEND_ECUDA;
     const int* fit = fits.of;
     const int tiles = (a.w.n + TILE_M - 1) / TILE_M * ((a.rows + NT - 1) / NT);
-    // CTAs of a tile: what takes the fewest chunks in a row, a tile's end counted as eight, or fourteen with sums to join
-    int cluster = 0;
+    // CTAs of a cluster, and whether they split its tiles: what takes the fewest chunks in a row, a tile's end counted as
+    // four, with sums to join as sixteen. (A split tile belongs to two CTAs: a cluster has as many tiles as CTAs.)
+    int cluster = 0, split = 0;
     long long best = 0;
     for (int c = 1; c <= TILE_MAX_CLUSTER && c <= a.w.chunks; ++c) {
         if (fit[c] <= 0) continue;
-        const long long cost = (long long)((tiles + fit[c] - 1) / fit[c]) * ((a.w.chunks + c - 1) / c + (c == 1 ? 8 : 14));
-        if (!cluster || cost < best) {
-            best = cost;
-            cluster = c;
+        const long long rounds = (tiles + fit[c] - 1) / fit[c];
+        for (int sp = 0; sp <= (c > 1 && tiles / fit[c] >= c && rounds * a.w.chunks < (1 << 24)); ++sp) {
+            const long long cost = sp ? (rounds * a.w.chunks + c - 1) / c + (rounds + c - 1) / c * 4 + 16
+                                      : rounds * ((a.w.chunks + c - 1) / c + (c == 1 ? 4 : 16));
+            if (!cluster || cost < best) {
+                best = cost;
+                cluster = c;
+                split = sp;
+            }
         }
     }
     if (!cluster) return BLEND_EUNSUPPORTED;
@@ -545,7 +601,7 @@ template <int NT, int G> int go_tile(const W4Linear& a, cudaStream_t s) {
     cfg.numAttrs = cluster > 1 ? 1 : 0;
     cfg.gridDim = dim3((unsigned)((tiles < fit[cluster] ? tiles : fit[cluster]) * cluster));
     cfg.dynamicSmemBytes = tile_smem<NT>();
-    if (cudaLaunchKernelEx(&cfg, kern, mc, mx, a, cluster) != cudaSuccess) return BLEND_ECUDA;
+    if (cudaLaunchKernelEx(&cfg, kern, mc, mx, a, cluster, split) != cudaSuccess) return BLEND_ECUDA;
     note_launch();
     return BLEND_OK;
 }

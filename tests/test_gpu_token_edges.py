@@ -264,3 +264,42 @@ def test_logprobs_of_many_short_rows(vocab, top, dtype):
     want = torch.where(ids[14:] >= 0, torch.gather(x[14:].double(), 1, ids[14:].long().clamp_min(0)) - lse, 0.0)
     inside(f64(got["logp"][14:]), f64(want), base + step * np.abs(f64(want)))
     b.blend_device_status(h)
+
+
+@pytest.mark.parametrize("rows,n,k,group,epi,out", [
+    (500, 5120, 4096, 128, "store", "bf16"), (389, 5000, 4104, 32, "add", "f32"), (20, 20480, 4096, 64, "store", "f32"),
+    (60, 20576, 4360, 128, "swiglu", "bf16"), (257, 9001, 5120, 64, "store", "f32"), (500, 5120, 13824, 128, "store", "f32")])
+def test_linear_tiles_that_two_ctas_share(rows, n, k, group, epi, out):
+    """Tiles that do not come out even over the SMs, so that CTAs take stretches of their line; against 64 bits on the GPU
+    with the packed values, which are exact in fp32."""
+    h = model("bf16")
+    w4 = b.W4Ref.empty(n, k, group)
+    w4.codes.random_(0, 256, generator=torch.Generator("cuda").manual_seed(90))
+    w4.scale.copy_(torch.rand(w4.scale.shape, device="cuda", generator=torch.Generator("cuda").manual_seed(91)) / 64 + 1 / 128)
+    w = torch.empty(n, k, device="cuda")
+    b.w4_unpack(model("f32"), w4, w)
+    w = w.double()
+    x = rows_of("bf16", rows, k, 92, 0.3)
+    want, mag = x.double() @ w.T, x.double().abs() @ w.abs().T
+    err = (3 * k / 16 + k / 32 + 64) * 2.0 ** -23 * mag
+    if epi == "swiglu":
+        (g, u), (eg, eu) = (t.view(rows, -1, 2, 16).unbind(2) for t in (want, err))
+        s = g * torch.sigmoid(g)
+        es = 1.1 * eg + (2 + g.abs()) * 2.0 ** -21 * s.abs()
+        err, want = ((u.abs() * es + s.abs() * eu + es * eu).reshape(rows, -1), (s * u).reshape(rows, -1))
+    wide = want.shape[1]
+    base = torch.randn(rows, wide, device="cuda")
+    room = torch.full((rows + 1, wide + 8), 7.0, dtype=TORCH[out], device="cuda")
+    y = room[:rows, :wide]
+    y.copy_(base)
+    again = y.clone()
+    b.w4_linear(h, w4, x, y, epi=epi)
+    if epi == "add":
+        want = want + base.double()
+    step = 2.0 ** -8 if out == "bf16" else 2.0 ** -24
+    bound = err * 1.01 + step * (want.abs() + err) + 1e-30 + (step * want.abs() if epi == "add" else 0)
+    assert bool(((y.double() - want).abs() <= bound).all())
+    assert bool((room[rows:] == 7.0).all()) and bool((room[:, wide:] == 7.0).all())
+    b.w4_linear(h, w4, x, again, epi=epi)
+    assert torch.equal(y, again)
+    b.blend_device_status(h)
