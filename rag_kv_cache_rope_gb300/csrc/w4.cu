@@ -9,8 +9,8 @@
 // codes nor scales are rounded.  fp32 inputs enter as three bf16 parts, which hold all 24 bits.
 //
 // Up to 8 rows come here (the instruction's other side has 8 columns), and fp32 rows of any number.  bf16, against the
-// tcgen05 kernel: 8 x 27648 x 5120 (groups of 32, SwiGLU) 22 us and 39; 8 x 152064 x 5120 80 and 130; 8 x 5120 x 13824 19.8
-// and 20.8; 9 rows in two blocks of this kernel 36.5 and 38.4, 26.0 and 21.1.
+// tcgen05 kernel: 8 x 27648 x 5120 (groups of 32, SwiGLU) 22 us and 34; 8 x 152064 x 5120 83 and 123; 8 x 5120 x 13824 19.7
+// and 19.5; 9 rows in two blocks of this kernel 36.4 and 34.2 (27648 x 5120, groups of 32), 25.9 and 19.5 (5120 x 13824).
 #include "w4.cuh"
 
 namespace blend {
@@ -19,7 +19,7 @@ namespace {
 // ---------------------------------------------------------------- pack, unpack
 // A warp takes a stretch of one row, a lane eight inputs (one word of codes) of it at a time, PACK_U times 32
 // words together: loads and stores are whole lines, and nothing is divided to find a place.  Packing 27648 x 5120 bf16 in
-// groups of 32 takes 85 us (4.3 TB/s), bound by instruction issue (71 % of slots: a maximum, an exact quotient and
+// groups of 32 takes 85 us (4.3 TB/s; 121 where the buffers lie unluckily), bound by instruction issue (71 % of slots: a maximum, an exact quotient and
 // a code for each weight); reading back 58 us (6.3 TB/s), bound by HBM.
 constexpr int PACK_THREADS = 256, PACK_U = 4;
 struct PackPlace {

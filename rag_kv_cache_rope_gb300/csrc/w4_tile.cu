@@ -12,17 +12,17 @@
 // What bounds it is that hand-over: a group's accumulators are awaited, read, released and added one after the
 // other by the same warps, about 480 cycles of 128 columns, where the products of 32 inputs take 128 and those of
 // 128 inputs 512.  So groups of 128 run near the products' rate and smaller groups do not: 500 x 27648 x 5120 in groups of 128, 64
-// and 32 takes 109, 158 and 251 us (1.30, 0.90 and 0.56 PFLOP/s), 2048 rows in groups of 128 404 us (1.43 PFLOP/s).  16 to
-// 128 rows are bound by turning codes into operands, about 650 cycles a chunk whatever its rows: 16 x 27648 x 5120 31 us,
-// 64 rows 33, 128 rows 39.  Tiles of 32 and 64 rows for as few rows: 31 us for 42, 35 for 45.
+// and 32 takes 111, 160 and 253 us (1.28, 0.88 and 0.56 PFLOP/s), 2048 rows in groups of 128 412 us (1.41 PFLOP/s).  16 to
+// 128 rows are bound by turning codes into operands, about 600 cycles a chunk whatever its rows: 16 x 27648 x 5120 27 us,
+// 64 rows 31, 128 rows 37.  Tiles of 32 and 64 rows for as few rows: 29 us for 35, 33 for 37.
 //
 //   warp 0      TMA: codes                       warp 1      tcgen05.mma of one lane, TMEM
 //   warp 2      TMA: inputs                      warp 3      products too, with tiles of 128 rows
 //   warps 4-11  codes to TMEM                    warps 12-19 scales, sums, results
 // Few tiles share their inputs' length among the CTAs of a cluster, which join their sums in order through
 // distributed shared memory (16 x 5120 x 13824: 19 us for 38).  Tiles that do not come out even over the SMs are a line of
-// chunks to a cluster, of which each CTA takes a stretch (500 x 5120 x 13824, 160 tiles on 152 SMs: 68 us for 91; 389 x 5120 x
-// 8192: 48 for 58; 128 x 27648 x 5120: 38.6 for 41.6).  All waits are bounded: on expiry the error word gets BLEND_ETIMEOUT, copies and
+// chunks to a cluster, of which each CTA takes a stretch (500 x 5120 x 13824, 160 tiles on 152 SMs: 62 us for 91; 389 x 5120 x
+// 8192: 43 for 58; 128 x 27648 x 5120: 37 for 41.6).  All waits are bounded: on expiry the error word gets BLEND_ETIMEOUT, copies and
 // products in flight are waited for and TMEM is freed.
 #include "w4.cuh"
 
@@ -101,10 +101,11 @@ template <int N> struct Ring {
     }
 };
 
-// NT: input rows of a tile; G: inputs of a group.
-template <int NT, int G>
+// NT: input rows of a tile; G: inputs of a group; split: CTAs take stretches of a line of tiles (a form of its own: in one
+// with the other, 500 x 27648 x 5120 took 113 us for 110).
+template <int NT, int G, bool split>
 __global__ void __launch_bounds__(TILE_THREADS, 1)
-    k_w4_tile(const __grid_constant__ CUtensorMap m_codes, const __grid_constant__ CUtensorMap m_x, const W4Linear a, int cluster, int split) {
+    k_w4_tile(const __grid_constant__ CUtensorMap m_codes, const __grid_constant__ CUtensorMap m_x, const W4Linear a, int cluster) {
     constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((NT >> 3) << 17) | ((TILE_M >> 4) << 24);
     constexpr int SPC = 128 / G, CW = NT / 2;  // groups of a chunk; columns of an epilogue thread
     constexpr int GB = SPC < 128 / NT ? SPC : 128 / NT;  // groups whose accumulators make a stage
@@ -544,7 +545,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
 }
 
 template <int NT, int G> int go_tile(const W4Linear& a, cudaStream_t s) {
-    auto* kern = k_w4_tile<NT, G>;
+    auto *kern = k_w4_tile<NT, G, false>, *kern_split = k_w4_tile<NT, G, true>;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(TILE_THREADS);
     cfg.stream = s;
@@ -559,7 +560,8 @@ template <int NT, int G> int go_tile(const W4Linear& a, cudaStream_t s) {
     };
     static const Fit fits = [&]() {
         Fit f;
-        f.ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_smem<NT>()) == cudaSuccess;
+        f.ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_smem<NT>()) == cudaSuccess &&
+               cudaFuncSetAttribute(kern_split, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_smem<NT>()) == cudaSuccess;
         for (int c = 1; c <= TILE_MAX_CLUSTER && f.ok; ++c) {
             attr.val.clusterDim.x = (unsigned)c;
             cfg.numAttrs = 1;
@@ -577,6 +579,7 @@ template <int NT, int G> int go_tile(const W4Linear& a, cudaStream_t s) {
     if (!fits.ok) return BLEND_ECUDA;
     const int* fit = fits.of;
     const int tiles = (a.w.n + TILE_M - 1) / TILE_M * ((a.rows + NT - 1) / NT);
+    // (the other form takes the same room)
     // CTAs of a cluster, and whether they split its tiles: what takes the fewest chunks in a row, a tile's end counted as
     // four, with sums to join as sixteen. (A split tile belongs to two CTAs: a cluster has as many tiles as CTAs.)
     int cluster = 0, split = 0;
@@ -601,7 +604,7 @@ template <int NT, int G> int go_tile(const W4Linear& a, cudaStream_t s) {
     cfg.numAttrs = cluster > 1 ? 1 : 0;
     cfg.gridDim = dim3((unsigned)((tiles < fit[cluster] ? tiles : fit[cluster]) * cluster));
     cfg.dynamicSmemBytes = tile_smem<NT>();
-    if (cudaLaunchKernelEx(&cfg, kern, mc, mx, a, cluster, split) != cudaSuccess) return BLEND_ECUDA;
+    if (cudaLaunchKernelEx(&cfg, split ? kern_split : kern, mc, mx, a, cluster) != cudaSuccess) return BLEND_ECUDA;
     note_launch();
     return BLEND_OK;
 }
