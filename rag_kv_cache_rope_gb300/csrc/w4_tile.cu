@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         if (*abort_flag) {
             // after a wait that ran out, what is still in flight: copies, then products
             int never = 0;
-            // (a stage's use before this one is of this round, others of the last)
+            // (stages before the next one were filled in this turn of the ring, the others in the last)
             if (warp == 0) {
 #pragma unroll 1
                 for (int i = 0; i < CS; ++i) phase_wait(&c_full[i], i < sc.at ? sc.phase : sc.phase ^ 1, &never);
