@@ -38,8 +38,9 @@ constexpr int LP_GROUPS = 64;   // groups of threads whose maxima bound the k-th
 constexpr int LP_CAND = 1024;   // candidates of one stretch
 constexpr int LP_MAX_CLUSTER = 16;
 constexpr float LP_RAISE = 2.f;
-// References beyond this are not used: x c - R, a rounding of R by then, could be anything.
-constexpr float LP_HUGE = 16777216.f;
+// References beyond this are not used: x c - R, a rounding of R by then, could be anything. A thread that saw nothing
+// above -LP_HUGE counts nothing; what it left out is 2^-LP_CLEAR of the row's sum at most where R is LP_CLEAR above.
+constexpr float LP_HUGE = 16777216.f, LP_CLEAR = 256.f;
 constexpr float LN2 = 0.693147180559945309f;
 constexpr float FAR = -200.f;    // 2^FAR is 0 in fp32, and 0 times FAR is a number
 // Logits count as this at least in the sums: with a scale of up to 2^20 they are numbers then, and 2^t of them 0.
@@ -446,11 +447,11 @@ __global__ void __launch_bounds__(NT, LP_CTAS<NT>) k_logprobs(const Logprobs a, 
         __syncthreads();
     t = sh.total;
     // Nothing counted (R is -infinity): nothing is allowed, or every logit is far below 0 (masks of the type's
-    // lowest value in a row that allows nothing else).  Such a row, and one of huge logits, once more,
-    // against its maximum.
+    // lowest value in a row that allows nothing else).  Such a row, one whose largest logit is so near -LP_HUGE that
+    // some threads may have counted and others not, and one of huge logits, once more, against its maximum.
     float low = 0.f;
     bool none = false;
-    if (!(fabsf(t.r) <= LP_HUGE)) {
+    if (!(t.r >= -LP_HUGE + LP_CLEAR && t.r <= LP_HUGE)) {
         float m = -INFINITY;
         for (int j = tid; j < row.n_vec; j += NT) {
             float x[VE];

@@ -1,0 +1,42 @@
+"""Token operators at the ends of the ranges that their documentation allows: logits, scales and masks far out, signs of
+what is reported, gates far below 0, buffers of one row.  Bounds count roundings as in the tests of each operator."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import token_oracle as O
+from rag_kv_cache_rope_gb300 import binding as b
+from tests.pagedcase import STEP, TORCH, f64, handle, i32
+from tests.test_gpu_tokens import check_logprobs, inside, linear_bounds, logprobs, model, random_logits, rows_of, weights
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("rows,vocab", [(2, 70001), (1600, 5000), (3, 300)])
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 20])
+def test_logprobs_just_above_the_lowest_reference(rows, vocab, scale):
+    """Rows whose largest logit, times log2(e), lies a little above -2^24, so that some threads find theirs below it and
+    others not: all of them count.  (Both logits and scale are exact, so that z is an integer.)"""
+    one = 1.0 / scale
+    x = torch.empty(4, vocab, device="cuda")
+    x[0] = -11629080.0
+    x[0, vocab - 7] = -11629079.0
+    x[1] = torch.arange(vocab, device="cuda") % 3 - 11629081.0
+    for r, up in ((2, 40.0), (3, 170.0)):
+        x[r] = torch.arange(vocab, device="cuda").remainder(200) - 11629250.0
+        x[r, 5] += up
+    ids = torch.tensor([[vocab - 7, 0, 5, vocab // 2]] * 4, dtype=torch.int32, device="cuda")
+    if rows > 4:  # one CTA a row
+        got = logprobs(model("bf16"), (x * one).repeat(rows // 4, 1), ids.repeat(rows // 4, 1), 9, scale)
+        few = check_logprobs(x * one, ids, 9, scale)
+        for k, v in few.items():
+            assert torch.allclose(got[k].double(), v.repeat(rows // 4, *[1] * (v.dim() - 1)).double(), rtol=2.0 ** -20, atol=2.0 ** -16), k
+        want = O.logprobs(f64(x * one), scale, ids.cpu().numpy(), 9)
+        base = (vocab / 256 + 64) * 2.0 ** -24 * (math.log(vocab) + 8)
+        inside(f64(got["logp"][:4]), want[0], base + 8 * 2.0 ** -24 * np.abs(want[0]))
+        inside(f64(got["entropy"][:4]), want[1], 5 * base)
+        assert np.array_equal(got["top_id"][:4].cpu().numpy(), want[2])
+    else:
+        check_logprobs(x * one, ids, 9, scale)
