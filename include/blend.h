@@ -587,7 +587,7 @@ int w4_linear(blend_handle* h, const blend_w4* w4, const void* x, int64_t ld_x, 
 /* ---- log probabilities --------------------------------------------------------
  * What is read off the logits of n_rows tokens (logits device [n_rows][vocab] of `dtype`, BLEND_F32 |
  * BLEND_BF16, ld elements between rows, any alignment of its elements).  With z = scale * logits (scale:
- * 1 / temperature, above 0 and at most 2^20) and p = softmax(z), per row and in fp32:
+ * 1 / temperature, 2^-64 to 2^20) and p = softmax(z), per row and in fp32:
  *   logp[r][i] = log p of token ids[r][i], i < n_ids (ids, logp device [n_rows][n_ids]; 0 for an id
  *   below 0, which stands for no token);
  *   entropy[r] = - sum p log p (device [n_rows], or NULL);

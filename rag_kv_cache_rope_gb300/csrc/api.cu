@@ -1624,7 +1624,7 @@ extern "C" int token_logprobs(blend_handle* h, const void* logits, int64_t ld, i
     if (n_rows < 0 || n_rows > (1 << 24) || vocab < 1 || vocab > (1 << 24) || n_ids < 0 || n_ids > (1 << 24))
         return fail(h, BLEND_EINVAL, "bad sizes n_rows=%d vocab=%d n_ids=%d", n_rows, vocab, n_ids);
     if (ld < vocab || ld > (1ll << 32)) return fail(h, BLEND_EINVAL, "bad row stride %lld", (long long)ld);
-    if (!(scale > 0.f) || !(scale <= 1048576.f)) return fail(h, BLEND_EINVAL, "scale must be positive and at most 2^20");
+    if (!(scale >= 0x1p-64f && scale <= 0x1p20f)) return fail(h, BLEND_EINVAL, "scale must be 2^-64 at least and 2^20 at most");
     if (top < 0 || top > BLEND_MAX_TOP || top > vocab)
         return fail(h, BLEND_EINVAL, "top=%d outside 0..%d or above vocab", top, BLEND_MAX_TOP);
     if ((n_ids > 0 && (!ids || !logp)) || (top > 0 && !top_id)) return fail(h, BLEND_EINVAL, "NULL pointer");

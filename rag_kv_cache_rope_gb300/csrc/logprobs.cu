@@ -43,7 +43,8 @@ constexpr float LP_RAISE = 2.f;
 constexpr float LP_HUGE = 16777216.f, LP_CLEAR = 256.f;
 constexpr float LN2 = 0.693147180559945309f;
 constexpr float FAR = -200.f;    // 2^FAR is 0 in fp32, and 0 times FAR is a number
-// Logits count as this at least in the sums: with a scale of up to 2^20 they are numbers then, and 2^t of them 0.
+// Logits count as this at least in the sums: with a scale of up to 2^20 they are numbers then, and 2^t of them 0 with one
+// of 2^-64 or more (LP_LOW c is -8e10 at most, R above -2^24).
 constexpr float LP_LOW = -1e30f;
 
 using key_t = unsigned long long;

@@ -40,3 +40,20 @@ def test_logprobs_just_above_the_lowest_reference(rows, vocab, scale):
         assert np.array_equal(got["top_id"][:4].cpu().numpy(), want[2])
     else:
         check_logprobs(x * one, ids, 9, scale)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_logprobs_smallest_scale(dtype):
+    """With a scale of 2^-64 all that is allowed is alike and what is not allowed still counts for nothing, nor does what
+    lies beside a row that begins and ends within a vector; smaller scales are refused."""
+    x = random_logits(3, 5001, dtype, 80, pad=2)
+    x[0, 100:] = -math.inf
+    x[1, ::2] = torch.finfo(x.dtype).min
+    ids = torch.tensor([[0, 200], [1, 200], [5000, 7]], dtype=torch.int32, device="cuda")
+    check_logprobs(x, ids, 5, 2.0 ** -64)
+    out, before = torch.zeros(3, device="cuda"), b.blend_launch_count()
+    for scale in (2.0 ** -65, 1e-24, 1e-30, 1e-44):
+        with pytest.raises(b.BlendError) as e:
+            b.token_logprobs(model("bf16"), x, entropy=out, scale=scale)
+        assert e.value.code == b.EINVAL
+    assert b.blend_launch_count() == before
