@@ -479,11 +479,12 @@ __global__ void __launch_bounds__(NT, LP_CTAS<NT>) k_logprobs(const Logprobs a, 
         }
     }
     const float lz = log2f(t.z);
-    // log p = ln 2 (x c - R - log2 Z); where x c alone is too low for fp32, the rest does not count
+    // log p = ln 2 (x c - R - log2 Z); where that difference is too low for fp32, the rest does not count (in halves:
+    // two numbers may be further apart than the largest number, and their scaled distance be one)
     auto logp_of = [&](float x) {
         if (none) return x != x ? x : -INFINITY;
         const float d = fmaf(x - low, c, -t.r);
-        return d == -INFINITY && x > d && lz == lz ? (x - low) * a.scale : LN2 * (d - lz);
+        return d == -INFINITY && x > d && lz == lz ? (0.5f * x - 0.5f * low) * a.scale * 2.f : LN2 * (d - lz);
     };
     if (tid == 0 && a.entropy) a.entropy[r] = none ? 0.f : LN2 * (lz - t.s / t.z);
     for (int i = tid; i < a.n_ids; i += NT) {

@@ -57,3 +57,27 @@ def test_logprobs_smallest_scale(dtype):
             b.token_logprobs(model("bf16"), x, entropy=out, scale=scale)
         assert e.value.code == b.EINVAL
     assert b.blend_launch_count() == before
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [0.5, 0.55, 2.0 ** -20, 1.0, 2.0 ** 20])
+def test_logprobs_of_logits_at_both_ends_of_the_type(scale, dtype):
+    """Logits further apart than the largest number: log p is a number where the scaled distance is one."""
+    x = random_logits(3, 700, dtype, 81)
+    top = 0.9 * torch.finfo(x.dtype).max
+    x[0, 3], x[0, 4] = 0.97 * top, -0.97 * top
+    x[1, 5:9] = torch.tensor([-top, top, top / 2, -top / 3], device="cuda").to(x.dtype)
+    x[2] = -top
+    x[2, 10], x[2, 11] = top / 4, -math.inf
+    ids = torch.tensor([[3, 4, 0, 9], [5, 6, 7, 8], [0, 10, 11, 20]], dtype=torch.int32, device="cuda")
+    got = logprobs(model("bf16"), x, ids, 5, scale)
+    logp, entropy, top_id, top_logp = O.logprobs(f64(x), scale, ids.cpu().numpy(), 5)
+    assert np.array_equal(got["top_id"].cpu().numpy(), top_id)
+    # (a distance below -3.4e38 is -infinity in fp32; the distance, scale log2(e), their product and that with ln 2 round
+    # once each, ln 2 by less)
+    big = float(torch.finfo(torch.float32).max)
+    assert (np.isinf(logp) | (np.abs(logp) < 0.999 * big) | (np.abs(logp) > 1.001 * big)).all()
+    for g, w in ((got["logp"], logp), (got["top_logp"], top_logp)):
+        w = np.where(w < -big, -np.inf, w)
+        inside(f64(g), w, 2.0 ** -16 + 5 * 2.0 ** -24 * np.abs(np.where(np.isfinite(w), w, 0)))
+    inside(f64(got["entropy"]), entropy, 2.0 ** -16)
