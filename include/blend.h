@@ -597,7 +597,8 @@ int w4_linear(blend_handle* h, const blend_w4* w4, const void* x, int64_t ld_x, 
  * A logit of -infinity is a token that is not allowed: log p is -infinity and it adds nothing.  A row
  * that allows nothing has log p of -infinity everywhere and an entropy of 0.  A NaN or +infinity makes
  * its row's log p and entropy NaN; top_id is still the ranking above.  Masks may be as low as the type
- * goes, also in a row that holds nothing else.  Deterministic.  Rows of logits are read once (a few parts of
+ * goes, also in a row that holds nothing else.  A log p is never above 0 and an entropy never below.
+ * Deterministic.  Rows of logits are read once (a few parts of
  * a row twice for the ranking).
  * Device-side check: an id of vocab or more gives NaN and BLEND_EDEVICE from blend_device_status (the
  * handle is used only for that).  Errors: BLEND_EINVAL for NULL or unaligned pointers, bad sizes, dtype,

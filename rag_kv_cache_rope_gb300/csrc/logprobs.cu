@@ -480,13 +480,18 @@ __global__ void __launch_bounds__(NT, LP_CTAS<NT>) k_logprobs(const Logprobs a, 
     }
     const float lz = log2f(t.z);
     // log p = ln 2 (x c - R - log2 Z); where that difference is too low for fp32, the rest does not count (in halves:
-    // two numbers may be further apart than the largest number, and their scaled distance be one)
+    // two numbers may be further apart than the largest number, and their scaled distance be one). Roundings do not make
+    // a probability larger than 1, nor an entropy smaller than 0.
     auto logp_of = [&](float x) {
         if (none) return x != x ? x : -INFINITY;
         const float d = fmaf(x - low, c, -t.r);
-        return d == -INFINITY && x > d && lz == lz ? (0.5f * x - 0.5f * low) * a.scale * 2.f : LN2 * (d - lz);
+        const float lp = d == -INFINITY && x > d && lz == lz ? (0.5f * x - 0.5f * low) * a.scale * 2.f : LN2 * (d - lz);
+        return lp > 0.f ? 0.f : lp;  // (NaN stays)
     };
-    if (tid == 0 && a.entropy) a.entropy[r] = none ? 0.f : LN2 * (lz - t.s / t.z);
+    if (tid == 0 && a.entropy) {
+        const float e = none ? 0.f : LN2 * (lz - t.s / t.z);
+        a.entropy[r] = e < 0.f ? 0.f : e;
+    }
     for (int i = tid; i < a.n_ids; i += NT) {
         const int id = i == tid ? my_id : __ldg(a.ids + r * a.n_ids + i);
         float lp = 0.f;

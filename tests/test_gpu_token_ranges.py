@@ -81,3 +81,25 @@ def test_logprobs_of_logits_at_both_ends_of_the_type(scale, dtype):
         w = np.where(w < -big, -np.inf, w)
         inside(f64(g), w, 2.0 ** -16 + 5 * 2.0 ** -24 * np.abs(np.where(np.isfinite(w), w, 0)))
     inside(f64(got["entropy"]), entropy, 2.0 ** -16)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [1.0, 0.7, 37.0])
+@pytest.mark.parametrize("rows,vocab", [(2000, 501), (9, 20011)])
+def test_logprobs_signs(rows, vocab, scale, dtype):
+    """No log p above 0 and no entropy below it, where one token has all of the probability or nearly all; NaN stays."""
+    x = (5 * torch.randn(rows, vocab, generator=torch.Generator().manual_seed(82))).to(TORCH[dtype]).cuda()
+    alone = torch.arange(rows, device="cuda") % 3
+    at = torch.arange(vocab, device="cuda") == 77
+    x = torch.where((alone == 0)[:, None] & ~at, torch.full_like(x, -math.inf), x)
+    x = torch.where((alone == 1)[:, None] & at, torch.full_like(x, 60.0), x)
+    x[rows - 1, 5] = math.nan
+    got = logprobs(model("bf16"), x, torch.full((rows, 1), 77, dtype=torch.int32, device="cuda"), 2, scale)
+    for k in ("logp", "top_logp"):
+        assert bool((got[k][:-1] <= 0).all()), k
+    assert bool((got["entropy"][:-1] >= 0).all())
+    assert all(bool(got[k][-1].isnan().all()) for k in ("logp", "top_logp", "entropy"))
+    # what has all of the probability: 0 up to the rounding of its logit's multiple of log2(e) and of the sum
+    bound = 2.0 ** -23 * (1 + scale * x[:, 77].float().abs() * 2.0 ** -20)
+    one = alone[:-1] == 0
+    assert bool((got["logp"][:-1, 0].abs() <= bound[:-1])[one].all()) and bool((got["entropy"][:-1] <= bound[:-1])[one].all())
