@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
             for (int o = 16 * rows * rank / cluster + in_half; o < o1; o += threads) {
                 const int m = o & 15, col = o >> 4;
                 const float gate = value(0, m, col), up = value(1, m, col);
-                const float y = gate / (1.f + __expf(-gate)) * up;
+                const float y = gate / (1.f + expf(-gate)) * up;
                 const long long at = (long long)(row0 + col) * a.ld_y + unit * 16 + m;
                 if (a.y_f32) ((float*)a.y)[at] = y;
                 else ((bf16*)a.y)[at] = __float2bfloat16_rn(y);

@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                     sums(at, v);
                     sums(at + 16, up);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = v[e] / (1.f + __expf(-v[e])) * up[e];
+                    for (int e = 0; e < 8; ++e) v[e] = v[e] / (1.f + expf(-v[e])) * up[e];
                 } else
                     sums(col * TILE_M + p * 8, v);
                 const int j0 = (wt * TILE_M >> (swiglu ? 1 : 0)) + p * 8;

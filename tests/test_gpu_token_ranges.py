@@ -103,3 +103,21 @@ def test_logprobs_signs(rows, vocab, scale, dtype):
     bound = 2.0 ** -23 * (1 + scale * x[:, 77].float().abs() * 2.0 ** -20)
     one = alone[:-1] == 0
     assert bool((got["logp"][:-1, 0].abs() <= bound[:-1])[one].all()) and bool((got["entropy"][:-1] <= bound[:-1])[one].all())
+
+
+@pytest.mark.parametrize("dtype,rows,n", [("f32", 5, 32), ("f32", 64, 96), ("bf16", 7, 32), ("bf16", 30, 128), ("bf16", 60, 160), ("bf16", 300, 128)])
+def test_linear_swiglu_of_gates_far_below_zero(dtype, rows, n):
+    """Gates and up values that are their inputs: silu(gate) * up stays right to a few steps of fp32."""
+    h, k, group = model(dtype), 128, 32
+    codes = torch.full((n, k), 8)
+    gate = torch.arange(n) // 16 % 2 == 0
+    codes[gate, 0], codes[~gate, 1] = 9, 9
+    w4 = b.W4Ref(b.w4_layout(codes).cuda(), torch.ones(n, k // group, dtype=torch.bfloat16, device="cuda"), k, group)
+    x = torch.zeros(rows, k, dtype=TORCH[dtype], device="cuda")
+    x[:, 0] = torch.linspace(-85, 30, rows)
+    x[:, 1] = torch.linspace(1, 2, rows)
+    y = torch.empty(rows, n // 2, device="cuda")
+    b.w4_linear(h, w4, x, y, epi="swiglu")
+    want = (O.silu(f64(x[:, 0])) * f64(x[:, 1]))[:, None].repeat(n // 2, 1)
+    # the exponential is within two steps of 2^-23 (its documented error), sum, quotient and product within half a step each
+    inside(f64(y), want, 3.6 * 2.0 ** -23 * np.abs(want))
