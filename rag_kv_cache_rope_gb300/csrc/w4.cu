@@ -498,8 +498,12 @@ template <typename T, int G> int go(const W4Linear& a, cudaStream_t s) {
     constexpr int P = sizeof(T) == 4 ? 3 : 1;
     constexpr int SMEM_MAX = 225 * 1024;
     auto* kern = k_w4_linear<T, G>;
-    static const cudaError_t set = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
-    if (set != cudaSuccess) return BLEND_ECUDA;
+    struct Set {
+        bool ok = false;
+    };
+    static PerDevice<Set> set;
+    if (!set.get([&] { return Set{cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX) == cudaSuccess}; }))
+        return BLEND_ECUDA;
     // Input rows of a launch block, CTAs that share a weight row's inputs and chunks on their way per warp: the
     // first of them that fit in shared memory, fewer chunks before more CTAs before fewer rows.
     const int units = (a.w.n + 31) / 32;

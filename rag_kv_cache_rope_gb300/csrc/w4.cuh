@@ -1,5 +1,8 @@
 // What the kernels of products with 4-bit weights share (layout in blend.h at blend_w4).
 #pragma once
+#include <atomic>
+#include <mutex>
+
 #include "attn_tc.cuh"
 #include "paged.cuh"
 #include "tokens.cuh"
@@ -84,6 +87,29 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 }  // namespace
+
+// What launches of a kernel need once on every device: a kernel's limits belong to a device's context.  `make` fills a T
+// (with a bool `ok`) on the current device; only what succeeded is kept.  NULL where it did not.
+template <typename T> class PerDevice {
+    static constexpr int MAX = 64;
+    std::mutex lock;
+    std::atomic<bool> made[MAX] = {};
+    T of[MAX];
+
+public:
+    template <typename Make> const T* get(Make make) {
+        int d = -1;
+        if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= MAX) return nullptr;
+        if (made[d].load(std::memory_order_acquire)) return &of[d];
+        std::lock_guard<std::mutex> hold(lock);
+        if (!made[d].load(std::memory_order_relaxed)) {
+            of[d] = make();
+            if (!of[d].ok) return nullptr;
+            made[d].store(true, std::memory_order_release);
+        }
+        return &of[d];
+    }
+};
 
 // A tensor map of the codes: boxes of `rows` weight rows by one chunk, 64-byte swizzle; of the inputs: boxes of `rows` rows by
 // 64 bf16, 128-byte swizzle.  False where they cannot be described.

@@ -553,12 +553,13 @@ template <int NT, int G> int go_tile(const W4Linear& a, cudaStream_t s) {
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
-    // clusters of 1..8 CTAs that run side by side, asked for once
+    // clusters of 1..8 CTAs that run side by side, asked for once on a device
     struct Fit {
         int of[TILE_MAX_CLUSTER + 1] = {};
         bool ok = false;
     };
-    static const Fit fits = [&]() {
+    static PerDevice<Fit> fits;
+    const Fit* here = fits.get([&] {
         Fit f;
         f.ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_smem<NT>()) == cudaSuccess &&
                cudaFuncSetAttribute(kern_split, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_smem<NT>()) == cudaSuccess;
@@ -575,9 +576,9 @@ template <int NT, int G> int go_tile(const W4Linear& a, cudaStream_t s) {
             f.of[c] = n < 152 / c ? n : 152 / c;
         }
         return f;
-    }();
-    if (!fits.ok) return BLEND_ECUDA;
-    const int* fit = fits.of;
+    });
+    if (!here) return BLEND_ECUDA;
+    const int* fit = here->of;
     const int tiles = (a.w.n + TILE_M - 1) / TILE_M * ((a.rows + NT - 1) / NT);
     // (the other form takes the same room)
     // CTAs of a cluster, and whether they split its tiles: what takes the fewest chunks in a row, a tile's end counted as

@@ -1,0 +1,142 @@
+"""Launches of the products with 4-bit weights over a stand-in for the CUDA runtime, which keeps a kernel's limits per
+device as the real one does: what a launch needs is set up on every device it is made on, once, and a failure is not
+remembered.  No GPU is needed."""
+import os
+import subprocess
+
+from rag_kv_cache_rope_gb300 import build as B
+
+RUNTIME = r"""
+#include <map>
+#include <mutex>
+#include <utility>
+#include "fake.h"
+thread_local int device = 0;
+int fail_next = 0, launches = 0, sets = 0;
+static std::mutex lock;
+static std::map<std::pair<int, const void*>, int> limit;
+static int enc(void) { return 0; }
+static bool fits(const void* f, size_t bytes) {
+    std::lock_guard<std::mutex> hold(lock);
+    return bytes <= 48 * 1024 || (limit.count({device, f}) && (size_t)limit[{device, f}] >= bytes);
+}
+extern "C" {
+cudaError_t cudaGetDevice(int* d) { *d = device; return cudaSuccess; }
+cudaError_t cudaGetLastError(void) { return cudaSuccess; }
+cudaError_t cudaFuncSetAttribute(const void* f, enum cudaFuncAttribute a, int v) {
+    std::lock_guard<std::mutex> hold(lock);
+    if (fail_next > 0) { --fail_next; return cudaErrorMemoryAllocation; }
+    if (a == cudaFuncAttributeMaxDynamicSharedMemorySize) { limit[{device, f}] = v; ++sets; }
+    return cudaSuccess;
+}
+cudaError_t cudaOccupancyMaxActiveClusters(int* n, const void* f, const cudaLaunchConfig_t* c) {
+    if (!fits(f, c->dynamicSmemBytes)) return cudaErrorInvalidValue;
+    *n = 152 / (int)c->attrs[0].val.clusterDim.x;
+    return cudaSuccess;
+}
+cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const void* f, void**) {
+    if (!fits(f, c->dynamicSmemBytes)) return cudaErrorInvalidValue;
+    __atomic_add_fetch(&launches, 1, __ATOMIC_RELAXED);
+    return cudaSuccess;
+}
+cudaError_t cudaGetDriverEntryPointByVersion(const char*, void** p, unsigned int, unsigned long long,
+                                             enum cudaDriverEntryPointQueryResult* r) {
+    *p = (void*)enc;
+    *r = cudaDriverEntryPointSuccess;
+    return cudaSuccess;
+}
+void** __cudaRegisterFatBinary(void*) { static void* h; return &h; }
+void __cudaRegisterFatBinaryEnd(void**) {}
+void __cudaUnregisterFatBinary(void**) {}
+void __cudaRegisterFunction(void**, const char*, char*, const char*, int, void*, void*, void*, void*, int*) {}
+char __cudaInitModule(void**) { return 0; }
+unsigned __cudaPushCallConfiguration(void) { return 1; }
+cudaError_t __cudaPopCallConfiguration(void) { return cudaErrorUnknown; }
+cudaError_t __cudaGetKernel(void) { return cudaErrorUnknown; }
+cudaError_t __cudaLaunchKernel(void) { return cudaErrorUnknown; }
+}
+"""
+
+FAKE_H = r"""
+#pragma once
+#include <cuda_runtime_api.h>
+extern thread_local int device;
+extern int fail_next, launches, sets;
+"""
+
+CALLS = r"""
+#include <stdio.h>
+#include <thread>
+#include <vector>
+#include "tokens.cuh"
+#include "fake.h"
+namespace blend {
+void note_launch(int) {}
+}
+using namespace blend;
+static int call(int rows, int group, int dtype = BLEND_BF16) {
+    static char mem[64] __attribute__((aligned(64)));
+    W4Linear a = {};
+    a.w.codes = (const uint4*)mem;
+    a.w.scale = (const bf16*)mem;
+    a.w.n = 5120;
+    a.w.k = 8192;
+    a.w.group = group;
+    a.w.chunks = 64;
+    a.x = a.y = mem;
+    a.ld_x = 8192;
+    a.ld_y = 5120;
+    a.rows = rows;
+    a.y_f32 = 1;
+    a.tc = true;
+    return launch_w4_linear(dtype, a, 0);
+}
+#define WANT(x) do { if (!(x)) { printf("%d: " #x "\n", __LINE__); return 1; } } while (0)
+int main(void) {
+    for (int d = 0; d < 3; ++d) {
+        device = d;
+        for (int rows : {1, 8, 30, 60, 500}) {
+            WANT(call(rows, 128) == BLEND_OK);
+            const int before = sets;
+            WANT(call(rows, 128) == BLEND_OK && sets == before);
+        }
+        WANT(call(3, 128, BLEND_F32) == BLEND_OK);
+    }
+    WANT(launches == 3 * 11);
+    // a failure is that call's alone
+    for (int rows : {2, 500}) {
+        device = 1;
+        fail_next = 1;
+        WANT(call(rows, 64) == BLEND_ECUDA);
+        WANT(call(rows, 64) == BLEND_OK);
+    }
+    // first calls of several threads on several devices at once
+    std::vector<std::thread> t;
+    int bad[8] = {};
+    for (int i = 0; i < 8; ++i)
+        t.emplace_back([&bad, i] {
+            device = i % 4;
+            for (int rows : {1, 30, 60, 500}) bad[i] += call(rows, 32) != BLEND_OK;
+        });
+    for (auto& x : t) x.join();
+    for (int b : bad) WANT(b == 0);
+    return 0;
+}
+"""
+
+
+def test_launches_on_every_device_and_after_a_failure(tmp_path):
+    B.build()
+    (tmp_path / "fake.h").write_text(FAKE_H)
+    (tmp_path / "runtime.cpp").write_text(RUNTIME)
+    (tmp_path / "calls.cu").write_text(CALLS)
+    inc = ["-I", str(tmp_path), "-I", B.CSRC, "-I", os.path.join(B.ROOT, "include"),
+           "-I", os.path.join(os.path.dirname(os.path.dirname(B.nvcc())), "include")]
+    objs = []
+    for cc, name in ((["g++"], "runtime.cpp"), ([B.nvcc(), *B.ARCH], "calls.cu")):
+        objs.append(str(tmp_path / (name + ".o")))
+        subprocess.run([*cc, "-std=c++17", *inc, "-c", str(tmp_path / name), "-o", objs[-1]], check=True)
+    exe = str(tmp_path / "probe")
+    subprocess.run(["g++", *objs, os.path.join(B.BUILD, "w4.cu.o"), os.path.join(B.BUILD, "w4_tile.cu.o"), "-o", exe, "-lpthread"], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0, r.stdout + r.stderr
