@@ -20,6 +20,8 @@
  *     PyTorch).  The library never frees or reallocates them.  "host" in a comment
  *     marks a host pointer.  Only the workspace given to blend_init is used as
  *     scratch by the handle; it must stay allocated until blend_destroy.
+ *   - A handle belongs to the device that is current at blend_init (its workspace and error
+ *     word lie there): calls with it are made with that device current, on its memory and streams.
  *   - All work is enqueued on the caller's stream (`stream` is a cudaStream_t;
  *     NULL is the legacy default stream).  Calls do not synchronise the device.
  *     Counts produced on the device (set sizes) stay on the device.

@@ -208,11 +208,12 @@ def _check(rc: int, h=None):
 class Handle:
     """A libblend handle plus the tensors it points into (kept alive here)."""
 
-    def __init__(self, ptr, cfg: ModelCfg, lim: Limits, keep):
+    def __init__(self, ptr, cfg: ModelCfg, lim: Limits, keep, index: int = 0):
         self.ptr = ptr
         self.cfg = cfg
         self.lim = lim
         self._keep = keep
+        self.index = index  # the GPU that holds its workspace and error word
 
     def __del__(self):
         if getattr(self, "ptr", None) and _lib is not None:
@@ -243,7 +244,7 @@ def blend_init(cfg: ModelCfg, packed: dict, lim: Limits, workspace: Optional[tor
     rc = lib().blend_init(C.byref(cfg), C.byref(w), C.byref(lim), _ptr(workspace), workspace.numel(),
                           _stream(stream), C.byref(out))
     _check(rc)
-    return Handle(out, cfg, lim, (packed, workspace))
+    return Handle(out, cfg, lim, (packed, workspace), workspace.get_device())
 
 
 def blend_destroy(h: Handle):
@@ -599,10 +600,12 @@ def paged_attention(h: Handle, pages: PagesRef, q, q_start, kv_len, max_q, out, 
 
 # ---------------------------------------------------------------- behind the cache: tokens
 # (Called once or more per layer and token, as the paged calls: each property is read once.)
-def _token_stream(index: int, stream):
-    """The call's stream: the tensors' GPU must be the current one, and the stream's."""
+def _token_stream(h: Handle, index: int, stream):
+    """The call's stream: the tensors' GPU must be the handle's, the current one, and the stream's."""
     if index < 0:
         raise ValueError("the tensors are not on a GPU")
+    if h.index != index:
+        raise ValueError(f"the tensors are on cuda:{index}, the handle on cuda:{h.index}")
     if torch.cuda.current_device() != index or (stream is not None and stream.device_index != index):
         raise ValueError(f"the tensors are on cuda:{index}: make it the current device and use a stream of it")
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
@@ -659,7 +662,7 @@ def w4_layout(codes: torch.Tensor) -> torch.Tensor:
 
 def w4_pack(h: Handle, w: torch.Tensor, w4: W4Ref, stream=None):
     """w: [n][k] of the model's dtype (rows at any stride of 16 bytes)."""
-    s = _token_stream(w4.index, stream)
+    s = _token_stream(h, w4.index, stream)
     ld = _matrix(w, "w", _model_dtype(h), w4.index, w4.n, w4.k)
     rc = lib().w4_pack(h.ptr, w4.ref, w.data_ptr(), ld, s)
     if rc:
@@ -668,7 +671,7 @@ def w4_pack(h: Handle, w: torch.Tensor, w4: W4Ref, stream=None):
 
 def w4_unpack(h: Handle, w4: W4Ref, out: torch.Tensor, stream=None):
     """out: [n][k] of the model's dtype (rows at any stride of 16 bytes)."""
-    s = _token_stream(w4.index, stream)
+    s = _token_stream(h, w4.index, stream)
     ld = _matrix(out, "out", _model_dtype(h), w4.index, w4.n, w4.k)
     rc = lib().w4_unpack(h.ptr, w4.ref, out.data_ptr(), ld, s)
     if rc:
@@ -678,7 +681,7 @@ def w4_unpack(h: Handle, w4: W4Ref, out: torch.Tensor, stream=None):
 def w4_linear(h: Handle, w4: W4Ref, x: torch.Tensor, y: torch.Tensor, epi: str = "store", stream=None):
     """x: [rows][k] of the model's dtype (rows at any stride of 16 bytes); y: [rows][n] ([n / 2] for
     "swiglu"), fp32 or bf16 (fp32 for "add"), rows at any stride."""
-    s = _token_stream(w4.index, stream)
+    s = _token_stream(h, w4.index, stream)
     code = W4_EPIS.get(epi)
     if code is None:
         raise ValueError(f"epi must be one of {', '.join(W4_EPIS)}")
@@ -701,7 +704,7 @@ def token_logprobs(h: Handle, logits: torch.Tensor, ids=None, logp=None, entropy
     """logits: [rows][vocab], fp32 or bf16, rows at any stride; ids int32 and logp fp32 [rows][n_ids]; entropy
     fp32 [rows]; top_id int32 and top_logp fp32 [rows][top].  What is None is left out."""
     dt, index = logits.dtype, logits.get_device()
-    s = _token_stream(index, stream)
+    s = _token_stream(h, index, stream)
     if dt is not torch.float32 and dt is not torch.bfloat16:
         raise ValueError("logits must be fp32 or bf16")
     if logits.dim() != 2:
@@ -779,7 +782,7 @@ def rope_rows(h: Handle, rope: Rope, k, k_out, rot, n, max_n, q=None, q_out=None
     of 16 bytes); q, q_out the same with the model's query heads; rot int32 per row; n a device int32 count of
     at most max_n rows.  An output may be its own input."""
     index = k.get_device()
-    s = _token_stream(index, stream)
+    s = _token_stream(h, index, stream)
     cfg, dt = h.cfg, _model_dtype(h)
     d = cfg.head_dim
     if (q is None) != (q_out is None):

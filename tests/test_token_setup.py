@@ -3,7 +3,12 @@ device as the real one does: what a launch needs is set up on every device it is
 remembered.  No GPU is needed."""
 import os
 import subprocess
+import types
 
+import pytest
+import torch
+
+from rag_kv_cache_rope_gb300 import binding as b
 from rag_kv_cache_rope_gb300 import build as B
 
 RUNTIME = r"""
@@ -140,3 +145,30 @@ def test_launches_on_every_device_and_after_a_failure(tmp_path):
     subprocess.run(["g++", *objs, os.path.join(B.BUILD, "w4.cu.o"), os.path.join(B.BUILD, "w4_tile.cu.o"), "-o", exe, "-lpthread"], check=True)
     r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+class Tensor(torch.Tensor):
+    """A tensor that says that it is on the second GPU."""
+
+    def get_device(self):
+        return 1
+
+
+def test_tensors_on_another_gpu_than_the_handle_are_refused(monkeypatch):
+    """A handle's error word lies on its own GPU, so a kernel on another must not get it."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0, raising=False)
+    h = types.SimpleNamespace(ptr=None, index=0, cfg=types.SimpleNamespace(dtype=b.BF16, head_dim=128, n_kv_heads=2, n_q_heads=4))
+
+    def at(t):
+        return t.as_subclass(Tensor)
+
+    w4 = b.W4Ref(at(torch.zeros(32, 64, dtype=torch.uint8)), torch.zeros(32, 1, dtype=torch.bfloat16), 128)
+    x, y = at(torch.zeros(1, 128, dtype=torch.bfloat16)), at(torch.zeros(1, 32))
+    k, one = at(torch.zeros(1, 2, 128, dtype=torch.bfloat16)), at(torch.ones(1, dtype=torch.int32))
+    w = at(torch.zeros(32, 128, dtype=torch.bfloat16))
+    for call in (lambda: b.w4_linear(h, w4, x, y), lambda: b.w4_pack(h, w, w4), lambda: b.w4_unpack(h, w4, w),
+                 lambda: b.token_logprobs(h, y, entropy=at(torch.zeros(1))),
+                 lambda: b.rope_rows(h, b.rope_desc(1e4, 128), k, k, one, one, 1)):
+        with pytest.raises(ValueError, match="the handle on cuda:0"):
+            call()
