@@ -1534,16 +1534,6 @@ int view_w4(blend_handle* h, const blend_w4* w, W4View* v) {
     v->chunks = (w->k + 127) / 128;
     return BLEND_OK;
 }
-// Do rows [layers][n][width] at a and b meet?  (Bytes; where both step alike, rows that lie side by side in
-// one buffer do not, although their ranges do.)
-bool rows_meet(const void* pa, long long row_a, long long layer_a, long long layers_a, long long wa, const void* pb,
-               long long row_b, long long layer_b, long long layers_b, long long wb, long long n) {
-    if (!overlap(pa, (layers_a - 1) * layer_a + (n - 1) * row_a + wa, pb, (layers_b - 1) * layer_b + (n - 1) * row_b + wb))
-        return false;
-    if (row_a != row_b || (layers_a > 1 && layer_a % row_a) || (layers_b > 1 && layer_b % row_b)) return true;
-    const long long d = (((long long)((intptr_t)pb - (intptr_t)pa)) % row_a + row_a) % row_a;  // b's place in a's rows
-    return d < wa || d + wb > row_a;
-}
 // Distance between rows of `width` elements of `dtype`: at least one row, a multiple of 16 bytes.
 bool stride16_ok(int dtype, long long ld, long long width) {
     return ld >= width && ld % (long long)(16 / elem_size(dtype)) == 0 && ld <= (1ll << 32);

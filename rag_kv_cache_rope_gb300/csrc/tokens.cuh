@@ -5,6 +5,30 @@
 
 namespace blend {
 
+// Do rows [layers][n][width] at pa and pb meet?  (Bytes.)  Exact where both step alike, so that rows which lie side by side in one
+// buffer do not, although their ranges do; rows that step differently count as meeting where their ranges meet.  A
+// step that a tensor does not take (one row, one layer) does not matter.
+inline bool rows_meet(const void* pa, long long row_a, long long layer_a, long long layers_a, long long wa, const void* pb,
+                      long long row_b, long long layer_b, long long layers_b, long long wb, long long n) {
+    const long long d = (long long)((intptr_t)pb - (intptr_t)pa);  // b's place from a's
+    const long long end_a = (layers_a - 1) * (layers_a > 1 ? layer_a : 0) + (n - 1) * row_a + wa;
+    const long long end_b = (layers_b - 1) * (layers_b > 1 ? layer_b : 0) + (n - 1) * row_b + wb;
+    if (d >= end_a || -d >= end_b) return false;
+    if ((n > 1 && row_a != row_b) || (layers_a > 1 && layers_b > 1 && layer_a != layer_b)) return true;
+    const long long layer = layers_a > 1 ? layer_a : layers_b > 1 ? layer_b : 0;
+    // a row of b and one of a, l layers and i rows apart: b's begins at + i row_a behind a's
+    for (long long l = 1 - layers_a; l < layers_b; ++l) {
+        const long long at = d + l * layer, end = -wb - at;
+        long long i = 0;  // the first step with which b's row ends behind a's start
+        if (n > 1) {
+            i = end / row_a - (end % row_a < 0) + 1;
+            if (i < 1 - n) i = 1 - n;
+        }
+        if (i < n && at + i * row_a < wa && at + i * row_a > -wb) return true;
+    }
+    return false;
+}
+
 // ---- 4-bit weights (w4.cu); layout in blend.h at blend_w4
 struct W4View {
     const uint4* codes;  // [n][4 chunks] sixteen-byte pieces

@@ -121,3 +121,35 @@ def test_linear_swiglu_of_gates_far_below_zero(dtype, rows, n):
     want = (O.silu(f64(x[:, 0])) * f64(x[:, 1]))[:, None].repeat(n // 2, 1)
     # the exponential is within two steps of 2^-23 (its documented error), sum, quotient and product within half a step each
     inside(f64(y), want, 3.6 * 2.0 ** -23 * np.abs(want))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,pad", [(1, 0), (1, 3), (2, 0), (5, 3)])
+def test_rope_rows_in_place_in_a_fused_buffer_of_layers(rows, pad, dtype):
+    """Queries and keys side by side in [layers][rows][heads][head dim], a single row of each layer among them, and layers
+    that do not lie a whole number of rows apart."""
+    h = model(dtype, 4, 2, 128)
+    L, heads, d = 3, 8, 128
+    step = rows * heads * d + pad * 16
+    g = torch.Generator().manual_seed(83)
+    flat = torch.randn(L * step, generator=g).to(TORCH[dtype]).cuda()
+    buf = torch.as_strided(flat, (L, rows, heads, d), (step, heads * d, d, 1))
+    first = buf.clone()
+    rot = i32([1000 * i + 7 for i in range(rows)])
+    rope = b.rope_desc(5e5, 64, "pairs")
+    q, k = buf[:, :, :4], buf[:, :, 4:6]
+    b.rope_rows(h, rope, k, k, rot, i32([rows]), rows, q=q, q_out=q)
+    want = torch.empty_like(first)
+    for i in range(L):
+        part = first[i].contiguous()
+        b.rope_rows(h, rope, part[:, 4:6], want[i, :, 4:6], rot, i32([rows]), rows, q=part[:, :4], q_out=want[i, :, :4])
+    want[:, :, 6:] = first[:, :, 6:]
+    assert torch.equal(buf, want) and not torch.equal(buf[:, :, :6], first[:, :, :6])
+    # what does meet is refused still
+    before = b.blend_launch_count()
+    for bad in (buf[:, :, 3:5], buf[:, :, 5:7]):
+        with pytest.raises(b.BlendError) as e:
+            b.rope_rows(h, rope, k, bad, rot, i32([rows]), rows)
+        assert e.value.code == b.EINVAL
+    assert b.blend_launch_count() == before
+    b.blend_device_status(h)

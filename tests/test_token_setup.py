@@ -1,6 +1,6 @@
-"""Launches of the products with 4-bit weights over a stand-in for the CUDA runtime, which keeps a kernel's limits per
-device as the real one does: what a launch needs is set up on every device it is made on, once, and a failure is not
-remembered.  No GPU is needed."""
+"""Host side of the token operators.  Launches of the products with 4-bit weights over a stand-in for the CUDA runtime,
+which keeps a kernel's limits per device as the real one does: what a launch needs is set up on every device it is made
+on, once, and a failure is not remembered.  Tensors of another GPU.  Which rows of two tensors meet.  No GPU is needed."""
 import os
 import subprocess
 import types
@@ -172,3 +172,60 @@ def test_tensors_on_another_gpu_than_the_handle_are_refused(monkeypatch):
                  lambda: b.rope_rows(h, b.rope_desc(1e4, 128), k, k, one, one, 1)):
         with pytest.raises(ValueError, match="the handle on cuda:0"):
             call()
+
+
+MEET = r"""
+#include <stdio.h>
+#include <stdlib.h>
+#include "tokens.cuh"
+static long long r(long long lo, long long hi) { return lo + rand() % (hi - lo + 1); }
+int main(void) {
+    srand(7);
+    static char a[4096], b[4096];
+    long long met = 0, apart = 0, wide = 0;
+    for (int t = 0; t < 400000; ++t) {
+        const long long n = r(1, 5), wa = r(1, 9), wb = r(1, 9), la = r(1, 4), lb = r(1, 4);
+        const bool alike = t % 8 != 0;
+        long long row_a = r(9, 40), row_b = alike ? row_a : r(9, 40);
+        long long layer_a = r(9, 120), layer_b = alike ? layer_a : r(9, 120);
+        if (n == 1 && t % 2) row_b = r(9, 40);       // a step that is not taken
+        if (la == 1 && t % 3) layer_a = r(0, 400) - 200;
+        if (lb == 1 && t % 3 == 1) layer_b = r(0, 400) - 200;
+        const long long pa = r(0, 300), pb = r(0, 300);
+        bool want = false;
+        for (long long l = 0; l < la; ++l)
+            for (long long i = 0; i < n; ++i)
+                for (long long m = 0; m < lb; ++m)
+                    for (long long j = 0; j < n; ++j) {
+                        const long long x = pa + (la > 1 ? l * layer_a : 0) + i * row_a, y = pb + (lb > 1 ? m * layer_b : 0) + j * row_b;
+                        want |= x < y + wb && y < x + wa;
+                    }
+        const bool got = blend::rows_meet(a + pa, row_a, layer_a, la, wa, a + pb, row_b, layer_b, lb, wb, n);
+        const bool steps = (n == 1 || row_a == row_b) && (la == 1 || lb == 1 || layer_a == layer_b);
+        if (steps ? got != want : want && !got) {
+            printf("n %lld rows %lld %lld layers %lld x %lld, %lld x %lld at %lld %lld: %d\n", n, row_a, row_b, la, layer_a, lb, layer_b, pa, pb, got);
+            return 1;
+        }
+        met += want;
+        apart += !want && steps;
+        wide += got && !want;
+    }
+    // many layers of long rows, far apart in one buffer, and the same layers
+    char* p = 0;
+    const long long row = 3ll << 20, layer = row << 18;
+    if (blend::rows_meet(p, row, layer, 1 << 16, 4096, p + 4096, row, layer, 1 << 16, 4096, 1 << 18)) return 2;
+    if (!blend::rows_meet(p, row, layer, 1 << 16, 4096, p + 4080, row, layer, 1 << 16, 4096, 1 << 18)) return 3;
+    printf("%lld %lld %lld\n", met, apart, wide);
+    return met > 1000 && apart > 1000 && (b[0] == 0) ? 0 : 4;
+}
+"""
+
+
+def test_which_rows_meet(tmp_path):
+    """Against every pair of rows, for small tensors of any steps."""
+    src, exe = tmp_path / "probe.cu", tmp_path / "probe"
+    src.write_text(MEET)
+    subprocess.run([B.nvcc(), *B.ARCH, "-std=c++17", "-I", B.CSRC, "-I", os.path.join(B.ROOT, "include"), str(src), "-o", str(exe)],
+                   check=True, capture_output=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, (r.returncode, r.stdout)
