@@ -650,8 +650,8 @@ typedef struct {
  * bit; fp32 arithmetic, one rounding.
  * Device-side checks (BLEND_EDEVICE from blend_device_status): a count outside 0..max_n is clamped; a row
  * whose rot is out of range is left alone.  Errors: BLEND_EINVAL for NULL or not 16-byte aligned pointers,
- * bad strides, sizes or blend_rope, a dst that meets a src (unless it is its own) or the other dst (nothing
- * is launched). */
+ * bad strides, sizes or blend_rope, a dst that meets a src (unless it is its own), the other dst, rot or n
+ * (nothing is launched). */
 int rope_rows(blend_handle* h, const blend_rope* rope, const blend_rope_rows* parts, int32_t n_parts,
               const int32_t* rot, const int32_t* n, int32_t max_n, void* stream);
 

@@ -1723,6 +1723,9 @@ extern "C" int rope_rows(blend_handle* h, const blend_rope* rope, const blend_ro
         const bool stacked = d.n_layers == 1 || d.dst_layer >= (max_n - 1ll) * d.dst_row + width;
         const bool woven = d.n_layers == 1 || d.dst_row >= (d.n_layers - 1ll) * d.dst_layer + width;
         if (!stacked && !woven) return fail(h, BLEND_EINVAL, "layers of dst overlap");
+        if (bytes_meet_rows(rot, 4ll * max_n, d.dst, d.dst_row * es, d.dst_layer * es, d.n_layers, dw, max_n) ||
+            bytes_meet_rows(n, 4, d.dst, d.dst_row * es, d.dst_layer * es, d.n_layers, dw, max_n))
+            return fail(h, BLEND_EINVAL, "dst overlaps rot or n");
         for (int j = 0; j < n_parts; ++j) {
             const blend_rope_rows& s = parts[j];
             const long long sw = (long long)s.heads * c.head_dim * es;

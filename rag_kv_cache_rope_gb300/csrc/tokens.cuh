@@ -29,6 +29,21 @@ inline bool rows_meet(const void* pa, long long row_a, long long layer_a, long l
     return false;
 }
 
+// Do `bytes` bytes at p meet rows [layers][n][width] at pa?  (Exact.)
+inline bool bytes_meet_rows(const void* p, long long bytes, const void* pa, long long row, long long layer, long long layers,
+                            long long width, long long n) {
+    const long long d = (long long)((intptr_t)p - (intptr_t)pa);
+    if (d >= (layers - 1) * (layers > 1 ? layer : 0) + (n - 1) * row + width || d + bytes <= 0) return false;
+    for (long long l = 0; l < layers; ++l) {
+        const long long at = d - (layers > 1 ? l * layer : 0), end = at - width;
+        // the first row that ends behind p
+        long long i = end / row - (end % row < 0) + 1;
+        if (i < 0) i = 0;
+        if (i < n && i * row < at + bytes) return true;
+    }
+    return false;
+}
+
 // ---- 4-bit weights (w4.cu); layout in blend.h at blend_w4
 struct W4View {
     const uint4* codes;  // [n][4 chunks] sixteen-byte pieces

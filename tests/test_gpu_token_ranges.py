@@ -153,3 +153,29 @@ def test_rope_rows_in_place_in_a_fused_buffer_of_layers(rows, pad, dtype):
         assert e.value.code == b.EINVAL
     assert b.blend_launch_count() == before
     b.blend_device_status(h)
+
+
+def test_rope_rows_keep_their_outputs_off_shifts_and_count():
+    """Shifts and count inside an output's rows are refused; between its rows they are not touched."""
+    h = model("bf16", 4, 2, 128)
+    rope, rows, width = b.rope_desc(1e4, 128), 4, 2 * 128
+    room = torch.full((rows, width + 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    words = room.view(torch.int32).view(rows, -1)
+    out = room[:, :width].view(rows, 2, 128)
+    k = torch.randn(rows, 2, 128, generator=torch.Generator().manual_seed(84)).bfloat16().cuda()
+    rot, n = i32([3, 4, 5, 6]), i32([rows])
+    before = b.blend_launch_count()
+    for bad in (dict(rot=words[0, 10:14]), dict(rot=words[0, 125:129]), dict(rot=words[1, 158:160].as_strided((4,), (1,))),
+                dict(n=words[3, 127:128])):
+        with pytest.raises(b.BlendError) as e:
+            b.rope_rows(h, rope, k, out, bad.get("rot", rot), bad.get("n", n), rows)
+        assert e.value.code == b.EINVAL and "rot or n" in str(e.value)
+    assert b.blend_launch_count() == before and bool((room == 5).all())
+    inside_gap, count = words[1, 130:134], words[2, 140:141]
+    inside_gap.copy_(rot)
+    count.copy_(n)
+    b.rope_rows(h, rope, k, out, inside_gap, count, rows)
+    want = torch.empty_like(k)
+    b.rope_rows(h, rope, k, want, rot, n, rows)
+    assert torch.equal(out, want) and torch.equal(inside_gap, rot) and torch.equal(count, n)
+    b.blend_device_status(h)

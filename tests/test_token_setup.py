@@ -206,6 +206,16 @@ int main(void) {
             printf("n %lld rows %lld %lld layers %lld x %lld, %lld x %lld at %lld %lld: %d\n", n, row_a, row_b, la, layer_a, lb, layer_b, pa, pb, got);
             return 1;
         }
+        bool in = false;  // b's first row alone
+        for (long long l = 0; l < la; ++l)
+            for (long long i = 0; i < n; ++i) {
+                const long long x = pa + (la > 1 ? l * layer_a : 0) + i * row_a;
+                in |= x < pb + wb && pb < x + wa;
+            }
+        if (blend::bytes_meet_rows(b + pb, wb, b + pa, row_a, layer_a, la, wa, n) != in) {
+            printf("%lld bytes at %lld, n %lld row %lld layers %lld x %lld width %lld at %lld: %d\\n", wb, pb, n, row_a, la, layer_a, wa, pa, !in);
+            return 5;
+        }
         met += want;
         apart += !want && steps;
         wide += got && !want;
