@@ -600,8 +600,9 @@ int w4_linear(blend_handle* h, const blend_w4* w4, const void* x, int64_t ld_x, 
  * that allows nothing has log p of -infinity everywhere and an entropy of 0.  A NaN or +infinity makes
  * its row's log p and entropy NaN; top_id is still the ranking above.  Masks may be as low as the type
  * goes, also in a row that holds nothing else.  A log p is never above 0 and an entropy never below.
- * Deterministic.  Rows of logits are read once (a few parts of
- * a row twice for the ranking).
+ * Deterministic.  Rows of logits are read once, a few parts of a row twice for
+ * the ranking; a row once more where the ranking ends among masks (one value of most logits, or values below
+ * -1e30, where each of them costs a reading), and twice more where its largest z is beyond +-1.16e7.
  * Device-side check: an id of vocab or more gives NaN and BLEND_EDEVICE from blend_device_status (the
  * handle is used only for that).  Errors: BLEND_EINVAL for NULL or unaligned pointers, bad sizes, dtype,
  * scale or top, an output over the logits, the ids or another output (nothing is launched). */

@@ -49,12 +49,12 @@ constexpr float LP_LOW = -1e30f;
 
 using key_t = unsigned long long;
 
-// Ranking key: value (order-preserving bits, -0 as +0, NaN lowest), then lower index first.
-__device__ __forceinline__ key_t rank_key(float x, int idx) {
+// Ranking key: value (order-preserving bits, -0 as +0, NaN 0), then lower index first.
+__device__ __forceinline__ uint32_t value_bits(float x) {
     const uint32_t b = __float_as_uint(x + 0.f);
-    const uint32_t o = x != x ? 0u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
-    return ((key_t)o << 32) | (uint32_t)~idx;
+    return x != x ? 0u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
+__device__ __forceinline__ key_t rank_key(float x, int idx) { return ((key_t)value_bits(x) << 32) | (uint32_t)~idx; }
 __device__ __forceinline__ float key_value(key_t k) {
     const uint32_t o = (uint32_t)(k >> 32);
     if (o == 0) return __int_as_float(0x7fc00000);
@@ -223,6 +223,20 @@ __device__ void rank_stretch(const Row<T>& row, int v0, int v1, int top, float m
     // threads that hold a candidate
     if (my_max >= bound) sh.active[atomicAdd(&sh.n_active, 1)] = tid;
     __syncthreads();
+    // Where most threads reach the bound, it is one value of many logits (a mask: fewer than `top` groups hold an allowed
+    // token). Then only what is above it, or above the masks, is collected, and the rest in order of its index: 2047 x 32003
+    // bf16, three tokens allowed, 5 alternatives 37 us under masks of -1e9 and 76 under -infinity; 189 with all of the masked
+    // as candidates.
+    const bool masked = sh.n_active > NT / 2;
+    float least = bound;
+    if (masked) {
+        least = nextafterf(fmaxf(bound, LP_LOW), INFINITY);
+        __syncthreads();
+        if (tid == 0) sh.n_active = 0;
+        __syncthreads();
+        if (my_max >= least) sh.active[atomicAdd(&sh.n_active, 1)] = tid;
+        __syncthreads();
+    }
     const int n_active = sh.n_active;
     const int w0 = max(v0, 1), w1 = min(v1, row.n_vec - 1);
     const int each = (max(w1 - w0, 0) + NT - 1) / NT;  // inner vectors of a thread
@@ -240,7 +254,7 @@ __device__ void rank_stretch(const Row<T>& row, int v0, int v1, int top, float m
             row.load(j, x);
 #pragma unroll
             for (int e = 0; e < VE; ++e)
-                if (x[e] >= bound && row.holds(j, e)) {
+                if (x[e] >= least && row.holds(j, e)) {
                     const int at = atomicAdd(&sh.n_cand, 1);
                     if (at < LP_CAND) sh.cand[at] = rank_key(x[e], row.index(j, e));
                     else sh.overflow = 1;
@@ -287,6 +301,32 @@ __device__ void rank_stretch(const Row<T>& row, int v0, int v1, int top, float m
         const int until = sh.n_cand + BLEND_MAX_TOP;
         __syncthreads();
         take_in_order(row, v0, v1, until, sh, [&](float x) { return x == bound; });
+    }
+    if (masked && !sh.overflow && sh.n_cand < top) {
+        __syncthreads();
+        if (bound > LP_LOW) take_in_order(row, v0, v1, top, sh, [&](float x) { return x == bound; });
+        // masks: one value after the other, one or two as a rule
+        uint32_t level = value_bits(LP_LOW) + 1u;
+        while (bound <= LP_LOW && sh.n_cand < top) {
+            uint32_t next = 0;
+            for (int j = v0 + tid; j < v1; j += NT) {
+                float x[VE];
+                row.load(j, x);
+#pragma unroll
+                for (int i = 0; i < VE; ++i) {
+                    const uint32_t o = value_bits(x[i]);
+                    if (row.holds(j, i) && o < level && o > next) next = o;
+                }
+            }
+            next = __reduce_max_sync(0xffffffffu, next);
+            if (lane == 0) sh.warp_tot[warp] = (int)next;
+            __syncthreads();
+            for (int w = 0; w < NT / 32; ++w) next = max(next, (uint32_t)sh.warp_tot[w]);
+            __syncthreads();
+            if (next == 0) break;
+            level = next;
+            take_in_order(row, v0, v1, top, sh, [&](float x) { return value_bits(x) == level; });
+        }
     }
     // fewer numbers than asked for: NaN in order
     if (sh.n_cand < top) {

@@ -179,3 +179,61 @@ def test_rope_rows_keep_their_outputs_off_shifts_and_count():
     b.rope_rows(h, rope, k, want, rot, n, rows)
     assert torch.equal(out, want) and torch.equal(inside_gap, rot) and torch.equal(count, n)
     b.blend_device_status(h)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,vocab,top", [(16, 96, 20), (16, 5003, 20), (16, 70001, 32), (1600, 9001, 8)])
+def test_logprobs_strict_masks(rows, vocab, top, dtype):
+    """Fewer allowed tokens than alternatives, under masks of every kind: the allowed first, then the masked by value and
+    index, NaN last."""
+    low = float(torch.finfo(TORCH[dtype]).min)
+    x = random_logits(16, vocab, dtype, 85)
+    at = torch.arange(vocab, device="cuda")
+    few = (at == 5) | (at == vocab // 2) | (at == vocab - 1)
+    for r, mask in enumerate((-math.inf, low, -1e9, -3e4, -1.5e30, -1e30, low / 2)):
+        x[r].masked_fill_(~few, mask)
+    x[7] = torch.where(few, x[7].float(), torch.where(at % 2 == 0, low, -math.inf)).to(x.dtype)
+    x[8] = torch.where(few, x[8].float(), torch.where(at % 500 == 7, -2e30, torch.where(at % 3 == 1, -math.inf, -3e30))).to(x.dtype)
+    x[9] = -math.inf
+    x[9, 0] = math.nan
+    x[10] = math.nan
+    x[10, vocab - 1], x[10, 3], x[10, 4] = 2.0, low, -math.inf
+    x[11] = 0.0
+    x[11, 40:43] = 1.0
+    x[12] = torch.where(at % 64 == 3, torch.full_like(x[12], 4.0), torch.full_like(x[12], -math.inf))
+    x[13] = torch.where(at < vocab // 3, x[13].float(), -math.inf).to(x.dtype)
+    x[14] = low
+    x[14, vocab - 2] = 0.0
+    x[15] = (-1e30 * (1 + at % 90)).to(x.dtype)
+    ids = torch.tensor([[5, vocab - 1, 3]] * 16, dtype=torch.int32, device="cuda")
+    _, _, top_id, _ = O.logprobs(f64(x), 1.0, ids.cpu().numpy(), top)
+    many = x.repeat(rows // 16, 1)
+    got = logprobs(model("bf16"), many, ids.repeat(rows // 16, 1), top, 1.0)["top_id"].view(-1, 16, top)
+    assert np.array_equal(got[0].cpu().numpy(), top_id)
+    assert bool((got == got[0]).all())
+
+
+def test_logprobs_strict_masks_cost_a_reading_more():
+    """A grammar that allows three tokens: its rows are read twice, not over and over (three times the ordinary rows' time
+    leaves room for noise; five and thirteen times it were measured with a reading for every alternative)."""
+    h, rows, vocab, top = model("bf16"), 2047, 32003, 5
+    x = random_logits(rows, vocab, "bf16", 86)
+    out = dict(top_id=torch.empty(rows, top, dtype=torch.int32, device="cuda"), top_logp=torch.empty(rows, top, device="cuda"))
+    few = torch.zeros(vocab, dtype=torch.bool, device="cuda")
+    few[[5, vocab // 2, vocab - 9]] = True
+
+    def best(logits):
+        times = []
+        for _ in range(8):
+            a, e = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(10):
+                b.token_logprobs(h, logits, **out)
+            e.record()
+            e.synchronize()
+            times.append(a.elapsed_time(e))
+        return min(times)
+
+    plain = best(x)
+    for mask in (-math.inf, -1e9, torch.finfo(x.dtype).min):
+        assert best(x.masked_fill(~few, mask)) < 3 * plain, mask
