@@ -579,10 +579,11 @@ int w4_unpack(blend_handle* h, const blend_w4* w4, void* out, int64_t ld_out, vo
  * BLEND_W4_SWIGLU (n a multiple of 2 * BLEND_GU_BLOCK, rows interleaved as in w_gu) writes
  * silu(gate) * up, y device [n_rows][n / 2].  y is of y_dtype (BLEND_F32 | BLEND_BF16; F32 for
  * BLEND_W4_ADD) with ld_y elements between rows, any alignment of its elements; rows of y stay apart
- * from x.  Inputs and scales have to be finite, |x| below 2^127; an infinity or a NaN in a row of x can make
- * that row of y NaN, no other.  The result does not depend on timing.
+ * from x.  Inputs and scales have to be finite, |x| at most 2^123 (a group's products are summed before its
+ * scale, and 128 of them with a code of 0 are 16 times as large); of fp32 inputs below 2^-110 bits are lost.  An
+ * infinity or a NaN in a row of x can make that row of y NaN, no other.  The result does not depend on timing.
  * Errors: BLEND_EINVAL for NULL or unaligned pointers, bad sizes, strides, group, dtype or epi, y over
- * x (nothing is launched). */
+ * x or the weights (nothing is launched). */
 int w4_linear(blend_handle* h, const blend_w4* w4, const void* x, int64_t ld_x, int32_t n_rows, void* y,
               int64_t ld_y, int32_t y_dtype, int32_t epi, void* stream);
 

@@ -237,3 +237,28 @@ def test_logprobs_strict_masks_cost_a_reading_more():
     plain = best(x)
     for mask in (-math.inf, -1e9, torch.finfo(x.dtype).min):
         assert best(x.masked_fill(~few, mask)) < 3 * plain, mask
+
+
+@pytest.mark.parametrize("dtype,rows", [("bf16", 3), ("bf16", 20), ("bf16", 40), ("bf16", 130), ("f32", 3), ("f32", 20)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_linear_inputs_at_the_ends_of_their_range(dtype, rows, group):
+    """The largest inputs, whose products with the lowest code all add up, and the smallest that keep all bits."""
+    h = model(dtype)
+    n, k = 160, 520
+    w4, values = weights(n, k, group, 87)
+    w4.codes[3] = 0
+    small = torch.full_like(w4.scale, 2.0 ** -30)
+    x = torch.full((rows, k), 2.0 ** 123, dtype=TORCH[dtype], device="cuda")
+    y = torch.empty(rows, n, device="cuda")
+    big = b.W4Ref(w4.codes, small, k, group)
+    b.w4_linear(h, big, x, y)
+    codes = np.rint(values / np.repeat(w4.scale.double().cpu().numpy()[:, :-(-k // group)], group, 1)[:, :k])
+    codes[3] = -8
+    want, bound = linear_bounds(codes * 2.0 ** -30, f64(x), "f32", False)
+    inside(f64(y), want, bound)
+    assert f64(y)[0, 3] == -8.0 * k * 2.0 ** 93
+    x = (rows_of(dtype, rows, k, 88).float() * 2.0 ** -108).to(TORCH[dtype])
+    x = torch.where(x.abs() < 2.0 ** -110, torch.zeros_like(x), x)
+    b.w4_linear(h, b.W4Ref(w4.codes, torch.ones_like(w4.scale), k, group), x, y)
+    want, bound = linear_bounds(codes, f64(x), "f32", False)
+    inside(f64(y), want, bound - 1e-30)  # (without what that allows beside numbers of usual size)
