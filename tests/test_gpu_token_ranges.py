@@ -8,7 +8,8 @@ import torch
 
 from oracle import token_oracle as O
 from rag_kv_cache_rope_gb300 import binding as b
-from tests.pagedcase import STEP, TORCH, f64, handle, i32
+from tests.pagedcase import TORCH, f64, i32
+from tests.test_gpu_decode import Model, Step, V
 from tests.test_gpu_tokens import check_logprobs, inside, linear_bounds, logprobs, model, random_logits, rows_of, weights
 
 pytestmark = pytest.mark.gpu
@@ -262,3 +263,74 @@ def test_linear_inputs_at_the_ends_of_their_range(dtype, rows, group):
     b.w4_linear(h, b.W4Ref(w4.codes, torch.ones_like(w4.scale), k, group), x, y)
     want, bound = linear_bounds(codes, f64(x), "f32", False)
     inside(f64(y), want, bound - 1e-30)  # (without what that allows beside numbers of usual size)
+
+
+@pytest.mark.parametrize("rows,n,k", [(9, 128, 256), (30, 160, 512), (60, 200, 512), (200, 384, 512), (500, 5120, 4096)])
+@pytest.mark.parametrize("group", [32, 128])
+def test_linear_tiles_keep_nan_and_infinity_in_their_row(rows, n, k, group):
+    """In the kernels of many rows too (whose outputs are 128 at least; the last case shares tiles between CTAs)."""
+    h = model("bf16")
+    w4 = b.W4Ref.empty(n, k, group)
+    w4.codes.random_(0, 256, generator=torch.Generator("cuda").manual_seed(89))
+    w4.scale.fill_(0.01)
+    x = rows_of("bf16", rows, k, 90)
+    clean, y = (torch.empty(rows, n, device="cuda") for _ in range(2))
+    b.w4_linear(h, w4, x, clean)
+    assert bool(clean.isfinite().all())
+    bad = sorted({1, 2, rows // 2, rows - 1})
+    x[bad[0], 7], x[bad[1], k - 1], x[bad[-2], 0], x[bad[-1], k // 2] = math.nan, math.inf, -math.inf, math.nan
+    b.w4_linear(h, w4, x, y)
+    keep = [r for r in range(rows) if r not in bad]
+    assert torch.equal(y[keep], clean[keep]) and bool(y[bad[0]].isnan().all()) and not bool(y[bad].isfinite().any())
+    # weights of a group that held an infinity: one output of every row
+    x = rows_of("bf16", rows, k, 90)
+    w4.scale[n - 3, 0] = math.nan
+    b.w4_linear(h, w4, x, y)
+    assert bool(y[:, n - 3].isnan().all())
+    keep = [j for j in range(n) if j != n - 3]
+    assert torch.equal(y[:, keep], clean[:, keep])
+
+
+@pytest.mark.parametrize("rows", [9, 40, 100, 200])
+def test_linear_tiles_outliers_with_weights_of_zero(rows):
+    """One input far larger than the others whose weights are 0: exact zeros, so the others keep their bits."""
+    h = model("bf16")
+    n, k, group = 160, 512, 64
+    w4, values = weights(n, k, group, 91)
+    x = rows_of("bf16", rows, k, 92)
+    x[:, 100] = 2.0 ** 60
+    x[1] *= 2.0 ** -100
+    codes = np.rint(values / np.repeat(w4.scale.double().cpu().numpy(), group, 1)).astype(np.int64) + 8
+    codes[:, 100] = 8
+    w4.codes.copy_(b.w4_layout(torch.from_numpy(codes)))
+    values[:, 100] = 0
+    y = torch.empty(rows, n, device="cuda")
+    b.w4_linear(h, w4, x, y)
+    xs = f64(x)
+    xs[:, 100] = 0
+    want, bound = linear_bounds(values, xs, "f32", False)
+    inside(f64(y), want, bound)
+
+
+@pytest.mark.parametrize("n_seq,group", [(3, 128), (20, 64)])
+def test_generated_tokens_in_bf16_are_as_near_as_their_roundings(n_seq, group):
+    """Some ten roundings a layer move their values by 2^-9 in the mean and add up like independent ones: over 2 layers the
+    logits are off by 2^-9 sqrt(20) of their size in the mean, none by more than eight times that (80000 values of a
+    normal distribution stay within five), and where the two highest are further apart than twice that, the token is the same."""
+    m = Model("bf16", group, 1)
+    st = Step(m, [(41 * s + 3) % 90 + 1 for s in range(n_seq)], 8, 2)
+    st.tok.copy_(torch.arange(n_seq) * 13 % V)
+    mean, clear = 2.0 ** -9 * math.sqrt(20), 0
+    for _ in range(4):
+        tok, pos = st.tok.cpu().numpy().copy(), st.pos.cpu().numpy().copy()
+        st.run()
+        want = st.oracle(tok, pos)
+        size = np.sqrt((want ** 2).mean(-1, keepdims=True))
+        off = np.abs(f64(st.logits) - want) / size
+        assert np.sqrt((off ** 2).mean()) <= mean and off.max() <= 8 * mean, (float(np.sqrt((off ** 2).mean()) / mean), float(off.max() / mean))
+        two = np.sort(want, -1)[:, -2:]
+        sure = (two[:, 1] - two[:, 0]) / size[:, 0] > 16 * mean
+        clear += int(sure.sum())
+        assert np.array_equal(st.top[:, 0].cpu().numpy()[sure], want.argmax(1)[sure])
+    assert clear > 0
+    b.blend_device_status(m.h)
