@@ -12,13 +12,13 @@
 // k-th largest of the maxima of 64 groups of threads is a lower bound T of the k-th largest logit, which
 // at most a few dozen logits of the stretch reach, and those lie with the few threads whose maximum reaches T: only
 // these threads' vectors are read again (from L2).  The candidates, 64-bit keys of value and index, are
-// ranked by counting.  Ties at T in numbers (a masked row) and NaN at the end of the ranking are taken in
-// order of their index.  Each CTA of a cluster ranks its own stretch; the first joins sums and lists through
+// ranked by counting.  Ties at T in numbers (a masked row), masks by value and NaN at the end of the ranking are taken
+// in order of their index.  Each CTA of a cluster ranks its own stretch; the first joins sums and lists through
 // distributed shared memory in the CTAs' order, so nothing depends on timing and no workspace is needed.
 //
 // 2047 x 32000 fp32, one alternative: 54 us, 4.9 TB/s; 2047 x 32003 bf16 35 us, 3.7 TB/s (without ranking 30 us): with
 // two bytes a logit, issue slots (62 %), the two exponentials of a pair and the barriers at a row's ends bound it.  512 x
-// 128256 bf16, 20 alternatives: 39 us.  Few rows are a chain of latencies: 1 x 152064 with 20 alternatives 7.8 us (without
+// 128256 bf16, 20 alternatives: 39 us.  Few rows are a chain of latencies: 1 x 152064 with 20 alternatives 8.2 us (without
 // 4.2), of which a cluster of 16 saves 10; 64 x 128256 fp32 13.4 us for 30.5 without clusters.
 #include <cooperative_groups.h>
 

@@ -13,7 +13,7 @@
 //
 // Cached keys of 16064 rows over 8 layers, 8 x 128 bf16: 87 us, 6.0 TB/s, 90 % of the copy rate, bound by HBM.  4099 rows of
 // 40 + 8 heads: 19.5 us (half of the dims, interleaved) to 20.8, 5 TB/s: the angles of a row are in the way of its first
-// loads.  One row: 2.6 us.
+// loads.  One row: 2.6 us.  fp32: 16064 rows 179 us (half layout) and 206 (interleaved), 157 at the copy rate.
 #include "tokens.cuh"
 
 namespace blend {

@@ -11,6 +11,8 @@
 // Up to 8 rows come here (the instruction's other side has 8 columns), and fp32 rows of any number.  bf16, against the
 // tcgen05 kernel: 8 x 27648 x 5120 (groups of 32, SwiGLU) 22 us and 34; 8 x 152064 x 5120 83 and 123; 8 x 5120 x 13824 19.7
 // and 19.5; 9 rows in two blocks of this kernel 36.4 and 34.2 (27648 x 5120, groups of 32), 25.9 and 19.5 (5120 x 13824).
+// fp32: 1 x 27648 x 5120 (groups of 32) 25 us, 8 rows 119 (three parts of the inputs, over two CTAs); many rows read all
+// codes again for each block of eight rows or fewer, 500 x 5120 x 13824 2.1 ms.
 #include "w4.cuh"
 
 namespace blend {
@@ -19,8 +21,9 @@ namespace {
 // ---------------------------------------------------------------- pack, unpack
 // A warp takes a stretch of one row, a lane eight inputs (one word of codes) of it at a time, PACK_U times 32
 // words together: loads and stores are whole lines, and nothing is divided to find a place.  Packing 27648 x 5120 bf16 in
-// groups of 32 takes 85 us (4.3 TB/s; 121 where the buffers lie unluckily), bound by instruction issue (71 % of slots: a maximum, an exact quotient and
-// a code for each weight); reading back 58 us (6.3 TB/s), bound by HBM.
+// groups of 32 takes 82-83 us (4.4 TB/s), wherever source, codes and scales lie, bound by instruction issue (71 % of slots: a
+// maximum, an exact quotient and a code for each weight), fp32 130 us (5.0 TB/s); reading back 57 us (6.4 TB/s), bound by HBM, to
+// fp32 141 us (4.6 TB/s: a lane's eight values are two halves of a line).
 constexpr int PACK_THREADS = 256, PACK_U = 4;
 struct PackPlace {
     int row, w0, w1;  // words w0 .. w1 - 1 of the row, in input order

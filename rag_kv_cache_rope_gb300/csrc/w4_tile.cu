@@ -7,7 +7,7 @@
 // Scales are not rounded into an operand: the products of one group are summed in a TMEM accumulator of
 // their own, and eight warps add it, times the row's scale, to sums in registers while the next group's products
 // run.  So a result is what the few rows' kernel gives up to the order of fp32 sums.  (Scales inside the operand
-// take 11 bits: two bf16 parts and twice the products.)
+// take 11 bits: two bf16 parts, exact, and twice the products.)
 //
 // What bounds it is that hand-over: a group's accumulators are awaited, read, released and added one after the
 // other by the same warps, about 480 cycles of 128 columns, where the products of 32 inputs take 128 and those of
