@@ -236,7 +236,9 @@ size_t blend_workspace_size(const blend_model_cfg* cfg, const blend_limits* lim)
 int blend_init(const blend_model_cfg* cfg, const blend_weights* w, const blend_limits* lim,
                void* workspace, size_t ws_bytes, void* stream, blend_handle** out);
 int blend_destroy(blend_handle* h);
-/* Text of the last error on this handle (or of the last handle-less call when h is NULL). */
+/* Text of the last error on this handle (or of the calling thread's last one when h is NULL).  Where the calling
+ * thread's last error was on this handle it is that one, whatever other threads' calls did meanwhile; valid
+ * until the thread's next call. */
 const char* blend_last_error(const blend_handle* h);
 /* Synchronises `stream`, then returns BLEND_OK, or BLEND_EDEVICE / BLEND_ETIMEOUT if a
  * device-side check of an earlier call on this handle failed (bad positions in a

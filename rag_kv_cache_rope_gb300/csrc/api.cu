@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <mutex>
 #include <string>
 #include <vector>
 
@@ -20,7 +21,8 @@
 #include "tokens.cuh"
 
 namespace {
-thread_local std::string g_err;
+thread_local std::string g_err;                   // this thread's last failure
+thread_local const blend_handle* g_err_of = nullptr;  // and the handle it was on
 }  // namespace
 
 namespace blend {
@@ -28,6 +30,7 @@ static std::atomic<long long> g_launches{0};
 void note_launch(int n) { g_launches += n; }
 int report_error(int code, const char* msg) {
     g_err = msg;
+    g_err_of = nullptr;
     return code;
 }
 }  // namespace blend
@@ -104,6 +107,7 @@ struct blend_handle {
     int32_t* paged_count;  // and the arrivals at each split item (zero between calls)
     float* split_ws;  // tensor-core GEMM: K-half partials of last-wave tiles
     int host_rc = 0;  // first failure of an internal launch during the current call
+    mutable std::mutex err_lock;  // calls of several threads may fail at once
     std::string last_error;
     // profiler
     bool prof_on = false;
@@ -175,8 +179,12 @@ int fail(blend_handle* h, int code, const char* fmt, ...) {
     va_start(ap, fmt);
     vsnprintf(buf, sizeof buf, fmt, ap);
     va_end(ap);
-    if (h) h->last_error = buf;
     g_err = buf;
+    g_err_of = h;
+    if (h) {
+        std::lock_guard<std::mutex> hold(h->err_lock);
+        h->last_error = buf;
+    }
     return code;
 }
 
@@ -448,7 +456,11 @@ size_t blend_workspace_size(const blend_model_cfg* cfg, const blend_limits* lim)
 }
 
 const char* blend_last_error(const blend_handle* h) {
-    return h ? h->last_error.c_str() : g_err.c_str();
+    if (!h || g_err_of == h) return g_err.c_str();
+    thread_local std::string other;  // another thread's
+    std::lock_guard<std::mutex> hold(h->err_lock);
+    other = h->last_error;
+    return other.c_str();
 }
 
 int blend_init(const blend_model_cfg* cfg, const blend_weights* w, const blend_limits* lim,
@@ -515,10 +527,11 @@ int blend_init(const blend_model_cfg* cfg, const blend_weights* w, const blend_l
     launch_rope_table(h->rope, cfg->max_pos, cfg->head_dim, cfg->rope_theta, s);
     int rc = check_cuda(h, "blend_init");
     if (rc != BLEND_OK) {
-        g_err = h->last_error;
+        g_err_of = nullptr;
         delete h;
         return rc;
     }
+    if (g_err_of == h) g_err_of = nullptr;  // (of an earlier handle at this address)
     *out = h;
     return BLEND_OK;
 }

@@ -1,6 +1,6 @@
 """Host side of the token operators.  Launches of the products with 4-bit weights over a stand-in for the CUDA runtime,
 which keeps a kernel's limits per device as the real one does: what a launch needs is set up on every device it is made
-on, once, and a failure is not remembered.  Tensors of another GPU.  Which rows of two tensors meet.  No GPU is needed."""
+on, once, and a failure is not remembered.  Texts of errors on several threads.  Tensors of another GPU.  Which rows of two tensors meet.  No GPU is needed."""
 import os
 import subprocess
 import types
@@ -55,6 +55,13 @@ void __cudaRegisterFatBinaryEnd(void**) {}
 void __cudaUnregisterFatBinary(void**) {}
 void __cudaRegisterFunction(void**, const char*, char*, const char*, int, void*, void*, void*, void*, int*) {}
 char __cudaInitModule(void**) { return 0; }
+void __cudaRegisterVar(void**, char*, char*, const char*, int, size_t, int, int) {}
+const char* cudaGetErrorString(cudaError_t) { return "failed"; }
+#define NOT_HERE(f) cudaError_t f(void) { return cudaErrorUnknown; }
+NOT_HERE(cudaDeviceGetAttribute) NOT_HERE(cudaStreamWaitEvent) NOT_HERE(cudaStreamSynchronize) NOT_HERE(cudaStreamDestroy)
+NOT_HERE(cudaStreamCreateWithFlags) NOT_HERE(cudaPointerGetAttributes) NOT_HERE(cudaMemsetAsync) NOT_HERE(cudaMemcpyAsync)
+NOT_HERE(cudaGetSymbolAddress) NOT_HERE(cudaGetDeviceProperties) NOT_HERE(cudaEventSynchronize) NOT_HERE(cudaEventRecord)
+NOT_HERE(cudaEventElapsedTime) NOT_HERE(cudaEventDestroy) NOT_HERE(cudaEventCreateWithFlags) NOT_HERE(cudaEventCreate)
 unsigned __cudaPushCallConfiguration(void) { return 1; }
 cudaError_t __cudaPopCallConfiguration(void) { return cudaErrorUnknown; }
 cudaError_t __cudaGetKernel(void) { return cudaErrorUnknown; }
@@ -64,7 +71,8 @@ cudaError_t __cudaLaunchKernel(void) { return cudaErrorUnknown; }
 
 FAKE_H = r"""
 #pragma once
-#include <cuda_runtime_api.h>
+#include <driver_types.h>
+#include <stddef.h>
 extern thread_local int device;
 extern int fail_next, launches, sets;
 """
@@ -130,21 +138,91 @@ int main(void) {
 """
 
 
-def test_launches_on_every_device_and_after_a_failure(tmp_path):
+def run_over_stand_in(tmp_path, name, source, objects):
+    """Builds `source` with the library's objects and the stand-in for the CUDA runtime, and runs it."""
     B.build()
     (tmp_path / "fake.h").write_text(FAKE_H)
     (tmp_path / "runtime.cpp").write_text(RUNTIME)
-    (tmp_path / "calls.cu").write_text(CALLS)
+    (tmp_path / name).write_text(source)
     inc = ["-I", str(tmp_path), "-I", B.CSRC, "-I", os.path.join(B.ROOT, "include"),
            "-I", os.path.join(os.path.dirname(os.path.dirname(B.nvcc())), "include")]
     objs = []
-    for cc, name in ((["g++"], "runtime.cpp"), ([B.nvcc(), *B.ARCH], "calls.cu")):
-        objs.append(str(tmp_path / (name + ".o")))
-        subprocess.run([*cc, "-std=c++17", *inc, "-c", str(tmp_path / name), "-o", objs[-1]], check=True)
+    for f in ("runtime.cpp", name):
+        cc = ["g++"] if f.endswith(".cpp") else [B.nvcc(), *B.ARCH]
+        objs.append(str(tmp_path / (f + ".o")))
+        subprocess.run([*cc, "-std=c++17", *inc, "-c", str(tmp_path / f), "-o", objs[-1]], check=True)
     exe = str(tmp_path / "probe")
-    subprocess.run(["g++", *objs, os.path.join(B.BUILD, "w4.cu.o"), os.path.join(B.BUILD, "w4_tile.cu.o"), "-o", exe, "-lpthread"], check=True)
+    subprocess.run(["g++", *objs, *objects, "-o", exe, "-lpthread", "-ldl"], check=True)
     r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
-    assert r.returncode == 0, r.stdout + r.stderr
+    assert r.returncode == 0, (r.returncode, r.stdout + r.stderr)
+
+
+def test_launches_on_every_device_and_after_a_failure(tmp_path):
+    run_over_stand_in(tmp_path, "calls.cu", CALLS, [os.path.join(B.BUILD, f + ".cu.o") for f in ("w4", "w4_tile")])
+
+
+ERRORS = r"""
+#include <stdio.h>
+#include <stdlib.h>
+#include <string.h>
+#include <string>
+#include <thread>
+#include <vector>
+#include "blend.h"
+int main(void) {
+    blend_model_cfg cfg = {1, 16, 4, 2, 128, 16, 16, BLEND_BF16, 1e4, 1e-6, 64};
+    blend_limits lim = {1, 1, 1, 1};
+    const size_t bytes = blend_workspace_size(&cfg, &lim);
+    void* ws = aligned_alloc(256, (bytes + 255) / 256 * 256);
+    static char mem[4096] __attribute__((aligned(256)));
+    blend_weights w = {mem, mem, mem, mem, mem, mem, mem, mem};
+    blend_handle *h = nullptr, *other = nullptr;
+    if (blend_init(&cfg, &w, &lim, ws, bytes, nullptr, &h) || blend_init(&cfg, &w, &lim, ws, bytes, nullptr, &other)) {
+        printf("no handle: %s\n", blend_last_error(nullptr));
+        return 1;
+    }
+    int wrong[4] = {};
+    std::vector<std::thread> t;
+    for (int i = 0; i < 4; ++i)
+        t.emplace_back([&, i] {
+            for (int n = 0; n < 20000; ++n) {
+                blend_w4 w4 = {32, 128, 48 + 1000 * i + n, mem, mem};
+                char want[64];
+                int rc;
+                if (i % 2) {
+                    rc = w4_linear(h, &w4, mem, 128, 1, mem, 32, BLEND_F32, BLEND_W4_STORE, nullptr);
+                    snprintf(want, sizeof want, "group=%d is not 32, 64 or 128", w4.group);
+                } else {
+                    rc = token_logprobs(h, i ? mem : nullptr, 1, 5 + n, 1, 1, 1.f, nullptr, 0, nullptr, nullptr, 0, nullptr, nullptr, nullptr);
+                    if (i) snprintf(want, sizeof want, "bad dtype %d", 5 + n);
+                    else snprintf(want, sizeof want, "NULL pointer");
+                }
+                wrong[i] += rc != BLEND_EINVAL || strcmp(blend_last_error(h), want) || strcmp(blend_last_error(nullptr), want);
+            }
+        });
+    for (auto& x : t) x.join();
+    for (int i = 0; i < 4; ++i)
+        if (wrong[i]) {
+            printf("thread %d: %d texts of other calls\n", i, wrong[i]);
+            return 2;
+        }
+    // one thread, two handles; another thread's text; a handle that follows one
+    w4_unpack(h, nullptr, mem, 8, nullptr);
+    w4_unpack(other, nullptr, nullptr, 8, nullptr);
+    rope_rows(other, nullptr, nullptr, 1, nullptr, nullptr, 1, nullptr);
+    if (strcmp(blend_last_error(h), "w4 is NULL") || strcmp(blend_last_error(other), "NULL pointer")) return 3;
+    std::thread([&] { token_logprobs(h, mem, 1, 7, 1, 1, 1.f, nullptr, 0, nullptr, nullptr, 0, nullptr, nullptr, nullptr); }).join();
+    if (strcmp(blend_last_error(h), "bad dtype 7")) return 4;
+    std::string seen;
+    std::thread([&] { seen = blend_last_error(h); }).join();
+    return seen == "bad dtype 7" ? 0 : 5;
+}
+"""
+
+
+def test_texts_of_calls_that_fail_on_several_threads(tmp_path):
+    """Refused calls of one handle on four threads: each reads its own text (and none another's half written)."""
+    run_over_stand_in(tmp_path, "errors.cpp", ERRORS, [os.path.join(B.BUILD, os.path.basename(f) + ".o") for f in B._sources()])
 
 
 class Tensor(torch.Tensor):
